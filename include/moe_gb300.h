@@ -472,6 +472,83 @@ moe_status moe_layer_backward_wgrad(const moe_config* cfg, const moe_weights* w,
                                     const moe_grads* g, void* act, size_t act_bytes, void* ws, size_t ws_bytes,
                                     void* stream);
 
+/* --------------------------------------------------------------------------
+ * Around the layer: the token embedding, the norm in front of an expert layer
+ * and the loss of the vocabulary head, each with its gradient.  The pages give
+ * no API for them; a training step of a model of these layers needs them.
+ *
+ * H is a multiple of 8, at most 16384.  Outputs do not overlap inputs.  The
+ * workspace is the caller's, as for the layer: its first 256 bytes are the same
+ * status region (moe_workspace_init once before first use), the rest scratch
+ * that every call overwrites, so a workspace of these calls is not also a
+ * layer's.  Token ids and labels are int32; -1 means none (padding, or a
+ * position that is not scored), any other value outside [0, V) is treated the
+ * same and sets MOE_ERR_BAD_INDEX on the device.
+ * ----------------------------------------------------------------------- */
+
+/* Workspace bytes of the two embedding calls (0 on bad sizes).  Host only.
+ * 0 <= n <= 2^24 tokens, 1 <= V <= 2^24. */
+size_t moe_embedding_workspace_bytes(int32_t n, int32_t V, int32_t H);
+
+/* out[i] = scale * table[tokens[i]], in fp32, rounded to bf16 once; a zero row
+ * where there is no token.  tokens [n]; table [V,H] bf16; out [n,H] bf16.  Uses
+ * only the status region of ws. */
+moe_status moe_embedding_forward(const int32_t* tokens, int32_t n, const void* table, int32_t V, int32_t H, float scale,
+                                 void* out, void* ws, void* stream);
+
+/* dtable[v] = base[v] + scale * sum of dy[i] over the i with tokens[i] == v, for
+ * every v (rows without a token included): fp32 sums in ascending i (in fixed
+ * groups), the same bits on every run.  dy [n,H] bf16; base [V,H] bf16 or NULL
+ * (0): the vocabulary head's dw where the two weights are tied; dtable [V,H]
+ * fp32, overwritten. */
+moe_status moe_embedding_backward(const int32_t* tokens, int32_t n, const void* dy, int32_t V, int32_t H, float scale,
+                                  const void* base, float* dtable, void* ws, size_t ws_bytes, void* stream);
+
+/* Layer norm with the residual sum in front of it.
+ *   s = x + residual rounded to bf16 (s = x without a residual),
+ *   y = (s - mean) * rstd * weight + bias,  rstd = 1 / sqrt(var + eps),
+ * mean and (biased) variance over H of s, in fp32.  x, residual [T,H] bf16
+ * (residual may be NULL); weight, bias [H] bf16 (bias may be NULL); y [T,H]
+ * bf16; sum_out [T,H] bf16 = s (with a residual only, NULL otherwise); mean,
+ * rstd [T] fp32, kept for the backward pass. */
+moe_status moe_layer_norm_forward(const void* x, const void* residual, const void* weight, const void* bias, int32_t T,
+                                  int32_t H, float eps, void* y, void* sum_out, float* mean, float* rstd,
+                                  void* stream);
+
+/* Workspace bytes of moe_layer_norm_backward (0 on bad sizes).  Host only. */
+size_t moe_layer_norm_workspace_bytes(int32_t T, int32_t H);
+
+/* Backward of the above: dx = d loss / d s (the gradient of both x and the
+ * residual), with dsum added where the stream s has a gradient of its own.
+ * dy, s [T,H] bf16; mean, rstd from the forward; dsum [T,H] bf16 or NULL; dx
+ * [T,H] bf16; dweight, dbias [H] fp32, overwritten (dbias may be NULL).  Sums
+ * are fp32 in a fixed order. */
+moe_status moe_layer_norm_backward(const void* dy, const void* s, const void* weight, const float* mean,
+                                   const float* rstd, const void* dsum, int32_t T, int32_t H, void* dx, float* dweight,
+                                   float* dbias, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of the two cross-entropy calls (0 on bad sizes).  piece: see
+ * moe_cross_entropy_backward.  Host only.  0 <= T <= 2^24, 1 <= V <= 2^24. */
+size_t moe_cross_entropy_workspace_bytes(int32_t T, int32_t H, int32_t V, int32_t piece);
+
+/* Softmax cross entropy of the vocabulary head; the logits z = x w^T (bf16
+ * operands, fp32 accumulation) are never stored.
+ *   lse[t] = log sum_v exp(z[t,v]);  loss[t] = lse[t] - z[t,labels[t]], 0 where
+ * there is no label.  x [T,H], w [V,H] bf16; labels [T]; loss, lse [T] fp32. */
+moe_status moe_cross_entropy_forward(const void* x, const void* w, const int32_t* labels, int32_t T, int32_t H,
+                                     int32_t V, float* loss, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of sum_t dloss[t] * loss[t].  With
+ *   d[t,v] = dloss[t] * (exp(z[t,v] - lse[t]) - [v == labels[t]])  (0 where there is no label,
+ * whatever that row of x, lse or dloss holds),  dx = d w, dw = d^T x: [T,H] and [V,H] bf16, overwritten,
+ * each rounded once from fp32 sums; d itself is rounded to bf16 between the
+ * products.  lse from the forward; dloss [T] fp32.  The logits are computed
+ * again, `piece` vocabulary entries at a time (rounded up to 256; 0: chosen by
+ * size); the workspace holds d of one piece. */
+moe_status moe_cross_entropy_backward(const void* x, const void* w, const int32_t* labels, const float* lse,
+                                      const float* dloss, int32_t T, int32_t H, int32_t V, int32_t piece, void* dx,
+                                      void* dw, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

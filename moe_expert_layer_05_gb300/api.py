@@ -26,6 +26,7 @@ MX_ROWS, MX_COLS_T, MX_ROWS_GATE_UP, MX_ROWS_G224, MX_COLS_T_G224 = range(5)
 c_i32 = ctypes.c_int32
 c_vp = ctypes.c_void_p
 c_sz = ctypes.c_size_t
+c_f32 = ctypes.c_float
 
 
 class MoeConfig(ctypes.Structure):
@@ -91,6 +92,17 @@ _SIGS = {
                                          c_vp, c_sz, c_vp]),
     "moe_layer_backward_wgrad": (c_i32, [_P(MoeConfig), _P(MoeWeights), c_vp, c_vp, _P(MoeGrads), c_vp, c_sz,
                                          c_vp, c_sz, c_vp]),
+    "moe_embedding_workspace_bytes": (c_sz, [c_i32, c_i32, c_i32]),
+    "moe_embedding_forward": (c_i32, [c_vp, c_i32, c_vp, c_i32, c_i32, c_f32, c_vp, c_vp, c_vp]),
+    "moe_embedding_backward": (c_i32, [c_vp, c_i32, c_vp, c_i32, c_i32, c_f32, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "moe_layer_norm_forward": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_i32, c_i32, c_f32, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "moe_layer_norm_workspace_bytes": (c_sz, [c_i32, c_i32]),
+    "moe_layer_norm_backward": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp,
+                                        c_sz, c_vp]),
+    "moe_cross_entropy_workspace_bytes": (c_sz, [c_i32, c_i32, c_i32, c_i32]),
+    "moe_cross_entropy_forward": (c_i32, [c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "moe_cross_entropy_backward": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp,
+                                           c_vp, c_sz, c_vp]),
 }
 
 _lib = None
@@ -272,6 +284,118 @@ def moe_layer_backward_wgrad(cfg, weights: MoeWeights, x, dy, grads: MoeGrads, a
                                           ctypes.byref(grads), ptr(act), act.numel() * act.element_size(),
                                           ptr(ws), ws.numel() * ws.element_size(), stream_ptr(stream)),
           "moe_layer_backward_wgrad")
+
+
+# ---------------------------------------------------------------- around the layer
+def _tensor(t, name: str, dtype, shape) -> int:
+    """Device address of a contiguous CUDA tensor of this type and shape; raises ValueError otherwise."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name}: expected a contiguous CUDA tensor {tuple(shape)} of {dtype}, got "
+                         f"{tuple(t.shape)} of {t.dtype} on {t.device}"
+                         + ("" if t.is_contiguous() else ", not contiguous"))
+    return t.data_ptr()
+
+
+def _opt_tensor(t, name: str, dtype, shape) -> int | None:
+    return None if t is None else _tensor(t, name, dtype, shape)
+
+
+def _matrix(t, name: str) -> tuple[int, int]:
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected two dimensions, got {tuple(t.shape)}")
+    return tuple(t.shape)
+
+
+def _scratch(ws) -> tuple[int, int]:
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("ws: expected a contiguous CUDA tensor")
+    nbytes = ws.numel() * ws.element_size()
+    if nbytes < 256:
+        raise MoeError(-4, "ws")
+    return ws.data_ptr(), nbytes
+
+
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def moe_embedding_workspace_bytes(n: int, V: int, H: int) -> int:
+    return int(load().moe_embedding_workspace_bytes(n, V, H))
+
+
+def moe_embedding_forward(tokens, table, out, ws, scale: float = 1.0, stream=None) -> None:
+    """out[i] = scale * table[tokens[i]] (bf16); a zero row where tokens[i] is -1."""
+    V, H = _matrix(table, "table")
+    n = tokens.numel()
+    check(load().moe_embedding_forward(_tensor(tokens, "tokens", _I32, (n,)), n, _tensor(table, "table", _BF16, (V, H)),
+                                       V, H, scale, _tensor(out, "out", _BF16, (n, H)), _scratch(ws)[0],
+                                       stream_ptr(stream)), "moe_embedding_forward")
+
+
+def moe_embedding_backward(tokens, dy, dtable, ws, scale: float = 1.0, base=None, stream=None) -> None:
+    """dtable[v] = base[v] + scale * (sum of dy[i] over tokens[i] == v), fp32, every row written."""
+    V, H = _matrix(dtable, "dtable")
+    n = tokens.numel()
+    wp, wn = _scratch(ws)
+    check(load().moe_embedding_backward(_tensor(tokens, "tokens", _I32, (n,)), n, _tensor(dy, "dy", _BF16, (n, H)), V,
+                                        H, scale, _opt_tensor(base, "base", _BF16, (V, H)),
+                                        _tensor(dtable, "dtable", _F32, (V, H)), wp, wn, stream_ptr(stream)),
+          "moe_embedding_backward")
+
+
+def moe_layer_norm_forward(x, weight, bias, y, mean, rstd, residual=None, sum_out=None, eps: float = 1e-5,
+                           stream=None) -> None:
+    """y = norm(s) * weight + bias with s = x + residual (written to sum_out); mean and rstd for the backward."""
+    T, H = _matrix(x, "x")
+    check(load().moe_layer_norm_forward(_tensor(x, "x", _BF16, (T, H)), _opt_tensor(residual, "residual", _BF16, (T, H)),
+                                        _tensor(weight, "weight", _BF16, (H,)), _opt_tensor(bias, "bias", _BF16, (H,)),
+                                        T, H, eps, _tensor(y, "y", _BF16, (T, H)),
+                                        _opt_tensor(sum_out, "sum_out", _BF16, (T, H)),
+                                        _tensor(mean, "mean", _F32, (T,)), _tensor(rstd, "rstd", _F32, (T,)),
+                                        stream_ptr(stream)), "moe_layer_norm_forward")
+
+
+def moe_layer_norm_workspace_bytes(T: int, H: int) -> int:
+    return int(load().moe_layer_norm_workspace_bytes(T, H))
+
+
+def moe_layer_norm_backward(dy, s, weight, mean, rstd, dx, dweight, dbias, ws, dsum=None, stream=None) -> None:
+    """dx = the gradient of s (plus dsum, the stream's own); dweight and dbias (or None), fp32."""
+    T, H = _matrix(s, "s")
+    wp, wn = _scratch(ws)
+    check(load().moe_layer_norm_backward(_tensor(dy, "dy", _BF16, (T, H)), _tensor(s, "s", _BF16, (T, H)),
+                                         _tensor(weight, "weight", _BF16, (H,)), _tensor(mean, "mean", _F32, (T,)),
+                                         _tensor(rstd, "rstd", _F32, (T,)), _opt_tensor(dsum, "dsum", _BF16, (T, H)),
+                                         T, H, _tensor(dx, "dx", _BF16, (T, H)),
+                                         _tensor(dweight, "dweight", _F32, (H,)),
+                                         _opt_tensor(dbias, "dbias", _F32, (H,)), wp, wn, stream_ptr(stream)),
+          "moe_layer_norm_backward")
+
+
+def moe_cross_entropy_workspace_bytes(T: int, H: int, V: int, piece: int = 0) -> int:
+    return int(load().moe_cross_entropy_workspace_bytes(T, H, V, piece))
+
+
+def moe_cross_entropy_forward(x, w, labels, loss, lse, ws, stream=None) -> None:
+    """loss[t] = lse[t] - <x[t], w[labels[t]]>, 0 where labels[t] is -1; the logits are not kept."""
+    T, H = _matrix(x, "x")
+    V = _matrix(w, "w")[0]
+    wp, wn = _scratch(ws)
+    check(load().moe_cross_entropy_forward(_tensor(x, "x", _BF16, (T, H)), _tensor(w, "w", _BF16, (V, H)),
+                                           _tensor(labels, "labels", _I32, (T,)), T, H, V,
+                                           _tensor(loss, "loss", _F32, (T,)), _tensor(lse, "lse", _F32, (T,)), wp, wn,
+                                           stream_ptr(stream)), "moe_cross_entropy_forward")
+
+
+def moe_cross_entropy_backward(x, w, labels, lse, dloss, dx, dw, ws, piece: int = 0, stream=None) -> None:
+    """dx and dw (bf16) of sum_t dloss[t] * loss[t], `piece` vocabulary entries at a time (0: chosen by size)."""
+    T, H = _matrix(x, "x")
+    V = _matrix(w, "w")[0]
+    wp, wn = _scratch(ws)
+    check(load().moe_cross_entropy_backward(_tensor(x, "x", _BF16, (T, H)), _tensor(w, "w", _BF16, (V, H)),
+                                            _tensor(labels, "labels", _I32, (T,)), _tensor(lse, "lse", _F32, (T,)),
+                                            _tensor(dloss, "dloss", _F32, (T,)), T, H, V, piece,
+                                            _tensor(dx, "dx", _BF16, (T, H)), _tensor(dw, "dw", _BF16, (V, H)), wp, wn,
+                                            stream_ptr(stream)), "moe_cross_entropy_backward")
 
 
 # ---------------------------------------------------------------- buffers

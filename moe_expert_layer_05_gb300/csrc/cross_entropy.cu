@@ -1,0 +1,328 @@
+// Softmax cross entropy of a vocabulary head, and its gradient, without ever
+// holding the logits:
+//
+//   z[t, v] = <x[t], w[v]>,  lse[t] = log sum_v exp z[t, v],
+//   loss[t] = lse[t] - z[t, label[t]];
+//   d[t, v] = dloss[t] (exp(z[t, v] - lse[t]) - [v = label[t]]),
+//   dx = d w,  dw = d^T x.
+//
+// Forward: one tcgen05 GEMM whose epilogue reduces each 256-column tile of
+// logits to a maximum and a sum of exponentials per row (ce_stats_tile), and
+// a kernel that joins the tiles' pairs in order.  The logits stay in TMEM.
+//
+// Backward, per piece of the vocabulary: the piece's logits again, turned into
+// d in the GEMM's epilogue (ce_grad_tile) and kept for this piece only, in
+// bf16 -- the operand type of the tensor cores' next two products: a rounding
+// of 2^-9 per element, of the size of the gradients' own rounding to bf16 at
+// the end -- then dx += d w_piece into fp32 slabs and dw_piece = d^T x.  dx's
+// contraction runs over the vocabulary, so with few tokens it is cut into
+// parts with a slab each; the last kernel adds the slabs in order and rounds
+// once.  Pieces follow one another on the stream, so the fp32 additions into a
+// slab have one order and the result does not depend on timing.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "entry_checks.h"
+#include "gemm_common.h"
+
+namespace moe {
+namespace {
+
+constexpr int kTile = 256;           // vocabulary entries of one logits tile
+constexpr int kMaxTokens = 1 << 24, kMaxVocab = 1 << 24;
+constexpr int kMaxSlabs = 16;
+
+// Elements of d kept at a time where the caller names no piece: 128 MB of
+// bf16, within the L2's size.
+constexpr long long kPieceElements = 1LL << 26;
+constexpr int kMinPiece = 4096;
+
+int round_up(int v, int m) { return (v + m - 1) / m * m; }
+
+int piece_of(int T, int V, int piece) {
+  if (piece <= 0) {
+    const long long p = kPieceElements / (T > 0 ? T : 1) / kTile * kTile;
+    piece = p < kMinPiece ? kMinPiece : p > (1 << 24) ? (1 << 24) : static_cast<int>(p);
+  }
+  const int all = round_up(V, kTile);
+  return piece < all ? round_up(piece, kTile) : all;
+}
+
+// Up to 128 tokens the logits and dx run on 128-row tiles of one CTA,
+// otherwise on 256-row tiles of CTA pairs.
+bool small_rows(int T) { return T <= 128; }
+
+// Parts of dx's contraction over a piece of kb k-blocks: about two tiles for
+// every CTA (or pair), at least 8 k-blocks each.
+int kb_per_split(int T, int H, int kb) {
+  const int units = small_rows(T) ? 152 : 76;
+  const int tiles = (small_rows(T) ? 1 : (T + 255) / 256) * ((H + kTile - 1) / kTile);
+  int splits = 2 * units / tiles;
+  if (splits > kMaxSlabs) splits = kMaxSlabs;
+  if (splits > kb / 8) splits = kb / 8;
+  if (splits < 1) splits = 1;
+  return (kb + splits - 1) / splits;
+}
+
+struct Ws {
+  size_t stats, label_logit;         // forward
+  size_t d, xz, slabs;               // backward
+  int piece, slab_count;
+  size_t total;
+};
+Ws layout(int T, int H, int V, int piece) {
+  Ws w;
+  size_t off = entry::kStatusBytes, end = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = entry::align_up(off + bytes);
+    return o;
+  };
+  const size_t rows = T;
+  w.stats = take(static_cast<size_t>((V + kTile - 1) / kTile) * rows * sizeof(float2));
+  w.label_logit = take(rows * 4);
+  end = off;
+  off = entry::kStatusBytes;
+  w.piece = piece_of(T, V, piece);
+  const int kb = w.piece / 64, per = kb_per_split(T, H, kb);
+  w.slab_count = (kb + per - 1) / per;
+  w.d = take(rows * w.piece * 2);
+  w.xz = take(rows * H * 2);
+  w.slabs = take(static_cast<size_t>(w.slab_count) * rows * H * 4);
+  w.total = end > off ? end : off;
+  return w;
+}
+
+template <class T>
+T* at(void* ws, size_t off) {
+  return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
+}
+
+// ---------------------------------------------------------------- logits GEMM
+template <Epi EP, bool PAIR>
+cudaError_t gemm_logits(const void* x, int T, int H, const void* w_rows, int rows, void* d, int ld, CeParams ce,
+                        int* status, cudaStream_t st) {
+  using C = GemmCfg<256, false, false, Sched::kDenseM, EP, 0, false, PAIR>;
+  CUtensorMap ta, tb, tc;
+  if (!make_tmap_bf16(&ta, x, H, T, 64, 128) || !make_tmap_bf16(&tb, w_rows, H, rows, 64, C::B_BOX_ROWS))
+    return cudaErrorInvalidValue;
+  tc = ta;
+  if (d != nullptr && !make_tmap_out_bf16(&tc, d, ld, T)) return cudaErrorInvalidValue;
+  GemmParams p = gemm_params_zero();
+  p.E = 1;
+  p.m_rows = T;
+  p.k_len = round_up(H, C::BK);          // (zeros past H)
+  p.n_tiles = (rows + kTile - 1) / kTile;
+  p.rows_cap = T;
+  p.status = status;
+  p.ce = ce;
+  const int tiles = (T + C::TILE_M - 1) / C::TILE_M * p.n_tiles;
+  if constexpr (PAIR)
+    return launch_gemm_pair<C>(ta, tb, tc, tc, p, tiles, st);
+  else
+    return launch_gemm<C>(ta, tb, tc, tc, p, tiles < num_sms() ? tiles : num_sms(), st);
+}
+
+// dx slabs (+)= d[T, cols] w_rows[cols, H]
+template <bool PAIR>
+cudaError_t gemm_dx(const void* d, int ld, int T, const void* w_rows, int rows, int H, int per, float* slabs,
+                    int slab_count, bool add, int* status, cudaStream_t st) {
+  using C = GemmCfg<256, false, true, Sched::kSplitK, Epi::kStoreF32, 0, false, PAIR>;
+  CUtensorMap ta, tb, tc;
+  if (!make_tmap_bf16(&ta, d, ld, T, 64, 128) || !make_tmap_bf16(&tb, w_rows, H, rows, 64, 64) ||
+      !make_tmap_slabs_f32(&tc, slabs, H, T, slab_count))
+    return cudaErrorInvalidValue;
+  GemmParams p = gemm_params_zero();
+  p.E = 1;
+  p.m_rows = T;
+  p.k_len = round_up(rows, kTile);       // whole tiles of d, zero past the vocabulary
+  p.n_tiles = (H + kTile - 1) / kTile;
+  p.rows_cap = T;
+  p.valid_cols = H;
+  p.kb_per_split = per;
+  p.c_add = add ? 1 : 0;
+  p.status = status;
+  const int splits = (p.k_len / C::BK + per - 1) / per;
+  const int tiles = (T + C::TILE_M - 1) / C::TILE_M * p.n_tiles * splits;
+  if constexpr (PAIR)
+    return launch_gemm_pair<C>(ta, tb, tc, tc, p, tiles, st);
+  else
+    return launch_gemm<C>(ta, tb, tc, tc, p, tiles < num_sms() ? tiles : num_sms(), st);
+}
+
+// dw_rows[rows, H] = d[T, rows]^T x[T, H]
+cudaError_t gemm_dw(const void* d, int ld, int T, const void* x, int H, void* dw_rows, int rows, int* status,
+                    cudaStream_t st) {
+  using C = GemmCfg<256, true, true, Sched::kRoutedK, Epi::kStoreBf16, 0, false, true>;
+  CUtensorMap ta, tb, tc;
+  if (!make_tmap_bf16(&ta, d, ld, T, 64, C::BK) || !make_tmap_bf16(&tb, x, H, T, 64, C::BK) ||
+      !make_tmap_out_bf16(&tc, dw_rows, H, rows))
+    return cudaErrorInvalidValue;
+  GemmParams p = gemm_params_zero();
+  p.E = 1;
+  p.m_rows = rows;
+  p.k_len = T;
+  p.m_tiles_w = (rows + 255) / 256;
+  p.n_tiles = (H + kTile - 1) / kTile;
+  p.valid_cols = H;
+  p.status = status;
+  return launch_gemm_pair<C>(ta, tb, tc, tc, p, p.m_tiles_w * p.n_tiles, st);
+}
+
+// ---------------------------------------------------------------- row kernels
+constexpr int kJoinRows = 32, kJoinStrands = 16;
+
+// lse and loss of each row from its tiles' (maximum, sum): strand s takes
+// tiles s, s + 16, ... in order, then the strands are joined in order.
+__global__ void __launch_bounds__(kJoinRows * kJoinStrands) ce_join_kernel(const float2* __restrict__ stats, int tiles,
+                                                                          const float* __restrict__ label_logit,
+                                                                          const int32_t* __restrict__ labels, int T,
+                                                                          int V, float* __restrict__ loss,
+                                                                          float* __restrict__ lse, int* status) {
+  pdl_entry();
+  __shared__ float2 s_part[kJoinStrands][kJoinRows];
+  const int lane = threadIdx.x % kJoinRows, strand = threadIdx.x / kJoinRows;
+  const int row = blockIdx.x * kJoinRows + lane;
+  auto join = [](float2 a, float2 b) {
+    const float m = fmaxf(a.x, b.x);
+    const float off = (m == -INFINITY ? 0.f : m) * kLog2e;
+    return make_float2(m, a.y * ex2(fmaf(a.x, kLog2e, -off)) + b.y * ex2(fmaf(b.x, kLog2e, -off)));
+  };
+  float2 a = make_float2(-INFINITY, 0.f);
+  if (row < T) {
+    #pragma unroll 4
+    for (int i = strand; i < tiles; i += kJoinStrands) a = join(a, stats[static_cast<long long>(i) * T + row]);
+  }
+  s_part[strand][lane] = a;
+  __syncthreads();
+  if (strand != 0 || row >= T) return;
+  #pragma unroll
+  for (int i = 1; i < kJoinStrands; ++i) a = join(a, s_part[i][lane]);
+  const float l = a.x + logf(a.y);
+  const int label = labels[row];
+  const bool scored = label >= 0 && label < V;
+  if (!scored && label != -1) set_status(status, kErrBadIndex);
+  lse[row] = l;
+  loss[row] = scored ? l - label_logit[row] : 0.f;
+}
+
+// x with the rows that are not scored set to zero: d is zero there, but the
+// product d^T x would still turn an infinity or NaN of such a row into NaN.
+__global__ void __launch_bounds__(128) ce_scored_rows_kernel(const uint4* __restrict__ x,
+                                                             const int32_t* __restrict__ labels, int V, int words,
+                                                             uint4* __restrict__ xz) {
+  pdl_entry();
+  const int label = labels[blockIdx.x];
+  const bool scored = label >= 0 && label < V;
+  const long long row = static_cast<long long>(blockIdx.x) * words;
+  for (int c = threadIdx.x; c < words; c += blockDim.x) xz[row + c] = scored ? x[row + c] : make_uint4(0, 0, 0, 0);
+}
+
+// dx = the slabs added in order, rounded to bf16.  n4 = T * H / 4.
+__global__ void __launch_bounds__(256) ce_dx_kernel(const float4* __restrict__ slabs, int count, long long n4,
+                                                    uint2* __restrict__ dx) {
+  pdl_entry();
+  const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= n4) return;
+  float4 a = slabs[i];
+  for (int s = 1; s < count; ++s) {
+    const float4 b = slabs[s * n4 + i];
+    a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+  }
+  dx[i] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+}
+
+bool sizes_ok(int32_t T, int32_t H, int32_t V, int32_t piece) {
+  return T >= 0 && T <= kMaxTokens && V > 0 && V <= kMaxVocab && entry::hidden_ok(H) && piece >= 0 &&
+         // tiles are counted in 32 bits
+         (static_cast<long long>(T) / 128 + 1) * (V / kTile + 1) < (1LL << 30);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+using namespace moe::entry;
+
+#define MOE_TRY(expr)                                 \
+  do {                                                \
+    if ((expr) != cudaSuccess) return MOE_ERR_CUDA;   \
+  } while (0)
+
+extern "C" {
+
+size_t moe_cross_entropy_workspace_bytes(int32_t T, int32_t H, int32_t V, int32_t piece) {
+  return sizes_ok(T, H, V, piece) ? layout(T, H, V, piece).total : 0;
+}
+
+moe_status moe_cross_entropy_forward(const void* x, const void* w, const int32_t* labels, int32_t T, int32_t H,
+                                     int32_t V, float* loss, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  if (!sizes_ok(T, H, V, 0) || !ptr_ok(w) || !ptr_ok(ws)) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!ptr_ok(x) || !ptr_ok(labels) || !ptr_ok(loss) || !ptr_ok(lse))) return MOE_ERR_INVALID_ARG;
+  const Ws l = layout(T, H, V, 0);
+  if (ws_bytes < l.label_logit + static_cast<size_t>(T) * 4) return MOE_ERR_WORKSPACE;
+  if (!device_is_gb300()) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int* status = static_cast<int*>(ws);
+  CeParams ce{};
+  ce.labels = labels;
+  ce.vocab = V;
+  ce.stats = at<float2>(ws, l.stats);
+  ce.label_logit = at<float>(ws, l.label_logit);
+  if (small_rows(T))
+    MOE_TRY((gemm_logits<Epi::kCeStats, false>(x, T, H, w, V, nullptr, 0, ce, status, st)));
+  else
+    MOE_TRY((gemm_logits<Epi::kCeStats, true>(x, T, H, w, V, nullptr, 0, ce, status, st)));
+  count_launches(1);
+  MOE_TRY(launch_k(ce_join_kernel, (T + kJoinRows - 1) / kJoinRows, kJoinRows * kJoinStrands, 0, st, ce.stats,
+                   (V + kTile - 1) / kTile, ce.label_logit, labels, T, V, loss, lse, status));
+  return MOE_OK;
+}
+
+moe_status moe_cross_entropy_backward(const void* x, const void* w, const int32_t* labels, const float* lse,
+                                      const float* dloss, int32_t T, int32_t H, int32_t V, int32_t piece, void* dx,
+                                      void* dw, void* ws, size_t ws_bytes, void* stream) {
+  if (!sizes_ok(T, H, V, piece) || !ptr_ok(w) || !ptr_ok(dw) || !ptr_ok(ws)) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!ptr_ok(x) || !ptr_ok(labels) || !ptr_ok(lse) || !ptr_ok(dloss) || !ptr_ok(dx)))
+    return MOE_ERR_INVALID_ARG;
+  const Ws l = layout(T, H, V, piece);
+  if (ws_bytes < l.total) return MOE_ERR_WORKSPACE;
+  if (!device_is_gb300()) return MOE_ERR_UNSUPPORTED;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (T == 0) return status_of(cudaMemsetAsync(dw, 0, static_cast<size_t>(V) * H * 2, st));
+  int* status = static_cast<int*>(ws);
+  void* d = at<char>(ws, l.d);
+  void* xz = at<char>(ws, l.xz);
+  float* slabs = at<float>(ws, l.slabs);
+  const bool small = small_rows(T);
+  CeParams ce{};
+  ce.labels = labels;
+  ce.vocab = V;
+  ce.lse = lse;
+  ce.dloss = dloss;
+  count_launches(1);
+  MOE_TRY(launch_k(ce_scored_rows_kernel, T, 128, 0, st, static_cast<const uint4*>(x), labels, V, H / 8,
+                   static_cast<uint4*>(xz)));
+  const int per = kb_per_split(T, H, l.piece / 64);
+  for (int v0 = 0; v0 < V; v0 += l.piece) {
+    const int rows = V - v0 < l.piece ? V - v0 : l.piece;
+    const char* w_rows = static_cast<const char*>(w) + static_cast<size_t>(v0) * H * 2;
+    ce.v0 = v0;
+    if (small) {
+      MOE_TRY((gemm_logits<Epi::kCeGrad, false>(x, T, H, w_rows, rows, d, l.piece, ce, status, st)));
+      MOE_TRY(gemm_dx<false>(d, l.piece, T, w_rows, rows, H, per, slabs, l.slab_count, v0 > 0, status, st));
+    } else {
+      MOE_TRY((gemm_logits<Epi::kCeGrad, true>(x, T, H, w_rows, rows, d, l.piece, ce, status, st)));
+      MOE_TRY(gemm_dx<true>(d, l.piece, T, w_rows, rows, H, per, slabs, l.slab_count, v0 > 0, status, st));
+    }
+    MOE_TRY(gemm_dw(d, l.piece, T, xz, H, static_cast<char*>(dw) + static_cast<size_t>(v0) * H * 2, rows, status, st));
+  }
+  const long long n4 = static_cast<long long>(T) * H / 4;
+  count_launches(1);
+  MOE_TRY(launch_k(ce_dx_kernel, static_cast<unsigned>((n4 + 255) / 256), 256, 0, st,
+                   reinterpret_cast<const float4*>(slabs), l.slab_count, n4, static_cast<uint2*>(dx)));
+  return MOE_OK;
+}
+
+}  // extern "C"

@@ -34,6 +34,8 @@ enum class Sched : int {
   kRoutedM = 0,  // rows grouped by expert (padded offsets on device), K fixed
   kDenseM = 1,   // one group of m_rows rows
   kRoutedK = 2,  // contraction over each expert's rows (weight gradients)
+  kSplitK = 3,   // one group of m_rows rows, the contraction cut into parts of
+                 // kb_per_split k-blocks, each with an output slab of its own
 };
 
 enum class Epi : int {
@@ -41,6 +43,19 @@ enum class Epi : int {
   kStoreBf16 = 1,   // -> bf16
   kSwiglu = 2,      // z = [gate | up] -> h = g * silu(gate) * up (bf16), z saved (bf16)
   kSwigluBwd = 3,   // dh -> dz = [dgate_in | dup] (bf16) and partial <dh, h> per row
+  kCeStats = 4,     // logits -> per row and tile: maximum, sum of exponentials; the label's logit
+  kCeGrad = 5,      // logits -> gradient of the cross entropy (bf16)
+};
+
+// The vocabulary head's epilogues (tile columns = vocabulary entries).
+struct CeParams {
+  const int32_t* labels;   // [rows]; outside [0, vocab): the row is not scored
+  int vocab;               // entries of the whole vocabulary
+  int v0;                  // vocabulary entry of B's first row
+  float2* stats;           // kCeStats: [n_tiles][rows] (maximum, sum of exp(z - maximum))
+  float* label_logit;      // kCeStats: [rows], written where the label is in the vocabulary
+  const float* lse;        // kCeGrad: [rows]
+  const float* dloss;      // kCeGrad: [rows]
 };
 
 struct GemmParams {
@@ -114,6 +129,9 @@ struct GemmParams {
   int* cmb_count;                  // [T, n_tiles], zero between launches
   const __nv_bfloat16* cmb_shared; // [T, ldc] or nullptr
   __nv_bfloat16* cmb_y;            // [T, ldc]
+  int kb_per_split;                // kSplitK: k-blocks of one part
+  int c_add;                       // kSplitK: add to the slabs (1) or overwrite them (0)
+  CeParams ce;
 };
 
 template <int BN_, bool A_MN_, bool B_MN_, Sched S_, Epi EP_, int MX_ = 0, bool M256_ = false,
@@ -161,7 +179,8 @@ struct GemmCfg {
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
   // Outputs leave through TMA stores staged in shared memory (every epilogue
   // but the router's narrow fp32 logits, whose rows need not be 16-byte sized).
-  static constexpr bool TMA_OUT = !(EP == Epi::kStoreF32 && S == Sched::kDenseM);
+  // (The cross entropy's statistics are two values a row, stored directly.)
+  static constexpr bool TMA_OUT = !(EP == Epi::kStoreF32 && S == Sched::kDenseM) && EP != Epi::kCeStats;
   // Epilogue warps: four (one per TMEM lane quarter), or eight for 256-row
   // tiles, where the second four write rows 128..255 at the same time.
   // NVFP4 SwiGLU tiles (one accumulator, MMAs fast enough that the MMA warp
@@ -244,9 +263,15 @@ struct GemmCfg {
   static_assert(!GATHER || (M256 && !MX && !A_MN && S == Sched::kRoutedM && BK == 64),
                 "gathered A: bf16 256-row row-grouped tiles");
   static_assert(!WIDE_K || (A_MN && B_MN), "128-row k-blocks only for MN-major operands");
-  static_assert(!PAIR || (!M256 && !MX && TMA_OUT && BN == 256 &&
-                          (S == Sched::kRoutedK ? (A_MN && B_MN && EP == Epi::kStoreF32) : !A_MN)),
+  static_assert(!PAIR || (!M256 && !MX && (TMA_OUT || EP == Epi::kCeStats) && BN == 256 &&
+                          (S == Sched::kRoutedK
+                               ? (A_MN && B_MN && (EP == Epi::kStoreF32 || EP == Epi::kStoreBf16))
+                               : !A_MN)),
                 "CTA pairs: bf16, N = 256; row-grouped GEMMs with K-major A, or MN-major weight gradients");
+  static_assert(S != Sched::kSplitK || (!MX && !M256 && B_MN && EP == Epi::kStoreF32),
+                "split contraction: bf16, B stored [K, N], fp32 slabs");
+  static_assert((EP != Epi::kCeStats && EP != Epi::kCeGrad) || (!MX && !M256 && !B_MN && S == Sched::kDenseM),
+                "cross entropy: bf16 logits of one dense group");
   static_assert(SMEM_USED <= SMEM_BYTES && SMEM_BYTES <= 232448, "shared memory per CTA");
   static_assert(STAGES >= 2, "pipeline depth");
   static_assert((STAGES * (A_BYTES + B_BYTES) + SF_REGION) % 1024 == 0, "staging buffers 1024-byte aligned");
@@ -291,6 +316,9 @@ __device__ __forceinline__ int total_tiles(const GemmParams& p, const int* s_pof
     return (s_poff[p.E] / C::BM) * p.n_tiles;
   } else if constexpr (C::S == Sched::kDenseM) {
     return ((p.m_rows + C::TILE_M - 1) / C::TILE_M) * p.n_tiles;
+  } else if constexpr (C::S == Sched::kSplitK) {
+    const int splits = (p.k_len / C::BK + p.kb_per_split - 1) / p.kb_per_split;
+    return ((p.m_rows + C::TILE_M - 1) / C::TILE_M) * p.n_tiles * splits;
   } else {
     return p.E * p.m_tiles_w * p.n_tiles;
   }
@@ -337,6 +365,16 @@ __device__ __forceinline__ TileInfo decode_tile(const GemmParams& p, const int* 
     ti.half1 = C::ROWS256 && (ti.m0 + 128 < p.m_rows);
     ti.num_kb = p.k_len / C::BK;
     ti.k_row0 = 0;
+  } else if constexpr (C::S == Sched::kSplitK) {
+    const int mb = (p.m_rows + C::TILE_M - 1) / C::TILE_M;
+    const int per = mb * p.n_tiles;
+    ti.group = t / per;                      // the part of the contraction
+    const int r = t % per;
+    ti.n = r / mb;
+    ti.m0 = (r % mb) * C::TILE_M;
+    ti.half1 = C::ROWS256 && (ti.m0 + 128 < p.m_rows);
+    ti.k_row0 = ti.group * p.kb_per_split * C::BK;
+    ti.num_kb = min(p.kb_per_split, p.k_len / C::BK - ti.group * p.kb_per_split);
   } else {
     const int per = p.m_tiles_w * p.n_tiles;
     ti.group = t / per;
@@ -400,11 +438,17 @@ __device__ __forceinline__ void issue_loads(const CUtensorMap* tmA, const CUtens
     // A[m, k] = Abuf[k_row0 + k, m0 + m]  (MN-major, two 64-wide chunks)
     tma_load_2d(a_dst, tmA, bar, ti.m0, ti.k_row0 + k0);
     tma_load_2d(a_dst + 8192, tmA, bar, ti.m0 + 64, ti.k_row0 + k0);
+  } else if constexpr (C::S == Sched::kSplitK) {
+    tma_load_2d(a_dst, tmA, bar, ti.k_row0 + k0, ti.m0);
   } else if constexpr (!C::GATHER) {
     tma_load_2d(a_dst, tmA, bar, k0, ti.m0);
   }
   // ---- B
   if constexpr (C::S == Sched::kRoutedK) {
+    #pragma unroll
+    for (int j = 0; j < C::BN / 64; ++j)
+      tma_load_2d(b_dst + j * 8192, tmB, bar, ti.n * C::BN + j * 64, ti.k_row0 + k0);
+  } else if constexpr (C::S == Sched::kSplitK) {
     #pragma unroll
     for (int j = 0; j < C::BN / 64; ++j)
       tma_load_2d(b_dst + j * 8192, tmB, bar, ti.n * C::BN + j * 64, ti.k_row0 + k0);
@@ -499,6 +543,19 @@ struct Stager {
     __syncwarp();
     if (lane == 0) {
       tma_store_2d(map, buf + cur * BUF, x, y);
+      bulk_commit_group();
+    }
+    cur = (cur + 1 == NBUF) ? 0 : cur + 1;
+  }
+  // into slab z of a 3-D output, overwriting or adding to what it holds
+  __device__ __forceinline__ void flush_slab(const CUtensorMap* map, int x, int y, int z, bool add) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      if (add)
+        tma_reduce_add_3d(map, buf + cur * BUF, x, y, z);
+      else
+        tma_store_3d(map, buf + cur * BUF, x, y, z);
       bulk_commit_group();
     }
     cur = (cur + 1 == NBUF) ? 0 : cur + 1;
@@ -661,6 +718,106 @@ __device__ __forceinline__ void fused_combine_rows(const GemmParams& p, int y0, 
   }
 }
 
+// ---------------------------------------------------------------- cross entropy
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Statistics of one tile of logits: this lane's row, columns [n BN, n BN +
+// BN).  A running maximum m and sum s of 2^((z - m) log2 e), 32 columns at a
+// time; columns past the vocabulary count as -infinity.
+template <class C>
+__device__ __forceinline__ void ce_stats_tile(const GemmParams& p, const TileInfo& ti, uint32_t tmem_acc, int quarter,
+                                              int lane) {
+  const uint32_t t0 = tmem_acc + (static_cast<uint32_t>(quarter * 32) << 16);
+  const int row = ti.m0 + quarter * 32 + lane;
+  const bool row_ok = row < p.m_rows;
+  const int col0 = p.ce.v0 + ti.n * C::BN;
+  const int nv = min(C::BN, p.ce.vocab - col0);              // columns of this tile in the vocabulary
+  const int rel = (row_ok ? p.ce.labels[row] : -1) - col0;  // the label's column of this tile
+  float m = -INFINITY, s = 0.f;
+  #pragma unroll 1
+  for (int c0 = 0; c0 < nv; c0 += 32) {
+    uint32_t u[2][16];
+    load32(t0 + c0, u[0], u[1]);
+    float z[32];
+    #pragma unroll
+    for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(u[j >> 4][j & 15]);
+    if (c0 + 32 > nv) {
+      #pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (c0 + j >= nv) z[j] = -INFINITY;
+    }
+    float cm = z[0];
+    #pragma unroll
+    for (int j = 1; j < 32; ++j) cm = fmaxf(cm, z[j]);
+    const float mn = fmaxf(m, cm);
+    const float off = (mn == -INFINITY ? 0.f : mn) * kLog2e;   // (a row of -infinity: every term is zero)
+    float t[4] = {0.f, 0.f, 0.f, 0.f};
+    #pragma unroll
+    for (int j = 0; j < 32; ++j) t[j & 3] += ex2(fmaf(z[j], kLog2e, -off));
+    s = s * ex2(fmaf(m, kLog2e, -off)) + ((t[0] + t[1]) + (t[2] + t[3]));
+    m = mn;
+    const bool here = rel >= c0 && rel < c0 + 32 && rel < nv;
+    if (__any_sync(0xffffffffu, here)) {
+      float zl = 0.f;
+      #pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (rel - c0 == j) zl = z[j];
+      if (here) p.ce.label_logit[row] = zl;
+    }
+  }
+  if (row_ok) p.ce.stats[static_cast<long long>(ti.n) * p.m_rows + row] = make_float2(m, s);
+}
+
+// Gradient of one tile of logits: d = dloss (exp(z - lse) - [column == label])
+// in bf16, the operand type of the two products that follow; zero in rows
+// without a label and in columns past the vocabulary, whatever the logits.
+template <class C, class St>
+__device__ __forceinline__ void ce_grad_tile(const GemmParams& p, const TileInfo& ti, uint32_t tmem_acc, int quarter,
+                                             int lane, St& st, const CUtensorMap* tmC) {
+  const uint32_t t0 = tmem_acc + (static_cast<uint32_t>(quarter * 32) << 16);
+  const int y = ti.m0 + quarter * 32;
+  if (y >= p.m_rows) return;
+  const int row = y + lane;
+  const int col0 = p.ce.v0 + ti.n * C::BN;
+  const int nv = min(C::BN, p.ce.vocab - col0);
+  const int label = row < p.m_rows ? p.ce.labels[row] : -1;
+  const bool scored = label >= 0 && label < p.ce.vocab;
+  const int rel = label - col0;
+  const float off = scored ? p.ce.lse[row] * kLog2e : 0.f;
+  const float dl = scored ? p.ce.dloss[row] : 0.f;
+  #pragma unroll 1
+  for (int c0 = 0; c0 < C::BN; c0 += 64) {
+    const bool label_here = __any_sync(0xffffffffu, rel >= c0 && rel < c0 + 64);
+    const bool edge = c0 + 64 > nv;
+    st.begin();
+    #pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t u[2][16];
+      load32(t0 + c0 + 32 * h, u[0], u[1]);
+      float d[32];
+      #pragma unroll
+      for (int j = 0; j < 32; ++j) d[j] = ex2(fmaf(__uint_as_float(u[j >> 4][j & 15]), kLog2e, -off));
+      if (label_here) {
+        #pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (rel - c0 - 32 * h == j) d[j] -= 1.f;
+      }
+      #pragma unroll
+      for (int j = 0; j < 32; ++j) d[j] = scored ? d[j] * dl : 0.f;
+      if (edge) {
+        #pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (c0 + 32 * h + j >= nv) d[j] = 0.f;
+      }
+      #pragma unroll
+      for (int q = 0; q < 4; ++q)
+        st.put(4 * h + q, pack_bf16x2(d[8 * q], d[8 * q + 1]), pack_bf16x2(d[8 * q + 2], d[8 * q + 3]),
+               pack_bf16x2(d[8 * q + 4], d[8 * q + 5]), pack_bf16x2(d[8 * q + 6], d[8 * q + 7]));
+    }
+    st.flush(tmC, ti.n * C::BN + c0, y);
+  }
+}
+
 // Epilogue with TMA stores.  Rows of the tile: warp quarter q owns rows
 // 32q..32q+31, lane = row.  Dense tiles past the last row are clipped by TMA.
 template <class C>
@@ -676,6 +833,24 @@ __device__ __forceinline__ void epilogue_tile_tma(const GemmParams& p, const Til
   const bool no_mma = (ti.num_kb == 0);         // empty group (weight gradients): result is zero
 
   if constexpr (C::EP == Epi::kStoreF32) {      // weight gradients: [group*M + row, col] fp32
+    if constexpr (C::S == Sched::kSplitK) {     // [part][row][col], rows and columns past the end left out
+      const int y = ti.m0 + quarter * 32;
+      if (y >= p.m_rows) return;
+      #pragma unroll 1
+      for (int c0 = 0; c0 < C::BN; c0 += 32) {
+        const int x = ti.n * C::BN + c0;
+        if (x >= p.valid_cols) break;
+        uint32_t a[16], b[16];
+        load32(t0 + c0, a, b);
+        st.begin();
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) st.put(j, a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) st.put(4 + j, b[4 * j], b[4 * j + 1], b[4 * j + 2], b[4 * j + 3]);
+        st.flush_slab(tmC, x, y, ti.group, p.c_add != 0);
+      }
+      return;
+    }
     const int y = ti.group * p.m_rows + ti.m0 + quarter * 32;
     if constexpr (C::ACC_BUFS == 1 && C::BN == 256 && C::STAGING_BUFS >= 4) {
       if (release_bar != nullptr) {
@@ -847,6 +1022,9 @@ __device__ __forceinline__ void epilogue_tile_tma(const GemmParams& p, const Til
     }
     #pragma unroll 1
     for (int c0 = 0; c0 < C::BN; c0 += 64) {
+      if constexpr (C::S == Sched::kRoutedK) {  // (a head of any size: nothing past its rows and columns)
+        if (ti.n * C::BN + c0 >= p.valid_cols || y >= p.m_rows) break;
+      }
       uint32_t v[4][16];                        // 64 columns in one TMEM round trip
       #pragma unroll
       for (int h = 0; h < 4; ++h) tmem_ld_x16(t0 + c0 + 16 * h, v[h]);
@@ -1634,6 +1812,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           epilogue_tile_tma<C>(p, th, tmem_base + acc * C::ACC_COLS + part * C::BN, quarter, lane, st, &tmC, &tmC2,
                                &tempty_bar[acc], &released, al);
         }
+      } else if constexpr (C::EP == Epi::kCeStats) {
+        ce_stats_tile<C>(p, ti, tmem_base + acc * C::ACC_COLS, quarter, lane);
+      } else if constexpr (C::EP == Epi::kCeGrad) {
+        ce_grad_tile<C>(p, ti, tmem_base + acc * C::ACC_COLS, quarter, lane, st, &tmC);
       } else if constexpr (C::TMA_OUT) {
         epilogue_tile_tma<C>(p, ti, tmem_base + acc * C::ACC_COLS, quarter, lane, st, &tmC, &tmC2,
                              &tempty_bar[acc], &released, al, C::SPLIT_COLS ? part : 0);
@@ -1677,6 +1859,13 @@ __device__ __forceinline__ void issue_loads_pair(const CUtensorMap* tmA, const C
     tma_load_2d_pair(a_dst + C::MN_CHUNK, tmA, bar_cluster_addr, mr + 64, ti.k_row0 + k0);
     tma_load_2d_pair(b_dst, tmB, bar_cluster_addr, nr, ti.k_row0 + k0);
     tma_load_2d_pair(b_dst + C::MN_CHUNK, tmB, bar_cluster_addr, nr + 64, ti.k_row0 + k0);
+    return;
+  }
+  if constexpr (C::S == Sched::kSplitK) {
+    const int nr = ti.n * C::BN + 128 * static_cast<int>(rank);
+    tma_load_2d_pair(a_dst, tmA, bar_cluster_addr, ti.k_row0 + k0, ti.m0 + 128 * static_cast<int>(rank));
+    tma_load_2d_pair(b_dst, tmB, bar_cluster_addr, nr, ti.k_row0 + k0);
+    tma_load_2d_pair(b_dst + 8192, tmB, bar_cluster_addr, nr + 64, ti.k_row0 + k0);
     return;
   }
   tma_load_2d_pair(a_dst, tmA, bar_cluster_addr, k0, ti.m0 + 128 * static_cast<int>(rank));
@@ -1878,7 +2067,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       if (leader || ti.half1) {           // a half tile: the odd CTA's rows are not this expert's
         TileInfo th = ti;
         th.m0 += 128 * static_cast<int>(rank);
-        epilogue_tile_tma<C>(p, th, tmem_base + acc * C::ACC_COLS, quarter, lane, st, &tmC, &tmC2);
+        const uint32_t t_acc = tmem_base + acc * C::ACC_COLS;
+        if constexpr (C::EP == Epi::kCeStats)
+          ce_stats_tile<C>(p, th, t_acc, quarter, lane);
+        else if constexpr (C::EP == Epi::kCeGrad)
+          ce_grad_tile<C>(p, th, t_acc, quarter, lane, st, &tmC);
+        else
+          epilogue_tile_tma<C>(p, th, t_acc, quarter, lane, st, &tmC, &tmC2);
       }
       tc_fence_before_sync();
       __syncwarp();
