@@ -151,8 +151,15 @@ def ptr(t) -> int | None:
     return t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it (0.1 us against
+# 3 us of a call's 8-11 us on the host), where this torch offers it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def stream_ptr(stream=None) -> int | None:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
 

@@ -497,6 +497,37 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// Two fp32 values in one 64-bit register: each operation is the ordinary fp32
+// one on both, in one instruction.
+struct F32x2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F32x2 make_f32x2(float x, float y) {
+  F32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 split_f32x2(F32x2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F32x2 fma2(F32x2 a, F32x2 b, F32x2 c) {
+  F32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F32x2 add2(F32x2 a, F32x2 b) {
+  F32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F32x2 mul2(F32x2 a, F32x2 b) {
+  F32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+
 // 2^x, approximate (about 2 ulp; results below the normal range are zero).
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -506,5 +537,10 @@ __device__ __forceinline__ float ex2(float x) {
 
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+__device__ __forceinline__ F32x2 bf16x2_f32x2(uint32_t v) { return make_f32x2(bf16_lo(v), bf16_hi(v)); }
+__device__ __forceinline__ uint32_t pack_bf16x2(F32x2 a) {
+  const float2 f = split_f32x2(a);
+  return pack_bf16x2(f.x, f.y);
+}
 
 }  // namespace moe
