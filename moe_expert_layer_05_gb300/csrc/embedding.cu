@@ -11,9 +11,14 @@
 // own, and the row adds their sums in order.  The sums are fp32.
 //
 // Both directions are bound by HBM: the lookup by the rows it reads and
-// writes, the gradient mostly by the V x H fp32 words it writes.
+// writes, the gradient mostly by the V x H fp32 words it writes.  Measured on
+// one GB300 (a plain copy reaches 6.68 TB/s): lookup of 16384 x 4096 31 us
+// (6.24 TB/s); gradient of 16384 rows into 32000 x 7168 195 us (5.91 TB/s: sort
+// 17, whole chunks 9, rows 165); 1003 rows into 50001 x 1024 on top of `base`
+// 62 us (4.99 TB/s: the sort's two passes and its launch are 10 of them).
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "entry_checks.h"
@@ -23,35 +28,82 @@ namespace moe {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kDigitBits = 8;
+constexpr int kDigitBits = 9;                          // two passes up to V = 2^18
 constexpr int kBins = 1 << kDigitBits;
-constexpr int kSortThreads = 256;
+constexpr int kSortThreads = 512;
 constexpr int kSortItems = 8;
 constexpr int kSortTile = kSortThreads * kSortItems;   // pairs one block ranks
-constexpr int kChunk = 64;                             // sorted positions summed by one block
+constexpr int kChunk = 32;                             // sorted positions summed by one block
 
 // ---------------------------------------------------------------- lookup
-// One block per token.  An id outside [0, V) gives a zero row; -1 is padding,
-// any other one is reported.
-__global__ void __launch_bounds__(128) embedding_fwd_kernel(const int32_t* __restrict__ tokens,
+// An id outside [0, V) gives a zero row; -1 is padding, any other one is
+// reported.  A thread has four 16-byte loads on their way: four words of one
+// row (wide rows, one block each), or, with rows of up to 128 words, a word of
+// four rows (`lanes` threads a row, a power of two).
+template <bool WIDE>
+__global__ void __launch_bounds__(128) embedding_fwd_kernel(const int32_t* __restrict__ tokens, int n,
                                                             const uint4* __restrict__ table, int V, int words,
-                                                            float scale, uint4* __restrict__ out, int* status) {
+                                                            int lanes, float scale, uint4* __restrict__ out,
+                                                            int* status) {
   pdl_entry();
-  const int tok = tokens[blockIdx.x];
-  const bool ok = tok >= 0 && tok < V;
-  if (!ok && tok != -1 && threadIdx.x == 0) set_status(status, kErrBadIndex);
-  const uint4* src = table + static_cast<long long>(ok ? tok : 0) * words;
-  uint4* dst = out + static_cast<long long>(blockIdx.x) * words;
-  for (int c = threadIdx.x; c < words; c += blockDim.x) {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (ok) {
-      v = src[c];
-      v = make_uint4(pack_bf16x2(bf16_lo(v.x) * scale, bf16_hi(v.x) * scale),
-                     pack_bf16x2(bf16_lo(v.y) * scale, bf16_hi(v.y) * scale),
-                     pack_bf16x2(bf16_lo(v.z) * scale, bf16_hi(v.z) * scale),
-                     pack_bf16x2(bf16_lo(v.w) * scale, bf16_hi(v.w) * scale));
+  const int rows = 128 / lanes;                        // (narrow) rows of one of the four loads
+  int tok[4];
+  long long row[4];
+  #pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    row[i] = WIDE ? blockIdx.x : static_cast<long long>(blockIdx.x) * 4 * rows + i * rows + threadIdx.x / lanes;
+    tok[i] = (WIDE && i > 0) ? tok[0] : row[i] < n ? tokens[row[i]] : -1;
+    if ((tok[i] < -1 || tok[i] >= V) && (WIDE ? threadIdx.x == 0 && i == 0 : threadIdx.x % lanes == 0))
+      set_status(status, kErrBadIndex);
+    if (tok[i] >= V) tok[i] = -1;
+  }
+  for (int c0 = WIDE ? threadIdx.x : threadIdx.x % lanes; c0 < words; c0 += 4 * 128) {
+    uint4 v[4];
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = WIDE ? c0 + i * 128 : c0;
+      v[i] = tok[i] >= 0 && c < words ? table[static_cast<long long>(tok[i]) * words + c] : make_uint4(0, 0, 0, 0);
     }
-    dst[c] = v;
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = WIDE ? c0 + i * 128 : c0;
+      if (c < words && row[i] < n)
+        out[row[i] * words + c] = make_uint4(pack_bf16x2(bf16_lo(v[i].x) * scale, bf16_hi(v[i].x) * scale),
+                                             pack_bf16x2(bf16_lo(v[i].y) * scale, bf16_hi(v[i].y) * scale),
+                                             pack_bf16x2(bf16_lo(v[i].z) * scale, bf16_hi(v[i].z) * scale),
+                                             pack_bf16x2(bf16_lo(v[i].w) * scale, bf16_hi(v[i].w) * scale));
+    }
+  }
+}
+
+__device__ __forceinline__ void add_row8(float (&a)[8], const uint4& v) {
+  a[0] += bf16_lo(v.x); a[1] += bf16_hi(v.x);
+  a[2] += bf16_lo(v.y); a[3] += bf16_hi(v.y);
+  a[4] += bf16_lo(v.z); a[5] += bf16_hi(v.z);
+  a[6] += bf16_lo(v.w); a[7] += bf16_hi(v.w);
+}
+
+// Eight fp32 values to a 16-byte aligned place: one 32-byte store where it is
+// 32-byte aligned.
+__device__ __forceinline__ void store8(float* p, const float (&a)[8]) {
+  if ((reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
+    st_global_v8(p, a);
+  } else {
+    reinterpret_cast<float4*>(p)[0] = make_float4(a[0], a[1], a[2], a[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(a[4], a[5], a[6], a[7]);
+  }
+}
+
+// A row of the gradient without a token: base, or zero.  One warp.
+__device__ __forceinline__ void fill_row(long long v, int words, const uint4* __restrict__ base,
+                                         float* __restrict__ dtable) {
+  const int lane = threadIdx.x & 31;
+  const long long row = v * words;
+  #pragma unroll 4
+  for (int c = lane; c < words; c += 32) {
+    float a[8] = {};
+    if (base != nullptr) add_row8(a, base[row + c]);
+    store8(dtable + (row + c) * 8, a);
   }
 }
 
@@ -64,13 +116,148 @@ __device__ __forceinline__ uint32_t key_of(const int32_t* __restrict__ tokens, i
   return static_cast<uint32_t>(V);
 }
 
-// Digit counts of each tile of kSortTile pairs: hist[tile][bin].  The first
-// pass reads the tokens themselves (keys == nullptr) and marks every row of
-// the table as without a run.
+// Up to kClusterSort positions: the whole sort in one cluster of eight blocks.
+// Each block holds an eighth of the pairs, in registers while it ranks them and
+// in shared memory between the passes.  A pass ranks the pairs as
+// sort_scatter_kernel does, with the digit counts of every warp in shared
+// memory; the blocks read each other's counts and write the pairs to their
+// places in each other's shared memory, and the sorted pairs are copied out
+// in one piece.  (Written to their places in global memory they cost a sector
+// each.)
+constexpr int kCluster = 8;
+constexpr int kClusterThreads = 512;                  // (half an SM's registers: the fill runs beside it)
+constexpr int kClusterWarps = kClusterThreads / 32;
+constexpr int kClusterItems = 16;                     // pairs per thread at most
+constexpr int kClusterSort = kCluster * kClusterThreads * kClusterItems;
+__host__ __device__ constexpr int cluster_rounds(int n) {
+  return (n + kCluster * kClusterThreads - 1) / (kCluster * kClusterThreads);
+}
+size_t cluster_sort_smem(int n) {
+  return static_cast<size_t>(kClusterWarps) * kBins * 2 + static_cast<size_t>(cluster_rounds(n)) * kClusterThreads * 8;
+}
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_sort(const int32_t* __restrict__ tokens, int n, int V, int passes,
+                                             uint32_t* __restrict__ keys_out, int32_t* __restrict__ pos_out,
+                                             int* status, uint8_t* s_raw) {
+  __shared__ uint32_t s_total[kBins];                 // this block's pairs of each digit
+  __shared__ uint32_t s_base[kBins];                  // where they go
+  __shared__ int s_warp[kClusterWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t me = cluster_ctarank();
+  const int rounds = cluster_rounds(n), slice = rounds * kClusterThreads;
+  uint16_t* s_cnt = reinterpret_cast<uint16_t*>(s_raw);              // [warp][bin]
+  uint32_t* s_key = reinterpret_cast<uint32_t*>(s_cnt + kClusterWarps * kBins);
+  uint32_t* s_pos = s_key + slice;
+  uint16_t* my_cnt = s_cnt + warp * kBins;
+  const int mine = min(max(n - static_cast<int>(me) * slice, 0), slice);   // pairs of this block
+  const int w0 = warp * 32 * rounds + lane;                                // this lane's: w0, w0 + 32, ...
+  uint32_t key[kClusterItems], where[kClusterItems];
+  uint16_t rank[kClusterItems];
+  #pragma unroll
+  for (int j = 0; j < kClusterItems; ++j) {
+    const int i = w0 + j * 32, g = static_cast<int>(me) * slice + i;
+    key[j] = (j < rounds && i < mine) ? key_of(tokens, g, V, status) : 0xffffffffu;
+    where[j] = static_cast<uint32_t>(g);
+  }
+  for (int pass = 0; pass < passes; ++pass) {
+    const int shift = pass * kDigitBits;
+    for (int i = lane; i < kBins / 2; i += 32) reinterpret_cast<uint32_t*>(my_cnt)[i] = 0;
+    __syncwarp();
+    #pragma unroll
+    for (int j = 0; j < kClusterItems; ++j) {
+      if (j < rounds) {
+        const bool live = w0 + j * 32 < mine;
+        const int d = live ? static_cast<int>((key[j] >> shift) & (kBins - 1)) : kBins;
+        const unsigned peers = __match_any_sync(kFull, d);
+        const int lead = __ffs(peers) - 1;
+        int seen = 0;
+        if (live && lane == lead) {
+          seen = my_cnt[d];
+          my_cnt[d] = static_cast<uint16_t>(seen + __popc(peers));
+        }
+        seen = __shfl_sync(kFull, seen, lead);
+        rank[j] = static_cast<uint16_t>(seen + __popc(peers & ((1u << lane) - 1u)));
+        __syncwarp();
+      }
+    }
+    __syncthreads();
+    if (tid < kBins) {                    // bin tid: where each warp's pairs begin among this block's
+      uint32_t run = 0;
+      #pragma unroll 8
+      for (int w = 0; w < kClusterWarps; ++w) {
+        const uint32_t c = s_cnt[w * kBins + tid];
+        s_cnt[w * kBins + tid] = static_cast<uint16_t>(run);
+        run += c;
+      }
+      s_total[tid] = run;
+    }
+    cluster_sync();
+    int total = 0, before = 0;            // bin tid: pairs of all blocks, and of those before this one
+    if (tid < kBins) {
+      #pragma unroll
+      for (uint32_t r = 0; r < kCluster; ++r) {
+        const int c = static_cast<int>(ld_cluster_u32(mapa_shared(smem_u32(&s_total[tid]), r)));
+        total += c;
+        if (r < me) before += c;
+      }
+    }
+    int inc = total;
+    #pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(kFull, inc, d);
+      if (lane >= d) inc += u;
+    }
+    if (lane == 31) s_warp[warp] = inc;
+    __syncthreads();
+    if (tid < kBins) {
+      int lower = 0;
+      for (int w = 0; w < warp; ++w) lower += s_warp[w];
+      s_base[tid] = static_cast<uint32_t>(lower + inc - total + before);
+    }
+    __syncthreads();
+    #pragma unroll
+    for (int j = 0; j < kClusterItems; ++j) {
+      if (j < rounds && w0 + j * 32 < mine) {
+        const int d = static_cast<int>((key[j] >> shift) & (kBins - 1));
+        const uint32_t to = s_base[d] + my_cnt[d] + rank[j];
+        const uint32_t block = (to / kClusterThreads) / static_cast<uint32_t>(rounds);
+        const uint32_t at = to - block * static_cast<uint32_t>(slice);
+        st_cluster_u32(mapa_shared(smem_u32(s_key + at), block), key[j]);
+        st_cluster_u32(mapa_shared(smem_u32(s_pos + at), block), where[j]);
+      }
+    }
+    cluster_sync();                       // every block's pairs are in their places
+    if (pass + 1 < passes) {
+      #pragma unroll
+      for (int j = 0; j < kClusterItems; ++j) {
+        const int i = w0 + j * 32;
+        if (j < rounds && i < mine) {
+          key[j] = s_key[i];
+          where[j] = s_pos[i];
+        }
+      }
+    }
+  }
+  const long long g0 = static_cast<long long>(me) * slice;
+  for (int i = tid; i < mine; i += kClusterThreads) {
+    keys_out[g0 + i] = s_key[i];
+    pos_out[g0 + i] = static_cast<int32_t>(s_pos[i]);
+  }
+}
+
+// More positions: two launches a pass.  Digit counts of each tile of kSortTile
+// pairs: hist[tile][bin].  The first pass reads the tokens themselves (keys ==
+// nullptr).
 __global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(const int32_t* __restrict__ tokens,
                                                                  const uint32_t* __restrict__ keys, int n, int V,
-                                                                 int shift, int32_t* __restrict__ hist,
-                                                                 int32_t* __restrict__ first, int* status) {
+                                                                 int shift, int32_t* __restrict__ hist, int* status) {
   pdl_entry();
   __shared__ int s_cnt[kBins];
   s_cnt[threadIdx.x] = 0;
@@ -86,11 +273,6 @@ __global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(const int32_t* 
   }
   __syncthreads();
   hist[static_cast<long long>(blockIdx.x) * kBins + threadIdx.x] = s_cnt[threadIdx.x];
-  if (keys == nullptr) {
-    const long long stride = static_cast<long long>(gridDim.x) * kSortThreads;
-    for (long long v = static_cast<long long>(blockIdx.x) * kSortThreads + threadIdx.x; v < V; v += stride)
-      first[v] = -1;
-  }
 }
 
 // Moves the pairs of one tile to their places for this digit, keeping the
@@ -180,87 +362,210 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(const int32_
   }
 }
 
-// ---------------------------------------------------------------- runs
-__device__ __forceinline__ void add_row8(float (&a)[8], const uint4& v) {
-  a[0] += bf16_lo(v.x); a[1] += bf16_hi(v.x);
-  a[2] += bf16_lo(v.y); a[3] += bf16_hi(v.y);
-  a[4] += bf16_lo(v.z); a[5] += bf16_hi(v.z);
-  a[6] += bf16_lo(v.w); a[7] += bf16_hi(v.w);
-}
-
-// Block (c, j): chunk c of the sorted positions, words [128 j, 128 j + 128) of
-// the rows.  Marks where each token's run begins and, for a whole chunk of
-// one token, leaves the sum of its rows in part[c].
-__global__ void __launch_bounds__(128) embedding_runs_kernel(const uint32_t* __restrict__ keys,
-                                                             const int32_t* __restrict__ pos, int n, int V, int words,
-                                                             const uint4* __restrict__ dy, int32_t* __restrict__ first,
-                                                             float4* __restrict__ part) {
+// ---------------------------------------------------------------- rows
+// First launch (up to kClusterSort positions): the first cluster sorts; the
+// other blocks clear the flags of the rows that have a token.
+constexpr int kClearRows = 1 << 17;     // flags one other cluster clears
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kClusterThreads)
+    cluster_sort_kernel(const int32_t* __restrict__ tokens, int n, int V, int passes, uint32_t* __restrict__ keys_out,
+                        int32_t* __restrict__ pos_out, uint8_t* __restrict__ has, int* status) {
   pdl_entry();
-  __shared__ int s_pos[kChunk];
-  const int i0 = blockIdx.x * kChunk, tid = threadIdx.x;
-  const int end = min(n, i0 + kChunk);
-  if (tid < end - i0) {
-    const uint32_t k = keys[i0 + tid];
-    s_pos[tid] = pos[i0 + tid];
-    if (blockIdx.y == 0 && k < static_cast<uint32_t>(V) && (i0 + tid == 0 || keys[i0 + tid - 1] != k))
-      first[k] = i0 + tid;
+  extern __shared__ __align__(16) uint8_t s_raw[];
+  if (blockIdx.x < kCluster) {
+    cluster_sort(tokens, n, V, passes, keys_out, pos_out, status, s_raw);
+    return;
   }
-  __syncthreads();
-  if (end - i0 < kChunk || keys[i0] != keys[end - 1] || keys[i0] >= static_cast<uint32_t>(V)) return;
-  const int c = blockIdx.y * 128 + tid;
-  if (c >= words) return;
-  float a[8] = {};
-  #pragma unroll 8
-  for (int r = 0; r < kChunk; ++r) add_row8(a, dy[static_cast<long long>(s_pos[r]) * words + c]);
-  float4* o = part + (static_cast<long long>(blockIdx.x) * words + c) * 2;
-  o[0] = make_float4(a[0], a[1], a[2], a[3]);
-  o[1] = make_float4(a[4], a[5], a[6], a[7]);
+  const int block = blockIdx.x - kCluster, blocks = gridDim.x - kCluster;
+  for (int v = block * kClusterThreads + threadIdx.x; v < V; v += blocks * kClusterThreads) has[v] = 0;
 }
 
-// Row v of the gradient, by one block (grid x: rows, y: columns): the row's
-// run is its positions up to a chunk border, whole chunks, and the rest.
-__global__ void __launch_bounds__(128) embedding_rows_kernel(const uint32_t* __restrict__ keys,
-                                                             const int32_t* __restrict__ pos, int n, int words,
-                                                             const uint4* __restrict__ dy,
-                                                             const int32_t* __restrict__ first,
-                                                             const float4* __restrict__ part,
-                                                             const uint4* __restrict__ base, float scale,
-                                                             float4* __restrict__ dtable) {
+// For more positions: the flags of the rows that have a token, cleared here and
+// set by embedding_chunks_kernel.
+__global__ void __launch_bounds__(256) clear_has_kernel(uint8_t* __restrict__ has, int V) {
   pdl_entry();
-  const uint32_t v = blockIdx.x;
-  const int c = blockIdx.y * 128 + threadIdx.x;
+  const int v = blockIdx.x * 256 + threadIdx.x;
+  if (v < V) has[v] = 0;
+}
+
+// Block q: chunk c = q / cols of the sorted positions, words [128 j, 128 j +
+// 128), j = q % cols, of the rows.  Flags the rows that have a token and, for a
+// whole chunk of one token, leaves the sum of its rows in part[c].
+__global__ void __launch_bounds__(128) embedding_chunks_kernel(const uint32_t* __restrict__ keys,
+                                                               const int32_t* __restrict__ pos, int n, int V, int words,
+                                                               int cols, const uint4* __restrict__ dy,
+                                                               uint8_t* __restrict__ has, float* __restrict__ part) {
+  pdl_entry();
+  const int chunk = blockIdx.x / cols, col = blockIdx.x % cols;
+  const int i0 = chunk * kChunk, tid = threadIdx.x;
+  const int end = min(n, i0 + kChunk);
+  if (col == 0 && i0 + tid < end) {
+    const uint32_t k = keys[i0 + tid];
+    if (k < static_cast<uint32_t>(V)) has[k] = 1;
+  }
+  const uint32_t k0 = keys[i0], k1 = keys[end - 1];
+  if (end - i0 < kChunk || k0 != k1 || k0 >= static_cast<uint32_t>(V)) return;
+  const int c = col * 128 + tid;
   if (c >= words) return;
   float a[8] = {};
-  int i = first[v];
-  if (i >= 0) {
-    while (i < n && keys[i] == v) {
-      if (i % kChunk == 0 && i + kChunk <= n && keys[i + kChunk - 1] == v) {
-        const float4* p = part + (static_cast<long long>(i / kChunk) * words + c) * 2;
-        const float4 p0 = p[0], p1 = p[1];
-        a[0] += p0.x; a[1] += p0.y; a[2] += p0.z; a[3] += p0.w;
-        a[4] += p1.x; a[5] += p1.y; a[6] += p1.z; a[7] += p1.w;
-        i += kChunk;
-      } else {
-        add_row8(a, dy[static_cast<long long>(pos[i]) * words + c]);
-        ++i;
-      }
+  #pragma unroll
+  for (int r0 = 0; r0 < kChunk; r0 += 8) {
+    uint4 d[8];
+    #pragma unroll
+    for (int r = 0; r < 8; ++r) d[r] = dy[static_cast<long long>(pos[i0 + r0 + r]) * words + c];
+    #pragma unroll
+    for (int r = 0; r < 8; ++r) add_row8(a, d[r]);
+  }
+  store8(part + (static_cast<long long>(chunk) * words + c) * 8, a);
+}
+
+// Two kinds of blocks, taking turns as long as there are both.  One, (b, j):
+// the rows whose runs begin at sorted positions [4 b, 4 b + 4), words [128 j,
+// 128 j + 128).  The batch's rows of dy (and of base) are loaded together; a run
+// that goes on past it is followed through the positions up to the next chunk,
+// the sums of the whole chunks, and the positions in the chunk where it ends --
+// so a block reads at most 62 rows of dy, however often a token occurs.  The
+// other fills those of fill_rows rows that have no token.
+constexpr int kBatch = 4;
+__global__ void __launch_bounds__(128, 8) embedding_rows_kernel(const uint32_t* __restrict__ keys,
+                                                             const int32_t* __restrict__ pos, int n, int V, int words,
+                                                             int cols, int run_blocks, const uint4* __restrict__ dy,
+                                                             const uint8_t* __restrict__ has,
+                                                             const float4* __restrict__ part, int fill_rows,
+                                                             const uint4* __restrict__ base, float scale,
+                                                             float* __restrict__ dtable) {
+  pdl_entry();
+  const int tid = threadIdx.x;
+  int block = blockIdx.x;
+  {
+    const int turns = min(run_blocks, static_cast<int>(gridDim.x) - run_blocks);
+    bool fills = run_blocks == turns;                  // the kind that is left after the turns
+    if (block < 2 * turns) {
+      fills = block & 1;
+      block >>= 1;
+    } else {
+      block -= turns;
     }
+    if (fills) {
+      const long long v0 = static_cast<long long>(block) * fill_rows;
+      for (int r = tid >> 5; r < fill_rows; r += 4)
+        if (v0 + r < V && has[v0 + r] == 0) fill_row(v0 + r, words, base, dtable);
+      return;
+    }
+  }
+  const int c = block % cols * 128 + tid;
+  block /= cols;
+  const int i0 = block * kBatch, len = min(n - i0, kBatch);
+  if (c >= words) return;
+  const uint32_t none = static_cast<uint32_t>(V);   // keys from here on are no token
+  uint32_t key[kBatch];
+  int at[kBatch];
+  const uint32_t before = i0 > 0 ? keys[i0 - 1] : 0xffffffffu;
+  #pragma unroll
+  for (int u = 0; u < kBatch; ++u) {
+    key[u] = u < len ? keys[i0 + u] : none;
+    at[u] = u < len ? pos[i0 + u] : 0;
+  }
+  float a[8] = {};
+  auto row_out = [&](uint32_t v, const uint4& b) {
     #pragma unroll
     for (int j = 0; j < 8; ++j) a[j] *= scale;
+    add_row8(a, b);
+    store8(dtable + (static_cast<long long>(v) * words + c) * 8, a);
+    #pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] = 0.f;
+  };
+  auto whole = [&](int i, uint32_t k) { return i % kChunk == 0 && i + kChunk <= n && keys[i + kChunk - 1] == k; };
+  uint4 d[kBatch], b[kBatch];
+  #pragma unroll
+  for (int u = 0; u < kBatch; ++u) {
+    d[u] = b[u] = make_uint4(0, 0, 0, 0);
+    const bool mine = key[u] < none && key[u] != before;
+    if (mine) d[u] = dy[static_cast<long long>(at[u]) * words + c];
+    if (mine && base != nullptr && (u == 0 || key[u] != key[u - 1]))
+      b[u] = base[static_cast<long long>(key[u]) * words + c];
   }
-  if (base != nullptr) add_row8(a, base[static_cast<long long>(v) * words + c]);
-  float4* o = dtable + (static_cast<long long>(v) * words + c) * 2;
-  o[0] = make_float4(a[0], a[1], a[2], a[3]);
-  o[1] = make_float4(a[4], a[5], a[6], a[7]);
+  uint32_t cur = none;                    // the run being summed (none: not yet one that begins here)
+  uint4 cur_base = make_uint4(0, 0, 0, 0);
+  int i = i0 + len;                       // where it goes on
+  if (key[0] < none && key[0] != before && whole(i0, key[0])) {
+    cur = key[0];                         // (a whole chunk: by its sum, below)
+    cur_base = b[0];
+    i = i0;
+  } else {
+    #pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (key[u] != before && key[u] != cur) {
+        if (cur < none) row_out(cur, cur_base);
+        cur = key[u];
+        cur_base = b[u];
+      }
+      if (cur < none && key[u] == cur) add_row8(a, d[u]);
+    }
+  }
+  if (cur >= none) return;
+  // single positions up to `stop` (a chunk border or the end); false where the run ends
+  auto follow = [&](int stop) {
+    while (i < stop) {
+      uint32_t k[kBatch];
+      uint4 e[kBatch];
+      #pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        k[u] = i + u < stop ? keys[i + u] : none;
+        at[u] = i + u < stop ? pos[i + u] : 0;
+      }
+      #pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (k[u] == cur) e[u] = dy[static_cast<long long>(at[u]) * words + c];
+      #pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        if (k[u] == cur) {
+          add_row8(a, e[u]);
+          ++i;
+        }
+      }
+      if (k[kBatch - 1] != cur) return i == stop;
+    }
+    return true;
+  };
+  if (follow(min(n, (i + kChunk - 1) / kChunk * kChunk))) {
+    // whole chunks, four on their way at a time, then the chunk it ends in
+    for (int more = kBatch; more == kBatch;) {
+      const int chunk = i / kChunk;
+      uint32_t k[kBatch];
+      #pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const long long last = static_cast<long long>(chunk + u + 1) * kChunk - 1;
+        k[u] = last < n ? keys[last] : none;
+      }
+      more = 0;
+      #pragma unroll
+      for (int u = 0; u < kBatch; ++u) more += k[u] == cur ? 1 : 0;    // (sorted: the first ones)
+      float4 p[kBatch][2];
+      #pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        if (u < more) {
+          const float4* src = part + (static_cast<long long>(chunk + u) * words + c) * 2;
+          p[u][0] = src[0];
+          p[u][1] = src[1];
+        }
+      }
+      #pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        if (u < more) {
+          a[0] += p[u][0].x; a[1] += p[u][0].y; a[2] += p[u][0].z; a[3] += p[u][0].w;
+          a[4] += p[u][1].x; a[5] += p[u][1].y; a[6] += p[u][1].z; a[7] += p[u][1].w;
+        }
+      }
+      i += more * kChunk;
+    }
+    follow(min(n, i + kChunk));
+  }
+  row_out(cur, cur_base);
 }
 
 // ---------------------------------------------------------------- workspace
-// Tiles of the sort; one where there is nothing to sort (its launch still
-// marks the table's rows).
-int sort_tiles(int n) { return n > 0 ? (n + kSortTile - 1) / kSortTile : 1; }
-
 struct Ws {
-  size_t keys[2], pos[2], hist, first, part, total;
+  size_t keys[2], pos[2], hist, has, part, total;
 };
 Ws layout(int n, int V, int H) {
   Ws w;
@@ -275,8 +580,8 @@ Ws layout(int n, int V, int H) {
     w.keys[i] = take(N * 4);
     w.pos[i] = take(N * 4);
   }
-  w.hist = take(static_cast<size_t>(sort_tiles(n)) * kBins * 4);
-  w.first = take(static_cast<size_t>(V) * 4);
+  w.hist = take((N + kSortTile - 1) / kSortTile * kBins * 4);
+  w.has = take(V);
   w.part = take(N / kChunk * H * 4);
   w.total = off;
   return w;
@@ -285,6 +590,18 @@ Ws layout(int n, int V, int H) {
 template <class T>
 T* at(void* ws, size_t off) {
   return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
+}
+
+// Once per device: the cluster sort's shared memory.
+cudaError_t sort_attr() {
+  static std::atomic<bool> set[64];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (set[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(cluster_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(cluster_sort_smem(kClusterSort)));
+  if (e == cudaSuccess) set[dev].store(true, std::memory_order_release);
+  return e;
 }
 
 constexpr int kMaxTokens = 1 << 24, kMaxVocab = 1 << 24;
@@ -311,8 +628,14 @@ moe_status moe_embedding_forward(const int32_t* tokens, int32_t n, const void* t
   if (!device_is_gb300()) return MOE_ERR_UNSUPPORTED;
   if (n == 0) return MOE_OK;
   count_launches(1);
-  return status_of(launch_k(embedding_fwd_kernel, n, 128, 0, static_cast<cudaStream_t>(stream), tokens,
-                            static_cast<const uint4*>(table), V, H / 8, scale, static_cast<uint4*>(out),
+  const int words = H / 8;
+  const bool wide = words > 128;
+  int lanes = 128;
+  while (!wide && lanes / 2 >= words) lanes /= 2;
+  const int per_block = wide ? 1 : 4 * (128 / lanes);
+  return status_of(launch_k(wide ? embedding_fwd_kernel<true> : embedding_fwd_kernel<false>,
+                            (n + per_block - 1) / per_block, 128, 0, static_cast<cudaStream_t>(stream), tokens, n,
+                            static_cast<const uint4*>(table), V, words, lanes, scale, static_cast<uint4*>(out),
                             static_cast<int*>(ws)));
 }
 
@@ -325,38 +648,58 @@ moe_status moe_embedding_backward(const int32_t* tokens, int32_t n, const void* 
   if (!device_is_gb300()) return MOE_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int* status = static_cast<int*>(ws);
-  int32_t* first = at<int32_t>(ws, w.first);
-  int32_t* hist = at<int32_t>(ws, w.hist);
-  const int tiles = sort_tiles(n);
+  const int words = H / 8;
+  const uint4* b16 = static_cast<const uint4*>(base);
+  const int cols = (words + 127) / 128;
+  uint8_t* has = at<uint8_t>(ws, w.has);
+  int passes = 1;                                    // digits of the keys 0 .. V
+  while (passes * kDigitBits < 32 && (V >> (passes * kDigitBits)) != 0) ++passes;
   int cur = 0, launches = 0;
-  // digits of the keys 0 .. V
-  for (int shift = 0; shift < 32 && (shift == 0 || (V >> shift) != 0); shift += kDigitBits) {
-    const uint32_t* keys = shift == 0 ? nullptr : at<uint32_t>(ws, w.keys[cur]);
-    const int32_t* pos = shift == 0 ? nullptr : at<int32_t>(ws, w.pos[cur]);
-    const int to = shift == 0 ? 0 : cur ^ 1;
-    if (launch_k(sort_hist_kernel, tiles, kSortThreads, 0, st, tokens, keys, n, V, shift, hist, first, status) !=
-            cudaSuccess ||
-        launch_k(sort_scatter_kernel, tiles, kSortThreads, 0, st, tokens, keys, pos, n, V, shift, hist,
-                 at<uint32_t>(ws, w.keys[to]), at<int32_t>(ws, w.pos[to])) != cudaSuccess)
+  if (n <= kClusterSort) {
+    if (sort_attr() != cudaSuccess) return MOE_ERR_CUDA;
+    const int grid = (1 + (V + kClearRows - 1) / kClearRows) * kCluster;
+    if (launch_k(cluster_sort_kernel, grid, kClusterThreads, cluster_sort_smem(n), st, tokens, n, V, passes,
+                 at<uint32_t>(ws, w.keys[0]), at<int32_t>(ws, w.pos[0]), has, status) != cudaSuccess)
       return MOE_ERR_CUDA;
-    launches += 2;
-    cur = to;
+    launches = 1;
+  } else {
+    int32_t* hist = at<int32_t>(ws, w.hist);
+    const int tiles = (n + kSortTile - 1) / kSortTile;
+    if (launch_k(clear_has_kernel, (V + 255) / 256, 256, 0, st, has, V) != cudaSuccess) return MOE_ERR_CUDA;
+    for (int pass = 0; pass < passes; ++pass) {
+      const uint32_t* keys = pass == 0 ? nullptr : at<uint32_t>(ws, w.keys[cur]);
+      const int32_t* pos = pass == 0 ? nullptr : at<int32_t>(ws, w.pos[cur]);
+      const int to = pass == 0 ? 0 : cur ^ 1, shift = pass * kDigitBits;
+      if (launch_k(sort_hist_kernel, tiles, kSortThreads, 0, st, tokens, keys, n, V, shift, hist, status) !=
+              cudaSuccess ||
+          launch_k(sort_scatter_kernel, tiles, kSortThreads, 0, st, tokens, keys, pos, n, V, shift, hist,
+                   at<uint32_t>(ws, w.keys[to]), at<int32_t>(ws, w.pos[to])) != cudaSuccess)
+        return MOE_ERR_CUDA;
+      cur = to;
+    }
+    launches = 1 + 2 * passes;
   }
   const uint32_t* keys = at<uint32_t>(ws, w.keys[cur]);
   const int32_t* pos = at<int32_t>(ws, w.pos[cur]);
-  const int words = H / 8;
-  const unsigned cols = (words + 127) / 128;
-  if (n > 0) {
-    if (launch_k(embedding_runs_kernel, dim3((n + kChunk - 1) / kChunk, cols), 128, 0, st, keys, pos, n, V, words,
-                 static_cast<const uint4*>(dy), first, at<float4>(ws, w.part)) != cudaSuccess)
+  const uint4* dy16 = static_cast<const uint4*>(dy);
+  const long long sums = static_cast<long long>((n + kChunk - 1) / kChunk) * cols;
+  const long long runs = static_cast<long long>((n + kBatch - 1) / kBatch) * cols;
+  const int fill_rows = words * 32 >= 65536 ? 1 : 65536 / (words * 32);      // 64 KB a block
+  const long long fills = (static_cast<long long>(V) + fill_rows - 1) / fill_rows;
+  if (sums > 0) {
+    if (launch_k(embedding_chunks_kernel, static_cast<unsigned>(sums), 128, 0, st, keys, pos, n, V, words, cols, dy16,
+                 has, at<float>(ws, w.part)) != cudaSuccess)
       return MOE_ERR_CUDA;
     ++launches;
   }
-  if (launch_k(embedding_rows_kernel, dim3(V, cols), 128, 0, st, keys, pos, n, words, static_cast<const uint4*>(dy),
-               first, at<float4>(ws, w.part), static_cast<const uint4*>(base), scale,
-               reinterpret_cast<float4*>(dtable)) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  count_launches(launches + 1);
+  if (runs + fills > 0) {
+    if (launch_k(embedding_rows_kernel, static_cast<unsigned>(runs + fills), 128, 0, st, keys, pos, n, V, words, cols,
+                 static_cast<int>(runs), dy16, has, at<float4>(ws, w.part), fill_rows, b16, scale,
+                 dtable) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    ++launches;
+  }
+  count_launches(launches);
   return MOE_OK;
 }
 

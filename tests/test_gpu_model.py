@@ -79,7 +79,7 @@ def test_embedding_forward_exact(lib, n, V, H, scale):
 
 @pytest.mark.parametrize("n,V,H", [(0, 7, 64), (1, 1, 8), (1, 1000, 128), (63, 10, 64), (64, 10, 64), (65, 3, 1000),
                                    (2048, 256, 64), (2049, 255, 72), (5000, 70000, 64), (16384, 700, 256),
-                                   (20011, 50001, 128), (70000, 65536, 16)])
+                                   (20011, 50001, 128), (70000, 65536, 16), (16385, 300_000, 8), (65536, 40_000, 8), (65537, 40_001, 8)])
 @pytest.mark.parametrize("kind", ["random", "zipf", "same", "none"])
 @pytest.mark.parametrize("tied", [False, True])
 def test_embedding_backward(lib, n, V, H, kind, tied):
@@ -97,6 +97,25 @@ def test_embedding_backward(lib, n, V, H, kind, tied):
     api.moe_embedding_backward(*args, again, ws, scale=scale, base=base_d)
     assert torch.equal(dt, again)                       # the same bits on a used workspace
     assert api.moe_read_device_status(ws) == 0
+
+
+def test_embedding_backward_at_16_byte_alignment(lib):
+    """Buffers that start 16 bytes into an allocation: the least the calls ask for."""
+    n, V, H = 300, 40, 72
+    rng = np.random.default_rng(8)
+    tok, dy, base = _tokens(rng, n, V, "zipf"), _bf(rng, n, H), _bf(rng, V, H)
+    flat = lambda *shape, dtype, off: torch.full((int(np.prod(shape)) + off,), float("nan"), dtype=dtype,   # noqa: E731
+                                                 device=DEV)[off:].view(*shape)
+    dt, dyd, based = flat(V, H, dtype=torch.float32, off=4), flat(n, H, dtype=BF, off=8), flat(V, H, dtype=BF, off=8)
+    dyd.copy_(dy), based.copy_(base)
+    tokd = torch.zeros(n + 4, dtype=torch.int32, device=DEV)[4:]
+    tokd.copy_(torch.from_numpy(tok))
+    need = api.moe_embedding_workspace_bytes(n, V, H)
+    ws = torch.full((need + 16,), 0xFF, dtype=torch.uint8, device=DEV)[16:]
+    api.moe_workspace_init(ws[:256])
+    api.moe_embedding_backward(tokd, dyd, dt, ws, base=based)
+    ref, mag, count = M.embedding_grad(tok.astype(np.int64), f64(dy), V, 1.0, f64(base))
+    _within(f64(dt), ref, (count[:, None] + 4) * U * mag, "dtable")
 
 
 def test_embedding_bad_ids_are_reported_and_left_out(lib):

@@ -76,7 +76,7 @@ def test_small_workspaces_refused():
     lib = api.load()
     for n, V, H in ((0, 8, 8), (1, 8, 8), (1000, 5003, 1000), (100000, 100, 64)):
         need = lib.moe_embedding_workspace_bytes(n, V, H)
-        assert need >= 256 + 16 * n + 4 * V + 1024           # one tile of digit counts at least
+        assert need >= 256 + 16 * n + V
         assert lib.moe_embedding_backward(16, n, 16, V, H, 1.0, None, 16, 16, need - 1, None) == -4
     for T, H in ((1, 8), (5000, 7168)):
         need = lib.moe_layer_norm_workspace_bytes(T, H)
