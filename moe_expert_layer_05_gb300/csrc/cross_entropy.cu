@@ -31,37 +31,53 @@ namespace {
 constexpr int kTile = 256;           // vocabulary entries of one logits tile
 constexpr int kMaxTokens = 1 << 24, kMaxVocab = 1 << 24;
 constexpr int kMaxSlabs = 16;
+constexpr int kFewRows = 2;          // tokens up to which the logits are matrix-vector products
+constexpr int kFewBlocks = 304;      // their blocks: two on each SM
 
-// Elements of d kept at a time where the caller names no piece: 128 MB of
-// bf16, within the L2's size.
-constexpr long long kPieceElements = 1LL << 26;
+// Elements of d kept at a time where the caller names no piece: 256 MB of bf16.
+constexpr long long kPieceElements = 1LL << 27;
 constexpr int kMinPiece = 4096;
 
 int round_up(int v, int m) { return (v + m - 1) / m * m; }
 
+// Vocabulary entries of one piece: whole tiles, the pieces as even as they come.
 int piece_of(int T, int V, int piece) {
+  long long most = piece;
   if (piece <= 0) {
-    const long long p = kPieceElements / (T > 0 ? T : 1) / kTile * kTile;
-    piece = p < kMinPiece ? kMinPiece : p > (1 << 24) ? (1 << 24) : static_cast<int>(p);
+    most = kPieceElements / (T > 0 ? T : 1);
+    if (most < kMinPiece) most = kMinPiece;
   }
-  const int all = round_up(V, kTile);
-  return piece < all ? round_up(piece, kTile) : all;
+  const int tiles = (V + kTile - 1) / kTile;
+  const long long per = most < kTile ? 1 : piece > 0 ? (most + kTile - 1) / kTile : most / kTile;
+  const int pieces = static_cast<int>((tiles + per - 1) / per);
+  return (tiles + pieces - 1) / pieces * kTile;
 }
 
 // Up to 128 tokens the logits and dx run on 128-row tiles of one CTA,
 // otherwise on 256-row tiles of CTA pairs.
 bool small_rows(int T) { return T <= 128; }
 
-// Parts of dx's contraction over a piece of kb k-blocks: about two tiles for
-// every CTA (or pair), at least 8 k-blocks each.
+// k-blocks of one part of dx's contraction over kb k-blocks.  Its output has
+// few tiles (T x H), so whole rounds of them leave SMs idle: the contraction is
+// cut into as many parts as make rounds x (part + a tile's start and end, some
+// 8 k-blocks) least.  At T = 4096, H = 4096 (256 tiles on 76 pairs) two parts
+// take 7 rounds of half the length instead of 4.
 int kb_per_split(int T, int H, int kb) {
   const int units = small_rows(T) ? 152 : 76;
   const int tiles = (small_rows(T) ? 1 : (T + 255) / 256) * ((H + kTile - 1) / kTile);
-  int splits = 2 * units / tiles;
-  if (splits > kMaxSlabs) splits = kMaxSlabs;
-  if (splits > kb / 8) splits = kb / 8;
-  if (splits < 1) splits = 1;
-  return (kb + splits - 1) / splits;
+  int best = kb;
+  long long least = -1;
+  for (int splits = 1; splits <= kMaxSlabs && splits <= kb; ++splits) {
+    const int per = (kb + splits - 1) / splits;
+    const int parts = (kb + per - 1) / per;
+    const long long rounds = (static_cast<long long>(tiles) * parts + units - 1) / units;
+    const long long cost = rounds * (per + 8) + parts;        // (a slab more to write and to add)
+    if (least < 0 || cost < least) {
+      least = cost;
+      best = per;
+    }
+  }
+  return best;
 }
 
 struct Ws {
@@ -79,7 +95,9 @@ Ws layout(int T, int H, int V, int piece) {
     return o;
   };
   const size_t rows = T;
-  w.stats = take(static_cast<size_t>((V + kTile - 1) / kTile) * rows * sizeof(float2));
+  size_t parts = 2 * ((V + kTile - 1) / kTile);
+  if (T <= kFewRows && parts < kFewBlocks) parts = kFewBlocks;
+  w.stats = take(parts * rows * sizeof(float2));
   w.label_logit = take(rows * 4);
   end = off;
   off = entry::kStatusBytes;
@@ -115,6 +133,10 @@ cudaError_t gemm_logits(const void* x, int T, int H, const void* w_rows, int row
   p.n_tiles = (rows + kTile - 1) / kTile;
   p.rows_cap = T;
   p.status = status;
+  // groups of up to 16 row blocks, their rows of x within 32 MB of the L2:
+  // 8192 x 4096 against 32000 entries 1.31 ms (all 32 row blocks at once: 1.38)
+  const int group = (32 << 20) / (512 * H);
+  p.m_group = group > 16 ? 16 : group < 4 ? 4 : group;
   p.ce = ce;
   const int tiles = (T + C::TILE_M - 1) / C::TILE_M * p.n_tiles;
   if constexpr (PAIR)
@@ -169,12 +191,164 @@ cudaError_t gemm_dw(const void* d, int ld, int T, const void* x, int H, void* dw
   return launch_gemm_pair<C>(ta, tb, tc, tc, p, p.m_tiles_w * p.n_tiles, st);
 }
 
+// ---------------------------------------------------------------- few tokens
+// Up to kFewRows tokens the logits are matrix-vector products: the head's
+// weight is read once, in whole rows, and nothing else counts.  (The tensor
+// cores' tiles read 128 bytes of each of 256 rows at a time, which costs HBM a
+// quarter of its rate: one token, 131072 x 4096, in 190 us, against 159 here,
+// 6.7 TB/s; from four tokens on the arithmetic here takes longer than that.)
+// A warp takes kFewStep entries at a time, lanes the words of their rows; x
+// stays in shared memory.  Lane t keeps token t's running maximum and sum; the
+// warps of a block are joined in order and leave one pair stats[block][t], and
+// the last block to finish joins the blocks' pairs, in an order of its own
+// that does not depend on who is last.
+constexpr int kFewStep = 2;
+constexpr int kFewWarps = 16;
+
+__device__ __forceinline__ float2 ce_join(float2 a, float2 b) {
+  const float m = fmaxf(a.x, b.x);
+  const float off = (m == -INFINITY ? 0.f : m) * kLog2e;
+  return make_float2(m, a.y * ex2(fmaf(a.x, kLog2e, -off)) + b.y * ex2(fmaf(b.x, kLog2e, -off)));
+}
+
+// lse and loss of one row from its joined pair.
+__device__ __forceinline__ void ce_row_out(float2 a, int row, const int32_t* __restrict__ labels, int V,
+                                           const float* label_logit, float* __restrict__ loss,
+                                           float* __restrict__ lse, int* status) {
+  const float l = a.x + logf(a.y);
+  const int label = labels[row];
+  const bool scored = label >= 0 && label < V;
+  if (!scored && label != -1) set_status(status, kErrBadIndex);
+  lse[row] = l;
+  loss[row] = scored ? l - label_logit[row] : 0.f;
+}
+
+template <int TT>
+__global__ void __launch_bounds__(32 * kFewWarps) ce_few_kernel(const uint4* __restrict__ x,
+                                                                const uint4* __restrict__ w,
+                                                                const int32_t* __restrict__ labels, int T, int words,
+                                                                int V, float2* stats, float* label_logit,
+                                                                float* __restrict__ loss, float* __restrict__ lse,
+                                                                int* status) {
+  pdl_entry();
+  extern __shared__ __align__(16) uint4 s_x[];          // [TT][words], zero past T
+  __shared__ float2 s_part[kFewWarps][TT];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = threadIdx.x; i < TT * words; i += blockDim.x)
+    s_x[i] = i < T * words ? x[i] : make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  const int label = lane < T ? labels[lane] : -1;
+  float2 run = make_float2(-INFINITY, 0.f);
+  const int stride = gridDim.x * kFewWarps * kFewStep;
+  for (int v0 = (blockIdx.x * kFewWarps + warp) * kFewStep; v0 < V; v0 += stride) {
+    F32x2 acc[kFewStep][TT];
+    #pragma unroll
+    for (int r = 0; r < kFewStep; ++r)
+      #pragma unroll
+      for (int t = 0; t < TT; ++t) acc[r][t] = make_f32x2(0.f, 0.f);
+    const uint4* rows[kFewStep];
+    #pragma unroll
+    for (int r = 0; r < kFewStep; ++r) rows[r] = w + static_cast<long long>(min(v0 + r, V - 1)) * words;
+    for (int c0 = lane; c0 < words; c0 += 4 * 32) {
+      uint4 u[4][kFewStep];
+      #pragma unroll
+      for (int i = 0; i < 4; ++i)
+        #pragma unroll
+        for (int r = 0; r < kFewStep; ++r)
+          u[i][r] = c0 + 32 * i < words ? rows[r][c0 + 32 * i] : make_uint4(0, 0, 0, 0);
+      #pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = c0 + 32 * i;
+        if (c < words) {
+          F32x2 wv[kFewStep][4];
+          #pragma unroll
+          for (int r = 0; r < kFewStep; ++r) {
+            wv[r][0] = bf16x2_f32x2(u[i][r].x);
+            wv[r][1] = bf16x2_f32x2(u[i][r].y);
+            wv[r][2] = bf16x2_f32x2(u[i][r].z);
+            wv[r][3] = bf16x2_f32x2(u[i][r].w);
+          }
+          #pragma unroll
+          for (int t = 0; t < TT; ++t) {
+            const uint4 xu = s_x[t * words + c];
+            const F32x2 xv[4] = {bf16x2_f32x2(xu.x), bf16x2_f32x2(xu.y), bf16x2_f32x2(xu.z), bf16x2_f32x2(xu.w)};
+            #pragma unroll
+            for (int r = 0; r < kFewStep; ++r)
+              #pragma unroll
+              for (int j = 0; j < 4; ++j) acc[r][t] = fma2(wv[r][j], xv[j], acc[r][t]);
+          }
+        }
+      }
+    }
+    #pragma unroll
+    for (int r = 0; r < kFewStep; ++r) {
+      float mine = 0.f;                     // lane t: token t's logit
+      #pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        const float2 f = split_f32x2(acc[r][t]);
+        float z = f.x + f.y;
+        #pragma unroll
+        for (int d = 16; d > 0; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+        if (lane == t) mine = z;
+      }
+      if (v0 + r < V && lane < T) {
+        run = ce_join(run, make_float2(mine, 1.f));
+        if (label == v0 + r) label_logit[lane] = mine;
+      }
+    }
+  }
+  if (lane < TT) s_part[warp][lane] = run;
+  __syncthreads();
+  if (warp == 0 && lane < T) {
+    float2 a = s_part[0][lane];
+    #pragma unroll
+    for (int i = 1; i < kFewWarps; ++i) a = ce_join(a, s_part[i][lane]);
+    stats[blockIdx.x * T + lane] = a;
+  }
+  __shared__ int s_last;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) s_last = atomicAdd(status + kFewDoneWord, 1) == static_cast<int>(gridDim.x) - 1 ? 1 : 0;
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  if (threadIdx.x == 0) atomicExch(status + kFewDoneWord, 0);      // zero for the next launch
+  if (warp < T) {                           // warp t: token t
+    float2 a = make_float2(-INFINITY, 0.f);
+    for (int i = lane; i < static_cast<int>(gridDim.x); i += 32) a = ce_join(a, __ldcg(stats + i * T + warp));
+    #pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+      a = ce_join(a, make_float2(__shfl_xor_sync(0xffffffffu, a.x, d), __shfl_xor_sync(0xffffffffu, a.y, d)));
+    if (lane == 0) ce_row_out(a, warp, labels, V, label_logit, loss, lse, status);
+  }
+}
+
+template <int TT>
+cudaError_t loss_few(const void* x, const void* w, int T, int H, int V, const CeParams& ce, float* loss, float* lse,
+                     int* status, cudaStream_t st) {
+  auto kern = ce_few_kernel<TT>;
+  static std::atomic<bool> attr_set[kMaxDevices];
+  const int dev = current_device();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TT * entry::kMaxH * 2);
+    if (e != cudaSuccess) return e;
+    attr_set[dev].store(true, std::memory_order_release);
+  }
+  const int need = (V + kFewWarps * kFewStep - 1) / (kFewWarps * kFewStep);
+  const int blocks = need < kFewBlocks ? need : kFewBlocks;
+  count_launches(1);
+  return launch_k(kern, blocks, 32 * kFewWarps, static_cast<size_t>(TT) * H * 2, st, static_cast<const uint4*>(x),
+                  static_cast<const uint4*>(w), ce.labels, T, H / 8, V, ce.stats, ce.label_logit, loss, lse,
+                  status);
+}
 // ---------------------------------------------------------------- row kernels
 constexpr int kJoinRows = 32, kJoinStrands = 16;
 
-// lse and loss of each row from its tiles' (maximum, sum): strand s takes
-// tiles s, s + 16, ... in order, then the strands are joined in order.
-__global__ void __launch_bounds__(kJoinRows * kJoinStrands) ce_join_kernel(const float2* __restrict__ stats, int tiles,
+// lse and loss of each row from its half tiles' (maximum, sum): strand s takes
+// pairs s, s + 16, ... in order, then the strands are joined in order.
+__global__ void __launch_bounds__(kJoinRows * kJoinStrands) ce_join_kernel(const float2* __restrict__ stats, int parts,
                                                                           const float* __restrict__ label_logit,
                                                                           const int32_t* __restrict__ labels, int T,
                                                                           int V, float* __restrict__ loss,
@@ -183,27 +357,17 @@ __global__ void __launch_bounds__(kJoinRows * kJoinStrands) ce_join_kernel(const
   __shared__ float2 s_part[kJoinStrands][kJoinRows];
   const int lane = threadIdx.x % kJoinRows, strand = threadIdx.x / kJoinRows;
   const int row = blockIdx.x * kJoinRows + lane;
-  auto join = [](float2 a, float2 b) {
-    const float m = fmaxf(a.x, b.x);
-    const float off = (m == -INFINITY ? 0.f : m) * kLog2e;
-    return make_float2(m, a.y * ex2(fmaf(a.x, kLog2e, -off)) + b.y * ex2(fmaf(b.x, kLog2e, -off)));
-  };
   float2 a = make_float2(-INFINITY, 0.f);
   if (row < T) {
     #pragma unroll 4
-    for (int i = strand; i < tiles; i += kJoinStrands) a = join(a, stats[static_cast<long long>(i) * T + row]);
+    for (int i = strand; i < parts; i += kJoinStrands) a = ce_join(a, stats[static_cast<long long>(i) * T + row]);
   }
   s_part[strand][lane] = a;
   __syncthreads();
   if (strand != 0 || row >= T) return;
   #pragma unroll
-  for (int i = 1; i < kJoinStrands; ++i) a = join(a, s_part[i][lane]);
-  const float l = a.x + logf(a.y);
-  const int label = labels[row];
-  const bool scored = label >= 0 && label < V;
-  if (!scored && label != -1) set_status(status, kErrBadIndex);
-  lse[row] = l;
-  loss[row] = scored ? l - label_logit[row] : 0.f;
+  for (int i = 1; i < kJoinStrands; ++i) a = ce_join(a, s_part[i][lane]);
+  ce_row_out(a, row, labels, V, label_logit, loss, lse, status);
 }
 
 // x with the rows that are not scored set to zero: d is zero there, but the
@@ -270,13 +434,15 @@ moe_status moe_cross_entropy_forward(const void* x, const void* w, const int32_t
   ce.vocab = V;
   ce.stats = at<float2>(ws, l.stats);
   ce.label_logit = at<float>(ws, l.label_logit);
+  if (T == 1) return status_of(loss_few<1>(x, w, T, H, V, ce, loss, lse, status, st));
+  if (T <= kFewRows) return status_of(loss_few<kFewRows>(x, w, T, H, V, ce, loss, lse, status, st));
   if (small_rows(T))
     MOE_TRY((gemm_logits<Epi::kCeStats, false>(x, T, H, w, V, nullptr, 0, ce, status, st)));
   else
     MOE_TRY((gemm_logits<Epi::kCeStats, true>(x, T, H, w, V, nullptr, 0, ce, status, st)));
   count_launches(1);
   MOE_TRY(launch_k(ce_join_kernel, (T + kJoinRows - 1) / kJoinRows, kJoinRows * kJoinStrands, 0, st, ce.stats,
-                   (V + kTile - 1) / kTile, ce.label_logit, labels, T, V, loss, lse, status));
+                   2 * ((V + kTile - 1) / kTile), ce.label_logit, labels, T, V, loss, lse, status));
   return MOE_OK;
 }
 

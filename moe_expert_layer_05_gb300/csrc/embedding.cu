@@ -38,8 +38,9 @@ constexpr int kChunk = 32;                             // sorted positions summe
 // ---------------------------------------------------------------- lookup
 // An id outside [0, V) gives a zero row; -1 is padding, any other one is
 // reported.  A thread has four 16-byte loads on their way: four words of one
-// row (wide rows, one block each), or, with rows of up to 128 words, a word of
-// four rows (`lanes` threads a row, a power of two).
+// row (wide rows, one block each), or, with rows of up to 256 words, a word of
+// four rows (`lanes` threads a row, a power of two): 16384 rows of 1032 in 10.7
+// us, against 17.3 with a block each.
 template <bool WIDE>
 __global__ void __launch_bounds__(128) embedding_fwd_kernel(const int32_t* __restrict__ tokens, int n,
                                                             const uint4* __restrict__ table, int V, int words,
@@ -57,7 +58,7 @@ __global__ void __launch_bounds__(128) embedding_fwd_kernel(const int32_t* __res
       set_status(status, kErrBadIndex);
     if (tok[i] >= V) tok[i] = -1;
   }
-  for (int c0 = WIDE ? threadIdx.x : threadIdx.x % lanes; c0 < words; c0 += 4 * 128) {
+  for (int c0 = WIDE ? threadIdx.x : threadIdx.x % lanes; c0 < words; c0 += WIDE ? 4 * 128 : lanes) {
     uint4 v[4];
     #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -629,7 +630,7 @@ moe_status moe_embedding_forward(const int32_t* tokens, int32_t n, const void* t
   if (n == 0) return MOE_OK;
   count_launches(1);
   const int words = H / 8;
-  const bool wide = words > 128;
+  const bool wide = words > 256;
   int lanes = 128;
   while (!wide && lanes / 2 >= words) lanes /= 2;
   const int per_block = wide ? 1 : 4 * (128 / lanes);

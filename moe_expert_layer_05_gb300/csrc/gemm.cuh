@@ -52,7 +52,7 @@ struct CeParams {
   const int32_t* labels;   // [rows]; outside [0, vocab): the row is not scored
   int vocab;               // entries of the whole vocabulary
   int v0;                  // vocabulary entry of B's first row
-  float2* stats;           // kCeStats: [n_tiles][rows] (maximum, sum of exp(z - maximum))
+  float2* stats;           // kCeStats: [2 n_tiles][rows] (maximum, sum of exp(z - maximum)) of each half tile
   float* label_logit;      // kCeStats: [rows], written where the label is in the vocabulary
   const float* lse;        // kCeGrad: [rows]
   const float* dloss;      // kCeGrad: [rows]
@@ -131,6 +131,7 @@ struct GemmParams {
   __nv_bfloat16* cmb_y;            // [T, ldc]
   int kb_per_split;                // kSplitK: k-blocks of one part
   int c_add;                       // kSplitK: add to the slabs (1) or overwrite them (0)
+  int m_group;                     // cross entropy: row blocks of one group of tiles
   CeParams ce;
 };
 
@@ -196,7 +197,13 @@ struct GemmCfg {
   // MXFP8 copies) in 32-column chunks through the same 2 KB staging.
   static constexpr bool SPLIT_FWD = MX && !NV4 && EP == Epi::kSwiglu && BN == 256;
   static constexpr bool SPLIT_COLS = (NV4 && EP == Epi::kSwiglu && BN == 256) || SPLIT_BWD || SPLIT_FWD;
-  static constexpr int EPI_WARPS = (M256 || SPLIT_COLS) ? 8 : 4;
+  // The vocabulary head's GEMMs (logits, split dx, bf16 weight gradient): eight
+  // warps too, the second four taking the upper half of the tile's columns.
+  // With a short contraction the epilogue is the longer part of a tile: the
+  // gradient's logits at 2048 x 512 x 50000 took 175 us on four warps.
+  static constexpr bool HEAD = EP == Epi::kCeStats || EP == Epi::kCeGrad || S == Sched::kSplitK ||
+                               (S == Sched::kRoutedK && EP == Epi::kStoreBf16);
+  static constexpr int EPI_WARPS = (M256 || SPLIT_COLS || HEAD) ? 8 : 4;
   // Shared memory (all of it dynamic): the k-block ring, 4 KB staging buffers
   // (32 rows x 128 B, 128B-swizzled) per epilogue warp -- two each, or one
   // where two would cost the ring its fourth stage -- and the bookkeeping
@@ -213,7 +220,8 @@ struct GemmCfg {
   // (256 x 224 MXFP8 weight-gradient tiles: eight warps, one buffer each, so
   // the ring keeps three 62 KB stages)
   static constexpr int WGRAD_BUFS = WIDE_K ? 2 : (M256 ? 1 : 4);
-  static constexpr int STAGING_BUFS = (S == Sched::kRoutedK && TMA_OUT) ? WGRAD_BUFS
+  static constexpr int STAGING_BUFS = HEAD ? 1
+                                      : (S == Sched::kRoutedK && TMA_OUT) ? WGRAD_BUFS
                                       // gate and up chunks side by side; one buffer (the up chunk
                                       // waits in registers) where two would cost the ring a stage
                                       : (EP == Epi::kSwigluBwd) ? ((MX && BN == 256) ? 1 : 2)
@@ -360,8 +368,18 @@ __device__ __forceinline__ TileInfo decode_tile(const GemmParams& p, const int* 
   } else if constexpr (C::S == Sched::kDenseM) {
     const int mb = (p.m_rows + C::TILE_M - 1) / C::TILE_M;
     ti.group = 0;
-    ti.n = t / mb;
-    ti.m0 = (t % mb) * C::TILE_M;
+    if (C::EP == Epi::kCeStats || C::EP == Epi::kCeGrad) {
+      // groups of m_group row blocks walk the columns one after another: the
+      // rows of a group stay in L2 while the columns stream past
+      const int first = t / (p.m_group * p.n_tiles) * p.m_group;
+      const int gm = min(p.m_group, mb - first);
+      const int r = t - first * p.n_tiles;
+      ti.n = r / gm;
+      ti.m0 = (first + r % gm) * C::TILE_M;
+    } else {
+      ti.n = t / mb;
+      ti.m0 = (t % mb) * C::TILE_M;
+    }
     ti.half1 = C::ROWS256 && (ti.m0 + 128 < p.m_rows);
     ti.num_kb = p.k_len / C::BK;
     ti.k_row0 = 0;
@@ -519,6 +537,11 @@ struct Stager {
   __device__ __forceinline__ void put(int c, uint32_t a, uint32_t b, uint32_t cc, uint32_t d) {
     const uint32_t base = smem_u32(buf + cur * BUF);
     st_shared_v4(base + lane * 128 + ((c ^ (lane & 7)) << 4), a, b, cc, d);
+  }
+  // one bf16 of this lane's row, column c of 64, over what put() left there
+  __device__ __forceinline__ void put_bf16(int c, float v) {
+    const uint32_t base = smem_u32(buf + cur * BUF);
+    st_shared_u16(base + lane * 128 + (((c >> 3) ^ (lane & 7)) << 4) + (c & 7) * 2, pack_bf16x2(v, 0.f) & 0xffffu);
   }
   // 16-byte chunk c of this lane's row in a buffer of 64-byte rows without
   // swizzle (for a 32-column bf16 box)
@@ -721,21 +744,57 @@ __device__ __forceinline__ void fused_combine_rows(const GemmParams& p, int y0, 
 // ---------------------------------------------------------------- cross entropy
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Statistics of one tile of logits: this lane's row, columns [n BN, n BN +
-// BN).  A running maximum m and sum s of 2^((z - m) log2 e), 32 columns at a
+// Statistics of one half of a tile of logits: this lane's row, columns [n BN +
+// part BN / 2, + BN / 2).  A running maximum m and sum s of 2^((z - m) log2 e), 32 columns at a
 // time; columns past the vocabulary count as -infinity.
+// What an epilogue thread needs of its row, loaded before it waits for the tile.
+struct CeRow {
+  int label;      // -1: none
+  float lse, dloss;
+};
 template <class C>
+__device__ __forceinline__ CeRow ce_row(const GemmParams& p, int row) {
+  CeRow r{-1, 0.f, 0.f};
+  if (row < p.m_rows) {
+    r.label = p.ce.labels[row];
+    if constexpr (C::EP == Epi::kCeGrad) {
+      r.lse = p.ce.lse[row];
+      r.dloss = p.ce.dloss[row];
+    }
+  }
+  return r;
+}
+
+// The label's logit of each lane that has its label's column `rel` in [c0, c0 +
+// n): read from TMEM by itself, one lane's column at a time.  (Few tiles hold
+// labels.  Picking it out of the lane's registers instead, by a compare for
+// each column under a branch, doubled the time of a tile's epilogue.)
+__device__ __forceinline__ float ce_label_logit(uint32_t t0, int rel, int c0, int n, int lane, float zl) {
+  unsigned todo = __ballot_sync(0xffffffffu, rel >= c0 && rel < c0 + n);
+  while (todo != 0) {
+    const int l = __ffs(todo) - 1;
+    todo &= todo - 1;
+    const float v = __uint_as_float(tmem_ld_x1(t0 + __shfl_sync(0xffffffffu, rel, l)));
+    if (lane == l) zl = v;
+  }
+  return zl;
+}
+
+// release() hands the accumulator back to the MMA warp.  It comes before the
+// row's stores: an arrive after them would wait for them to reach L2, every
+// tile (2048 x 512 against 50000 entries: 102 us, against 76).
+template <class C, class Release>
 __device__ __forceinline__ void ce_stats_tile(const GemmParams& p, const TileInfo& ti, uint32_t tmem_acc, int quarter,
-                                              int lane) {
+                                              int lane, int part, const CeRow& cr, Release&& release) {
   const uint32_t t0 = tmem_acc + (static_cast<uint32_t>(quarter * 32) << 16);
   const int row = ti.m0 + quarter * 32 + lane;
   const bool row_ok = row < p.m_rows;
   const int col0 = p.ce.v0 + ti.n * C::BN;
   const int nv = min(C::BN, p.ce.vocab - col0);              // columns of this tile in the vocabulary
-  const int rel = (row_ok ? p.ce.labels[row] : -1) - col0;  // the label's column of this tile
+  const int rel = cr.label - col0;                           // the label's column of this tile
   float m = -INFINITY, s = 0.f;
   #pragma unroll 1
-  for (int c0 = 0; c0 < nv; c0 += 32) {
+  for (int c0 = part * (C::BN / 2); c0 < min(nv, (part + 1) * (C::BN / 2)); c0 += 32) {
     uint32_t u[2][16];
     load32(t0 + c0, u[0], u[1]);
     float z[32];
@@ -756,52 +815,47 @@ __device__ __forceinline__ void ce_stats_tile(const GemmParams& p, const TileInf
     for (int j = 0; j < 32; ++j) t[j & 3] += ex2(fmaf(z[j], kLog2e, -off));
     s = s * ex2(fmaf(m, kLog2e, -off)) + ((t[0] + t[1]) + (t[2] + t[3]));
     m = mn;
-    const bool here = rel >= c0 && rel < c0 + 32 && rel < nv;
-    if (__any_sync(0xffffffffu, here)) {
-      float zl = 0.f;
-      #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (rel - c0 == j) zl = z[j];
-      if (here) p.ce.label_logit[row] = zl;
-    }
   }
-  if (row_ok) p.ce.stats[static_cast<long long>(ti.n) * p.m_rows + row] = make_float2(m, s);
+  const float zl = ce_label_logit(t0, rel, part * (C::BN / 2), C::BN / 2, lane, 0.f);
+  release();
+  if (rel >= part * (C::BN / 2) && rel < min(nv, (part + 1) * (C::BN / 2))) p.ce.label_logit[row] = zl;
+  if (row_ok) p.ce.stats[(2ll * ti.n + part) * p.m_rows + row] = make_float2(m, s);
 }
 
-// Gradient of one tile of logits: d = dloss (exp(z - lse) - [column == label])
+// Gradient of one half of a tile of logits: d = dloss (exp(z - lse) - [column == label])
 // in bf16, the operand type of the two products that follow; zero in rows
 // without a label and in columns past the vocabulary, whatever the logits.
-template <class C, class St>
+template <class C, class St, class Release>
 __device__ __forceinline__ void ce_grad_tile(const GemmParams& p, const TileInfo& ti, uint32_t tmem_acc, int quarter,
-                                             int lane, St& st, const CUtensorMap* tmC) {
+                                             int lane, St& st, const CUtensorMap* tmC, int part,
+                                             const CeRow& cr, Release&& release) {
   const uint32_t t0 = tmem_acc + (static_cast<uint32_t>(quarter * 32) << 16);
   const int y = ti.m0 + quarter * 32;
-  if (y >= p.m_rows) return;
-  const int row = y + lane;
+  if (y >= p.m_rows) {
+    release();
+    return;
+  }
   const int col0 = p.ce.v0 + ti.n * C::BN;
   const int nv = min(C::BN, p.ce.vocab - col0);
-  const int label = row < p.m_rows ? p.ce.labels[row] : -1;
-  const bool scored = label >= 0 && label < p.ce.vocab;
-  const int rel = label - col0;
-  const float off = scored ? p.ce.lse[row] * kLog2e : 0.f;
-  const float dl = scored ? p.ce.dloss[row] : 0.f;
+  const bool scored = cr.label >= 0 && cr.label < p.ce.vocab;
+  const int rel = cr.label - col0;
+  const float off = scored ? cr.lse * kLog2e : 0.f;
+  const float dl = scored ? cr.dloss : 0.f;
   #pragma unroll 1
-  for (int c0 = 0; c0 < C::BN; c0 += 64) {
-    const bool label_here = __any_sync(0xffffffffu, rel >= c0 && rel < c0 + 64);
+  for (int c0 = part * (C::BN / 2); c0 < (part + 1) * (C::BN / 2); c0 += 64) {
     const bool edge = c0 + 64 > nv;
+    uint32_t w[2][2][16];
+    load32(t0 + c0, w[0][0], w[0][1]);
+    load32(t0 + c0 + 32, w[1][0], w[1][1]);
+    const float zl = ce_label_logit(t0, rel, c0, 64, lane, 0.f);
+    if (c0 + 64 == (part + 1) * (C::BN / 2)) release();
     st.begin();
     #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t u[2][16];
-      load32(t0 + c0 + 32 * h, u[0], u[1]);
+      const uint32_t (&u)[2][16] = w[h];
       float d[32];
       #pragma unroll
       for (int j = 0; j < 32; ++j) d[j] = ex2(fmaf(__uint_as_float(u[j >> 4][j & 15]), kLog2e, -off));
-      if (label_here) {
-        #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (rel - c0 - 32 * h == j) d[j] -= 1.f;
-      }
       #pragma unroll
       for (int j = 0; j < 32; ++j) d[j] = scored ? d[j] * dl : 0.f;
       if (edge) {
@@ -814,6 +868,8 @@ __device__ __forceinline__ void ce_grad_tile(const GemmParams& p, const TileInfo
         st.put(4 * h + q, pack_bf16x2(d[8 * q], d[8 * q + 1]), pack_bf16x2(d[8 * q + 2], d[8 * q + 3]),
                pack_bf16x2(d[8 * q + 4], d[8 * q + 5]), pack_bf16x2(d[8 * q + 6], d[8 * q + 7]));
     }
+    if (scored && rel >= c0 && rel < c0 + 64)      // the label's own column
+      st.put_bf16(rel - c0, (ex2(fmaf(zl, kLog2e, -off)) - 1.f) * dl);
     st.flush(tmC, ti.n * C::BN + c0, y);
   }
 }
@@ -837,7 +893,7 @@ __device__ __forceinline__ void epilogue_tile_tma(const GemmParams& p, const Til
       const int y = ti.m0 + quarter * 32;
       if (y >= p.m_rows) return;
       #pragma unroll 1
-      for (int c0 = 0; c0 < C::BN; c0 += 32) {
+      for (int c0 = cpart * (C::BN / 2); c0 < (cpart + 1) * (C::BN / 2); c0 += 32) {
         const int x = ti.n * C::BN + c0;
         if (x >= p.valid_cols) break;
         uint32_t a[16], b[16];
@@ -1020,8 +1076,9 @@ __device__ __forceinline__ void epilogue_tile_tma(const GemmParams& p, const Til
         return;
       }
     }
+    constexpr int kCols = C::HEAD ? C::BN / 2 : C::BN;
     #pragma unroll 1
-    for (int c0 = 0; c0 < C::BN; c0 += 64) {
+    for (int c0 = C::HEAD ? cpart * kCols : 0; c0 < (C::HEAD ? cpart + 1 : 1) * kCols; c0 += 64) {
       if constexpr (C::S == Sched::kRoutedK) {  // (a head of any size: nothing past its rows and columns)
         if (ti.n * C::BN + c0 >= p.valid_cols || y >= p.m_rows) break;
       }
@@ -1802,9 +1859,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       if (lane == 0) mbar_arrive(&bk.sched_empty[slot]);
       if (t < 0) break;
       const TileInfo ti = decode_tile<C>(p, s_poff, s_tpre, t);
+      [[maybe_unused]] CeRow cr{};
+      if constexpr (C::EP == Epi::kCeStats || C::EP == Epi::kCeGrad) cr = ce_row<C>(p, ti.m0 + quarter * 32 + lane);
       if (!mbar_wait(&tfull_bar[acc], acc_phase, abort_ptr, wait_lim)) break;
       tc_fence_after_sync();
       bool released = false;                 // accumulator already handed back by the epilogue
+      auto release = [&] {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty_bar[acc]);
+        released = true;
+      };
       if constexpr (C::M256) {
         if (part == 0 || ti.half1) {
           TileInfo th = ti;
@@ -1813,12 +1878,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                &tempty_bar[acc], &released, al);
         }
       } else if constexpr (C::EP == Epi::kCeStats) {
-        ce_stats_tile<C>(p, ti, tmem_base + acc * C::ACC_COLS, quarter, lane);
+        ce_stats_tile<C>(p, ti, tmem_base + acc * C::ACC_COLS, quarter, lane, part, cr, release);
       } else if constexpr (C::EP == Epi::kCeGrad) {
-        ce_grad_tile<C>(p, ti, tmem_base + acc * C::ACC_COLS, quarter, lane, st, &tmC);
+        ce_grad_tile<C>(p, ti, tmem_base + acc * C::ACC_COLS, quarter, lane, st, &tmC, part, cr, release);
       } else if constexpr (C::TMA_OUT) {
         epilogue_tile_tma<C>(p, ti, tmem_base + acc * C::ACC_COLS, quarter, lane, st, &tmC, &tmC2,
-                             &tempty_bar[acc], &released, al, C::SPLIT_COLS ? part : 0);
+                             &tempty_bar[acc], &released, al, (C::SPLIT_COLS || C::HEAD) ? part : 0);
       } else {
         epilogue_tile<C>(p, ti, tmem_base + acc * C::BN, quarter, lane);
       }
@@ -2053,8 +2118,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       }
     }
   } else {
-    // -------------------------------------------------- epilogue (warps 2..5 of both CTAs)
+    // -------------------------------------------------- epilogue (warps 2.. of both CTAs)
     const int quarter = warp & 3;
+    const int part = (warp - 2) >> 2;      // (eight warps) which half of the tile's columns
     const uint32_t tempty_leader = mapa_shared(smem_u32(&tempty_bar[0]), 0);
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -2062,22 +2128,33 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                                lane};
     for (int t = cid; t < ntiles; t += ncl) {
       const TileInfo ti = decode_tile<C>(p, s_poff, s_tpre, t);
+      [[maybe_unused]] CeRow cr{};
+      if constexpr (C::EP == Epi::kCeStats || C::EP == Epi::kCeGrad)
+        cr = ce_row<C>(p, ti.m0 + 128 * static_cast<int>(rank) + quarter * 32 + lane);
       if (!mbar_wait(&tfull_bar[acc], acc_phase, abort_ptr, wait_lim)) break;
       tc_fence_after_sync();
+      bool released = false;
+      auto release = [&] {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (C::HEAD) mbar_arrive_cluster_relaxed(tempty_leader + 8u * acc);
+          else mbar_arrive_cluster(tempty_leader + 8u * acc);
+        }
+        released = true;
+      };
       if (leader || ti.half1) {           // a half tile: the odd CTA's rows are not this expert's
         TileInfo th = ti;
         th.m0 += 128 * static_cast<int>(rank);
         const uint32_t t_acc = tmem_base + acc * C::ACC_COLS;
         if constexpr (C::EP == Epi::kCeStats)
-          ce_stats_tile<C>(p, th, t_acc, quarter, lane);
+          ce_stats_tile<C>(p, th, t_acc, quarter, lane, part, cr, release);
         else if constexpr (C::EP == Epi::kCeGrad)
-          ce_grad_tile<C>(p, th, t_acc, quarter, lane, st, &tmC);
+          ce_grad_tile<C>(p, th, t_acc, quarter, lane, st, &tmC, part, cr, release);
         else
-          epilogue_tile_tma<C>(p, th, t_acc, quarter, lane, st, &tmC, &tmC2);
+          epilogue_tile_tma<C>(p, th, t_acc, quarter, lane, st, &tmC, &tmC2, nullptr, nullptr, 1.0f, part);
       }
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(tempty_leader + 8u * acc);
+      if (!released) release();
       if (++acc == C::ACC_BUFS) { acc = 0; acc_phase ^= 1u; }
     }
     st.drain();

@@ -14,6 +14,8 @@ constexpr int kMaxK = 32;
 // Int of the workspace's 256-byte status region that counts the finished
 // blocks of the permutation's histogram launch (zero between launches).
 constexpr int kMapsDoneWord = 40;
+// The same for the blocks of the few-token cross entropy.
+constexpr int kFewDoneWord = 41;
 
 int num_sms();
 bool device_is_gb300();
