@@ -57,14 +57,13 @@ int piece_of(int T, int V, int piece) {
 // otherwise on 256-row tiles of CTA pairs.
 bool small_rows(int T) { return T <= 128; }
 
-// k-blocks of one part of dx's contraction over kb k-blocks.  Its output has
-// few tiles (T x H), so whole rounds of them leave SMs idle: the contraction is
-// cut into as many parts as make rounds x (part + a tile's start and end, some
-// 8 k-blocks) least.  At T = 4096, H = 4096 (256 tiles on 76 pairs) two parts
-// take 7 rounds of half the length instead of 4.
-int kb_per_split(int T, int H, int kb) {
-  const int units = small_rows(T) ? 152 : 76;
-  const int tiles = (small_rows(T) ? 1 : (T + 255) / 256) * ((H + kTile - 1) / kTile);
+// k-blocks of one part of a contraction over kb k-blocks whose output has
+// `tiles` tiles for `units` CTAs or pairs.  Few tiles leave SMs idle in whole
+// rounds, so the contraction is cut into as many parts as make rounds x (part +
+// a tile's start and end, some 8 k-blocks) least.  dx at T = 4096, H = 4096
+// (256 tiles on 76 pairs): two parts take 7 rounds of half the length instead
+// of 4.
+int kb_per_split(int tiles, int units, int kb) {
   int best = kb;
   long long least = -1;
   for (int splits = 1; splits <= kMaxSlabs && splits <= kb; ++splits) {
@@ -80,9 +79,26 @@ int kb_per_split(int T, int H, int kb) {
   return best;
 }
 
+int dx_per_split(int T, int H, int kb) {
+  const int n_tiles = (H + kTile - 1) / kTile;
+  return small_rows(T) ? kb_per_split(n_tiles, 152, kb) : kb_per_split((T + 255) / 256 * n_tiles, 76, kb);
+}
+// The weight gradient's contraction, over the tokens, is cut only where its
+// tiles do not make one round.
+constexpr int kDwBlock = 128;        // tokens of one of its k-blocks
+int dw_per_split(int T, int H, int rows) {
+  const int tiles = (rows + 255) / 256 * ((H + kTile - 1) / kTile), kb = (T + kDwBlock - 1) / kDwBlock;
+  return tiles < 76 ? kb_per_split(tiles, 76, kb) : kb;
+}
+
+size_t dw_slab_bytes(int T, int H, int rows) {
+  const int kb = (T + kDwBlock - 1) / kDwBlock, per = dw_per_split(T, H, rows);
+  return per < kb ? static_cast<size_t>((kb + per - 1) / per) * round_up(rows, 256) * H * 4 : 0;
+}
+
 struct Ws {
   size_t stats, label_logit;         // forward
-  size_t d, xz, slabs;               // backward
+  size_t d, xz, slabs, dw_slabs;     // backward
   int piece, slab_count;
   size_t total;
 };
@@ -102,11 +118,15 @@ Ws layout(int T, int H, int V, int piece) {
   end = off;
   off = entry::kStatusBytes;
   w.piece = piece_of(T, V, piece);
-  const int kb = w.piece / 64, per = kb_per_split(T, H, kb);
+  const int kb = w.piece / 64, per = dx_per_split(T, H, kb);
   w.slab_count = (kb + per - 1) / per;
   w.d = take(rows * w.piece * 2);
   w.xz = take(rows * H * 2);
   w.slabs = take(static_cast<size_t>(w.slab_count) * rows * H * 4);
+  // (the last piece may be smaller, and its contraction cut into more parts)
+  const int first = V < w.piece ? V : w.piece, last = V - (V - 1) / w.piece * w.piece;
+  const size_t sf = dw_slab_bytes(T, H, first), sl = dw_slab_bytes(T, H, last);
+  w.dw_slabs = take(sf > sl ? sf : sl);
   w.total = end > off ? end : off;
   return w;
 }
@@ -119,8 +139,8 @@ T* at(void* ws, size_t off) {
 // ---------------------------------------------------------------- logits GEMM
 template <Epi EP, bool PAIR>
 cudaError_t gemm_logits(const void* x, int T, int H, const void* w_rows, int rows, void* d, int ld, CeParams ce,
-                        int* status, cudaStream_t st) {
-  using C = GemmCfg<256, false, false, Sched::kDenseM, EP, 0, false, PAIR>;
+                        const SideJob& side, int* status, cudaStream_t st) {
+  using C = GemmCfg<256, false, false, Sched::kDenseM, EP, 0, false, PAIR, false, true>;
   CUtensorMap ta, tb, tc;
   if (!make_tmap_bf16(&ta, x, H, T, 64, 128) || !make_tmap_bf16(&tb, w_rows, H, rows, 64, C::B_BOX_ROWS))
     return cudaErrorInvalidValue;
@@ -138,6 +158,7 @@ cudaError_t gemm_logits(const void* x, int T, int H, const void* w_rows, int row
   const int group = (32 << 20) / (512 * H);
   p.m_group = group > 16 ? 16 : group < 4 ? 4 : group;
   p.ce = ce;
+  p.side = side;
   const int tiles = (T + C::TILE_M - 1) / C::TILE_M * p.n_tiles;
   if constexpr (PAIR)
     return launch_gemm_pair<C>(ta, tb, tc, tc, p, tiles, st);
@@ -149,7 +170,7 @@ cudaError_t gemm_logits(const void* x, int T, int H, const void* w_rows, int row
 template <bool PAIR>
 cudaError_t gemm_dx(const void* d, int ld, int T, const void* w_rows, int rows, int H, int per, float* slabs,
                     int slab_count, bool add, int* status, cudaStream_t st) {
-  using C = GemmCfg<256, false, true, Sched::kSplitK, Epi::kStoreF32, 0, false, PAIR>;
+  using C = GemmCfg<256, false, true, Sched::kSplitK, Epi::kStoreF32, 0, false, PAIR, false, true>;
   CUtensorMap ta, tb, tc;
   if (!make_tmap_bf16(&ta, d, ld, T, 64, 128) || !make_tmap_bf16(&tb, w_rows, H, rows, 64, 64) ||
       !make_tmap_slabs_f32(&tc, slabs, H, T, slab_count))
@@ -172,23 +193,34 @@ cudaError_t gemm_dx(const void* d, int ld, int T, const void* w_rows, int rows, 
     return launch_gemm<C>(ta, tb, tc, tc, p, tiles < num_sms() ? tiles : num_sms(), st);
 }
 
-// dw_rows[rows, H] = d[T, rows]^T x[T, H]
-cudaError_t gemm_dw(const void* d, int ld, int T, const void* x, int H, void* dw_rows, int rows, int* status,
-                    cudaStream_t st) {
-  using C = GemmCfg<256, true, true, Sched::kRoutedK, Epi::kStoreBf16, 0, false, true>;
+// dw_rows[rows, H] = d[T, rows]^T x[T, H]: in bf16, or (parts > 1) as fp32 slabs
+// [parts][rows rounded up to 256][H] of parts of the contraction.
+cudaError_t gemm_dw(const void* d, int ld, int T, const void* x, int H, void* dw_rows, int rows, int per, float* slabs,
+                    const SideJob& side, int* status, cudaStream_t st) {
+  using C = GemmCfg<256, true, true, Sched::kRoutedK, Epi::kStoreBf16, 0, false, true, false, true>;
+  using CS = GemmCfg<256, true, true, Sched::kRoutedK, Epi::kStoreF32, 0, false, true, false, true>;
+  static_assert(C::BK == kDwBlock && CS::BK == kDwBlock, "k-blocks of the weight gradient");
+  const int kb = (T + kDwBlock - 1) / kDwBlock, parts = (kb + per - 1) / per;
   CUtensorMap ta, tb, tc;
-  if (!make_tmap_bf16(&ta, d, ld, T, 64, C::BK) || !make_tmap_bf16(&tb, x, H, T, 64, C::BK) ||
-      !make_tmap_out_bf16(&tc, dw_rows, H, rows))
-    return cudaErrorInvalidValue;
   GemmParams p = gemm_params_zero();
-  p.E = 1;
-  p.m_rows = rows;
+  p.E = parts;
+  p.m_rows = parts > 1 ? round_up(rows, 256) : rows;
   p.k_len = T;
+  p.kb_per_split = per;
   p.m_tiles_w = (rows + 255) / 256;
   p.n_tiles = (H + kTile - 1) / kTile;
   p.valid_cols = H;
+  p.side = side;
   p.status = status;
-  return launch_gemm_pair<C>(ta, tb, tc, tc, p, p.m_tiles_w * p.n_tiles, st);
+  if (!make_tmap_bf16(&ta, d, ld, T, 64, kDwBlock) || !make_tmap_bf16(&tb, x, H, T, 64, kDwBlock))
+    return cudaErrorInvalidValue;
+  const int tiles = parts * p.m_tiles_w * p.n_tiles;
+  if (parts > 1) {
+    if (!make_tmap_out_f32(&tc, slabs, H, static_cast<uint64_t>(parts) * p.m_rows)) return cudaErrorInvalidValue;
+    return launch_gemm_pair<CS>(ta, tb, tc, tc, p, tiles, st);
+  }
+  if (!make_tmap_out_bf16(&tc, dw_rows, H, rows)) return cudaErrorInvalidValue;
+  return launch_gemm_pair<C>(ta, tb, tc, tc, p, tiles, st);
 }
 
 // ---------------------------------------------------------------- few tokens
@@ -370,30 +402,20 @@ __global__ void __launch_bounds__(kJoinRows * kJoinStrands) ce_join_kernel(const
   ce_row_out(a, row, labels, V, label_logit, loss, lse, status);
 }
 
-// x with the rows that are not scored set to zero: d is zero there, but the
-// product d^T x would still turn an infinity or NaN of such a row into NaN.
-__global__ void __launch_bounds__(128) ce_scored_rows_kernel(const uint4* __restrict__ x,
-                                                             const int32_t* __restrict__ labels, int V, int words,
-                                                             uint4* __restrict__ xz) {
-  pdl_entry();
-  const int label = labels[blockIdx.x];
-  const bool scored = label >= 0 && label < V;
-  const long long row = static_cast<long long>(blockIdx.x) * words;
-  for (int c = threadIdx.x; c < words; c += blockDim.x) xz[row + c] = scored ? x[row + c] : make_uint4(0, 0, 0, 0);
-}
-
-// dx = the slabs added in order, rounded to bf16.  n4 = T * H / 4.
-__global__ void __launch_bounds__(256) ce_dx_kernel(const float4* __restrict__ slabs, int count, long long n4,
-                                                    uint2* __restrict__ dx) {
+// The weight gradient's slabs added in order, rounded to bf16.  n4 = values of
+// the output / 4, stride4 = those of a slab.
+__global__ void __launch_bounds__(256) ce_dw_kernel(const float4* __restrict__ slabs, int count, long long n4,
+                                                    long long stride4, uint2* __restrict__ dw) {
   pdl_entry();
   const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= n4) return;
   float4 a = slabs[i];
+  #pragma unroll 4
   for (int s = 1; s < count; ++s) {
-    const float4 b = slabs[s * n4 + i];
+    const float4 b = slabs[s * stride4 + i];
     a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
   }
-  dx[i] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+  dw[i] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
 }
 
 bool sizes_ok(int32_t T, int32_t H, int32_t V, int32_t piece) {
@@ -437,9 +459,9 @@ moe_status moe_cross_entropy_forward(const void* x, const void* w, const int32_t
   if (T == 1) return status_of(loss_few<1>(x, w, T, H, V, ce, loss, lse, status, st));
   if (T <= kFewRows) return status_of(loss_few<kFewRows>(x, w, T, H, V, ce, loss, lse, status, st));
   if (small_rows(T))
-    MOE_TRY((gemm_logits<Epi::kCeStats, false>(x, T, H, w, V, nullptr, 0, ce, status, st)));
+    MOE_TRY((gemm_logits<Epi::kCeStats, false>(x, T, H, w, V, nullptr, 0, ce, SideJob{}, status, st)));
   else
-    MOE_TRY((gemm_logits<Epi::kCeStats, true>(x, T, H, w, V, nullptr, 0, ce, status, st)));
+    MOE_TRY((gemm_logits<Epi::kCeStats, true>(x, T, H, w, V, nullptr, 0, ce, SideJob{}, status, st)));
   count_launches(1);
   MOE_TRY(launch_k(ce_join_kernel, (T + kJoinRows - 1) / kJoinRows, kJoinRows * kJoinStrands, 0, st, ce.stats,
                    2 * ((V + kTile - 1) / kTile), ce.label_logit, labels, T, V, loss, lse, status));
@@ -467,27 +489,44 @@ moe_status moe_cross_entropy_backward(const void* x, const void* w, const int32_
   ce.vocab = V;
   ce.lse = lse;
   ce.dloss = dloss;
-  count_launches(1);
-  MOE_TRY(launch_k(ce_scored_rows_kernel, T, 128, 0, st, static_cast<const uint4*>(x), labels, V, H / 8,
-                   static_cast<uint4*>(xz)));
-  const int per = kb_per_split(T, H, l.piece / 64);
+  const int per = dx_per_split(T, H, l.piece / 64);
+  SideJob copy{};                            // beside the first piece's logits: x without its unscored rows
+  copy.src = static_cast<const uint4*>(x);
+  copy.dst = xz;
+  copy.n = T;
+  copy.words = H / 8;
   for (int v0 = 0; v0 < V; v0 += l.piece) {
     const int rows = V - v0 < l.piece ? V - v0 : l.piece;
-    const char* w_rows = static_cast<const char*>(w) + static_cast<size_t>(v0) * H * 2;
+    const size_t at_w = static_cast<size_t>(v0) * H * 2;
+    const char* w_rows = static_cast<const char*>(w) + at_w;
+    char* dw_rows = static_cast<char*>(dw) + at_w;
     ce.v0 = v0;
     if (small) {
-      MOE_TRY((gemm_logits<Epi::kCeGrad, false>(x, T, H, w_rows, rows, d, l.piece, ce, status, st)));
+      MOE_TRY((gemm_logits<Epi::kCeGrad, false>(x, T, H, w_rows, rows, d, l.piece, ce, copy, status, st)));
       MOE_TRY(gemm_dx<false>(d, l.piece, T, w_rows, rows, H, per, slabs, l.slab_count, v0 > 0, status, st));
     } else {
-      MOE_TRY((gemm_logits<Epi::kCeGrad, true>(x, T, H, w_rows, rows, d, l.piece, ce, status, st)));
+      MOE_TRY((gemm_logits<Epi::kCeGrad, true>(x, T, H, w_rows, rows, d, l.piece, ce, copy, status, st)));
       MOE_TRY(gemm_dx<true>(d, l.piece, T, w_rows, rows, H, per, slabs, l.slab_count, v0 > 0, status, st));
     }
-    MOE_TRY(gemm_dw(d, l.piece, T, xz, H, static_cast<char*>(dw) + static_cast<size_t>(v0) * H * 2, rows, status, st));
+    copy.n = 0;
+    SideJob join{};                          // beside the last piece's weight gradient: dx from its slabs
+    if (v0 + l.piece >= V) {
+      join.src = reinterpret_cast<const uint4*>(slabs);
+      join.dst = dx;
+      join.n = static_cast<long long>(T) * H / 4;
+      join.words = l.slab_count;
+    }
+    const int dw_per = dw_per_split(T, H, rows), dw_kb = (T + kDwBlock - 1) / kDwBlock;
+    float* dw_slabs = at<float>(ws, l.dw_slabs);
+    MOE_TRY(gemm_dw(d, l.piece, T, xz, H, dw_rows, rows, dw_per, dw_slabs, join, status, st));
+    if (dw_per < dw_kb) {
+      const long long n4 = static_cast<long long>(rows) * H / 4;
+      count_launches(1);
+      MOE_TRY(launch_k(ce_dw_kernel, static_cast<unsigned>((n4 + 255) / 256), 256, 0, st,
+                       reinterpret_cast<const float4*>(dw_slabs), (dw_kb + dw_per - 1) / dw_per, n4,
+                       static_cast<long long>(round_up(rows, 256)) * H / 4, reinterpret_cast<uint2*>(dw_rows)));
+    }
   }
-  const long long n4 = static_cast<long long>(T) * H / 4;
-  count_launches(1);
-  MOE_TRY(launch_k(ce_dx_kernel, static_cast<unsigned>((n4 + 255) / 256), 256, 0, st,
-                   reinterpret_cast<const float4*>(slabs), l.slab_count, n4, static_cast<uint2*>(dx)));
   return MOE_OK;
 }
 

@@ -58,6 +58,16 @@ struct CeParams {
   const float* dloss;      // kCeGrad: [rows]
 };
 
+// Work that the epilogue warps of the head's backward GEMMs do before their
+// first tile, while the first k-blocks are on their way: it would be a launch
+// of its own otherwise.  n = 0: none.
+struct SideJob {
+  const uint4* src;        // kCeGrad: x; weight gradient: the slabs of dx (fp32)
+  void* dst;               // kCeGrad: x with the rows that are not scored zero; weight gradient: dx (bf16)
+  long long n;             // kCeGrad: rows; weight gradient: groups of four values
+  int words;               // kCeGrad: 16-byte words of a row; weight gradient: slabs
+};
+
 struct GemmParams {
   const int* poffsets;     // [E+1] padded row offsets (kRoutedM, kRoutedK); nullptr = one group
   int E;                   // number of groups
@@ -129,14 +139,15 @@ struct GemmParams {
   int* cmb_count;                  // [T, n_tiles], zero between launches
   const __nv_bfloat16* cmb_shared; // [T, ldc] or nullptr
   __nv_bfloat16* cmb_y;            // [T, ldc]
-  int kb_per_split;                // kSplitK: k-blocks of one part
+  int kb_per_split;                // kSplitK, or kRoutedK without offsets: k-blocks of one part (0: all)
   int c_add;                       // kSplitK: add to the slabs (1) or overwrite them (0)
+  SideJob side;
   int m_group;                     // cross entropy: row blocks of one group of tiles
   CeParams ce;
 };
 
 template <int BN_, bool A_MN_, bool B_MN_, Sched S_, Epi EP_, int MX_ = 0, bool M256_ = false,
-          bool PAIR_ = false, bool GATHER_ = false>
+          bool PAIR_ = false, bool GATHER_ = false, bool HEAD_ = false>
 struct GemmCfg {
   static constexpr int BM = 128;                  // rows of A and D per CTA and MMA
   static constexpr bool M256 = M256_;             // 256-row tiles: two MMAs share each B k-block
@@ -197,12 +208,10 @@ struct GemmCfg {
   // MXFP8 copies) in 32-column chunks through the same 2 KB staging.
   static constexpr bool SPLIT_FWD = MX && !NV4 && EP == Epi::kSwiglu && BN == 256;
   static constexpr bool SPLIT_COLS = (NV4 && EP == Epi::kSwiglu && BN == 256) || SPLIT_BWD || SPLIT_FWD;
-  // The vocabulary head's GEMMs (logits, split dx, bf16 weight gradient): eight
-  // warps too, the second four taking the upper half of the tile's columns.
+  // The vocabulary head's GEMMs (logits, split dx, weight gradient): eight warps too, the second four taking the upper half of the tile's columns.
   // With a short contraction the epilogue is the longer part of a tile: the
   // gradient's logits at 2048 x 512 x 50000 took 175 us on four warps.
-  static constexpr bool HEAD = EP == Epi::kCeStats || EP == Epi::kCeGrad || S == Sched::kSplitK ||
-                               (S == Sched::kRoutedK && EP == Epi::kStoreBf16);
+  static constexpr bool HEAD = HEAD_;
   static constexpr int EPI_WARPS = (M256 || SPLIT_COLS || HEAD) ? 8 : 4;
   // Shared memory (all of it dynamic): the k-block ring, 4 KB staging buffers
   // (32 rows x 128 B, 128B-swizzled) per epilogue warp -- two each, or one
@@ -276,9 +285,10 @@ struct GemmCfg {
                                ? (A_MN && B_MN && (EP == Epi::kStoreF32 || EP == Epi::kStoreBf16))
                                : !A_MN)),
                 "CTA pairs: bf16, N = 256; row-grouped GEMMs with K-major A, or MN-major weight gradients");
-  static_assert(S != Sched::kSplitK || (!MX && !M256 && B_MN && EP == Epi::kStoreF32),
+  static_assert(!HEAD || (!MX && !M256), "the head's GEMMs: bf16, one accumulator row block per CTA");
+  static_assert(S != Sched::kSplitK || (HEAD && B_MN && EP == Epi::kStoreF32),
                 "split contraction: bf16, B stored [K, N], fp32 slabs");
-  static_assert((EP != Epi::kCeStats && EP != Epi::kCeGrad) || (!MX && !M256 && !B_MN && S == Sched::kDenseM),
+  static_assert((EP != Epi::kCeStats && EP != Epi::kCeGrad) || (HEAD && !B_MN && S == Sched::kDenseM),
                 "cross entropy: bf16 logits of one dense group");
   static_assert(SMEM_USED <= SMEM_BYTES && SMEM_BYTES <= 232448, "shared memory per CTA");
   static_assert(STAGES >= 2, "pipeline depth");
@@ -403,6 +413,10 @@ __device__ __forceinline__ TileInfo decode_tile(const GemmParams& p, const int* 
     if (p.poffsets != nullptr) {
       ti.k_row0 = s_poff[ti.group];
       ti.num_kb = (s_poff[ti.group + 1] - s_poff[ti.group]) / C::BK;
+    } else if (C::S == Sched::kRoutedK && p.kb_per_split > 0) {   // parts of one contraction, as groups
+      const int kb = (p.k_len + C::BK - 1) / C::BK;
+      ti.k_row0 = ti.group * p.kb_per_split * C::BK;
+      ti.num_kb = min(p.kb_per_split, kb - ti.group * p.kb_per_split);
     } else {
       ti.k_row0 = 0;
       ti.num_kb = (p.k_len + C::BK - 1) / C::BK;
@@ -780,6 +794,37 @@ __device__ __forceinline__ float ce_label_logit(uint32_t t0, int rel, int c0, in
   return zl;
 }
 
+// The side job of this kernel (see SideJob), by the nth of `threads` threads of
+// block `block` of `blocks`.
+template <class C>
+__device__ __forceinline__ void side_job(const GemmParams& p, int thread, int threads, int block, int blocks) {
+  if constexpr (C::EP == Epi::kCeGrad) {
+    // x with the rows that are not scored set to zero: d is zero there, but the
+    // product d^T x would still turn an infinity or NaN of such a row into NaN
+    uint4* dst = static_cast<uint4*>(p.side.dst);
+    for (long long r = block; r < p.side.n; r += blocks) {
+      const int label = p.ce.labels[r];
+      const bool scored = label >= 0 && label < p.ce.vocab;
+      for (int c = thread; c < p.side.words; c += threads)
+        dst[r * p.side.words + c] = scored ? p.side.src[r * p.side.words + c] : make_uint4(0, 0, 0, 0);
+    }
+  } else if constexpr (C::HEAD && C::S == Sched::kRoutedK) {
+    // dx = its slabs added in order, rounded once
+    const float4* slabs = reinterpret_cast<const float4*>(p.side.src);
+    uint2* dx = static_cast<uint2*>(p.side.dst);
+    for (long long i = static_cast<long long>(block) * threads + thread; i < p.side.n;
+         i += static_cast<long long>(blocks) * threads) {
+      float4 a = slabs[i];
+      #pragma unroll 4
+      for (int k = 1; k < p.side.words; ++k) {
+        const float4 b = slabs[k * p.side.n + i];
+        a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+      }
+      dx[i] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+    }
+  }
+}
+
 // release() hands the accumulator back to the MMA warp.  It comes before the
 // row's stores: an arrive after them would wait for them to reach L2, every
 // tile (2048 x 512 against 50000 entries: 102 us, against 76).
@@ -978,8 +1023,12 @@ __device__ __forceinline__ void epilogue_tile_tma(const GemmParams& p, const Til
         return;
       }
     }
+    constexpr int kColsF = C::HEAD ? C::BN / 2 : C::BN;
     #pragma unroll 1
-    for (int c0 = 0; c0 < C::BN; c0 += 32) {
+    for (int c0 = C::HEAD ? cpart * kColsF : 0; c0 < (C::HEAD ? cpart + 1 : 1) * kColsF; c0 += 32) {
+      if constexpr (C::HEAD) {
+        if (ti.n * C::BN + c0 >= p.valid_cols) break;
+      }
       uint32_t a[16], b[16];
       load32(t0 + c0, a, b);
       st.begin();
@@ -1079,7 +1128,7 @@ __device__ __forceinline__ void epilogue_tile_tma(const GemmParams& p, const Til
     constexpr int kCols = C::HEAD ? C::BN / 2 : C::BN;
     #pragma unroll 1
     for (int c0 = C::HEAD ? cpart * kCols : 0; c0 < (C::HEAD ? cpart + 1 : 1) * kCols; c0 += 64) {
-      if constexpr (C::S == Sched::kRoutedK) {  // (a head of any size: nothing past its rows and columns)
+      if constexpr (C::HEAD) {                  // (a head of any size: nothing past its rows and columns)
         if (ti.n * C::BN + c0 >= p.valid_cols || y >= p.m_rows) break;
       }
       uint32_t v[4][16];                        // 64 columns in one TMEM round trip
@@ -1851,6 +1900,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     uint32_t acc_phase = 0;
     Stager<C::STAGING_BUFS, C::STAGING_BUF> st{stage_smem + ew * (C::STAGING_BUFS * C::STAGING_BUF), 0, lane};
     const float al = acc_scale<C>(p);
+    if constexpr (C::HEAD) side_job<C>(p, threadIdx.x - 64, C::THREADS - 64, blockIdx.x, gridDim.x);
     for (int j = 0;; ++j) {
       const int slot = j % kSchedDepth;
       if (!mbar_wait(&bk.sched_full[slot], (j / kSchedDepth) & 1, abort_ptr, wait_lim)) break;
@@ -2126,6 +2176,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     uint32_t acc_phase = 0;
     Stager<C::STAGING_BUFS, C::STAGING_BUF> st{stage_smem + (warp - 2) * (C::STAGING_BUFS * C::STAGING_BUF), 0,
                                                lane};
+    if constexpr (C::HEAD) side_job<C>(p, threadIdx.x - 64, C::THREADS - 64, blockIdx.x, gridDim.x);
     for (int t = cid; t < ntiles; t += ncl) {
       const TileInfo ti = decode_tile<C>(p, s_poff, s_tpre, t);
       [[maybe_unused]] CeRow cr{};

@@ -290,7 +290,8 @@ def _dz(ref):
 
 
 CE_SHAPES = [(1, 8, 1), (1, 64, 1000), (2, 8, 255), (5, 72, 256), (64, 200, 257), (127, 1000, 511), (128, 128, 5003),
-             (129, 1000, 5003), (256, 64, 1000), (300, 264, 769), (1003, 1000, 2049), (513, 4096, 3001)]
+             (129, 1000, 5003), (256, 64, 1000), (300, 264, 769), (1003, 1000, 2049), (513, 4096, 3001),
+             (3000, 64, 300), (2500, 512, 1025)]
 
 
 @pytest.mark.parametrize("T,H,V", CE_SHAPES)
