@@ -236,9 +236,14 @@ __global__ void __launch_bounds__(512, 1) layer_norm_bwd_kernel(const uint4* __r
   if (gtid == 0) {
     for (int i = 0; i < stages; ++i) load(t0 + static_cast<long long>(i) * step, i);
   }
-  P8 w[NV];
-  #pragma unroll
-  for (int i = 0; i < NV; ++i) w[i] = pairs8(word_of(weight, gtid + i * gthreads, words));
+  // (KEEP: weight, s - mu and g in registers; wider rows leave those to the sums
+  // and take the row a second time from shared memory)
+  constexpr bool KEEP = NV == 2;
+  P8 w[KEEP ? NV : 1];
+  if constexpr (KEEP) {
+    #pragma unroll
+    for (int i = 0; i < NV; ++i) w[i] = pairs8(word_of(weight, gtid + i * gthreads, words));
+  }
   P8 dw[NV] = {}, db[NV] = {};
   const float inv_h = 1.0f / H;
   int stage = 0, flip = 0;
@@ -258,22 +263,26 @@ __global__ void __launch_bounds__(512, 1) layer_norm_bwd_kernel(const uint4* __r
     // taking bf16 pairs apart is what the kernel's arithmetic mostly costs
     const F32x2 neg_mu = make_f32x2(-mu, -mu), rs2 = make_f32x2(rs, rs);
     F32x2 s1 = make_f32x2(0.f, 0.f), s2 = make_f32x2(0.f, 0.f);
-    P8 cen[NV], g[NV];
-    uint4 ue[NV];
+    P8 cen[KEEP ? NV : 1], g[KEEP ? NV : 1];
+    uint4 ue[KEEP ? NV : 1];
     #pragma unroll
     for (int i = 0; i < NV; ++i) {               // (words past the row: dy = 0 adds nothing)
       const int c = gtid + i * gthreads;
       const P8 xs = pairs8(word_of(row_s, c, words)), d = pairs8(word_of(row_s + words, c, words));
-      if constexpr (DSUM) ue[i] = word_of(row_s + 2 * words, c, words);
+      if constexpr (DSUM && KEEP) ue[i] = word_of(row_s + 2 * words, c, words);
+      const P8 wv = KEEP ? w[KEEP ? i : 0] : pairs8(word_of(weight, c, words));
       #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        cen[i].p[j] = add2(xs.p[j], neg_mu);
-        g[i].p[j] = mul2(d.p[j], w[i].p[j]);
-        const F32x2 xh = mul2(cen[i].p[j], rs2);
+        const F32x2 cj = add2(xs.p[j], neg_mu), gj = mul2(d.p[j], wv.p[j]);
+        const F32x2 xh = mul2(cj, rs2);
         dw[i].p[j] = fma2(d.p[j], xh, dw[i].p[j]);
         db[i].p[j] = add2(db[i].p[j], d.p[j]);
-        s1 = add2(s1, g[i].p[j]);
-        s2 = fma2(g[i].p[j], xh, s2);
+        s1 = add2(s1, gj);
+        s2 = fma2(gj, xh, s2);
+        if constexpr (KEEP) {
+          cen[i].p[j] = cj;
+          g[i].p[j] = gj;
+        }
       }
     }
     const float2 f1 = split_f32x2(s1), f2 = split_f32x2(s2);
@@ -299,8 +308,10 @@ __global__ void __launch_bounds__(512, 1) layer_norm_bwd_kernel(const uint4* __r
     } else {
       __syncwarp();
     }
-    // every thread of the group has read the buffer
-    if (gtid == 0 && !*static_cast<volatile int*>(&s_abort)) load(t + static_cast<long long>(stages) * step, stage);
+    auto refill = [&] {                    // every thread of the group has read the buffer
+      if (gtid == 0 && !*static_cast<volatile int*>(&s_abort)) load(t + static_cast<long long>(stages) * step, stage);
+    };
+    if constexpr (KEEP) refill();
     // dx = rs g - rs <g> - (s - mu) rs^2 <g xh>
     m1 *= -inv_h * rs;
     m2 *= -inv_h * rs * rs;
@@ -310,15 +321,28 @@ __global__ void __launch_bounds__(512, 1) layer_norm_bwd_kernel(const uint4* __r
     for (int i = 0; i < NV; ++i) {
       const int c = gtid + i * gthreads;
       P8 o;
-      #pragma unroll
-      for (int j = 0; j < 4; ++j) o.p[j] = fma2(cen[i].p[j], k2, fma2(g[i].p[j], rs2, k1));
+      if constexpr (KEEP) {
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) o.p[j] = fma2(cen[i].p[j], k2, fma2(g[i].p[j], rs2, k1));
+      } else {
+        const P8 xs = pairs8(word_of(row_s, c, words)), d = pairs8(word_of(row_s + words, c, words));
+        const P8 wv = pairs8(word_of(weight, c, words));
+        #pragma unroll
+        for (int j = 0; j < 4; ++j)
+          o.p[j] = fma2(add2(xs.p[j], neg_mu), k2, fma2(mul2(d.p[j], wv.p[j]), rs2, k1));
+      }
       if constexpr (DSUM) {
-        const P8 e = pairs8(ue[i]);
+        const P8 e = pairs8(KEEP ? ue[KEEP ? i : 0] : word_of(row_s + 2 * words, c, words));
         #pragma unroll
         for (int j = 0; j < 4; ++j) o.p[j] = add2(o.p[j], e.p[j]);
       }
       if (c < words)
         dx[row + c] = make_uint4(pack_bf16x2(o.p[0]), pack_bf16x2(o.p[1]), pack_bf16x2(o.p[2]), pack_bf16x2(o.p[3]));
+    }
+    if constexpr (!KEEP) {
+      if (warps > 1) group_sync(group, gthreads);
+      else __syncwarp();
+      refill();
     }
     if (++stage == stages) {
       stage = 0;
