@@ -38,6 +38,10 @@ constexpr int kFewBlocks = 304;      // their blocks: two on each SM
 constexpr long long kPieceElements = 1LL << 27;
 constexpr int kMinPiece = 4096;
 
+// The forward's logits of up to kWhole products are added up whole by the
+// tensor cores (losses 8e-7 off at that length), longer ones in segments.
+constexpr int kWhole = 4096, kSegment = 2048;
+
 int round_up(int v, int m) { return (v + m - 1) / m * m; }
 
 // Vocabulary entries of one piece: whole tiles, the pieces as even as they come.
@@ -157,6 +161,7 @@ cudaError_t gemm_logits(const void* x, int T, int H, const void* w_rows, int row
   // 8192 x 4096 against 32000 entries 1.31 ms (all 32 row blocks at once: 1.38)
   const int group = (32 << 20) / (512 * H);
   p.m_group = group > 16 ? 16 : group < 4 ? 4 : group;
+  p.seg_kb = kSegment / C::BK;
   p.ce = ce;
   p.side = side;
   const int tiles = (T + C::TILE_M - 1) / C::TILE_M * p.n_tiles;
@@ -458,10 +463,13 @@ moe_status moe_cross_entropy_forward(const void* x, const void* w, const int32_t
   ce.label_logit = at<float>(ws, l.label_logit);
   if (T == 1) return status_of(loss_few<1>(x, w, T, H, V, ce, loss, lse, status, st));
   if (T <= kFewRows) return status_of(loss_few<kFewRows>(x, w, T, H, V, ce, loss, lse, status, st));
-  if (small_rows(T))
-    MOE_TRY((gemm_logits<Epi::kCeStats, false>(x, T, H, w, V, nullptr, 0, ce, SideJob{}, status, st)));
+  const bool small = small_rows(T);
+  if (H > kWhole)
+    MOE_TRY(small ? (gemm_logits<Epi::kCeStatsSeg, false>(x, T, H, w, V, nullptr, 0, ce, SideJob{}, status, st))
+                  : (gemm_logits<Epi::kCeStatsSeg, true>(x, T, H, w, V, nullptr, 0, ce, SideJob{}, status, st)));
   else
-    MOE_TRY((gemm_logits<Epi::kCeStats, true>(x, T, H, w, V, nullptr, 0, ce, SideJob{}, status, st)));
+    MOE_TRY(small ? (gemm_logits<Epi::kCeStats, false>(x, T, H, w, V, nullptr, 0, ce, SideJob{}, status, st))
+                  : (gemm_logits<Epi::kCeStats, true>(x, T, H, w, V, nullptr, 0, ce, SideJob{}, status, st)));
   count_launches(1);
   MOE_TRY(launch_k(ce_join_kernel, (T + kJoinRows - 1) / kJoinRows, kJoinRows * kJoinStrands, 0, st, ce.stats,
                    2 * ((V + kTile - 1) / kTile), ce.label_logit, labels, T, V, loss, lse, status));

@@ -45,6 +45,7 @@ enum class Epi : int {
   kSwigluBwd = 3,   // dh -> dz = [dgate_in | dup] (bf16) and partial <dh, h> per row
   kCeStats = 4,     // logits -> per row and tile: maximum, sum of exponentials; the label's logit
   kCeGrad = 5,      // logits -> gradient of the cross entropy (bf16)
+  kCeStatsSeg = 6,  // kCeStats with the contraction added up in segments (see ce_keep)
 };
 
 // The vocabulary head's epilogues (tile columns = vocabulary entries).
@@ -142,6 +143,7 @@ struct GemmParams {
   int kb_per_split;                // kSplitK, or kRoutedK without offsets: k-blocks of one part (0: all)
   int c_add;                       // kSplitK: add to the slabs (1) or overwrite them (0)
   SideJob side;
+  int seg_kb;                      // kCeStatsSeg: k-blocks added up in the tensor cores at a time
   int m_group;                     // cross entropy: row blocks of one group of tiles
   CeParams ce;
 };
@@ -192,7 +194,8 @@ struct GemmCfg {
   // Outputs leave through TMA stores staged in shared memory (every epilogue
   // but the router's narrow fp32 logits, whose rows need not be 16-byte sized).
   // (The cross entropy's statistics are two values a row, stored directly.)
-  static constexpr bool TMA_OUT = !(EP == Epi::kStoreF32 && S == Sched::kDenseM) && EP != Epi::kCeStats;
+  static constexpr bool TMA_OUT =
+      !(EP == Epi::kStoreF32 && S == Sched::kDenseM) && EP != Epi::kCeStats && EP != Epi::kCeStatsSeg;
   // Epilogue warps: four (one per TMEM lane quarter), or eight for 256-row
   // tiles, where the second four write rows 128..255 at the same time.
   // NVFP4 SwiGLU tiles (one accumulator, MMAs fast enough that the MMA warp
@@ -212,6 +215,8 @@ struct GemmCfg {
   // With a short contraction the epilogue is the longer part of a tile: the
   // gradient's logits at 2048 x 512 x 50000 took 175 us on four warps.
   static constexpr bool HEAD = HEAD_;
+  static constexpr bool CE_SEG = EP == Epi::kCeStatsSeg;
+  static constexpr bool CE_STATS = EP == Epi::kCeStats || CE_SEG;
   static constexpr int EPI_WARPS = (M256 || SPLIT_COLS || HEAD) ? 8 : 4;
   // Shared memory (all of it dynamic): the k-block ring, 4 KB staging buffers
   // (32 rows x 128 B, 128B-swizzled) per epilogue warp -- two each, or one
@@ -280,7 +285,7 @@ struct GemmCfg {
   static_assert(!GATHER || (M256 && !MX && !A_MN && S == Sched::kRoutedM && BK == 64),
                 "gathered A: bf16 256-row row-grouped tiles");
   static_assert(!WIDE_K || (A_MN && B_MN), "128-row k-blocks only for MN-major operands");
-  static_assert(!PAIR || (!M256 && !MX && (TMA_OUT || EP == Epi::kCeStats) && BN == 256 &&
+  static_assert(!PAIR || (!M256 && !MX && (TMA_OUT || CE_STATS) && BN == 256 &&
                           (S == Sched::kRoutedK
                                ? (A_MN && B_MN && (EP == Epi::kStoreF32 || EP == Epi::kStoreBf16))
                                : !A_MN)),
@@ -288,7 +293,7 @@ struct GemmCfg {
   static_assert(!HEAD || (!MX && !M256), "the head's GEMMs: bf16, one accumulator row block per CTA");
   static_assert(S != Sched::kSplitK || (HEAD && B_MN && EP == Epi::kStoreF32),
                 "split contraction: bf16, B stored [K, N], fp32 slabs");
-  static_assert((EP != Epi::kCeStats && EP != Epi::kCeGrad) || (HEAD && !B_MN && S == Sched::kDenseM),
+  static_assert((!CE_STATS && EP != Epi::kCeGrad) || (HEAD && !B_MN && S == Sched::kDenseM),
                 "cross entropy: bf16 logits of one dense group");
   static_assert(SMEM_USED <= SMEM_BYTES && SMEM_BYTES <= 232448, "shared memory per CTA");
   static_assert(STAGES >= 2, "pipeline depth");
@@ -378,7 +383,7 @@ __device__ __forceinline__ TileInfo decode_tile(const GemmParams& p, const int* 
   } else if constexpr (C::S == Sched::kDenseM) {
     const int mb = (p.m_rows + C::TILE_M - 1) / C::TILE_M;
     ti.group = 0;
-    if (C::EP == Epi::kCeStats || C::EP == Epi::kCeGrad) {
+    if (C::CE_STATS || C::EP == Epi::kCeGrad) {
       // groups of m_group row blocks walk the columns one after another: the
       // rows of a group stay in L2 while the columns stream past
       const int first = t / (p.m_group * p.n_tiles) * p.m_group;
@@ -825,30 +830,63 @@ __device__ __forceinline__ void side_job(const GemmParams& p, int thread, int th
   }
 }
 
+// A long contraction is added up in segments: the tensor cores align and cut
+// off at every step, always towards zero, so that a logit of 7168 products would
+// be 2e-5 short; with fp32 additions between segments of 2048 it is a quarter
+// of that.  The half tile's sums so far wait in registers (`kept`) while the
+// next segment fills the other accumulator.
+template <class C>
+__device__ __forceinline__ void ce_keep(uint32_t tmem_acc, int quarter, int part, bool first,
+                                        float (&kept)[C::BN / 2]) {
+  const uint32_t t0 = tmem_acc + (static_cast<uint32_t>(quarter * 32) << 16) + part * (C::BN / 2);
+  #pragma unroll
+  for (int c0 = 0; c0 < C::BN / 2; c0 += 32) {
+    uint32_t u[2][16];
+    load32(t0 + c0, u[0], u[1]);
+    #pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const float v = __uint_as_float(u[j >> 4][j & 15]);
+      kept[c0 + j] = first ? v : kept[c0 + j] + v;
+    }
+  }
+}
+
+// The label's logit of one segment.
+template <class C>
+__device__ __forceinline__ float ce_segment_label(const GemmParams& p, const TileInfo& ti, uint32_t tmem_acc,
+                                                  int quarter, int lane, int part, const CeRow& cr) {
+  return ce_label_logit(tmem_acc + (static_cast<uint32_t>(quarter * 32) << 16), cr.label - p.ce.v0 - ti.n * C::BN,
+                        part * (C::BN / 2), C::BN / 2, lane, 0.f);
+}
+
 // release() hands the accumulator back to the MMA warp.  It comes before the
 // row's stores: an arrive after them would wait for them to reach L2, every
-// tile (2048 x 512 against 50000 entries: 102 us, against 76).
-template <class C, class Release>
+// tile.  kept, zl: the sums and the label's logit of the segments before.
+template <class C, int KEPT_COLS, class Release>
 __device__ __forceinline__ void ce_stats_tile(const GemmParams& p, const TileInfo& ti, uint32_t tmem_acc, int quarter,
-                                              int lane, int part, const CeRow& cr, Release&& release) {
+                                              int lane, int part, const CeRow& cr, const float (&kept)[KEPT_COLS],
+                                              float zl, Release&& release) {
   const uint32_t t0 = tmem_acc + (static_cast<uint32_t>(quarter * 32) << 16);
   const int row = ti.m0 + quarter * 32 + lane;
   const bool row_ok = row < p.m_rows;
   const int col0 = p.ce.v0 + ti.n * C::BN;
+  const int begin = part * (C::BN / 2);
   const int nv = min(C::BN, p.ce.vocab - col0);              // columns of this tile in the vocabulary
   const int rel = cr.label - col0;                           // the label's column of this tile
   float m = -INFINITY, s = 0.f;
-  #pragma unroll 1
-  for (int c0 = part * (C::BN / 2); c0 < min(nv, (part + 1) * (C::BN / 2)); c0 += 32) {
+  auto columns = [&](int c0) {                               // 32 columns from c0 of this half on
     uint32_t u[2][16];
-    load32(t0 + c0, u[0], u[1]);
+    load32(t0 + begin + c0, u[0], u[1]);
     float z[32];
     #pragma unroll
-    for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(u[j >> 4][j & 15]);
-    if (c0 + 32 > nv) {
+    for (int j = 0; j < 32; ++j) {
+      z[j] = __uint_as_float(u[j >> 4][j & 15]);
+      if constexpr (C::CE_SEG) z[j] += kept[c0 + j];
+    }
+    if (begin + c0 + 32 > nv) {
       #pragma unroll
       for (int j = 0; j < 32; ++j)
-        if (c0 + j >= nv) z[j] = -INFINITY;
+        if (begin + c0 + j >= nv) z[j] = -INFINITY;
     }
     float cm = z[0];
     #pragma unroll
@@ -860,10 +898,18 @@ __device__ __forceinline__ void ce_stats_tile(const GemmParams& p, const TileInf
     for (int j = 0; j < 32; ++j) t[j & 3] += ex2(fmaf(z[j], kLog2e, -off));
     s = s * ex2(fmaf(m, kLog2e, -off)) + ((t[0] + t[1]) + (t[2] + t[3]));
     m = mn;
+  };
+  if constexpr (C::CE_SEG) {
+    #pragma unroll
+    for (int c0 = 0; c0 < C::BN / 2; c0 += 32)
+      if (begin + c0 < nv) columns(c0);
+  } else {
+    #pragma unroll 1
+    for (int c0 = 0; c0 < C::BN / 2 && begin + c0 < nv; c0 += 32) columns(c0);
   }
-  const float zl = ce_label_logit(t0, rel, part * (C::BN / 2), C::BN / 2, lane, 0.f);
+  zl += ce_label_logit(t0, rel, begin, C::BN / 2, lane, 0.f);
   release();
-  if (rel >= part * (C::BN / 2) && rel < min(nv, (part + 1) * (C::BN / 2))) p.ce.label_logit[row] = zl;
+  if (rel >= begin && rel < min(nv, begin + C::BN / 2)) p.ce.label_logit[row] = zl;
   if (row_ok) p.ce.stats[(2ll * ti.n + part) * p.m_rows + row] = make_float2(m, s);
 }
 
@@ -1808,8 +1854,19 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const TileInfo ti = decode_tile<C>(p, s_poff, s_tpre, t);
         if (!mbar_wait(&tempty_bar[acc], acc_phase ^ 1u, abort_ptr, wait_lim)) { ok = false; break; }
         tc_fence_after_sync();
-        const uint32_t d_tmem = tmem_base + acc * C::ACC_COLS;
+        uint32_t d_tmem = tmem_base + acc * C::ACC_COLS;
+        [[maybe_unused]] int seg = 0;      // k-blocks of this segment so far (kCeStatsSeg)
         for (int kb = 0; kb < ti.num_kb; ++kb) {
+          if constexpr (C::CE_SEG) {
+            if (seg == p.seg_kb) {           // the next segment goes to the other accumulator
+              mma_commit(&tfull_bar[acc]);
+              if (++acc == C::ACC_BUFS) { acc = 0; acc_phase ^= 1u; }
+              if (!mbar_wait(&tempty_bar[acc], acc_phase ^ 1u, abort_ptr, wait_lim)) { ok = false; break; }
+              tc_fence_after_sync();
+              d_tmem = tmem_base + acc * C::ACC_COLS;
+              seg = 0;
+            }
+          }
           if (!mbar_wait(&full_bar[stage], phase, abort_ptr, wait_lim)) { ok = false; break; }
           tc_fence_after_sync();
           const uint32_t a_addr = smem_u32(a_smem + stage * C::A_BYTES);
@@ -1868,7 +1925,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                           : smem_desc_sw128(a_addr + kk * 32, 16, 1024);
               const uint64_t bd = C::B_MN ? smem_desc_sw128(b_addr + kk * 2048, 8192, 1024)
                                           : smem_desc_sw128(b_addr + kk * 32, 16, 1024);
-              mma_bf16_ss(d_tmem, ad, bd, C::IDESC, (kb | kk) != 0 ? 1u : 0u);
+              mma_bf16_ss(d_tmem, ad, bd, C::IDESC, ((C::CE_SEG ? seg : kb) | kk) != 0 ? 1u : 0u);
               if constexpr (C::M256) {
                 // rows 128..255 of the A tile (16 KB further on) against the same B k-block
                 if (ti.half1)
@@ -1878,6 +1935,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
           }
           any = true;
+          if constexpr (C::CE_SEG) ++seg;
           mma_commit(&empty_bar[stage]);
           if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
         }
@@ -1910,7 +1968,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       if (t < 0) break;
       const TileInfo ti = decode_tile<C>(p, s_poff, s_tpre, t);
       [[maybe_unused]] CeRow cr{};
-      if constexpr (C::EP == Epi::kCeStats || C::EP == Epi::kCeGrad) cr = ce_row<C>(p, ti.m0 + quarter * 32 + lane);
+      if constexpr (C::CE_STATS || C::EP == Epi::kCeGrad) cr = ce_row<C>(p, ti.m0 + quarter * 32 + lane);
       if (!mbar_wait(&tfull_bar[acc], acc_phase, abort_ptr, wait_lim)) break;
       tc_fence_after_sync();
       bool released = false;                 // accumulator already handed back by the epilogue
@@ -1920,6 +1978,24 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (lane == 0) mbar_arrive(&tempty_bar[acc]);
         released = true;
       };
+      if constexpr (C::CE_SEG) {
+        float kept[C::BN / 2], zl = 0.f;
+        bool first = true, ok = true;
+        for (int left = ti.num_kb - p.seg_kb; left > 0; left -= p.seg_kb, first = false) {   // segments after this
+          const uint32_t t_acc = tmem_base + acc * C::ACC_COLS;
+          ce_keep<C>(t_acc, quarter, part, first, kept);
+          zl += ce_segment_label<C>(p, ti, t_acc, quarter, lane, part, cr);
+          release();
+          if (++acc == C::ACC_BUFS) { acc = 0; acc_phase ^= 1u; }
+          if (!mbar_wait(&tfull_bar[acc], acc_phase, abort_ptr, wait_lim)) { ok = false; break; }
+          tc_fence_after_sync();
+        }
+        if (!ok) break;
+        ce_stats_tile<C>(p, ti, tmem_base + acc * C::ACC_COLS, quarter, lane, part, cr, kept, zl, release);
+      } else if constexpr (C::CE_STATS) {
+        const float none[1] = {};
+        ce_stats_tile<C>(p, ti, tmem_base + acc * C::ACC_COLS, quarter, lane, part, cr, none, 0.f, release);
+      } else
       if constexpr (C::M256) {
         if (part == 0 || ti.half1) {
           TileInfo th = ti;
@@ -1927,8 +2003,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           epilogue_tile_tma<C>(p, th, tmem_base + acc * C::ACC_COLS + part * C::BN, quarter, lane, st, &tmC, &tmC2,
                                &tempty_bar[acc], &released, al);
         }
-      } else if constexpr (C::EP == Epi::kCeStats) {
-        ce_stats_tile<C>(p, ti, tmem_base + acc * C::ACC_COLS, quarter, lane, part, cr, release);
       } else if constexpr (C::EP == Epi::kCeGrad) {
         ce_grad_tile<C>(p, ti, tmem_base + acc * C::ACC_COLS, quarter, lane, st, &tmC, part, cr, release);
       } else if constexpr (C::TMA_OUT) {
@@ -2140,8 +2214,19 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const TileInfo ti = decode_tile<C>(p, s_poff, s_tpre, t);
         if (!mbar_wait_cluster(&tempty_bar[acc], acc_phase ^ 1u, abort_ptr, wait_lim)) { ok = false; break; }
         tc_fence_after_sync();
-        const uint32_t d_tmem = tmem_base + acc * C::ACC_COLS;
+        uint32_t d_tmem = tmem_base + acc * C::ACC_COLS;
+        [[maybe_unused]] int seg = 0;      // k-blocks of this segment so far (kCeStatsSeg)
         for (int kb = 0; kb < ti.num_kb; ++kb) {
+          if constexpr (C::CE_SEG) {
+            if (seg == p.seg_kb) {           // the next segment goes to the other accumulator
+              mma_commit_pair_both(&tfull_bar[acc]);
+              if (++acc == C::ACC_BUFS) { acc = 0; acc_phase ^= 1u; }
+              if (!mbar_wait_cluster(&tempty_bar[acc], acc_phase ^ 1u, abort_ptr, wait_lim)) { ok = false; break; }
+              tc_fence_after_sync();
+              d_tmem = tmem_base + acc * C::ACC_COLS;
+              seg = 0;
+            }
+          }
           if (!mbar_wait(&full_bar[stage], phase, abort_ptr, wait_lim)) { ok = false; break; }
           tc_fence_after_sync();
           const uint32_t a_addr = smem_u32(a_smem + stage * C::A_BYTES);
@@ -2152,9 +2237,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                         : smem_desc_sw128(a_addr + kk * 32, 16, 1024);
             const uint64_t bd = C::B_MN ? smem_desc_sw128(b_addr + kk * 2048, C::MN_CHUNK, 1024)
                                         : smem_desc_sw128(b_addr + kk * 32, 16, 1024);
-            mma_bf16_pair(d_tmem, ad, bd, C::IDESC, (kb | kk) != 0 ? 1u : 0u);
+            mma_bf16_pair(d_tmem, ad, bd, C::IDESC, ((C::CE_SEG ? seg : kb) | kk) != 0 ? 1u : 0u);
           }
           any = true;
+          if constexpr (C::CE_SEG) ++seg;
           mma_commit_pair_both(&empty_bar[stage]);
           if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
         }
@@ -2180,7 +2266,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     for (int t = cid; t < ntiles; t += ncl) {
       const TileInfo ti = decode_tile<C>(p, s_poff, s_tpre, t);
       [[maybe_unused]] CeRow cr{};
-      if constexpr (C::EP == Epi::kCeStats || C::EP == Epi::kCeGrad)
+      if constexpr (C::CE_STATS || C::EP == Epi::kCeGrad)
         cr = ce_row<C>(p, ti.m0 + 128 * static_cast<int>(rank) + quarter * 32 + lane);
       if (!mbar_wait(&tfull_bar[acc], acc_phase, abort_ptr, wait_lim)) break;
       tc_fence_after_sync();
@@ -2194,13 +2280,35 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         released = true;
       };
-      if (leader || ti.half1) {           // a half tile: the odd CTA's rows are not this expert's
+      const bool mine = leader || ti.half1;   // a half tile: the odd CTA's rows are not this expert's
+      if constexpr (C::CE_SEG) {
+        TileInfo th = ti;
+        th.m0 += 128 * static_cast<int>(rank);
+        float kept[C::BN / 2], zl = 0.f;
+        bool first = true, ok = true;
+        for (int left = ti.num_kb - p.seg_kb; left > 0; left -= p.seg_kb, first = false) {   // segments after this
+          const uint32_t t_acc = tmem_base + acc * C::ACC_COLS;
+          if (mine) {
+            ce_keep<C>(t_acc, quarter, part, first, kept);
+            zl += ce_segment_label<C>(p, th, t_acc, quarter, lane, part, cr);
+          }
+          release();
+          released = false;
+          if (++acc == C::ACC_BUFS) { acc = 0; acc_phase ^= 1u; }
+          if (!mbar_wait(&tfull_bar[acc], acc_phase, abort_ptr, wait_lim)) { ok = false; break; }
+          tc_fence_after_sync();
+        }
+        if (!ok) break;
+        if (mine) ce_stats_tile<C>(p, th, tmem_base + acc * C::ACC_COLS, quarter, lane, part, cr, kept, zl, release);
+      } else
+      if (mine) {
         TileInfo th = ti;
         th.m0 += 128 * static_cast<int>(rank);
         const uint32_t t_acc = tmem_base + acc * C::ACC_COLS;
-        if constexpr (C::EP == Epi::kCeStats)
-          ce_stats_tile<C>(p, th, t_acc, quarter, lane, part, cr, release);
-        else if constexpr (C::EP == Epi::kCeGrad)
+        if constexpr (C::CE_STATS) {
+          const float none[1] = {};
+          ce_stats_tile<C>(p, th, t_acc, quarter, lane, part, cr, none, 0.f, release);
+        } else if constexpr (C::EP == Epi::kCeGrad)
           ce_grad_tile<C>(p, th, t_acc, quarter, lane, st, &tmC, part, cr, release);
         else
           epilogue_tile_tma<C>(p, th, t_acc, quarter, lane, st, &tmC, &tmC2, nullptr, nullptr, 1.0f, part);
