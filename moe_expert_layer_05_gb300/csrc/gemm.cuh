@@ -1629,7 +1629,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmC2,
                         const GemmParams p) {
-  pdl_wait();
+  if constexpr (!C::HEAD) pdl_wait();
   static_assert(sizeof(GemmBook<C>) <= C::BOOK_BYTES, "bookkeeping size");
   static_assert(!C::PAIR, "CTA-pair tiles run in grouped_gemm_pair_kernel");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -1637,6 +1637,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // the ring needs a 1024-byte aligned base inside the allocation
     const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
     if (pad + C::SMEM_USED > static_cast<uint32_t>(C::SMEM_BYTES)) {
+      if constexpr (C::HEAD) pdl_wait();
       if (threadIdx.x == 0) {
         set_status(p.status, kErrLaunch);
         sched_finish(p.sched);
@@ -1704,6 +1705,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
+  if constexpr (C::HEAD) pdl_wait();     // (nothing above touches global memory)
   const uint32_t tmem_base = tmem_slot;
   volatile int* abort_ptr = &abort_flag;
   const unsigned long long wait_lim = p.wait_ns != 0 ? p.wait_ns : kWaitLimitNs;
@@ -2091,7 +2093,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                              const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmC2,
                              const GemmParams p) {
-  pdl_wait();
+  if constexpr (!C::HEAD) pdl_wait();
   static_assert(C::PAIR, "pair configuration");
   static_assert(sizeof(GemmBook<C>) <= C::BOOK_BYTES, "bookkeeping size");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -2102,6 +2104,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   {
     const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
     if (pad + C::SMEM_USED > static_cast<uint32_t>(C::SMEM_BYTES)) {
+      if constexpr (C::HEAD) pdl_wait();
       if (threadIdx.x == 0) set_status(p.status, kErrLaunch);
       cluster_sync();   // the peer meets both cluster barriers whatever it finds
       cluster_sync();
@@ -2158,6 +2161,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   __syncthreads();
   cluster_sync();                       // barriers of both CTAs initialised before any cross-CTA signal
   tc_fence_after_sync();
+  if constexpr (C::HEAD) pdl_wait();     // (nothing above touches global memory)
   const uint32_t tmem_base = bk.tmem_slot;
   volatile int* abort_ptr = &bk.abort_flag;
   const unsigned long long wait_lim = p.wait_ns != 0 ? p.wait_ns : kWaitLimitNs;

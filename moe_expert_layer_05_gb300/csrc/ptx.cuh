@@ -30,7 +30,8 @@ constexpr int kSchedCounterWord = 32;
 // kernels then let the next grid launch at once (pdl_entry); the persistent
 // GEMMs only once their tiles are done (pdl_wait first, pdl_launch_next at
 // their teardown) -- a GEMM that released its dependents at its start ran
-// the long layers about 0.5 % slower.  (A kernel whose predecessor was
+// the long layers about 0.5 % slower.  The vocabulary head's GEMMs set up
+// their barriers and TMEM before the wait.  (A kernel whose predecessor was
 // launched without the attribute simply starts after it, as usual.)
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
