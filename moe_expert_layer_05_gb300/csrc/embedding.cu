@@ -15,7 +15,7 @@
 // one GB300 (a plain copy reaches 6.68 TB/s): lookup of 16384 x 4096 31 us
 // (6.24 TB/s); gradient of 16384 rows into 32000 x 7168 195 us (5.91 TB/s: sort
 // 17, whole chunks 9, rows 165); 1003 rows into 50001 x 1024 on top of `base`
-// 62 us (4.99 TB/s: the sort's two passes and its launch are 10 of them).
+// 60 us (5.17 TB/s: sort 7, rows 50).
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -117,8 +117,9 @@ __device__ __forceinline__ uint32_t key_of(const int32_t* __restrict__ tokens, i
   return static_cast<uint32_t>(V);
 }
 
-// Up to kClusterSort positions: the whole sort in one cluster of eight blocks.
-// Each block holds an eighth of the pairs, in registers while it ranks them and
+// Up to kClusterSort positions: the whole sort in one launch, by one block (up
+// to kBlockSort positions) or a cluster of eight (16384 positions in 17 us;
+// BLOCKS).  Each block holds its share of the pairs, in registers while it ranks them and
 // in shared memory between the passes.  A pass ranks the pairs as
 // sort_scatter_kernel does, with the digit counts of every warp in shared
 // memory; the blocks read each other's counts and write the pairs to their
@@ -130,11 +131,12 @@ constexpr int kClusterThreads = 512;                  // (half an SM's registers
 constexpr int kClusterWarps = kClusterThreads / 32;
 constexpr int kClusterItems = 16;                     // pairs per thread at most
 constexpr int kClusterSort = kCluster * kClusterThreads * kClusterItems;
-__host__ __device__ constexpr int cluster_rounds(int n) {
-  return (n + kCluster * kClusterThreads - 1) / (kCluster * kClusterThreads);
+constexpr int kBlockSort = 2 * kClusterThreads;       // (beyond, a cluster's eight times fewer rounds are faster)
+__host__ __device__ constexpr int sort_rounds(int n, int blocks) {
+  return (n + blocks * kClusterThreads - 1) / (blocks * kClusterThreads);
 }
-size_t cluster_sort_smem(int n) {
-  return static_cast<size_t>(kClusterWarps) * kBins * 2 + static_cast<size_t>(cluster_rounds(n)) * kClusterThreads * 8;
+size_t sort_smem(int n, int blocks) {
+  return static_cast<size_t>(kClusterWarps) * kBins * 2 + static_cast<size_t>(sort_rounds(n, blocks)) * kClusterThreads * 8;
 }
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   uint32_t v;
@@ -144,6 +146,13 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
 __device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+// Barrier over the blocks that sort together.
+template <int BLOCKS>
+__device__ __forceinline__ void sort_sync() {
+  if constexpr (BLOCKS > 1) cluster_sync();
+  else __syncthreads();
+}
+template <int BLOCKS>
 __device__ __forceinline__ void cluster_sort(const int32_t* __restrict__ tokens, int n, int V, int passes,
                                              uint32_t* __restrict__ keys_out, int32_t* __restrict__ pos_out,
                                              int* status, uint8_t* s_raw) {
@@ -151,8 +160,8 @@ __device__ __forceinline__ void cluster_sort(const int32_t* __restrict__ tokens,
   __shared__ uint32_t s_base[kBins];                  // where they go
   __shared__ int s_warp[kClusterWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t me = cluster_ctarank();
-  const int rounds = cluster_rounds(n), slice = rounds * kClusterThreads;
+  const uint32_t me = BLOCKS > 1 ? cluster_ctarank() : 0;
+  const int rounds = sort_rounds(n, BLOCKS), slice = rounds * kClusterThreads;
   uint16_t* s_cnt = reinterpret_cast<uint16_t*>(s_raw);              // [warp][bin]
   uint32_t* s_key = reinterpret_cast<uint32_t*>(s_cnt + kClusterWarps * kBins);
   uint32_t* s_pos = s_key + slice;
@@ -199,14 +208,18 @@ __device__ __forceinline__ void cluster_sort(const int32_t* __restrict__ tokens,
       }
       s_total[tid] = run;
     }
-    cluster_sync();
+    sort_sync<BLOCKS>();
     int total = 0, before = 0;            // bin tid: pairs of all blocks, and of those before this one
     if (tid < kBins) {
-      #pragma unroll
-      for (uint32_t r = 0; r < kCluster; ++r) {
-        const int c = static_cast<int>(ld_cluster_u32(mapa_shared(smem_u32(&s_total[tid]), r)));
-        total += c;
-        if (r < me) before += c;
+      if constexpr (BLOCKS > 1) {
+        #pragma unroll
+        for (uint32_t r = 0; r < BLOCKS; ++r) {
+          const int c = static_cast<int>(ld_cluster_u32(mapa_shared(smem_u32(&s_total[tid]), r)));
+          total += c;
+          if (r < me) before += c;
+        }
+      } else {
+        total = static_cast<int>(s_total[tid]);
       }
     }
     int inc = total;
@@ -228,13 +241,18 @@ __device__ __forceinline__ void cluster_sort(const int32_t* __restrict__ tokens,
       if (j < rounds && w0 + j * 32 < mine) {
         const int d = static_cast<int>((key[j] >> shift) & (kBins - 1));
         const uint32_t to = s_base[d] + my_cnt[d] + rank[j];
-        const uint32_t block = (to / kClusterThreads) / static_cast<uint32_t>(rounds);
-        const uint32_t at = to - block * static_cast<uint32_t>(slice);
-        st_cluster_u32(mapa_shared(smem_u32(s_key + at), block), key[j]);
-        st_cluster_u32(mapa_shared(smem_u32(s_pos + at), block), where[j]);
+        if constexpr (BLOCKS > 1) {
+          const uint32_t block = (to / kClusterThreads) / static_cast<uint32_t>(rounds);
+          const uint32_t at = to - block * static_cast<uint32_t>(slice);
+          st_cluster_u32(mapa_shared(smem_u32(s_key + at), block), key[j]);
+          st_cluster_u32(mapa_shared(smem_u32(s_pos + at), block), where[j]);
+        } else {
+          s_key[to] = key[j];
+          s_pos[to] = where[j];
+        }
       }
     }
-    cluster_sync();                       // every block's pairs are in their places
+    sort_sync<BLOCKS>();                  // every block's pairs are in their places
     if (pass + 1 < passes) {
       #pragma unroll
       for (int j = 0; j < kClusterItems; ++j) {
@@ -244,6 +262,7 @@ __device__ __forceinline__ void cluster_sort(const int32_t* __restrict__ tokens,
           where[j] = s_pos[i];
         }
       }
+      if constexpr (BLOCKS == 1) __syncthreads();
     }
   }
   const long long g0 = static_cast<long long>(me) * slice;
@@ -364,20 +383,32 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(const int32_
 }
 
 // ---------------------------------------------------------------- rows
-// First launch (up to kClusterSort positions): the first cluster sorts; the
-// other blocks clear the flags of the rows that have a token.
-constexpr int kClearRows = 1 << 17;     // flags one other cluster clears
+// First launch (up to kClusterSort positions): the first block or cluster sorts;
+// the others clear the flags of the rows that have a token.
+constexpr int kClearRows = 1 << 14;     // flags one other block clears
+template <int BLOCKS>
+__device__ __forceinline__ void sort_launch(const int32_t* __restrict__ tokens, int n, int V, int passes,
+                                            uint32_t* __restrict__ keys_out, int32_t* __restrict__ pos_out,
+                                            uint8_t* __restrict__ has, int* status) {
+  extern __shared__ __align__(16) uint8_t s_raw[];
+  if (blockIdx.x < BLOCKS) {
+    cluster_sort<BLOCKS>(tokens, n, V, passes, keys_out, pos_out, status, s_raw);
+    return;
+  }
+  const int block = blockIdx.x - BLOCKS, blocks = gridDim.x - BLOCKS;
+  for (int v = block * kClusterThreads + threadIdx.x; v < V; v += blocks * kClusterThreads) has[v] = 0;
+}
+__global__ void __launch_bounds__(kClusterThreads)
+    block_sort_kernel(const int32_t* __restrict__ tokens, int n, int V, int passes, uint32_t* __restrict__ keys_out,
+                      int32_t* __restrict__ pos_out, uint8_t* __restrict__ has, int* status) {
+  pdl_entry();
+  sort_launch<1>(tokens, n, V, passes, keys_out, pos_out, has, status);
+}
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kClusterThreads)
     cluster_sort_kernel(const int32_t* __restrict__ tokens, int n, int V, int passes, uint32_t* __restrict__ keys_out,
                         int32_t* __restrict__ pos_out, uint8_t* __restrict__ has, int* status) {
   pdl_entry();
-  extern __shared__ __align__(16) uint8_t s_raw[];
-  if (blockIdx.x < kCluster) {
-    cluster_sort(tokens, n, V, passes, keys_out, pos_out, status, s_raw);
-    return;
-  }
-  const int block = blockIdx.x - kCluster, blocks = gridDim.x - kCluster;
-  for (int v = block * kClusterThreads + threadIdx.x; v < V; v += blocks * kClusterThreads) has[v] = 0;
+  sort_launch<kCluster>(tokens, n, V, passes, keys_out, pos_out, has, status);
 }
 
 // For more positions: the flags of the rows that have a token, cleared here and
@@ -427,6 +458,7 @@ __global__ void __launch_bounds__(128) embedding_chunks_kernel(const uint32_t* _
 // so a block reads at most 62 rows of dy, however often a token occurs.  The
 // other fills those of fill_rows rows that have no token.
 constexpr int kBatch = 4;
+constexpr int kFollow = 6;
 __global__ void __launch_bounds__(128, 8) embedding_rows_kernel(const uint32_t* __restrict__ keys,
                                                              const int32_t* __restrict__ pos, int n, int V, int words,
                                                              int cols, int run_blocks, const uint4* __restrict__ dy,
@@ -453,10 +485,11 @@ __global__ void __launch_bounds__(128, 8) embedding_rows_kernel(const uint32_t* 
       return;
     }
   }
-  const int c = block % cols * 128 + tid;
+  const int c_ = block % cols * 128 + tid;
   block /= cols;
   const int i0 = block * kBatch, len = min(n - i0, kBatch);
-  if (c >= words) return;
+  const bool mine = c_ < words;           // (the other lanes of the last warp go along: they share the lookups)
+  const int c = mine ? c_ : 0, lane = tid & 31;
   const uint32_t none = static_cast<uint32_t>(V);   // keys from here on are no token
   uint32_t key[kBatch];
   int at[kBatch];
@@ -471,7 +504,7 @@ __global__ void __launch_bounds__(128, 8) embedding_rows_kernel(const uint32_t* 
     #pragma unroll
     for (int j = 0; j < 8; ++j) a[j] *= scale;
     add_row8(a, b);
-    store8(dtable + (static_cast<long long>(v) * words + c) * 8, a);
+    if (mine) store8(dtable + (static_cast<long long>(v) * words + c) * 8, a);
     #pragma unroll
     for (int j = 0; j < 8; ++j) a[j] = 0.f;
   };
@@ -480,9 +513,9 @@ __global__ void __launch_bounds__(128, 8) embedding_rows_kernel(const uint32_t* 
   #pragma unroll
   for (int u = 0; u < kBatch; ++u) {
     d[u] = b[u] = make_uint4(0, 0, 0, 0);
-    const bool mine = key[u] < none && key[u] != before;
-    if (mine) d[u] = dy[static_cast<long long>(at[u]) * words + c];
-    if (mine && base != nullptr && (u == 0 || key[u] != key[u - 1]))
+    const bool begins = key[u] < none && key[u] != before;   // (its run begins in this batch)
+    if (begins) d[u] = dy[static_cast<long long>(at[u]) * words + c];
+    if (begins && base != nullptr && (u == 0 || key[u] != key[u - 1]))
       b[u] = base[static_cast<long long>(key[u]) * words + c];
   }
   uint32_t cur = none;                    // the run being summed (none: not yet one that begins here)
@@ -504,57 +537,48 @@ __global__ void __launch_bounds__(128, 8) embedding_rows_kernel(const uint32_t* 
     }
   }
   if (cur >= none) return;
-  // single positions up to `stop` (a chunk border or the end); false where the run ends
+  // Positions up to `stop`, at most a chunk further (one lookup: a lane each);
+  // false where the run ends before.
   auto follow = [&](int stop) {
-    while (i < stop) {
-      uint32_t k[kBatch];
-      uint4 e[kBatch];
+    const uint32_t k = i + lane < stop ? keys[i + lane] : none;
+    const int p = i + lane < stop ? pos[i + lane] : 0;
+    const int count = __popc(__ballot_sync(kFull, k == cur));     // (sorted: the first ones)
+    for (int r = 0; r < count; r += kFollow) {
+      uint4 e[kFollow];
       #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        k[u] = i + u < stop ? keys[i + u] : none;
-        at[u] = i + u < stop ? pos[i + u] : 0;
+      for (int u = 0; u < kFollow; ++u) {
+        const int row = __shfl_sync(kFull, p, (r + u) & 31);
+        if (r + u < count) e[u] = dy[static_cast<long long>(row) * words + c];
       }
       #pragma unroll
-      for (int u = 0; u < kBatch; ++u)
-        if (k[u] == cur) e[u] = dy[static_cast<long long>(at[u]) * words + c];
-      #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        if (k[u] == cur) {
-          add_row8(a, e[u]);
-          ++i;
-        }
-      }
-      if (k[kBatch - 1] != cur) return i == stop;
+      for (int u = 0; u < kFollow; ++u)
+        if (r + u < count) add_row8(a, e[u]);
     }
-    return true;
+    i += count;
+    return i == stop;
   };
   if (follow(min(n, (i + kChunk - 1) / kChunk * kChunk))) {
-    // whole chunks, four on their way at a time, then the chunk it ends in
-    for (int more = kBatch; more == kBatch;) {
+    // whole chunks, 32 looked up at a time, then the chunk it ends in
+    for (int more = 32; more == 32;) {
       const int chunk = i / kChunk;
-      uint32_t k[kBatch];
-      #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const long long last = static_cast<long long>(chunk + u + 1) * kChunk - 1;
-        k[u] = last < n ? keys[last] : none;
-      }
-      more = 0;
-      #pragma unroll
-      for (int u = 0; u < kBatch; ++u) more += k[u] == cur ? 1 : 0;    // (sorted: the first ones)
-      float4 p[kBatch][2];
-      #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        if (u < more) {
-          const float4* src = part + (static_cast<long long>(chunk + u) * words + c) * 2;
-          p[u][0] = src[0];
-          p[u][1] = src[1];
+      const long long last = static_cast<long long>(chunk + lane + 1) * kChunk - 1;
+      more = __popc(__ballot_sync(kFull, last < n && keys[last] == cur));
+      for (int r = 0; r < more; r += 4) {
+        float4 q[4][2];
+        #pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (r + u < more) {
+            const float4* src = part + (static_cast<long long>(chunk + r + u) * words + c) * 2;
+            q[u][0] = src[0];
+            q[u][1] = src[1];
+          }
         }
-      }
-      #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        if (u < more) {
-          a[0] += p[u][0].x; a[1] += p[u][0].y; a[2] += p[u][0].z; a[3] += p[u][0].w;
-          a[4] += p[u][1].x; a[5] += p[u][1].y; a[6] += p[u][1].z; a[7] += p[u][1].w;
+        #pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (r + u < more) {
+            a[0] += q[u][0].x; a[1] += q[u][0].y; a[2] += q[u][0].z; a[3] += q[u][0].w;
+            a[4] += q[u][1].x; a[5] += q[u][1].y; a[6] += q[u][1].z; a[7] += q[u][1].w;
+          }
         }
       }
       i += more * kChunk;
@@ -593,14 +617,17 @@ T* at(void* ws, size_t off) {
   return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
 }
 
-// Once per device: the cluster sort's shared memory.
+// Once per device: the sorts' shared memory.
 cudaError_t sort_attr() {
   static std::atomic<bool> set[64];
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (set[dev].load(std::memory_order_acquire)) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(cluster_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(cluster_sort_smem(kClusterSort)));
+  cudaError_t e = cudaFuncSetAttribute(cluster_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(sort_smem(kClusterSort, kCluster)));
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(block_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(sort_smem(kBlockSort, 1)));
   if (e == cudaSuccess) set[dev].store(true, std::memory_order_release);
   return e;
 }
@@ -658,9 +685,10 @@ moe_status moe_embedding_backward(const int32_t* tokens, int32_t n, const void* 
   int cur = 0, launches = 0;
   if (n <= kClusterSort) {
     if (sort_attr() != cudaSuccess) return MOE_ERR_CUDA;
-    const int grid = (1 + (V + kClearRows - 1) / kClearRows) * kCluster;
-    if (launch_k(cluster_sort_kernel, grid, kClusterThreads, cluster_sort_smem(n), st, tokens, n, V, passes,
-                 at<uint32_t>(ws, w.keys[0]), at<int32_t>(ws, w.pos[0]), has, status) != cudaSuccess)
+    const int clear = (V + kClearRows - 1) / kClearRows, blocks = n <= kBlockSort ? 1 : kCluster;
+    if (launch_k(blocks == 1 ? block_sort_kernel : cluster_sort_kernel,
+                 blocks + (clear + blocks - 1) / blocks * blocks, kClusterThreads, sort_smem(n, blocks), st, tokens, n,
+                 V, passes, at<uint32_t>(ws, w.keys[0]), at<int32_t>(ws, w.pos[0]), has, status) != cudaSuccess)
       return MOE_ERR_CUDA;
     launches = 1;
   } else {
@@ -685,7 +713,9 @@ moe_status moe_embedding_backward(const int32_t* tokens, int32_t n, const void* 
   const uint4* dy16 = static_cast<const uint4*>(dy);
   const long long sums = static_cast<long long>((n + kChunk - 1) / kChunk) * cols;
   const long long runs = static_cast<long long>((n + kBatch - 1) / kBatch) * cols;
-  const int fill_rows = words * 32 >= 65536 ? 1 : 65536 / (words * 32);      // 64 KB a block
+  // rows one block fills: 64 KB, less where that would leave SMs without a block
+  int fill_rows = words * 32 >= 65536 ? 1 : 65536 / (words * 32);
+  if (fill_rows > (V + 1215) / 1216) fill_rows = (V + 1215) / 1216 < 4 ? 4 : (V + 1215) / 1216;
   const long long fills = (static_cast<long long>(V) + fill_rows - 1) / fill_rows;
   if (sums > 0) {
     if (launch_k(embedding_chunks_kernel, static_cast<unsigned>(sums), 128, 0, st, keys, pos, n, V, words, cols, dy16,

@@ -78,7 +78,7 @@ def test_embedding_forward_exact(lib, n, V, H, scale):
 
 
 @pytest.mark.parametrize("n,V,H", [(0, 7, 64), (1, 1, 8), (1, 1000, 128), (63, 10, 64), (64, 10, 64), (65, 3, 1000),
-                                   (2048, 256, 64), (2049, 255, 72), (5000, 70000, 64), (16384, 700, 256),
+                                   (2048, 256, 64), (2049, 255, 72), (4097, 600, 64), (5000, 70000, 64), (16384, 700, 256),
                                    (20011, 50001, 128), (70000, 65536, 16), (16385, 300_000, 8), (65536, 40_000, 8), (65537, 40_001, 8)])
 @pytest.mark.parametrize("kind", ["random", "zipf", "same", "none"])
 @pytest.mark.parametrize("tied", [False, True])
