@@ -48,7 +48,7 @@ typedef enum {
   MOE_ERR_UNSUPPORTED = -2,  /* not a GB300, or a shape outside the limits below */
   MOE_ERR_CUDA = -3,         /* a CUDA runtime / driver call failed */
   MOE_ERR_WORKSPACE = -4,    /* workspace or activation buffer too small */
-  MOE_ERR_BAD_INDEX = -5,    /* device: an expert index was outside [0, E) */
+  MOE_ERR_BAD_INDEX = -5,    /* device: an expert index was outside [0, E), or a token id or label outside [0, V) */
   MOE_ERR_TIMEOUT = -6       /* device: a pipeline wait exceeded its limit */
 } moe_status;
 
@@ -504,7 +504,7 @@ moe_status moe_embedding_forward(const int32_t* tokens, int32_t n, const void* t
 moe_status moe_embedding_backward(const int32_t* tokens, int32_t n, const void* dy, int32_t V, int32_t H, float scale,
                                   const void* base, float* dtable, void* ws, size_t ws_bytes, void* stream);
 
-/* Layer norm with the residual sum in front of it.
+/* Layer norm with the residual sum in front of it (0 <= T <= 2^30).
  *   s = x + residual rounded to bf16 (s = x without a residual),
  *   y = (s - mean) * rstd * weight + bias,  rstd = 1 / sqrt(var + eps),
  * mean and (biased) variance over H of s, in fp32.  x, residual [T,H] bf16

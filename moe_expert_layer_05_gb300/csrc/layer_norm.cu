@@ -454,6 +454,8 @@ cudaError_t bwd(const BwdShape& b, const void* dy, const void* s, const void* we
                   b.stages, static_cast<uint4*>(dx), part, status, wait != 0 ? wait : kWaitLimitNs);
 }
 
+bool rows_ok(int32_t T) { return T >= 0 && T <= (1 << 30); }
+
 }  // namespace
 }  // namespace moe
 
@@ -463,7 +465,7 @@ using namespace moe::entry;
 extern "C" {
 
 size_t moe_layer_norm_workspace_bytes(int32_t T, int32_t H) {
-  if (T < 0 || !hidden_ok(H)) return 0;
+  if (!rows_ok(T) || !hidden_ok(H)) return 0;
   const size_t blocks = T < kBwdBlocks ? T : kBwdBlocks;
   return kStatusBytes + align_up(blocks * 2 * H * sizeof(float));
 }
@@ -471,7 +473,7 @@ size_t moe_layer_norm_workspace_bytes(int32_t T, int32_t H) {
 moe_status moe_layer_norm_forward(const void* x, const void* residual, const void* weight, const void* bias, int32_t T,
                                   int32_t H, float eps, void* y, void* sum_out, float* mean, float* rstd,
                                   void* stream) {
-  if (T < 0 || !hidden_ok(H) || !(eps >= 0.f)) return MOE_ERR_INVALID_ARG;
+  if (!rows_ok(T) || !hidden_ok(H) || !(eps >= 0.f)) return MOE_ERR_INVALID_ARG;
   if (!ptr_ok(weight) || !opt_ok(bias)) return MOE_ERR_INVALID_ARG;
   if (T > 0 && (!ptr_ok(x) || !opt_ok(residual) || !ptr_ok(y) || !ptr_ok(mean) || !ptr_ok(rstd)))
     return MOE_ERR_INVALID_ARG;
@@ -493,7 +495,7 @@ moe_status moe_layer_norm_forward(const void* x, const void* residual, const voi
 moe_status moe_layer_norm_backward(const void* dy, const void* s, const void* weight, const float* mean,
                                    const float* rstd, const void* dsum, int32_t T, int32_t H, void* dx, float* dweight,
                                    float* dbias, void* ws, size_t ws_bytes, void* stream) {
-  if (T < 0 || !hidden_ok(H)) return MOE_ERR_INVALID_ARG;
+  if (!rows_ok(T) || !hidden_ok(H)) return MOE_ERR_INVALID_ARG;
   if (!ptr_ok(weight) || !ptr_ok(dweight) || !opt_ok(dbias) || !ptr_ok(ws)) return MOE_ERR_INVALID_ARG;
   if (T > 0 && (!ptr_ok(dy) || !ptr_ok(s) || !ptr_ok(mean) || !ptr_ok(rstd) || !opt_ok(dsum) || !ptr_ok(dx)))
     return MOE_ERR_INVALID_ARG;

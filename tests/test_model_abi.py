@@ -37,6 +37,14 @@ def test_bad_counts_refused(n, V):
     assert lib.moe_cross_entropy_backward(16, 16, 16, 16, 16, n, 64, V, 0, 16, 16, 16, BIG, None) == -1
 
 
+@pytest.mark.parametrize("T", [-1, (1 << 30) + 1])
+def test_bad_row_counts_refused(T):
+    lib = api.load()
+    assert lib.moe_layer_norm_workspace_bytes(T, 64) == 0
+    assert lib.moe_layer_norm_forward(16, None, 16, None, T, 64, 1e-5, 16, None, 16, 16, None) == -1
+    assert lib.moe_layer_norm_backward(16, 16, 16, 16, 16, None, T, 64, 16, 16, 16, 16, BIG, None) == -1
+
+
 def _each_pointer(call, required, optional=()):
     """Every required pointer missing or misaligned, every optional one misaligned."""
     for i in required:
