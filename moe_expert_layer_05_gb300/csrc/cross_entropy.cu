@@ -77,7 +77,7 @@ bool small_rows(int T) { return T <= 128; }
 // rounds, so the contraction is cut into as many parts as make rounds x (part +
 // a tile's start and end, some 8 k-blocks) least.  dx at T = 4096, H = 4096
 // (256 tiles on 76 pairs): two parts take 7 rounds of half the length instead
-// of 4.
+// of 4.  A further part has to save 1 %: it is a slab more of workspace.
 int kb_per_split(int tiles, int units, int kb) {
   int best = kb;
   long long least = -1;
@@ -86,7 +86,7 @@ int kb_per_split(int tiles, int units, int kb) {
     const int parts = (kb + per - 1) / per;
     const long long rounds = (static_cast<long long>(tiles) * parts + units - 1) / units;
     const long long cost = rounds * (per + 8) + parts;        // (a slab more to write and to add)
-    if (least < 0 || cost < least) {
+    if (least < 0 || cost * 100 < least * 99) {
       least = cost;
       best = per;
     }
@@ -245,12 +245,12 @@ cudaError_t gemm_dw(const void* d, int ld, int T, const void* x, int H, void* dw
 // cores' tiles read 128 bytes of each of 256 rows at a time, which costs HBM a
 // quarter of its rate: one token, 131072 x 4096, in 190 us, against 159 here,
 // 6.7 TB/s; from four tokens on the arithmetic here takes longer than that.)
-// A warp takes kFewStep entries at a time, lanes the words of their rows; x
+// A warp takes STEP entries at a time, lanes the words of their rows (two for one
+// token, one for two: 45 and 47 us at 32000 x 4096, 54 with two and two); x
 // stays in shared memory.  Lane t keeps token t's running maximum and sum; the
 // warps of a block are joined in order and leave one pair stats[block][t], and
 // the last block to finish joins the blocks' pairs, in an order of its own
 // that does not depend on who is last.
-constexpr int kFewStep = 2;
 constexpr int kFewWarps = 16;
 
 __device__ __forceinline__ float2 ce_join(float2 a, float2 b) {
@@ -268,10 +268,10 @@ __device__ __forceinline__ void ce_row_out(float2 a, int row, const int32_t* __r
   const bool scored = label >= 0 && label < V;
   if (!scored && label != -1) set_status(status, kErrBadIndex);
   lse[row] = l;
-  loss[row] = scored ? l - label_logit[row] : 0.f;
+  loss[row] = scored ? l - __ldcg(label_logit + row) : 0.f;    // (another block may have written it)
 }
 
-template <int TT>
+template <int TT, int STEP>
 __global__ void __launch_bounds__(32 * kFewWarps) ce_few_kernel(const uint4* __restrict__ x,
                                                                 const uint4* __restrict__ w,
                                                                 const int32_t* __restrict__ labels, int T, int words,
@@ -287,30 +287,30 @@ __global__ void __launch_bounds__(32 * kFewWarps) ce_few_kernel(const uint4* __r
   __syncthreads();
   const int label = lane < T ? labels[lane] : -1;
   float2 run = make_float2(-INFINITY, 0.f);
-  const int stride = gridDim.x * kFewWarps * kFewStep;
-  for (int v0 = (blockIdx.x * kFewWarps + warp) * kFewStep; v0 < V; v0 += stride) {
-    F32x2 acc[kFewStep][TT];
+  const int stride = gridDim.x * kFewWarps * STEP;
+  for (int v0 = (blockIdx.x * kFewWarps + warp) * STEP; v0 < V; v0 += stride) {
+    F32x2 acc[STEP][TT];
     #pragma unroll
-    for (int r = 0; r < kFewStep; ++r)
+    for (int r = 0; r < STEP; ++r)
       #pragma unroll
       for (int t = 0; t < TT; ++t) acc[r][t] = make_f32x2(0.f, 0.f);
-    const uint4* rows[kFewStep];
+    const uint4* rows[STEP];
     #pragma unroll
-    for (int r = 0; r < kFewStep; ++r) rows[r] = w + static_cast<long long>(min(v0 + r, V - 1)) * words;
+    for (int r = 0; r < STEP; ++r) rows[r] = w + static_cast<long long>(min(v0 + r, V - 1)) * words;
     for (int c0 = lane; c0 < words; c0 += 4 * 32) {
-      uint4 u[4][kFewStep];
+      uint4 u[4][STEP];
       #pragma unroll
       for (int i = 0; i < 4; ++i)
         #pragma unroll
-        for (int r = 0; r < kFewStep; ++r)
+        for (int r = 0; r < STEP; ++r)
           u[i][r] = c0 + 32 * i < words ? rows[r][c0 + 32 * i] : make_uint4(0, 0, 0, 0);
       #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int c = c0 + 32 * i;
         if (c < words) {
-          F32x2 wv[kFewStep][4];
+          F32x2 wv[STEP][4];
           #pragma unroll
-          for (int r = 0; r < kFewStep; ++r) {
+          for (int r = 0; r < STEP; ++r) {
             wv[r][0] = bf16x2_f32x2(u[i][r].x);
             wv[r][1] = bf16x2_f32x2(u[i][r].y);
             wv[r][2] = bf16x2_f32x2(u[i][r].z);
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) ce_few_kernel(const uint4* __r
             const uint4 xu = s_x[t * words + c];
             const F32x2 xv[4] = {bf16x2_f32x2(xu.x), bf16x2_f32x2(xu.y), bf16x2_f32x2(xu.z), bf16x2_f32x2(xu.w)};
             #pragma unroll
-            for (int r = 0; r < kFewStep; ++r)
+            for (int r = 0; r < STEP; ++r)
               #pragma unroll
               for (int j = 0; j < 4; ++j) acc[r][t] = fma2(wv[r][j], xv[j], acc[r][t]);
           }
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) ce_few_kernel(const uint4* __r
       }
     }
     #pragma unroll
-    for (int r = 0; r < kFewStep; ++r) {
+    for (int r = 0; r < STEP; ++r) {
       float mine = 0.f;                     // lane t: token t's logit
       #pragma unroll
       for (int t = 0; t < TT; ++t) {
@@ -371,10 +371,10 @@ __global__ void __launch_bounds__(32 * kFewWarps) ce_few_kernel(const uint4* __r
   }
 }
 
-template <int TT>
+template <int TT, int STEP>
 cudaError_t loss_few(const void* x, const void* w, int T, int H, int V, const CeParams& ce, float* loss, float* lse,
                      int* status, cudaStream_t st) {
-  auto kern = ce_few_kernel<TT>;
+  auto kern = ce_few_kernel<TT, STEP>;
   static std::atomic<bool> attr_set[kMaxDevices];
   const int dev = current_device();
   if (dev < 0) return cudaErrorInvalidDevice;
@@ -384,13 +384,14 @@ cudaError_t loss_few(const void* x, const void* w, int T, int H, int V, const Ce
     if (e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
-  const int need = (V + kFewWarps * kFewStep - 1) / (kFewWarps * kFewStep);
+  const int need = (V + kFewWarps * STEP - 1) / (kFewWarps * STEP);
   const int blocks = need < kFewBlocks ? need : kFewBlocks;
   count_launches(1);
   return launch_k(kern, blocks, 32 * kFewWarps, static_cast<size_t>(TT) * H * 2, st, static_cast<const uint4*>(x),
                   static_cast<const uint4*>(w), ce.labels, T, H / 8, V, ce.stats, ce.label_logit, loss, lse,
                   status);
 }
+
 // ---------------------------------------------------------------- row kernels
 constexpr int kJoinRows = 32, kJoinStrands = 16;
 
@@ -472,8 +473,8 @@ moe_status moe_cross_entropy_forward(const void* x, const void* w, const int32_t
   ce.vocab = V;
   ce.stats = at<float2>(ws, l.stats);
   ce.label_logit = at<float>(ws, l.label_logit);
-  if (T == 1) return status_of(loss_few<1>(x, w, T, H, V, ce, loss, lse, status, st));
-  if (T <= kFewRows) return status_of(loss_few<kFewRows>(x, w, T, H, V, ce, loss, lse, status, st));
+  if (T == 1) return status_of(loss_few<1, 2>(x, w, T, H, V, ce, loss, lse, status, st));
+  if (T <= kFewRows) return status_of(loss_few<kFewRows, 1>(x, w, T, H, V, ce, loss, lse, status, st));
   const bool small = small_rows(T);
   if (H > kWhole)
     MOE_TRY(small ? (gemm_logits<Epi::kCeStatsSeg, false>(x, T, H, w, V, nullptr, 0, ce, SideJob{}, status, st))

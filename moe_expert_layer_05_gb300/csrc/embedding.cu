@@ -15,7 +15,7 @@
 // one GB300 (a plain copy reaches 6.68 TB/s): lookup of 16384 x 4096 31 us
 // (6.24 TB/s); gradient of 16384 rows into 32000 x 7168 195 us (5.91 TB/s: sort
 // 17, whole chunks 9, rows 165); 1003 rows into 50001 x 1024 on top of `base`
-// 60 us (5.17 TB/s: sort 7, rows 50).
+// 59 us (5.25 TB/s: sort 7, rows 49).
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -95,16 +95,129 @@ __device__ __forceinline__ void store8(float* p, const float (&a)[8]) {
   }
 }
 
-// A row of the gradient without a token: base, or zero.  One warp.
-__device__ __forceinline__ void fill_row(long long v, int words, const uint4* __restrict__ base,
-                                         float* __restrict__ dtable) {
-  const int lane = threadIdx.x & 31;
-  const long long row = v * words;
+// Words [begin, end) of two rows of the gradient without a token (those that
+// `fill` says): base, or zero.  One warp, eight loads on their way.
+__device__ __forceinline__ void fill_rows(const long long (&v)[2], const bool (&fill)[2], int words, int begin, int end,
+                                          const uint4* __restrict__ base, float* __restrict__ dtable) {
+  for (int c0 = begin + (threadIdx.x & 31); c0 < end; c0 += 128) {
+    uint4 b[2][4];
+    #pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      #pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        b[u][k] = make_uint4(0, 0, 0, 0);
+        if (base != nullptr && fill[u] && c0 + 32 * k < end) b[u][k] = base[v[u] * words + c0 + 32 * k];
+      }
+    }
+    #pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      #pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float a[8] = {};
+        add_row8(a, b[u][k]);
+        if (fill[u] && c0 + 32 * k < end) store8(dtable + (v[u] * words + c0 + 32 * k) * 8, a);
+      }
+    }
+  }
+}
+
+// Narrow rows (up to 16 words): `lanes`, a power of two, for a row.  Calls f(row,
+// word) for each of the block's rows [0, rows) and words, as many rows at a time
+// as the block's threads hold.
+template <class F>
+__device__ __forceinline__ void narrow_rows(int rows, int words, F&& f) {
+  int lanes = 16;
+  while (lanes / 2 >= words) lanes /= 2;
+  const int c = threadIdx.x % lanes;
   #pragma unroll 4
-  for (int c = lane; c < words; c += 32) {
-    float a[8] = {};
-    if (base != nullptr) add_row8(a, base[row + c]);
-    store8(dtable + (row + c) * 8, a);
+  for (int r = threadIdx.x / lanes; r < rows; r += 128 / lanes)
+    if (c < words) f(r, c);
+}
+constexpr int kNarrow = 16;
+
+// ---------------------------------------------------------------- few tokens
+// Up to kFewTokens positions there is nothing to sort: one launch, in which
+// block (b, j) writes words [128 j, 128 j + 128) of the table's rows b, b + grid,
+// ... (strided, because token ids are mostly ordered by frequency), a warp a
+// row.  The block looks through all tokens for the rows that have one; such a
+// row's warp finds its positions, in ascending order, and sums them.  64 tokens
+// into 11000 x 680 8.0 us (the sort's three launches: 12.3); at 256 both take 13.
+constexpr int kFewTokens = 128;
+__global__ void __launch_bounds__(128) embedding_few_kernel(const int32_t* __restrict__ tokens, int n, int V, int words,
+                                                            const uint4* __restrict__ dy,
+                                                            const uint4* __restrict__ base, float scale,
+                                                            float* __restrict__ dtable, int* status) {
+  pdl_entry();
+  extern __shared__ uint32_t s_has[];                  // a bit for each of the block's rows
+  __shared__ int s_tok[kFewTokens];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int first = blockIdx.x, step = gridDim.x, rows = (V - first + step - 1) / step;
+  const int c0 = blockIdx.y * 128 + lane;
+  for (int i = tid; i < (rows + 31) / 32; i += 128) s_has[i] = 0;
+  __syncthreads();
+  for (int i = tid; i < kFewTokens; i += 128) {
+    const int t = i < n ? tokens[i] : -1;
+    s_tok[i] = t;
+    if (first == 0 && blockIdx.y == 0 && (t < -1 || t >= V)) set_status(status, kErrBadIndex);
+    const int off = t - first;
+    if (t >= 0 && t < V && off >= 0 && off % step == 0) atomicOr(&s_has[off / step >> 5], 1u << (off / step & 31));
+  }
+  __syncthreads();
+  auto has = [&](int r) { return ((s_has[r >> 5] >> (r & 31)) & 1u) != 0; };
+  if (words <= kNarrow) {
+    narrow_rows(rows, words, [&](int r, int c) {
+      const long long at = (first + static_cast<long long>(r) * step) * words + c;
+      if (has(r)) return;
+      float a[8] = {};
+      if (base != nullptr) add_row8(a, base[at]);
+      store8(dtable + at * 8, a);
+    });
+  }
+  for (int r = words <= kNarrow ? rows : warp; r < rows; r += 8) {
+    const long long v[2] = {first + static_cast<long long>(r) * step, first + static_cast<long long>(r + 4) * step};
+    const bool fill[2] = {!has(r), r + 4 < rows && !has(r + 4)};
+    fill_rows(v, fill, words, blockIdx.y * 128, min(words, static_cast<int>(blockIdx.y) * 128 + 128), base, dtable);
+  }
+  for (int r = warp; r < rows; r += 4) {
+    if (!has(r)) continue;
+    const int v = first + r * step;
+    const long long row = static_cast<long long>(v) * words;
+    float a[4][8] = {};
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      unsigned match = __ballot_sync(kFull, s_tok[i0 + lane] == v);
+      while (match != 0) {                             // two positions at a time
+        const int p0 = i0 + __ffs(match) - 1;
+        match &= match - 1;
+        const bool two = match != 0;
+        const int p1 = two ? i0 + __ffs(match) - 1 : p0;
+        match &= match - 1;
+        uint4 e[2][4];
+        #pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (c0 + 32 * k < words) {
+            e[0][k] = dy[static_cast<long long>(p0) * words + c0 + 32 * k];
+            if (two) e[1][k] = dy[static_cast<long long>(p1) * words + c0 + 32 * k];
+          }
+        }
+        #pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (c0 + 32 * k < words) {
+            add_row8(a[k], e[0][k]);
+            if (two) add_row8(a[k], e[1][k]);
+          }
+        }
+      }
+    }
+    #pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = c0 + 32 * k;
+      if (c < words) {
+        #pragma unroll
+        for (int j = 0; j < 8; ++j) a[k][j] *= scale;
+        if (base != nullptr) add_row8(a[k], base[row + c]);
+        store8(dtable + (row + c) * 8, a[k]);
+      }
+    }
   }
 }
 
@@ -117,17 +230,17 @@ __device__ __forceinline__ uint32_t key_of(const int32_t* __restrict__ tokens, i
   return static_cast<uint32_t>(V);
 }
 
-// Up to kClusterSort positions: the whole sort in one launch, by one block (up
-// to kBlockSort positions) or a cluster of eight (16384 positions in 17 us;
-// BLOCKS).  Each block holds its share of the pairs, in registers while it ranks them and
-// in shared memory between the passes.  A pass ranks the pairs as
-// sort_scatter_kernel does, with the digit counts of every warp in shared
-// memory; the blocks read each other's counts and write the pairs to their
-// places in each other's shared memory, and the sorted pairs are copied out
-// in one piece.  (Written to their places in global memory they cost a sector
-// each.)
+// Up to kClusterSort positions: the whole sort in one launch, by BLOCKS blocks:
+// one up to kBlockSort positions (1003 in 7 us), a cluster of eight beyond
+// (16384 in 17 us).  Each block holds its share of the pairs, in registers
+// while it ranks them and in shared memory between the passes.  A pass ranks
+// the pairs as sort_scatter_kernel does, with the digit counts of every warp in
+// shared memory; the blocks read each other's counts and write the pairs to
+// their places in each other's shared memory, and the sorted pairs are copied
+// out in one piece.  (Written to their places in global memory they cost a
+// sector each.)
 constexpr int kCluster = 8;
-constexpr int kClusterThreads = 512;                  // (half an SM's registers: the fill runs beside it)
+constexpr int kClusterThreads = 512;                  // (one for each bin)
 constexpr int kClusterWarps = kClusterThreads / 32;
 constexpr int kClusterItems = 16;                     // pairs per thread at most
 constexpr int kClusterSort = kCluster * kClusterThreads * kClusterItems;
@@ -455,17 +568,20 @@ __global__ void __launch_bounds__(128) embedding_chunks_kernel(const uint32_t* _
 // 128 j + 128).  The batch's rows of dy (and of base) are loaded together; a run
 // that goes on past it is followed through the positions up to the next chunk,
 // the sums of the whole chunks, and the positions in the chunk where it ends --
-// so a block reads at most 62 rows of dy, however often a token occurs.  The
-// other fills those of fill_rows rows that have no token.
+// so a block reads at most 63 rows of dy, however often a token occurs.  The
+// other fills those of rows_each rows that have no token.  64 registers and so
+// 32 warps on an SM: with batches of 8 and 114 registers the filling blocks
+// were too few (1003 tokens, 50001 x 1024: 70 us, against 61).
 constexpr int kBatch = 4;
-constexpr int kFollow = 6;
+constexpr int kFollow = 6;              // a followed run's rows of dy on their way at a time
 __global__ void __launch_bounds__(128, 8) embedding_rows_kernel(const uint32_t* __restrict__ keys,
-                                                             const int32_t* __restrict__ pos, int n, int V, int words,
-                                                             int cols, int run_blocks, const uint4* __restrict__ dy,
-                                                             const uint8_t* __restrict__ has,
-                                                             const float4* __restrict__ part, int fill_rows,
-                                                             const uint4* __restrict__ base, float scale,
-                                                             float* __restrict__ dtable) {
+                                                                const int32_t* __restrict__ pos, int n, int V,
+                                                                int words, int cols, int run_blocks,
+                                                                const uint4* __restrict__ dy,
+                                                                const uint8_t* __restrict__ has,
+                                                                const float4* __restrict__ part, int rows_each,
+                                                                const uint4* __restrict__ base, float scale,
+                                                                float* __restrict__ dtable) {
   pdl_entry();
   const int tid = threadIdx.x;
   int block = blockIdx.x;
@@ -479,9 +595,24 @@ __global__ void __launch_bounds__(128, 8) embedding_rows_kernel(const uint32_t* 
       block -= turns;
     }
     if (fills) {
-      const long long v0 = static_cast<long long>(block) * fill_rows;
-      for (int r = tid >> 5; r < fill_rows; r += 4)
-        if (v0 + r < V && has[v0 + r] == 0) fill_row(v0 + r, words, base, dtable);
+      const long long v0 = static_cast<long long>(block) * rows_each;
+      if (words <= kNarrow) {
+        narrow_rows(static_cast<int>(min(static_cast<long long>(rows_each), V - v0)), words, [&](int r, int c) {
+          if (has[v0 + r] != 0) return;
+          float a[8] = {};
+          if (base != nullptr) add_row8(a, base[(v0 + r) * words + c]);
+          store8(dtable + ((v0 + r) * words + c) * 8, a);
+        });
+        return;
+      }
+      // two rows a warp, or (wide rows) a quarter of two rows
+      const int warp = tid >> 5, apart = words < 512 ? 4 : 1;
+      const int quarter = (words + 3) / 4, begin = apart == 4 ? 0 : warp * quarter;
+      for (int r = apart == 4 ? warp : 0; r < rows_each; r += 2 * apart) {
+        const long long v[2] = {v0 + r, v0 + r + apart};
+        const bool fill[2] = {v[0] < V && has[v[0]] == 0, r + apart < rows_each && v[1] < V && has[v[1]] == 0};
+        fill_rows(v, fill, words, begin, apart == 4 ? words : min(words, begin + quarter), base, dtable);
+      }
       return;
     }
   }
@@ -679,6 +810,16 @@ moe_status moe_embedding_backward(const int32_t* tokens, int32_t n, const void* 
   const int words = H / 8;
   const uint4* b16 = static_cast<const uint4*>(base);
   const int cols = (words + 127) / 128;
+  if (n <= kFewTokens) {
+    // 64 KB a block, less where that would leave SMs without a block
+    const int wide = words < 128 ? words : 128;
+    const int even = static_cast<int>((static_cast<long long>(V) * cols + 1215) / 1216);
+    const int rows = even < 4 ? 4 : even < 65536 / (wide * 32) ? even : 65536 / (wide * 32);
+    const int blocks = (V + rows - 1) / rows;
+    count_launches(1);
+    return status_of(launch_k(embedding_few_kernel, dim3(blocks, cols), 128, (V / blocks + 32) / 32 * 4 + 4, st, tokens, n,
+                              V, words, static_cast<const uint4*>(dy), b16, scale, dtable, status));
+  }
   uint8_t* has = at<uint8_t>(ws, w.has);
   int passes = 1;                                    // digits of the keys 0 .. V
   while (passes * kDigitBits < 32 && (V >> (passes * kDigitBits)) != 0) ++passes;
