@@ -296,21 +296,17 @@ def moe_layer_backward_wgrad(cfg, weights: MoeWeights, x, dy, grads: MoeGrads, a
 # ---------------------------------------------------------------- around the layer
 def _tensor(t, name: str, dtype, shape) -> int:
     """Device address of a contiguous CUDA tensor of this type and shape; raises ValueError otherwise."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name}: expected a contiguous CUDA tensor {tuple(shape)} of {dtype}, got "
-                         f"{tuple(t.shape)} of {t.dtype} on {t.device}"
-                         + ("" if t.is_contiguous() else ", not contiguous"))
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name}: expected a contiguous CUDA tensor {tuple(shape)} of {dtype}, got {tuple(t.shape)} of "
+                     f"{t.dtype} on {t.device}" + ("" if t.is_contiguous() else ", not contiguous"))
 
 
-def _opt_tensor(t, name: str, dtype, shape) -> int | None:
-    return None if t is None else _tensor(t, name, dtype, shape)
-
-
-def _matrix(t, name: str) -> tuple[int, int]:
-    if t.dim() != 2:
-        raise ValueError(f"{name}: expected two dimensions, got {tuple(t.shape)}")
-    return tuple(t.shape)
+def _matrix(t, name: str) -> torch.Size:
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: expected two dimensions, got {tuple(shape)}")
+    return shape
 
 
 def _scratch(ws) -> tuple[int, int]:
@@ -331,9 +327,9 @@ def moe_embedding_workspace_bytes(n: int, V: int, H: int) -> int:
 
 def moe_embedding_forward(tokens, table, out, ws, scale: float = 1.0, stream=None) -> None:
     """out[i] = scale * table[tokens[i]] (bf16); a zero row where tokens[i] is -1."""
-    V, H = _matrix(table, "table")
+    V, H = rows = _matrix(table, "table")
     n = tokens.numel()
-    check(load().moe_embedding_forward(_tensor(tokens, "tokens", _I32, (n,)), n, _tensor(table, "table", _BF16, (V, H)),
+    check(load().moe_embedding_forward(_tensor(tokens, "tokens", _I32, (n,)), n, _tensor(table, "table", _BF16, rows),
                                        V, H, scale, _tensor(out, "out", _BF16, (n, H)), _scratch(ws)[0],
                                        stream_ptr(stream)), "moe_embedding_forward")
 
@@ -344,7 +340,7 @@ def moe_embedding_backward(tokens, dy, dtable, ws, scale: float = 1.0, base=None
     n = tokens.numel()
     wp, wn = _scratch(ws)
     check(load().moe_embedding_backward(_tensor(tokens, "tokens", _I32, (n,)), n, _tensor(dy, "dy", _BF16, (n, H)), V,
-                                        H, scale, _opt_tensor(base, "base", _BF16, (V, H)),
+                                        H, scale, None if base is None else _tensor(base, "base", _BF16, (V, H)),
                                         _tensor(dtable, "dtable", _F32, (V, H)), wp, wn, stream_ptr(stream)),
           "moe_embedding_backward")
 
@@ -352,11 +348,13 @@ def moe_embedding_backward(tokens, dy, dtable, ws, scale: float = 1.0, base=None
 def moe_layer_norm_forward(x, weight, bias, y, mean, rstd, residual=None, sum_out=None, eps: float = 1e-5,
                            stream=None) -> None:
     """y = norm(s) * weight + bias with s = x + residual (written to sum_out); mean and rstd for the backward."""
-    T, H = _matrix(x, "x")
-    check(load().moe_layer_norm_forward(_tensor(x, "x", _BF16, (T, H)), _opt_tensor(residual, "residual", _BF16, (T, H)),
-                                        _tensor(weight, "weight", _BF16, (H,)), _opt_tensor(bias, "bias", _BF16, (H,)),
-                                        T, H, eps, _tensor(y, "y", _BF16, (T, H)),
-                                        _opt_tensor(sum_out, "sum_out", _BF16, (T, H)),
+    T, H = rows = _matrix(x, "x")
+    check(load().moe_layer_norm_forward(_tensor(x, "x", _BF16, rows),
+                                        None if residual is None else _tensor(residual, "residual", _BF16, rows),
+                                        _tensor(weight, "weight", _BF16, (H,)),
+                                        None if bias is None else _tensor(bias, "bias", _BF16, (H,)),
+                                        T, H, eps, _tensor(y, "y", _BF16, rows),
+                                        None if sum_out is None else _tensor(sum_out, "sum_out", _BF16, rows),
                                         _tensor(mean, "mean", _F32, (T,)), _tensor(rstd, "rstd", _F32, (T,)),
                                         stream_ptr(stream)), "moe_layer_norm_forward")
 
@@ -367,14 +365,16 @@ def moe_layer_norm_workspace_bytes(T: int, H: int) -> int:
 
 def moe_layer_norm_backward(dy, s, weight, mean, rstd, dx, dweight, dbias, ws, dsum=None, stream=None) -> None:
     """dx = the gradient of s (plus dsum, the stream's own); dweight and dbias (or None), fp32."""
-    T, H = _matrix(s, "s")
+    T, H = rows = _matrix(s, "s")
     wp, wn = _scratch(ws)
-    check(load().moe_layer_norm_backward(_tensor(dy, "dy", _BF16, (T, H)), _tensor(s, "s", _BF16, (T, H)),
+    check(load().moe_layer_norm_backward(_tensor(dy, "dy", _BF16, rows), _tensor(s, "s", _BF16, rows),
                                          _tensor(weight, "weight", _BF16, (H,)), _tensor(mean, "mean", _F32, (T,)),
-                                         _tensor(rstd, "rstd", _F32, (T,)), _opt_tensor(dsum, "dsum", _BF16, (T, H)),
-                                         T, H, _tensor(dx, "dx", _BF16, (T, H)),
+                                         _tensor(rstd, "rstd", _F32, (T,)),
+                                         None if dsum is None else _tensor(dsum, "dsum", _BF16, rows),
+                                         T, H, _tensor(dx, "dx", _BF16, rows),
                                          _tensor(dweight, "dweight", _F32, (H,)),
-                                         _opt_tensor(dbias, "dbias", _F32, (H,)), wp, wn, stream_ptr(stream)),
+                                         None if dbias is None else _tensor(dbias, "dbias", _F32, (H,)), wp, wn,
+                                         stream_ptr(stream)),
           "moe_layer_norm_backward")
 
 

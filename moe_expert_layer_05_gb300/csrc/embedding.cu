@@ -4,9 +4,9 @@
 //   dtable[v] = base[v] + scale * sum over the i with tok[i] = v of dy[i].
 //
 // The gradient never adds through atomics: the token positions are sorted by
-// token (a stable radix sort), a run of equal tokens is summed in ascending
-// position, and every row of dtable is written once, so the result does not
-// depend on timing.  A frequent token's run is cut at multiples of kChunk
+// token (a stable radix sort; up to kFewTokens are searched instead), a run of
+// equal tokens is summed in ascending position, and every row of dtable is
+// written once, so the result does not depend on timing.  A frequent token's run is cut at multiples of kChunk
 // sorted positions: whole chunks of one token are summed by blocks of their
 // own, and the row adds their sums in order.  The sums are fp32.
 //
