@@ -15,7 +15,13 @@
 // d in the GEMM's epilogue (ce_grad_tile) and kept for this piece only, in
 // bf16 -- the operand type of the tensor cores' next two products: a rounding
 // of 2^-9 per element, of the size of the gradients' own rounding to bf16 at
-// the end -- then dx += d w_piece into fp32 slabs and dw_piece = d^T x.  dx's
+// the end -- then dx += d w_piece into fp32 slabs and dw_piece = d^T x.  That
+// holds where the roundings of many rows average out (the gradients' rel-L2 error
+// is 2.2e-3, their own rounding 1.7e-3), and was up to 4e-3 elsewhere.  So what
+// the rows' weights have in common stays out of d and multiplies the gradients in
+// fp32 (ce_unit), and up to kTwoParts tokens d is kept in two bf16 parts, as
+// twice the rows: 1.7e-3 with equal weights or few tokens, at 0.3 % and (64
+// tokens, H = 4096, 32000 entries) 5 % of the time.  dx's
 // contraction runs over the vocabulary and has few tiles, so it is cut into
 // parts with a slab each, which are added in order and rounded once.  Pieces
 // follow one another on the stream, so the fp32 additions into a slab have one
@@ -25,11 +31,11 @@
 // there by the power limit over many passes.  Measured on one GB300 (cuBLAS
 // bf16: 1914 TFLOP/s in a burst, 1721 sustained): forward of 8192 tokens, H =
 // 4096, 32000 entries 1.26 ms (1.70 PFLOP/s); a training step of 4096 tokens, H
-// = 4096, 131072 entries 10.6 ms (1.66 PFLOP/s: 4.4 TFLOP forward, 13.2
+// = 4096, 131072 entries 10.4 to 10.9 ms (1.61 to 1.69 PFLOP/s: 4.4 TFLOP forward, 13.2
 // backward).  With few tokens bound by reading the weight: one token, H = 4096,
 // 32000 entries 45 us (5.8 TB/s), 131072 entries 154 us (7.0 TB/s).  Between
 // them by the launches and the rounds of tiles: 1003 tokens, H = 1000, 5003
-// entries 69 us, five launches, 80 tiles on 76 CTA pairs.
+// entries 70 us, five launches, 80 tiles on 76 CTA pairs.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -67,6 +73,12 @@ int piece_of(int T, int V, int piece) {
   const int pieces = static_cast<int>((tiles + per - 1) / per);
   return (tiles + pieces - 1) / pieces * kTile;
 }
+
+// Tokens up to which d has two parts: their rows fit in one 128-row tile that has
+// to be read and multiplied whole anyway.
+constexpr int kTwoParts = 64;
+int low_row(int T) { return T <= kTwoParts ? round_up(T, 32) : 0; }     // first row of the lower parts; 0: none
+int d_rows(int T) { return T <= kTwoParts ? 2 * low_row(T) : T; }       // rows of d, of x in dw, of dx's slabs
 
 // Up to 128 tokens the logits and dx run on 128-row tiles of one CTA,
 // otherwise on 256-row tiles of CTA pairs.
@@ -132,15 +144,16 @@ Ws layout(int T, int H, int V, int piece) {
   w.label_logit = take(rows * 4);
   end = off;
   off = entry::kStatusBytes;
-  w.piece = piece_of(T, V, piece);
-  const int kb = w.piece / 64, per = dx_per_split(T, H, kb);
+  const size_t dr = d_rows(T);
+  w.piece = piece_of(d_rows(T), V, piece);
+  const int kb = w.piece / 64, per = dx_per_split(d_rows(T), H, kb);
   w.slab_count = (kb + per - 1) / per;
-  w.d = take(rows * w.piece * 2);
-  w.xz = take(rows * H * 2);
-  w.slabs = take(static_cast<size_t>(w.slab_count) * rows * H * 4);
+  w.d = take(dr * w.piece * 2);
+  w.xz = take(dr * H * 2);
+  w.slabs = take(static_cast<size_t>(w.slab_count) * dr * H * 4);
   // (the last piece may be smaller, and its contraction cut into more parts)
   const int first = V < w.piece ? V : w.piece, last = V - (V - 1) / w.piece * w.piece;
-  const size_t sf = dw_slab_bytes(T, H, first), sl = dw_slab_bytes(T, H, last);
+  const size_t sf = dw_slab_bytes(d_rows(T), H, first), sl = dw_slab_bytes(d_rows(T), H, last);
   w.dw_slabs = take(sf > sl ? sf : sl);
   w.total = end > off ? end : off;
   return w;
@@ -160,7 +173,7 @@ cudaError_t gemm_logits(const void* x, int T, int H, const void* w_rows, int row
   if (!make_tmap_bf16(&ta, x, H, T, 64, 128) || !make_tmap_bf16(&tb, w_rows, H, rows, 64, C::B_BOX_ROWS))
     return cudaErrorInvalidValue;
   tc = ta;
-  if (d != nullptr && !make_tmap_out_bf16(&tc, d, ld, T)) return cudaErrorInvalidValue;
+  if (d != nullptr && !make_tmap_out_bf16(&tc, d, ld, d_rows(T))) return cudaErrorInvalidValue;
   GemmParams p = gemm_params_zero();
   p.E = 1;
   p.m_rows = T;
@@ -182,7 +195,7 @@ cudaError_t gemm_logits(const void* x, int T, int H, const void* w_rows, int row
     return launch_gemm<C>(ta, tb, tc, tc, p, tiles < num_sms() ? tiles : num_sms(), st);
 }
 
-// dx slabs (+)= d[T, cols] w_rows[cols, H]
+// dx slabs (+)= d[T, cols] w_rows[cols, H] (T: rows of d)
 template <bool PAIR>
 cudaError_t gemm_dx(const void* d, int ld, int T, const void* w_rows, int rows, int H, int per, float* slabs,
                     int slab_count, bool add, int* status, cudaStream_t st) {
@@ -210,9 +223,9 @@ cudaError_t gemm_dx(const void* d, int ld, int T, const void* w_rows, int rows, 
 }
 
 // dw_rows[rows, H] = d[T, rows]^T x[T, H]: in bf16, or (parts > 1) as fp32 slabs
-// [parts][rows rounded up to 256][H] of parts of the contraction.
+// [parts][rows rounded up to 256][H] of parts of the contraction (T: rows of d).
 cudaError_t gemm_dw(const void* d, int ld, int T, const void* x, int H, void* dw_rows, int rows, int per, float* slabs,
-                    const SideJob& side, int* status, cudaStream_t st) {
+                    const CeParams& ce, const SideJob& side, int* status, cudaStream_t st) {
   using C = GemmCfg<256, true, true, Sched::kRoutedK, Epi::kStoreBf16, 0, false, true, false, true>;
   using CS = GemmCfg<256, true, true, Sched::kRoutedK, Epi::kStoreF32, 0, false, true, false, true>;
   static_assert(C::BK == kDwBlock && CS::BK == kDwBlock, "k-blocks of the weight gradient");
@@ -226,6 +239,7 @@ cudaError_t gemm_dw(const void* d, int ld, int T, const void* x, int H, void* dw
   p.m_tiles_w = (rows + 255) / 256;
   p.n_tiles = (H + kTile - 1) / kTile;
   p.valid_cols = H;
+  p.ce = ce;
   p.side = side;
   p.status = status;
   if (!make_tmap_bf16(&ta, d, ld, T, 64, kDwBlock) || !make_tmap_bf16(&tb, x, H, T, 64, kDwBlock))
@@ -509,11 +523,14 @@ moe_status moe_cross_entropy_backward(const void* x, const void* w, const int32_
   ce.vocab = V;
   ce.lse = lse;
   ce.dloss = dloss;
-  const int per = dx_per_split(T, H, l.piece / 64);
+  ce.rows = T;
+  ce.low = low_row(T);
+  const int D = d_rows(T);
+  const int per = dx_per_split(D, H, l.piece / 64);
   SideJob copy{};                            // beside the first piece's logits: x without its unscored rows
   copy.src = static_cast<const uint4*>(x);
   copy.dst = xz;
-  copy.n = T;
+  copy.n = D;
   copy.words = H / 8;
   for (int v0 = 0; v0 < V; v0 += l.piece) {
     const int rows = V - v0 < l.piece ? V - v0 : l.piece;
@@ -523,10 +540,10 @@ moe_status moe_cross_entropy_backward(const void* x, const void* w, const int32_
     ce.v0 = v0;
     if (small) {
       MOE_TRY((gemm_logits<Epi::kCeGrad, false>(x, T, H, w_rows, rows, d, l.piece, ce, copy, status, st)));
-      MOE_TRY(gemm_dx<false>(d, l.piece, T, w_rows, rows, H, per, slabs, l.slab_count, v0 > 0, status, st));
+      MOE_TRY(gemm_dx<false>(d, l.piece, D, w_rows, rows, H, per, slabs, l.slab_count, v0 > 0, status, st));
     } else {
       MOE_TRY((gemm_logits<Epi::kCeGrad, true>(x, T, H, w_rows, rows, d, l.piece, ce, copy, status, st)));
-      MOE_TRY(gemm_dx<true>(d, l.piece, T, w_rows, rows, H, per, slabs, l.slab_count, v0 > 0, status, st));
+      MOE_TRY(gemm_dx<true>(d, l.piece, D, w_rows, rows, H, per, slabs, l.slab_count, v0 > 0, status, st));
     }
     copy.n = 0;
     SideJob join{};                          // beside the last piece's weight gradient: dx from its slabs
@@ -534,11 +551,12 @@ moe_status moe_cross_entropy_backward(const void* x, const void* w, const int32_
       join.src = reinterpret_cast<const uint4*>(slabs);
       join.dst = dx;
       join.n = static_cast<long long>(T) * H / 4;
-      join.words = l.slab_count;
+      join.stride = static_cast<long long>(ce.low > 0 ? ce.low : T) * H / 4;
+      join.words = ce.low > 0 ? 2 * l.slab_count : l.slab_count;   // (the lower part of each after its upper one)
     }
-    const int dw_per = dw_per_split(T, H, rows), dw_kb = (T + kDwBlock - 1) / kDwBlock;
+    const int dw_per = dw_per_split(D, H, rows), dw_kb = (D + kDwBlock - 1) / kDwBlock;
     float* dw_slabs = at<float>(ws, l.dw_slabs);
-    MOE_TRY(gemm_dw(d, l.piece, T, xz, H, dw_rows, rows, dw_per, dw_slabs, join, status, st));
+    MOE_TRY(gemm_dw(d, l.piece, D, xz, H, dw_rows, rows, dw_per, dw_slabs, ce, join, status, st));
     if (dw_per < dw_kb) {
       const long long n4 = static_cast<long long>(rows) * H / 4;
       count_launches(1);

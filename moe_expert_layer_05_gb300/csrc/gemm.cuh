@@ -56,7 +56,9 @@ struct CeParams {
   float2* stats;           // kCeStats: [2 n_tiles][rows] (maximum, sum of exp(z - maximum)) of each half tile
   float* label_logit;      // kCeStats: [rows], written where the label is in the vocabulary
   const float* lse;        // kCeGrad: [rows]
-  const float* dloss;      // kCeGrad: [rows]
+  const float* dloss;      // kCeGrad, weight gradient: [rows]
+  int rows;                // kCeGrad, weight gradient: tokens
+  int low;                 // kCeGrad: d in two parts, the lower one `low` rows further on; 0: one part
 };
 
 // Work that the epilogue warps of the head's backward GEMMs do before their
@@ -65,7 +67,8 @@ struct CeParams {
 struct SideJob {
   const uint4* src;        // kCeGrad: x; weight gradient: the slabs of dx (fp32)
   void* dst;               // kCeGrad: x with the rows that are not scored zero; weight gradient: dx (bf16)
-  long long n;             // kCeGrad: rows; weight gradient: groups of four values
+  long long n;             // kCeGrad: rows of dst; weight gradient: groups of four values of dx
+  long long stride;        // weight gradient: groups from slab to slab
   int words;               // kCeGrad: 16-byte words of a row; weight gradient: slabs
 };
 
@@ -772,16 +775,45 @@ struct CeRow {
   float lse, dloss;
 };
 template <class C>
-__device__ __forceinline__ CeRow ce_row(const GemmParams& p, int row) {
+__device__ __forceinline__ CeRow ce_row(const GemmParams& p, int row, float unit) {
   CeRow r{-1, 0.f, 0.f};
   if (row < p.m_rows) {
     r.label = p.ce.labels[row];
     if constexpr (C::EP == Epi::kCeGrad) {
       r.lse = p.ce.lse[row];
-      r.dloss = p.ce.dloss[row];
+      r.dloss = p.ce.dloss[row] / unit;
     }
   }
   return r;
+}
+
+// A factor that d leaves out and the gradients get back in fp32: the mantissa, in
+// [1, 2), of the largest weight among the first 256 rows that have a scored one
+// (sought in kUnitRows rows).  A mean over N rows weights all of them by 1 / N,
+// and as the label's entry is about -1 / N in each, its rounding to bf16 would be
+// the same in every row and not average out (gradients up to 4e-3 off); without
+// its mantissa the weight is a power of two.  Unequal weights lie below a power of
+// two then, where the places of a bf16 are closer.  Any factor would be right.
+constexpr int kUnitRows = 4096;
+template <class C>
+__device__ __forceinline__ float ce_unit(const CeParams& ce, int lane) {
+  if constexpr (C::EP == Epi::kCeGrad || (C::HEAD && C::S == Sched::kRoutedK)) {
+    const int rows = min(ce.rows, kUnitRows);
+    for (int base = 0; base < rows; base += 256) {
+      unsigned most = 0;
+      #pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = base + 32 * i + lane;
+        const int label = r < rows ? ce.labels[r] : -1;
+        const unsigned w = r < rows ? __float_as_uint(ce.dloss[r]) & 0x7fffffffu : 0u;
+        if (label >= 0 && label < ce.vocab && w >= 0x00800000u && w < 0x7f800000u)   // (normal numbers)
+          most = max(most, w);
+      }
+      most = __reduce_max_sync(0xffffffffu, most);
+      if (most != 0) return __uint_as_float((most & 0x7fffffu) | 0x3f800000u);
+    }
+  }
+  return 1.0f;
 }
 
 // The label's logit of each lane that has its label's column `rel` in [c0, c0 +
@@ -802,19 +834,22 @@ __device__ __forceinline__ float ce_label_logit(uint32_t t0, int rel, int c0, in
 // The side job of this kernel (see SideJob), by the nth of `threads` threads of
 // block `block` of `blocks`.
 template <class C>
-__device__ __forceinline__ void side_job(const GemmParams& p, int thread, int threads, int block, int blocks) {
+__device__ __forceinline__ void side_job(const GemmParams& p, int thread, int threads, int block, int blocks,
+                                         float unit) {
   if constexpr (C::EP == Epi::kCeGrad) {
     // x with the rows that are not scored set to zero: d is zero there, but the
     // product d^T x would still turn an infinity or NaN of such a row into NaN
+    // (twice, where d has two parts)
     uint4* dst = static_cast<uint4*>(p.side.dst);
     for (long long r = block; r < p.side.n; r += blocks) {
-      const int label = p.ce.labels[r];
+      const long long t = p.ce.low > 0 && r >= p.ce.low ? r - p.ce.low : r;
+      const int label = t < p.ce.rows ? p.ce.labels[t] : -1;
       const bool scored = label >= 0 && label < p.ce.vocab;
       for (int c = thread; c < p.side.words; c += threads)
-        dst[r * p.side.words + c] = scored ? p.side.src[r * p.side.words + c] : make_uint4(0, 0, 0, 0);
+        dst[r * p.side.words + c] = scored ? p.side.src[t * p.side.words + c] : make_uint4(0, 0, 0, 0);
     }
   } else if constexpr (C::HEAD && C::S == Sched::kRoutedK) {
-    // dx = its slabs added in order, rounded once
+    // dx = its slabs added in order, times the unit, rounded once
     const float4* slabs = reinterpret_cast<const float4*>(p.side.src);
     uint2* dx = static_cast<uint2*>(p.side.dst);
     for (long long i = static_cast<long long>(block) * threads + thread; i < p.side.n;
@@ -822,10 +857,10 @@ __device__ __forceinline__ void side_job(const GemmParams& p, int thread, int th
       float4 a = slabs[i];
       #pragma unroll 4
       for (int k = 1; k < p.side.words; ++k) {
-        const float4 b = slabs[k * p.side.n + i];
+        const float4 b = slabs[k * p.side.stride + i];
         a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
       }
-      dx[i] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+      dx[i] = make_uint2(pack_bf16x2(a.x * unit, a.y * unit), pack_bf16x2(a.z * unit, a.w * unit));
     }
   }
 }
@@ -915,7 +950,9 @@ __device__ __forceinline__ void ce_stats_tile(const GemmParams& p, const TileInf
 
 // Gradient of one half of a tile of logits: d = dloss (exp(z - lse) - [column == label])
 // in bf16, the operand type of the two products that follow; zero in rows
-// without a label and in columns past the vocabulary, whatever the logits.
+// without a label and in columns past the vocabulary, whatever the logits.  With
+// p.ce.low a second pass over the tile writes what the rounding left, to the
+// rows `low` further on.
 template <class C, class St, class Release>
 __device__ __forceinline__ void ce_grad_tile(const GemmParams& p, const TileInfo& ti, uint32_t tmem_acc, int quarter,
                                              int lane, St& st, const CUtensorMap* tmC, int part,
@@ -933,35 +970,44 @@ __device__ __forceinline__ void ce_grad_tile(const GemmParams& p, const TileInfo
   const float off = scored ? cr.lse * kLog2e : 0.f;
   const float dl = scored ? cr.dloss : 0.f;
   #pragma unroll 1
-  for (int c0 = part * (C::BN / 2); c0 < (part + 1) * (C::BN / 2); c0 += 64) {
-    const bool edge = c0 + 64 > nv;
-    uint32_t w[2][2][16];
-    load32(t0 + c0, w[0][0], w[0][1]);
-    load32(t0 + c0 + 32, w[1][0], w[1][1]);
-    const float zl = ce_label_logit(t0, rel, c0, 64, lane, 0.f);
-    if (c0 + 64 == (part + 1) * (C::BN / 2)) release();
-    st.begin();
-    #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t (&u)[2][16] = w[h];
-      float d[32];
+  for (int low = 0, lows = p.ce.low > 0 ? 1 : 0; low <= lows; ++low) {
+    #pragma unroll 1
+    for (int c0 = part * (C::BN / 2); c0 < (part + 1) * (C::BN / 2); c0 += 64) {
+      const bool edge = c0 + 64 > nv;
+      uint32_t w[2][2][16];
+      load32(t0 + c0, w[0][0], w[0][1]);
+      load32(t0 + c0 + 32, w[1][0], w[1][1]);
+      const float zl = ce_label_logit(t0, rel, c0, 64, lane, 0.f);
+      if (low == lows && c0 + 64 == (part + 1) * (C::BN / 2)) release();
+      st.begin();
       #pragma unroll
-      for (int j = 0; j < 32; ++j) d[j] = ex2(fmaf(__uint_as_float(u[j >> 4][j & 15]), kLog2e, -off));
-      #pragma unroll
-      for (int j = 0; j < 32; ++j) d[j] = scored ? d[j] * dl : 0.f;
-      if (edge) {
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t (&u)[2][16] = w[h];
+        float d[32];
         #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (c0 + 32 * h + j >= nv) d[j] = 0.f;
+        for (int j = 0; j < 32; ++j) d[j] = ex2(fmaf(__uint_as_float(u[j >> 4][j & 15]), kLog2e, -off));
+        #pragma unroll
+        for (int j = 0; j < 32; ++j) d[j] = scored ? d[j] * dl : 0.f;
+        if (edge) {
+          #pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (c0 + 32 * h + j >= nv) d[j] = 0.f;
+        }
+        if (low != 0) {
+          #pragma unroll
+          for (int j = 0; j < 32; ++j) d[j] -= bf16_lo(pack_bf16x2(d[j], 0.f));
+        }
+        #pragma unroll
+        for (int q = 0; q < 4; ++q)
+          st.put(4 * h + q, pack_bf16x2(d[8 * q], d[8 * q + 1]), pack_bf16x2(d[8 * q + 2], d[8 * q + 3]),
+                 pack_bf16x2(d[8 * q + 4], d[8 * q + 5]), pack_bf16x2(d[8 * q + 6], d[8 * q + 7]));
       }
-      #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        st.put(4 * h + q, pack_bf16x2(d[8 * q], d[8 * q + 1]), pack_bf16x2(d[8 * q + 2], d[8 * q + 3]),
-               pack_bf16x2(d[8 * q + 4], d[8 * q + 5]), pack_bf16x2(d[8 * q + 6], d[8 * q + 7]));
+      if (scored && rel >= c0 && rel < c0 + 64) {    // the label's own column
+        const float d = (ex2(fmaf(zl, kLog2e, -off)) - 1.f) * dl;
+        st.put_bf16(rel - c0, low != 0 ? d - bf16_lo(pack_bf16x2(d, 0.f)) : d);
+      }
+      st.flush(tmC, ti.n * C::BN + c0, low != 0 ? y + p.ce.low : y);
     }
-    if (scored && rel >= c0 && rel < c0 + 64)      // the label's own column
-      st.put_bf16(rel - c0, (ex2(fmaf(zl, kLog2e, -off)) - 1.f) * dl);
-    st.flush(tmC, ti.n * C::BN + c0, y);
   }
 }
 
@@ -1077,6 +1123,13 @@ __device__ __forceinline__ void epilogue_tile_tma(const GemmParams& p, const Til
       }
       uint32_t a[16], b[16];
       load32(t0 + c0, a, b);
+      if constexpr (C::HEAD) {
+        #pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          a[j] = __float_as_uint(__uint_as_float(a[j]) * al);
+          b[j] = __float_as_uint(__uint_as_float(b[j]) * al);
+        }
+      }
       st.begin();
       #pragma unroll
       for (int j = 0; j < 4; ++j) st.put(j, no_mma ? 0u : a[4 * j], no_mma ? 0u : a[4 * j + 1],
@@ -1960,7 +2013,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     uint32_t acc_phase = 0;
     Stager<C::STAGING_BUFS, C::STAGING_BUF> st{stage_smem + ew * (C::STAGING_BUFS * C::STAGING_BUF), 0, lane};
     const float al = acc_scale<C>(p);
-    if constexpr (C::HEAD) side_job<C>(p, threadIdx.x - 64, C::THREADS - 64, blockIdx.x, gridDim.x);
+    const float unit = ce_unit<C>(p.ce, lane);
+    if constexpr (C::HEAD) side_job<C>(p, threadIdx.x - 64, C::THREADS - 64, blockIdx.x, gridDim.x, unit);
     for (int j = 0;; ++j) {
       const int slot = j % kSchedDepth;
       if (!mbar_wait(&bk.sched_full[slot], (j / kSchedDepth) & 1, abort_ptr, wait_lim)) break;
@@ -1970,7 +2024,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       if (t < 0) break;
       const TileInfo ti = decode_tile<C>(p, s_poff, s_tpre, t);
       [[maybe_unused]] CeRow cr{};
-      if constexpr (C::CE_STATS || C::EP == Epi::kCeGrad) cr = ce_row<C>(p, ti.m0 + quarter * 32 + lane);
+      if constexpr (C::CE_STATS || C::EP == Epi::kCeGrad) cr = ce_row<C>(p, ti.m0 + quarter * 32 + lane, unit);
       if (!mbar_wait(&tfull_bar[acc], acc_phase, abort_ptr, wait_lim)) break;
       tc_fence_after_sync();
       bool released = false;                 // accumulator already handed back by the epilogue
@@ -2266,12 +2320,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     uint32_t acc_phase = 0;
     Stager<C::STAGING_BUFS, C::STAGING_BUF> st{stage_smem + (warp - 2) * (C::STAGING_BUFS * C::STAGING_BUF), 0,
                                                lane};
-    if constexpr (C::HEAD) side_job<C>(p, threadIdx.x - 64, C::THREADS - 64, blockIdx.x, gridDim.x);
+    const float unit = ce_unit<C>(p.ce, lane);
+    if constexpr (C::HEAD) side_job<C>(p, threadIdx.x - 64, C::THREADS - 64, blockIdx.x, gridDim.x, unit);
     for (int t = cid; t < ntiles; t += ncl) {
       const TileInfo ti = decode_tile<C>(p, s_poff, s_tpre, t);
       [[maybe_unused]] CeRow cr{};
       if constexpr (C::CE_STATS || C::EP == Epi::kCeGrad)
-        cr = ce_row<C>(p, ti.m0 + 128 * static_cast<int>(rank) + quarter * 32 + lane);
+        cr = ce_row<C>(p, ti.m0 + 128 * static_cast<int>(rank) + quarter * 32 + lane, unit);
       if (!mbar_wait(&tfull_bar[acc], acc_phase, abort_ptr, wait_lim)) break;
       tc_fence_after_sync();
       bool released = false;
@@ -2315,7 +2370,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         } else if constexpr (C::EP == Epi::kCeGrad)
           ce_grad_tile<C>(p, th, t_acc, quarter, lane, st, &tmC, part, cr, release);
         else
-          epilogue_tile_tma<C>(p, th, t_acc, quarter, lane, st, &tmC, &tmC2, nullptr, nullptr, 1.0f, part);
+          epilogue_tile_tma<C>(p, th, t_acc, quarter, lane, st, &tmC, &tmC2, nullptr, nullptr, unit, part);
       }
       if (!released) release();
       if (++acc == C::ACC_BUFS) { acc = 0; acc_phase ^= 1u; }

@@ -359,6 +359,36 @@ def test_cross_entropy_training_sizes(lib):
     assert abs(f64(loss).sum() - M.cross_entropy(f64(x), f64(w), lab)["loss"].sum()) <= 2e-5 * T * np.log(V)
 
 
+@pytest.mark.parametrize("T,skip,equal", [(1, 0, True), (2, 0, False), (33, 1, True), (64, 0, False), (65, 0, True),
+                                          (600, 300, True), (2000, 1500, True)])
+@pytest.mark.parametrize("piece", [0, 1024])
+def test_cross_entropy_few_rows_or_equal_weights(lib, T, skip, equal, piece):
+    """Where the roundings of d do not average out over rows: few of them, or all of one weight, half a place above a
+    power of two, where its own rounding costs most (3.9e-3).  What is left is the rounding of the exact gradients to
+    bf16 (about 1.7e-3 in rel-L2), and for equal weights the label's probability, below the last place of -1 + p: its
+    root mean square is e^(1/2) / V = 3.3e-4 for logits of deviation one.  Independent errors add up in squares."""
+    H, V = 512, 5000
+    rng = np.random.default_rng(T)
+    x, w, lab = _bf(rng, T, H), _bf(rng, V, H, std=1.0 / np.sqrt(H)), _labels(rng, T, V, False)
+    lab[:skip] = -1
+    dl = np.full(T, (1 + 0.99 * 2.0 ** -8) * 2.0 ** -9, np.float32)
+    if not equal:
+        dl *= rng.uniform(1.0, 1.003, T).astype(np.float32)
+    fwd = M.cross_entropy(f64(x), f64(w), lab)
+    ref = M.cross_entropy_grad(f64(x), f64(w), lab, np.where(lab >= 0, dl, 0.0).astype(np.float64))
+    dl[:skip] = np.nan
+    dx, dw = _nan(T, H), _nan(V, H)
+    ws = _ws(api.moe_cross_entropy_workspace_bytes(T, H, V, piece))
+    api.moe_cross_entropy_backward(x.to(DEV), w.to(DEV), torch.from_numpy(lab).to(DEV),
+                                   torch.from_numpy(fwd["lse"].astype(np.float32)).to(DEV),
+                                   torch.from_numpy(dl).to(DEV), dx, dw, ws, piece=piece)
+    for got, name in ((dx, "dx"), (dw, "dw")):
+        rounded = rel_l2(f64(torch.from_numpy(ref[name]).to(torch.bfloat16)), ref[name])
+        assert rel_l2(f64(got), ref[name]) <= np.hypot(rounded, 2 * 3.3e-4)
+    assert not f64(dx)[:skip].any()
+    assert api.moe_read_device_status(ws) == 0
+
+
 def test_cross_entropy_extreme_logits(lib):
     """Logits of several hundred in both signs: the running maximum keeps every exponential finite, and
     probabilities that underflow are zero."""
