@@ -214,7 +214,8 @@ struct GemmCfg {
   // MXFP8 copies) in 32-column chunks through the same 2 KB staging.
   static constexpr bool SPLIT_FWD = MX && !NV4 && EP == Epi::kSwiglu && BN == 256;
   static constexpr bool SPLIT_COLS = (NV4 && EP == Epi::kSwiglu && BN == 256) || SPLIT_BWD || SPLIT_FWD;
-  // The vocabulary head's GEMMs (logits, split dx, weight gradient): eight warps too, the second four taking the upper half of the tile's columns.
+  // The vocabulary head's GEMMs (logits, split dx, weight gradient): eight warps too, the second four taking the
+  // upper half of the tile's columns.
   // With a short contraction the epilogue is the longer part of a tile: the
   // gradient's logits at 2048 x 512 x 50000 took 175 us on four warps.
   static constexpr bool HEAD = HEAD_;
