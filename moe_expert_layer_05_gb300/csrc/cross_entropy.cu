@@ -267,10 +267,13 @@ cudaError_t gemm_dw(const void* d, int ld, int T, const void* x, int H, void* dw
 // that does not depend on who is last.
 constexpr int kFewWarps = 16;
 
+// Two (maximum, sum) pairs as one.  The exponents are differences of maxima, so
+// that the side that has the maximum keeps its sum to the bit: a product rounded
+// before the subtraction would leave it a factor that grows with every join
+// (losses of sure rows 1.9e-4 off over 131072 entries, a logit of 90).
 __device__ __forceinline__ float2 ce_join(float2 a, float2 b) {
-  const float m = fmaxf(a.x, b.x);
-  const float off = (m == -INFINITY ? 0.f : m) * kLog2e;
-  return make_float2(m, a.y * ex2(fmaf(a.x, kLog2e, -off)) + b.y * ex2(fmaf(b.x, kLog2e, -off)));
+  const float m = fmaxf(a.x, b.x), top = m == -INFINITY ? 0.f : m;
+  return make_float2(m, a.y * ex2((a.x - top) * kLog2e) + b.y * ex2((b.x - top) * kLog2e));
 }
 
 // lse and loss of one row from its joined pair.

@@ -928,11 +928,14 @@ __device__ __forceinline__ void ce_stats_tile(const GemmParams& p, const TileInf
     #pragma unroll
     for (int j = 1; j < 32; ++j) cm = fmaxf(cm, z[j]);
     const float mn = fmaxf(m, cm);
-    const float off = (mn == -INFINITY ? 0.f : mn) * kLog2e;   // (a row of -infinity: every term is zero)
+    const float top = mn == -INFINITY ? 0.f : mn;              // (a row of -infinity: every term is zero)
+    const float off = top * kLog2e;
     float t[4] = {0.f, 0.f, 0.f, 0.f};
     #pragma unroll
     for (int j = 0; j < 32; ++j) t[j & 3] += ex2(fmaf(z[j], kLog2e, -off));
-    s = s * ex2(fmaf(m, kLog2e, -off)) + ((t[0] + t[1]) + (t[2] + t[3]));
+    // off's rounding is taken out of the new terms' sum; the old sum goes by the
+    // difference of the maxima, exactly 1 where the maximum stays (see ce_join)
+    s = s * ex2((m - top) * kLog2e) + ((t[0] + t[1]) + (t[2] + t[3])) * ex2(-fmaf(top, kLog2e, -off));
     m = mn;
   };
   if constexpr (C::CE_SEG) {

@@ -1,0 +1,49 @@
+"""The embedding, the layer norm and the vocabulary cross entropy where their
+kernels take another course than at small sizes: several rows for each group of
+warps, several groups of tiles, a dominant logit in a large vocabulary, values
+at the ends of the number range, and what is not finite.  Against the fp64
+oracle, as in test_gpu_model.py, whose error bounds are used where none is
+derived here."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_helpers import f64
+from moe_expert_layer_05_gb300 import api
+from oracle import model_oracle as M
+from test_gpu_model import BF, DEV, U, _bf, _dz, _labels, _nan, _within, _ws
+
+pytestmark = pytest.mark.gpu
+F32 = torch.float32
+
+
+def _dev(a, dtype=None):
+    return torch.from_numpy(np.asarray(a, dtype)).to(DEV)
+
+
+def _loss(x, w, lab):
+    """loss, lse and the workspace of one forward call (inputs on the device)."""
+    T, (V, H) = len(x), w.shape
+    loss, lse = _nan(T, dtype=F32), _nan(T, dtype=F32)
+    ws = _ws(api.moe_cross_entropy_workspace_bytes(T, H, V))
+    api.moe_cross_entropy_forward(x, w, lab, loss, lse, ws)
+    return loss, lse, ws
+
+
+# -------------------------------------------------------------- cross entropy
+@pytest.mark.parametrize("T,H", [(1, 64), (2, 64), (40, 64), (140, 64), (5, 4160), (140, 4160)])
+@pytest.mark.parametrize("top", [20.25, 90.0])
+def test_cross_entropy_dominant_label_in_a_large_vocabulary(lib, T, H, top):
+    """Rows that are sure of their label: the sum of exponentials is one and a little, so the loss is what the sum's
+    errors leave.  The label's logit is the same fp32 value in both terms of the loss.  A pair of sums is joined
+    with one rounding of the larger (fewer than V / 2048 + 96 in a row) and an exponential of zero, which is exact;
+    what is smaller by e^20 does not count; then lse is rounded once, and the logarithm's argument twice more."""
+    V, label = 131072 if H < 4096 else 32768, 3
+    rng = np.random.default_rng(T + H)
+    x, w = _bf(rng, T, H, std=0.1), _bf(rng, V, H, std=0.1)
+    x[:, 0], w[:, 0], w[label, 0] = top, 0.0, 1.0
+    ref = M.cross_entropy(f64(x), f64(w), np.full(T, label))
+    loss, lse, _ = _loss(x.to(DEV), w.to(DEV), torch.full((T,), label, dtype=torch.int32, device=DEV))
+    ulp = np.spacing(ref["lse"].astype(np.float32)).astype(np.float64)
+    _within(f64(loss), ref["loss"], (V / 2048 + 96) * U + 1.5 * ulp, "loss")
+    assert (f64(loss) >= -ulp).all()
