@@ -846,6 +846,7 @@ __device__ __forceinline__ void side_job(const GemmParams& p, int thread, int th
       const long long t = p.ce.low > 0 && r >= p.ce.low ? r - p.ce.low : r;
       const int label = t < p.ce.rows ? p.ce.labels[t] : -1;
       const bool scored = label >= 0 && label < p.ce.vocab;
+      if (thread == 0 && !scored && label != -1) set_status(p.status, kErrBadIndex);
       for (int c = thread; c < p.side.words; c += threads)
         dst[r * p.side.words + c] = scored ? p.side.src[t * p.side.words + c] : make_uint4(0, 0, 0, 0);
     }

@@ -47,3 +47,20 @@ def test_cross_entropy_dominant_label_in_a_large_vocabulary(lib, T, H, top):
     ulp = np.spacing(ref["lse"].astype(np.float32)).astype(np.float64)
     _within(f64(loss), ref["loss"], (V / 2048 + 96) * U + 1.5 * ulp, "loss")
     assert (f64(loss) >= -ulp).all()
+
+
+def test_cross_entropy_backward_reports_bad_labels(lib):
+    H, V = 64, 300
+    for T in (6, 200):                                    # (d in two parts, and in one)
+        rng = np.random.default_rng(T)
+        x, w = _bf(rng, T, H).to(DEV), _bf(rng, V, H, std=0.1).to(DEV)
+        good = rng.integers(0, V, T).astype(np.int32)
+        good[::3] = -1
+        for bad in (V, -2, 511, 2 ** 31 - 1, -(2 ** 31), None):
+            lab = good.copy()
+            if bad is not None:
+                lab[T - 1] = bad
+            _, lse, ws = _loss(x, w, _dev(lab))
+            api.moe_workspace_init(ws[:256])
+            api.moe_cross_entropy_backward(x, w, _dev(lab), lse, torch.ones(T, device=DEV), _nan(T, H), _nan(V, H), ws)
+            assert api.moe_read_device_status(ws) == (0 if bad is None else -5), (T, bad)
