@@ -45,7 +45,8 @@ enum class Epi : int {
   kSwigluBwd = 3,   // dh -> dz = [dgate_in | dup] (bf16) and partial <dh, h> per row
   kCeStats = 4,     // logits -> per row and tile: maximum, sum of exponentials; the label's logit
   kCeGrad = 5,      // logits -> gradient of the cross entropy (bf16)
-  kCeStatsSeg = 6,  // kCeStats with the contraction added up in segments (see ce_keep)
+  kCeStatsSeg = 6,  // the same two with the contraction added up in segments
+  kCeGradSeg = 7,   // (see ce_keep)
 };
 
 // The vocabulary head's epilogues (tile columns = vocabulary entries).
@@ -146,7 +147,7 @@ struct GemmParams {
   int kb_per_split;                // kSplitK, or kRoutedK without offsets: k-blocks of one part (0: all)
   int c_add;                       // kSplitK: add to the slabs (1) or overwrite them (0)
   SideJob side;
-  int seg_kb;                      // kCeStatsSeg: k-blocks added up in the tensor cores at a time
+  int seg_kb;                      // kCeStatsSeg, kCeGradSeg: k-blocks added up in the tensor cores at a time
   int m_group;                     // cross entropy: row blocks of one group of tiles
   CeParams ce;
 };
@@ -219,8 +220,9 @@ struct GemmCfg {
   // With a short contraction the epilogue is the longer part of a tile: the
   // gradient's logits at 2048 x 512 x 50000 took 175 us on four warps.
   static constexpr bool HEAD = HEAD_;
-  static constexpr bool CE_SEG = EP == Epi::kCeStatsSeg;
-  static constexpr bool CE_STATS = EP == Epi::kCeStats || CE_SEG;
+  static constexpr bool CE_SEG = EP == Epi::kCeStatsSeg || EP == Epi::kCeGradSeg;
+  static constexpr bool CE_STATS = EP == Epi::kCeStats || EP == Epi::kCeStatsSeg;
+  static constexpr bool CE_GRAD = EP == Epi::kCeGrad || EP == Epi::kCeGradSeg;
   static constexpr int EPI_WARPS = (M256 || SPLIT_COLS || HEAD) ? 8 : 4;
   // Shared memory (all of it dynamic): the k-block ring, 4 KB staging buffers
   // (32 rows x 128 B, 128B-swizzled) per epilogue warp -- two each, or one
@@ -297,7 +299,7 @@ struct GemmCfg {
   static_assert(!HEAD || (!MX && !M256), "the head's GEMMs: bf16, one accumulator row block per CTA");
   static_assert(S != Sched::kSplitK || (HEAD && B_MN && EP == Epi::kStoreF32),
                 "split contraction: bf16, B stored [K, N], fp32 slabs");
-  static_assert((!CE_STATS && EP != Epi::kCeGrad) || (HEAD && !B_MN && S == Sched::kDenseM),
+  static_assert((!CE_STATS && !CE_GRAD) || (HEAD && !B_MN && S == Sched::kDenseM),
                 "cross entropy: bf16 logits of one dense group");
   static_assert(SMEM_USED <= SMEM_BYTES && SMEM_BYTES <= 232448, "shared memory per CTA");
   static_assert(STAGES >= 2, "pipeline depth");
@@ -387,7 +389,7 @@ __device__ __forceinline__ TileInfo decode_tile(const GemmParams& p, const int* 
   } else if constexpr (C::S == Sched::kDenseM) {
     const int mb = (p.m_rows + C::TILE_M - 1) / C::TILE_M;
     ti.group = 0;
-    if (C::CE_STATS || C::EP == Epi::kCeGrad) {
+    if (C::CE_STATS || C::CE_GRAD) {
       // groups of m_group row blocks walk the columns one after another: the
       // rows of a group stay in L2 while the columns stream past
       const int first = t / (p.m_group * p.n_tiles) * p.m_group;
@@ -780,7 +782,7 @@ __device__ __forceinline__ CeRow ce_row(const GemmParams& p, int row, float unit
   CeRow r{-1, 0.f, 0.f};
   if (row < p.m_rows) {
     r.label = p.ce.labels[row];
-    if constexpr (C::EP == Epi::kCeGrad) {
+    if constexpr (C::CE_GRAD) {
       r.lse = p.ce.lse[row];
       r.dloss = p.ce.dloss[row] / unit;
     }
@@ -798,7 +800,7 @@ __device__ __forceinline__ CeRow ce_row(const GemmParams& p, int row, float unit
 constexpr int kUnitRows = 4096;
 template <class C>
 __device__ __forceinline__ float ce_unit(const CeParams& ce, int lane) {
-  if constexpr (C::EP == Epi::kCeGrad || (C::HEAD && C::S == Sched::kRoutedK)) {
+  if constexpr (C::CE_GRAD || (C::HEAD && C::S == Sched::kRoutedK)) {
     const int rows = min(ce.rows, kUnitRows);
     for (int base = 0; base < rows; base += 256) {
       unsigned most = 0;
@@ -837,7 +839,7 @@ __device__ __forceinline__ float ce_label_logit(uint32_t t0, int rel, int c0, in
 template <class C>
 __device__ __forceinline__ void side_job(const GemmParams& p, int thread, int threads, int block, int blocks,
                                          float unit) {
-  if constexpr (C::EP == Epi::kCeGrad) {
+  if constexpr (C::CE_GRAD) {
     // x with the rows that are not scored set to zero: d is zero there, but the
     // product d^T x would still turn an infinity or NaN of such a row into NaN
     // (twice, where d has two parts)
@@ -958,10 +960,12 @@ __device__ __forceinline__ void ce_stats_tile(const GemmParams& p, const TileInf
 // without a label and in columns past the vocabulary, whatever the logits.  With
 // p.ce.low a second pass over the tile writes what the rounding left, to the
 // rows `low` further on.
-template <class C, class St, class Release>
+// kept, zl_kept: the sums and the label's logit of the segments before.
+template <class C, class St, int KEPT_COLS, class Release>
 __device__ __forceinline__ void ce_grad_tile(const GemmParams& p, const TileInfo& ti, uint32_t tmem_acc, int quarter,
                                              int lane, St& st, const CUtensorMap* tmC, int part,
-                                             const CeRow& cr, Release&& release) {
+                                             const CeRow& cr, const float (&kept)[KEPT_COLS], float zl_kept,
+                                             Release&& release) {
   const uint32_t t0 = tmem_acc + (static_cast<uint32_t>(quarter * 32) << 16);
   const int y = ti.m0 + quarter * 32;
   if (y >= p.m_rows) {
@@ -974,44 +978,71 @@ __device__ __forceinline__ void ce_grad_tile(const GemmParams& p, const TileInfo
   const int rel = cr.label - col0;
   const float off = scored ? cr.lse * kLog2e : 0.f;
   const float dl = scored ? cr.dloss : 0.f;
-  #pragma unroll 1
-  for (int low = 0, lows = p.ce.low > 0 ? 1 : 0; low <= lows; ++low) {
-    #pragma unroll 1
-    for (int c0 = part * (C::BN / 2); c0 < (part + 1) * (C::BN / 2); c0 += 64) {
-      const bool edge = c0 + 64 > nv;
-      uint32_t w[2][2][16];
-      load32(t0 + c0, w[0][0], w[0][1]);
-      load32(t0 + c0 + 32, w[1][0], w[1][1]);
-      const float zl = ce_label_logit(t0, rel, c0, 64, lane, 0.f);
-      if (low == lows && c0 + 64 == (part + 1) * (C::BN / 2)) release();
-      st.begin();
+  const int begin = part * (C::BN / 2);
+  // 32 columns of d from their logits, columns [c0, c0 + 32) of the tile, into chunks q0 .. q0 + 3 of the staged rows
+  auto put32 = [&](const uint32_t (&u)[2][16], int c0, int q0, int low, [[maybe_unused]] int at) {
+    float d[32];
+    #pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      float z = __uint_as_float(u[j >> 4][j & 15]);
+      if constexpr (C::CE_SEG) z += kept[at + j];
+      d[j] = ex2(fmaf(z, kLog2e, -off));
+    }
+    #pragma unroll
+    for (int j = 0; j < 32; ++j) d[j] = scored ? d[j] * dl : 0.f;
+    if (c0 + 32 > nv) {
       #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t (&u)[2][16] = w[h];
-        float d[32];
-        #pragma unroll
-        for (int j = 0; j < 32; ++j) d[j] = ex2(fmaf(__uint_as_float(u[j >> 4][j & 15]), kLog2e, -off));
-        #pragma unroll
-        for (int j = 0; j < 32; ++j) d[j] = scored ? d[j] * dl : 0.f;
-        if (edge) {
-          #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (c0 + 32 * h + j >= nv) d[j] = 0.f;
-        }
-        if (low != 0) {
-          #pragma unroll
-          for (int j = 0; j < 32; ++j) d[j] -= bf16_lo(pack_bf16x2(d[j], 0.f));
-        }
-        #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          st.put(4 * h + q, pack_bf16x2(d[8 * q], d[8 * q + 1]), pack_bf16x2(d[8 * q + 2], d[8 * q + 3]),
-                 pack_bf16x2(d[8 * q + 4], d[8 * q + 5]), pack_bf16x2(d[8 * q + 6], d[8 * q + 7]));
+      for (int j = 0; j < 32; ++j)
+        if (c0 + j >= nv) d[j] = 0.f;
+    }
+    if (low != 0) {
+      #pragma unroll
+      for (int j = 0; j < 32; ++j) d[j] -= bf16_lo(pack_bf16x2(d[j], 0.f));
+    }
+    #pragma unroll
+    for (int q = 0; q < 4; ++q)
+      st.put(q0 + q, pack_bf16x2(d[8 * q], d[8 * q + 1]), pack_bf16x2(d[8 * q + 2], d[8 * q + 3]),
+             pack_bf16x2(d[8 * q + 4], d[8 * q + 5]), pack_bf16x2(d[8 * q + 6], d[8 * q + 7]));
+  };
+  // the label's own column, where it is one of [c0, c0 + 64); then the 64 columns leave
+  auto finish = [&](int c0, int low, float zl) {
+    if (scored && rel >= c0 && rel < c0 + 64) {
+      const float d = (ex2(fmaf(zl, kLog2e, -off)) - 1.f) * dl;
+      st.put_bf16(rel - c0, low != 0 ? d - bf16_lo(pack_bf16x2(d, 0.f)) : d);
+    }
+    st.flush(tmC, ti.n * C::BN + c0, low != 0 ? y + p.ce.low : y);
+  };
+  const int lows = p.ce.low > 0 ? 1 : 0;
+  #pragma unroll 1
+  for (int low = 0; low <= lows; ++low) {
+    if constexpr (C::CE_SEG) {
+      // (the sums of the segments before take up the registers: 32 columns at a time)
+      #pragma unroll
+      for (int at = 0; at < C::BN / 2; at += 64) {
+        const int c0 = begin + at;
+        uint32_t u[2][16];
+        load32(t0 + c0, u[0], u[1]);
+        st.begin();
+        put32(u, c0, 0, low, at);
+        load32(t0 + c0 + 32, u[0], u[1]);
+        const float zl = zl_kept + ce_label_logit(t0, rel, c0, 64, lane, 0.f);
+        if (low == lows && at + 64 == C::BN / 2) release();
+        put32(u, c0 + 32, 4, low, at + 32);
+        finish(c0, low, zl);
       }
-      if (scored && rel >= c0 && rel < c0 + 64) {    // the label's own column
-        const float d = (ex2(fmaf(zl, kLog2e, -off)) - 1.f) * dl;
-        st.put_bf16(rel - c0, low != 0 ? d - bf16_lo(pack_bf16x2(d, 0.f)) : d);
+    } else {
+      #pragma unroll 1
+      for (int c0 = begin; c0 < begin + C::BN / 2; c0 += 64) {
+        uint32_t w[2][2][16];
+        load32(t0 + c0, w[0][0], w[0][1]);
+        load32(t0 + c0 + 32, w[1][0], w[1][1]);
+        const float zl = ce_label_logit(t0, rel, c0, 64, lane, 0.f);
+        if (low == lows && c0 + 64 == begin + C::BN / 2) release();
+        st.begin();
+        put32(w[0], c0, 0, low, 0);
+        put32(w[1], c0 + 32, 4, low, 0);
+        finish(c0, low, zl);
       }
-      st.flush(tmC, ti.n * C::BN + c0, low != 0 ? y + p.ce.low : y);
     }
   }
 }
@@ -1915,7 +1946,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (!mbar_wait(&tempty_bar[acc], acc_phase ^ 1u, abort_ptr, wait_lim)) { ok = false; break; }
         tc_fence_after_sync();
         uint32_t d_tmem = tmem_base + acc * C::ACC_COLS;
-        [[maybe_unused]] int seg = 0;      // k-blocks of this segment so far (kCeStatsSeg)
+        [[maybe_unused]] int seg = 0;      // k-blocks of this segment so far (CE_SEG)
         for (int kb = 0; kb < ti.num_kb; ++kb) {
           if constexpr (C::CE_SEG) {
             if (seg == p.seg_kb) {           // the next segment goes to the other accumulator
@@ -2029,7 +2060,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       if (t < 0) break;
       const TileInfo ti = decode_tile<C>(p, s_poff, s_tpre, t);
       [[maybe_unused]] CeRow cr{};
-      if constexpr (C::CE_STATS || C::EP == Epi::kCeGrad) cr = ce_row<C>(p, ti.m0 + quarter * 32 + lane, unit);
+      if constexpr (C::CE_STATS || C::CE_GRAD) cr = ce_row<C>(p, ti.m0 + quarter * 32 + lane, unit);
       if (!mbar_wait(&tfull_bar[acc], acc_phase, abort_ptr, wait_lim)) break;
       tc_fence_after_sync();
       bool released = false;                 // accumulator already handed back by the epilogue
@@ -2052,7 +2083,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           tc_fence_after_sync();
         }
         if (!ok) break;
-        ce_stats_tile<C>(p, ti, tmem_base + acc * C::ACC_COLS, quarter, lane, part, cr, kept, zl, release);
+        const uint32_t t_acc = tmem_base + acc * C::ACC_COLS;
+        if constexpr (C::CE_STATS)
+          ce_stats_tile<C>(p, ti, t_acc, quarter, lane, part, cr, kept, zl, release);
+        else
+          ce_grad_tile<C>(p, ti, t_acc, quarter, lane, st, &tmC, part, cr, kept, zl, release);
       } else if constexpr (C::CE_STATS) {
         const float none[1] = {};
         ce_stats_tile<C>(p, ti, tmem_base + acc * C::ACC_COLS, quarter, lane, part, cr, none, 0.f, release);
@@ -2065,7 +2100,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                &tempty_bar[acc], &released, al);
         }
       } else if constexpr (C::EP == Epi::kCeGrad) {
-        ce_grad_tile<C>(p, ti, tmem_base + acc * C::ACC_COLS, quarter, lane, st, &tmC, part, cr, release);
+        const float none[1] = {};
+        ce_grad_tile<C>(p, ti, tmem_base + acc * C::ACC_COLS, quarter, lane, st, &tmC, part, cr, none, 0.f, release);
       } else if constexpr (C::TMA_OUT) {
         epilogue_tile_tma<C>(p, ti, tmem_base + acc * C::ACC_COLS, quarter, lane, st, &tmC, &tmC2,
                              &tempty_bar[acc], &released, al, (C::SPLIT_COLS || C::HEAD) ? part : 0);
@@ -2278,7 +2314,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (!mbar_wait_cluster(&tempty_bar[acc], acc_phase ^ 1u, abort_ptr, wait_lim)) { ok = false; break; }
         tc_fence_after_sync();
         uint32_t d_tmem = tmem_base + acc * C::ACC_COLS;
-        [[maybe_unused]] int seg = 0;      // k-blocks of this segment so far (kCeStatsSeg)
+        [[maybe_unused]] int seg = 0;      // k-blocks of this segment so far (CE_SEG)
         for (int kb = 0; kb < ti.num_kb; ++kb) {
           if constexpr (C::CE_SEG) {
             if (seg == p.seg_kb) {           // the next segment goes to the other accumulator
@@ -2330,7 +2366,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     for (int t = cid; t < ntiles; t += ncl) {
       const TileInfo ti = decode_tile<C>(p, s_poff, s_tpre, t);
       [[maybe_unused]] CeRow cr{};
-      if constexpr (C::CE_STATS || C::EP == Epi::kCeGrad)
+      if constexpr (C::CE_STATS || C::CE_GRAD)
         cr = ce_row<C>(p, ti.m0 + 128 * static_cast<int>(rank) + quarter * 32 + lane, unit);
       if (!mbar_wait(&tfull_bar[acc], acc_phase, abort_ptr, wait_lim)) break;
       tc_fence_after_sync();
@@ -2363,17 +2399,23 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           tc_fence_after_sync();
         }
         if (!ok) break;
-        if (mine) ce_stats_tile<C>(p, th, tmem_base + acc * C::ACC_COLS, quarter, lane, part, cr, kept, zl, release);
+        if (mine) {
+          const uint32_t t_acc = tmem_base + acc * C::ACC_COLS;
+          if constexpr (C::CE_STATS)
+            ce_stats_tile<C>(p, th, t_acc, quarter, lane, part, cr, kept, zl, release);
+          else
+            ce_grad_tile<C>(p, th, t_acc, quarter, lane, st, &tmC, part, cr, kept, zl, release);
+        }
       } else
       if (mine) {
         TileInfo th = ti;
         th.m0 += 128 * static_cast<int>(rank);
         const uint32_t t_acc = tmem_base + acc * C::ACC_COLS;
-        if constexpr (C::CE_STATS) {
-          const float none[1] = {};
+        [[maybe_unused]] const float none[1] = {};
+        if constexpr (C::CE_STATS)
           ce_stats_tile<C>(p, th, t_acc, quarter, lane, part, cr, none, 0.f, release);
-        } else if constexpr (C::EP == Epi::kCeGrad)
-          ce_grad_tile<C>(p, th, t_acc, quarter, lane, st, &tmC, part, cr, release);
+        else if constexpr (C::EP == Epi::kCeGrad)
+          ce_grad_tile<C>(p, th, t_acc, quarter, lane, st, &tmC, part, cr, none, 0.f, release);
         else
           epilogue_tile_tma<C>(p, th, t_acc, quarter, lane, st, &tmC, &tmC2, nullptr, nullptr, unit, part);
       }

@@ -64,3 +64,40 @@ def test_cross_entropy_backward_reports_bad_labels(lib):
             api.moe_workspace_init(ws[:256])
             api.moe_cross_entropy_backward(x, w, _dev(lab), lse, torch.ones(T, device=DEV), _nan(T, H), _nan(V, H), ws)
             assert api.moe_read_device_status(ws) == (0 if bad is None else -5), (T, bad)
+
+
+def _sure_rows(T, H, top):
+    """Each row sure of a label of its own (p within e^-top V of 1): what is left of exp(z - lse) - 1 there is the
+    gradient, and the error of z - lse its error.  z is the same fp32 value in the forward's lse and here, so that
+    error is lse's rounding (half an ulp), the product's with log2 e (less than one ulp of lse) and the relative
+    error of lse's sum (2 (V / 2048 + 96) u, with the two exponentials' 2^-21); an error of z itself counts only in
+    proportion to d.  The rest as for other rows."""
+    V = 8192
+    rng = np.random.default_rng(T + H)
+    x, lab = _bf(rng, T, H), rng.permutation(V)[:T].astype(np.int32)
+    w = _bf(rng, V, H, std=1 / np.sqrt(H)).float()
+    xf = x.float()
+    w[torch.from_numpy(lab).long()] += top * xf / (xf * xf).sum(1, keepdim=True)
+    w = w.to(BF)
+    xd, wd, ld = x.to(DEV), w.to(DEV), _dev(lab)
+    _, lse, ws = _loss(xd, wd, ld)
+    dl = (rng.uniform(0.5, 1.5, T) / T).astype(np.float32)
+    dx, dw = _nan(T, H), _nan(V, H)
+    api.moe_cross_entropy_backward(xd, wd, ld, lse, _dev(dl), dx, dw, ws)
+    ref = M.cross_entropy(f64(x), f64(w), lab)
+    g = M.cross_entropy_grad(f64(x), f64(w), lab, dl.astype(np.float64))
+    dz = 2 * _dz(ref, H).max()
+    ulp = np.spacing(ref["lse"].astype(np.float32)).astype(np.float64)
+    d_err = dl * (1.5 * ulp + 2 * (V / 2048 + 96) * U + 2.0 ** -21)
+    label_err = {"dx": d_err[:, None] * np.abs(f64(w)[lab]), "dw": np.zeros(w.shape)}
+    label_err["dw"][lab] = d_err[:, None] * np.abs(f64(x))
+    for got, name in ((dx, "dx"), (dw, "dw")):
+        _within(f64(got), g[name], 2.0 ** -8 * np.abs(g[name]) + 2.0 ** -7 * g[name + "_sq"]
+                + (2 * dz + 2.0 ** -15) * g[name + "_mag"] + 1.01 * label_err[name] + 1e-30, name)
+    assert api.moe_read_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("T,H", [(5, 1024), (140, 4096), (3, 7168), (70, 4104), (140, 7168), (33, 16384)])
+@pytest.mark.parametrize("top", [20.0, 60.0])
+def test_cross_entropy_gradient_of_sure_rows(lib, T, H, top):
+    _sure_rows(T, H, top)
