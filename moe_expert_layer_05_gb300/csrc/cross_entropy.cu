@@ -78,9 +78,12 @@ int piece_of(int T, int V, int piece) {
 }
 
 // Tokens up to which d has two parts: their rows fit in one 128-row tile that has
-// to be read and multiplied whole anyway.
+// to be read and multiplied whole anyway.  (The tiles' stores are 32 rows high; for
+// up to kFewRows tokens d comes by entries.)
 constexpr int kTwoParts = 64;
-int low_row(int T) { return T <= kTwoParts ? round_up(T, 32) : 0; }     // first row of the lower parts; 0: none
+int low_row(int T) {                                                    // first row of the lower parts; 0: none
+  return T <= kFewRows ? T : T <= kTwoParts ? round_up(T, 32) : 0;
+}
 int d_rows(int T) { return T <= kTwoParts ? 2 * low_row(T) : T; }       // rows of d, of x in dw, of dx's slabs
 
 // Up to 128 tokens the logits and dx run on 128-row tiles of one CTA,
@@ -291,6 +294,62 @@ __device__ __forceinline__ void ce_row_out(float2 a, int row, const int32_t* __r
   loss[row] = scored ? l - __ldcg(label_logit + row) : 0.f;    // (another block may have written it)
 }
 
+// Logits of STEP entries (their rows of w) and TT tokens, by one warp: mine[r] is
+// token t's of entry r in lane t.  Both directions call this: where a row is sure of
+// its label, z and lse have to come of the same additions.
+template <int TT, int STEP>
+__device__ __forceinline__ void few_logits(const uint4* const (&rows)[STEP], int words, const uint4* s_x, int lane,
+                                           float (&mine)[STEP]) {
+  F32x2 acc[STEP][TT];
+  #pragma unroll
+  for (int r = 0; r < STEP; ++r)
+    #pragma unroll
+    for (int t = 0; t < TT; ++t) acc[r][t] = make_f32x2(0.f, 0.f);
+  for (int c0 = lane; c0 < words; c0 += 4 * 32) {
+    uint4 u[4][STEP];
+    #pragma unroll
+    for (int i = 0; i < 4; ++i)
+      #pragma unroll
+      for (int r = 0; r < STEP; ++r)
+        u[i][r] = c0 + 32 * i < words ? rows[r][c0 + 32 * i] : make_uint4(0, 0, 0, 0);
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = c0 + 32 * i;
+      if (c < words) {
+        F32x2 wv[STEP][4];
+        #pragma unroll
+        for (int r = 0; r < STEP; ++r) {
+          wv[r][0] = bf16x2_f32x2(u[i][r].x);
+          wv[r][1] = bf16x2_f32x2(u[i][r].y);
+          wv[r][2] = bf16x2_f32x2(u[i][r].z);
+          wv[r][3] = bf16x2_f32x2(u[i][r].w);
+        }
+        #pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          const uint4 xu = s_x[t * words + c];
+          const F32x2 xv[4] = {bf16x2_f32x2(xu.x), bf16x2_f32x2(xu.y), bf16x2_f32x2(xu.z), bf16x2_f32x2(xu.w)};
+          #pragma unroll
+          for (int r = 0; r < STEP; ++r)
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) acc[r][t] = fma2(wv[r][j], xv[j], acc[r][t]);
+        }
+      }
+    }
+  }
+  #pragma unroll
+  for (int r = 0; r < STEP; ++r) {
+    mine[r] = 0.f;
+    #pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      const float2 f = split_f32x2(acc[r][t]);
+      float z = f.x + f.y;
+      #pragma unroll
+      for (int d = 16; d > 0; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+      if (lane == t) mine[r] = z;
+    }
+  }
+}
+
 template <int TT, int STEP>
 __global__ void __launch_bounds__(32 * kFewWarps) ce_few_kernel(const uint4* __restrict__ x,
                                                                 const uint4* __restrict__ w,
@@ -309,59 +368,16 @@ __global__ void __launch_bounds__(32 * kFewWarps) ce_few_kernel(const uint4* __r
   float2 run = make_float2(-INFINITY, 0.f);
   const int stride = gridDim.x * kFewWarps * STEP;
   for (int v0 = (blockIdx.x * kFewWarps + warp) * STEP; v0 < V; v0 += stride) {
-    F32x2 acc[STEP][TT];
-    #pragma unroll
-    for (int r = 0; r < STEP; ++r)
-      #pragma unroll
-      for (int t = 0; t < TT; ++t) acc[r][t] = make_f32x2(0.f, 0.f);
     const uint4* rows[STEP];
     #pragma unroll
     for (int r = 0; r < STEP; ++r) rows[r] = w + static_cast<long long>(min(v0 + r, V - 1)) * words;
-    for (int c0 = lane; c0 < words; c0 += 4 * 32) {
-      uint4 u[4][STEP];
-      #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        #pragma unroll
-        for (int r = 0; r < STEP; ++r)
-          u[i][r] = c0 + 32 * i < words ? rows[r][c0 + 32 * i] : make_uint4(0, 0, 0, 0);
-      #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = c0 + 32 * i;
-        if (c < words) {
-          F32x2 wv[STEP][4];
-          #pragma unroll
-          for (int r = 0; r < STEP; ++r) {
-            wv[r][0] = bf16x2_f32x2(u[i][r].x);
-            wv[r][1] = bf16x2_f32x2(u[i][r].y);
-            wv[r][2] = bf16x2_f32x2(u[i][r].z);
-            wv[r][3] = bf16x2_f32x2(u[i][r].w);
-          }
-          #pragma unroll
-          for (int t = 0; t < TT; ++t) {
-            const uint4 xu = s_x[t * words + c];
-            const F32x2 xv[4] = {bf16x2_f32x2(xu.x), bf16x2_f32x2(xu.y), bf16x2_f32x2(xu.z), bf16x2_f32x2(xu.w)};
-            #pragma unroll
-            for (int r = 0; r < STEP; ++r)
-              #pragma unroll
-              for (int j = 0; j < 4; ++j) acc[r][t] = fma2(wv[r][j], xv[j], acc[r][t]);
-          }
-        }
-      }
-    }
+    float mine[STEP];
+    few_logits<TT, STEP>(rows, words, s_x, lane, mine);
     #pragma unroll
     for (int r = 0; r < STEP; ++r) {
-      float mine = 0.f;                     // lane t: token t's logit
-      #pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const float2 f = split_f32x2(acc[r][t]);
-        float z = f.x + f.y;
-        #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
-        if (lane == t) mine = z;
-      }
       if (v0 + r < V && lane < T) {
-        run = ce_join(run, make_float2(mine, 1.f));
-        if (label == v0 + r) label_logit[lane] = mine;
+        run = ce_join(run, make_float2(mine[r], 1.f));
+        if (label == v0 + r) label_logit[lane] = mine[r];
       }
     }
   }
@@ -391,11 +407,60 @@ __global__ void __launch_bounds__(32 * kFewWarps) ce_few_kernel(const uint4* __r
   }
 }
 
+// d of one piece (w: its rows) for as few tokens, as ce_grad_tile's: in two bf16
+// parts, rows t and T + t, zero from the piece's last entry to the end of its last
+// tile.  Block 0 also leaves the copy of x that the weight gradient reads, twice,
+// without the rows that are not scored (xz: null but for the first piece).
 template <int TT, int STEP>
-cudaError_t loss_few(const void* x, const void* w, int T, int H, int V, const CeParams& ce, float* loss, float* lse,
-                     int* status, cudaStream_t st) {
-  auto kern = ce_few_kernel<TT, STEP>;
-  static std::atomic<bool> attr_set[kMaxDevices];
+__global__ void __launch_bounds__(32 * kFewWarps) ce_few_grad_kernel(const uint4* __restrict__ x,
+                                                                     const uint4* __restrict__ w, int T, int words,
+                                                                     int entries, const CeParams ce, int ld,
+                                                                     __nv_bfloat16* __restrict__ d,
+                                                                     uint4* __restrict__ xz, int* status) {
+  pdl_entry();
+  extern __shared__ __align__(16) uint4 s_x[];          // [TT][words], zero past T
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = threadIdx.x; i < TT * words; i += blockDim.x)
+    s_x[i] = i < T * words ? x[i] : make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  const float unit = ce_unit_of(ce, lane);
+  const int label = lane < T ? ce.labels[lane] : -1;
+  const bool scored = label >= 0 && label < ce.vocab;
+  const float off = scored ? ce.lse[lane] * kLog2e : 0.f, dl = scored ? ce.dloss[lane] / unit : 0.f;
+  if (blockIdx.x == 0 && xz != nullptr) {
+    if (warp == 0 && !scored && label != -1) set_status(status, kErrBadIndex);
+    const unsigned rows_scored = __ballot_sync(0xffffffffu, scored);
+    for (int i = threadIdx.x; i < T * words; i += blockDim.x)
+      xz[i] = xz[T * words + i] = (rows_scored >> (i / words)) & 1u ? s_x[i] : make_uint4(0, 0, 0, 0);
+  }
+  const int end = (entries + kTile - 1) / kTile * kTile;
+  const int stride = gridDim.x * kFewWarps * STEP;
+  for (int v0 = (blockIdx.x * kFewWarps + warp) * STEP; v0 < end; v0 += stride) {
+    const uint4* rows[STEP];
+    #pragma unroll
+    for (int r = 0; r < STEP; ++r) rows[r] = w + static_cast<long long>(min(v0 + r, entries - 1)) * words;
+    float mine[STEP];
+    few_logits<TT, STEP>(rows, words, s_x, lane, mine);
+    if (lane < T) {
+      #pragma unroll
+      for (int r = 0; r < STEP; ++r) {                  // (kTile is a multiple of STEP: v0 + r < end)
+        float g = ex2(fmaf(mine[r], kLog2e, -off));
+        if (label == ce.v0 + v0 + r) g -= 1.f;
+        g = scored && v0 + r < entries ? g * dl : 0.f;
+        const __nv_bfloat16 upper = __float2bfloat16_rn(g);
+        __nv_bfloat16* to = d + static_cast<long long>(lane) * ld + v0 + r;
+        to[0] = upper;
+        to[static_cast<long long>(T) * ld] = __float2bfloat16_rn(g - __bfloat162float(upper));
+      }
+    }
+  }
+}
+
+// Launches either kernel for `entries` entries: dynamic shared memory for x, as
+// many blocks as there is work for.
+template <int TT, int STEP, class Kern, class... Args>
+cudaError_t launch_few(Kern kern, std::atomic<bool> (&attr_set)[kMaxDevices], int H, int entries, cudaStream_t st,
+                       Args... args) {
   const int dev = current_device();
   if (dev < 0) return cudaErrorInvalidDevice;
   if (!attr_set[dev].load(std::memory_order_acquire)) {
@@ -404,12 +469,28 @@ cudaError_t loss_few(const void* x, const void* w, int T, int H, int V, const Ce
     if (e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
-  const int need = (V + kFewWarps * STEP - 1) / (kFewWarps * STEP);
-  const int blocks = need < kFewBlocks ? need : kFewBlocks;
+  const int need = (entries + kFewWarps * STEP - 1) / (kFewWarps * STEP);
   count_launches(1);
-  return launch_k(kern, blocks, 32 * kFewWarps, static_cast<size_t>(TT) * H * 2, st, static_cast<const uint4*>(x),
-                  static_cast<const uint4*>(w), ce.labels, T, H / 8, V, ce.stats, ce.label_logit, loss, lse,
-                  status);
+  return launch_k(kern, need < kFewBlocks ? need : kFewBlocks, 32 * kFewWarps, static_cast<size_t>(TT) * H * 2, st,
+                  args...);
+}
+
+template <int TT, int STEP>
+cudaError_t loss_few(const void* x, const void* w, int T, int H, int V, const CeParams& ce, float* loss, float* lse,
+                     int* status, cudaStream_t st) {
+  static std::atomic<bool> attr_set[kMaxDevices];
+  return launch_few<TT, STEP>(ce_few_kernel<TT, STEP>, attr_set, H, V, st, static_cast<const uint4*>(x),
+                              static_cast<const uint4*>(w), ce.labels, T, H / 8, V, ce.stats, ce.label_logit, loss,
+                              lse, status);
+}
+
+template <int TT, int STEP>
+cudaError_t grad_few(const void* x, const void* w_rows, int T, int H, int rows, const CeParams& ce, int ld, void* d,
+                     void* xz, int* status, cudaStream_t st) {
+  static std::atomic<bool> attr_set[kMaxDevices];
+  return launch_few<TT, STEP>(ce_few_grad_kernel<TT, STEP>, attr_set, H, round_up(rows, kTile), st,
+                              static_cast<const uint4*>(x), static_cast<const uint4*>(w_rows), T, H / 8, rows, ce, ld,
+                              static_cast<__nv_bfloat16*>(d), static_cast<uint4*>(xz), status);
 }
 
 // ---------------------------------------------------------------- row kernels
@@ -544,12 +625,17 @@ moe_status moe_cross_entropy_backward(const void* x, const void* w, const int32_
     const char* w_rows = static_cast<const char*>(w) + at_w;
     char* dw_rows = static_cast<char*>(dw) + at_w;
     ce.v0 = v0;
-    if (H > kWhole)
+    if (T <= kFewRows) {
+      void* x_to = v0 == 0 ? xz : nullptr;
+      MOE_TRY(T == 1 ? (grad_few<1, 2>(x, w_rows, T, H, rows, ce, l.piece, d, x_to, status, st))
+                     : (grad_few<kFewRows, 1>(x, w_rows, T, H, rows, ce, l.piece, d, x_to, status, st)));
+    } else if (H > kWhole) {
       MOE_TRY(small ? (gemm_logits<Epi::kCeGradSeg, false>(x, T, H, w_rows, rows, d, l.piece, ce, copy, status, st))
                     : (gemm_logits<Epi::kCeGradSeg, true>(x, T, H, w_rows, rows, d, l.piece, ce, copy, status, st)));
-    else
+    } else {
       MOE_TRY(small ? (gemm_logits<Epi::kCeGrad, false>(x, T, H, w_rows, rows, d, l.piece, ce, copy, status, st))
                     : (gemm_logits<Epi::kCeGrad, true>(x, T, H, w_rows, rows, d, l.piece, ce, copy, status, st)));
+    }
     if (small) {
       MOE_TRY(gemm_dx<false>(d, l.piece, D, w_rows, rows, H, per, slabs, l.slab_count, v0 > 0, status, st));
     } else {

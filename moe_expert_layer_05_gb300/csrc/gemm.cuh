@@ -798,24 +798,27 @@ __device__ __forceinline__ CeRow ce_row(const GemmParams& p, int row, float unit
 // its mantissa the weight is a power of two.  Unequal weights lie below a power of
 // two then, where the places of a bf16 are closer.  Any factor would be right.
 constexpr int kUnitRows = 4096;
+__device__ __forceinline__ float ce_unit_of(const CeParams& ce, int lane) {
+  const int rows = min(ce.rows, kUnitRows);
+  for (int base = 0; base < rows; base += 256) {
+    unsigned most = 0;
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = base + 32 * i + lane;
+      const int label = r < rows ? ce.labels[r] : -1;
+      const unsigned w = r < rows ? __float_as_uint(ce.dloss[r]) & 0x7fffffffu : 0u;
+      if (label >= 0 && label < ce.vocab && w >= 0x00800000u && w < 0x7f800000u)   // (normal numbers)
+        most = max(most, w);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (most != 0) return __uint_as_float((most & 0x7fffffu) | 0x3f800000u);
+  }
+  return 1.0f;
+}
+// Of a kernel that makes d or ends in a gradient; 1 in the others.
 template <class C>
 __device__ __forceinline__ float ce_unit(const CeParams& ce, int lane) {
-  if constexpr (C::CE_GRAD || (C::HEAD && C::S == Sched::kRoutedK)) {
-    const int rows = min(ce.rows, kUnitRows);
-    for (int base = 0; base < rows; base += 256) {
-      unsigned most = 0;
-      #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = base + 32 * i + lane;
-        const int label = r < rows ? ce.labels[r] : -1;
-        const unsigned w = r < rows ? __float_as_uint(ce.dloss[r]) & 0x7fffffffu : 0u;
-        if (label >= 0 && label < ce.vocab && w >= 0x00800000u && w < 0x7f800000u)   // (normal numbers)
-          most = max(most, w);
-      }
-      most = __reduce_max_sync(0xffffffffu, most);
-      if (most != 0) return __uint_as_float((most & 0x7fffffu) | 0x3f800000u);
-    }
-  }
+  if constexpr (C::CE_GRAD || (C::HEAD && C::S == Sched::kRoutedK)) return ce_unit_of(ce, lane);
   return 1.0f;
 }
 

@@ -101,3 +101,9 @@ def _sure_rows(T, H, top):
 @pytest.mark.parametrize("top", [20.0, 60.0])
 def test_cross_entropy_gradient_of_sure_rows(lib, T, H, top):
     _sure_rows(T, H, top)
+
+
+@pytest.mark.parametrize("T,H", [(1, 64), (1, 1024), (2, 1024), (1, 7168), (2, 4096)])
+@pytest.mark.parametrize("top", [20.0, 60.0])
+def test_cross_entropy_gradient_of_one_or_two_sure_rows(lib, T, H, top):
+    _sure_rows(T, H, top)
