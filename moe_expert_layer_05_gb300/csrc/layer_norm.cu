@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(512, 1) layer_norm_bwd_kernel(const uint4* __r
   if (gtid == 0) {
     for (int i = 0; i < stages; ++i) load(t0 + static_cast<long long>(i) * step, i);
   }
-  // (KEEP: weight, s - mu and g in registers; wider rows leave those to the sums
+  // (KEEP: weight, xh and g in registers; wider rows leave those to the sums
   // and take the row a second time from shared memory)
   constexpr bool KEEP = NV == 2;
   P8 w[KEEP ? NV : 1];
@@ -259,11 +259,11 @@ __global__ void __launch_bounds__(512, 1) layer_norm_bwd_kernel(const uint4* __r
     // together, on whatever the buffer holds, and starts no more copies)
     mbar_wait(&s_full[group][stage], phase, &s_abort, wait_ns);
     const uint4* row_s = buf + static_cast<size_t>(stage) * ROWS * words;
-    // (s - mu) and g stay in registers for the second half of the row's work:
+    // xh and g stay in registers for the second half of the row's work:
     // taking bf16 pairs apart is what the kernel's arithmetic mostly costs
     const F32x2 neg_mu = make_f32x2(-mu, -mu), rs2 = make_f32x2(rs, rs);
     F32x2 s1 = make_f32x2(0.f, 0.f), s2 = make_f32x2(0.f, 0.f);
-    P8 cen[KEEP ? NV : 1], g[KEEP ? NV : 1];
+    P8 norm[KEEP ? NV : 1], g[KEEP ? NV : 1];
     uint4 ue[KEEP ? NV : 1];
     #pragma unroll
     for (int i = 0; i < NV; ++i) {               // (words past the row: dy = 0 adds nothing)
@@ -273,14 +273,13 @@ __global__ void __launch_bounds__(512, 1) layer_norm_bwd_kernel(const uint4* __r
       const P8 wv = KEEP ? w[KEEP ? i : 0] : pairs8(word_of(weight, c, words));
       #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const F32x2 cj = add2(xs.p[j], neg_mu), gj = mul2(d.p[j], wv.p[j]);
-        const F32x2 xh = mul2(cj, rs2);
+        const F32x2 xh = mul2(add2(xs.p[j], neg_mu), rs2), gj = mul2(d.p[j], wv.p[j]);
         dw[i].p[j] = fma2(d.p[j], xh, dw[i].p[j]);
         db[i].p[j] = add2(db[i].p[j], d.p[j]);
         s1 = add2(s1, gj);
         s2 = fma2(gj, xh, s2);
         if constexpr (KEEP) {
-          cen[i].p[j] = cj;
+          norm[i].p[j] = xh;
           g[i].p[j] = gj;
         }
       }
@@ -312,9 +311,9 @@ __global__ void __launch_bounds__(512, 1) layer_norm_bwd_kernel(const uint4* __r
       if (gtid == 0 && !*static_cast<volatile int*>(&s_abort)) load(t + static_cast<long long>(stages) * step, stage);
     };
     if constexpr (KEEP) refill();
-    // dx = rs g - rs <g> - (s - mu) rs^2 <g xh>
+    // dx = rs g - rs <g> - xh rs <g xh>  (rs^2 would leave fp32 where rs does not)
     m1 *= -inv_h * rs;
-    m2 *= -inv_h * rs * rs;
+    m2 *= -inv_h * rs;
     const F32x2 k1 = make_f32x2(m1, m1), k2 = make_f32x2(m2, m2);
     const long long row = t * words;
     #pragma unroll
@@ -323,13 +322,13 @@ __global__ void __launch_bounds__(512, 1) layer_norm_bwd_kernel(const uint4* __r
       P8 o;
       if constexpr (KEEP) {
         #pragma unroll
-        for (int j = 0; j < 4; ++j) o.p[j] = fma2(cen[i].p[j], k2, fma2(g[i].p[j], rs2, k1));
+        for (int j = 0; j < 4; ++j) o.p[j] = fma2(norm[i].p[j], k2, fma2(g[i].p[j], rs2, k1));
       } else {
         const P8 xs = pairs8(word_of(row_s, c, words)), d = pairs8(word_of(row_s + words, c, words));
         const P8 wv = pairs8(word_of(weight, c, words));
         #pragma unroll
         for (int j = 0; j < 4; ++j)
-          o.p[j] = fma2(add2(xs.p[j], neg_mu), k2, fma2(mul2(d.p[j], wv.p[j]), rs2, k1));
+          o.p[j] = fma2(mul2(add2(xs.p[j], neg_mu), rs2), k2, fma2(mul2(d.p[j], wv.p[j]), rs2, k1));
       }
       if constexpr (DSUM) {
         const P8 e = pairs8(KEEP ? ue[KEEP ? i : 0] : word_of(row_s + 2 * words, c, words));

@@ -107,3 +107,27 @@ def test_cross_entropy_gradient_of_sure_rows(lib, T, H, top):
 @pytest.mark.parametrize("top", [20.0, 60.0])
 def test_cross_entropy_gradient_of_one_or_two_sure_rows(lib, T, H, top):
     _sure_rows(T, H, top)
+
+
+# ----------------------------------------------------------------- layer norm
+def _norm_grad_case(rng, T, H, spread=1.0):
+    s = _bf(rng, T, H, std=spread, mean=0.3 * spread)
+    return s, _bf(rng, H, std=0.2, mean=1.0), _bf(rng, T, H)
+
+
+@pytest.mark.parametrize("H", [512, 4096, 10248])
+@pytest.mark.parametrize("size", [1e-20, 3e18])
+def test_layer_norm_backward_at_the_ends_of_the_range(lib, H, size):
+    """Rows so small (eps = 0) or large that the square of their rstd leaves fp32: rstd and dx do not."""
+    T = 40
+    rng = np.random.default_rng(H)
+    s, w, dy = _norm_grad_case(rng, T, H, spread=size)
+    f = M.layer_norm(f64(s), f64(w), eps=0.0)
+    mean, rstd = _dev(f["mean"], np.float32), _dev(f["rstd"], np.float32)
+    dx, dw, db = _nan(T, H), _nan(H, dtype=F32), _nan(H, dtype=F32)
+    ws = _ws(api.moe_layer_norm_workspace_bytes(T, H))
+    api.moe_layer_norm_backward(dy.to(DEV), s.to(DEV), w.to(DEV), mean, rstd, dx, dw, db, ws)
+    ref = M.layer_norm_grad(f64(dy), f64(s), f64(w), f64(mean), f64(rstd))
+    chain = H / 8 + 64
+    _within(f64(dx), ref["dx"], 2.0 ** -8 * np.abs(ref["dx"]) + (chain + 16) * U * ref["dx_mag"], "dx")
+    _within(f64(dw), ref["dweight"], 88 * U * ref["dweight_mag"] + 1e-30, "dweight")
