@@ -68,11 +68,12 @@ __global__ void __launch_bounds__(128) embedding_fwd_kernel(const int32_t* __res
     #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int c = WIDE ? c0 + i * 128 : c0;
+      const float by = tok[i] >= 0 ? scale : 0.f;      // (a zero row whatever the scale)
       if (c < words && row[i] < n)
-        out[row[i] * words + c] = make_uint4(pack_bf16x2(bf16_lo(v[i].x) * scale, bf16_hi(v[i].x) * scale),
-                                             pack_bf16x2(bf16_lo(v[i].y) * scale, bf16_hi(v[i].y) * scale),
-                                             pack_bf16x2(bf16_lo(v[i].z) * scale, bf16_hi(v[i].z) * scale),
-                                             pack_bf16x2(bf16_lo(v[i].w) * scale, bf16_hi(v[i].w) * scale));
+        out[row[i] * words + c] = make_uint4(pack_bf16x2(bf16_lo(v[i].x) * by, bf16_hi(v[i].x) * by),
+                                             pack_bf16x2(bf16_lo(v[i].y) * by, bf16_hi(v[i].y) * by),
+                                             pack_bf16x2(bf16_lo(v[i].z) * by, bf16_hi(v[i].z) * by),
+                                             pack_bf16x2(bf16_lo(v[i].w) * by, bf16_hi(v[i].w) * by));
     }
   }
 }

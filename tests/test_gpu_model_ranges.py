@@ -131,3 +131,18 @@ def test_layer_norm_backward_at_the_ends_of_the_range(lib, H, size):
     chain = H / 8 + 64
     _within(f64(dx), ref["dx"], 2.0 ** -8 * np.abs(ref["dx"]) + (chain + 16) * U * ref["dx_mag"], "dx")
     _within(f64(dw), ref["dweight"], 88 * U * ref["dweight_mag"] + 1e-30, "dweight")
+
+
+# ------------------------------------------------------------------ embedding
+@pytest.mark.parametrize("H", [64, 2056])
+@pytest.mark.parametrize("scale", [float("inf"), float("nan"), -3.0])
+def test_embedding_padding_is_zero_whatever_the_scale(lib, H, scale):
+    V = 20
+    table = _bf(np.random.default_rng(H), V, H).to(DEV)
+    tok = torch.tensor([3, -1, 19, -1, 0], dtype=torch.int32, device=DEV)
+    out, ws = _nan(5, H), _ws(256)
+    api.moe_embedding_forward(tok, table, out, ws, scale=scale)
+    pad = tok < 0
+    assert not out[pad].view(torch.int16).any()              # (+0, to the bit)
+    want = (table[tok[~pad].long()].float() * scale).to(BF)
+    assert torch.equal(out[~pad].nan_to_num(nan=7.0), want.nan_to_num(nan=7.0))
