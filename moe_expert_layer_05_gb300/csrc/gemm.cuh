@@ -1924,8 +1924,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
       }
       sched_finish(p.sched);
-      if (!ok) {
+      if (!ok || C::HEAD) {
         // unwinding: let every load still in flight land before the CTA exits
+        // (the head's short contractions may all be on their way when the MMA
+        // warp gives up; in a run that does not, they have landed by the end)
         for (int s = 0; s < C::STAGES; ++s)
           if (issued_mask & (1u << s)) mbar_wait_drain(&full_bar[s], (issued_parity >> s) & 1u);
       }
@@ -2291,9 +2293,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
         }
       }
-      if (!ok) {
+      if (!ok || (C::HEAD && leader)) {
         if (leader) {
           // unwinding: let every stage still counted on this CTA's barriers land
+          // (head: see grouped_gemm_kernel)
           for (int s = 0; s < C::STAGES; ++s)
             if (issued_mask & (1u << s)) mbar_wait_drain(&full_bar[s], (issued_parity >> s) & 1u);
         } else {
@@ -2431,6 +2434,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
+  if constexpr (C::HEAD) {
+    // loads that the odd CTA's producer had issued when another warp gave up: the
+    // same time to land
+    if (!leader && bk.abort_flag && threadIdx.x == 0) {
+      const unsigned long long t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 200000ull) {
+      }
+    }
+    __syncwarp();
+  }
   cluster_sync();                       // the peer no longer reads this CTA's memory or signals its barriers
   pdl_launch_next();
   if (threadIdx.x == 0 && bk.abort_flag) set_status(p.status, kErrTimeout);
