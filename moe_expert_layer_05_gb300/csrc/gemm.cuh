@@ -1050,6 +1050,16 @@ __device__ __forceinline__ void ce_grad_tile(const GemmParams& p, const TileInfo
   }
 }
 
+// An epilogue warp's wait.  The head's epilogues take votes and shuffles over the
+// whole warp, so there its lanes go on together or, if one has given up, not at all.
+template <class C>
+__device__ __forceinline__ bool epilogue_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                              unsigned long long limit_ns) {
+  const bool ok = mbar_wait(bar, parity, abort, limit_ns);
+  if constexpr (C::HEAD) return __all_sync(0xffffffffu, ok) != 0;
+  return ok;
+}
+
 // Epilogue with TMA stores.  Rows of the tile: warp quarter q owns rows
 // 32q..32q+31, lane = row.  Dense tiles past the last row are clipped by TMA.
 template <class C>
@@ -2058,7 +2068,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     if constexpr (C::HEAD) side_job<C>(p, threadIdx.x - 64, C::THREADS - 64, blockIdx.x, gridDim.x, unit);
     for (int j = 0;; ++j) {
       const int slot = j % kSchedDepth;
-      if (!mbar_wait(&bk.sched_full[slot], (j / kSchedDepth) & 1, abort_ptr, wait_lim)) break;
+      if (!epilogue_wait<C>(&bk.sched_full[slot], (j / kSchedDepth) & 1, abort_ptr, wait_lim)) break;
       const int t = bk.sched_tile[slot];
       __syncwarp();
       if (lane == 0) mbar_arrive(&bk.sched_empty[slot]);
@@ -2066,7 +2076,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const TileInfo ti = decode_tile<C>(p, s_poff, s_tpre, t);
       [[maybe_unused]] CeRow cr{};
       if constexpr (C::CE_STATS || C::CE_GRAD) cr = ce_row<C>(p, ti.m0 + quarter * 32 + lane, unit);
-      if (!mbar_wait(&tfull_bar[acc], acc_phase, abort_ptr, wait_lim)) break;
+      if (!epilogue_wait<C>(&tfull_bar[acc], acc_phase, abort_ptr, wait_lim)) break;
       tc_fence_after_sync();
       bool released = false;                 // accumulator already handed back by the epilogue
       auto release = [&] {
@@ -2084,7 +2094,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           zl += ce_segment_label<C>(p, ti, t_acc, quarter, lane, part, cr);
           release();
           if (++acc == C::ACC_BUFS) { acc = 0; acc_phase ^= 1u; }
-          if (!mbar_wait(&tfull_bar[acc], acc_phase, abort_ptr, wait_lim)) { ok = false; break; }
+          if (!epilogue_wait<C>(&tfull_bar[acc], acc_phase, abort_ptr, wait_lim)) { ok = false; break; }
           tc_fence_after_sync();
         }
         if (!ok) break;
@@ -2374,7 +2384,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       [[maybe_unused]] CeRow cr{};
       if constexpr (C::CE_STATS || C::CE_GRAD)
         cr = ce_row<C>(p, ti.m0 + 128 * static_cast<int>(rank) + quarter * 32 + lane, unit);
-      if (!mbar_wait(&tfull_bar[acc], acc_phase, abort_ptr, wait_lim)) break;
+      if (!epilogue_wait<C>(&tfull_bar[acc], acc_phase, abort_ptr, wait_lim)) break;
       tc_fence_after_sync();
       bool released = false;
       auto release = [&] {
@@ -2401,7 +2411,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           release();
           released = false;
           if (++acc == C::ACC_BUFS) { acc = 0; acc_phase ^= 1u; }
-          if (!mbar_wait(&tfull_bar[acc], acc_phase, abort_ptr, wait_lim)) { ok = false; break; }
+          if (!epilogue_wait<C>(&tfull_bar[acc], acc_phase, abort_ptr, wait_lim)) { ok = false; break; }
           tc_fence_after_sync();
         }
         if (!ok) break;
