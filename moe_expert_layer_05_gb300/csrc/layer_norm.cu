@@ -208,6 +208,7 @@ __global__ void __launch_bounds__(512, 1) layer_norm_bwd_kernel(const uint4* __r
   __shared__ uint64_t s_full[kBwdWarps][kMaxStages];
   __shared__ float2 s_red[2][kBwdWarps];
   __shared__ int s_abort;
+  __shared__ int s_stop[kBwdWarps];      // a group's first row that started no later row's copy
   constexpr int ROWS = DSUM ? 3 : 2;
   const int words = H / 8;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -216,8 +217,10 @@ __global__ void __launch_bounds__(512, 1) layer_norm_bwd_kernel(const uint4* __r
   uint4* buf = ring + static_cast<size_t>(group) * stages * ROWS * words;
   const int t0 = blockIdx.x * groups + group, step = gridDim.x * groups;
   if (threadIdx.x == 0) {
-    for (int g = 0; g < groups; ++g)
+    for (int g = 0; g < groups; ++g) {
       for (int i = 0; i < stages; ++i) mbar_init(&s_full[g][i], 1);
+      s_stop[g] = T;
+    }
     s_abort = 0;
     fence_mbarrier_init();
   }
@@ -308,7 +311,11 @@ __global__ void __launch_bounds__(512, 1) layer_norm_bwd_kernel(const uint4* __r
       __syncwarp();
     }
     auto refill = [&] {                    // every thread of the group has read the buffer
-      if (gtid == 0 && !*static_cast<volatile int*>(&s_abort)) load(t + static_cast<long long>(stages) * step, stage);
+      if (gtid != 0) return;
+      if (!*static_cast<volatile int*>(&s_abort))
+        load(t + static_cast<long long>(stages) * step, stage);
+      else
+        s_stop[group] = min(s_stop[group], static_cast<int>(t));
     };
     if constexpr (KEEP) refill();
     // dx = rs g - rs <g> - xh rs <g xh>  (rs^2 would leave fp32 where rs does not)
@@ -350,10 +357,17 @@ __global__ void __launch_bounds__(512, 1) layer_norm_bwd_kernel(const uint4* __r
   }
   __syncthreads();
   if (s_abort) {
-    if (threadIdx.x == 0) {
-      set_status(status, kErrTimeout);
-      const unsigned long long t_end = global_timer_ns();   // copies still in flight: time to land
-      while (global_timer_ns() - t_end < 200000ull) {
+    if (threadIdx.x == 0) set_status(status, kErrTimeout);
+    if (gtid == 0 && t0 < T) {
+      // copies still on their way, of the last `stages` rows that were started:
+      // each is waited for, half a second at most
+      const int rows = (T - t0 + step - 1) / step, stop = (s_stop[group] - t0 + step - 1) / step;
+      const int started = min(rows, stop + stages);
+      for (int k = max(started - stages, 0); k < started; ++k) {
+        const unsigned long long since = global_timer_ns();
+        while (!mbar_try_wait(&s_full[group][k % stages], k / stages & 1) &&
+               global_timer_ns() - since < kWaitLimitNs / 4) {
+        }
       }
     }
     __syncthreads();
