@@ -302,10 +302,26 @@ def _tensor(t, name: str, dtype, shape) -> int:
                      f"{t.dtype} on {t.device}" + ("" if t.is_contiguous() else ", not contiguous"))
 
 
+# Sizes cross the C ABI in 32 bits; ctypes would cut a larger one off without a word.
+_MAX_SIZE = 2 ** 31 - 1
+
+
+def _fits(size: int, name: str) -> int:
+    if not -_MAX_SIZE <= size <= _MAX_SIZE:
+        raise MoeError(-1, name)
+    return size
+
+
+def _sized(*sizes: int) -> bool:
+    return all(abs(n) <= _MAX_SIZE for n in sizes)
+
+
 def _matrix(t, name: str) -> torch.Size:
     shape = t.shape
     if len(shape) != 2:
         raise ValueError(f"{name}: expected two dimensions, got {tuple(shape)}")
+    if shape[0] > _MAX_SIZE or shape[1] > _MAX_SIZE:
+        raise MoeError(-1, name)
     return shape
 
 
@@ -322,13 +338,13 @@ _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
 def moe_embedding_workspace_bytes(n: int, V: int, H: int) -> int:
-    return int(load().moe_embedding_workspace_bytes(n, V, H))
+    return int(load().moe_embedding_workspace_bytes(n, V, H)) if _sized(n, V, H) else 0
 
 
 def moe_embedding_forward(tokens, table, out, ws, scale: float = 1.0, stream=None) -> None:
     """out[i] = scale * table[tokens[i]] (bf16); a zero row where tokens[i] is -1."""
     V, H = rows = _matrix(table, "table")
-    n = tokens.numel()
+    n = _fits(tokens.numel(), "tokens")
     check(load().moe_embedding_forward(_tensor(tokens, "tokens", _I32, (n,)), n, _tensor(table, "table", _BF16, rows),
                                        V, H, scale, _tensor(out, "out", _BF16, (n, H)), _scratch(ws)[0],
                                        stream_ptr(stream)), "moe_embedding_forward")
@@ -337,7 +353,7 @@ def moe_embedding_forward(tokens, table, out, ws, scale: float = 1.0, stream=Non
 def moe_embedding_backward(tokens, dy, dtable, ws, scale: float = 1.0, base=None, stream=None) -> None:
     """dtable[v] = base[v] + scale * (sum of dy[i] over tokens[i] == v), fp32, every row written."""
     V, H = _matrix(dtable, "dtable")
-    n = tokens.numel()
+    n = _fits(tokens.numel(), "tokens")
     wp, wn = _scratch(ws)
     check(load().moe_embedding_backward(_tensor(tokens, "tokens", _I32, (n,)), n, _tensor(dy, "dy", _BF16, (n, H)), V,
                                         H, scale, None if base is None else _tensor(base, "base", _BF16, (V, H)),
@@ -360,7 +376,7 @@ def moe_layer_norm_forward(x, weight, bias, y, mean, rstd, residual=None, sum_ou
 
 
 def moe_layer_norm_workspace_bytes(T: int, H: int) -> int:
-    return int(load().moe_layer_norm_workspace_bytes(T, H))
+    return int(load().moe_layer_norm_workspace_bytes(T, H)) if _sized(T, H) else 0
 
 
 def moe_layer_norm_backward(dy, s, weight, mean, rstd, dx, dweight, dbias, ws, dsum=None, stream=None) -> None:
@@ -379,7 +395,7 @@ def moe_layer_norm_backward(dy, s, weight, mean, rstd, dx, dweight, dbias, ws, d
 
 
 def moe_cross_entropy_workspace_bytes(T: int, H: int, V: int, piece: int = 0) -> int:
-    return int(load().moe_cross_entropy_workspace_bytes(T, H, V, piece))
+    return int(load().moe_cross_entropy_workspace_bytes(T, H, V, piece)) if _sized(T, H, V, piece) else 0
 
 
 def moe_cross_entropy_forward(x, w, labels, loss, lse, ws, stream=None) -> None:
@@ -400,7 +416,7 @@ def moe_cross_entropy_backward(x, w, labels, lse, dloss, dx, dw, ws, piece: int 
     wp, wn = _scratch(ws)
     check(load().moe_cross_entropy_backward(_tensor(x, "x", _BF16, (T, H)), _tensor(w, "w", _BF16, (V, H)),
                                             _tensor(labels, "labels", _I32, (T,)), _tensor(lse, "lse", _F32, (T,)),
-                                            _tensor(dloss, "dloss", _F32, (T,)), T, H, V, piece,
+                                            _tensor(dloss, "dloss", _F32, (T,)), T, H, V, _fits(piece, "piece"),
                                             _tensor(dx, "dx", _BF16, (T, H)), _tensor(dw, "dw", _BF16, (V, H)), wp, wn,
                                             stream_ptr(stream)), "moe_cross_entropy_backward")
 
