@@ -156,10 +156,11 @@ def ptr(t) -> int | None:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def stream_ptr(stream=None) -> int | None:
+def stream_ptr(stream=None, dev: int | None = None) -> int | None:
+    """Handle of `stream`, or of the current stream of the current GPU (dev, where the caller has asked already)."""
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(torch.cuda.current_device() if dev is None else dev)
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
 
@@ -294,12 +295,23 @@ def moe_layer_backward_wgrad(cfg, weights: MoeWeights, x, dy, grads: MoeGrads, a
 
 
 # ---------------------------------------------------------------- around the layer
-def _tensor(t, name: str, dtype, shape) -> int:
-    """Device address of a contiguous CUDA tensor of this type and shape; raises ValueError otherwise."""
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _device() -> int:
+    """The current GPU, on which a call's kernels run and its tensors have to be (-2, no tensor's, without one)."""
+    try:
+        return _get_device()
+    except (RuntimeError, AssertionError):
+        return -2
+
+
+def _tensor(t, name: str, dtype, shape, dev: int) -> int:
+    """Address of a contiguous tensor of this type and shape on GPU `dev`; raises ValueError otherwise."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
         return t.data_ptr()
-    raise ValueError(f"{name}: expected a contiguous CUDA tensor {tuple(shape)} of {dtype}, got {tuple(t.shape)} of "
-                     f"{t.dtype} on {t.device}" + ("" if t.is_contiguous() else ", not contiguous"))
+    raise ValueError(f"{name}: expected a contiguous tensor {tuple(shape)} of {dtype} on the current GPU, got "
+                     f"{tuple(t.shape)} of {t.dtype} on {t.device}" + ("" if t.is_contiguous() else ", not contiguous"))
 
 
 # Sizes cross the C ABI in 32 bits; ctypes would cut a larger one off without a word.
@@ -312,8 +324,9 @@ def _fits(size: int, name: str) -> int:
     return size
 
 
-def _sized(*sizes: int) -> bool:
-    return all(abs(n) <= _MAX_SIZE for n in sizes)
+def _sized(a: int, b: int, c: int = 0, d: int = 0) -> bool:
+    return (-_MAX_SIZE <= a <= _MAX_SIZE and -_MAX_SIZE <= b <= _MAX_SIZE and -_MAX_SIZE <= c <= _MAX_SIZE
+            and -_MAX_SIZE <= d <= _MAX_SIZE)
 
 
 def _matrix(t, name: str) -> torch.Size:
@@ -325,9 +338,9 @@ def _matrix(t, name: str) -> torch.Size:
     return shape
 
 
-def _scratch(ws) -> tuple[int, int]:
-    if not ws.is_cuda or not ws.is_contiguous():
-        raise ValueError("ws: expected a contiguous CUDA tensor")
+def _scratch(ws, dev: int) -> tuple[int, int]:
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws: expected a contiguous tensor on the current GPU, got one on {ws.device}")
     nbytes = ws.numel() * ws.element_size()
     if nbytes < 256:
         raise MoeError(-4, "ws")
@@ -343,36 +356,42 @@ def moe_embedding_workspace_bytes(n: int, V: int, H: int) -> int:
 
 def moe_embedding_forward(tokens, table, out, ws, scale: float = 1.0, stream=None) -> None:
     """out[i] = scale * table[tokens[i]] (bf16); a zero row where tokens[i] is -1."""
+    dev = _device()
     V, H = rows = _matrix(table, "table")
     n = _fits(tokens.numel(), "tokens")
-    check(load().moe_embedding_forward(_tensor(tokens, "tokens", _I32, (n,)), n, _tensor(table, "table", _BF16, rows),
-                                       V, H, scale, _tensor(out, "out", _BF16, (n, H)), _scratch(ws)[0],
-                                       stream_ptr(stream)), "moe_embedding_forward")
+    check(load().moe_embedding_forward(_tensor(tokens, "tokens", _I32, (n,), dev), n,
+                                       _tensor(table, "table", _BF16, rows, dev), V, H, scale,
+                                       _tensor(out, "out", _BF16, (n, H), dev), _scratch(ws, dev)[0],
+                                       stream_ptr(stream, dev)),
+          "moe_embedding_forward")
 
 
 def moe_embedding_backward(tokens, dy, dtable, ws, scale: float = 1.0, base=None, stream=None) -> None:
     """dtable[v] = base[v] + scale * (sum of dy[i] over tokens[i] == v), fp32, every row written."""
+    dev = _device()
     V, H = _matrix(dtable, "dtable")
     n = _fits(tokens.numel(), "tokens")
-    wp, wn = _scratch(ws)
-    check(load().moe_embedding_backward(_tensor(tokens, "tokens", _I32, (n,)), n, _tensor(dy, "dy", _BF16, (n, H)), V,
-                                        H, scale, None if base is None else _tensor(base, "base", _BF16, (V, H)),
-                                        _tensor(dtable, "dtable", _F32, (V, H)), wp, wn, stream_ptr(stream)),
+    wp, wn = _scratch(ws, dev)
+    check(load().moe_embedding_backward(_tensor(tokens, "tokens", _I32, (n,), dev), n,
+                                        _tensor(dy, "dy", _BF16, (n, H), dev), V, H, scale,
+                                        None if base is None else _tensor(base, "base", _BF16, (V, H), dev),
+                                        _tensor(dtable, "dtable", _F32, (V, H), dev), wp, wn, stream_ptr(stream, dev)),
           "moe_embedding_backward")
 
 
 def moe_layer_norm_forward(x, weight, bias, y, mean, rstd, residual=None, sum_out=None, eps: float = 1e-5,
                            stream=None) -> None:
     """y = norm(s) * weight + bias with s = x + residual (written to sum_out); mean and rstd for the backward."""
+    dev = _device()
     T, H = rows = _matrix(x, "x")
-    check(load().moe_layer_norm_forward(_tensor(x, "x", _BF16, rows),
-                                        None if residual is None else _tensor(residual, "residual", _BF16, rows),
-                                        _tensor(weight, "weight", _BF16, (H,)),
-                                        None if bias is None else _tensor(bias, "bias", _BF16, (H,)),
-                                        T, H, eps, _tensor(y, "y", _BF16, rows),
-                                        None if sum_out is None else _tensor(sum_out, "sum_out", _BF16, rows),
-                                        _tensor(mean, "mean", _F32, (T,)), _tensor(rstd, "rstd", _F32, (T,)),
-                                        stream_ptr(stream)), "moe_layer_norm_forward")
+    check(load().moe_layer_norm_forward(_tensor(x, "x", _BF16, rows, dev),
+                                        None if residual is None else _tensor(residual, "residual", _BF16, rows, dev),
+                                        _tensor(weight, "weight", _BF16, (H,), dev),
+                                        None if bias is None else _tensor(bias, "bias", _BF16, (H,), dev),
+                                        T, H, eps, _tensor(y, "y", _BF16, rows, dev),
+                                        None if sum_out is None else _tensor(sum_out, "sum_out", _BF16, rows, dev),
+                                        _tensor(mean, "mean", _F32, (T,), dev), _tensor(rstd, "rstd", _F32, (T,), dev),
+                                        stream_ptr(stream, dev)), "moe_layer_norm_forward")
 
 
 def moe_layer_norm_workspace_bytes(T: int, H: int) -> int:
@@ -381,16 +400,17 @@ def moe_layer_norm_workspace_bytes(T: int, H: int) -> int:
 
 def moe_layer_norm_backward(dy, s, weight, mean, rstd, dx, dweight, dbias, ws, dsum=None, stream=None) -> None:
     """dx = the gradient of s (plus dsum, the stream's own); dweight and dbias (or None), fp32."""
+    dev = _device()
     T, H = rows = _matrix(s, "s")
-    wp, wn = _scratch(ws)
-    check(load().moe_layer_norm_backward(_tensor(dy, "dy", _BF16, rows), _tensor(s, "s", _BF16, rows),
-                                         _tensor(weight, "weight", _BF16, (H,)), _tensor(mean, "mean", _F32, (T,)),
-                                         _tensor(rstd, "rstd", _F32, (T,)),
-                                         None if dsum is None else _tensor(dsum, "dsum", _BF16, rows),
-                                         T, H, _tensor(dx, "dx", _BF16, rows),
-                                         _tensor(dweight, "dweight", _F32, (H,)),
-                                         None if dbias is None else _tensor(dbias, "dbias", _F32, (H,)), wp, wn,
-                                         stream_ptr(stream)),
+    wp, wn = _scratch(ws, dev)
+    check(load().moe_layer_norm_backward(_tensor(dy, "dy", _BF16, rows, dev), _tensor(s, "s", _BF16, rows, dev),
+                                         _tensor(weight, "weight", _BF16, (H,), dev),
+                                         _tensor(mean, "mean", _F32, (T,), dev), _tensor(rstd, "rstd", _F32, (T,), dev),
+                                         None if dsum is None else _tensor(dsum, "dsum", _BF16, rows, dev),
+                                         T, H, _tensor(dx, "dx", _BF16, rows, dev),
+                                         _tensor(dweight, "dweight", _F32, (H,), dev),
+                                         None if dbias is None else _tensor(dbias, "dbias", _F32, (H,), dev), wp, wn,
+                                         stream_ptr(stream, dev)),
           "moe_layer_norm_backward")
 
 
@@ -400,25 +420,30 @@ def moe_cross_entropy_workspace_bytes(T: int, H: int, V: int, piece: int = 0) ->
 
 def moe_cross_entropy_forward(x, w, labels, loss, lse, ws, stream=None) -> None:
     """loss[t] = lse[t] - <x[t], w[labels[t]]>, 0 where labels[t] is -1; the logits are not kept."""
+    dev = _device()
     T, H = _matrix(x, "x")
     V = _matrix(w, "w")[0]
-    wp, wn = _scratch(ws)
-    check(load().moe_cross_entropy_forward(_tensor(x, "x", _BF16, (T, H)), _tensor(w, "w", _BF16, (V, H)),
-                                           _tensor(labels, "labels", _I32, (T,)), T, H, V,
-                                           _tensor(loss, "loss", _F32, (T,)), _tensor(lse, "lse", _F32, (T,)), wp, wn,
-                                           stream_ptr(stream)), "moe_cross_entropy_forward")
+    wp, wn = _scratch(ws, dev)
+    check(load().moe_cross_entropy_forward(_tensor(x, "x", _BF16, (T, H), dev), _tensor(w, "w", _BF16, (V, H), dev),
+                                           _tensor(labels, "labels", _I32, (T,), dev), T, H, V,
+                                           _tensor(loss, "loss", _F32, (T,), dev),
+                                           _tensor(lse, "lse", _F32, (T,), dev), wp, wn, stream_ptr(stream, dev)),
+          "moe_cross_entropy_forward")
 
 
 def moe_cross_entropy_backward(x, w, labels, lse, dloss, dx, dw, ws, piece: int = 0, stream=None) -> None:
     """dx and dw (bf16) of sum_t dloss[t] * loss[t], `piece` vocabulary entries at a time (0: chosen by size)."""
+    dev = _device()
     T, H = _matrix(x, "x")
     V = _matrix(w, "w")[0]
-    wp, wn = _scratch(ws)
-    check(load().moe_cross_entropy_backward(_tensor(x, "x", _BF16, (T, H)), _tensor(w, "w", _BF16, (V, H)),
-                                            _tensor(labels, "labels", _I32, (T,)), _tensor(lse, "lse", _F32, (T,)),
-                                            _tensor(dloss, "dloss", _F32, (T,)), T, H, V, _fits(piece, "piece"),
-                                            _tensor(dx, "dx", _BF16, (T, H)), _tensor(dw, "dw", _BF16, (V, H)), wp, wn,
-                                            stream_ptr(stream)), "moe_cross_entropy_backward")
+    wp, wn = _scratch(ws, dev)
+    check(load().moe_cross_entropy_backward(_tensor(x, "x", _BF16, (T, H), dev), _tensor(w, "w", _BF16, (V, H), dev),
+                                            _tensor(labels, "labels", _I32, (T,), dev),
+                                            _tensor(lse, "lse", _F32, (T,), dev),
+                                            _tensor(dloss, "dloss", _F32, (T,), dev), T, H, V, _fits(piece, "piece"),
+                                            _tensor(dx, "dx", _BF16, (T, H), dev),
+                                            _tensor(dw, "dw", _BF16, (V, H), dev), wp, wn, stream_ptr(stream, dev)),
+          "moe_cross_entropy_backward")
 
 
 # ---------------------------------------------------------------- buffers

@@ -1,5 +1,6 @@
 """The binding's checks of the embedding, layer-norm and cross-entropy calls that
-need no GPU: sizes past 32 bits are refused, not cut off."""
+need no GPU: sizes past 32 bits are refused, not cut off; tensors of a GPU other
+than the current one are refused."""
 import pytest
 
 from moe_expert_layer_05_gb300 import api
@@ -43,7 +44,8 @@ def calls(monkeypatch):
             return lambda *a: made.append(name) or 0
 
     monkeypatch.setattr(api, "load", lambda: Library())
-    monkeypatch.setattr(api, "stream_ptr", lambda stream=None: None)
+    monkeypatch.setattr(api, "stream_ptr", lambda *a: None)
+    monkeypatch.setattr(api, "_device", lambda: 0, raising=False)
     return made
 
 
@@ -96,3 +98,30 @@ def test_workspaces_of_sizes_past_32_bits_are_zero():
     assert api.moe_layer_norm_workspace_bytes(PAST, 64) == 0 and api.moe_layer_norm_workspace_bytes(8, 2 ** 32 + 64) == 0
     assert api.moe_cross_entropy_workspace_bytes(8, 64, 8, 2 ** 32 + 256) == 0
     assert api.moe_embedding_workspace_bytes(8, 8, 64) > 0
+
+
+def test_tensors_of_another_gpu_are_refused(calls):
+    """Each tensor of each call on GPU 1 while GPU 0 is the current one, whose kernel could not read it."""
+    ws = FakeTensor(1 << 20)
+    by_call = {
+        api.moe_embedding_forward: [_i32(4), _bf(8, 64), _bf(4, 64), ws],
+        api.moe_embedding_backward: [_i32(4), _bf(4, 64), _f32(8, 64), ws],
+        api.moe_layer_norm_forward: [_bf(4, 64), _bf(64), _bf(64), _bf(4, 64), _f32(4), _f32(4)],
+        api.moe_layer_norm_backward: [_bf(4, 64), _bf(4, 64), _bf(64), _f32(4), _f32(4), _bf(4, 64), _f32(64), _f32(64),
+                                      ws],
+        api.moe_cross_entropy_forward: [_bf(4, 64), _bf(9, 64), _i32(4), _f32(4), _f32(4), ws],
+        api.moe_cross_entropy_backward: [_bf(4, 64), _bf(9, 64), _i32(4), _f32(4), _f32(4), _bf(4, 64), _bf(9, 64), ws],
+    }
+    optional = {api.moe_embedding_backward: {"base": _bf(8, 64)},
+                api.moe_layer_norm_forward: {"residual": _bf(4, 64), "sum_out": _bf(4, 64)},
+                api.moe_layer_norm_backward: {"dsum": _bf(4, 64)}}
+    for call, args in by_call.items():
+        named = optional.get(call, {})
+        call(*args, **named)
+        assert calls.pop() == call.__name__
+        for t in [*args, *named.values()]:
+            t.index = 1
+            with pytest.raises(ValueError):
+                call(*args, **named)
+            t.index = 0
+        assert calls == []
