@@ -11,8 +11,10 @@ With no --workload the run measures all five configurations one after the
 other (tiny, Mixtral-like, Qwen3-like training, DeepSeek-like bf16 forward,
 DeepSeek-like MXFP8 training) and prints one line whose headline is the
 largest, the DeepSeek-like MXFP8 training layer (T=16384, H=7168, E=256 + one
-shared expert, k=8, F=2048); the other four are complete sub-records under
-"configs".  Under torchrun (N>1) every rank runs the headline only.
+shared expert, k=8, F=2048), with the other four's rates under "configs".  The
+complete records (every grouped GEMM's roofline, the stages' times) go to the file
+that --details names.  Under torchrun (N>1) every rank runs the headline
+only.
 
 Timing: W untimed warm-up steps, then K steps, each bracketed by CUDA events on
 the launching stream, with L2 flushed (a 512 MB write) before every step outside
@@ -25,7 +27,7 @@ and set against its roofline: max(flops / tensor peak, algorithmic bytes / HBM
 bandwidth), both terms reported.  nvidia-smi samples the clocks from the first
 warm-up step to the end of the end-to-end leg.
 
-  python bench.py [--gpus N] [--steps K] [--warmup W] [--workload NAME]
+  python bench.py [--gpus N] [--steps K] [--warmup W] [--workload NAME] [--details FILE]
   python bench.py --impl reference ...   # the fp64 CPU oracle on host cores
 """
 from __future__ import annotations
@@ -821,6 +823,30 @@ def run_ours(args) -> dict | None:
     return out
 
 
+def summary(out: dict) -> dict:
+    """The line for stdout: the record without its long parts, short enough for a
+    reader that keeps only the end of a program's output (the complete record of
+    the five configurations is 27 KB)."""
+    def short(v):
+        if isinstance(v, dict):
+            return {k: short(x) for k, x in v.items()}
+        return float(f"{v:.6g}") if isinstance(v, float) else v
+
+    line = {k: v if isinstance(v, float) else short(v) for k, v in out.items()
+            if k not in ("gemm_ops", "stages_ms", "experts_with_rows", "configs", "headline")}
+    if isinstance(line.get("roofline"), dict):
+        line["roofline"] = {k: v for k, v in line["roofline"].items() if k in (
+            "bound", "kernel", "achieved", "peak", "unit", "frac", "peak_source", "traffic", "ms_per_launch",
+            "flop_per_launch", "bytes_per_launch")}
+    if isinstance(line.get("e2e"), dict):
+        line["e2e"].pop("how", None)
+    if "configs" in out:
+        line["configs"] = {name: {"value": short(r["value"]), "ms_per_step": short(r["ms_per_step"]),
+                                  "e2e": short(r["e2e"]["value"]), "dtype": r["dtype"], "pass": r["config"]["pass"]}
+                           for name, r in out["configs"].items()}
+    return line
+
+
 # ---------------------------------------------------------------- profiler captures
 PROFILE_OPS = GEMM_OPS + ("router", "permute", "combine", "step")
 
@@ -1012,6 +1038,7 @@ def main():
     ap.add_argument("--impl", choices=["ours", "reference"], default="ours")
     ap.add_argument("--workload", choices=sorted(WORKLOADS), default=None,
                     help="one workload only (default: all five configurations, headline the largest)")
+    ap.add_argument("--details", default=None, metavar="FILE", help="also write the complete record to this file")
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--no-graph", action="store_true", help="launch each timed step eagerly, not as a CUDA graph")
     ap.add_argument("--tokens", type=int, default=None,
@@ -1029,6 +1056,11 @@ def main():
     else:
         out = run_reference(args) if args.impl == "reference" else run_ours(args)
     if out is not None:
+        if args.impl == "ours" and args.profile_op is None:
+            if args.details is not None:
+                with open(args.details, "w") as f:
+                    json.dump(out, f)
+            out = summary(out)
         print(json.dumps(out), flush=True)
     world, _, _ = dist_env()
     if world > 1 and torch.distributed.is_initialized():
