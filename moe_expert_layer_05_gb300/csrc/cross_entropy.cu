@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) ce_few_grad_kernel(const uint4
   const float unit = ce_unit_of(ce, lane);
   const int label = lane < T ? ce.labels[lane] : -1;
   const bool scored = label >= 0 && label < ce.vocab;
-  const float off = scored ? ce.lse[lane] * kLog2e : 0.f, dl = scored ? ce.dloss[lane] / unit : 0.f;
+  const float lse = scored ? ce.lse[lane] : 0.f, dl = scored ? ce.dloss[lane] / unit : 0.f;
   if (blockIdx.x == 0 && xz != nullptr) {
     if (warp == 0 && !scored && label != -1) set_status(status, kErrBadIndex);
     const unsigned rows_scored = __ballot_sync(0xffffffffu, scored);
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) ce_few_grad_kernel(const uint4
     if (lane < T) {
       #pragma unroll
       for (int r = 0; r < STEP; ++r) {                  // (kTile is a multiple of STEP: v0 + r < end)
-        float g = ex2(fmaf(mine[r], kLog2e, -off));
+        float g = ex2((mine[r] - lse) * kLog2e);
         if (label == ce.v0 + v0 + r) g -= 1.f;
         g = scored && v0 + r < entries ? g * dl : 0.f;
         const __nv_bfloat16 upper = __float2bfloat16_rn(g);

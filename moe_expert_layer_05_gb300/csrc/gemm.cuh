@@ -979,8 +979,10 @@ __device__ __forceinline__ void ce_grad_tile(const GemmParams& p, const TileInfo
   const int nv = min(C::BN, p.ce.vocab - col0);
   const bool scored = cr.label >= 0 && cr.label < p.ce.vocab;
   const int rel = cr.label - col0;
-  const float off = scored ? cr.lse * kLog2e : 0.f;
-  const float dl = scored ? cr.dloss : 0.f;
+  // 2^(z log2 e - off) is off's rounding away from exp(z - lse), which dl takes back;
+  // the label's column, of which 1 is subtracted, goes by the difference itself
+  const float lse = scored ? cr.lse : 0.f, off = lse * kLog2e;
+  const float dl = scored ? cr.dloss : 0.f, dl_off = dl * ex2(-fmaf(lse, kLog2e, -off));
   const int begin = part * (C::BN / 2);
   // 32 columns of d from their logits, columns [c0, c0 + 32) of the tile, into chunks q0 .. q0 + 3 of the staged rows
   auto put32 = [&](const uint32_t (&u)[2][16], int c0, int q0, int low, [[maybe_unused]] int at) {
@@ -992,7 +994,7 @@ __device__ __forceinline__ void ce_grad_tile(const GemmParams& p, const TileInfo
       d[j] = ex2(fmaf(z, kLog2e, -off));
     }
     #pragma unroll
-    for (int j = 0; j < 32; ++j) d[j] = scored ? d[j] * dl : 0.f;
+    for (int j = 0; j < 32; ++j) d[j] = scored ? d[j] * dl_off : 0.f;
     if (c0 + 32 > nv) {
       #pragma unroll
       for (int j = 0; j < 32; ++j)
@@ -1010,7 +1012,7 @@ __device__ __forceinline__ void ce_grad_tile(const GemmParams& p, const TileInfo
   // the label's own column, where it is one of [c0, c0 + 64); then the 64 columns leave
   auto finish = [&](int c0, int low, float zl) {
     if (scored && rel >= c0 && rel < c0 + 64) {
-      const float d = (ex2(fmaf(zl, kLog2e, -off)) - 1.f) * dl;
+      const float d = (ex2((zl - lse) * kLog2e) - 1.f) * dl;
       st.put_bf16(rel - c0, low != 0 ? d - bf16_lo(pack_bf16x2(d, 0.f)) : d);
     }
     st.flush(tmC, ti.n * C::BN + c0, low != 0 ? y + p.ce.low : y);

@@ -109,6 +109,24 @@ def test_cross_entropy_gradient_of_one_or_two_sure_rows(lib, T, H, top):
     _sure_rows(T, H, top)
 
 
+@pytest.mark.parametrize("T,H", [(1, 1024), (2, 4096), (5, 1024), (140, 4096), (140, 7168)])
+def test_cross_entropy_gradient_vanishes_where_the_label_is_certain(lib, T, H):
+    """Probabilities of other entries below e^-80 V: lse is the label's logit to the bit (its sum of exponentials is
+    1 within 2^-22, the logit's place 2^-18 or more), so that entry's gradient is zero and the others' below e^-75."""
+    V = 3000
+    rng = np.random.default_rng(T + H)
+    x, lab = _bf(rng, T, H), rng.permutation(V)[:T].astype(np.int32)
+    w = _bf(rng, V, H, std=1 / np.sqrt(H)).float()
+    xf = x.float()
+    w[torch.from_numpy(lab).long()] += rng.uniform(85, 110) * xf / (xf * xf).sum(1, keepdim=True)
+    xd, wd, ld = x.to(DEV), w.to(BF).to(DEV), _dev(lab)
+    loss, lse, ws = _loss(xd, wd, ld)
+    dx, dw = _nan(T, H), _nan(V, H)
+    api.moe_cross_entropy_backward(xd, wd, ld, lse, torch.ones(T, device=DEV), dx, dw, ws)
+    assert not loss.any()
+    assert dx.abs().max() <= 1e-25 and dw.abs().max() <= 1e-25
+
+
 @pytest.mark.parametrize("T,H,V", [(4400, 64, 700), (9000, 72, 513), (1300, 16384, 300)])
 def test_cross_entropy_several_groups_of_tiles(lib, T, H, V):
     """More row blocks than one group of the tile order holds, the last group shorter than the others."""
