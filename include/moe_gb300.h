@@ -542,9 +542,14 @@ moe_status moe_cross_entropy_forward(const void* x, const void* w, const int32_t
  *   d[t,v] = dloss[t] * (exp(z[t,v] - lse[t]) - [v == labels[t]])  (0 where there is no label,
  * whatever that row of x, lse or dloss holds),  dx = d w, dw = d^T x: [T,H] and [V,H] bf16, overwritten,
  * each rounded once from fp32 sums; d itself is rounded to bf16 between the
- * products.  lse from the forward; dloss [T] fp32.  The logits are computed
- * again, `piece` vocabulary entries at a time (rounded up to 256; 0: chosen by
- * size); the workspace holds d of one piece. */
+ * products (up to 64 tokens kept in two bf16 parts).  lse from a forward call on
+ * the same T rows: the logits are added up alike then, which the gradient of a row
+ * that is sure of its label rests on; dloss [T] fp32.  The logits are computed
+ * again, `piece` vocabulary entries at a time (rounded up to 256; 0: as many as
+ * make 256 MB of d, 4096 at least).  The workspace holds d of one piece (2 bytes x
+ * T x piece, twice that up to 64 tokens), a copy of x, up to 16 fp32 [T,H] slabs
+ * of dx and, where a piece of dw has fewer than 76 tiles of 256 x 256, up to 16
+ * fp32 slabs of it. */
 moe_status moe_cross_entropy_backward(const void* x, const void* w, const int32_t* labels, const float* lse,
                                       const float* dloss, int32_t T, int32_t H, int32_t V, int32_t piece, void* dx,
                                       void* dw, void* ws, size_t ws_bytes, void* stream);

@@ -9,7 +9,7 @@
 // Forward: one tcgen05 GEMM whose epilogue reduces each half of a 256-column
 // tile of logits to a maximum and a sum of exponentials per row
 // (ce_stats_tile), and a kernel that joins the pairs in order.  The logits stay
-// in TMEM.
+// in TMEM.  Up to kFewRows tokens they are dot products instead (ce_few_kernel).
 //
 // Backward, per piece of the vocabulary: the piece's logits again, turned into
 // d in the GEMM's epilogue (ce_grad_tile) and kept for this piece only, in
@@ -27,15 +27,24 @@
 // follow one another on the stream, so the fp32 additions into a slab have one
 // order and the result does not depend on timing.
 //
+// Where a row is sure of its label, d is what is left of exp(z - lse) - 1, of the
+// size of fp32's rounding of z.  The backward therefore makes each logit by the same
+// additions as the forward: whole, in segments (kWhole), or as a dot product
+// (kFewRows); and both keep the rounding of a product with log2 e out of
+// differences.  Such rows' gradients are then as near to the exact ones as the plain
+// fp32 form's (300 rows, 1 - p of 5e-5, H from 1024 to 16384: 1.00 to 1.06 times its
+// error).
+//
 // Bound by the tensor cores where there are some hundred tokens or more, and
 // there by the power limit over many passes.  Measured on one GB300 (cuBLAS
 // bf16: 1914 TFLOP/s in a burst, 1721 sustained): forward of 8192 tokens, H =
 // 4096, 32000 entries 1.26 ms (1.70 PFLOP/s); a training step of 4096 tokens, H
 // = 4096, 131072 entries 10.4 to 10.9 ms (1.61 to 1.69 PFLOP/s: 4.4 TFLOP forward, 13.2
-// backward).  With few tokens bound by reading the weight: one token, H = 4096,
-// 32000 entries 45 us (5.8 TB/s), 131072 entries 154 us (7.0 TB/s).  Between
+// backward); at H = 7168, 4096 tokens and 32000 entries 4.7 ms (1.59), of which the
+// forward 1.12 (1.68).  With few tokens bound by reading the weight: one token, H = 4096,
+// 32000 entries 45 us (5.9 TB/s), 131072 entries 153 us (7.0 TB/s).  Between
 // them by the launches and the rounds of tiles: 1003 tokens, H = 1000, 5003
-// entries 70 us, five launches, 80 tiles on 76 CTA pairs.
+// entries 71 us, five launches, 80 tiles on 76 CTA pairs.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -51,7 +60,8 @@ constexpr int kMaxSlabs = 16;
 constexpr int kFewRows = 2;          // tokens up to which the logits are matrix-vector products
 constexpr int kFewBlocks = 304;      // their blocks: two on each SM
 
-// Elements of d kept at a time where the caller names no piece: 256 MB of bf16.
+// Elements of d kept at a time where the caller names no piece: 256 MB of bf16, but
+// pieces of kMinPiece entries at least (above 32768 tokens d is 8 KB a token).
 constexpr long long kPieceElements = 1LL << 27;
 constexpr int kMinPiece = 4096;
 
@@ -263,8 +273,8 @@ cudaError_t gemm_dw(const void* d, int ld, int T, const void* x, int H, void* dw
 // Up to kFewRows tokens the logits are matrix-vector products: the head's
 // weight is read once, in whole rows, and nothing else counts.  (The tensor
 // cores' tiles read 128 bytes of each of 256 rows at a time, which costs HBM a
-// quarter of its rate: one token, 131072 x 4096, in 190 us, against 159 here,
-// 6.7 TB/s; from four tokens on the arithmetic here takes longer than that.)
+// quarter of its rate: one token, 131072 x 4096, in 190 us, against 153 here,
+// 7.0 TB/s; from four tokens on the arithmetic here takes longer than that.)
 // A warp takes STEP entries at a time, lanes the words of their rows (two for one
 // token, one for two: 45 and 47 us at 32000 x 4096, 54 with two and two); x
 // stays in shared memory.  Lane t keeps token t's running maximum and sum; the

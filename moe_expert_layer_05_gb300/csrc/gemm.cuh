@@ -769,9 +769,6 @@ __device__ __forceinline__ void fused_combine_rows(const GemmParams& p, int y0, 
 // ---------------------------------------------------------------- cross entropy
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Statistics of one half of a tile of logits: this lane's row, columns [n BN +
-// part BN / 2, + BN / 2).  A running maximum m and sum s of 2^((z - m) log2 e), 32 columns at a
-// time; columns past the vocabulary count as -infinity.
 // What an epilogue thread needs of its row, loaded before it waits for the tile.
 struct CeRow {
   int label;      // -1: none
@@ -876,7 +873,10 @@ __device__ __forceinline__ void side_job(const GemmParams& p, int thread, int th
 // off at every step, always towards zero, so that a logit of 7168 products would
 // be 2e-5 short; with fp32 additions between segments of 2048 it is a quarter
 // of that.  The half tile's sums so far wait in registers (`kept`) while the
-// next segment fills the other accumulator.
+// next segment fills the other accumulator.  (128 sums a thread beside a tile's 32
+// columns: some 60 to 80 registers spill at the 168 that ten warps have each.  2048
+// x 7168 x 32000: 598 us for the statistics, 620 for the gradient, 1.57 and 1.52
+// PFLOP/s, where whole contractions of 4096 run at 1.73 and 1.67.)
 template <class C>
 __device__ __forceinline__ void ce_keep(uint32_t tmem_acc, int quarter, int part, bool first,
                                         float (&kept)[C::BN / 2]) {
@@ -901,6 +901,9 @@ __device__ __forceinline__ float ce_segment_label(const GemmParams& p, const Til
                         part * (C::BN / 2), C::BN / 2, lane, 0.f);
 }
 
+// Statistics of one half of a tile of logits: this lane's row, columns [n BN +
+// part BN / 2, + BN / 2).  A running maximum m and sum s of 2^((z - m) log2 e), 32 columns at a
+// time; columns past the vocabulary count as -infinity.
 // release() hands the accumulator back to the MMA warp.  It comes before the
 // row's stores: an arrive after them would wait for them to reach L2, every
 // tile.  kept, zl: the sums and the label's logit of the segments before.
