@@ -554,6 +554,63 @@ moe_status moe_cross_entropy_backward(const void* x, const void* w, const int32_
                                       const float* dloss, int32_t T, int32_t H, int32_t V, int32_t piece, void* dx,
                                       void* dw, void* ws, size_t ws_bytes, void* stream);
 
+/* --------------------------------------------------------------------------
+ * Attention between the expert layers: causal, over sequences packed into one
+ * batch, with grouped heads, and its gradient.  bf16 tensors, fp32 scores and
+ * sums.
+ * ----------------------------------------------------------------------- */
+
+/* A tensor [T, heads, width] bf16 with its own strides (in elements; the width is
+ * contiguous): parts of one buffer, as a fused projection writes them, or any other
+ * order of tokens and heads.  data 16-byte aligned; strides positive multiples of 8,
+ * below 2^38 (not looked at where the dimension has one element).  The elements of
+ * an output are all different places. */
+typedef struct {
+  void* data;
+  int64_t token_stride, head_stride;
+} moe_heads;
+
+/* T rows that hold `sequences` sequences one after the other.  Query head h goes with
+ * key-value head h / (q_heads / kv_heads).  Limits: 0 <= T <= 2^24; 0 <= sequences <=
+ * 2^24; 1 <= kv_heads, q_heads <= 1024 and a multiple of kv_heads; head_dim a multiple of
+ * 8, at most 128; scale (of the scores, 1/sqrt(head_dim) as a rule) finite, above 0. */
+typedef struct {
+  int32_t T, sequences, q_heads, kv_heads, head_dim;
+  float scale;
+} moe_attention_config;
+
+/* Workspace bytes of the two calls (0 on a bad config): the status region and 8 bytes
+ * per row and query head.  Host only. */
+size_t moe_attention_workspace_bytes(const moe_attention_config* cfg);
+
+/* out[i] = sum_j p[i,j] v[j],  p[i,j] = exp(scale <q[i], k[j]> - lse[i]), over the rows j <= i
+ * of row i's sequence;  lse[i] = log sum_j exp(scale <q[i], k[j]>).
+ * q [T,q_heads,head_dim], k and v [T,kv_heads,head_dim], out as q; lse [q_heads,T] fp32,
+ * for the backward pass.  cu_seqlens [sequences + 1] int32, device: sequence b is the
+ * rows cu_seqlens[b] .. cu_seqlens[b+1] - 1; empty ones are allowed.  Rows before the
+ * first and behind the last sequence are neither read into any result nor written.
+ * Boundaries that descend or lie outside [0, T] set MOE_ERR_BAD_INDEX on the device;
+ * the results are then unspecified, and nothing outside the tensors is touched.
+ * A value that is not finite reaches the rows that see it and no other.
+ * The probabilities are rounded to bf16 for the product with v, relative to a
+ * reference within 2^8 of their maximum.  The same bits on every run.  Uses only the
+ * status region of ws. */
+moe_status moe_attention_forward(const moe_attention_config* cfg, const moe_heads* q, const moe_heads* k,
+                                 const moe_heads* v, const int32_t* cu_seqlens, const moe_heads* out, float* lse,
+                                 void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of sum <dout, out>, from the forward's q, k, v, out and lse:  with
+ * ds[i,j] = p[i,j] (<dout[i], v[j]> - <dout[i], out[i]>),
+ *   dq[i] = scale sum_j ds[i,j] k[j],  dk[j] = scale sum_i ds[i,j] q[i],  dv[j] = sum_i p[i,j] dout[i],
+ * dk and dv summed over the query heads of the group.  Shapes as q, k, v; each
+ * rounded once from fp32 sums in a fixed order; p and ds are rounded to bf16 between
+ * the products.  Rows of no sequence are left as they were.  Where a row of dout is
+ * not finite, so are dv, dk (whole rows) of what it sees and its dq. */
+moe_status moe_attention_backward(const moe_attention_config* cfg, const moe_heads* q, const moe_heads* k,
+                                  const moe_heads* v, const int32_t* cu_seqlens, const moe_heads* out, const float* lse,
+                                  const moe_heads* dout, const moe_heads* dq, const moe_heads* dk, const moe_heads* dv,
+                                  void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

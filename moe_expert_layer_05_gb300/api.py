@@ -61,6 +61,15 @@ class MoeGemmArgs(ctypes.Structure):
                 ("qt_codes", c_vp), ("qt_scales", c_vp)]
 
 
+class MoeHeads(ctypes.Structure):
+    _fields_ = [("data", c_vp), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class MoeAttentionConfig(ctypes.Structure):
+    _fields_ = [("T", c_i32), ("sequences", c_i32), ("q_heads", c_i32), ("kv_heads", c_i32), ("head_dim", c_i32),
+                ("scale", c_f32)]
+
+
 _P = ctypes.POINTER
 _SIGS = {
     "moe_status_string": (ctypes.c_char_p, [c_i32]),
@@ -103,6 +112,12 @@ _SIGS = {
     "moe_cross_entropy_forward": (c_i32, [c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_sz, c_vp]),
     "moe_cross_entropy_backward": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp,
                                            c_vp, c_sz, c_vp]),
+    "moe_attention_workspace_bytes": (c_sz, [_P(MoeAttentionConfig)]),
+    "moe_attention_forward": (c_i32, [_P(MoeAttentionConfig), _P(MoeHeads), _P(MoeHeads), _P(MoeHeads), c_vp,
+                                      _P(MoeHeads), c_vp, c_vp, c_sz, c_vp]),
+    "moe_attention_backward": (c_i32, [_P(MoeAttentionConfig), _P(MoeHeads), _P(MoeHeads), _P(MoeHeads), c_vp,
+                                       _P(MoeHeads), c_vp, _P(MoeHeads), _P(MoeHeads), _P(MoeHeads), _P(MoeHeads),
+                                       c_vp, c_sz, c_vp]),
 }
 
 _lib = None
@@ -444,6 +459,66 @@ def moe_cross_entropy_backward(x, w, labels, lse, dloss, dx, dw, ws, piece: int 
                                             _tensor(dx, "dx", _BF16, (T, H), dev),
                                             _tensor(dw, "dw", _BF16, (V, H), dev), wp, wn, stream_ptr(stream, dev)),
           "moe_cross_entropy_backward")
+
+
+# ---------------------------------------------------------------- attention
+def _heads(t, name: str, shape, dev: int) -> MoeHeads:
+    """A [T, heads, width] bf16 tensor on GPU `dev` with a contiguous last dimension, in any order of the others."""
+    if t.dtype is not _BF16 or t.shape != shape or t.get_device() != dev or (t.stride(2) != 1 and shape[2] != 1):
+        raise ValueError(f"{name}: expected {tuple(shape)} of {_BF16} on the current GPU, its last dimension contiguous, "
+                         f"got {tuple(t.shape)} of {t.dtype} on {t.device}, strides {tuple(t.stride())}")
+    return MoeHeads(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _attention(q, k, cu_seqlens, scale, dev: int):
+    """The config of a call, and the shapes of q and of k and v."""
+    if len(q.shape) != 3 or len(k.shape) != 3:
+        raise ValueError(f"q, k: expected three dimensions, got {tuple(q.shape)} and {tuple(k.shape)}")
+    T, Hq, D = q.shape
+    Hkv, n = k.shape[1], cu_seqlens.numel() - 1
+    if n < 0:
+        raise ValueError("cu_seqlens: expected the sequences' first rows and the last one's end")
+    if not (_sized(T, Hq, Hkv, D) and _sized(n, 0)):
+        raise MoeError(-1, "q, k, cu_seqlens")
+    if scale is None:
+        scale = D ** -0.5 if D > 0 else 1.0
+    return MoeAttentionConfig(T, n, Hq, Hkv, D, scale), (T, Hq, D), (T, Hkv, D)
+
+
+def moe_attention_workspace_bytes(T: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    if not _sized(T, q_heads, kv_heads, head_dim):
+        return 0
+    return int(load().moe_attention_workspace_bytes(ctypes.byref(MoeAttentionConfig(T, 1, q_heads, kv_heads, head_dim,
+                                                                                    1.0))))
+
+
+def moe_attention_forward(q, k, v, cu_seqlens, out, lse, ws, scale: float | None = None, stream=None) -> None:
+    """Causal attention of each packed sequence; lse for the backward pass.
+
+    q, out [T, q_heads, D] and k, v [T, kv_heads, D] bf16 in any strides; cu_seqlens int32, the sequences' first
+    rows and the last one's end; lse [q_heads, T] fp32; scale 1/sqrt(D) unless given.
+    """
+    dev = _device()
+    cfg, sq, sk = _attention(q, k, cu_seqlens, scale, dev)
+    wp, wn = _scratch(ws, dev)
+    check(load().moe_attention_forward(cfg, _heads(q, "q", sq, dev), _heads(k, "k", sk, dev), _heads(v, "v", sk, dev),
+                                       _tensor(cu_seqlens, "cu_seqlens", _I32, (cfg.sequences + 1,), dev),
+                                       _heads(out, "out", sq, dev), _tensor(lse, "lse", _F32, (sq[1], sq[0]), dev),
+                                       wp, wn, stream_ptr(stream, dev)), "moe_attention_forward")
+
+
+def moe_attention_backward(q, k, v, cu_seqlens, out, lse, dout, dq, dk, dv, ws, scale: float | None = None,
+                           stream=None) -> None:
+    """dq, dk, dv of sum <dout, out>; q, k, v, out, lse (and scale) as in the forward call."""
+    dev = _device()
+    cfg, sq, sk = _attention(q, k, cu_seqlens, scale, dev)
+    wp, wn = _scratch(ws, dev)
+    check(load().moe_attention_backward(cfg, _heads(q, "q", sq, dev), _heads(k, "k", sk, dev), _heads(v, "v", sk, dev),
+                                        _tensor(cu_seqlens, "cu_seqlens", _I32, (cfg.sequences + 1,), dev),
+                                        _heads(out, "out", sq, dev), _tensor(lse, "lse", _F32, (sq[1], sq[0]), dev),
+                                        _heads(dout, "dout", sq, dev), _heads(dq, "dq", sq, dev),
+                                        _heads(dk, "dk", sk, dev), _heads(dv, "dv", sk, dev), wp, wn,
+                                        stream_ptr(stream, dev)), "moe_attention_backward")
 
 
 # ---------------------------------------------------------------- buffers

@@ -1,0 +1,1128 @@
+// Causal attention over packed sequences with grouped heads, and its gradient.
+//
+//   o[i] = sum_j p[i, j] v[j],  p[i, j] = exp(scale <q[i], k[j]> - lse[i]),  start(i) <= j <= i,
+//   lse[i] = log sum_j exp(scale <q[i], k[j]>);
+//   delta[i] = <do[i], o[i]>,  ds[i, j] = p[i, j] (<do[i], v[j]> - delta[i]),
+//   dv[j] = sum_i p[i, j] do[i],  dk[j] = scale sum_i ds[i, j] q[i],  dq[i] = scale sum_j ds[i, j] k[j],
+//
+// start(i): the first row of row i's sequence.  The rows are cut into tiles of 128
+// whatever the sequences: a tile's keys are the rows from its first row's start to its
+// own last one, and what a row does not see is masked.  So the tile list needs the
+// number of rows alone, which the host knows, and each CTA reads from cu_seqlens where
+// its own rows' sequences begin and end (row_map).  A key tile ends where the row
+// tile does, so each row finds its own key in the first tile it meets and its
+// maximum is finite from then on.
+//
+// Every product is a tcgen05.mma on 128-row tiles that TMA brings (zeros outside
+// the tensor and past the head's width); one thread issues them, and eight warps
+// work on the scores in TMEM, a thread a row.
+//
+// Values that are not finite: a product with a probability of zero is still a NaN
+// on the tensor cores.  Where a tile has masked places the operand along the
+// contraction is therefore looked through first, and what is not finite there is
+// put to zero (clean_tile); rows that do see it are given it back at the end.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+
+#include "entry_checks.h"
+#include "gemm_common.h"
+
+namespace moe {
+namespace {
+
+constexpr int kRows = 128;                 // rows of a tile
+constexpr int kArith = 256;                // threads that work on the scores
+constexpr int kThreads = kArith + 128;     // and four warps, of which one loads and one issues the products
+constexpr int kLoadWarp = kArith / 32, kMmaWarp = kLoadWarp + 1;
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kMaxTokens = 1 << 24, kMaxHeads = 1024, kMaxHeadDim = 128, kMaxSequences = 1 << 24;
+
+struct Heads {                             // [T, heads, D] bf16, strides in elements
+  __nv_bfloat16* p;
+  long long token, head;
+};
+
+struct AttnParams {
+  const int32_t* cu;       // [B + 1]
+  int B, T, Hq, Hkv, D;
+  float scale, scale2;     // scale, scale * log2 e
+  int pair_rows;           // forward: the two tiles of a CTA are rows of one head (else two heads of one group)
+  int tiles;               // tiles along the rows
+  Heads o, d0, d1;         // forward: out; gradients: dq or dk, dv
+  Heads dout;              // delta
+  float* lse;              // [Hq, T]
+  float2* stats;           // [Hq, pitch]: lse * log2 e, delta
+  long long pitch;
+  int* status;
+  unsigned long long wait_ns;
+};
+
+// ---------------------------------------------------------------- sequences
+// Where the sequences of rows r0 .. r0 + R - 1 begin and end.
+struct RowMap {
+  int first, last;         // rows of any sequence: [first, last)
+  int start, end;          // of the sequence of row r0 (last boundary <= r0); next boundary past the rows
+  uint32_t bits[8];        // boundaries at r0 + 1 .. r0 + R - 1
+};
+
+// All threads of the CTA; one pass over cu_seqlens with independent loads, however
+// many sequences.  Boundaries that do not ascend or lie outside [0, T] leave the
+// ranges inside [0, T] all the same.
+template <int R>
+__device__ __forceinline__ void row_map(const AttnParams& p, int r0, RowMap* m) {
+  if (threadIdx.x < 8) m->bits[threadIdx.x] = 0u;
+  if (threadIdx.x == 0) {
+    m->start = 0;
+    m->end = p.T;
+    m->first = max(p.cu[0], 0);
+    m->last = min(p.cu[p.B], p.T);
+  }
+  __syncthreads();
+  int lo = 0, hi = p.T;
+  for (int i = threadIdx.x; i <= p.B; i += kThreads) {
+    const int c = p.cu[i];
+    if (c <= r0)
+      lo = max(lo, c);
+    else if (c >= r0 + R)
+      hi = min(hi, c);
+    else
+      atomicOr(&m->bits[(c - r0) >> 5], 1u << ((c - r0) & 31));
+    if (blockIdx.x == 0 && (c < 0 || c > p.T || (i > 0 && p.cu[i - 1] > c))) set_status(p.status, kErrBadIndex);
+  }
+  lo = __reduce_max_sync(kFull, lo);
+  hi = __reduce_min_sync(kFull, hi);
+  if ((threadIdx.x & 31) == 0) {
+    atomicMax(&m->start, lo);
+    atomicMin(&m->end, hi);
+  }
+  __syncthreads();
+}
+__device__ __forceinline__ int start_of(const RowMap* m, int r0, int row) {
+  const int off = row - r0;
+  uint32_t b = m->bits[off >> 5] & (0xffffffffu >> (31 - (off & 31)));
+  for (int w = off >> 5;;) {
+    if (b != 0) return r0 + 32 * w + 31 - __clz(b);
+    if (--w < 0) return m->start;
+    b = m->bits[w];
+  }
+}
+__device__ __forceinline__ int end_of(const RowMap* m, int r0, int row, int words) {
+  const int off = row - r0;
+  uint32_t b = m->bits[off >> 5] & (0xfffffffeu << (off & 31));
+  for (int w = off >> 5;;) {
+    if (b != 0) return r0 + 32 * w + __ffs(b) - 1;
+    if (++w >= words) return m->end;
+    b = m->bits[w];
+  }
+}
+
+// ---------------------------------------------------------------- tiles
+template <int DP>
+struct Tile {
+  static constexpr int kBytes = kRows * DP * 2;
+  static constexpr int kChunk = kRows * 128;           // 64 columns of all rows, 128-byte swizzled
+  static constexpr int kStages = DP == 128 ? 4 : 8;    // forward: key and value tiles in flight
+  static constexpr uint32_t kScores = idesc_bf16_f32(128, 128, false, false);
+  static constexpr uint32_t kSums = idesc_bf16_f32(128, DP, false, true);
+};
+
+template <int DP>
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int head, int row) {
+  #pragma unroll
+  for (int c = 0; c < DP / 64; ++c) tma_load_3d(dst + c * Tile<DP>::kChunk, map, bar, 64 * c, head, row);
+}
+
+// D[128 x 128] = A[128 rows, DP] B[128 rows, DP]^T
+template <int DP>
+__device__ __forceinline__ void mma_scores(uint32_t d, const uint8_t* a, const uint8_t* b) {
+  const uint32_t aa = smem_u32(a), ba = smem_u32(b);
+  #pragma unroll
+  for (int c = 0; c < DP / 64; ++c)
+    #pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      const uint32_t off = c * Tile<DP>::kChunk + kk * 32;
+      mma_bf16_ss(d, smem_desc_sw128(aa + off, 16, 1024), smem_desc_sw128(ba + off, 16, 1024), Tile<DP>::kScores,
+                  (c | kk) != 0 ? 1u : 0u);
+    }
+}
+
+// D[128 x DP] (+)= W[128 x 128] B[128 rows, DP], W in TMEM: its two halves of 64 along
+// the contraction at w and w + half.
+template <int DP>
+__device__ __forceinline__ void mma_sums(uint32_t d, uint32_t w, uint32_t half, const uint8_t* b, bool add) {
+  const uint32_t ba = smem_u32(b);
+  #pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    mma_bf16_ts(d, w + (kk >> 2) * half + (kk & 3) * 8, smem_desc_sw128(ba + kk * 2048, Tile<DP>::kChunk, 1024),
+                Tile<DP>::kSums, (add || kk != 0) ? 1u : 0u);
+}
+
+// Words t, t + n, ... of a tile: what is not finite becomes zero.  True where this thread found any.
+template <int DP>
+__device__ __forceinline__ bool clean_tile(uint8_t* tile, int t, int n) {
+  uint4* w = reinterpret_cast<uint4*>(tile);
+  const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+  __nv_bfloat162 acc = zero;
+  auto add = [&](uint32_t v) { acc = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&v), zero, acc); };
+  #pragma unroll 4
+  for (int i = t; i < Tile<DP>::kBytes / 16; i += n) {
+    const uint4 v = w[i];
+    add(v.x);
+    add(v.y);
+    add(v.z);
+    add(v.w);
+  }
+  if ((*reinterpret_cast<uint32_t*>(&acc) & 0x7fff7fffu) == 0) return false;     // (a sum of zeros)
+  auto part = [](uint32_t v) {
+    if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
+    if ((v & 0x7f800000u) == 0x7f800000u) v &= 0x0000ffffu;
+    return v;
+  };
+  for (int i = t; i < Tile<DP>::kBytes / 16; i += n) {
+    const uint4 v = w[i];
+    w[i] = make_uint4(part(v.x), part(v.y), part(v.z), part(v.w));
+  }
+  fence_proxy_async_smem();
+  return true;
+}
+
+__device__ __forceinline__ float as_f(uint32_t v) { return __uint_as_float(v); }
+
+// A warp's wait: its lanes go on together or, if one has given up, not at all.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned long long ns) {
+  const bool ok = mbar_wait(bar, parity, abort, ns);
+  return __all_sync(kFull, ok) != 0;
+}
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  tc_fence_before_sync();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+// Loads that may still be on their way when a warp has given up: the last parity of each barrier.
+struct Issued {
+  uint32_t mask = 0, parity = 0;
+  __device__ __forceinline__ void note(int slot, uint32_t ph) {
+    mask |= 1u << slot;
+    parity = (parity & ~(1u << slot)) | (ph << slot);
+  }
+  __device__ __forceinline__ void drain(uint64_t* bars) const {
+    for (int s = 0; s < 32; ++s)
+      if (mask >> s & 1u) mbar_wait_drain(bars + s, parity >> s & 1u);
+  }
+};
+
+// 32 columns of this thread's row, rounded, the words below the head's width.
+__device__ __forceinline__ void store_cols(__nv_bfloat16* row, int col, int D, const float (&v)[32]) {
+  #pragma unroll
+  for (int w = 0; w < 4; ++w)
+    if (col + 8 * w < D)
+      *reinterpret_cast<uint4*>(row + col + 8 * w) =
+          make_uint4(pack_bf16x2(v[8 * w], v[8 * w + 1]), pack_bf16x2(v[8 * w + 2], v[8 * w + 3]),
+                     pack_bf16x2(v[8 * w + 4], v[8 * w + 5]), pack_bf16x2(v[8 * w + 6], v[8 * w + 7]));
+}
+
+// ---------------------------------------------------------------- forward
+// A CTA has two tiles of 128 query rows, each with four warps, and one stream of key
+// and value tiles for both: two heads of a group on the same rows, or (groups of an
+// odd size) 256 rows of one head.  The tensor cores alternate between them: while one
+// tile's scores are exponentiated, the other's products run.  TMEM: scores 128
+// columns each (their first 64 become the probabilities), sums DP columns each.
+struct FwdBook {
+  uint64_t full[8], q_full;                // (one after the other: Issued counts on it)
+  uint64_t empty[8], s_full[2], p_full[2], o_full[2], drain;
+  uint32_t tmem;
+  int abort_flag;
+  int bad_lo, bad_hi;                      // key rows of tiles in which clean_tile found something
+  RowMap map;
+};
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV, const AttnParams p) {
+  using C = Tile<DP>;
+  constexpr int ST = C::kStages;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* q_smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* ring = q_smem + 2 * C::kBytes;
+  FwdBook& bk = *reinterpret_cast<FwdBook*>(ring + ST * C::kBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 8; ++s) {
+      mbar_init(&bk.full[s], 1);
+      mbar_init(&bk.empty[s], 1);
+    }
+    mbar_init(&bk.q_full, 1);
+    for (int u = 0; u < 2; ++u) {
+      mbar_init(&bk.s_full[u], 1);
+      mbar_init(&bk.p_full[u], 4);
+      mbar_init(&bk.o_full[u], 1);
+    }
+    mbar_init(&bk.drain, 1);
+    bk.abort_flag = 0;
+    bk.bad_lo = INT_MAX;
+    bk.bad_hi = -1;
+    fence_mbarrier_init();
+    prefetch_tensormap(&tmQ);
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&bk.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  pdl_wait();
+
+  // the last tiles first: they have the longest rows of keys
+  const int per = p.pair_rows ? p.Hq : p.Hq / 2;
+  const int item = static_cast<int>(blockIdx.x) % per;
+  const int t = p.tiles - 1 - static_cast<int>(blockIdx.x) / per;
+  const int q0 = t * (p.pair_rows ? 2 * kRows : kRows);
+  row_map<2 * kRows>(p, q0, &bk.map);
+  tc_fence_after_sync();
+  const uint32_t tmem = bk.tmem;
+  volatile int* abort = &bk.abort_flag;
+  const unsigned long long lim = p.wait_ns;
+
+  // key tile i: rows [top - 128 (i + 1), top - 128 i); query tile u meets tiles [from[u], to[u])
+  const int top = q0 + (p.pair_rows ? 2 * kRows : kRows);
+  int from[2], to[2], base[2], head[2];
+  #pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    base[u] = q0 + (p.pair_rows ? kRows * u : 0);
+    head[u] = p.pair_rows ? item : 2 * item + u;
+    const int a = max(base[u], bk.map.first), b = min(base[u] + kRows, bk.map.last);
+    from[u] = p.pair_rows ? 1 - u : 0;
+    to[u] = a < b ? from[u] + (base[u] + kRows - start_of(&bk.map, q0, a) + kRows - 1) / kRows : from[u];
+  }
+  const int kv = head[0] / (p.Hq / p.Hkv);
+  const bool on0 = to[0] > from[0], on1 = to[1] > from[1];
+  const int ib = on1 ? from[1] : from[0];
+  const int n = (on0 || on1) ? max(to[0], to[1]) - ib : 0;      // key tiles of this CTA
+
+  if (n > 0 && warp == kLoadWarp) {
+    if (lane == 0) {
+      Issued got;
+      mbar_arrive_expect_tx(&bk.q_full, (on0 ? C::kBytes : 0) + (on1 ? C::kBytes : 0));
+      if (on0) load_tile<DP>(q_smem, &tmQ, &bk.q_full, head[0], base[0]);
+      if (on1) load_tile<DP>(q_smem + C::kBytes, &tmQ, &bk.q_full, head[1], base[1]);
+      got.note(8, 0);
+      bool ok = true;
+      for (int s = 0; s < 2 * n && ok; ++s) {                   // key, value, key, ...
+        const int slot = s % ST;
+        const uint32_t ph = (s / ST) & 1;
+        if (s >= ST && !mbar_wait(&bk.empty[slot], ph ^ 1u, abort, lim)) { ok = false; break; }
+        mbar_arrive_expect_tx(&bk.full[slot], C::kBytes);
+        load_tile<DP>(ring + slot * C::kBytes, (s & 1) ? &tmV : &tmK, &bk.full[slot], kv,
+                      top - kRows * (ib + (s >> 1) + 1));
+        got.note(slot, ph);
+      }
+      got.drain(bk.full);                    // (they have landed by the end, unless another warp gave up)
+    }
+  } else if (n > 0 && warp == kMmaWarp) {
+    if (lane == 0) {
+      bool any = false;
+      auto tile = [&](int s) { return ring + (s % ST) * C::kBytes; };
+      auto full = [&](int s) { return mbar_wait(&bk.full[s % ST], (s / ST) & 1, abort, lim); };
+      auto release = [&](int s) { if (s + ST < 2 * n) mma_commit(&bk.empty[s % ST]); };
+      auto in = [&](int u, int i) { return i >= from[u] && i < to[u]; };
+      auto scores = [&](int u, int s) {
+        mma_scores<DP>(tmem + 128 * u, q_smem + u * C::kBytes, tile(s));
+        mma_commit(&bk.s_full[u]);
+        any = true;
+      };
+      bool ok = mbar_wait(&bk.q_full, 0, abort, lim) && full(0);
+      if (ok) {
+        tc_fence_after_sync();
+        for (int u = 0; u < 2; ++u)
+          if (in(u, ib)) scores(u, 0);
+        release(0);
+      }
+      for (int i = ib; ok && i < ib + n; ++i) {
+        const int sk = 2 * (i - ib), sv = sk + 1;               // this key tile's and value tile's turn
+        const bool more = i + 1 < ib + n;
+        if (!full(sv) || (more && !full(sk + 2))) { ok = false; break; }
+        for (int u = 0; u < 2; ++u) {
+          if (in(u, i)) {
+            if (!mbar_wait(&bk.p_full[u], (i - from[u]) & 1, abort, lim)) { ok = false; break; }
+            tc_fence_after_sync();
+            mma_sums<DP>(tmem + 256 + DP * u, tmem + 128 * u, 32, tile(sv), i > from[u]);
+            if (i + 1 == to[u]) mma_commit(&bk.o_full[u]);
+          }
+          if (in(u, i + 1)) scores(u, sk + 2);
+        }
+        if (!ok) break;
+        release(sv);
+        if (more) release(sk + 2);
+      }
+      if (any) {                             // (TMEM is given back after them, whoever gave up)
+        mma_commit(&bk.drain);
+        mbar_wait_drain(&bk.drain, 0);
+      }
+    }
+  } else if (n > 0 && warp < kLoadWarp) {
+    // ------------------------------------------------ a thread a row
+    const int u = warp >> 2;
+    const int f = u ? from[1] : from[0], e = u ? to[1] : to[0], r0 = u ? base[1] : base[0], h = u ? head[1] : head[0];
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + 128 * u + lanes, to_ = tmem + 256 + DP * u + lanes;
+    const int row = r0 + (warp & 3) * 32 + lane;
+    const bool valid = row >= bk.map.first && row < bk.map.last;
+    const int key_lo = valid ? start_of(&bk.map, q0, row) : INT_MIN / 2, key_hi = valid ? row : INT_MAX / 2;
+    // keys from here on are seen by every row of the tile (up to the diagonal)
+    const int all_from = e > f ? start_of(&bk.map, q0, min(r0 + kRows, bk.map.last) - 1) : 0;
+    const int other_from = u ? from[0] : from[1], other_to = u ? to[0] : to[1];
+    const int other_all = other_to > other_from ?
+        start_of(&bk.map, q0, min((u ? base[0] : base[1]) + kRows, bk.map.last) - 1) : 0;
+    // probabilities are relative to a reference that follows the maximum once it is 2^8 above
+    const float slack = 8.f / p.scale2;
+    float ref = -INFINITY, sum = 0.f;
+    bool ok = true;
+    for (int i = f; i < e; ++i) {
+      if (!warp_wait(&bk.s_full[u], (i - f) & 1, abort, lim)) { ok = false; break; }
+      tc_fence_after_sync();
+      uint32_t s[4][32];
+      #pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld_x32(ts + 32 * c, s[c]);
+      #pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld_wait(s[c]);
+      const int k0 = top - kRows * (i + 1);
+      const bool masked = i == f || k0 < all_from;
+      if (masked) {
+        const int lo = key_lo - k0, hi = key_hi - k0;
+        #pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c < lo || c > hi) s[c >> 5][c & 31] = 0xff800000u;
+      }
+      float mx[4];
+      #pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        mx[c] = as_f(s[c][0]);
+        #pragma unroll
+        for (int j = 1; j < 32; ++j) mx[c] = fmaxf(mx[c], as_f(s[c][j]));
+      }
+      const float m = fmaxf(ref, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+      if (i == f) {
+        ref = m;
+      } else {
+        const bool grow = m > ref + slack;
+        if (__any_sync(kFull, grow)) {
+          // (this tile's s_full came after the sums so far)
+          const float a = grow ? ex2((ref - m) * p.scale2) : 1.f;
+          if (grow) ref = m;
+          sum *= a;
+          #pragma unroll
+          for (int c = 0; c < DP / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld_x32(to_ + 32 * c, o);
+            tmem_ld_wait(o);
+            #pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(as_f(o[j]) * a);
+            tmem_st_x32(to_ + 32 * c, o);
+          }
+        }
+      }
+      const float off = ref == -INFINITY ? 0.f : -ref * p.scale2;
+      const F32x2 off2 = make_f32x2(off, off), mul2_ = make_f32x2(p.scale2, p.scale2);
+      F32x2 part[4];
+      #pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w[16];
+        part[c] = make_f32x2(0.f, 0.f);
+        #pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float2 x = split_f32x2(fma2(make_f32x2(as_f(s[c][2 * j]), as_f(s[c][2 * j + 1])), mul2_, off2));
+          const F32x2 q = make_f32x2(ex2(x.x), ex2(x.y));
+          part[c] = add2(part[c], q);
+          w[j] = pack_bf16x2(q);
+        }
+        tmem_st_x16(ts + 16 * c, w);
+      }
+      const float2 total = split_f32x2(add2(add2(part[0], part[1]), add2(part[2], part[3])));
+      sum += total.x + total.y;
+      // One tile of rows looks through the values for both, before any product takes them.
+      const bool both = i >= other_from && i < other_to;
+      if ((masked || (both && (i == other_from || k0 < other_all))) && (u == 0 || !both)) {
+        const int turn = 2 * (i - ib) + 1;
+        if (!warp_wait(&bk.full[turn % ST], (turn / ST) & 1, abort, lim)) { ok = false; break; }
+        if (clean_tile<DP>(ring + (turn % ST) * C::kBytes, threadIdx.x & 127, 128)) {
+          atomicMin(&bk.bad_lo, k0);
+          atomicMax(&bk.bad_hi, k0 + kRows - 1);
+        }
+      }
+      tmem_st_wait();
+      warp_arrive(&bk.p_full[u], lane);
+    }
+    if (ok && e > f && warp_wait(&bk.o_full[u], 0, abort, lim)) {
+      tc_fence_after_sync();
+      const float inv = 1.f / sum;
+      const int bad_lo = *const_cast<volatile int*>(&bk.bad_lo), bad_hi = *const_cast<volatile int*>(&bk.bad_hi);
+      __nv_bfloat16* out = p.o.p + row * p.o.token + h * p.o.head;
+      #pragma unroll 1
+      for (int c = 0; c < DP / 32; ++c) {
+        uint32_t o[32];
+        float v[32];
+        tmem_ld_x32(to_ + 32 * c, o);
+        tmem_ld_wait(o);
+        #pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = as_f(o[j]) * inv;
+        if (valid) {
+          // what clean_tile took out, for the rows that see it
+          for (int j = max(key_lo, bad_lo); j <= min(key_hi, bad_hi); ++j) {
+            const __nv_bfloat16* src = p.d0.p + j * p.d0.token + kv * p.d0.head + 32 * c;
+            #pragma unroll
+            for (int x = 0; x < 32; ++x) {
+              const float y = 32 * c + x < p.D ? __bfloat162float(src[x]) : 0.f;
+              if (!isfinite(y)) v[x] += y;
+            }
+          }
+          store_cols(out, 32 * c, p.D, v);
+        }
+      }
+      if (valid) p.lse[static_cast<long long>(h) * p.T + row] = (ref == -INFINITY ? 0.f : ref * p.scale) + logf(sum);
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  pdl_launch_next();
+  if (threadIdx.x == 0 && bk.abort_flag) set_status(p.status, kErrTimeout);
+  if (warp == kMmaWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- gradients
+// stats[h, i] = (lse log2 e, <do, o>) of each row; 16 lanes a row.
+__global__ void __launch_bounds__(256) attention_stats_kernel(const AttnParams p) {
+  pdl_entry();
+  const int first = max(p.cu[0], 0), last = min(p.cu[p.B], p.T);
+  const int part = threadIdx.x & 15;
+  const long long n = static_cast<long long>(p.T) * p.Hq;
+  const long long step = static_cast<long long>(gridDim.x) * 16;
+  for (long long r0 = static_cast<long long>(blockIdx.x) * 16; r0 < n; r0 += step) {
+    const long long r = r0 + (threadIdx.x >> 4);
+    const int row = static_cast<int>(r / p.Hq), h = static_cast<int>(r % p.Hq);
+    const bool valid = r < n && row >= first && row < last;
+    float d = 0.f;
+    if (valid && 8 * part < p.D) {
+      const uint4 a = *reinterpret_cast<const uint4*>(p.o.p + row * p.o.token + h * p.o.head + 8 * part);
+      const uint4 b = *reinterpret_cast<const uint4*>(p.dout.p + row * p.dout.token + h * p.dout.head + 8 * part);
+      d = bf16_lo(a.x) * bf16_lo(b.x) + bf16_hi(a.x) * bf16_hi(b.x) + bf16_lo(a.y) * bf16_lo(b.y) +
+          bf16_hi(a.y) * bf16_hi(b.y) + bf16_lo(a.z) * bf16_lo(b.z) + bf16_hi(a.z) * bf16_hi(b.z) +
+          bf16_lo(a.w) * bf16_lo(b.w) + bf16_hi(a.w) * bf16_hi(b.w);
+    }
+    #pragma unroll
+    for (int m = 8; m > 0; m >>= 1) d += __shfl_xor_sync(kFull, d, m);
+    if (valid && part == 0)
+      p.stats[h * p.pitch + row] = make_float2(p.lse[static_cast<long long>(h) * p.T + row] * kLog2e, d);
+  }
+}
+
+// dq: 128 query rows of one head against their key tiles.  TMEM: dq DP columns from 0,
+// two score buffers at 128 and 256, dp at 384 (which becomes ds).  The scores of the
+// next key tile run while this one's ds is worked out.
+struct DqBook {
+  uint64_t q_full, k_full[2], v_full[2];
+  uint64_t k_empty[2], v_empty[2], s_full[2], dp_full, ds_full, done;
+  uint32_t tmem;
+  int abort_flag;
+  RowMap map;
+};
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDo,
+                        const AttnParams p) {
+  using C = Tile<DP>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* q_smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* do_smem = q_smem + C::kBytes;
+  uint8_t* k_smem = do_smem + C::kBytes;
+  uint8_t* v_smem = k_smem + 2 * C::kBytes;
+  DqBook& bk = *reinterpret_cast<DqBook*>(v_smem + 2 * C::kBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(&bk.q_full, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bk.k_full[s], 1);
+      mbar_init(&bk.v_full[s], 1);
+      mbar_init(&bk.k_empty[s], 1);
+      mbar_init(&bk.v_empty[s], 1);
+      mbar_init(&bk.s_full[s], 1);
+    }
+    mbar_init(&bk.dp_full, 1);
+    mbar_init(&bk.ds_full, 8);
+    mbar_init(&bk.done, 1);
+    bk.abort_flag = 0;
+    fence_mbarrier_init();
+    prefetch_tensormap(&tmQ);
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+    prefetch_tensormap(&tmDo);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&bk.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  pdl_wait();
+  const int h = static_cast<int>(blockIdx.x) % p.Hq;
+  const int q0 = (p.tiles - 1 - static_cast<int>(blockIdx.x) / p.Hq) * kRows;
+  row_map<kRows>(p, q0, &bk.map);
+  tc_fence_after_sync();
+  const uint32_t tmem = bk.tmem;
+  volatile int* abort = &bk.abort_flag;
+  const unsigned long long lim = p.wait_ns;
+  const int kv = h / (p.Hq / p.Hkv), top = q0 + kRows;
+  const int a = max(q0, bk.map.first), b = min(top, bk.map.last);
+  const int n = a < b ? (top - start_of(&bk.map, q0, a) + kRows - 1) / kRows : 0;
+
+  if (n > 0 && warp == kLoadWarp) {
+    if (lane == 0) {
+      Issued got;
+      mbar_arrive_expect_tx(&bk.q_full, 2 * C::kBytes);
+      load_tile<DP>(q_smem, &tmQ, &bk.q_full, h, q0);
+      load_tile<DP>(do_smem, &tmDo, &bk.q_full, h, q0);
+      got.note(0, 0);
+      bool ok = true;
+      for (int j = 0; j < n && ok; ++j) {
+        const int s = j & 1, row = top - kRows * (j + 1);
+        const uint32_t ph = (j >> 1) & 1;
+        if (j >= 2 && !mbar_wait(&bk.k_empty[s], ph ^ 1u, abort, lim)) { ok = false; break; }
+        mbar_arrive_expect_tx(&bk.k_full[s], C::kBytes);
+        load_tile<DP>(k_smem + s * C::kBytes, &tmK, &bk.k_full[s], kv, row);
+        got.note(1 + s, ph);
+        if (j >= 2 && !mbar_wait(&bk.v_empty[s], ph ^ 1u, abort, lim)) { ok = false; break; }
+        mbar_arrive_expect_tx(&bk.v_full[s], C::kBytes);
+        load_tile<DP>(v_smem + s * C::kBytes, &tmV, &bk.v_full[s], kv, row);
+        got.note(3 + s, ph);
+      }
+      got.drain(&bk.q_full);
+    }
+  } else if (n > 0 && warp == kMmaWarp) {
+    if (lane == 0) {
+      bool any = false;
+      auto scores = [&](int j) {
+        if (!mbar_wait(&bk.k_full[j & 1], (j >> 1) & 1, abort, lim)) return false;
+        tc_fence_after_sync();
+        mma_scores<DP>(tmem + 128 + 128 * (j & 1), q_smem, k_smem + (j & 1) * C::kBytes);
+        mma_commit(&bk.s_full[j & 1]);
+        any = true;
+        return true;
+      };
+      auto dprob = [&](int j) {
+        if (!mbar_wait(&bk.v_full[j & 1], (j >> 1) & 1, abort, lim)) return false;
+        tc_fence_after_sync();
+        mma_scores<DP>(tmem + 384, do_smem, v_smem + (j & 1) * C::kBytes);
+        mma_commit(&bk.dp_full);
+        if (j + 2 < n) mma_commit(&bk.v_empty[j & 1]);
+        return true;
+      };
+      bool ok = mbar_wait(&bk.q_full, 0, abort, lim) && scores(0) && dprob(0);
+      for (int j = 0; ok && j < n; ++j) {
+        if (j + 1 < n && !scores(j + 1)) { ok = false; break; }
+        if (!mbar_wait(&bk.ds_full, j & 1, abort, lim)) { ok = false; break; }
+        tc_fence_after_sync();
+        mma_sums<DP>(tmem, tmem + 384, 64, k_smem + (j & 1) * C::kBytes, j > 0);
+        if (j + 2 < n) mma_commit(&bk.k_empty[j & 1]);
+        if (j + 1 < n && !dprob(j + 1)) { ok = false; break; }
+      }
+      if (any) {
+        mma_commit(&bk.done);
+        mbar_wait_drain(&bk.done, 0);
+      }
+    }
+  } else if (n > 0 && warp < kLoadWarp) {
+    // a thread a row, the two groups of four warps each half of the keys
+    const int half = warp >> 2;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int row = q0 + (warp & 3) * 32 + lane;
+    const bool valid = row >= bk.map.first && row < bk.map.last;
+    const int key_lo = valid ? start_of(&bk.map, q0, row) : p.T, key_hi = valid ? row : -1;
+    const int all_from = start_of(&bk.map, q0, b - 1);
+    const float2 st = valid ? p.stats[h * p.pitch + row] : make_float2(0.f, 0.f);
+    const F32x2 lse2 = make_f32x2(-st.x, -st.x), delta2 = make_f32x2(-st.y, -st.y);
+    const F32x2 mul2_ = make_f32x2(p.scale2, p.scale2);
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      if (!warp_wait(&bk.s_full[j & 1], (j >> 1) & 1, abort, lim)) { ok = false; break; }
+      tc_fence_after_sync();
+      const int k0 = top - kRows * (j + 1);
+      const bool masked = j == 0 || k0 < all_from;
+      const int lo = max(key_lo, k0) - k0 - 64 * half, hi = min(key_hi, k0 + kRows) - k0 - 64 * half;
+      uint32_t s[2][32];
+      #pragma unroll
+      for (int c = 0; c < 2; ++c) tmem_ld_x32(tmem + lanes + 128 + 128 * (j & 1) + 64 * half + 32 * c, s[c]);
+      #pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        tmem_ld_wait(s[c]);
+        #pragma unroll
+        for (int x = 0; x < 32; x += 2) {
+          const float2 y = split_f32x2(fma2(make_f32x2(as_f(s[c][x]), as_f(s[c][x + 1])), mul2_, lse2));
+          s[c][x] = __float_as_uint(ex2(y.x));
+          s[c][x + 1] = __float_as_uint(ex2(y.y));
+        }
+      }
+      if (masked) {
+        if (!warp_wait(&bk.k_full[j & 1], (j >> 1) & 1, abort, lim)) { ok = false; break; }
+        clean_tile<DP>(k_smem + (j & 1) * C::kBytes, threadIdx.x, kArith);
+      }
+      if (!warp_wait(&bk.dp_full, j & 1, abort, lim)) { ok = false; break; }
+      tc_fence_after_sync();
+      uint32_t w[32];
+      #pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t d[32];
+        tmem_ld_x32(tmem + lanes + 384 + 64 * half + 32 * c, d);
+        tmem_ld_wait(d);
+        #pragma unroll
+        for (int x = 0; x < 32; x += 2) {
+          float2 y = split_f32x2(mul2(make_f32x2(as_f(s[c][x]), as_f(s[c][x + 1])),
+                                      add2(make_f32x2(as_f(d[x]), as_f(d[x + 1])), delta2)));
+          if (masked) {
+            if (32 * c + x < lo || 32 * c + x > hi) y.x = 0.f;
+            if (32 * c + x + 1 < lo || 32 * c + x + 1 > hi) y.y = 0.f;
+          }
+          w[16 * c + x / 2] = pack_bf16x2(y.x, y.y);
+        }
+      }
+      tmem_st_x32(tmem + lanes + 384 + 64 * half, w);
+      tmem_st_wait();
+      warp_arrive(&bk.ds_full, lane);
+    }
+    if (ok && warp_wait(&bk.done, 0, abort, lim)) {
+      tc_fence_after_sync();
+      __nv_bfloat16* out = p.d0.p + row * p.d0.token + h * p.d0.head;
+      #pragma unroll
+      for (int c = 0; c < DP / 64; ++c) {
+        const int col = half * (DP / 2) + 32 * c;
+        uint32_t o[32];
+        float v[32];
+        tmem_ld_x32(tmem + lanes + col, o);
+        tmem_ld_wait(o);
+        #pragma unroll
+        for (int x = 0; x < 32; ++x) v[x] = as_f(o[x]) * p.scale;
+        if (valid) store_cols(out, col, p.D, v);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  pdl_launch_next();
+  if (threadIdx.x == 0 && bk.abort_flag) set_status(p.status, kErrTimeout);
+  if (warp == kMmaWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// dk and dv: 128 key rows of one key-value head against the query tiles of every head of
+// its group, so that the group's sum is a sum in TMEM.  Scores transposed (a thread a
+// key), so that the probabilities lie in TMEM as the A operand of the sums.  TMEM: dk, dv
+// DP columns from 0 and 128, scores at 256 (which become p), dp at 384 (ds).  In the
+// order dv(j), scores(j + 1), dk(j), dp(j + 1) each buffer is free again when its turn
+// comes, and the arithmetic on one has the time of two products.
+struct DkvBook {
+  uint64_t kv_full, q_full[2], do_full[2];
+  uint64_t q_empty[2], do_empty[2], s_full, p_full, dp_full, ds_full, done;
+  uint32_t tmem;
+  int abort_flag;
+  RowMap map;
+};
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDo,
+                         const AttnParams p) {
+  using C = Tile<DP>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* k_smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* v_smem = k_smem + C::kBytes;
+  uint8_t* q_smem = v_smem + C::kBytes;
+  uint8_t* do_smem = q_smem + 2 * C::kBytes;
+  float2* st_smem = reinterpret_cast<float2*>(do_smem + 2 * C::kBytes);        // [2][128]
+  DkvBook& bk = *reinterpret_cast<DkvBook*>(st_smem + 2 * kRows);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(&bk.kv_full, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bk.q_full[s], 1);
+      mbar_init(&bk.do_full[s], 1);
+      mbar_init(&bk.q_empty[s], 1);
+      mbar_init(&bk.do_empty[s], 1);
+    }
+    mbar_init(&bk.s_full, 1);
+    mbar_init(&bk.p_full, 8);
+    mbar_init(&bk.dp_full, 1);
+    mbar_init(&bk.ds_full, 8);
+    mbar_init(&bk.done, 1);
+    bk.abort_flag = 0;
+    fence_mbarrier_init();
+    prefetch_tensormap(&tmQ);
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+    prefetch_tensormap(&tmDo);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&bk.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  pdl_wait();
+  const int kv = static_cast<int>(blockIdx.x) % p.Hkv, k0 = static_cast<int>(blockIdx.x) / p.Hkv * kRows;
+  row_map<kRows>(p, k0, &bk.map);
+  tc_fence_after_sync();
+  const uint32_t tmem = bk.tmem;
+  volatile int* abort = &bk.abort_flag;
+  const unsigned long long lim = p.wait_ns;
+  const int group = p.Hq / p.Hkv;
+  // query tiles k0, k0 + 128, ... up to the end of the last key's sequence, for each head
+  const int a = max(k0, bk.map.first), b = min(k0 + kRows, bk.map.last);
+  const int end = a < b ? end_of(&bk.map, k0, b - 1, kRows / 32) : k0;
+  const int nq = a < b ? (end - k0 + kRows - 1) / kRows : 0, n = nq * group;
+
+  if (n > 0 && warp == kLoadWarp) {
+    if (lane == 0) {
+      Issued got;
+      mbar_arrive_expect_tx(&bk.kv_full, 2 * C::kBytes);
+      load_tile<DP>(k_smem, &tmK, &bk.kv_full, kv, k0);
+      load_tile<DP>(v_smem, &tmV, &bk.kv_full, kv, k0);
+      got.note(0, 0);
+      bool ok = true;
+      int h = kv * group, row = k0;
+      for (int j = 0; j < n && ok; ++j) {
+        const int s = j & 1;
+        const uint32_t ph = (j >> 1) & 1;
+        if (j >= 2 && !mbar_wait(&bk.q_empty[s], ph ^ 1u, abort, lim)) { ok = false; break; }
+        mbar_arrive_expect_tx(&bk.q_full[s], C::kBytes + kRows * sizeof(float2));
+        load_tile<DP>(q_smem + s * C::kBytes, &tmQ, &bk.q_full[s], h, row);
+        bulk_load(st_smem + s * kRows, p.stats + h * p.pitch + row, kRows * sizeof(float2), &bk.q_full[s]);
+        got.note(1 + s, ph);
+        if (j >= 2 && !mbar_wait(&bk.do_empty[s], ph ^ 1u, abort, lim)) { ok = false; break; }
+        mbar_arrive_expect_tx(&bk.do_full[s], C::kBytes);
+        load_tile<DP>(do_smem + s * C::kBytes, &tmDo, &bk.do_full[s], h, row);
+        got.note(3 + s, ph);
+        row += kRows;
+        if (row >= k0 + nq * kRows) {
+          row = k0;
+          ++h;
+        }
+      }
+      got.drain(&bk.kv_full);
+    }
+  } else if (n > 0 && warp == kMmaWarp) {
+    if (lane == 0) {
+      bool any = false;
+      auto scores = [&](int j) {
+        if (!mbar_wait(&bk.q_full[j & 1], (j >> 1) & 1, abort, lim)) return false;
+        tc_fence_after_sync();
+        mma_scores<DP>(tmem + 256, k_smem, q_smem + (j & 1) * C::kBytes);
+        mma_commit(&bk.s_full);
+        any = true;
+        return true;
+      };
+      auto dprob = [&](int j) {
+        if (!mbar_wait(&bk.do_full[j & 1], (j >> 1) & 1, abort, lim)) return false;
+        tc_fence_after_sync();
+        mma_scores<DP>(tmem + 384, v_smem, do_smem + (j & 1) * C::kBytes);
+        mma_commit(&bk.dp_full);
+        return true;
+      };
+      bool ok = mbar_wait(&bk.kv_full, 0, abort, lim) && scores(0) && dprob(0);
+      for (int j = 0; ok && j < n; ++j) {
+        if (!mbar_wait(&bk.p_full, j & 1, abort, lim)) { ok = false; break; }
+        tc_fence_after_sync();
+        mma_sums<DP>(tmem + 128, tmem + 256, 64, do_smem + (j & 1) * C::kBytes, j > 0);
+        if (j + 2 < n) mma_commit(&bk.do_empty[j & 1]);
+        if (j + 1 < n && !scores(j + 1)) { ok = false; break; }
+        if (!mbar_wait(&bk.ds_full, j & 1, abort, lim)) { ok = false; break; }
+        tc_fence_after_sync();
+        mma_sums<DP>(tmem, tmem + 384, 64, q_smem + (j & 1) * C::kBytes, j > 0);
+        if (j + 2 < n) mma_commit(&bk.q_empty[j & 1]);
+        if (j + 1 < n && !dprob(j + 1)) { ok = false; break; }
+      }
+      if (any) {
+        mma_commit(&bk.done);
+        mbar_wait_drain(&bk.done, 0);
+      }
+    }
+  } else if (n > 0 && warp < kLoadWarp) {
+    // a thread a key, the two groups of four warps each half of the queries
+    const int half = warp >> 2;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int key = k0 + (warp & 3) * 32 + lane;
+    const bool valid = key >= bk.map.first && key < bk.map.last;
+    const int key_end = valid ? end_of(&bk.map, k0, key, kRows / 32) : INT_MAX;
+    const int all_to = end_of(&bk.map, k0, a, kRows / 32);      // queries up to here see every key (from the diagonal)
+    const F32x2 mul2_ = make_f32x2(p.scale2, p.scale2);
+    bool ok = true;
+    int q0 = k0;
+    for (int j = 0; j < n; ++j) {
+      if (!warp_wait(&bk.q_full[j & 1], (j >> 1) & 1, abort, lim) || !warp_wait(&bk.s_full, j & 1, abort, lim)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after_sync();
+      const bool masked = q0 == k0 || q0 + kRows > all_to;
+      const int lo = max(key, q0) - q0 - 64 * half, hi = min(key_end, q0 + kRows) - q0 - 64 * half;   // queries [lo, hi)
+      const float4* st = reinterpret_cast<const float4*>(st_smem + (j & 1) * kRows + 64 * half);
+      uint32_t s[2][32];
+      #pragma unroll
+      for (int c = 0; c < 2; ++c) tmem_ld_x32(tmem + lanes + 256 + 64 * half + 32 * c, s[c]);
+      uint32_t w[32];
+      #pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        tmem_ld_wait(s[c]);
+        #pragma unroll
+        for (int x = 0; x < 32; x += 2) {
+          const float4 a4 = st[16 * c + x / 2];       // (lse2, delta) of two queries
+          float2 y = split_f32x2(fma2(make_f32x2(as_f(s[c][x]), as_f(s[c][x + 1])), mul2_, make_f32x2(-a4.x, -a4.z)));
+          y.x = ex2(y.x);
+          y.y = ex2(y.y);
+          s[c][x] = __float_as_uint(y.x);
+          s[c][x + 1] = __float_as_uint(y.y);
+          if (masked) {
+            // (a query whose do is not finite has no finite delta: what it sees keeps that)
+            y.x = (32 * c + x < lo || 32 * c + x >= hi) ? 0.f : fmaf(0.f, a4.y, y.x);
+            y.y = (32 * c + x + 1 < lo || 32 * c + x + 1 >= hi) ? 0.f : fmaf(0.f, a4.w, y.y);
+          }
+          w[16 * c + x / 2] = pack_bf16x2(y.x, y.y);
+        }
+      }
+      tmem_st_x32(tmem + lanes + 256 + 64 * half, w);
+      if (masked) {
+        if (!warp_wait(&bk.do_full[j & 1], (j >> 1) & 1, abort, lim)) { ok = false; break; }
+        clean_tile<DP>(do_smem + (j & 1) * C::kBytes, threadIdx.x, kArith);
+        clean_tile<DP>(q_smem + (j & 1) * C::kBytes, threadIdx.x, kArith);
+      }
+      tmem_st_wait();
+      warp_arrive(&bk.p_full, lane);
+      if (!warp_wait(&bk.dp_full, j & 1, abort, lim)) { ok = false; break; }
+      tc_fence_after_sync();
+      #pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t d[32];
+        tmem_ld_x32(tmem + lanes + 384 + 64 * half + 32 * c, d);
+        tmem_ld_wait(d);
+        #pragma unroll
+        for (int x = 0; x < 32; x += 2) {
+          const float4 a4 = st[16 * c + x / 2];
+          float2 y = split_f32x2(mul2(make_f32x2(as_f(s[c][x]), as_f(s[c][x + 1])),
+                                      add2(make_f32x2(as_f(d[x]), as_f(d[x + 1])), make_f32x2(-a4.y, -a4.w))));
+          if (masked) {
+            if (32 * c + x < lo || 32 * c + x >= hi) y.x = 0.f;
+            if (32 * c + x + 1 < lo || 32 * c + x + 1 >= hi) y.y = 0.f;
+          }
+          w[16 * c + x / 2] = pack_bf16x2(y.x, y.y);
+        }
+      }
+      tmem_st_x32(tmem + lanes + 384 + 64 * half, w);
+      tmem_st_wait();
+      warp_arrive(&bk.ds_full, lane);
+      q0 += kRows;
+      if (q0 >= k0 + nq * kRows) q0 = k0;
+    }
+    if (ok && warp_wait(&bk.done, 0, abort, lim)) {
+      tc_fence_after_sync();
+      // the first four warps store dk, the others dv
+      const Heads& to = half == 0 ? p.d0 : p.d1;
+      const float mul = half == 0 ? p.scale : 1.f;
+      __nv_bfloat16* out = to.p + key * to.token + kv * to.head;
+      #pragma unroll
+      for (int c = 0; c < DP / 32; ++c) {
+        uint32_t o[32];
+        float v[32];
+        tmem_ld_x32(tmem + lanes + 128 * half + 32 * c, o);
+        tmem_ld_wait(o);
+        #pragma unroll
+        for (int x = 0; x < 32; ++x) v[x] = as_f(o[x]) * mul;
+        if (valid) store_cols(out, 32 * c, p.D, v);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  pdl_launch_next();
+  if (threadIdx.x == 0 && bk.abort_flag) set_status(p.status, kErrTimeout);
+  if (warp == kMmaWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- host
+template <int DP>
+constexpr int fwd_smem() { return 1024 + (2 + Tile<DP>::kStages) * Tile<DP>::kBytes + static_cast<int>(sizeof(FwdBook)); }
+template <int DP>
+constexpr int dq_smem() { return 1024 + 6 * Tile<DP>::kBytes + static_cast<int>(sizeof(DqBook)); }
+template <int DP>
+constexpr int dkv_smem() {
+  return 1024 + 6 * Tile<DP>::kBytes + 2 * kRows * static_cast<int>(sizeof(float2)) + static_cast<int>(sizeof(DkvBook));
+}
+static_assert(fwd_smem<128>() <= 232448 && dq_smem<128>() <= 232448 && dkv_smem<128>() <= 232448, "shared memory");
+
+template <class... KArgs, class... Args>
+cudaError_t launch_big(void (*kern)(KArgs...), std::atomic<bool>* attr_set, int grid, int smem, cudaStream_t st,
+                       Args&&... args) {
+  const int dev = current_device();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    attr_set[dev].store(true, std::memory_order_release);
+  }
+  count_launches(1);
+  return launch_k(kern, grid, kThreads, smem, st, args...);
+}
+
+// How a tensor's strides count where a dimension has one element: as if it were dense.
+Heads heads_of(const moe_heads* t, int T, int heads, int D) {
+  Heads h;
+  h.p = static_cast<__nv_bfloat16*>(t->data);
+  h.head = heads > 1 ? t->head_stride : D;
+  h.token = T > 1 ? t->token_stride : (heads > 1 ? static_cast<long long>(heads) * h.head : D);
+  return h;
+}
+bool stride_ok(long long s) { return s > 0 && s % 8 == 0 && s < (1LL << 38); }
+bool heads_ok(const moe_heads* t, int T, int heads, int D, bool output) {
+  if (t == nullptr || !entry::ptr_ok(t->data)) return false;
+  const Heads h = heads_of(t, T, heads, D);
+  if (!stride_ok(h.token) || !stride_ok(h.head)) return false;
+  if (!output) return true;
+  // each element its own place
+  return (h.head >= D && h.token >= (heads - 1) * h.head + D) || (h.token >= D && h.head >= (T - 1) * h.token + D);
+}
+bool config_ok(const moe_attention_config* c) {
+  if (c == nullptr || c->T < 0 || c->T > kMaxTokens || c->sequences < 0 || c->sequences > kMaxSequences) return false;
+  if (c->q_heads <= 0 || c->q_heads > kMaxHeads || c->kv_heads <= 0 || c->q_heads % c->kv_heads != 0) return false;
+  if (c->head_dim <= 0 || c->head_dim > kMaxHeadDim || c->head_dim % 8 != 0) return false;
+  return c->scale > 0.f && c->scale < INFINITY;
+}
+long long stats_pitch(int T) { return (static_cast<long long>(T) + kRows - 1) / kRows * kRows; }
+
+AttnParams params_of(const moe_attention_config* c, const int32_t* cu, void* ws) {
+  AttnParams p = {};
+  p.cu = cu;
+  p.B = c->sequences;
+  p.T = c->T;
+  p.Hq = c->q_heads;
+  p.Hkv = c->kv_heads;
+  p.D = c->head_dim;
+  p.scale = c->scale;
+  p.scale2 = c->scale * kLog2e;
+  p.tiles = (c->T + kRows - 1) / kRows;
+  p.status = static_cast<int*>(ws);
+  p.stats = reinterpret_cast<float2*>(static_cast<char*>(ws) + entry::kStatusBytes);
+  p.pitch = stats_pitch(c->T);
+  const unsigned long long wait = gemm_wait_limit_ns();
+  p.wait_ns = wait != 0 ? wait : kWaitLimitNs;
+  return p;
+}
+
+bool make_map(CUtensorMap* m, const moe_heads* t, int T, int heads, int D) {
+  const Heads h = heads_of(t, T, heads, D);
+  return make_tmap_heads(m, h.p, D, heads, T, h.head, h.token);
+}
+
+template <int DP>
+cudaError_t forward(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const AttnParams& p,
+                    cudaStream_t st) {
+  static std::atomic<bool> attr_set[kMaxDevices];
+  const int grid = p.tiles * (p.pair_rows ? p.Hq : p.Hq / 2);
+  return launch_big(attention_fwd_kernel<DP>, attr_set, grid, fwd_smem<DP>(), st, tq, tk, tv, p);
+}
+template <int DP>
+cudaError_t backward(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& td,
+                     AttnParams p, const Heads& dq, const Heads& dk, const Heads& dv, cudaStream_t st) {
+  static std::atomic<bool> dq_set[kMaxDevices], dkv_set[kMaxDevices];
+  p.d0 = dk;
+  p.d1 = dv;
+  cudaError_t e = launch_big(attention_dkv_kernel<DP>, dkv_set, p.tiles * p.Hkv, dkv_smem<DP>(), st, tq, tk, tv, td, p);
+  if (e != cudaSuccess) return e;
+  p.d0 = dq;
+  return launch_big(attention_dq_kernel<DP>, dq_set, p.tiles * p.Hq, dq_smem<DP>(), st, tq, tk, tv, td, p);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+using namespace moe::entry;
+
+extern "C" {
+
+size_t moe_attention_workspace_bytes(const moe_attention_config* cfg) {
+  if (!config_ok(cfg)) return 0;
+  return kStatusBytes + align_up(static_cast<size_t>(cfg->q_heads) * stats_pitch(cfg->T) * sizeof(float2));
+}
+
+moe_status moe_attention_forward(const moe_attention_config* cfg, const moe_heads* q, const moe_heads* k,
+                                 const moe_heads* v, const int32_t* cu_seqlens, const moe_heads* out, float* lse,
+                                 void* ws, size_t ws_bytes, void* stream) {
+  if (!config_ok(cfg) || !ptr_ok(ws)) return MOE_ERR_INVALID_ARG;
+  const int T = cfg->T, Hq = cfg->q_heads, Hkv = cfg->kv_heads, D = cfg->head_dim;
+  const bool none = T == 0 || cfg->sequences == 0;
+  if (!none && (!ptr_ok(cu_seqlens) || !ptr_ok(lse) || !heads_ok(q, T, Hq, D, false) || !heads_ok(k, T, Hkv, D, false) ||
+                !heads_ok(v, T, Hkv, D, false) || !heads_ok(out, T, Hq, D, true)))
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < kStatusBytes) return MOE_ERR_WORKSPACE;
+  if (!device_is_gb300()) return MOE_ERR_UNSUPPORTED;
+  if (none) return MOE_OK;
+  AttnParams p = params_of(cfg, cu_seqlens, ws);
+  p.pair_rows = Hq / Hkv % 2;
+  if (p.pair_rows) p.tiles = (T + 2 * kRows - 1) / (2 * kRows);
+  p.o = heads_of(out, T, Hq, D);
+  p.d0 = heads_of(v, T, Hkv, D);
+  p.lse = lse;
+  CUtensorMap tq, tk, tv;
+  if (!make_map(&tq, q, T, Hq, D) || !make_map(&tk, k, T, Hkv, D) || !make_map(&tv, v, T, Hkv, D))
+    return MOE_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return status_of(D <= 64 ? forward<64>(tq, tk, tv, p, st) : forward<128>(tq, tk, tv, p, st));
+}
+
+moe_status moe_attention_backward(const moe_attention_config* cfg, const moe_heads* q, const moe_heads* k,
+                                  const moe_heads* v, const int32_t* cu_seqlens, const moe_heads* out, const float* lse,
+                                  const moe_heads* dout, const moe_heads* dq, const moe_heads* dk, const moe_heads* dv,
+                                  void* ws, size_t ws_bytes, void* stream) {
+  if (!config_ok(cfg) || !ptr_ok(ws)) return MOE_ERR_INVALID_ARG;
+  const int T = cfg->T, Hq = cfg->q_heads, Hkv = cfg->kv_heads, D = cfg->head_dim;
+  const bool none = T == 0 || cfg->sequences == 0;
+  if (!none && (!ptr_ok(cu_seqlens) || !ptr_ok(lse) || !heads_ok(q, T, Hq, D, false) || !heads_ok(k, T, Hkv, D, false) ||
+                !heads_ok(v, T, Hkv, D, false) || !heads_ok(out, T, Hq, D, false) || !heads_ok(dout, T, Hq, D, false) ||
+                !heads_ok(dq, T, Hq, D, true) || !heads_ok(dk, T, Hkv, D, true) || !heads_ok(dv, T, Hkv, D, true)))
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < moe_attention_workspace_bytes(cfg)) return MOE_ERR_WORKSPACE;
+  if (!device_is_gb300()) return MOE_ERR_UNSUPPORTED;
+  if (none) return MOE_OK;
+  AttnParams p = params_of(cfg, cu_seqlens, ws);
+  p.o = heads_of(out, T, Hq, D);
+  p.dout = heads_of(dout, T, Hq, D);
+  p.lse = const_cast<float*>(lse);
+  CUtensorMap tq, tk, tv, td;
+  if (!make_map(&tq, q, T, Hq, D) || !make_map(&tk, k, T, Hkv, D) || !make_map(&tv, v, T, Hkv, D) ||
+      !make_map(&td, dout, T, Hq, D))
+    return MOE_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const long long rows = static_cast<long long>(T) * Hq;
+  const long long blocks = (rows + 15) / 16;
+  count_launches(1);
+  const cudaError_t e = launch_k(attention_stats_kernel, static_cast<int>(blocks < 4864 ? blocks : 4864), 256, 0, st, p);
+  if (e != cudaSuccess) return MOE_ERR_CUDA;
+  const Heads hq = heads_of(dq, T, Hq, D), hk = heads_of(dk, T, Hkv, D), hv = heads_of(dv, T, Hkv, D);
+  return status_of(D <= 64 ? backward<64>(tq, tk, tv, td, p, hq, hk, hv, st)
+                           : backward<128>(tq, tk, tv, td, p, hq, hk, hv, st));
+}
+
+}  // extern "C"

@@ -22,6 +22,10 @@ bool make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype,
 // fp32 slabs [depth][rows][cols]: stored (or added to) in boxes of 128 bytes x 32 rows, 128B swizzle.
 bool make_tmap_slabs_f32(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint64_t depth);
 
+// [tokens][heads][width] bf16 with these strides (elements): boxes of 64 columns of one head x 128 tokens, 128B swizzle.
+bool make_tmap_heads(CUtensorMap* map, const void* base, uint64_t width, uint64_t heads, uint64_t tokens,
+                     uint64_t head_stride, uint64_t token_stride);
+
 inline bool make_tmap_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint32_t box_inner,
                            uint32_t box_outer) {
   return make_tmap_2d(map, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, outer, box_inner, box_outer);

@@ -57,6 +57,20 @@ bool make_tmap_slabs_f32(CUtensorMap* map, const void* base, uint64_t cols, uint
   return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_heads(CUtensorMap* map, const void* base, uint64_t width, uint64_t heads, uint64_t tokens,
+                     uint64_t head_stride, uint64_t token_stride) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[3] = {width, heads, tokens};
+  cuuint64_t strides[2] = {head_stride * 2, token_stride * 2};
+  cuuint32_t box[3] = {64, 1, 128};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 namespace {
 
 template <int BN>

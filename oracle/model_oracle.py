@@ -79,3 +79,60 @@ def cross_entropy_grad(x, w, labels, dloss, lse=None):
             # root of the sum of squares and sum of magnitudes of the terms, for error bounds
             "dx_sq": np.sqrt((d * d) @ (w * w)), "dw_sq": np.sqrt((d * d).T @ (xs * xs)),
             "dx_mag": np.abs(d) @ np.abs(w), "dw_mag": np.abs(d).T @ np.abs(xs)}
+
+
+# ------------------------------------------------------------------ attention
+def _sequences(cu, T):
+    return [(int(a), int(b)) for a, b in zip(cu, cu[1:]) if b > a]
+
+
+def attention(q, k, v, cu, scale):
+    """Causal attention of each sequence: out, lse (0 in rows of no sequence), and sums of magnitudes for bounds."""
+    T, Hq, D = q.shape
+    G = Hq // k.shape[1]
+    out, mag = np.zeros((T, Hq, v.shape[2])), np.zeros((T, Hq, v.shape[2]))
+    lse, s_mag = np.zeros((Hq, T)), np.zeros((Hq, T))
+    for a, b in _sequences(cu, T):
+        seen = np.tril(np.ones((b - a, b - a), bool))
+        for h in range(Hq):
+            s = np.where(seen, scale * q[a:b, h] @ k[a:b, h // G].T, -np.inf)
+            m = s.max(1, keepdims=True)
+            e = np.exp(s - m)
+            l = e.sum(1, keepdims=True)
+            p = e / l
+            out[a:b, h], lse[h, a:b] = p @ v[a:b, h // G], (m + np.log(l))[:, 0]
+            mag[a:b, h] = p @ np.abs(v[a:b, h // G])
+            s_mag[h, a:b] = (np.where(seen, np.abs(q[a:b, h]) @ np.abs(k[a:b, h // G]).T, 0.0)).max(1) * scale
+    return {"out": out, "lse": lse, "out_mag": mag, "s_mag": s_mag}
+
+
+def attention_grad(q, k, v, cu, scale, dout):
+    """dq, dk, dv, and for each the sums of magnitudes behind its error bounds.
+
+    *_mag: the terms' magnitudes; *_delta: what an error of one part in <|dout|, |out|> moves; *_delta_sq: the
+    variance from independent errors of variance 1 in each of the row's products dout out.
+    """
+    T, Hq, D = q.shape
+    G = Hq // k.shape[1]
+    f = attention(q, k, v, cu, scale)
+    r = {n: np.zeros(t.shape) for n, t in (("dq", q), ("dk", k), ("dv", v), ("dq_mag", q), ("dk_mag", k), ("dv_mag", v),
+                                           ("dq_delta", q), ("dk_delta", k), ("dq_delta_sq", q), ("dk_delta_sq", k))}
+    for a, b in _sequences(cu, T):
+        seen = np.tril(np.ones((b - a, b - a), bool))
+        for h in range(Hq):
+            qs, ks, vs, do = q[a:b, h], k[a:b, h // G], v[a:b, h // G], dout[a:b, h]
+            p = np.where(seen, np.exp(np.where(seen, scale * qs @ ks.T, -np.inf) - f["lse"][h, a:b, None]), 0.0)
+            delta = (do * f["out"][a:b, h]).sum(1, keepdims=True)
+            ds = p * (do @ vs.T - delta)
+            mag = p * (np.abs(do) @ np.abs(vs).T + np.abs(delta))
+            dl = p * (np.abs(do) * np.abs(f["out"][a:b, h])).sum(1, keepdims=True)
+            for name, w in (("", ds), ("_mag", mag), ("_delta", dl)):
+                aq, ak = (qs, ks) if name == "" else (np.abs(qs), np.abs(ks))
+                r["dq" + name][a:b, h] += scale * w @ ak
+                r["dk" + name][a:b, h // G] += scale * w.T @ aq
+            var = ((do * f["out"][a:b, h]) ** 2).sum(1, keepdims=True)
+            r["dq_delta_sq"][a:b, h] += scale ** 2 * var * (p @ ks) ** 2
+            r["dk_delta_sq"][a:b, h // G] += scale ** 2 * (p ** 2 * var).T @ qs ** 2
+            r["dv"][a:b, h // G] += p.T @ do
+            r["dv_mag"][a:b, h // G] += p.T @ np.abs(do)
+    return {**r, **f}
