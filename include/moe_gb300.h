@@ -611,6 +611,94 @@ moe_status moe_attention_backward(const moe_attention_config* cfg, const moe_hea
                                   const moe_heads* dout, const moe_heads* dq, const moe_heads* dk, const moe_heads* dv,
                                   void* ws, size_t ws_bytes, void* stream);
 
+/* --------------------------------------------------------------------------
+ * Rotary positions of queries and keys
+ * ----------------------------------------------------------------------- */
+
+typedef enum {
+  MOE_ROTARY_PLAIN = 0,     /* freq[i] = base^(-2i/R) */
+  MOE_ROTARY_LINEAR = 1,    /* all of them divided by the factor */
+  MOE_ROTARY_BY_PARTS = 2   /* pairs that turn fewer than `slow` times within the original length divided by the
+                               factor, those that turn more than `fast` times left, a ramp between (over the pairs'
+                               indices); the rotated values then take the scale 0.1 ln(factor) + 1 */
+} moe_rotary_scaling;
+
+/* Fill freq [R/2] (host) with the angle per position of each pair, and *scale (host).
+ * R a multiple of 16, at most 512; base > 1; factor >= 1 and, by parts, original_length > 0
+ * and fast >= slow > 0 (32 and 1 are usual); arguments a scaling does not use are not looked at.
+ * Host only. */
+moe_status moe_rotary_frequencies(int32_t R, double base, int32_t scaling, double factor, int32_t original_length,
+                                  double fast, double slow, double* freq, float* scale);
+
+/* Turn each pair (a, b) of the first R values of every head by its angle
+ * positions[t] * freq[i]:  (a, b) -> scale (a cos - b sin, b cos + a sin);  with inverse = 1
+ * by the negative angle, which is the gradient of the call without it.  Pair i is the
+ * values 2i, 2i + 1 (interleaved = 1) or i, i + R/2 (0).  Values from R on are copied.
+ * x, out [T,heads,width] bf16 in strides of their own (see moe_heads); out is x itself with
+ * the same strides, or does not overlap it.  positions [T] int32, any value; freq [R/2]
+ * fp64, finite (device: moe_rotary_frequencies' or any other).  Angles are exact to 2^-24 of
+ * a turn at any position; each value is rounded once.  0 <= T <= 2^24, heads <= 1024, width a
+ * multiple of 8, at most 512, R a multiple of 16, at most the width. */
+moe_status moe_rotary(const moe_heads* x, const int32_t* positions, const double* freq, int32_t T, int32_t heads,
+                      int32_t width, int32_t R, int32_t interleaved, float scale, int32_t inverse, const moe_heads* out,
+                      void* stream);
+
+/* --------------------------------------------------------------------------
+ * Balance loss of the router
+ * ----------------------------------------------------------------------- */
+
+/* Workspace bytes of moe_balance_loss_forward (0 on bad sizes).  0 <= T <= 2^24,
+ * 1 <= E <= 256.  Host only. */
+size_t moe_balance_loss_workspace_bytes(int32_t T, int32_t E);
+
+/* loss = sum_e slope[e] sum_t p[t,e],  slope[e] = E counts[e] / (k N^2), over the N tokens that
+ * count: counts[e] times expert e is among their choices, p[t] the softmax of logits[t]
+ * (score MOE_SCORE_SOFTMAX) or their sigmoids divided by the sigmoids' sum (SIGMOID).  1 where
+ * choices and probabilities are even; 0 with no token.
+ * logits [T,E] fp32 and topk_idx [T,k] int32 as moe_router_topk writes them; tokens [T] int32 or NULL: a token
+ * below 0 is padding and does not count, whatever its row of logits and choices holds.
+ * Outputs: loss [1] fp32, counts [E] int32, slope [E] fp32 (for the backward pass).  A logit of
+ * -infinity has probability 0 (a row of nothing else: all 0).  A choice outside [0,E) is
+ * not counted and sets MOE_ERR_BAD_INDEX on the device.  1 <= k <= 32, k <= E.  Sums in a
+ * fixed order. */
+moe_status moe_balance_loss_forward(const float* logits, const int32_t* topk_idx, const int32_t* tokens, int32_t T,
+                                    int32_t E, int32_t k, int32_t score, float* loss, int32_t* counts, float* slope,
+                                    void* ws, size_t ws_bytes, void* stream);
+
+/* dlogits [T,E] fp32 = dloss[0] * d loss / d logits (the choices are constants), overwritten; zero
+ * rows for padding.  logits, tokens, score and slope as in the forward call; dloss [1] fp32, device. */
+moe_status moe_balance_loss_backward(const float* logits, const float* slope, const int32_t* tokens, int32_t T,
+                                     int32_t E, int32_t score, const float* dloss, float* dlogits, void* stream);
+
+/* --------------------------------------------------------------------------
+ * Norm and clipping of gradients
+ * ----------------------------------------------------------------------- */
+
+typedef enum { MOE_TYPE_BF16 = 0, MOE_TYPE_FP32 = 1 } moe_type;
+
+/* n values of one type, contiguous, 16-byte aligned (n may be 0, or any odd number). */
+typedef struct {
+  void* data;
+  int64_t n;
+  int32_t type;   /* moe_type */
+} moe_tensor;
+
+/* Workspace bytes of moe_grad_norm for n tensors (0 <= n <= 2^20; 0 on a bad n).  Host only. */
+size_t moe_grad_norm_workspace_bytes(int32_t n);
+
+/* norm [1] fp32, device = the square root of the sum of the squares of all values of all tensors,
+ * fp32 squares joined in fp64 (in fp64 from the start where squares leave fp32's range), in a
+ * fixed order.  grads: n descriptions in host memory, which may be reused when the call
+ * returns; at most 2^40 values a tensor. */
+moe_status moe_grad_norm(const moe_tensor* grads, int32_t n, float* norm, void* ws, size_t ws_bytes, void* stream);
+
+/* out = g * min(1, limit / (norm[0] + 1e-6)), each value rounded once.  outs: as many
+ * tensors of the same sizes and types that do not overlap the gradients, or NULL: in place,
+ * and nothing is written where the factor is 1.  limit >= 0.  With an infinite norm the factor is 0
+ * (infinite values become NaN), with a NaN norm everything becomes NaN. */
+moe_status moe_grad_clip(const moe_tensor* grads, const moe_tensor* outs, int32_t n, const float* norm, float limit,
+                         void* stream);
+
 #ifdef __cplusplus
 }
 #endif

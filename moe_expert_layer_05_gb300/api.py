@@ -21,12 +21,14 @@ GEMM_DTYPE = {"bf16": 0, "mxfp8": 1, "nvfp4": 2}
 
 (GG_FC1_SWIGLU, GG_FC2, GG_DGRAD_FC2, GG_DGRAD_FC1, GG_WGRAD_FC1, GG_WGRAD_FC2, GG_FC1_SWIGLU_GATHERED,
  GG_FC2_COMBINE) = range(8)
+ROTARY_SCALING = {"plain": 0, "linear": 1, "by_parts": 2}
 MX_ROWS, MX_COLS_T, MX_ROWS_GATE_UP, MX_ROWS_G224, MX_COLS_T_G224 = range(5)
 
 c_i32 = ctypes.c_int32
 c_vp = ctypes.c_void_p
 c_sz = ctypes.c_size_t
 c_f32 = ctypes.c_float
+c_f64 = ctypes.c_double
 
 
 class MoeConfig(ctypes.Structure):
@@ -68,6 +70,10 @@ class MoeHeads(ctypes.Structure):
 class MoeAttentionConfig(ctypes.Structure):
     _fields_ = [("T", c_i32), ("sequences", c_i32), ("q_heads", c_i32), ("kv_heads", c_i32), ("head_dim", c_i32),
                 ("scale", c_f32)]
+
+
+class MoeTensor(ctypes.Structure):
+    _fields_ = [("data", c_vp), ("n", ctypes.c_int64), ("type", c_i32)]
 
 
 _P = ctypes.POINTER
@@ -118,6 +124,16 @@ _SIGS = {
     "moe_attention_backward": (c_i32, [_P(MoeAttentionConfig), _P(MoeHeads), _P(MoeHeads), _P(MoeHeads), c_vp,
                                        _P(MoeHeads), c_vp, _P(MoeHeads), _P(MoeHeads), _P(MoeHeads), _P(MoeHeads),
                                        c_vp, c_sz, c_vp]),
+    "moe_rotary_frequencies": (c_i32, [c_i32, c_f64, c_i32, c_f64, c_i32, c_f64, c_f64, _P(c_f64), _P(c_f32)]),
+    "moe_rotary": (c_i32, [_P(MoeHeads), c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_i32, c_f32, c_i32, _P(MoeHeads),
+                           c_vp]),
+    "moe_balance_loss_workspace_bytes": (c_sz, [c_i32, c_i32]),
+    "moe_balance_loss_forward": (c_i32, [c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_sz,
+                                         c_vp]),
+    "moe_balance_loss_backward": (c_i32, [c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp]),
+    "moe_grad_norm_workspace_bytes": (c_sz, [c_i32]),
+    "moe_grad_norm": (c_i32, [_P(MoeTensor), c_i32, c_vp, c_vp, c_sz, c_vp]),
+    "moe_grad_clip": (c_i32, [_P(MoeTensor), _P(MoeTensor), c_i32, c_vp, c_f32, c_vp]),
 }
 
 _lib = None
@@ -519,6 +535,109 @@ def moe_attention_backward(q, k, v, cu_seqlens, out, lse, dout, dq, dk, dv, ws, 
                                         _heads(dout, "dout", sq, dev), _heads(dq, "dq", sq, dev),
                                         _heads(dk, "dk", sk, dev), _heads(dv, "dv", sk, dev), wp, wn,
                                         stream_ptr(stream, dev)), "moe_attention_backward")
+
+
+def moe_rotary_frequencies(R: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+                           original_length: int = 0, fast: float = 32.0, slow: float = 1.0, device="cuda"):
+    """(freq, scale) for moe_rotary: the angle per position of each pair (fp64, on `device`), the values' factor."""
+    if not _sized(R, original_length):
+        raise MoeError(-1, "moe_rotary_frequencies")
+    freq, scale = (c_f64 * max(R // 2, 1))(), c_f32(1.0)
+    check(load().moe_rotary_frequencies(R, base, ROTARY_SCALING[scaling], factor, original_length, fast, slow, freq,
+                                        ctypes.byref(scale)), "moe_rotary_frequencies")
+    return torch.tensor(list(freq), dtype=torch.float64, device=device), scale.value
+
+
+def moe_rotary(x, positions, freq, out, interleaved: bool = False, scale: float = 1.0, inverse: bool = False,
+               stream=None) -> None:
+    """out = the first 2 len(freq) values of every head of x turned by positions * freq, the others copied.
+
+    x, out [T, heads, width] bf16 in any strides (out may be x); inverse: by the negative angles, the gradient.
+    """
+    dev = _device()
+    if len(x.shape) != 3:
+        raise ValueError(f"x: expected three dimensions, got {tuple(x.shape)}")
+    T, heads, width = shape = x.shape
+    pairs = freq.numel()
+    if not _sized(T, heads, width, 2 * pairs):
+        raise MoeError(-1, "x, freq")
+    check(load().moe_rotary(_heads(x, "x", shape, dev), _tensor(positions, "positions", _I32, (T,), dev),
+                            _tensor(freq, "freq", torch.float64, (pairs,), dev), T, heads, width, 2 * pairs,
+                            1 if interleaved else 0, scale, 1 if inverse else 0, _heads(out, "out", shape, dev),
+                            stream_ptr(stream, dev)), "moe_rotary")
+
+
+# ---------------------------------------------------------------- balance loss
+def moe_balance_loss_workspace_bytes(T: int, E: int) -> int:
+    return int(load().moe_balance_loss_workspace_bytes(T, E)) if _sized(T, E) else 0
+
+
+def moe_balance_loss_forward(logits, topk_idx, loss, counts, slope, ws, tokens=None, score: str = "softmax",
+                             stream=None) -> None:
+    """loss [1] of the router's choices topk_idx [T, k] among logits [T, E]; counts [E] per expert; slope [E] for
+    the backward.  tokens [T]: rows below 0 are padding."""
+    dev = _device()
+    T, E = _matrix(logits, "logits")
+    k = _matrix(topk_idx, "topk_idx")[1]
+    wp, wn = _scratch(ws, dev)
+    check(load().moe_balance_loss_forward(_tensor(logits, "logits", _F32, (T, E), dev),
+                                          _tensor(topk_idx, "topk_idx", _I32, (T, k), dev),
+                                          None if tokens is None else _tensor(tokens, "tokens", _I32, (T,), dev),
+                                          T, E, k, SCORE[score], _tensor(loss, "loss", _F32, (1,), dev),
+                                          _tensor(counts, "counts", _I32, (E,), dev),
+                                          _tensor(slope, "slope", _F32, (E,), dev), wp, wn, stream_ptr(stream, dev)),
+          "moe_balance_loss_forward")
+
+
+def moe_balance_loss_backward(logits, slope, dloss, dlogits, tokens=None, score: str = "softmax", stream=None) -> None:
+    """dlogits [T, E] of dloss[0] times the loss; zero rows for padding."""
+    dev = _device()
+    T, E = rows = _matrix(logits, "logits")
+    check(load().moe_balance_loss_backward(_tensor(logits, "logits", _F32, rows, dev),
+                                           _tensor(slope, "slope", _F32, (E,), dev),
+                                           None if tokens is None else _tensor(tokens, "tokens", _I32, (T,), dev),
+                                           T, E, SCORE[score], _tensor(dloss, "dloss", _F32, (1,), dev),
+                                           _tensor(dlogits, "dlogits", _F32, rows, dev), stream_ptr(stream, dev)),
+          "moe_balance_loss_backward")
+
+
+# ---------------------------------------------------------------- gradient norm
+def _tensors(ts, name: str, dev: int):
+    """Descriptions of contiguous bf16 or fp32 tensors on GPU `dev`."""
+    out = (MoeTensor * max(len(ts), 1))()
+    for d, t in zip(out, ts):
+        dtype = t.dtype
+        if (dtype is not _F32 and dtype is not _BF16) or t.get_device() != dev or not t.is_contiguous():
+            raise ValueError(f"{name}: expected contiguous tensors of {_F32} or {_BF16} on the current GPU, got one of "
+                             f"{dtype} on {t.device}" + ("" if t.is_contiguous() else ", not contiguous"))
+        d.data, d.n, d.type = t.data_ptr(), t.numel(), 1 if dtype is _F32 else 0
+    return out
+
+
+def moe_grad_norm_workspace_bytes(n: int) -> int:
+    return int(load().moe_grad_norm_workspace_bytes(n)) if _sized(n, 0) else 0
+
+
+def moe_grad_norm(grads, norm, ws, stream=None) -> None:
+    """norm [1] = the 2-norm of all tensors of the list (bf16 or fp32) together."""
+    dev = _device()
+    wp, wn = _scratch(ws, dev)
+    check(load().moe_grad_norm(_tensors(grads, "grads", dev), len(grads), _tensor(norm, "norm", _F32, (1,), dev), wp, wn,
+                               stream_ptr(stream, dev)), "moe_grad_norm")
+
+
+def moe_grad_clip(grads, norm, limit: float, outs=None, stream=None) -> None:
+    """Every tensor times min(1, limit / (norm + 1e-6)), in place or into outs (tensors of the same shapes)."""
+    dev = _device()
+    if outs is not None:
+        if len(outs) != len(grads):
+            raise ValueError(f"outs: expected {len(grads)} tensors, got {len(outs)}")
+        for g, o in zip(grads, outs):
+            if g.shape != o.shape or g.dtype is not o.dtype:
+                raise ValueError(f"outs: expected {tuple(g.shape)} of {g.dtype}, got {tuple(o.shape)} of {o.dtype}")
+    check(load().moe_grad_clip(_tensors(grads, "grads", dev), None if outs is None else _tensors(outs, "outs", dev),
+                               len(grads), _tensor(norm, "norm", _F32, (1,), dev), limit, stream_ptr(stream, dev)),
+          "moe_grad_clip")
 
 
 # ---------------------------------------------------------------- buffers

@@ -19,7 +19,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB_NAME = "libmoe_gb300.so"
 LIB_PATH = os.path.join(BUILD, LIB_NAME)
 SOURCES = ["api.cu", "route.cu", "gemm_fwd.cu", "gemm_bwd.cu", "gemm_mx.cu", "mxfp8.cu", "nvfp4.cu", "permute_noalloc.cu",
-           "embedding.cu", "layer_norm.cu", "cross_entropy.cu", "attention.cu"]
+           "embedding.cu", "layer_norm.cu", "cross_entropy.cu", "attention.cu", "rotary.cu", "balance_loss.cu",
+           "grad_clip.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
           "-Xptxas", "-warn-spills"]

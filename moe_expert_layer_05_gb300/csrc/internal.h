@@ -16,6 +16,9 @@ constexpr int kMaxK = 32;
 constexpr int kMapsDoneWord = 40;
 // The same for the blocks of the few-token cross entropy.
 constexpr int kFewDoneWord = 41;
+// The same for the balance loss and for the gradient norm.
+constexpr int kBalanceDoneWord = 42;
+constexpr int kNormDoneWord = 43;
 
 int num_sms();
 bool device_is_gb300();

@@ -136,3 +136,57 @@ def attention_grad(q, k, v, cu, scale, dout):
             r["dv"][a:b, h // G] += p.T @ do
             r["dv_mag"][a:b, h // G] += p.T @ np.abs(do)
     return {**r, **f}
+
+
+# --------------------------------------------------------------------- rotary
+def rotary(x, positions, freq, interleaved=False, scale=1.0, inverse=False):
+    """x [T, heads, width]; the first 2 len(freq) values of each head turned by positions * freq."""
+    n = len(freq)
+    angle = positions.astype(np.float64)[:, None, None] * freq * (-1.0 if inverse else 1.0)
+    turn = scale * np.exp(1j * angle)
+    a, b = (x[..., 0:2 * n:2], x[..., 1:2 * n:2]) if interleaved else (x[..., :n], x[..., n:2 * n])
+    z = (a + 1j * b) * turn
+    y = x.astype(np.float64).copy()
+    if interleaved:
+        y[..., 0:2 * n:2], y[..., 1:2 * n:2] = z.real, z.imag
+    else:
+        y[..., :n], y[..., n:2 * n] = z.real, z.imag
+    return y
+
+
+# --------------------------------------------------------------- balance loss
+def _shares(logits, sigmoid):
+    """Probabilities of each row (0 in a row of -infinity) and 1 - sigmoid."""
+    m = logits.max(1, keepdims=True)
+    with np.errstate(invalid="ignore", over="ignore"):
+        if sigmoid:
+            log_s = -np.logaddexp(0.0, -logits)
+            e = np.exp(log_s - log_s.max(1, keepdims=True))
+        else:
+            e = np.exp(logits - m)
+        p = e / e.sum(1, keepdims=True)
+        rest = np.exp(-np.logaddexp(0.0, logits))
+    return np.where(np.isneginf(m), 0.0, p), rest
+
+
+def balance_loss(logits, topk, k, tokens=None, sigmoid=False):
+    T, E = logits.shape
+    on = np.ones(T, bool) if tokens is None else tokens >= 0
+    ids = topk[on].reshape(-1)
+    counts = np.bincount(ids[(ids >= 0) & (ids < E)], minlength=E)
+    n = int(on.sum())
+    slope = E * counts / (k * n * n) if n else np.zeros(E)
+    p, rest = _shares(logits[on], sigmoid)
+    grad = np.zeros((T, E))
+    grad[on] = p * (slope - (p * slope).sum(1, keepdims=True)) * (rest if sigmoid else 1.0)
+    mag = np.zeros((T, E))
+    mag[on] = p * (slope + (p * slope).sum(1, keepdims=True))
+    return {"loss": float((slope * p.sum(0)).sum()), "counts": counts, "slope": slope, "grad": grad, "grad_mag": mag}
+
+
+# -------------------------------------------------------------- gradient norm
+def clip(grads, limit):
+    """(norm, every gradient times min(1, limit / (norm + 1e-6)))."""
+    norm = np.sqrt(sum((g.astype(np.float64) ** 2).sum() for g in grads))
+    c = min(1.0, limit / (norm + 1e-6))
+    return norm, [g * c for g in grads]
