@@ -25,6 +25,7 @@
 #include <cuda_runtime.h>
 
 #include <climits>
+#include <type_traits>
 
 #include "entry_checks.h"
 #include "gemm_common.h"
@@ -51,13 +52,28 @@ struct AttnParams {
   int pair_rows;           // forward: the two tiles of a CTA are rows of one head (else two heads of one group)
   int tiles;               // tiles along the rows
   Heads o, d0, d1;         // forward: out; gradients: dq or dk, dv
-  Heads dout;              // delta
+  Heads dout;
   float* lse;              // [Hq, T]
-  float2* stats;           // [Hq, pitch]: lse * log2 e, delta
+  float* stats;            // [2][Hq, pitch]: -lse log2 e, -delta
   long long pitch;
   int* status;
   unsigned long long wait_ns;
 };
+
+// Registers move from the warps that load and issue to those that work on the scores:
+// 8 x 32 x 216 + 4 x 32 x 72 = 12 x 32 x 168, what the block is launched with.
+constexpr int kArithRegs = 216, kOtherRegs = 72;
+static_assert(kArith * kArithRegs + (kThreads - kArith) * kOtherRegs <= kThreads * 168, "registers of a block");
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// A barrier of the arithmetic threads alone.
+__device__ __forceinline__ void arith_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kArith) : "memory"); }
 
 // ---------------------------------------------------------------- sequences
 // Where the sequences of rows r0 .. r0 + R - 1 begin and end.
@@ -151,10 +167,11 @@ __device__ __forceinline__ void mma_scores(uint32_t d, const uint8_t* a, const u
 // D[128 x DP] (+)= W[128 x 128] B[128 rows, DP], W in TMEM: its two halves of 64 along
 // the contraction at w and w + half.
 template <int DP>
-__device__ __forceinline__ void mma_sums(uint32_t d, uint32_t w, uint32_t half, const uint8_t* b, bool add) {
+__device__ __forceinline__ void mma_sums(uint32_t d, uint32_t w, uint32_t half, const uint8_t* b, bool add, int from = 0,
+                                         int to = 8) {
   const uint32_t ba = smem_u32(b);
   #pragma unroll
-  for (int kk = 0; kk < 8; ++kk)
+  for (int kk = from; kk < to; ++kk)
     mma_bf16_ts(d, w + (kk >> 2) * half + (kk & 3) * 8, smem_desc_sw128(ba + kk * 2048, Tile<DP>::kChunk, 1024),
                 Tile<DP>::kSums, (add || kk != 0) ? 1u : 0u);
 }
@@ -232,7 +249,7 @@ __device__ __forceinline__ void store_cols(__nv_bfloat16* row, int col, int D, c
 // columns each (their first 64 become the probabilities), sums DP columns each.
 struct FwdBook {
   uint64_t full[8], q_full;                // (one after the other: Issued counts on it)
-  uint64_t empty[8], s_full[2], p_full[2], o_full[2], drain;
+  uint64_t empty[8], s_full[2], p_full[2][2], o_full[2], drain;
   uint32_t tmem;
   int abort_flag;
   int bad_lo, bad_hi;                      // key rows of tiles in which clean_tile found something
@@ -258,7 +275,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bk.q_full, 1);
     for (int u = 0; u < 2; ++u) {
       mbar_init(&bk.s_full[u], 1);
-      mbar_init(&bk.p_full[u], 4);
+      mbar_init(&bk.p_full[u][0], 4);
+      mbar_init(&bk.p_full[u][1], 4);
       mbar_init(&bk.o_full[u], 1);
     }
     mbar_init(&bk.drain, 1);
@@ -304,7 +322,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int ib = on1 ? from[1] : from[0];
   const int n = (on0 || on1) ? max(to[0], to[1]) - ib : 0;      // key tiles of this CTA
 
-  if (n > 0 && warp == kLoadWarp) {
+  if (warp >= kLoadWarp) {
+   fewer_registers<kOtherRegs>();
+   if (n > 0 && warp == kLoadWarp) {
     if (lane == 0) {
       Issued got;
       mbar_arrive_expect_tx(&bk.q_full, (on0 ? C::kBytes : 0) + (on1 ? C::kBytes : 0));
@@ -323,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       got.drain(bk.full);                    // (they have landed by the end, unless another warp gave up)
     }
-  } else if (n > 0 && warp == kMmaWarp) {
+   } else if (n > 0 && warp == kMmaWarp) {
     if (lane == 0) {
       bool any = false;
       auto tile = [&](int s) { return ring + (s % ST) * C::kBytes; };
@@ -348,9 +368,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!full(sv) || (more && !full(sk + 2))) { ok = false; break; }
         for (int u = 0; u < 2; ++u) {
           if (in(u, i)) {
-            if (!mbar_wait(&bk.p_full[u], (i - from[u]) & 1, abort, lim)) { ok = false; break; }
-            tc_fence_after_sync();
-            mma_sums<DP>(tmem + 256 + DP * u, tmem + 128 * u, 32, tile(sv), i > from[u]);
+            // (the first half of the keys while the second is still exponentiated)
+            for (int half = 0; half < 2 && ok; ++half) {
+              ok = mbar_wait(&bk.p_full[u][half], (i - from[u]) & 1, abort, lim);
+              tc_fence_after_sync();
+              if (ok)
+                mma_sums<DP>(tmem + 256 + DP * u, tmem + 128 * u, 32, tile(sv), i > from[u] || half, 4 * half,
+                             4 * half + 4);
+            }
+            if (!ok) break;
             if (i + 1 == to[u]) mma_commit(&bk.o_full[u]);
           }
           if (in(u, i + 1)) scores(u, sk + 2);
@@ -364,7 +390,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait_drain(&bk.drain, 0);
       }
     }
-  } else if (n > 0 && warp < kLoadWarp) {
+   }
+  } else {
+   more_registers<kArithRegs>();
+   if (n > 0) {
     // ------------------------------------------------ a thread a row
     const int u = warp >> 2;
     const int f = u ? from[1] : from[0], e = u ? to[1] : to[0], r0 = u ? base[1] : base[0], h = u ? head[1] : head[0];
@@ -386,24 +415,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!warp_wait(&bk.s_full[u], (i - f) & 1, abort, lim)) { ok = false; break; }
       tc_fence_after_sync();
       uint32_t s[4][32];
-      #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld_x32(ts + 32 * c, s[c]);
-      #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld_wait(s[c]);
       const int k0 = top - kRows * (i + 1);
       const bool masked = i == f || k0 < all_from;
-      if (masked) {
-        const int lo = key_lo - k0, hi = key_hi - k0;
-        #pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c < lo || c > hi) s[c >> 5][c & 31] = 0xff800000u;
-      }
       float mx[4];
+      tmem_ld_x32(ts, s[0]);
       #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        mx[c] = as_f(s[c][0]);
+        tmem_ld_wait(s[c]);
+        if (c < 3) tmem_ld_x32(ts + 32 * (c + 1), s[c + 1 < 4 ? c + 1 : 3]);
+        if (masked) {
+          const int lo = key_lo - k0 - 32 * c, hi = key_hi - k0 - 32 * c;
+          #pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (j < lo || j > hi) s[c][j] = 0xff800000u;
+        }
+        mx[c] = fmaxf(as_f(s[c][0]), as_f(s[c][1]));
         #pragma unroll
-        for (int j = 1; j < 32; ++j) mx[c] = fmaxf(mx[c], as_f(s[c][j]));
+        for (int j = 2; j < 32; j += 2) mx[c] = fmaxf(fmaxf(mx[c], as_f(s[c][j])), as_f(s[c][j + 1]));
       }
       const float m = fmaxf(ref, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
       if (i == f) {
@@ -428,22 +456,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float off = ref == -INFINITY ? 0.f : -ref * p.scale2;
       const F32x2 off2 = make_f32x2(off, off), mul2_ = make_f32x2(p.scale2, p.scale2);
-      F32x2 part[4];
-      #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t w[16];
-        part[c] = make_f32x2(0.f, 0.f);
-        #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float2 x = split_f32x2(fma2(make_f32x2(as_f(s[c][2 * j]), as_f(s[c][2 * j + 1])), mul2_, off2));
-          const F32x2 q = make_f32x2(ex2(x.x), ex2(x.y));
-          part[c] = add2(part[c], q);
-          w[j] = pack_bf16x2(q);
-        }
-        tmem_st_x16(ts + 16 * c, w);
-      }
-      const float2 total = split_f32x2(add2(add2(part[0], part[1]), add2(part[2], part[3])));
-      sum += total.x + total.y;
       // One tile of rows looks through the values for both, before any product takes them.
       const bool both = i >= other_from && i < other_to;
       if ((masked || (both && (i == other_from || k0 < other_all))) && (u == 0 || !both)) {
@@ -454,8 +466,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           atomicMax(&bk.bad_hi, k0 + kRows - 1);
         }
       }
-      tmem_st_wait();
-      warp_arrive(&bk.p_full[u], lane);
+      F32x2 part[4];
+      #pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t w[32];
+        #pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t(&x)[32] = s[2 * half + c];
+          F32x2& sum2 = part[2 * half + c];
+          sum2 = make_f32x2(0.f, 0.f);
+          #pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float2 y = split_f32x2(fma2(make_f32x2(as_f(x[2 * j]), as_f(x[2 * j + 1])), mul2_, off2));
+            const F32x2 q = make_f32x2(ex2(y.x), ex2(y.y));
+            sum2 = add2(sum2, q);
+            w[16 * c + j] = pack_bf16x2(q);
+          }
+        }
+        tmem_st_x32(ts + 32 * half, w);
+        tmem_st_wait();
+        warp_arrive(&bk.p_full[u][half], lane);
+      }
+      const float2 total = split_f32x2(add2(add2(part[0], part[1]), add2(part[2], part[3])));
+      sum += total.x + total.y;
     }
     if (ok && e > f && warp_wait(&bk.o_full[u], 0, abort, lim)) {
       tc_fence_after_sync();
@@ -486,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (valid) p.lse[static_cast<long long>(h) * p.T + row] = (ref == -INFINITY ? 0.f : ref * p.scale) + logf(sum);
     }
   }
-
+  }
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
@@ -499,41 +532,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- gradients
-// stats[h, i] = (lse log2 e, <do, o>) of each row; 16 lanes a row.
-__global__ void __launch_bounds__(256) attention_stats_kernel(const AttnParams p) {
-  pdl_entry();
-  const int first = max(p.cu[0], 0), last = min(p.cu[p.B], p.T);
-  const int part = threadIdx.x & 15;
-  const long long n = static_cast<long long>(p.T) * p.Hq;
-  const long long step = static_cast<long long>(gridDim.x) * 16;
-  for (long long r0 = static_cast<long long>(blockIdx.x) * 16; r0 < n; r0 += step) {
-    const long long r = r0 + (threadIdx.x >> 4);
-    const int row = static_cast<int>(r / p.Hq), h = static_cast<int>(r % p.Hq);
-    const bool valid = r < n && row >= first && row < last;
-    float d = 0.f;
-    if (valid && 8 * part < p.D) {
-      const uint4 a = *reinterpret_cast<const uint4*>(p.o.p + row * p.o.token + h * p.o.head + 8 * part);
-      const uint4 b = *reinterpret_cast<const uint4*>(p.dout.p + row * p.dout.token + h * p.dout.head + 8 * part);
-      d = bf16_lo(a.x) * bf16_lo(b.x) + bf16_hi(a.x) * bf16_hi(b.x) + bf16_lo(a.y) * bf16_lo(b.y) +
-          bf16_hi(a.y) * bf16_hi(b.y) + bf16_lo(a.z) * bf16_lo(b.z) + bf16_hi(a.z) * bf16_hi(b.z) +
-          bf16_lo(a.w) * bf16_lo(b.w) + bf16_hi(a.w) * bf16_hi(b.w);
-    }
-    #pragma unroll
-    for (int m = 8; m > 0; m >>= 1) d += __shfl_xor_sync(kFull, d, m);
-    if (valid && part == 0)
-      p.stats[h * p.pitch + row] = make_float2(p.lse[static_cast<long long>(h) * p.T + row] * kLog2e, d);
-  }
-}
-
 // dq: 128 query rows of one head against their key tiles.  TMEM: dq DP columns from 0,
 // two score buffers at 128 and 256, dp at 384 (which becomes ds).  The scores of the
 // next key tile run while this one's ds is worked out.
+//
+// delta comes from the rounded out, an error of out's rounding in each of its products.  Where a
+// row sees few keys that is of the size of ds; rows that begin within their first key tile
+// take delta = sum_j p dp there instead.  Either goes to stats, for dk.
 struct DqBook {
   uint64_t q_full, k_full[2], v_full[2];
   uint64_t k_empty[2], v_empty[2], s_full[2], dp_full, ds_full, done;
   uint32_t tmem;
   int abort_flag;
   RowMap map;
+  float sums[2][2][kRows];                 // halves of rows that two threads share
 };
 
 template <int DP>
@@ -585,7 +597,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int a = max(q0, bk.map.first), b = min(top, bk.map.last);
   const int n = a < b ? (top - start_of(&bk.map, q0, a) + kRows - 1) / kRows : 0;
 
-  if (n > 0 && warp == kLoadWarp) {
+  if (warp >= kLoadWarp) {
+   fewer_registers<kOtherRegs>();
+   if (n > 0 && warp == kLoadWarp) {
     if (lane == 0) {
       Issued got;
       mbar_arrive_expect_tx(&bk.q_full, 2 * C::kBytes);
@@ -607,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       got.drain(&bk.q_full);
     }
-  } else if (n > 0 && warp == kMmaWarp) {
+   } else if (n > 0 && warp == kMmaWarp) {
     if (lane == 0) {
       bool any = false;
       auto scores = [&](int j) {
@@ -640,7 +654,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait_drain(&bk.done, 0);
       }
     }
-  } else if (n > 0 && warp < kLoadWarp) {
+   }
+  } else {
+   more_registers<kArithRegs>();
+   if (n > 0) {
     // a thread a row, the two groups of four warps each half of the keys
     const int half = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -648,17 +665,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool valid = row >= bk.map.first && row < bk.map.last;
     const int key_lo = valid ? start_of(&bk.map, q0, row) : p.T, key_hi = valid ? row : -1;
     const int all_from = start_of(&bk.map, q0, b - 1);
-    const float2 st = valid ? p.stats[h * p.pitch + row] : make_float2(0.f, 0.f);
-    const F32x2 lse2 = make_f32x2(-st.x, -st.x), delta2 = make_f32x2(-st.y, -st.y);
-    const F32x2 mul2_ = make_f32x2(p.scale2, p.scale2);
+    const int lr = row - q0;
+    float delta = 0.f, lse = 0.f;
+    if (valid) {
+      const uint4* o = reinterpret_cast<const uint4*>(p.o.p + row * p.o.token + h * p.o.head);
+      const uint4* d = reinterpret_cast<const uint4*>(p.dout.p + row * p.dout.token + h * p.dout.head);
+      #pragma unroll
+      for (int w = half; w < DP / 8; w += 2)
+        if (8 * w < p.D) {
+          const uint4 x = o[w], y = d[w];
+          delta += bf16_lo(x.x) * bf16_lo(y.x) + bf16_hi(x.x) * bf16_hi(y.x) + bf16_lo(x.y) * bf16_lo(y.y) +
+                   bf16_hi(x.y) * bf16_hi(y.y) + bf16_lo(x.z) * bf16_lo(y.z) + bf16_hi(x.z) * bf16_hi(y.z) +
+                   bf16_lo(x.w) * bf16_lo(y.w) + bf16_hi(x.w) * bf16_hi(y.w);
+        }
+      lse = -p.lse[static_cast<long long>(h) * p.T + row] * kLog2e;
+    }
+    bk.sums[0][half][lr] = delta;
+    arith_sync();
+    delta = -(bk.sums[0][0][lr] + bk.sums[0][1][lr]);
+    const F32x2 lse2 = make_f32x2(lse, lse), mul2_ = make_f32x2(p.scale2, p.scale2);
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      if (!warp_wait(&bk.s_full[j & 1], (j >> 1) & 1, abort, lim)) { ok = false; break; }
+    auto step = [&](int j, auto masked_c) {
+      constexpr bool masked = decltype(masked_c)::value;
+      auto give_up = [&] {
+        if (masked && j == 0) arith_sync();        // (the others come to theirs)
+        return false;
+      };
+      if (!warp_wait(&bk.s_full[j & 1], (j >> 1) & 1, abort, lim)) return give_up();
       tc_fence_after_sync();
       const int k0 = top - kRows * (j + 1);
-      const bool masked = j == 0 || k0 < all_from;
       const int lo = max(key_lo, k0) - k0 - 64 * half, hi = min(key_hi, k0 + kRows) - k0 - 64 * half;
-      uint32_t s[2][32];
+      uint32_t s[2][32], d[2][32];
       #pragma unroll
       for (int c = 0; c < 2; ++c) tmem_ld_x32(tmem + lanes + 128 + 128 * (j & 1) + 64 * half + 32 * c, s[c]);
       #pragma unroll
@@ -666,38 +703,67 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait(s[c]);
         #pragma unroll
         for (int x = 0; x < 32; x += 2) {
-          const float2 y = split_f32x2(fma2(make_f32x2(as_f(s[c][x]), as_f(s[c][x + 1])), mul2_, lse2));
-          s[c][x] = __float_as_uint(ex2(y.x));
-          s[c][x + 1] = __float_as_uint(ex2(y.y));
+          float2 y = split_f32x2(fma2(make_f32x2(as_f(s[c][x]), as_f(s[c][x + 1])), mul2_, lse2));
+          y.x = ex2(y.x);
+          y.y = ex2(y.y);
+          if (masked) {
+            if (32 * c + x < lo || 32 * c + x > hi) y.x = 0.f;
+            if (32 * c + x + 1 < lo || 32 * c + x + 1 > hi) y.y = 0.f;
+          }
+          s[c][x] = __float_as_uint(y.x);
+          s[c][x + 1] = __float_as_uint(y.y);
         }
       }
       if (masked) {
-        if (!warp_wait(&bk.k_full[j & 1], (j >> 1) & 1, abort, lim)) { ok = false; break; }
+        if (!warp_wait(&bk.k_full[j & 1], (j >> 1) & 1, abort, lim)) return give_up();
         clean_tile<DP>(k_smem + (j & 1) * C::kBytes, threadIdx.x, kArith);
       }
-      if (!warp_wait(&bk.dp_full, j & 1, abort, lim)) { ok = false; break; }
+      if (!warp_wait(&bk.dp_full, j & 1, abort, lim)) return give_up();
       tc_fence_after_sync();
+      #pragma unroll
+      for (int c = 0; c < 2; ++c) tmem_ld_x32(tmem + lanes + 384 + 64 * half + 32 * c, d[c]);
+      #pragma unroll
+      for (int c = 0; c < 2; ++c) tmem_ld_wait(d[c]);
+      if (masked && j == 0) {
+        F32x2 sum = make_f32x2(0.f, 0.f);
+        #pragma unroll
+        for (int c = 0; c < 2; ++c)
+          #pragma unroll
+          for (int x = 0; x < 32; x += 2) {
+            const float a0 = (32 * c + x < lo || 32 * c + x > hi) ? 0.f : as_f(d[c][x]);
+            const float a1 = (32 * c + x + 1 < lo || 32 * c + x + 1 > hi) ? 0.f : as_f(d[c][x + 1]);
+            sum = fma2(make_f32x2(as_f(s[c][x]), as_f(s[c][x + 1])), make_f32x2(a0, a1), sum);
+          }
+        const float2 t = split_f32x2(sum);
+        bk.sums[1][half][lr] = t.x + t.y;
+        arith_sync();
+        if (key_lo >= k0) delta = -(bk.sums[1][0][lr] + bk.sums[1][1][lr]);
+        if (valid && half == 0) {
+          p.stats[h * p.pitch + row] = lse;
+          p.stats[(p.Hq + h) * p.pitch + row] = delta;
+        }
+      }
+      const F32x2 delta2 = make_f32x2(delta, delta);
       uint32_t w[32];
       #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t d[32];
-        tmem_ld_x32(tmem + lanes + 384 + 64 * half + 32 * c, d);
-        tmem_ld_wait(d);
+      for (int c = 0; c < 2; ++c)
         #pragma unroll
         for (int x = 0; x < 32; x += 2) {
           float2 y = split_f32x2(mul2(make_f32x2(as_f(s[c][x]), as_f(s[c][x + 1])),
-                                      add2(make_f32x2(as_f(d[x]), as_f(d[x + 1])), delta2)));
+                                      add2(make_f32x2(as_f(d[c][x]), as_f(d[c][x + 1])), delta2)));
           if (masked) {
             if (32 * c + x < lo || 32 * c + x > hi) y.x = 0.f;
             if (32 * c + x + 1 < lo || 32 * c + x + 1 > hi) y.y = 0.f;
           }
           w[16 * c + x / 2] = pack_bf16x2(y.x, y.y);
         }
-      }
       tmem_st_x32(tmem + lanes + 384 + 64 * half, w);
       tmem_st_wait();
       warp_arrive(&bk.ds_full, lane);
-    }
+      return true;
+    };
+    for (int j = 0; ok && j < n; ++j)
+      ok = j == 0 || top - kRows * (j + 1) < all_from ? step(j, std::true_type{}) : step(j, std::false_type{});
     if (ok && warp_wait(&bk.done, 0, abort, lim)) {
       tc_fence_after_sync();
       __nv_bfloat16* out = p.d0.p + row * p.d0.token + h * p.d0.head;
@@ -713,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (valid) store_cols(out, col, p.D, v);
       }
     }
-  }
+  }  }
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
@@ -750,8 +816,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* v_smem = k_smem + C::kBytes;
   uint8_t* q_smem = v_smem + C::kBytes;
   uint8_t* do_smem = q_smem + 2 * C::kBytes;
-  float2* st_smem = reinterpret_cast<float2*>(do_smem + 2 * C::kBytes);        // [2][128]
-  DkvBook& bk = *reinterpret_cast<DkvBook*>(st_smem + 2 * kRows);
+  float* st_smem = reinterpret_cast<float*>(do_smem + 2 * C::kBytes);          // [2][-lse log2 e, -delta][128]
+  DkvBook& bk = *reinterpret_cast<DkvBook*>(st_smem + 4 * kRows);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(&bk.kv_full, 1);
@@ -791,7 +857,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int end = a < b ? end_of(&bk.map, k0, b - 1, kRows / 32) : k0;
   const int nq = a < b ? (end - k0 + kRows - 1) / kRows : 0, n = nq * group;
 
-  if (n > 0 && warp == kLoadWarp) {
+  if (warp >= kLoadWarp) {
+   fewer_registers<kOtherRegs>();
+   if (n > 0 && warp == kLoadWarp) {
     if (lane == 0) {
       Issued got;
       mbar_arrive_expect_tx(&bk.kv_full, 2 * C::kBytes);
@@ -804,9 +872,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = j & 1;
         const uint32_t ph = (j >> 1) & 1;
         if (j >= 2 && !mbar_wait(&bk.q_empty[s], ph ^ 1u, abort, lim)) { ok = false; break; }
-        mbar_arrive_expect_tx(&bk.q_full[s], C::kBytes + kRows * sizeof(float2));
+        mbar_arrive_expect_tx(&bk.q_full[s], C::kBytes + 2 * kRows * 4);
         load_tile<DP>(q_smem + s * C::kBytes, &tmQ, &bk.q_full[s], h, row);
-        bulk_load(st_smem + s * kRows, p.stats + h * p.pitch + row, kRows * sizeof(float2), &bk.q_full[s]);
+        bulk_load(st_smem + 2 * s * kRows, p.stats + h * p.pitch + row, kRows * 4, &bk.q_full[s]);
+        bulk_load(st_smem + (2 * s + 1) * kRows, p.stats + (p.Hq + h) * p.pitch + row, kRows * 4, &bk.q_full[s]);
         got.note(1 + s, ph);
         if (j >= 2 && !mbar_wait(&bk.do_empty[s], ph ^ 1u, abort, lim)) { ok = false; break; }
         mbar_arrive_expect_tx(&bk.do_full[s], C::kBytes);
@@ -820,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       got.drain(&bk.kv_full);
     }
-  } else if (n > 0 && warp == kMmaWarp) {
+   } else if (n > 0 && warp == kMmaWarp) {
     if (lane == 0) {
       bool any = false;
       auto scores = [&](int j) {
@@ -856,7 +925,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait_drain(&bk.done, 0);
       }
     }
-  } else if (n > 0 && warp < kLoadWarp) {
+   }
+  } else {
+   more_registers<kArithRegs>();
+   if (n > 0) {
     // a thread a key, the two groups of four warps each half of the queries
     const int half = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -866,69 +938,80 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int all_to = end_of(&bk.map, k0, a, kRows / 32);      // queries up to here see every key (from the diagonal)
     const F32x2 mul2_ = make_f32x2(p.scale2, p.scale2);
     bool ok = true;
-    int q0 = k0;
-    for (int j = 0; j < n; ++j) {
-      if (!warp_wait(&bk.q_full[j & 1], (j >> 1) & 1, abort, lim) || !warp_wait(&bk.s_full, j & 1, abort, lim)) {
-        ok = false;
-        break;
-      }
+    auto step = [&](int j, int q0, auto masked_c) {
+      constexpr bool masked = decltype(masked_c)::value;
+      if (!warp_wait(&bk.q_full[j & 1], (j >> 1) & 1, abort, lim) || !warp_wait(&bk.s_full, j & 1, abort, lim)) return false;
       tc_fence_after_sync();
-      const bool masked = q0 == k0 || q0 + kRows > all_to;
       const int lo = max(key, q0) - q0 - 64 * half, hi = min(key_end, q0 + kRows) - q0 - 64 * half;   // queries [lo, hi)
-      const float4* st = reinterpret_cast<const float4*>(st_smem + (j & 1) * kRows + 64 * half);
-      uint32_t s[2][32];
+      const float4* lse = reinterpret_cast<const float4*>(st_smem + 2 * (j & 1) * kRows + 64 * half);
+      const float4* delta = lse + kRows / 4;
+      uint32_t s[2][32], w[32];
       #pragma unroll
       for (int c = 0; c < 2; ++c) tmem_ld_x32(tmem + lanes + 256 + 64 * half + 32 * c, s[c]);
-      uint32_t w[32];
       #pragma unroll
       for (int c = 0; c < 2; ++c) {
         tmem_ld_wait(s[c]);
         #pragma unroll
-        for (int x = 0; x < 32; x += 2) {
-          const float4 a4 = st[16 * c + x / 2];       // (lse2, delta) of two queries
-          float2 y = split_f32x2(fma2(make_f32x2(as_f(s[c][x]), as_f(s[c][x + 1])), mul2_, make_f32x2(-a4.x, -a4.z)));
-          y.x = ex2(y.x);
-          y.y = ex2(y.y);
-          s[c][x] = __float_as_uint(y.x);
-          s[c][x + 1] = __float_as_uint(y.y);
+        for (int x = 0; x < 32; x += 4) {
+          const float4 l4 = lse[8 * c + x / 4];
+          float2 y = split_f32x2(fma2(make_f32x2(as_f(s[c][x]), as_f(s[c][x + 1])), mul2_, make_f32x2(l4.x, l4.y)));
+          float2 z = split_f32x2(fma2(make_f32x2(as_f(s[c][x + 2]), as_f(s[c][x + 3])), mul2_, make_f32x2(l4.z, l4.w)));
+          float v[4] = {ex2(y.x), ex2(y.y), ex2(z.x), ex2(z.y)};
+          #pragma unroll
+          for (int e = 0; e < 4; ++e) s[c][x + e] = __float_as_uint(v[e]);
           if (masked) {
             // (a query whose do is not finite has no finite delta: what it sees keeps that)
-            y.x = (32 * c + x < lo || 32 * c + x >= hi) ? 0.f : fmaf(0.f, a4.y, y.x);
-            y.y = (32 * c + x + 1 < lo || 32 * c + x + 1 >= hi) ? 0.f : fmaf(0.f, a4.w, y.y);
+            const float4 d4 = delta[8 * c + x / 4];
+            const float dd[4] = {d4.x, d4.y, d4.z, d4.w};
+            #pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[e] = (32 * c + x + e < lo || 32 * c + x + e >= hi) ? 0.f : fmaf(0.f, dd[e], v[e]);
           }
-          w[16 * c + x / 2] = pack_bf16x2(y.x, y.y);
+          w[16 * c + x / 2] = pack_bf16x2(v[0], v[1]);
+          w[16 * c + x / 2 + 1] = pack_bf16x2(v[2], v[3]);
         }
       }
       tmem_st_x32(tmem + lanes + 256 + 64 * half, w);
       if (masked) {
-        if (!warp_wait(&bk.do_full[j & 1], (j >> 1) & 1, abort, lim)) { ok = false; break; }
+        if (!warp_wait(&bk.do_full[j & 1], (j >> 1) & 1, abort, lim)) return false;
         clean_tile<DP>(do_smem + (j & 1) * C::kBytes, threadIdx.x, kArith);
         clean_tile<DP>(q_smem + (j & 1) * C::kBytes, threadIdx.x, kArith);
       }
       tmem_st_wait();
       warp_arrive(&bk.p_full, lane);
-      if (!warp_wait(&bk.dp_full, j & 1, abort, lim)) { ok = false; break; }
+      if (!warp_wait(&bk.dp_full, j & 1, abort, lim)) return false;
       tc_fence_after_sync();
+      uint32_t d[2][32];
+      #pragma unroll
+      for (int c = 0; c < 2; ++c) tmem_ld_x32(tmem + lanes + 384 + 64 * half + 32 * c, d[c]);
       #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        uint32_t d[32];
-        tmem_ld_x32(tmem + lanes + 384 + 64 * half + 32 * c, d);
-        tmem_ld_wait(d);
+        tmem_ld_wait(d[c]);
         #pragma unroll
-        for (int x = 0; x < 32; x += 2) {
-          const float4 a4 = st[16 * c + x / 2];
-          float2 y = split_f32x2(mul2(make_f32x2(as_f(s[c][x]), as_f(s[c][x + 1])),
-                                      add2(make_f32x2(as_f(d[x]), as_f(d[x + 1])), make_f32x2(-a4.y, -a4.w))));
+        for (int x = 0; x < 32; x += 4) {
+          const float4 d4 = delta[8 * c + x / 4];
+          const float2 y = split_f32x2(mul2(make_f32x2(as_f(s[c][x]), as_f(s[c][x + 1])),
+                                            add2(make_f32x2(as_f(d[c][x]), as_f(d[c][x + 1])), make_f32x2(d4.x, d4.y))));
+          const float2 z = split_f32x2(mul2(make_f32x2(as_f(s[c][x + 2]), as_f(s[c][x + 3])),
+                                            add2(make_f32x2(as_f(d[c][x + 2]), as_f(d[c][x + 3])), make_f32x2(d4.z, d4.w))));
+          float v[4] = {y.x, y.y, z.x, z.y};
           if (masked) {
-            if (32 * c + x < lo || 32 * c + x >= hi) y.x = 0.f;
-            if (32 * c + x + 1 < lo || 32 * c + x + 1 >= hi) y.y = 0.f;
+            #pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (32 * c + x + e < lo || 32 * c + x + e >= hi) v[e] = 0.f;
           }
-          w[16 * c + x / 2] = pack_bf16x2(y.x, y.y);
+          w[16 * c + x / 2] = pack_bf16x2(v[0], v[1]);
+          w[16 * c + x / 2 + 1] = pack_bf16x2(v[2], v[3]);
         }
       }
       tmem_st_x32(tmem + lanes + 384 + 64 * half, w);
       tmem_st_wait();
       warp_arrive(&bk.ds_full, lane);
+      return true;
+    };
+    int q0 = k0;
+    for (int j = 0; ok && j < n; ++j) {
+      ok = q0 == k0 || q0 + kRows > all_to ? step(j, q0, std::true_type{}) : step(j, q0, std::false_type{});
       q0 += kRows;
       if (q0 >= k0 + nq * kRows) q0 = k0;
     }
@@ -949,7 +1032,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (valid) store_cols(out, 32 * c, p.D, v);
       }
     }
-  }
+  }  }
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
@@ -968,7 +1051,7 @@ template <int DP>
 constexpr int dq_smem() { return 1024 + 6 * Tile<DP>::kBytes + static_cast<int>(sizeof(DqBook)); }
 template <int DP>
 constexpr int dkv_smem() {
-  return 1024 + 6 * Tile<DP>::kBytes + 2 * kRows * static_cast<int>(sizeof(float2)) + static_cast<int>(sizeof(DkvBook));
+  return 1024 + 6 * Tile<DP>::kBytes + 4 * kRows * 4 + static_cast<int>(sizeof(DkvBook));
 }
 static_assert(fwd_smem<128>() <= 232448 && dq_smem<128>() <= 232448 && dkv_smem<128>() <= 232448, "shared memory");
 
@@ -1023,7 +1106,7 @@ AttnParams params_of(const moe_attention_config* c, const int32_t* cu, void* ws)
   p.scale2 = c->scale * kLog2e;
   p.tiles = (c->T + kRows - 1) / kRows;
   p.status = static_cast<int*>(ws);
-  p.stats = reinterpret_cast<float2*>(static_cast<char*>(ws) + entry::kStatusBytes);
+  p.stats = reinterpret_cast<float*>(static_cast<char*>(ws) + entry::kStatusBytes);
   p.pitch = stats_pitch(c->T);
   const unsigned long long wait = gemm_wait_limit_ns();
   p.wait_ns = wait != 0 ? wait : kWaitLimitNs;
@@ -1046,12 +1129,13 @@ template <int DP>
 cudaError_t backward(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& td,
                      AttnParams p, const Heads& dq, const Heads& dk, const Heads& dv, cudaStream_t st) {
   static std::atomic<bool> dq_set[kMaxDevices], dkv_set[kMaxDevices];
+  p.d0 = dq;
+  const cudaError_t e =
+      launch_big(attention_dq_kernel<DP>, dq_set, p.tiles * p.Hq, dq_smem<DP>(), st, tq, tk, tv, td, p);
+  if (e != cudaSuccess) return e;
   p.d0 = dk;
   p.d1 = dv;
-  cudaError_t e = launch_big(attention_dkv_kernel<DP>, dkv_set, p.tiles * p.Hkv, dkv_smem<DP>(), st, tq, tk, tv, td, p);
-  if (e != cudaSuccess) return e;
-  p.d0 = dq;
-  return launch_big(attention_dq_kernel<DP>, dq_set, p.tiles * p.Hq, dq_smem<DP>(), st, tq, tk, tv, td, p);
+  return launch_big(attention_dkv_kernel<DP>, dkv_set, p.tiles * p.Hkv, dkv_smem<DP>(), st, tq, tk, tv, td, p);
 }
 
 }  // namespace
@@ -1064,7 +1148,7 @@ extern "C" {
 
 size_t moe_attention_workspace_bytes(const moe_attention_config* cfg) {
   if (!config_ok(cfg)) return 0;
-  return kStatusBytes + align_up(static_cast<size_t>(cfg->q_heads) * stats_pitch(cfg->T) * sizeof(float2));
+  return kStatusBytes + align_up(static_cast<size_t>(cfg->q_heads) * stats_pitch(cfg->T) * 2 * sizeof(float));
 }
 
 moe_status moe_attention_forward(const moe_attention_config* cfg, const moe_heads* q, const moe_heads* k,
@@ -1115,11 +1199,6 @@ moe_status moe_attention_backward(const moe_attention_config* cfg, const moe_hea
       !make_map(&td, dout, T, Hq, D))
     return MOE_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const long long rows = static_cast<long long>(T) * Hq;
-  const long long blocks = (rows + 15) / 16;
-  count_launches(1);
-  const cudaError_t e = launch_k(attention_stats_kernel, static_cast<int>(blocks < 4864 ? blocks : 4864), 256, 0, st, p);
-  if (e != cudaSuccess) return MOE_ERR_CUDA;
   const Heads hq = heads_of(dq, T, Hq, D), hk = heads_of(dk, T, Hkv, D), hv = heads_of(dv, T, Hkv, D);
   return status_of(D <= 64 ? backward<64>(tq, tk, tv, td, p, hq, hk, hv, st)
                            : backward<128>(tq, tk, tv, td, p, hq, hk, hv, st));
