@@ -100,6 +100,17 @@ __device__ __forceinline__ uint4 word_at(const uint4* src, long long w, long lon
   return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
+// A thread's words of a chunk.  A whole chunk's loads stand side by side, without a branch between them.
+__device__ __forceinline__ void load_chunk(const uint4* src, long long w0, long long n, bool fp32, uint4 (&v)[kWords]) {
+  if ((w0 - threadIdx.x + kChunkWords) * (fp32 ? 4 : 8) <= n) {
+    #pragma unroll
+    for (int j = 0; j < kWords; ++j) v[j] = src[w0 + j * kThreads];
+  } else {
+    #pragma unroll
+    for (int j = 0; j < kWords; ++j) v[j] = word_at(src, w0 + j * kThreads, n, fp32);
+  }
+}
+
 __device__ __forceinline__ double block_sum(double v, double* s) {
   s[threadIdx.x] = v;
   __syncthreads();
@@ -127,8 +138,7 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
     const bool fp32 = list.fp32[i] != 0;
     const long long w0 = (c - (i > 0 ? list.end[i - 1] : 0)) * kChunkWords + threadIdx.x;
     uint4 v[kWords];
-    #pragma unroll
-    for (int j = 0; j < kWords; ++j) v[j] = word_at(list.src[i], w0 + j * kThreads, list.n[i], fp32);
+    load_chunk(list.src[i], w0, list.n[i], fp32, v);
     float s[2] = {0.f, 0.f};
     #pragma unroll
     for (int j = 0; j < kWords; ++j) s[j & 1] += squares(v[j], fp32);
@@ -175,9 +185,9 @@ __global__ void __launch_bounds__(kThreads) grad_clip_kernel(const __grid_consta
     const bool fp32 = list.fp32[i] != 0;
     const int per = fp32 ? 4 : 8;
     const long long w0 = (chunk - (i > 0 ? list.end[i - 1] : 0)) * kChunkWords + threadIdx.x, n = list.n[i];
+    const bool whole = (w0 - threadIdx.x + kChunkWords) * per <= n;
     uint4 v[kWords];
-    #pragma unroll
-    for (int j = 0; j < kWords; ++j) v[j] = word_at(list.src[i], w0 + j * kThreads, n, fp32);
+    load_chunk(list.src[i], w0, n, fp32, v);
     #pragma unroll
     for (int j = 0; j < kWords; ++j) {
       uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
@@ -185,8 +195,8 @@ __global__ void __launch_bounds__(kThreads) grad_clip_kernel(const __grid_consta
       for (int e = 0; e < 4; ++e)
         u[e] = fp32 ? __float_as_uint(__uint_as_float(u[e]) * c) : pack_bf16x2(bf16_lo(u[e]) * c, bf16_hi(u[e]) * c);
       const long long w = w0 + j * kThreads, left = n - w * per;
-      if (left >= per) {
-        list.dst[i][w] = make_uint4(u[0], u[1], u[2], u[3]);
+      if (whole || left >= per) {
+        __stcs(list.dst[i] + w, make_uint4(u[0], u[1], u[2], u[3]));
       } else {
         for (int e = 0; e < left; ++e) {
           if (fp32)

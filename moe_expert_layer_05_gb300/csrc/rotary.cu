@@ -8,8 +8,8 @@
 //
 // Angles of far positions have no digits left in fp32, so a pair's frequency is taken in
 // turns as a 64-bit binary fraction, and position * fraction modulo 2^64 is the angle's
-// fraction of a turn, exactly: 2^-56 turns off per position from the frequency's own
-// fp64 rounding, 2^-25 at position 2^31.
+// fraction of a turn, exactly: off by 2^-62 (for pairs of up to a radian a position) times the
+// position, 2^-31 turns at the last one.
 //
 // A block works out the sines of kTokens tokens once for all heads, while its first values
 // are on their way.  Bound by HBM: every value is read and written once.
@@ -24,8 +24,9 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTokens = 4;             // of one block
-constexpr int kMaxHeads = 1024, kMaxWidth = 512;
+constexpr int kTokens = 8;             // of one block, at most
+constexpr int kAhead = 4;              // pieces a thread has on their way
+constexpr int kMaxHeads = 1024, kMaxWidth = 512;      // (kTokens of the widest: 16 KB of sines)
 
 struct RotaryParams {
   const __nv_bfloat16* x;
@@ -36,6 +37,7 @@ struct RotaryParams {
   int T, heads, R;
   int turned, tasks;                   // pieces of 16 values of a row: those that turn, all
   int words;                           // 16-byte words of a row
+  int block_tokens;
   float scale;
   int interleaved, inverse;
 };
@@ -52,11 +54,31 @@ __device__ __forceinline__ void turn_pair(uint32_t& w, const float2& r) {
   w = pack_bf16x2(a * r.x - b * r.y, b * r.x + a * r.y);
 }
 
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p) {
-  __shared__ float2 s_turn[kTokens * kMaxWidth / 2];       // [token][pair]: cos, sin, times scale
+// freq / (2 pi) modulo 1 as a 64-bit binary fraction: the mantissa times 2^64 / (2 pi), shifted.
+// (In whole numbers: fp64 arithmetic has two lanes an SM.)
+__device__ __forceinline__ unsigned long long turn_fraction(double freq) {
+  constexpr unsigned long long kTurn = 0x28BE60DB9391054Aull;            // 2^64 / (2 pi)
+  const unsigned long long bits = static_cast<unsigned long long>(__double_as_longlong(freq));
+  const int e = static_cast<int>(bits >> 52 & 0x7ff);
+  if (e == 0) return 0;                                                  // below 2^-1022
+  const unsigned long long m = (bits & 0xfffffffffffffull) | 1ull << 52;
+  const unsigned long long lo = m * kTurn, hi = __umul64hi(m, kTurn);    // times 2^(e - 1075)
+  const int s = 1075 - e;
+  unsigned long long r;
+  if (s <= 0)
+    r = s > -64 ? lo << -s : 0;
+  else if (s < 64)
+    r = lo >> s | hi << (64 - s);
+  else
+    r = s < 128 ? hi >> (s - 64) : 0;
+  return bits >> 63 ? 0 - r : r;
+}
+
+__global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const RotaryParams p) {
+  extern __shared__ __align__(16) float2 s_turn[];         // [token][pair]: cos, sin, times scale
   pdl_entry();
-  const int t0 = static_cast<int>(blockIdx.x) * kTokens;
-  const int tokens = min(kTokens, p.T - t0), pairs = p.R / 2;
+  const int t0 = static_cast<int>(blockIdx.x) * p.block_tokens;
+  const int tokens = min(p.block_tokens, p.T - t0), pairs = p.R / 2;
   const int rows = tokens * p.heads, all = rows * p.tasks;
   // piece j of a row: words first, second
   auto first_word = [&](int j) { return j < p.turned ? (p.interleaved ? 2 * j : j) : 2 * j; };
@@ -65,7 +87,6 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p) 
     const int t = row / p.heads;
     return reinterpret_cast<const uint4*>(p.x + (t0 + t) * p.x_token + (row - t * p.heads) * p.x_head);
   };
-  constexpr int kAhead = 4;
   uint4 a[kAhead], b[kAhead];
   auto load = [&](int i0) {
     #pragma unroll
@@ -82,8 +103,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p) 
   load(threadIdx.x);
   for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
     const int t = i / pairs;
-    const double turns = p.freq[i - t * pairs] * 0.15915494309189533577;       // 1 / (2 pi)
-    const unsigned long long frac = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
+    const unsigned long long frac = turn_fraction(p.freq[i - t * pairs]);
     const unsigned long long angle = static_cast<unsigned long long>(static_cast<long long>(p.positions[t0 + t])) * frac;
     float s, c;
     sincospif(static_cast<float>(static_cast<int>(angle >> 32)) * (1.f / 2147483648.f), &s, &c);   // (half turns)
@@ -122,6 +142,23 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p) 
       if (second_word(j) < p.words) dst[second_word(j)] = w;
     }
   }
+}
+
+// Tokens of a block: as many as fill whole rounds of kAhead pieces a thread best (40 heads of 128, 8 pieces each:
+// three tokens make 0.94 of a round; four 1.25, and took 68 us where three take 57 at 16384 tokens).
+int tokens_of_block(int T, int heads, int tasks) {
+  constexpr long long kRound = kThreads * kAhead;
+  int best = 1;
+  double most = 0.0;
+  for (int t = 1; t <= kTokens && t <= T; ++t) {
+    const long long n = static_cast<long long>(t) * heads * tasks;
+    const double used = static_cast<double>(n) / ((n + kRound - 1) / kRound * kRound);
+    if (used > most * 1.01) {
+      most = used;
+      best = t;
+    }
+  }
+  return best;
 }
 
 bool stride_ok(long long s) { return s > 0 && s % 8 == 0 && s < (1LL << 38); }
@@ -201,7 +238,10 @@ moe_status moe_rotary(const moe_heads* x, const int32_t* positions, const double
   p.interleaved = interleaved != 0;
   p.inverse = inverse != 0;
   count_launches(1);
-  return status_of(launch_k(rotary_kernel, (T + kTokens - 1) / kTokens, kThreads, 0, static_cast<cudaStream_t>(stream), p));
+  p.block_tokens = tokens_of_block(T, heads, p.tasks);
+  return status_of(launch_k(rotary_kernel, (T + p.block_tokens - 1) / p.block_tokens, kThreads,
+                            static_cast<size_t>(p.block_tokens) * (R / 2) * sizeof(float2),
+                            static_cast<cudaStream_t>(stream), p));
 }
 
 }  // extern "C"
