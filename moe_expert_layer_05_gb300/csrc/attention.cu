@@ -72,6 +72,9 @@ template <int N>
 __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
+// A value that is the same in all lanes, known as such to the compiler.
+template <class T>
+__device__ __forceinline__ T uniform(T v) { return __shfl_sync(0xffffffffu, v, 0); }
 // A barrier of the arithmetic threads alone.
 __device__ __forceinline__ void arith_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kArith) : "memory"); }
 
@@ -150,30 +153,35 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, 
   for (int c = 0; c < DP / 64; ++c) tma_load_3d(dst + c * Tile<DP>::kChunk, map, bar, 64 * c, head, row);
 }
 
+// The warp that issues the products runs converged, one lane issuing (mma_bf16_ss_warp).
+// Descriptors of a tile's first rows and columns: as the operand of the scores (columns along the
+// contraction) and of the sums (rows along it).
+__device__ __forceinline__ uint64_t scores_desc(const uint8_t* tile) { return smem_desc_sw128(smem_u32(tile), 16, 1024); }
+__device__ __forceinline__ uint64_t sums_desc(const uint8_t* tile) {
+  return smem_desc_sw128(smem_u32(tile), kRows * 128, 1024);
+}
+
 // D[128 x 128] = A[128 rows, DP] B[128 rows, DP]^T
 template <int DP>
-__device__ __forceinline__ void mma_scores(uint32_t d, const uint8_t* a, const uint8_t* b) {
-  const uint32_t aa = smem_u32(a), ba = smem_u32(b);
+__device__ __forceinline__ void mma_scores(uint32_t leader, uint32_t d, uint64_t a, uint64_t b) {
   #pragma unroll
   for (int c = 0; c < DP / 64; ++c)
     #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
-      const uint32_t off = c * Tile<DP>::kChunk + kk * 32;
-      mma_bf16_ss(d, smem_desc_sw128(aa + off, 16, 1024), smem_desc_sw128(ba + off, 16, 1024), Tile<DP>::kScores,
-                  (c | kk) != 0 ? 1u : 0u);
+      const uint64_t off = (c * Tile<DP>::kChunk + kk * 32) >> 4;
+      mma_bf16_ss_warp(leader, d, a + off, b + off, Tile<DP>::kScores, (c | kk) != 0 ? 1u : 0u);
     }
 }
 
 // D[128 x DP] (+)= W[128 x 128] B[128 rows, DP], W in TMEM: its two halves of 64 along
-// the contraction at w and w + half.
+// the contraction at w and w + half; steps [from, to) of eight.
 template <int DP>
-__device__ __forceinline__ void mma_sums(uint32_t d, uint32_t w, uint32_t half, const uint8_t* b, bool add, int from = 0,
-                                         int to = 8) {
-  const uint32_t ba = smem_u32(b);
+__device__ __forceinline__ void mma_sums(uint32_t leader, uint32_t d, uint32_t w, uint32_t half, uint64_t b, bool add,
+                                         int from = 0, int to = 8) {
   #pragma unroll
   for (int kk = from; kk < to; ++kk)
-    mma_bf16_ts(d, w + (kk >> 2) * half + (kk & 3) * 8, smem_desc_sw128(ba + kk * 2048, Tile<DP>::kChunk, 1024),
-                Tile<DP>::kSums, (add || kk != 0) ? 1u : 0u);
+    mma_bf16_ts_warp(leader, d, w + (kk >> 2) * half + (kk & 3) * 8, b + kk * (2048 >> 4), Tile<DP>::kSums,
+                     (add || kk != 0) ? 1u : 0u);
 }
 
 // Words t, t + n, ... of a tile: what is not finite becomes zero.  True where this thread found any.
@@ -266,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* q_smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = q_smem + 2 * C::kBytes;
   FwdBook& bk = *reinterpret_cast<FwdBook*>(ring + ST * C::kBytes);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < 8; ++s) {
       mbar_init(&bk.full[s], 1);
@@ -302,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int q0 = t * (p.pair_rows ? 2 * kRows : kRows);
   row_map<2 * kRows>(p, q0, &bk.map);
   tc_fence_after_sync();
-  const uint32_t tmem = bk.tmem;
+  const uint32_t tmem = uniform(bk.tmem);
   volatile int* abort = &bk.abort_flag;
   const unsigned long long lim = p.wait_ns;
 
@@ -344,51 +352,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       got.drain(bk.full);                    // (they have landed by the end, unless another warp gave up)
     }
    } else if (n > 0 && warp == kMmaWarp) {
-    if (lane == 0) {
-      bool any = false;
-      auto tile = [&](int s) { return ring + (s % ST) * C::kBytes; };
-      auto full = [&](int s) { return mbar_wait(&bk.full[s % ST], (s / ST) & 1, abort, lim); };
-      auto release = [&](int s) { if (s + ST < 2 * n) mma_commit(&bk.empty[s % ST]); };
-      auto in = [&](int u, int i) { return i >= from[u] && i < to[u]; };
-      auto scores = [&](int u, int s) {
-        mma_scores<DP>(tmem + 128 * u, q_smem + u * C::kBytes, tile(s));
-        mma_commit(&bk.s_full[u]);
-        any = true;
-      };
-      bool ok = mbar_wait(&bk.q_full, 0, abort, lim) && full(0);
-      if (ok) {
-        tc_fence_after_sync();
-        for (int u = 0; u < 2; ++u)
-          if (in(u, ib)) scores(u, 0);
-        release(0);
-      }
-      for (int i = ib; ok && i < ib + n; ++i) {
-        const int sk = 2 * (i - ib), sv = sk + 1;               // this key tile's and value tile's turn
-        const bool more = i + 1 < ib + n;
-        if (!full(sv) || (more && !full(sk + 2))) { ok = false; break; }
-        for (int u = 0; u < 2; ++u) {
-          if (in(u, i)) {
-            // (the first half of the keys while the second is still exponentiated)
-            for (int half = 0; half < 2 && ok; ++half) {
-              ok = mbar_wait(&bk.p_full[u][half], (i - from[u]) & 1, abort, lim);
-              tc_fence_after_sync();
-              if (ok)
-                mma_sums<DP>(tmem + 256 + DP * u, tmem + 128 * u, 32, tile(sv), i > from[u] || half, 4 * half,
-                             4 * half + 4);
-            }
-            if (!ok) break;
-            if (i + 1 == to[u]) mma_commit(&bk.o_full[u]);
+    const uint32_t leader = elect_one() ? 1u : 0u;
+    const uint64_t q_desc = scores_desc(q_smem), k_desc = scores_desc(ring), v_desc = sums_desc(ring);
+    const int f0 = uniform(from[0]), f1 = uniform(from[1]), e0 = uniform(to[0]), e1 = uniform(to[1]);
+    const int first = uniform(ib), last = uniform(ib + n) - 1;
+    const int turns = 2 * (last - first + 1);
+    bool any = false, ok = true;
+    auto full = [&](int s) { return warp_wait(&bk.full[s % ST], (s / ST) & 1, abort, lim); };
+    auto release = [&](int s) { if (s + ST < turns) mma_commit_warp(leader, &bk.empty[s % ST]); };
+    auto scores = [&](int u, int s) {
+      mma_scores<DP>(leader, tmem + 128 * u, q_desc + u * (C::kBytes >> 4), k_desc + (s % ST) * (C::kBytes >> 4));
+      mma_commit_warp(leader, &bk.s_full[u]);
+      any = true;
+    };
+    ok = warp_wait(&bk.q_full, 0, abort, lim) && full(0);
+    if (ok) {
+      tc_fence_after_sync();
+      if (first >= f0 && first < e0) scores(0, 0);
+      if (first >= f1 && first < e1) scores(1, 0);
+      release(0);
+    }
+    for (int i = first; ok && i <= last; ++i) {
+      const int sk = 2 * (i - first), sv = sk + 1;              // this key tile's and value tile's turn
+      if (!full(sv) || (i < last && !full(sk + 2))) { ok = false; break; }
+      #pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int f = u ? f1 : f0, e = u ? e1 : e0;
+        if (i >= f && i < e) {
+          // (the first half of the keys while the second is still exponentiated)
+          #pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            ok = ok && warp_wait(&bk.p_full[u][half], (i - f) & 1, abort, lim);
+            tc_fence_after_sync();
+            if (ok)
+              mma_sums<DP>(leader, tmem + 256 + DP * u, tmem + 128 * u, 32, v_desc + (sv % ST) * (C::kBytes >> 4),
+                           i > f || half, 4 * half, 4 * half + 4);
           }
-          if (in(u, i + 1)) scores(u, sk + 2);
+          if (ok && i + 1 == e) mma_commit_warp(leader, &bk.o_full[u]);
         }
-        if (!ok) break;
-        release(sv);
-        if (more) release(sk + 2);
+        if (ok && i + 1 >= f && i + 1 < e) scores(u, sk + 2);
       }
-      if (any) {                             // (TMEM is given back after them, whoever gave up)
-        mma_commit(&bk.drain);
-        mbar_wait_drain(&bk.drain, 0);
-      }
+      if (!ok) break;
+      release(sv);
+      if (i < last) release(sk + 2);
+    }
+    if (any) {                               // (TMEM is given back after them, whoever gave up)
+      mma_commit_warp(leader, &bk.drain);
+      mbar_wait_drain(&bk.drain, 0);
     }
    }
   } else {
@@ -560,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* k_smem = do_smem + C::kBytes;
   uint8_t* v_smem = k_smem + 2 * C::kBytes;
   DqBook& bk = *reinterpret_cast<DqBook*>(v_smem + 2 * C::kBytes);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(&bk.q_full, 1);
     for (int s = 0; s < 2; ++s) {
@@ -590,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int q0 = (p.tiles - 1 - static_cast<int>(blockIdx.x) / p.Hq) * kRows;
   row_map<kRows>(p, q0, &bk.map);
   tc_fence_after_sync();
-  const uint32_t tmem = bk.tmem;
+  const uint32_t tmem = uniform(bk.tmem);
   volatile int* abort = &bk.abort_flag;
   const unsigned long long lim = p.wait_ns;
   const int kv = h / (p.Hq / p.Hkv), top = q0 + kRows;
@@ -622,37 +632,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       got.drain(&bk.q_full);
     }
    } else if (n > 0 && warp == kMmaWarp) {
-    if (lane == 0) {
-      bool any = false;
-      auto scores = [&](int j) {
-        if (!mbar_wait(&bk.k_full[j & 1], (j >> 1) & 1, abort, lim)) return false;
-        tc_fence_after_sync();
-        mma_scores<DP>(tmem + 128 + 128 * (j & 1), q_smem, k_smem + (j & 1) * C::kBytes);
-        mma_commit(&bk.s_full[j & 1]);
-        any = true;
-        return true;
-      };
-      auto dprob = [&](int j) {
-        if (!mbar_wait(&bk.v_full[j & 1], (j >> 1) & 1, abort, lim)) return false;
-        tc_fence_after_sync();
-        mma_scores<DP>(tmem + 384, do_smem, v_smem + (j & 1) * C::kBytes);
-        mma_commit(&bk.dp_full);
-        if (j + 2 < n) mma_commit(&bk.v_empty[j & 1]);
-        return true;
-      };
-      bool ok = mbar_wait(&bk.q_full, 0, abort, lim) && scores(0) && dprob(0);
-      for (int j = 0; ok && j < n; ++j) {
-        if (j + 1 < n && !scores(j + 1)) { ok = false; break; }
-        if (!mbar_wait(&bk.ds_full, j & 1, abort, lim)) { ok = false; break; }
-        tc_fence_after_sync();
-        mma_sums<DP>(tmem, tmem + 384, 64, k_smem + (j & 1) * C::kBytes, j > 0);
-        if (j + 2 < n) mma_commit(&bk.k_empty[j & 1]);
-        if (j + 1 < n && !dprob(j + 1)) { ok = false; break; }
-      }
-      if (any) {
-        mma_commit(&bk.done);
-        mbar_wait_drain(&bk.done, 0);
-      }
+    const uint32_t leader = elect_one() ? 1u : 0u;
+    const uint64_t q_desc = scores_desc(q_smem), do_desc = scores_desc(do_smem), k_desc = scores_desc(k_smem),
+                   v_desc = scores_desc(v_smem), kt_desc = sums_desc(k_smem);
+    constexpr uint64_t kNext = C::kBytes >> 4;
+    const int tiles = uniform(n);
+    bool any = false;
+    auto scores = [&](int j) {
+      if (!warp_wait(&bk.k_full[j & 1], (j >> 1) & 1, abort, lim)) return false;
+      tc_fence_after_sync();
+      mma_scores<DP>(leader, tmem + 128 + 128 * (j & 1), q_desc, k_desc + (j & 1) * kNext);
+      mma_commit_warp(leader, &bk.s_full[j & 1]);
+      any = true;
+      return true;
+    };
+    auto dprob = [&](int j) {
+      if (!warp_wait(&bk.v_full[j & 1], (j >> 1) & 1, abort, lim)) return false;
+      tc_fence_after_sync();
+      mma_scores<DP>(leader, tmem + 384, do_desc, v_desc + (j & 1) * kNext);
+      mma_commit_warp(leader, &bk.dp_full);
+      if (j + 2 < tiles) mma_commit_warp(leader, &bk.v_empty[j & 1]);
+      return true;
+    };
+    bool ok = warp_wait(&bk.q_full, 0, abort, lim) && scores(0) && dprob(0);
+    for (int j = 0; ok && j < tiles; ++j) {
+      if (j + 1 < tiles && !scores(j + 1)) { ok = false; break; }
+      if (!warp_wait(&bk.ds_full, j & 1, abort, lim)) { ok = false; break; }
+      tc_fence_after_sync();
+      mma_sums<DP>(leader, tmem, tmem + 384, 64, kt_desc + (j & 1) * kNext, j > 0);
+      if (j + 2 < tiles) mma_commit_warp(leader, &bk.k_empty[j & 1]);
+      if (j + 1 < tiles && !dprob(j + 1)) { ok = false; break; }
+    }
+    if (any) {
+      mma_commit_warp(leader, &bk.done);
+      mbar_wait_drain(&bk.done, 0);
     }
    }
   } else {
@@ -818,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* do_smem = q_smem + 2 * C::kBytes;
   float* st_smem = reinterpret_cast<float*>(do_smem + 2 * C::kBytes);          // [2][-lse log2 e, -delta][128]
   DkvBook& bk = *reinterpret_cast<DkvBook*>(st_smem + 4 * kRows);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(&bk.kv_full, 1);
     for (int s = 0; s < 2; ++s) {
@@ -848,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kv = static_cast<int>(blockIdx.x) % p.Hkv, k0 = static_cast<int>(blockIdx.x) / p.Hkv * kRows;
   row_map<kRows>(p, k0, &bk.map);
   tc_fence_after_sync();
-  const uint32_t tmem = bk.tmem;
+  const uint32_t tmem = uniform(bk.tmem);
   volatile int* abort = &bk.abort_flag;
   const unsigned long long lim = p.wait_ns;
   const int group = p.Hq / p.Hkv;
@@ -890,40 +903,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       got.drain(&bk.kv_full);
     }
    } else if (n > 0 && warp == kMmaWarp) {
-    if (lane == 0) {
-      bool any = false;
-      auto scores = [&](int j) {
-        if (!mbar_wait(&bk.q_full[j & 1], (j >> 1) & 1, abort, lim)) return false;
-        tc_fence_after_sync();
-        mma_scores<DP>(tmem + 256, k_smem, q_smem + (j & 1) * C::kBytes);
-        mma_commit(&bk.s_full);
-        any = true;
-        return true;
-      };
-      auto dprob = [&](int j) {
-        if (!mbar_wait(&bk.do_full[j & 1], (j >> 1) & 1, abort, lim)) return false;
-        tc_fence_after_sync();
-        mma_scores<DP>(tmem + 384, v_smem, do_smem + (j & 1) * C::kBytes);
-        mma_commit(&bk.dp_full);
-        return true;
-      };
-      bool ok = mbar_wait(&bk.kv_full, 0, abort, lim) && scores(0) && dprob(0);
-      for (int j = 0; ok && j < n; ++j) {
-        if (!mbar_wait(&bk.p_full, j & 1, abort, lim)) { ok = false; break; }
-        tc_fence_after_sync();
-        mma_sums<DP>(tmem + 128, tmem + 256, 64, do_smem + (j & 1) * C::kBytes, j > 0);
-        if (j + 2 < n) mma_commit(&bk.do_empty[j & 1]);
-        if (j + 1 < n && !scores(j + 1)) { ok = false; break; }
-        if (!mbar_wait(&bk.ds_full, j & 1, abort, lim)) { ok = false; break; }
-        tc_fence_after_sync();
-        mma_sums<DP>(tmem, tmem + 384, 64, q_smem + (j & 1) * C::kBytes, j > 0);
-        if (j + 2 < n) mma_commit(&bk.q_empty[j & 1]);
-        if (j + 1 < n && !dprob(j + 1)) { ok = false; break; }
-      }
-      if (any) {
-        mma_commit(&bk.done);
-        mbar_wait_drain(&bk.done, 0);
-      }
+    const uint32_t leader = elect_one() ? 1u : 0u;
+    const uint64_t k_desc = scores_desc(k_smem), v_desc = scores_desc(v_smem), q_desc = scores_desc(q_smem),
+                   do_desc = scores_desc(do_smem), qt_desc = sums_desc(q_smem), dot_desc = sums_desc(do_smem);
+    constexpr uint64_t kNext = C::kBytes >> 4;
+    const int tiles = uniform(n);
+    bool any = false;
+    auto scores = [&](int j) {
+      if (!warp_wait(&bk.q_full[j & 1], (j >> 1) & 1, abort, lim)) return false;
+      tc_fence_after_sync();
+      mma_scores<DP>(leader, tmem + 256, k_desc, q_desc + (j & 1) * kNext);
+      mma_commit_warp(leader, &bk.s_full);
+      any = true;
+      return true;
+    };
+    auto dprob = [&](int j) {
+      if (!warp_wait(&bk.do_full[j & 1], (j >> 1) & 1, abort, lim)) return false;
+      tc_fence_after_sync();
+      mma_scores<DP>(leader, tmem + 384, v_desc, do_desc + (j & 1) * kNext);
+      mma_commit_warp(leader, &bk.dp_full);
+      return true;
+    };
+    bool ok = warp_wait(&bk.kv_full, 0, abort, lim) && scores(0) && dprob(0);
+    for (int j = 0; ok && j < tiles; ++j) {
+      if (!warp_wait(&bk.p_full, j & 1, abort, lim)) { ok = false; break; }
+      tc_fence_after_sync();
+      mma_sums<DP>(leader, tmem + 128, tmem + 256, 64, dot_desc + (j & 1) * kNext, j > 0);
+      if (j + 2 < tiles) mma_commit_warp(leader, &bk.do_empty[j & 1]);
+      if (j + 1 < tiles && !scores(j + 1)) { ok = false; break; }
+      if (!warp_wait(&bk.ds_full, j & 1, abort, lim)) { ok = false; break; }
+      tc_fence_after_sync();
+      mma_sums<DP>(leader, tmem, tmem + 384, 64, qt_desc + (j & 1) * kNext, j > 0);
+      if (j + 2 < tiles) mma_commit_warp(leader, &bk.q_empty[j & 1]);
+      if (j + 1 < tiles && !dprob(j + 1)) { ok = false; break; }
+    }
+    if (any) {
+      mma_commit_warp(leader, &bk.done);
+      mbar_wait_drain(&bk.done, 0);
     }
    }
   } else {

@@ -305,6 +305,34 @@ __device__ __forceinline__ void mma_nvf4_ss(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
+// The same two, and the commit, for a warp that runs converged: every lane calls with the same
+// operands and the lane whose `leader` is set issues.  Without a branch around them the operands stay
+// in uniform registers, which is where these instructions take them from; behind `if (lane == 0)` each
+// one is moved there first, some 100 cycles an MMA against the 64 that a 128 x 128 x 16 product runs.
+__device__ __forceinline__ void mma_bf16_ss_warp(uint32_t leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                 uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred P, L;\n setp.ne.b32 P, %4, 0;\n setp.ne.b32 L, %5, 0;\n"
+      " @L tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, P;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void mma_bf16_ts_warp(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                                 uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred P, L;\n setp.ne.b32 P, %4, 0;\n setp.ne.b32 L, %5, 0;\n"
+      " @L tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, P;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_warp(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred L;\n setp.ne.b32 L, %1, 0;\n"
+      " @L tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+      "r"(leader)
+      : "memory");
+}
+
 // Copy 32 rows x 16 bytes from shared memory into TMEM, replicated into the
 // four 32-lane quarters: lane i (of every quarter), column c receives bytes
 // [4c, 4c+4) of row i.  Used for the MXFP8 scale factors.
