@@ -6,8 +6,10 @@ is not a GB300 the calls raise.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -63,19 +65,6 @@ class MoeGemmArgs(ctypes.Structure):
                 ("qt_codes", c_vp), ("qt_scales", c_vp)]
 
 
-class MoeHeads(ctypes.Structure):
-    _fields_ = [("data", c_vp), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
-
-
-class MoeAttentionConfig(ctypes.Structure):
-    _fields_ = [("T", c_i32), ("sequences", c_i32), ("q_heads", c_i32), ("kv_heads", c_i32), ("head_dim", c_i32),
-                ("scale", c_f32)]
-
-
-class MoeTensor(ctypes.Structure):
-    _fields_ = [("data", c_vp), ("n", ctypes.c_int64), ("type", c_i32)]
-
-
 _P = ctypes.POINTER
 _SIGS = {
     "moe_status_string": (ctypes.c_char_p, [c_i32]),
@@ -118,22 +107,22 @@ _SIGS = {
     "moe_cross_entropy_forward": (c_i32, [c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_sz, c_vp]),
     "moe_cross_entropy_backward": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp,
                                            c_vp, c_sz, c_vp]),
-    "moe_attention_workspace_bytes": (c_sz, [_P(MoeAttentionConfig)]),
-    "moe_attention_forward": (c_i32, [_P(MoeAttentionConfig), _P(MoeHeads), _P(MoeHeads), _P(MoeHeads), c_vp,
-                                      _P(MoeHeads), c_vp, c_vp, c_sz, c_vp]),
-    "moe_attention_backward": (c_i32, [_P(MoeAttentionConfig), _P(MoeHeads), _P(MoeHeads), _P(MoeHeads), c_vp,
-                                       _P(MoeHeads), c_vp, _P(MoeHeads), _P(MoeHeads), _P(MoeHeads), _P(MoeHeads),
+    "moe_attention_workspace_bytes": (c_sz, [c_vp]),
+    "moe_attention_forward": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp,
+                                      c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "moe_attention_backward": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp,
+                                       c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
                                        c_vp, c_sz, c_vp]),
     "moe_rotary_frequencies": (c_i32, [c_i32, c_f64, c_i32, c_f64, c_i32, c_f64, c_f64, _P(c_f64), _P(c_f32)]),
-    "moe_rotary": (c_i32, [_P(MoeHeads), c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_i32, c_f32, c_i32, _P(MoeHeads),
+    "moe_rotary": (c_i32, [c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_i32, c_f32, c_i32, c_vp,
                            c_vp]),
     "moe_balance_loss_workspace_bytes": (c_sz, [c_i32, c_i32]),
     "moe_balance_loss_forward": (c_i32, [c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_sz,
                                          c_vp]),
     "moe_balance_loss_backward": (c_i32, [c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp]),
     "moe_grad_norm_workspace_bytes": (c_sz, [c_i32]),
-    "moe_grad_norm": (c_i32, [_P(MoeTensor), c_i32, c_vp, c_vp, c_sz, c_vp]),
-    "moe_grad_clip": (c_i32, [_P(MoeTensor), _P(MoeTensor), c_i32, c_vp, c_f32, c_vp]),
+    "moe_grad_norm": (c_i32, [c_vp, c_i32, c_vp, c_vp, c_sz, c_vp]),
+    "moe_grad_clip": (c_i32, [c_vp, c_vp, c_i32, c_vp, c_f32, c_vp]),
 }
 
 _lib = None
@@ -478,34 +467,35 @@ def moe_cross_entropy_backward(x, w, labels, lse, dloss, dx, dw, ws, piece: int 
 
 
 # ---------------------------------------------------------------- attention
-def _heads(t, name: str, shape, dev: int) -> MoeHeads:
-    """A [T, heads, width] bf16 tensor on GPU `dev` with a contiguous last dimension, in any order of the others."""
-    if t.dtype is not _BF16 or t.shape != shape or t.get_device() != dev or (t.stride(2) != 1 and shape[2] != 1):
-        raise ValueError(f"{name}: expected {tuple(shape)} of {_BF16} on the current GPU, its last dimension contiguous, "
-                         f"got {tuple(t.shape)} of {t.dtype} on {t.device}, strides {tuple(t.stride())}")
-    return MoeHeads(t.data_ptr(), t.stride(0), t.stride(1))
+# moe_heads, moe_tensor and moe_attention_config cross as packed bytes: a ctypes structure takes 1 us to make.
+def _heads(t, name: str, shape, dev: int) -> tuple[int, int, int]:
+    """The fields of moe_heads for a [T, heads, width] bf16 tensor on GPU `dev` with a contiguous last dimension."""
+    strides = t.stride()
+    if t.dtype is _BF16 and t.shape == shape and t.get_device() == dev and (strides[2] == 1 or shape[2] == 1):
+        return t.data_ptr(), strides[0], strides[1]
+    raise ValueError(f"{name}: expected {tuple(shape)} of {_BF16} on the current GPU, its last dimension contiguous, "
+                     f"got {tuple(t.shape)} of {t.dtype} on {t.device}, strides {strides}")
 
 
-def _attention(q, k, cu_seqlens, scale, dev: int):
-    """The config of a call, and the shapes of q and of k and v."""
+def _attention(q, k, cu_seqlens, scale):
+    """Bytes of the config, number of sequences, shapes of q and of k and v."""
     if len(q.shape) != 3 or len(k.shape) != 3:
         raise ValueError(f"q, k: expected three dimensions, got {tuple(q.shape)} and {tuple(k.shape)}")
     T, Hq, D = q.shape
     Hkv, n = k.shape[1], cu_seqlens.numel() - 1
     if n < 0:
         raise ValueError("cu_seqlens: expected the sequences' first rows and the last one's end")
-    if not (_sized(T, Hq, Hkv, D) and _sized(n, 0)):
+    if not (_sized(T, Hq, Hkv, D) and n <= _MAX_SIZE):
         raise MoeError(-1, "q, k, cu_seqlens")
     if scale is None:
         scale = D ** -0.5 if D > 0 else 1.0
-    return MoeAttentionConfig(T, n, Hq, Hkv, D, scale), (T, Hq, D), (T, Hkv, D)
+    return struct.pack("5if", T, n, Hq, Hkv, D, scale), n, (T, Hq, D), (T, Hkv, D)
 
 
 def moe_attention_workspace_bytes(T: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
     if not _sized(T, q_heads, kv_heads, head_dim):
         return 0
-    return int(load().moe_attention_workspace_bytes(ctypes.byref(MoeAttentionConfig(T, 1, q_heads, kv_heads, head_dim,
-                                                                                    1.0))))
+    return load().moe_attention_workspace_bytes(struct.pack("5if", T, 1, q_heads, kv_heads, head_dim, 1.0))
 
 
 def moe_attention_forward(q, k, v, cu_seqlens, out, lse, ws, scale: float | None = None, stream=None) -> None:
@@ -515,26 +505,30 @@ def moe_attention_forward(q, k, v, cu_seqlens, out, lse, ws, scale: float | None
     rows and the last one's end; lse [q_heads, T] fp32; scale 1/sqrt(D) unless given.
     """
     dev = _device()
-    cfg, sq, sk = _attention(q, k, cu_seqlens, scale, dev)
+    cfg, n, sq, sk = _attention(q, k, cu_seqlens, scale)
     wp, wn = _scratch(ws, dev)
-    check(load().moe_attention_forward(cfg, _heads(q, "q", sq, dev), _heads(k, "k", sk, dev), _heads(v, "v", sk, dev),
-                                       _tensor(cu_seqlens, "cu_seqlens", _I32, (cfg.sequences + 1,), dev),
-                                       _heads(out, "out", sq, dev), _tensor(lse, "lse", _F32, (sq[1], sq[0]), dev),
-                                       wp, wn, stream_ptr(stream, dev)), "moe_attention_forward")
+    heads = array.array("q", _heads(q, "q", sq, dev) + _heads(k, "k", sk, dev) + _heads(v, "v", sk, dev)
+                        + _heads(out, "out", sq, dev))
+    at = heads.buffer_info()[0]
+    check(load().moe_attention_forward(cfg, at, at + 24, at + 48, _tensor(cu_seqlens, "cu_seqlens", _I32, (n + 1,), dev),
+                                       at + 72, _tensor(lse, "lse", _F32, (sq[1], sq[0]), dev), wp, wn,
+                                       stream_ptr(stream, dev)), "moe_attention_forward")
 
 
 def moe_attention_backward(q, k, v, cu_seqlens, out, lse, dout, dq, dk, dv, ws, scale: float | None = None,
                            stream=None) -> None:
     """dq, dk, dv of sum <dout, out>; q, k, v, out, lse (and scale) as in the forward call."""
     dev = _device()
-    cfg, sq, sk = _attention(q, k, cu_seqlens, scale, dev)
+    cfg, n, sq, sk = _attention(q, k, cu_seqlens, scale)
     wp, wn = _scratch(ws, dev)
-    check(load().moe_attention_backward(cfg, _heads(q, "q", sq, dev), _heads(k, "k", sk, dev), _heads(v, "v", sk, dev),
-                                        _tensor(cu_seqlens, "cu_seqlens", _I32, (cfg.sequences + 1,), dev),
-                                        _heads(out, "out", sq, dev), _tensor(lse, "lse", _F32, (sq[1], sq[0]), dev),
-                                        _heads(dout, "dout", sq, dev), _heads(dq, "dq", sq, dev),
-                                        _heads(dk, "dk", sk, dev), _heads(dv, "dv", sk, dev), wp, wn,
-                                        stream_ptr(stream, dev)), "moe_attention_backward")
+    heads = array.array("q", _heads(q, "q", sq, dev) + _heads(k, "k", sk, dev) + _heads(v, "v", sk, dev)
+                        + _heads(out, "out", sq, dev) + _heads(dout, "dout", sq, dev) + _heads(dq, "dq", sq, dev)
+                        + _heads(dk, "dk", sk, dev) + _heads(dv, "dv", sk, dev))
+    at = heads.buffer_info()[0]
+    check(load().moe_attention_backward(cfg, at, at + 24, at + 48, _tensor(cu_seqlens, "cu_seqlens", _I32, (n + 1,), dev),
+                                        at + 72, _tensor(lse, "lse", _F32, (sq[1], sq[0]), dev), at + 96, at + 120,
+                                        at + 144, at + 168, wp, wn, stream_ptr(stream, dev)),
+          "moe_attention_backward")
 
 
 def moe_rotary_frequencies(R: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
@@ -561,10 +555,12 @@ def moe_rotary(x, positions, freq, out, interleaved: bool = False, scale: float 
     pairs = freq.numel()
     if not _sized(T, heads, width, 2 * pairs):
         raise MoeError(-1, "x, freq")
-    check(load().moe_rotary(_heads(x, "x", shape, dev), _tensor(positions, "positions", _I32, (T,), dev),
+    both = array.array("q", _heads(x, "x", shape, dev) + _heads(out, "out", shape, dev))
+    at = both.buffer_info()[0]
+    check(load().moe_rotary(at, _tensor(positions, "positions", _I32, (T,), dev),
                             _tensor(freq, "freq", torch.float64, (pairs,), dev), T, heads, width, 2 * pairs,
-                            1 if interleaved else 0, scale, 1 if inverse else 0, _heads(out, "out", shape, dev),
-                            stream_ptr(stream, dev)), "moe_rotary")
+                            1 if interleaved else 0, scale, 1 if inverse else 0, at + 24, stream_ptr(stream, dev)),
+          "moe_rotary")
 
 
 # ---------------------------------------------------------------- balance loss
@@ -602,16 +598,16 @@ def moe_balance_loss_backward(logits, slope, dloss, dlogits, tokens=None, score:
 
 
 # ---------------------------------------------------------------- gradient norm
-def _tensors(ts, name: str, dev: int):
-    """Descriptions of contiguous bf16 or fp32 tensors on GPU `dev`."""
-    out = (MoeTensor * max(len(ts), 1))()
-    for d, t in zip(out, ts):
+def _tensors(ts, name: str, dev: int) -> array.array:
+    """moe_tensor of each contiguous bf16 or fp32 tensor on GPU `dev`, as 64-bit words (the type in the low half)."""
+    words = []
+    for t in ts:
         dtype = t.dtype
         if (dtype is not _F32 and dtype is not _BF16) or t.get_device() != dev or not t.is_contiguous():
             raise ValueError(f"{name}: expected contiguous tensors of {_F32} or {_BF16} on the current GPU, got one of "
                              f"{dtype} on {t.device}" + ("" if t.is_contiguous() else ", not contiguous"))
-        d.data, d.n, d.type = t.data_ptr(), t.numel(), 1 if dtype is _F32 else 0
-    return out
+        words += (t.data_ptr(), t.numel(), 1 if dtype is _F32 else 0)
+    return array.array("q", words)
 
 
 def moe_grad_norm_workspace_bytes(n: int) -> int:
@@ -622,22 +618,20 @@ def moe_grad_norm(grads, norm, ws, stream=None) -> None:
     """norm [1] = the 2-norm of all tensors of the list (bf16 or fp32) together."""
     dev = _device()
     wp, wn = _scratch(ws, dev)
-    check(load().moe_grad_norm(_tensors(grads, "grads", dev), len(grads), _tensor(norm, "norm", _F32, (1,), dev), wp, wn,
+    words = _tensors(grads, "grads", dev)
+    check(load().moe_grad_norm(words.buffer_info()[0], len(grads), _tensor(norm, "norm", _F32, (1,), dev), wp, wn,
                                stream_ptr(stream, dev)), "moe_grad_norm")
 
 
 def moe_grad_clip(grads, norm, limit: float, outs=None, stream=None) -> None:
-    """Every tensor times min(1, limit / (norm + 1e-6)), in place or into outs (tensors of the same shapes)."""
+    """Every tensor times min(1, limit / (norm + 1e-6)), in place or into outs (tensors of the same sizes and types)."""
     dev = _device()
-    if outs is not None:
-        if len(outs) != len(grads):
-            raise ValueError(f"outs: expected {len(grads)} tensors, got {len(outs)}")
-        for g, o in zip(grads, outs):
-            if g.shape != o.shape or g.dtype is not o.dtype:
-                raise ValueError(f"outs: expected {tuple(g.shape)} of {g.dtype}, got {tuple(o.shape)} of {o.dtype}")
-    check(load().moe_grad_clip(_tensors(grads, "grads", dev), None if outs is None else _tensors(outs, "outs", dev),
-                               len(grads), _tensor(norm, "norm", _F32, (1,), dev), limit, stream_ptr(stream, dev)),
-          "moe_grad_clip")
+    words = _tensors(grads, "grads", dev)
+    to = None if outs is None else _tensors(outs, "outs", dev)
+    if to is not None and (to[1::3] != words[1::3] or to[2::3] != words[2::3]):
+        raise ValueError("outs: expected as many tensors as the gradients, of the same sizes and types")
+    check(load().moe_grad_clip(words.buffer_info()[0], None if to is None else to.buffer_info()[0], len(grads),
+                               _tensor(norm, "norm", _F32, (1,), dev), limit, stream_ptr(stream, dev)), "moe_grad_clip")
 
 
 # ---------------------------------------------------------------- buffers

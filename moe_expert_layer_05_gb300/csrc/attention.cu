@@ -35,6 +35,7 @@ namespace {
 
 constexpr int kRows = 128;                 // rows of a tile
 constexpr int kArith = 256;                // threads that work on the scores
+constexpr int kMaxSmem = 232448;
 constexpr int kThreads = kArith + 128;     // and four warps, of which one loads and one issues the products
 constexpr int kLoadWarp = kArith / 32, kMmaWarp = kLoadWarp + 1;
 constexpr uint32_t kFull = 0xffffffffu;
@@ -77,6 +78,13 @@ template <class T>
 __device__ __forceinline__ T uniform(T v) { return __shfl_sync(0xffffffffu, v, 0); }
 // A barrier of the arithmetic threads alone.
 __device__ __forceinline__ void arith_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kArith) : "memory"); }
+
+// Whether what a kernel keeps in shared memory ends inside what it was given.
+__device__ __forceinline__ bool smem_fits(const uint8_t* base, const void* end) {
+  uint32_t given;
+  asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(given));
+  return static_cast<const uint8_t*>(end) <= base + given;
+}
 
 // ---------------------------------------------------------------- sequences
 // Where the sequences of rows r0 .. r0 + R - 1 begin and end.
@@ -274,6 +282,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* q_smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = q_smem + 2 * C::kBytes;
   FwdBook& bk = *reinterpret_cast<FwdBook*>(ring + ST * C::kBytes);
+  if (!smem_fits(smem_raw, &bk + 1)) {
+    pdl_wait();
+    if (threadIdx.x == 0) set_status(p.status, kErrLaunch);
+    return;
+  }
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < 8; ++s) {
@@ -543,15 +556,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- gradients
 // dq: 128 query rows of one head against their key tiles.  TMEM: dq DP columns from 0,
-// two score buffers at 128 and 256, dp at 384 (which becomes ds).  The scores of the
-// next key tile run while this one's ds is worked out.
+// scores at 128, two buffers of dp at 256 and 384 (each becomes ds).  Both products of the
+// next key tile run while this one's ds is worked out, the scores once they have been read.
 //
 // delta comes from the rounded out, an error of out's rounding in each of its products.  Where a
 // row sees few keys that is of the size of ds; rows that begin within their first key tile
 // take delta = sum_j p dp there instead.  Either goes to stats, for dk.
+constexpr int kKStages = 3;                // key tiles in flight: one is held from its scores to its dq
 struct DqBook {
-  uint64_t q_full, k_full[2], v_full[2];
-  uint64_t k_empty[2], v_empty[2], s_full[2], dp_full, ds_full, done;
+  uint64_t q_full, k_full[kKStages], v_full[2];
+  uint64_t k_empty[kKStages], v_empty[2], s_full, s_empty, dp_full[2], ds_full, done;
   uint32_t tmem;
   int abort_flag;
   RowMap map;
@@ -568,19 +582,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* q_smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* do_smem = q_smem + C::kBytes;
   uint8_t* k_smem = do_smem + C::kBytes;
-  uint8_t* v_smem = k_smem + 2 * C::kBytes;
+  uint8_t* v_smem = k_smem + kKStages * C::kBytes;
   DqBook& bk = *reinterpret_cast<DqBook*>(v_smem + 2 * C::kBytes);
+  if (!smem_fits(smem_raw, &bk + 1)) {
+    pdl_wait();
+    if (threadIdx.x == 0) set_status(p.status, kErrLaunch);
+    return;
+  }
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(&bk.q_full, 1);
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kKStages; ++s) {
       mbar_init(&bk.k_full[s], 1);
-      mbar_init(&bk.v_full[s], 1);
       mbar_init(&bk.k_empty[s], 1);
-      mbar_init(&bk.v_empty[s], 1);
-      mbar_init(&bk.s_full[s], 1);
     }
-    mbar_init(&bk.dp_full, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bk.v_full[s], 1);
+      mbar_init(&bk.v_empty[s], 1);
+      mbar_init(&bk.dp_full[s], 1);
+    }
+    mbar_init(&bk.s_full, 1);
+    mbar_init(&bk.s_empty, 8);
     mbar_init(&bk.ds_full, 8);
     mbar_init(&bk.done, 1);
     bk.abort_flag = 0;
@@ -618,16 +640,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       got.note(0, 0);
       bool ok = true;
       for (int j = 0; j < n && ok; ++j) {
-        const int s = j & 1, row = top - kRows * (j + 1);
-        const uint32_t ph = (j >> 1) & 1;
-        if (j >= 2 && !mbar_wait(&bk.k_empty[s], ph ^ 1u, abort, lim)) { ok = false; break; }
+        const int s = j % kKStages, s2 = j & 1, row = top - kRows * (j + 1);
+        const uint32_t ph = (j / kKStages) & 1, ph2 = (j >> 1) & 1;
+        if (j >= kKStages && !mbar_wait(&bk.k_empty[s], ph ^ 1u, abort, lim)) { ok = false; break; }
         mbar_arrive_expect_tx(&bk.k_full[s], C::kBytes);
         load_tile<DP>(k_smem + s * C::kBytes, &tmK, &bk.k_full[s], kv, row);
         got.note(1 + s, ph);
-        if (j >= 2 && !mbar_wait(&bk.v_empty[s], ph ^ 1u, abort, lim)) { ok = false; break; }
-        mbar_arrive_expect_tx(&bk.v_full[s], C::kBytes);
-        load_tile<DP>(v_smem + s * C::kBytes, &tmV, &bk.v_full[s], kv, row);
-        got.note(3 + s, ph);
+        if (j >= 2 && !mbar_wait(&bk.v_empty[s2], ph2 ^ 1u, abort, lim)) { ok = false; break; }
+        mbar_arrive_expect_tx(&bk.v_full[s2], C::kBytes);
+        load_tile<DP>(v_smem + s2 * C::kBytes, &tmV, &bk.v_full[s2], kv, row);
+        got.note(1 + kKStages + s2, ph2);
       }
       got.drain(&bk.q_full);
     }
@@ -638,30 +660,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint64_t kNext = C::kBytes >> 4;
     const int tiles = uniform(n);
     bool any = false;
-    auto scores = [&](int j) {
-      if (!warp_wait(&bk.k_full[j & 1], (j >> 1) & 1, abort, lim)) return false;
+    auto products = [&](int j) {
+      if (!warp_wait(&bk.k_full[j % kKStages], (j / kKStages) & 1, abort, lim) || (j > 0 && !warp_wait(&bk.s_empty, (j - 1) & 1, abort, lim)))
+        return false;
       tc_fence_after_sync();
-      mma_scores<DP>(leader, tmem + 128 + 128 * (j & 1), q_desc, k_desc + (j & 1) * kNext);
-      mma_commit_warp(leader, &bk.s_full[j & 1]);
+      mma_scores<DP>(leader, tmem + 128, q_desc, k_desc + (j % kKStages) * kNext);
+      mma_commit_warp(leader, &bk.s_full);
       any = true;
-      return true;
-    };
-    auto dprob = [&](int j) {
       if (!warp_wait(&bk.v_full[j & 1], (j >> 1) & 1, abort, lim)) return false;
       tc_fence_after_sync();
-      mma_scores<DP>(leader, tmem + 384, do_desc, v_desc + (j & 1) * kNext);
-      mma_commit_warp(leader, &bk.dp_full);
+      mma_scores<DP>(leader, tmem + 256 + 128 * (j & 1), do_desc, v_desc + (j & 1) * kNext);
+      mma_commit_warp(leader, &bk.dp_full[j & 1]);
       if (j + 2 < tiles) mma_commit_warp(leader, &bk.v_empty[j & 1]);
       return true;
     };
-    bool ok = warp_wait(&bk.q_full, 0, abort, lim) && scores(0) && dprob(0);
+    bool ok = warp_wait(&bk.q_full, 0, abort, lim) && products(0);
     for (int j = 0; ok && j < tiles; ++j) {
-      if (j + 1 < tiles && !scores(j + 1)) { ok = false; break; }
+      if (j + 1 < tiles && !products(j + 1)) { ok = false; break; }
       if (!warp_wait(&bk.ds_full, j & 1, abort, lim)) { ok = false; break; }
       tc_fence_after_sync();
-      mma_sums<DP>(leader, tmem, tmem + 384, 64, kt_desc + (j & 1) * kNext, j > 0);
-      if (j + 2 < tiles) mma_commit_warp(leader, &bk.k_empty[j & 1]);
-      if (j + 1 < tiles && !dprob(j + 1)) { ok = false; break; }
+      mma_sums<DP>(leader, tmem, tmem + 256 + 128 * (j & 1), 64, kt_desc + (j % kKStages) * kNext, j > 0);
+      if (j + kKStages < tiles) mma_commit_warp(leader, &bk.k_empty[j % kKStages]);
     }
     if (any) {
       mma_commit_warp(leader, &bk.done);
@@ -704,16 +723,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (masked && j == 0) arith_sync();        // (the others come to theirs)
         return false;
       };
-      if (!warp_wait(&bk.s_full[j & 1], (j >> 1) & 1, abort, lim)) return give_up();
+      if (!warp_wait(&bk.s_full, j & 1, abort, lim)) return give_up();
       tc_fence_after_sync();
       const int k0 = top - kRows * (j + 1);
       const int lo = max(key_lo, k0) - k0 - 64 * half, hi = min(key_hi, k0 + kRows) - k0 - 64 * half;
       uint32_t s[2][32], d[2][32];
       #pragma unroll
-      for (int c = 0; c < 2; ++c) tmem_ld_x32(tmem + lanes + 128 + 128 * (j & 1) + 64 * half + 32 * c, s[c]);
+      for (int c = 0; c < 2; ++c) tmem_ld_x32(tmem + lanes + 128 + 64 * half + 32 * c, s[c]);
+      #pragma unroll
+      for (int c = 0; c < 2; ++c) tmem_ld_wait(s[c]);
+      warp_arrive(&bk.s_empty, lane);
       #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        tmem_ld_wait(s[c]);
         #pragma unroll
         for (int x = 0; x < 32; x += 2) {
           float2 y = split_f32x2(fma2(make_f32x2(as_f(s[c][x]), as_f(s[c][x + 1])), mul2_, lse2));
@@ -728,13 +749,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (masked) {
-        if (!warp_wait(&bk.k_full[j & 1], (j >> 1) & 1, abort, lim)) return give_up();
-        clean_tile<DP>(k_smem + (j & 1) * C::kBytes, threadIdx.x, kArith);
+        if (!warp_wait(&bk.k_full[j % kKStages], (j / kKStages) & 1, abort, lim)) return give_up();
+        clean_tile<DP>(k_smem + (j % kKStages) * C::kBytes, threadIdx.x, kArith);
       }
-      if (!warp_wait(&bk.dp_full, j & 1, abort, lim)) return give_up();
+      if (!warp_wait(&bk.dp_full[j & 1], (j >> 1) & 1, abort, lim)) return give_up();
+      const uint32_t tdp = tmem + lanes + 256 + 128 * (j & 1) + 64 * half;
       tc_fence_after_sync();
       #pragma unroll
-      for (int c = 0; c < 2; ++c) tmem_ld_x32(tmem + lanes + 384 + 64 * half + 32 * c, d[c]);
+      for (int c = 0; c < 2; ++c) tmem_ld_x32(tdp + 32 * c, d[c]);
       #pragma unroll
       for (int c = 0; c < 2; ++c) tmem_ld_wait(d[c]);
       if (masked && j == 0) {
@@ -770,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           w[16 * c + x / 2] = pack_bf16x2(y.x, y.y);
         }
-      tmem_st_x32(tmem + lanes + 384 + 64 * half, w);
+      tmem_st_x32(tdp, w);
       tmem_st_wait();
       warp_arrive(&bk.ds_full, lane);
       return true;
@@ -810,9 +832,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // DP columns from 0 and 128, scores at 256 (which become p), dp at 384 (ds).  In the
 // order dv(j), scores(j + 1), dk(j), dp(j + 1) each buffer is free again when its turn
 // comes, and the arithmetic on one has the time of two products.
+constexpr int kQStages = 3;                // query tiles in flight: one is held from its scores to its dk
 struct DkvBook {
-  uint64_t kv_full, q_full[2], do_full[2];
-  uint64_t q_empty[2], do_empty[2], s_full, p_full, dp_full, ds_full, done;
+  uint64_t kv_full, q_full[kQStages], do_full[2];
+  uint64_t q_empty[kQStages], do_empty[2], s_full, p_full, dp_full, ds_full, done;
   uint32_t tmem;
   int abort_flag;
   RowMap map;
@@ -828,16 +851,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* k_smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* v_smem = k_smem + C::kBytes;
   uint8_t* q_smem = v_smem + C::kBytes;
-  uint8_t* do_smem = q_smem + 2 * C::kBytes;
-  float* st_smem = reinterpret_cast<float*>(do_smem + 2 * C::kBytes);          // [2][-lse log2 e, -delta][128]
-  DkvBook& bk = *reinterpret_cast<DkvBook*>(st_smem + 4 * kRows);
+  uint8_t* do_smem = q_smem + kQStages * C::kBytes;
+  float* lse_smem = reinterpret_cast<float*>(do_smem + 2 * C::kBytes);         // [2][128] -lse log2 e, with do
+  float* delta_smem = lse_smem + 2 * kRows;                                    // [kQStages][128] -delta, with q
+  DkvBook& bk = *reinterpret_cast<DkvBook*>(delta_smem + kQStages * kRows);
+  if (!smem_fits(smem_raw, &bk + 1)) {
+    pdl_wait();
+    if (threadIdx.x == 0) set_status(p.status, kErrLaunch);
+    return;
+  }
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(&bk.kv_full, 1);
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kQStages; ++s) {
       mbar_init(&bk.q_full[s], 1);
-      mbar_init(&bk.do_full[s], 1);
       mbar_init(&bk.q_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bk.do_full[s], 1);
       mbar_init(&bk.do_empty[s], 1);
     }
     mbar_init(&bk.s_full, 1);
@@ -882,18 +913,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int h = kv * group, row = k0;
       for (int j = 0; j < n && ok; ++j) {
-        const int s = j & 1;
-        const uint32_t ph = (j >> 1) & 1;
-        if (j >= 2 && !mbar_wait(&bk.q_empty[s], ph ^ 1u, abort, lim)) { ok = false; break; }
-        mbar_arrive_expect_tx(&bk.q_full[s], C::kBytes + 2 * kRows * 4);
+        const int s = j % kQStages, s2 = j & 1;
+        const uint32_t ph = (j / kQStages) & 1, ph2 = (j >> 1) & 1;
+        if (j >= kQStages && !mbar_wait(&bk.q_empty[s], ph ^ 1u, abort, lim)) { ok = false; break; }
+        mbar_arrive_expect_tx(&bk.q_full[s], C::kBytes + kRows * 4);
         load_tile<DP>(q_smem + s * C::kBytes, &tmQ, &bk.q_full[s], h, row);
-        bulk_load(st_smem + 2 * s * kRows, p.stats + h * p.pitch + row, kRows * 4, &bk.q_full[s]);
-        bulk_load(st_smem + (2 * s + 1) * kRows, p.stats + (p.Hq + h) * p.pitch + row, kRows * 4, &bk.q_full[s]);
+        bulk_load(delta_smem + s * kRows, p.stats + (p.Hq + h) * p.pitch + row, kRows * 4, &bk.q_full[s]);
         got.note(1 + s, ph);
-        if (j >= 2 && !mbar_wait(&bk.do_empty[s], ph ^ 1u, abort, lim)) { ok = false; break; }
-        mbar_arrive_expect_tx(&bk.do_full[s], C::kBytes);
-        load_tile<DP>(do_smem + s * C::kBytes, &tmDo, &bk.do_full[s], h, row);
-        got.note(3 + s, ph);
+        if (j >= 2 && !mbar_wait(&bk.do_empty[s2], ph2 ^ 1u, abort, lim)) { ok = false; break; }
+        mbar_arrive_expect_tx(&bk.do_full[s2], C::kBytes + kRows * 4);
+        load_tile<DP>(do_smem + s2 * C::kBytes, &tmDo, &bk.do_full[s2], h, row);
+        bulk_load(lse_smem + s2 * kRows, p.stats + h * p.pitch + row, kRows * 4, &bk.do_full[s2]);
+        got.note(1 + kQStages + s2, ph2);
         row += kRows;
         if (row >= k0 + nq * kRows) {
           row = k0;
@@ -910,9 +941,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tiles = uniform(n);
     bool any = false;
     auto scores = [&](int j) {
-      if (!warp_wait(&bk.q_full[j & 1], (j >> 1) & 1, abort, lim)) return false;
+      if (!warp_wait(&bk.q_full[j % kQStages], (j / kQStages) & 1, abort, lim)) return false;
       tc_fence_after_sync();
-      mma_scores<DP>(leader, tmem + 256, k_desc, q_desc + (j & 1) * kNext);
+      mma_scores<DP>(leader, tmem + 256, k_desc, q_desc + (j % kQStages) * kNext);
       mma_commit_warp(leader, &bk.s_full);
       any = true;
       return true;
@@ -933,8 +964,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (j + 1 < tiles && !scores(j + 1)) { ok = false; break; }
       if (!warp_wait(&bk.ds_full, j & 1, abort, lim)) { ok = false; break; }
       tc_fence_after_sync();
-      mma_sums<DP>(leader, tmem, tmem + 384, 64, qt_desc + (j & 1) * kNext, j > 0);
-      if (j + 2 < tiles) mma_commit_warp(leader, &bk.q_empty[j & 1]);
+      mma_sums<DP>(leader, tmem, tmem + 384, 64, qt_desc + (j % kQStages) * kNext, j > 0);
+      if (j + kQStages < tiles) mma_commit_warp(leader, &bk.q_empty[j % kQStages]);
       if (j + 1 < tiles && !dprob(j + 1)) { ok = false; break; }
     }
     if (any) {
@@ -956,11 +987,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     auto step = [&](int j, int q0, auto masked_c) {
       constexpr bool masked = decltype(masked_c)::value;
-      if (!warp_wait(&bk.q_full[j & 1], (j >> 1) & 1, abort, lim) || !warp_wait(&bk.s_full, j & 1, abort, lim)) return false;
+      if (!warp_wait(&bk.q_full[j % kQStages], (j / kQStages) & 1, abort, lim) ||
+          !warp_wait(&bk.do_full[j & 1], (j >> 1) & 1, abort, lim) || !warp_wait(&bk.s_full, j & 1, abort, lim))
+        return false;
       tc_fence_after_sync();
       const int lo = max(key, q0) - q0 - 64 * half, hi = min(key_end, q0 + kRows) - q0 - 64 * half;   // queries [lo, hi)
-      const float4* lse = reinterpret_cast<const float4*>(st_smem + 2 * (j & 1) * kRows + 64 * half);
-      const float4* delta = lse + kRows / 4;
+      const float4* lse = reinterpret_cast<const float4*>(lse_smem + (j & 1) * kRows + 64 * half);
+      const float4* delta = reinterpret_cast<const float4*>(delta_smem + (j % kQStages) * kRows + 64 * half);
       uint32_t s[2][32], w[32];
       #pragma unroll
       for (int c = 0; c < 2; ++c) tmem_ld_x32(tmem + lanes + 256 + 64 * half + 32 * c, s[c]);
@@ -989,9 +1022,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tmem_st_x32(tmem + lanes + 256 + 64 * half, w);
       if (masked) {
-        if (!warp_wait(&bk.do_full[j & 1], (j >> 1) & 1, abort, lim)) return false;
         clean_tile<DP>(do_smem + (j & 1) * C::kBytes, threadIdx.x, kArith);
-        clean_tile<DP>(q_smem + (j & 1) * C::kBytes, threadIdx.x, kArith);
+        clean_tile<DP>(q_smem + (j % kQStages) * C::kBytes, threadIdx.x, kArith);
       }
       tmem_st_wait();
       warp_arrive(&bk.p_full, lane);
@@ -1061,15 +1093,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- host
+// What a kernel uses, and up to 1 KB in front of it for the first 1024-byte boundary (of which there
+// may be less: each kernel looks).
+constexpr int smem_of(int used) { return used + 1024 < kMaxSmem ? used + 1024 : kMaxSmem; }
 template <int DP>
-constexpr int fwd_smem() { return 1024 + (2 + Tile<DP>::kStages) * Tile<DP>::kBytes + static_cast<int>(sizeof(FwdBook)); }
+constexpr int fwd_smem() { return (2 + Tile<DP>::kStages) * Tile<DP>::kBytes + static_cast<int>(sizeof(FwdBook)); }
 template <int DP>
-constexpr int dq_smem() { return 1024 + 6 * Tile<DP>::kBytes + static_cast<int>(sizeof(DqBook)); }
+constexpr int dq_smem() { return (4 + kKStages) * Tile<DP>::kBytes + static_cast<int>(sizeof(DqBook)); }
 template <int DP>
 constexpr int dkv_smem() {
-  return 1024 + 6 * Tile<DP>::kBytes + 4 * kRows * 4 + static_cast<int>(sizeof(DkvBook));
+  return (4 + kQStages) * Tile<DP>::kBytes + (2 + kQStages) * kRows * 4 + static_cast<int>(sizeof(DkvBook));
 }
-static_assert(fwd_smem<128>() <= 232448 && dq_smem<128>() <= 232448 && dkv_smem<128>() <= 232448, "shared memory");
+static_assert(fwd_smem<128>() <= kMaxSmem && dq_smem<128>() <= kMaxSmem && dkv_smem<128>() <= kMaxSmem, "shared memory");
 
 template <class... KArgs, class... Args>
 cudaError_t launch_big(void (*kern)(KArgs...), std::atomic<bool>* attr_set, int grid, int smem, cudaStream_t st,
@@ -1139,7 +1174,7 @@ cudaError_t forward(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensor
                     cudaStream_t st) {
   static std::atomic<bool> attr_set[kMaxDevices];
   const int grid = p.tiles * (p.pair_rows ? p.Hq : p.Hq / 2);
-  return launch_big(attention_fwd_kernel<DP>, attr_set, grid, fwd_smem<DP>(), st, tq, tk, tv, p);
+  return launch_big(attention_fwd_kernel<DP>, attr_set, grid, smem_of(fwd_smem<DP>()), st, tq, tk, tv, p);
 }
 template <int DP>
 cudaError_t backward(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& td,
@@ -1147,11 +1182,11 @@ cudaError_t backward(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
   static std::atomic<bool> dq_set[kMaxDevices], dkv_set[kMaxDevices];
   p.d0 = dq;
   const cudaError_t e =
-      launch_big(attention_dq_kernel<DP>, dq_set, p.tiles * p.Hq, dq_smem<DP>(), st, tq, tk, tv, td, p);
+      launch_big(attention_dq_kernel<DP>, dq_set, p.tiles * p.Hq, smem_of(dq_smem<DP>()), st, tq, tk, tv, td, p);
   if (e != cudaSuccess) return e;
   p.d0 = dk;
   p.d1 = dv;
-  return launch_big(attention_dkv_kernel<DP>, dkv_set, p.tiles * p.Hkv, dkv_smem<DP>(), st, tq, tk, tv, td, p);
+  return launch_big(attention_dkv_kernel<DP>, dkv_set, p.tiles * p.Hkv, smem_of(dkv_smem<DP>()), st, tq, tk, tv, td, p);
 }
 
 }  // namespace
