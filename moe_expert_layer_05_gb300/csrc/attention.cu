@@ -52,6 +52,7 @@ struct AttnParams {
   float scale, scale2;     // scale, scale * log2 e
   int pair_rows;           // forward: the two tiles of a CTA are rows of one head (else two heads of one group)
   int tiles;               // tiles along the rows
+  int split;               // dk, dv: CTAs that share a group's heads
   Heads o, d0, d1;         // forward: out; gradients: dq or dk, dv
   Heads dout;
   float* lse;              // [Hq, T]
@@ -221,6 +222,7 @@ __device__ __forceinline__ bool clean_tile(uint8_t* tile, int t, int n) {
   return true;
 }
 
+__device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
 __device__ __forceinline__ float as_f(uint32_t v) { return __uint_as_float(v); }
 
 // A warp's wait: its lanes go on together or, if one has given up, not at all.
@@ -832,10 +834,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 // DP columns from 0 and 128, scores at 256 (which become p), dp at 384 (ds).  In the
 // order dv(j), scores(j + 1), dk(j), dp(j + 1) each buffer is free again when its turn
 // comes, and the arithmetic on one has the time of two products.
+//
+// The heads of a group may be shared out among the CTAs of a cluster (p.split of them): each leaves
+// its sums in its shared memory, and each adds up its share of the rows over all of them, in
+// the order of the CTAs, through distributed shared memory.
 constexpr int kQStages = 3;                // query tiles in flight: one is held from its scores to its dk
 struct DkvBook {
   uint64_t kv_full, q_full[kQStages], do_full[2];
-  uint64_t q_empty[kQStages], do_empty[2], s_full, p_full, dp_full, ds_full, done;
+  uint64_t q_empty[kQStages], do_empty[2], s_full, p_full[2], dp_full, ds_full, done;
   uint32_t tmem;
   int abort_flag;
   RowMap map;
@@ -854,6 +860,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* do_smem = q_smem + kQStages * C::kBytes;
   float* lse_smem = reinterpret_cast<float*>(do_smem + 2 * C::kBytes);         // [2][128] -lse log2 e, with do
   float* delta_smem = lse_smem + 2 * kRows;                                    // [kQStages][128] -delta, with q
+  float4* sums = reinterpret_cast<float4*>(q_smem);                            // [dk, dv][128][DP], in place of q and do
   DkvBook& bk = *reinterpret_cast<DkvBook*>(delta_smem + kQStages * kRows);
   if (!smem_fits(smem_raw, &bk + 1)) {
     pdl_wait();
@@ -872,7 +879,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bk.do_empty[s], 1);
     }
     mbar_init(&bk.s_full, 1);
-    mbar_init(&bk.p_full, 8);
+    mbar_init(&bk.p_full[0], 8);
+    mbar_init(&bk.p_full[1], 8);
     mbar_init(&bk.dp_full, 1);
     mbar_init(&bk.ds_full, 8);
     mbar_init(&bk.done, 1);
@@ -889,17 +897,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before_sync();
   pdl_wait();
-  const int kv = static_cast<int>(blockIdx.x) % p.Hkv, k0 = static_cast<int>(blockIdx.x) / p.Hkv * kRows;
+  const int split = p.split, rank = static_cast<int>(blockIdx.x) % split, item = static_cast<int>(blockIdx.x) / split;
+  const int kv = item % p.Hkv, k0 = item / p.Hkv * kRows;
   row_map<kRows>(p, k0, &bk.map);
   tc_fence_after_sync();
   const uint32_t tmem = uniform(bk.tmem);
   volatile int* abort = &bk.abort_flag;
   const unsigned long long lim = p.wait_ns;
   const int group = p.Hq / p.Hkv;
-  // query tiles k0, k0 + 128, ... up to the end of the last key's sequence, for each head
+  // query tiles k0, k0 + 128, ... up to the end of the last key's sequence, for each of this CTA's heads
   const int a = max(k0, bk.map.first), b = min(k0 + kRows, bk.map.last);
   const int end = a < b ? end_of(&bk.map, k0, b - 1, kRows / 32) : k0;
-  const int nq = a < b ? (end - k0 + kRows - 1) / kRows : 0, n = nq * group;
+  const int nq = a < b ? (end - k0 + kRows - 1) / kRows : 0, n = nq * (group / split);
 
   if (warp >= kLoadWarp) {
    fewer_registers<kOtherRegs>();
@@ -911,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       load_tile<DP>(v_smem, &tmV, &bk.kv_full, kv, k0);
       got.note(0, 0);
       bool ok = true;
-      int h = kv * group, row = k0;
+      int h = kv * group + rank * (group / split), row = k0;
       for (int j = 0; j < n && ok; ++j) {
         const int s = j % kQStages, s2 = j & 1;
         const uint32_t ph = (j / kQStages) & 1, ph2 = (j >> 1) & 1;
@@ -957,9 +966,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     bool ok = warp_wait(&bk.kv_full, 0, abort, lim) && scores(0) && dprob(0);
     for (int j = 0; ok && j < tiles; ++j) {
-      if (!warp_wait(&bk.p_full, j & 1, abort, lim)) { ok = false; break; }
-      tc_fence_after_sync();
-      mma_sums<DP>(leader, tmem + 128, tmem + 256, 64, dot_desc + (j & 1) * kNext, j > 0);
+      // (the first 32 queries of each half while the others are still exponentiated)
+      #pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        ok = ok && warp_wait(&bk.p_full[part], j & 1, abort, lim);
+        if (!ok) break;
+        tc_fence_after_sync();
+        #pragma unroll
+        for (int half = 0; half < 2; ++half)
+          mma_sums<DP>(leader, tmem + 128, tmem + 256, 64, dot_desc + (j & 1) * kNext, j > 0 || part + half > 0,
+                       4 * half + 2 * part, 4 * half + 2 * part + 2);
+      }
+      if (!ok) break;
       if (j + 2 < tiles) mma_commit_warp(leader, &bk.do_empty[j & 1]);
       if (j + 1 < tiles && !scores(j + 1)) { ok = false; break; }
       if (!warp_wait(&bk.ds_full, j & 1, abort, lim)) { ok = false; break; }
@@ -994,12 +1012,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lo = max(key, q0) - q0 - 64 * half, hi = min(key_end, q0 + kRows) - q0 - 64 * half;   // queries [lo, hi)
       const float4* lse = reinterpret_cast<const float4*>(lse_smem + (j & 1) * kRows + 64 * half);
       const float4* delta = reinterpret_cast<const float4*>(delta_smem + (j % kQStages) * kRows + 64 * half);
-      uint32_t s[2][32], w[32];
+      uint32_t s[2][32];
       #pragma unroll
       for (int c = 0; c < 2; ++c) tmem_ld_x32(tmem + lanes + 256 + 64 * half + 32 * c, s[c]);
       #pragma unroll
+      for (int c = 0; c < 2; ++c) tmem_ld_wait(s[c]);
+      if (masked) {
+        clean_tile<DP>(do_smem + (j & 1) * C::kBytes, threadIdx.x, kArith);
+        clean_tile<DP>(q_smem + (j % kQStages) * C::kBytes, threadIdx.x, kArith);
+      }
+      #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        tmem_ld_wait(s[c]);
+        uint32_t w[16];
         #pragma unroll
         for (int x = 0; x < 32; x += 4) {
           const float4 l4 = lse[8 * c + x / 4];
@@ -1016,20 +1040,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 4; ++e)
               v[e] = (32 * c + x + e < lo || 32 * c + x + e >= hi) ? 0.f : fmaf(0.f, dd[e], v[e]);
           }
-          w[16 * c + x / 2] = pack_bf16x2(v[0], v[1]);
-          w[16 * c + x / 2 + 1] = pack_bf16x2(v[2], v[3]);
+          w[x / 2] = pack_bf16x2(v[0], v[1]);
+          w[x / 2 + 1] = pack_bf16x2(v[2], v[3]);
         }
+        tmem_st_x16(tmem + lanes + 256 + 64 * half + 16 * c, w);
+        tmem_st_wait();
+        warp_arrive(&bk.p_full[c], lane);
       }
-      tmem_st_x32(tmem + lanes + 256 + 64 * half, w);
-      if (masked) {
-        clean_tile<DP>(do_smem + (j & 1) * C::kBytes, threadIdx.x, kArith);
-        clean_tile<DP>(q_smem + (j % kQStages) * C::kBytes, threadIdx.x, kArith);
-      }
-      tmem_st_wait();
-      warp_arrive(&bk.p_full, lane);
       if (!warp_wait(&bk.dp_full, j & 1, abort, lim)) return false;
       tc_fence_after_sync();
-      uint32_t d[2][32];
+      uint32_t d[2][32], w[32];
       #pragma unroll
       for (int c = 0; c < 2; ++c) tmem_ld_x32(tmem + lanes + 384 + 64 * half + 32 * c, d[c]);
       #pragma unroll
@@ -1069,6 +1089,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Heads& to = half == 0 ? p.d0 : p.d1;
       const float mul = half == 0 ? p.scale : 1.f;
       __nv_bfloat16* out = to.p + key * to.token + kv * to.head;
+      float4* row = sums + (half * kRows + key - k0) * (DP / 4);
       #pragma unroll
       for (int c = 0; c < DP / 32; ++c) {
         uint32_t o[32];
@@ -1077,10 +1098,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait(o);
         #pragma unroll
         for (int x = 0; x < 32; ++x) v[x] = as_f(o[x]) * mul;
-        if (valid) store_cols(out, 32 * c, p.D, v);
+        if (split == 1) {
+          if (valid) store_cols(out, 32 * c, p.D, v);
+        } else {
+          #pragma unroll
+          for (int x = 0; x < 8; ++x)
+            row[(8 * c + x) ^ (key & (DP / 4 - 1))] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+        }
       }
     }
-  }  }
+   }
+  }
+  if (split > 1 && n > 0) {                 // (n is the same in all CTAs of a cluster)
+    __syncwarp();
+    cluster_sync();
+    const int each = (kRows + split - 1) / split, r0 = rank * each, rows = min(each, kRows - r0);
+    for (int i = threadIdx.x; i < 2 * rows * (DP / 8); i += kThreads) {
+      const int w = i % (DP / 8), r = r0 + i / (DP / 8) % rows, half = i / (DP / 8) / rows, key = k0 + r;
+      const float4* mine = sums + (half * kRows + r) * (DP / 4);
+      const uint32_t lo = smem_u32(mine + ((2 * w) ^ (key & (DP / 4 - 1)))), hi = smem_u32(mine + ((2 * w + 1) ^ (key & (DP / 4 - 1))));
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+      for (int c = 0; c < split; ++c) {
+        x = add4(x, ld_cluster_v4(mapa_shared(lo, c)));
+        y = add4(y, ld_cluster_v4(mapa_shared(hi, c)));
+      }
+      const Heads& to = half == 0 ? p.d0 : p.d1;
+      if (key >= bk.map.first && key < bk.map.last && 8 * w < p.D)
+        *reinterpret_cast<uint4*>(to.p + key * to.token + kv * to.head + 8 * w) =
+            make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+    }
+    cluster_sync();                         // (the others read this CTA's shared memory until here)
+  }
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
@@ -1106,8 +1154,9 @@ constexpr int dkv_smem() {
 }
 static_assert(fwd_smem<128>() <= kMaxSmem && dq_smem<128>() <= kMaxSmem && dkv_smem<128>() <= kMaxSmem, "shared memory");
 
+// Launch of kThreads-wide blocks with much shared memory, in clusters of `cluster`.
 template <class... KArgs, class... Args>
-cudaError_t launch_big(void (*kern)(KArgs...), std::atomic<bool>* attr_set, int grid, int smem, cudaStream_t st,
+cudaError_t launch_big(void (*kern)(KArgs...), std::atomic<bool>* attr_set, int grid, int smem, cudaStream_t st, int cluster,
                        Args&&... args) {
   const int dev = current_device();
   if (dev < 0) return cudaErrorInvalidDevice;
@@ -1116,8 +1165,35 @@ cudaError_t launch_big(void (*kern)(KArgs...), std::atomic<bool>* attr_set, int 
     if (e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // (see launch_k)
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = kThreads;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   count_launches(1);
-  return launch_k(kern, grid, kThreads, smem, st, args...);
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+
+// CTAs that share the heads of a group in dk and dv's kernel.  As few as leave no CTA more than 5/4 of an SM's share of
+// one long sequence's tiles: a CTA of the first keys has tiles * group / split of them, an SM (tiles + 1) tiles
+// q_heads / 2 / 152.  Large batches take one: clusters of four leave SMs of a GPC idle (8192 rows, 32/8 heads of
+// 128, backward: 1.38 ms alone, 1.41 in pairs, 1.56 by four); small ones gain (2048 rows, 32/4 heads: 0.28, 0.19, 0.16 and,
+// by eight, 0.23 ms; 1000 rows, 6/2 heads of 80: 69 us, 47 by three).
+int group_split(const AttnParams& p) {
+  const int group = p.Hq / p.Hkv;
+  int best = 1;
+  for (int c = 2; c <= 8 && static_cast<long long>(best) * (p.tiles + 1) * p.Hkv < 243; ++c)
+    if (group % c == 0) best = c;
+  return best;
 }
 
 // How a tensor's strides count where a dimension has one element: as if it were dense.
@@ -1174,7 +1250,7 @@ cudaError_t forward(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensor
                     cudaStream_t st) {
   static std::atomic<bool> attr_set[kMaxDevices];
   const int grid = p.tiles * (p.pair_rows ? p.Hq : p.Hq / 2);
-  return launch_big(attention_fwd_kernel<DP>, attr_set, grid, smem_of(fwd_smem<DP>()), st, tq, tk, tv, p);
+  return launch_big(attention_fwd_kernel<DP>, attr_set, grid, smem_of(fwd_smem<DP>()), st, 1, tq, tk, tv, p);
 }
 template <int DP>
 cudaError_t backward(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& td,
@@ -1182,11 +1258,13 @@ cudaError_t backward(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
   static std::atomic<bool> dq_set[kMaxDevices], dkv_set[kMaxDevices];
   p.d0 = dq;
   const cudaError_t e =
-      launch_big(attention_dq_kernel<DP>, dq_set, p.tiles * p.Hq, smem_of(dq_smem<DP>()), st, tq, tk, tv, td, p);
+      launch_big(attention_dq_kernel<DP>, dq_set, p.tiles * p.Hq, smem_of(dq_smem<DP>()), st, 1, tq, tk, tv, td, p);
   if (e != cudaSuccess) return e;
   p.d0 = dk;
   p.d1 = dv;
-  return launch_big(attention_dkv_kernel<DP>, dkv_set, p.tiles * p.Hkv, smem_of(dkv_smem<DP>()), st, tq, tk, tv, td, p);
+  p.split = group_split(p);
+  return launch_big(attention_dkv_kernel<DP>, dkv_set, p.tiles * p.Hkv * p.split, smem_of(dkv_smem<DP>()), st, p.split,
+                    tq, tk, tv, td, p);
 }
 
 }  // namespace
