@@ -34,10 +34,11 @@ namespace moe {
 namespace {
 
 constexpr int kRows = 128;                 // rows of a tile
-constexpr int kArith = 256;                // threads that work on the scores
 constexpr int kMaxSmem = 232448;
-constexpr int kThreads = kArith + 128;     // and four warps, of which one loads and one issues the products
-constexpr int kLoadWarp = kArith / 32, kMmaWarp = kLoadWarp + 1;
+// Warps that work on the scores, then four more, of which one loads and one issues the products.
+constexpr int kFwdArith = 256, kFwdThreads = kFwdArith + 128;
+constexpr int kBwdArith = 512, kBwdThreads = kBwdArith + 128;
+constexpr int kParts = kBwdArith / kRows;  // gradients: threads that share a row, 32 columns each
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kMaxTokens = 1 << 24, kMaxHeads = 1024, kMaxHeadDim = 128, kMaxSequences = 1 << 24;
 
@@ -56,16 +57,17 @@ struct AttnParams {
   Heads o, d0, d1;         // forward: out; gradients: dq or dk, dv
   Heads dout;
   float* lse;              // [Hq, T]
-  float* stats;            // [2][Hq, pitch]: -lse log2 e, -delta
+  uint4* stats;            // [2][Hq, pitch]: -lse / scale, -delta, each as eight bf16 (split_row)
   long long pitch;
   int* status;
   unsigned long long wait_ns;
 };
 
-// Registers move from the warps that load and issue to those that work on the scores:
-// 8 x 32 x 216 + 4 x 32 x 72 = 12 x 32 x 168, what the block is launched with.
-constexpr int kArithRegs = 216, kOtherRegs = 72;
-static_assert(kArith * kArithRegs + (kThreads - kArith) * kOtherRegs <= kThreads * 168, "registers of a block");
+// Registers move from the warps that load and issue to those that work on the scores; the block is
+// launched with as many as a thread of it can have.
+constexpr int kFwdRegs = 216, kFwdOtherRegs = 72, kBwdRegs = 104, kBwdOtherRegs = 64;
+static_assert(kFwdArith * kFwdRegs + 128 * kFwdOtherRegs <= kFwdThreads * 168, "registers of a block");
+static_assert(kBwdArith * kBwdRegs + 128 * kBwdOtherRegs <= kBwdThreads * 96, "registers of a block");
 template <int N>
 __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -78,7 +80,7 @@ __device__ __forceinline__ void fewer_registers() {
 template <class T>
 __device__ __forceinline__ T uniform(T v) { return __shfl_sync(0xffffffffu, v, 0); }
 // A barrier of the arithmetic threads alone.
-__device__ __forceinline__ void arith_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kArith) : "memory"); }
+__device__ __forceinline__ void arith_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kBwdArith) : "memory"); }
 
 // Whether what a kernel keeps in shared memory ends inside what it was given.
 __device__ __forceinline__ bool smem_fits(const uint8_t* base, const void* end) {
@@ -109,7 +111,7 @@ __device__ __forceinline__ void row_map(const AttnParams& p, int r0, RowMap* m) 
   }
   __syncthreads();
   int lo = 0, hi = p.T;
-  for (int i = threadIdx.x; i <= p.B; i += kThreads) {
+  for (int i = threadIdx.x; i <= p.B; i += blockDim.x) {
     const int c = p.cu[i];
     if (c <= r0)
       lo = max(lo, c);
@@ -170,6 +172,15 @@ __device__ __forceinline__ uint64_t sums_desc(const uint8_t* tile) {
   return smem_desc_sw128(smem_u32(tile), kRows * 128, 1024);
 }
 
+// Descriptor of 128 rows of 16 columns, not swizzled: the first eight columns as 16 bytes a row at
+// `rows`, the other eight at `rest`, further on.
+__device__ __forceinline__ uint64_t rows_desc(const uint8_t* rows, const uint8_t* rest) {
+  return static_cast<uint64_t>((smem_u32(rows) & 0x3FFFFu) >> 4) |
+         static_cast<uint64_t>((smem_u32(rest) - smem_u32(rows)) >> 4) << 16 |   // between the two halves
+         static_cast<uint64_t>(128u >> 4) << 32 |                               // between groups of eight rows
+         static_cast<uint64_t>(1) << 46;                                        // descriptor version for tcgen05
+}
+
 // D[128 x 128] = A[128 rows, DP] B[128 rows, DP]^T
 template <int DP>
 __device__ __forceinline__ void mma_scores(uint32_t leader, uint32_t d, uint64_t a, uint64_t b) {
@@ -182,14 +193,15 @@ __device__ __forceinline__ void mma_scores(uint32_t leader, uint32_t d, uint64_t
     }
 }
 
-// D[128 x DP] (+)= W[128 x 128] B[128 rows, DP], W in TMEM: its two halves of 64 along
-// the contraction at w and w + half; steps [from, to) of eight.
-template <int DP>
-__device__ __forceinline__ void mma_sums(uint32_t leader, uint32_t d, uint32_t w, uint32_t half, uint64_t b, bool add,
-                                         int from = 0, int to = 8) {
+// D[128 x DP] (+)= W[128 x 128] B[128 rows, DP], W in TMEM as one thread's packed values after the other's: SPAN steps
+// of 16 rows along the contraction side by side, the next ones 16 SPAN columns further (where the
+// thread's scores were); steps [from, to) of eight.
+template <int DP, int SPAN>
+__device__ __forceinline__ void mma_sums(uint32_t leader, uint32_t d, uint32_t w, uint64_t b, bool add, int from = 0,
+                                         int to = 8) {
   #pragma unroll
   for (int kk = from; kk < to; ++kk)
-    mma_bf16_ts_warp(leader, d, w + (kk >> 2) * half + (kk & 3) * 8, b + kk * (2048 >> 4), Tile<DP>::kSums,
+    mma_bf16_ts_warp(leader, d, w + kk / SPAN * (16 * SPAN) + kk % SPAN * 8, b + kk * (2048 >> 4), Tile<DP>::kSums,
                      (add || kk != 0) ? 1u : 0u);
 }
 
@@ -274,8 +286,10 @@ struct FwdBook {
   RowMap map;
 };
 
+constexpr int kFwdLoadWarp = kFwdArith / 32, kFwdMmaWarp = kFwdLoadWarp + 1;
+
 template <int DP>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kFwdThreads, 1)
     attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const AttnParams p) {
   using C = Tile<DP>;
@@ -311,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&tmK);
     prefetch_tensormap(&tmV);
   }
-  if (warp == kMmaWarp) {
+  if (warp == kFwdMmaWarp) {
     tmem_alloc(&bk.tmem, 512);
     tmem_relinquish();
   }
@@ -345,9 +359,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int ib = on1 ? from[1] : from[0];
   const int n = (on0 || on1) ? max(to[0], to[1]) - ib : 0;      // key tiles of this CTA
 
-  if (warp >= kLoadWarp) {
-   fewer_registers<kOtherRegs>();
-   if (n > 0 && warp == kLoadWarp) {
+  if (warp >= kFwdLoadWarp) {
+   fewer_registers<kFwdOtherRegs>();
+   if (n > 0 && warp == kFwdLoadWarp) {
     if (lane == 0) {
       Issued got;
       mbar_arrive_expect_tx(&bk.q_full, (on0 ? C::kBytes : 0) + (on1 ? C::kBytes : 0));
@@ -366,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       got.drain(bk.full);                    // (they have landed by the end, unless another warp gave up)
     }
-   } else if (n > 0 && warp == kMmaWarp) {
+   } else if (n > 0 && warp == kFwdMmaWarp) {
     const uint32_t leader = elect_one() ? 1u : 0u;
     const uint64_t q_desc = scores_desc(q_smem), k_desc = scores_desc(ring), v_desc = sums_desc(ring);
     const int f0 = uniform(from[0]), f1 = uniform(from[1]), e0 = uniform(to[0]), e1 = uniform(to[1]);
@@ -400,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = ok && warp_wait(&bk.p_full[u][half], (i - f) & 1, abort, lim);
             tc_fence_after_sync();
             if (ok)
-              mma_sums<DP>(leader, tmem + 256 + DP * u, tmem + 128 * u, 32, v_desc + (sv % ST) * (C::kBytes >> 4),
+              mma_sums<DP, 8>(leader, tmem + 256 + DP * u, tmem + 128 * u, v_desc + (sv % ST) * (C::kBytes >> 4),
                            i > f || half, 4 * half, 4 * half + 4);
           }
           if (ok && i + 1 == e) mma_commit_warp(leader, &bk.o_full[u]);
@@ -417,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
    }
   } else {
-   more_registers<kArithRegs>();
+   more_registers<kFwdRegs>();
    if (n > 0) {
     // ------------------------------------------------ a thread a row
     const int u = warp >> 2;
@@ -550,13 +564,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   pdl_launch_next();
   if (threadIdx.x == 0 && bk.abort_flag) set_status(p.status, kErrTimeout);
-  if (warp == kMmaWarp) {
+  if (warp == kFwdMmaWarp) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
   }
 }
 
 // ---------------------------------------------------------------- gradients
+// Four threads share a row of scores, 32 columns each.  (Two, with half as many warps, left the loop
+// waiting for its own latencies a third of the time: a step of dk and dv 2900 cycles, whatever the width.)
+constexpr int kBwdLoadWarp = kBwdArith / 32, kBwdMmaWarp = kBwdLoadWarp + 1;
+
+// A value as three bf16 whose sum has its 24 bits, and five zeros.
+__device__ __forceinline__ uint4 split_row(float v) {
+  const __nv_bfloat16 a = __float2bfloat16(v);
+  const float r = v - __bfloat162float(a);
+  const __nv_bfloat16 b = __float2bfloat16(r), c = __float2bfloat16(r - __bfloat162float(b));
+  return make_uint4(static_cast<uint32_t>(__bfloat16_as_ushort(a)) | static_cast<uint32_t>(__bfloat16_as_ushort(b)) << 16,
+                    __bfloat16_as_ushort(c), 0u, 0u);
+}
+
 // dq: 128 query rows of one head against their key tiles.  TMEM: dq DP columns from 0,
 // scores at 128, two buffers of dp at 256 and 384 (each becomes ds).  Both products of the
 // next key tile run while this one's ds is worked out, the scores once they have been read.
@@ -571,11 +598,11 @@ struct DqBook {
   uint32_t tmem;
   int abort_flag;
   RowMap map;
-  float sums[2][2][kRows];                 // halves of rows that two threads share
+  float sums[kParts][kRows];               // parts of rows' sums
 };
 
 template <int DP>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kBwdThreads, 1)
     attention_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDo,
                         const AttnParams p) {
@@ -604,8 +631,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bk.dp_full[s], 1);
     }
     mbar_init(&bk.s_full, 1);
-    mbar_init(&bk.s_empty, 8);
-    mbar_init(&bk.ds_full, 8);
+    mbar_init(&bk.s_empty, kBwdArith / 32);
+    mbar_init(&bk.ds_full, kBwdArith / 32);
     mbar_init(&bk.done, 1);
     bk.abort_flag = 0;
     fence_mbarrier_init();
@@ -614,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&tmV);
     prefetch_tensormap(&tmDo);
   }
-  if (warp == kMmaWarp) {
+  if (warp == kBwdMmaWarp) {
     tmem_alloc(&bk.tmem, 512);
     tmem_relinquish();
   }
@@ -631,9 +658,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int a = max(q0, bk.map.first), b = min(top, bk.map.last);
   const int n = a < b ? (top - start_of(&bk.map, q0, a) + kRows - 1) / kRows : 0;
 
-  if (warp >= kLoadWarp) {
-   fewer_registers<kOtherRegs>();
-   if (n > 0 && warp == kLoadWarp) {
+  if (warp >= kBwdLoadWarp) {
+   fewer_registers<kBwdOtherRegs>();
+   if (n > 0 && warp == kBwdLoadWarp) {
     if (lane == 0) {
       Issued got;
       mbar_arrive_expect_tx(&bk.q_full, 2 * C::kBytes);
@@ -655,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       got.drain(&bk.q_full);
     }
-   } else if (n > 0 && warp == kMmaWarp) {
+   } else if (n > 0 && warp == kBwdMmaWarp) {
     const uint32_t leader = elect_one() ? 1u : 0u;
     const uint64_t q_desc = scores_desc(q_smem), do_desc = scores_desc(do_smem), k_desc = scores_desc(k_smem),
                    v_desc = scores_desc(v_smem), kt_desc = sums_desc(k_smem);
@@ -681,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (j + 1 < tiles && !products(j + 1)) { ok = false; break; }
       if (!warp_wait(&bk.ds_full, j & 1, abort, lim)) { ok = false; break; }
       tc_fence_after_sync();
-      mma_sums<DP>(leader, tmem, tmem + 256 + 128 * (j & 1), 64, kt_desc + (j % kKStages) * kNext, j > 0);
+      mma_sums<DP, 2>(leader, tmem, tmem + 256 + 128 * (j & 1), kt_desc + (j % kKStages) * kNext, j > 0);
       if (j + kKStages < tiles) mma_commit_warp(leader, &bk.k_empty[j % kKStages]);
     }
     if (any) {
@@ -690,33 +717,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
    }
   } else {
-   more_registers<kArithRegs>();
+   more_registers<kBwdRegs>();
    if (n > 0) {
-    // a thread a row, the two groups of four warps each half of the keys
-    const int half = warp >> 2;
+    const int part = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const int row = q0 + (warp & 3) * 32 + lane;
+    const int lr = (warp & 3) * 32 + lane, row = q0 + lr;
     const bool valid = row >= bk.map.first && row < bk.map.last;
     const int key_lo = valid ? start_of(&bk.map, q0, row) : p.T, key_hi = valid ? row : -1;
     const int all_from = start_of(&bk.map, q0, b - 1);
-    const int lr = row - q0;
-    float delta = 0.f, lse = 0.f;
+    float delta = 0.f, lse = 0.f, lse_raw = 0.f;
     if (valid) {
       const uint4* o = reinterpret_cast<const uint4*>(p.o.p + row * p.o.token + h * p.o.head);
       const uint4* d = reinterpret_cast<const uint4*>(p.dout.p + row * p.dout.token + h * p.dout.head);
       #pragma unroll
-      for (int w = half; w < DP / 8; w += 2)
+      for (int w = part; w < DP / 8; w += kParts)
         if (8 * w < p.D) {
           const uint4 x = o[w], y = d[w];
           delta += bf16_lo(x.x) * bf16_lo(y.x) + bf16_hi(x.x) * bf16_hi(y.x) + bf16_lo(x.y) * bf16_lo(y.y) +
                    bf16_hi(x.y) * bf16_hi(y.y) + bf16_lo(x.z) * bf16_lo(y.z) + bf16_hi(x.z) * bf16_hi(y.z) +
                    bf16_lo(x.w) * bf16_lo(y.w) + bf16_hi(x.w) * bf16_hi(y.w);
         }
-      lse = -p.lse[static_cast<long long>(h) * p.T + row] * kLog2e;
+      const float l = p.lse[static_cast<long long>(h) * p.T + row];
+      lse = -l * kLog2e;
+      lse_raw = -l / p.scale;
     }
-    bk.sums[0][half][lr] = delta;
-    arith_sync();
-    delta = -(bk.sums[0][0][lr] + bk.sums[0][1][lr]);
+    auto row_sum = [&](float v) {
+      bk.sums[part][lr] = v;
+      arith_sync();
+      return (bk.sums[0][lr] + bk.sums[1][lr]) + (bk.sums[2][lr] + bk.sums[3][lr]);
+    };
+    delta = -row_sum(delta);
+    arith_sync();                                  // (read by all before the next sum)
     const F32x2 lse2 = make_f32x2(lse, lse), mul2_ = make_f32x2(p.scale2, p.scale2);
     bool ok = true;
     auto step = [&](int j, auto masked_c) {
@@ -728,73 +759,60 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!warp_wait(&bk.s_full, j & 1, abort, lim)) return give_up();
       tc_fence_after_sync();
       const int k0 = top - kRows * (j + 1);
-      const int lo = max(key_lo, k0) - k0 - 64 * half, hi = min(key_hi, k0 + kRows) - k0 - 64 * half;
-      uint32_t s[2][32], d[2][32];
-      #pragma unroll
-      for (int c = 0; c < 2; ++c) tmem_ld_x32(tmem + lanes + 128 + 64 * half + 32 * c, s[c]);
-      #pragma unroll
-      for (int c = 0; c < 2; ++c) tmem_ld_wait(s[c]);
+      const int lo = max(key_lo, k0) - k0 - 32 * part, hi = min(key_hi, k0 + kRows) - k0 - 32 * part;
+      uint32_t s[32], d[32], w[16];
+      tmem_ld_x32(tmem + lanes + 128 + 32 * part, s);
+      tmem_ld_wait(s);
       warp_arrive(&bk.s_empty, lane);
       #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        #pragma unroll
-        for (int x = 0; x < 32; x += 2) {
-          float2 y = split_f32x2(fma2(make_f32x2(as_f(s[c][x]), as_f(s[c][x + 1])), mul2_, lse2));
-          y.x = ex2(y.x);
-          y.y = ex2(y.y);
-          if (masked) {
-            if (32 * c + x < lo || 32 * c + x > hi) y.x = 0.f;
-            if (32 * c + x + 1 < lo || 32 * c + x + 1 > hi) y.y = 0.f;
-          }
-          s[c][x] = __float_as_uint(y.x);
-          s[c][x + 1] = __float_as_uint(y.y);
+      for (int x = 0; x < 32; x += 2) {
+        float2 y = split_f32x2(fma2(make_f32x2(as_f(s[x]), as_f(s[x + 1])), mul2_, lse2));
+        y.x = ex2(y.x);
+        y.y = ex2(y.y);
+        if (masked) {
+          if (x < lo || x > hi) y.x = 0.f;
+          if (x + 1 < lo || x + 1 > hi) y.y = 0.f;
         }
+        s[x] = __float_as_uint(y.x);
+        s[x + 1] = __float_as_uint(y.y);
       }
       if (masked) {
         if (!warp_wait(&bk.k_full[j % kKStages], (j / kKStages) & 1, abort, lim)) return give_up();
-        clean_tile<DP>(k_smem + (j % kKStages) * C::kBytes, threadIdx.x, kArith);
+        clean_tile<DP>(k_smem + (j % kKStages) * C::kBytes, threadIdx.x, kBwdArith);
       }
       if (!warp_wait(&bk.dp_full[j & 1], (j >> 1) & 1, abort, lim)) return give_up();
-      const uint32_t tdp = tmem + lanes + 256 + 128 * (j & 1) + 64 * half;
+      const uint32_t tdp = tmem + lanes + 256 + 128 * (j & 1) + 32 * part;
       tc_fence_after_sync();
-      #pragma unroll
-      for (int c = 0; c < 2; ++c) tmem_ld_x32(tdp + 32 * c, d[c]);
-      #pragma unroll
-      for (int c = 0; c < 2; ++c) tmem_ld_wait(d[c]);
+      tmem_ld_x32(tdp, d);
+      tmem_ld_wait(d);
       if (masked && j == 0) {
         F32x2 sum = make_f32x2(0.f, 0.f);
         #pragma unroll
-        for (int c = 0; c < 2; ++c)
-          #pragma unroll
-          for (int x = 0; x < 32; x += 2) {
-            const float a0 = (32 * c + x < lo || 32 * c + x > hi) ? 0.f : as_f(d[c][x]);
-            const float a1 = (32 * c + x + 1 < lo || 32 * c + x + 1 > hi) ? 0.f : as_f(d[c][x + 1]);
-            sum = fma2(make_f32x2(as_f(s[c][x]), as_f(s[c][x + 1])), make_f32x2(a0, a1), sum);
-          }
+        for (int x = 0; x < 32; x += 2) {
+          const float a0 = (x < lo || x > hi) ? 0.f : as_f(d[x]), a1 = (x + 1 < lo || x + 1 > hi) ? 0.f : as_f(d[x + 1]);
+          sum = fma2(make_f32x2(as_f(s[x]), as_f(s[x + 1])), make_f32x2(a0, a1), sum);
+        }
         const float2 t = split_f32x2(sum);
-        bk.sums[1][half][lr] = t.x + t.y;
-        arith_sync();
-        if (key_lo >= k0) delta = -(bk.sums[1][0][lr] + bk.sums[1][1][lr]);
-        if (valid && half == 0) {
-          p.stats[h * p.pitch + row] = lse;
-          p.stats[(p.Hq + h) * p.pitch + row] = delta;
+        const float exact = row_sum(t.x + t.y);
+        if (key_lo >= k0) delta = -exact;
+        if (valid && part == 0) {
+          // (where do is not finite, nor is delta: p of this row shall not be either)
+          p.stats[h * p.pitch + row] = split_row(isfinite(delta) ? lse_raw : delta - delta);
+          p.stats[(p.Hq + h) * p.pitch + row] = split_row(delta);
         }
       }
       const F32x2 delta2 = make_f32x2(delta, delta);
-      uint32_t w[32];
       #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        #pragma unroll
-        for (int x = 0; x < 32; x += 2) {
-          float2 y = split_f32x2(mul2(make_f32x2(as_f(s[c][x]), as_f(s[c][x + 1])),
-                                      add2(make_f32x2(as_f(d[c][x]), as_f(d[c][x + 1])), delta2)));
-          if (masked) {
-            if (32 * c + x < lo || 32 * c + x > hi) y.x = 0.f;
-            if (32 * c + x + 1 < lo || 32 * c + x + 1 > hi) y.y = 0.f;
-          }
-          w[16 * c + x / 2] = pack_bf16x2(y.x, y.y);
+      for (int x = 0; x < 32; x += 2) {
+        float2 y = split_f32x2(mul2(make_f32x2(as_f(s[x]), as_f(s[x + 1])),
+                                    add2(make_f32x2(as_f(d[x]), as_f(d[x + 1])), delta2)));
+        if (masked) {
+          if (x < lo || x > hi) y.x = 0.f;
+          if (x + 1 < lo || x + 1 > hi) y.y = 0.f;
         }
-      tmem_st_x32(tdp, w);
+        w[x / 2] = pack_bf16x2(y.x, y.y);
+      }
+      tmem_st_x16(tdp, w);
       tmem_st_wait();
       warp_arrive(&bk.ds_full, lane);
       return true;
@@ -803,26 +821,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = j == 0 || top - kRows * (j + 1) < all_from ? step(j, std::true_type{}) : step(j, std::false_type{});
     if (ok && warp_wait(&bk.done, 0, abort, lim)) {
       tc_fence_after_sync();
-      __nv_bfloat16* out = p.d0.p + row * p.d0.token + h * p.d0.head;
-      #pragma unroll
-      for (int c = 0; c < DP / 64; ++c) {
-        const int col = half * (DP / 2) + 32 * c;
+      const int col = 32 * part;
+      if (col < DP) {
         uint32_t o[32];
         float v[32];
         tmem_ld_x32(tmem + lanes + col, o);
         tmem_ld_wait(o);
         #pragma unroll
         for (int x = 0; x < 32; ++x) v[x] = as_f(o[x]) * p.scale;
-        if (valid) store_cols(out, col, p.D, v);
+        if (valid) store_cols(p.d0.p + row * p.d0.token + h * p.d0.head, col, p.D, v);
       }
     }
-  }  }
+   }
+  }
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
   pdl_launch_next();
   if (threadIdx.x == 0 && bk.abort_flag) set_status(p.status, kErrTimeout);
-  if (warp == kMmaWarp) {
+  if (warp == kBwdMmaWarp) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
   }
@@ -833,22 +850,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 // key), so that the probabilities lie in TMEM as the A operand of the sums.  TMEM: dk, dv
 // DP columns from 0 and 128, scores at 256 (which become p), dp at 384 (ds).  In the
 // order dv(j), scores(j + 1), dk(j), dp(j + 1) each buffer is free again when its turn
-// comes, and the arithmetic on one has the time of two products.
+// comes.
+//
+// A thread's columns are queries, each with an lse and a delta of its own.  Read from shared memory
+// they cost it 128 KB a step, as much as the tiles (a step 2900 cycles, whatever the width); so
+// the products subtract them: one more step of the contraction, three bf16 parts of -lse / scale (or
+// -delta) against ones.
 //
 // The heads of a group may be shared out among the CTAs of a cluster (p.split of them): each leaves
 // its sums in its shared memory, and each adds up its share of the rows over all of them, in
 // the order of the CTAs, through distributed shared memory.
-constexpr int kQStages = 3;                // query tiles in flight: one is held from its scores to its dk
+constexpr int kRowBytes = kRows * 16;      // a block of statistics
 struct DkvBook {
-  uint64_t kv_full, q_full[kQStages], do_full[2];
-  uint64_t q_empty[kQStages], do_empty[2], s_full, p_full[2], dp_full, ds_full, done;
+  uint64_t kv_full, q_full[2], do_full[2];
+  uint64_t q_empty[2], do_empty[2], s_full, p_full, dp_full, ds_full, done;
   uint32_t tmem;
   int abort_flag;
   RowMap map;
 };
 
 template <int DP>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kBwdThreads, 1)
     attention_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDo,
                          const AttnParams p) {
@@ -857,11 +879,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* k_smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* v_smem = k_smem + C::kBytes;
   uint8_t* q_smem = v_smem + C::kBytes;
-  uint8_t* do_smem = q_smem + kQStages * C::kBytes;
-  float* lse_smem = reinterpret_cast<float*>(do_smem + 2 * C::kBytes);         // [2][128] -lse log2 e, with do
-  float* delta_smem = lse_smem + 2 * kRows;                                    // [kQStages][128] -delta, with q
+  uint8_t* do_smem = q_smem + 2 * C::kBytes;
+  uint8_t* lse_smem = do_smem + 2 * C::kBytes;           // two blocks of 128 rows of 16 bytes, with q
+  uint8_t* delta_smem = lse_smem + 2 * kRowBytes;        // the same, with do
+  uint8_t* ones_smem = delta_smem + 2 * kRowBytes;       // 128 rows of three ones and five zeros
+  uint8_t* zero_smem = ones_smem + kRowBytes;            // the other half of each operand's 16 columns
   float4* sums = reinterpret_cast<float4*>(q_smem);                            // [dk, dv][128][DP], in place of q and do
-  DkvBook& bk = *reinterpret_cast<DkvBook*>(delta_smem + kQStages * kRows);
+  DkvBook& bk = *reinterpret_cast<DkvBook*>(zero_smem + kRowBytes);
   if (!smem_fits(smem_raw, &bk + 1)) {
     pdl_wait();
     if (threadIdx.x == 0) set_status(p.status, kErrLaunch);
@@ -870,19 +894,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(&bk.kv_full, 1);
-    for (int s = 0; s < kQStages; ++s) {
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&bk.q_full[s], 1);
       mbar_init(&bk.q_empty[s], 1);
-    }
-    for (int s = 0; s < 2; ++s) {
       mbar_init(&bk.do_full[s], 1);
       mbar_init(&bk.do_empty[s], 1);
     }
     mbar_init(&bk.s_full, 1);
-    mbar_init(&bk.p_full[0], 8);
-    mbar_init(&bk.p_full[1], 8);
+    mbar_init(&bk.p_full, kBwdArith / 32);
     mbar_init(&bk.dp_full, 1);
-    mbar_init(&bk.ds_full, 8);
+    mbar_init(&bk.ds_full, kBwdArith / 32);
     mbar_init(&bk.done, 1);
     bk.abort_flag = 0;
     fence_mbarrier_init();
@@ -891,7 +912,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&tmV);
     prefetch_tensormap(&tmDo);
   }
-  if (warp == kMmaWarp) {
+  if (threadIdx.x < kRows) {
+    reinterpret_cast<uint4*>(ones_smem)[threadIdx.x] = make_uint4(0x3f803f80u, 0x3f80u, 0u, 0u);
+    reinterpret_cast<uint4*>(zero_smem)[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+  }
+  if (warp == kBwdMmaWarp) {
     tmem_alloc(&bk.tmem, 512);
     tmem_relinquish();
   }
@@ -910,9 +936,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int end = a < b ? end_of(&bk.map, k0, b - 1, kRows / 32) : k0;
   const int nq = a < b ? (end - k0 + kRows - 1) / kRows : 0, n = nq * (group / split);
 
-  if (warp >= kLoadWarp) {
-   fewer_registers<kOtherRegs>();
-   if (n > 0 && warp == kLoadWarp) {
+  if (warp >= kBwdLoadWarp) {
+   fewer_registers<kBwdOtherRegs>();
+   if (n > 0 && warp == kBwdLoadWarp) {
     if (lane == 0) {
       Issued got;
       mbar_arrive_expect_tx(&bk.kv_full, 2 * C::kBytes);
@@ -922,18 +948,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int h = kv * group + rank * (group / split), row = k0;
       for (int j = 0; j < n && ok; ++j) {
-        const int s = j % kQStages, s2 = j & 1;
-        const uint32_t ph = (j / kQStages) & 1, ph2 = (j >> 1) & 1;
-        if (j >= kQStages && !mbar_wait(&bk.q_empty[s], ph ^ 1u, abort, lim)) { ok = false; break; }
-        mbar_arrive_expect_tx(&bk.q_full[s], C::kBytes + kRows * 4);
+        const int s = j & 1;
+        const uint32_t ph = (j >> 1) & 1;
+        if (j >= 2 && !mbar_wait(&bk.q_empty[s], ph ^ 1u, abort, lim)) { ok = false; break; }
+        mbar_arrive_expect_tx(&bk.q_full[s], C::kBytes + kRowBytes);
         load_tile<DP>(q_smem + s * C::kBytes, &tmQ, &bk.q_full[s], h, row);
-        bulk_load(delta_smem + s * kRows, p.stats + (p.Hq + h) * p.pitch + row, kRows * 4, &bk.q_full[s]);
+        bulk_load(lse_smem + s * kRowBytes, p.stats + h * p.pitch + row, kRowBytes, &bk.q_full[s]);
         got.note(1 + s, ph);
-        if (j >= 2 && !mbar_wait(&bk.do_empty[s2], ph2 ^ 1u, abort, lim)) { ok = false; break; }
-        mbar_arrive_expect_tx(&bk.do_full[s2], C::kBytes + kRows * 4);
-        load_tile<DP>(do_smem + s2 * C::kBytes, &tmDo, &bk.do_full[s2], h, row);
-        bulk_load(lse_smem + s2 * kRows, p.stats + h * p.pitch + row, kRows * 4, &bk.do_full[s2]);
-        got.note(1 + kQStages + s2, ph2);
+        if (j >= 2 && !mbar_wait(&bk.do_empty[s], ph ^ 1u, abort, lim)) { ok = false; break; }
+        mbar_arrive_expect_tx(&bk.do_full[s], C::kBytes + kRowBytes);
+        load_tile<DP>(do_smem + s * C::kBytes, &tmDo, &bk.do_full[s], h, row);
+        bulk_load(delta_smem + s * kRowBytes, p.stats + (p.Hq + h) * p.pitch + row, kRowBytes, &bk.do_full[s]);
+        got.note(3 + s, ph);
         row += kRows;
         if (row >= k0 + nq * kRows) {
           row = k0;
@@ -942,17 +968,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       got.drain(&bk.kv_full);
     }
-   } else if (n > 0 && warp == kMmaWarp) {
+   } else if (n > 0 && warp == kBwdMmaWarp) {
     const uint32_t leader = elect_one() ? 1u : 0u;
     const uint64_t k_desc = scores_desc(k_smem), v_desc = scores_desc(v_smem), q_desc = scores_desc(q_smem),
                    do_desc = scores_desc(do_smem), qt_desc = sums_desc(q_smem), dot_desc = sums_desc(do_smem);
+    const uint64_t ones_desc = rows_desc(ones_smem, zero_smem);
     constexpr uint64_t kNext = C::kBytes >> 4;
     const int tiles = uniform(n);
     bool any = false;
     auto scores = [&](int j) {
-      if (!warp_wait(&bk.q_full[j % kQStages], (j / kQStages) & 1, abort, lim)) return false;
+      if (!warp_wait(&bk.q_full[j & 1], (j >> 1) & 1, abort, lim)) return false;
       tc_fence_after_sync();
-      mma_scores<DP>(leader, tmem + 256, k_desc, q_desc + (j % kQStages) * kNext);
+      mma_scores<DP>(leader, tmem + 256, k_desc, q_desc + (j & 1) * kNext);
+      mma_bf16_ss_warp(leader, tmem + 256, ones_desc, rows_desc(lse_smem + (j & 1) * kRowBytes, zero_smem), C::kScores, 1u);
       mma_commit_warp(leader, &bk.s_full);
       any = true;
       return true;
@@ -961,29 +989,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!warp_wait(&bk.do_full[j & 1], (j >> 1) & 1, abort, lim)) return false;
       tc_fence_after_sync();
       mma_scores<DP>(leader, tmem + 384, v_desc, do_desc + (j & 1) * kNext);
+      mma_bf16_ss_warp(leader, tmem + 384, ones_desc, rows_desc(delta_smem + (j & 1) * kRowBytes, zero_smem), C::kScores, 1u);
       mma_commit_warp(leader, &bk.dp_full);
       return true;
     };
     bool ok = warp_wait(&bk.kv_full, 0, abort, lim) && scores(0) && dprob(0);
     for (int j = 0; ok && j < tiles; ++j) {
-      // (the first 32 queries of each half while the others are still exponentiated)
-      #pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        ok = ok && warp_wait(&bk.p_full[part], j & 1, abort, lim);
-        if (!ok) break;
-        tc_fence_after_sync();
-        #pragma unroll
-        for (int half = 0; half < 2; ++half)
-          mma_sums<DP>(leader, tmem + 128, tmem + 256, 64, dot_desc + (j & 1) * kNext, j > 0 || part + half > 0,
-                       4 * half + 2 * part, 4 * half + 2 * part + 2);
-      }
-      if (!ok) break;
+      if (!warp_wait(&bk.p_full, j & 1, abort, lim)) { ok = false; break; }
+      tc_fence_after_sync();
+      mma_sums<DP, 2>(leader, tmem + 128, tmem + 256, dot_desc + (j & 1) * kNext, j > 0);
       if (j + 2 < tiles) mma_commit_warp(leader, &bk.do_empty[j & 1]);
       if (j + 1 < tiles && !scores(j + 1)) { ok = false; break; }
       if (!warp_wait(&bk.ds_full, j & 1, abort, lim)) { ok = false; break; }
       tc_fence_after_sync();
-      mma_sums<DP>(leader, tmem, tmem + 384, 64, qt_desc + (j % kQStages) * kNext, j > 0);
-      if (j + kQStages < tiles) mma_commit_warp(leader, &bk.q_empty[j % kQStages]);
+      mma_sums<DP, 2>(leader, tmem, tmem + 384, qt_desc + (j & 1) * kNext, j > 0);
+      if (j + 2 < tiles) mma_commit_warp(leader, &bk.q_empty[j & 1]);
       if (j + 1 < tiles && !dprob(j + 1)) { ok = false; break; }
     }
     if (any) {
@@ -992,10 +1012,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
    }
   } else {
-   more_registers<kArithRegs>();
+   more_registers<kBwdRegs>();
    if (n > 0) {
-    // a thread a key, the two groups of four warps each half of the queries
-    const int half = warp >> 2;
+    const int part = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int key = k0 + (warp & 3) * 32 + lane;
     const bool valid = key >= bk.map.first && key < bk.map.last;
@@ -1005,74 +1024,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     auto step = [&](int j, int q0, auto masked_c) {
       constexpr bool masked = decltype(masked_c)::value;
-      if (!warp_wait(&bk.q_full[j % kQStages], (j / kQStages) & 1, abort, lim) ||
-          !warp_wait(&bk.do_full[j & 1], (j >> 1) & 1, abort, lim) || !warp_wait(&bk.s_full, j & 1, abort, lim))
-        return false;
+      if (!warp_wait(&bk.s_full, j & 1, abort, lim)) return false;
       tc_fence_after_sync();
-      const int lo = max(key, q0) - q0 - 64 * half, hi = min(key_end, q0 + kRows) - q0 - 64 * half;   // queries [lo, hi)
-      const float4* lse = reinterpret_cast<const float4*>(lse_smem + (j & 1) * kRows + 64 * half);
-      const float4* delta = reinterpret_cast<const float4*>(delta_smem + (j % kQStages) * kRows + 64 * half);
-      uint32_t s[2][32];
-      #pragma unroll
-      for (int c = 0; c < 2; ++c) tmem_ld_x32(tmem + lanes + 256 + 64 * half + 32 * c, s[c]);
-      #pragma unroll
-      for (int c = 0; c < 2; ++c) tmem_ld_wait(s[c]);
+      const int lo = max(key, q0) - q0 - 32 * part, hi = min(key_end, q0 + kRows) - q0 - 32 * part;   // queries [lo, hi)
+      uint32_t s[32], d[32], w[16];
+      tmem_ld_x32(tmem + lanes + 256 + 32 * part, s);
+      tmem_ld_wait(s);
       if (masked) {
-        clean_tile<DP>(do_smem + (j & 1) * C::kBytes, threadIdx.x, kArith);
-        clean_tile<DP>(q_smem + (j % kQStages) * C::kBytes, threadIdx.x, kArith);
+        if (!warp_wait(&bk.q_full[j & 1], (j >> 1) & 1, abort, lim) || !warp_wait(&bk.do_full[j & 1], (j >> 1) & 1, abort, lim))
+          return false;
+        clean_tile<DP>(do_smem + (j & 1) * C::kBytes, threadIdx.x, kBwdArith);
+        clean_tile<DP>(q_smem + (j & 1) * C::kBytes, threadIdx.x, kBwdArith);
       }
       #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t w[16];
-        #pragma unroll
-        for (int x = 0; x < 32; x += 4) {
-          const float4 l4 = lse[8 * c + x / 4];
-          float2 y = split_f32x2(fma2(make_f32x2(as_f(s[c][x]), as_f(s[c][x + 1])), mul2_, make_f32x2(l4.x, l4.y)));
-          float2 z = split_f32x2(fma2(make_f32x2(as_f(s[c][x + 2]), as_f(s[c][x + 3])), mul2_, make_f32x2(l4.z, l4.w)));
-          float v[4] = {ex2(y.x), ex2(y.y), ex2(z.x), ex2(z.y)};
-          #pragma unroll
-          for (int e = 0; e < 4; ++e) s[c][x + e] = __float_as_uint(v[e]);
-          if (masked) {
-            // (a query whose do is not finite has no finite delta: what it sees keeps that)
-            const float4 d4 = delta[8 * c + x / 4];
-            const float dd[4] = {d4.x, d4.y, d4.z, d4.w};
-            #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              v[e] = (32 * c + x + e < lo || 32 * c + x + e >= hi) ? 0.f : fmaf(0.f, dd[e], v[e]);
-          }
-          w[x / 2] = pack_bf16x2(v[0], v[1]);
-          w[x / 2 + 1] = pack_bf16x2(v[2], v[3]);
+      for (int x = 0; x < 32; x += 2) {
+        float2 y = split_f32x2(mul2(make_f32x2(as_f(s[x]), as_f(s[x + 1])), mul2_));
+        y.x = ex2(y.x);
+        y.y = ex2(y.y);
+        if (masked) {
+          if (x < lo || x >= hi) y.x = 0.f;
+          if (x + 1 < lo || x + 1 >= hi) y.y = 0.f;
         }
-        tmem_st_x16(tmem + lanes + 256 + 64 * half + 16 * c, w);
-        tmem_st_wait();
-        warp_arrive(&bk.p_full[c], lane);
+        s[x] = __float_as_uint(y.x);
+        s[x + 1] = __float_as_uint(y.y);
+        w[x / 2] = pack_bf16x2(y.x, y.y);
       }
+      tmem_st_x16(tmem + lanes + 256 + 32 * part, w);
+      tmem_st_wait();
+      warp_arrive(&bk.p_full, lane);
       if (!warp_wait(&bk.dp_full, j & 1, abort, lim)) return false;
       tc_fence_after_sync();
-      uint32_t d[2][32], w[32];
+      tmem_ld_x32(tmem + lanes + 384 + 32 * part, d);
+      tmem_ld_wait(d);
       #pragma unroll
-      for (int c = 0; c < 2; ++c) tmem_ld_x32(tmem + lanes + 384 + 64 * half + 32 * c, d[c]);
-      #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        tmem_ld_wait(d[c]);
-        #pragma unroll
-        for (int x = 0; x < 32; x += 4) {
-          const float4 d4 = delta[8 * c + x / 4];
-          const float2 y = split_f32x2(mul2(make_f32x2(as_f(s[c][x]), as_f(s[c][x + 1])),
-                                            add2(make_f32x2(as_f(d[c][x]), as_f(d[c][x + 1])), make_f32x2(d4.x, d4.y))));
-          const float2 z = split_f32x2(mul2(make_f32x2(as_f(s[c][x + 2]), as_f(s[c][x + 3])),
-                                            add2(make_f32x2(as_f(d[c][x + 2]), as_f(d[c][x + 3])), make_f32x2(d4.z, d4.w))));
-          float v[4] = {y.x, y.y, z.x, z.y};
-          if (masked) {
-            #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (32 * c + x + e < lo || 32 * c + x + e >= hi) v[e] = 0.f;
-          }
-          w[16 * c + x / 2] = pack_bf16x2(v[0], v[1]);
-          w[16 * c + x / 2 + 1] = pack_bf16x2(v[2], v[3]);
+      for (int x = 0; x < 32; x += 2) {
+        float2 y = split_f32x2(mul2(make_f32x2(as_f(s[x]), as_f(s[x + 1])), make_f32x2(as_f(d[x]), as_f(d[x + 1]))));
+        if (masked) {
+          if (x < lo || x >= hi) y.x = 0.f;
+          if (x + 1 < lo || x + 1 >= hi) y.y = 0.f;
         }
+        w[x / 2] = pack_bf16x2(y.x, y.y);
       }
-      tmem_st_x32(tmem + lanes + 384 + 64 * half, w);
+      tmem_st_x16(tmem + lanes + 384 + 32 * part, w);
       tmem_st_wait();
       warp_arrive(&bk.ds_full, lane);
       return true;
@@ -1085,13 +1078,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (ok && warp_wait(&bk.done, 0, abort, lim)) {
       tc_fence_after_sync();
-      // the first four warps store dk, the others dv
+      // eight warps store dk, the others dv
+      const int half = part >> 1;
       const Heads& to = half == 0 ? p.d0 : p.d1;
       const float mul = half == 0 ? p.scale : 1.f;
       __nv_bfloat16* out = to.p + key * to.token + kv * to.head;
       float4* row = sums + (half * kRows + key - k0) * (DP / 4);
       #pragma unroll
-      for (int c = 0; c < DP / 32; ++c) {
+      for (int c = part & 1; c < DP / 32; c += 2) {
         uint32_t o[32];
         float v[32];
         tmem_ld_x32(tmem + lanes + 128 * half + 32 * c, o);
@@ -1113,7 +1107,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     cluster_sync();
     const int each = (kRows + split - 1) / split, r0 = rank * each, rows = min(each, kRows - r0);
-    for (int i = threadIdx.x; i < 2 * rows * (DP / 8); i += kThreads) {
+    for (int i = threadIdx.x; i < 2 * rows * (DP / 8); i += kBwdThreads) {
       const int w = i % (DP / 8), r = r0 + i / (DP / 8) % rows, half = i / (DP / 8) / rows, key = k0 + r;
       const float4* mine = sums + (half * kRows + r) * (DP / 4);
       const uint32_t lo = smem_u32(mine + ((2 * w) ^ (key & (DP / 4 - 1)))), hi = smem_u32(mine + ((2 * w + 1) ^ (key & (DP / 4 - 1))));
@@ -1134,7 +1128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   pdl_launch_next();
   if (threadIdx.x == 0 && bk.abort_flag) set_status(p.status, kErrTimeout);
-  if (warp == kMmaWarp) {
+  if (warp == kBwdMmaWarp) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
   }
@@ -1150,13 +1144,13 @@ template <int DP>
 constexpr int dq_smem() { return (4 + kKStages) * Tile<DP>::kBytes + static_cast<int>(sizeof(DqBook)); }
 template <int DP>
 constexpr int dkv_smem() {
-  return (4 + kQStages) * Tile<DP>::kBytes + (2 + kQStages) * kRows * 4 + static_cast<int>(sizeof(DkvBook));
+  return 6 * Tile<DP>::kBytes + 6 * kRowBytes + static_cast<int>(sizeof(DkvBook));
 }
 static_assert(fwd_smem<128>() <= kMaxSmem && dq_smem<128>() <= kMaxSmem && dkv_smem<128>() <= kMaxSmem, "shared memory");
 
-// Launch of kThreads-wide blocks with much shared memory, in clusters of `cluster`.
+// Launch of blocks with much shared memory, in clusters of `cluster`.
 template <class... KArgs, class... Args>
-cudaError_t launch_big(void (*kern)(KArgs...), std::atomic<bool>* attr_set, int grid, int smem, cudaStream_t st, int cluster,
+cudaError_t launch_big(void (*kern)(KArgs...), std::atomic<bool>* attr_set, int grid, int threads, int smem, cudaStream_t st, int cluster,
                        Args&&... args) {
   const int dev = current_device();
   if (dev < 0) return cudaErrorInvalidDevice;
@@ -1174,7 +1168,7 @@ cudaError_t launch_big(void (*kern)(KArgs...), std::atomic<bool>* attr_set, int 
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = kThreads;
+  cfg.blockDim = threads;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
@@ -1233,7 +1227,7 @@ AttnParams params_of(const moe_attention_config* c, const int32_t* cu, void* ws)
   p.scale2 = c->scale * kLog2e;
   p.tiles = (c->T + kRows - 1) / kRows;
   p.status = static_cast<int*>(ws);
-  p.stats = reinterpret_cast<float*>(static_cast<char*>(ws) + entry::kStatusBytes);
+  p.stats = reinterpret_cast<uint4*>(static_cast<char*>(ws) + entry::kStatusBytes);
   p.pitch = stats_pitch(c->T);
   const unsigned long long wait = gemm_wait_limit_ns();
   p.wait_ns = wait != 0 ? wait : kWaitLimitNs;
@@ -1250,7 +1244,7 @@ cudaError_t forward(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensor
                     cudaStream_t st) {
   static std::atomic<bool> attr_set[kMaxDevices];
   const int grid = p.tiles * (p.pair_rows ? p.Hq : p.Hq / 2);
-  return launch_big(attention_fwd_kernel<DP>, attr_set, grid, smem_of(fwd_smem<DP>()), st, 1, tq, tk, tv, p);
+  return launch_big(attention_fwd_kernel<DP>, attr_set, grid, kFwdThreads, smem_of(fwd_smem<DP>()), st, 1, tq, tk, tv, p);
 }
 template <int DP>
 cudaError_t backward(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& td,
@@ -1258,12 +1252,12 @@ cudaError_t backward(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
   static std::atomic<bool> dq_set[kMaxDevices], dkv_set[kMaxDevices];
   p.d0 = dq;
   const cudaError_t e =
-      launch_big(attention_dq_kernel<DP>, dq_set, p.tiles * p.Hq, smem_of(dq_smem<DP>()), st, 1, tq, tk, tv, td, p);
+      launch_big(attention_dq_kernel<DP>, dq_set, p.tiles * p.Hq, kBwdThreads, smem_of(dq_smem<DP>()), st, 1, tq, tk, tv, td, p);
   if (e != cudaSuccess) return e;
   p.d0 = dk;
   p.d1 = dv;
   p.split = group_split(p);
-  return launch_big(attention_dkv_kernel<DP>, dkv_set, p.tiles * p.Hkv * p.split, smem_of(dkv_smem<DP>()), st, p.split,
+  return launch_big(attention_dkv_kernel<DP>, dkv_set, p.tiles * p.Hkv * p.split, kBwdThreads, smem_of(dkv_smem<DP>()), st, p.split,
                     tq, tk, tv, td, p);
 }
 
@@ -1277,7 +1271,7 @@ extern "C" {
 
 size_t moe_attention_workspace_bytes(const moe_attention_config* cfg) {
   if (!config_ok(cfg)) return 0;
-  return kStatusBytes + align_up(static_cast<size_t>(cfg->q_heads) * stats_pitch(cfg->T) * 2 * sizeof(float));
+  return kStatusBytes + align_up(static_cast<size_t>(cfg->q_heads) * stats_pitch(cfg->T) * 2 * sizeof(uint4));
 }
 
 moe_status moe_attention_forward(const moe_attention_config* cfg, const moe_heads* q, const moe_heads* k,
