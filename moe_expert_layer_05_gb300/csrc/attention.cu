@@ -205,9 +205,9 @@ __device__ __forceinline__ void mma_sums(uint32_t leader, uint32_t d, uint32_t w
                      (add || kk != 0) ? 1u : 0u);
 }
 
-// Words t, t + n, ... of a tile: what is not finite becomes zero.  True where this thread found any.
-template <int DP>
-__device__ __forceinline__ bool clean_tile(uint8_t* tile, int t, int n) {
+// Words t, t + n, ... of a tile: what is not finite becomes zero, after found().
+template <int DP, class F>
+__device__ __forceinline__ void clean_tile(uint8_t* tile, int t, int n, F found) {
   uint4* w = reinterpret_cast<uint4*>(tile);
   const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
   __nv_bfloat162 acc = zero;
@@ -220,7 +220,8 @@ __device__ __forceinline__ bool clean_tile(uint8_t* tile, int t, int n) {
     add(v.z);
     add(v.w);
   }
-  if ((*reinterpret_cast<uint32_t*>(&acc) & 0x7fff7fffu) == 0) return false;     // (a sum of zeros)
+  if ((*reinterpret_cast<uint32_t*>(&acc) & 0x7fff7fffu) == 0) return;      // (a sum of zeros)
+  found();
   auto part = [](uint32_t v) {
     if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
     if ((v & 0x7f800000u) == 0x7f800000u) v &= 0x0000ffffu;
@@ -231,16 +232,17 @@ __device__ __forceinline__ bool clean_tile(uint8_t* tile, int t, int n) {
     w[i] = make_uint4(part(v.x), part(v.y), part(v.z), part(v.w));
   }
   fence_proxy_async_smem();
-  return true;
 }
 
 __device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
 __device__ __forceinline__ float as_f(uint32_t v) { return __uint_as_float(v); }
 
-// A warp's wait: its lanes go on together or, if one has given up, not at all.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned long long ns) {
-  const bool ok = mbar_wait(bar, parity, abort, ns);
-  return __all_sync(kFull, ok) != 0;
+// A converged warp's wait.  It returns when the phase is complete, or when a wait of the block has given up: the
+// warp then goes through the rest of its loops, whose waits all return, on whatever the buffers hold, and
+// what it leaves behind does not count (MOE_ERR_TIMEOUT).  A vote whether to go on would double its 60 cycles.
+__device__ __forceinline__ void warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned long long ns) {
+  mbar_wait(bar, parity, abort, ns);
+  __syncwarp();
 }
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   tc_fence_before_sync();
@@ -381,29 +383,28 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       got.drain(bk.full);                    // (they have landed by the end, unless another warp gave up)
     }
    } else if (n > 0 && warp == kFwdMmaWarp) {
+    // (One warp for both tiles of rows: two that issue in turn slow each other, 0.53 ms against 0.41.)
     const uint32_t leader = elect_one() ? 1u : 0u;
     const uint64_t q_desc = scores_desc(q_smem), k_desc = scores_desc(ring), v_desc = sums_desc(ring);
     const int f0 = uniform(from[0]), f1 = uniform(from[1]), e0 = uniform(to[0]), e1 = uniform(to[1]);
     const int first = uniform(ib), last = uniform(ib + n) - 1;
     const int turns = 2 * (last - first + 1);
-    bool any = false, ok = true;
-    auto full = [&](int s) { return warp_wait(&bk.full[s % ST], (s / ST) & 1, abort, lim); };
+    auto full = [&](int s) { warp_wait(&bk.full[s % ST], (s / ST) & 1, abort, lim); };
     auto release = [&](int s) { if (s + ST < turns) mma_commit_warp(leader, &bk.empty[s % ST]); };
     auto scores = [&](int u, int s) {
       mma_scores<DP>(leader, tmem + 128 * u, q_desc + u * (C::kBytes >> 4), k_desc + (s % ST) * (C::kBytes >> 4));
       mma_commit_warp(leader, &bk.s_full[u]);
-      any = true;
     };
-    ok = warp_wait(&bk.q_full, 0, abort, lim) && full(0);
-    if (ok) {
-      tc_fence_after_sync();
-      if (first >= f0 && first < e0) scores(0, 0);
-      if (first >= f1 && first < e1) scores(1, 0);
-      release(0);
-    }
-    for (int i = first; ok && i <= last; ++i) {
+    warp_wait(&bk.q_full, 0, abort, lim);
+    full(0);
+    tc_fence_after_sync();
+    if (first >= f0 && first < e0) scores(0, 0);
+    if (first >= f1 && first < e1) scores(1, 0);
+    release(0);
+    for (int i = first; i <= last; ++i) {
       const int sk = 2 * (i - first), sv = sk + 1;              // this key tile's and value tile's turn
-      if (!full(sv) || (i < last && !full(sk + 2))) { ok = false; break; }
+      full(sv);
+      if (i < last) full(sk + 2);
       #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int f = u ? f1 : f0, e = u ? e1 : e0;
@@ -411,24 +412,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           // (the first half of the keys while the second is still exponentiated)
           #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            ok = ok && warp_wait(&bk.p_full[u][half], (i - f) & 1, abort, lim);
+            warp_wait(&bk.p_full[u][half], (i - f) & 1, abort, lim);
             tc_fence_after_sync();
-            if (ok)
-              mma_sums<DP, 8>(leader, tmem + 256 + DP * u, tmem + 128 * u, v_desc + (sv % ST) * (C::kBytes >> 4),
-                           i > f || half, 4 * half, 4 * half + 4);
+            mma_sums<DP, 8>(leader, tmem + 256 + DP * u, tmem + 128 * u, v_desc + (sv % ST) * (C::kBytes >> 4),
+                            i > f || half, 4 * half, 4 * half + 4);
           }
-          if (ok && i + 1 == e) mma_commit_warp(leader, &bk.o_full[u]);
+          if (i + 1 == e) mma_commit_warp(leader, &bk.o_full[u]);
         }
-        if (ok && i + 1 >= f && i + 1 < e) scores(u, sk + 2);
+        if (i + 1 >= f && i + 1 < e) scores(u, sk + 2);
       }
-      if (!ok) break;
       release(sv);
       if (i < last) release(sk + 2);
     }
-    if (any) {                               // (TMEM is given back after them, whoever gave up)
-      mma_commit_warp(leader, &bk.drain);
-      mbar_wait_drain(&bk.drain, 0);
-    }
+    mma_commit_warp(leader, &bk.drain);      // (TMEM is given back after them, whoever gave up)
+    mbar_wait_drain(&bk.drain, 0);
    }
   } else {
    more_registers<kFwdRegs>();
@@ -443,15 +440,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int key_lo = valid ? start_of(&bk.map, q0, row) : INT_MIN / 2, key_hi = valid ? row : INT_MAX / 2;
     // keys from here on are seen by every row of the tile (up to the diagonal)
     const int all_from = e > f ? start_of(&bk.map, q0, min(r0 + kRows, bk.map.last) - 1) : 0;
-    const int other_from = u ? from[0] : from[1], other_to = u ? to[0] : to[1];
-    const int other_all = other_to > other_from ?
-        start_of(&bk.map, q0, min((u ? base[0] : base[1]) + kRows, bk.map.last) - 1) : 0;
     // probabilities are relative to a reference that follows the maximum once it is 2^8 above
     const float slack = 8.f / p.scale2;
     float ref = -INFINITY, sum = 0.f;
-    bool ok = true;
     for (int i = f; i < e; ++i) {
-      if (!warp_wait(&bk.s_full[u], (i - f) & 1, abort, lim)) { ok = false; break; }
+      warp_wait(&bk.s_full[u], (i - f) & 1, abort, lim);
       tc_fence_after_sync();
       uint32_t s[4][32];
       const int k0 = top - kRows * (i + 1);
@@ -495,15 +488,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       }
       const float off = ref == -INFINITY ? 0.f : -ref * p.scale2;
       const F32x2 off2 = make_f32x2(off, off), mul2_ = make_f32x2(p.scale2, p.scale2);
-      // One tile of rows looks through the values for both, before any product takes them.
-      const bool both = i >= other_from && i < other_to;
-      if ((masked || (both && (i == other_from || k0 < other_all))) && (u == 0 || !both)) {
+      if (masked) {
         const int turn = 2 * (i - ib) + 1;
-        if (!warp_wait(&bk.full[turn % ST], (turn / ST) & 1, abort, lim)) { ok = false; break; }
-        if (clean_tile<DP>(ring + (turn % ST) * C::kBytes, threadIdx.x & 127, 128)) {
+        warp_wait(&bk.full[turn % ST], (turn / ST) & 1, abort, lim);
+        clean_tile<DP>(ring + (turn % ST) * C::kBytes, threadIdx.x & 127, 128, [&] {
           atomicMin(&bk.bad_lo, k0);
           atomicMax(&bk.bad_hi, k0 + kRows - 1);
-        }
+          __threadfence_block();                 // (the other tile of rows may find the zeros: it shall know)
+        });
       }
       F32x2 part[4];
       #pragma unroll
@@ -529,7 +521,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const float2 total = split_f32x2(add2(add2(part[0], part[1]), add2(part[2], part[3])));
       sum += total.x + total.y;
     }
-    if (ok && e > f && warp_wait(&bk.o_full[u], 0, abort, lim)) {
+    if (e > f) {
+      warp_wait(&bk.o_full[u], 0, abort, lim);
       tc_fence_after_sync();
       const float inv = 1.f / sum;
       const int bad_lo = *const_cast<volatile int*>(&bk.bad_lo), bad_hi = *const_cast<volatile int*>(&bk.bad_hi);
@@ -594,7 +587,7 @@ __device__ __forceinline__ uint4 split_row(float v) {
 constexpr int kKStages = 3;                // key tiles in flight: one is held from its scores to its dq
 struct DqBook {
   uint64_t q_full, k_full[kKStages], v_full[2];
-  uint64_t k_empty[kKStages], v_empty[2], s_full, s_empty, dp_full[2], ds_full, done;
+  uint64_t k_empty[kKStages], v_empty[2], s_full, s_empty, dp_full[2], dp_empty[2], ds_full, done;
   uint32_t tmem;
   int abort_flag;
   RowMap map;
@@ -629,11 +622,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       mbar_init(&bk.v_full[s], 1);
       mbar_init(&bk.v_empty[s], 1);
       mbar_init(&bk.dp_full[s], 1);
+      mbar_init(&bk.dp_empty[s], 1);
     }
     mbar_init(&bk.s_full, 1);
     mbar_init(&bk.s_empty, kBwdArith / 32);
     mbar_init(&bk.ds_full, kBwdArith / 32);
-    mbar_init(&bk.done, 1);
+    mbar_init(&bk.done, 2);
     bk.abort_flag = 0;
     fence_mbarrier_init();
     prefetch_tensormap(&tmQ);
@@ -682,39 +676,41 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
       got.drain(&bk.q_full);
     }
-   } else if (n > 0 && warp == kBwdMmaWarp) {
+   } else if (n > 0 && (warp == kBwdMmaWarp || warp == kBwdMmaWarp + 1)) {
+    // One warp issues the scores and dp, the other dq: what one waits for costs the other nothing.
     const uint32_t leader = elect_one() ? 1u : 0u;
-    const uint64_t q_desc = scores_desc(q_smem), do_desc = scores_desc(do_smem), k_desc = scores_desc(k_smem),
-                   v_desc = scores_desc(v_smem), kt_desc = sums_desc(k_smem);
     constexpr uint64_t kNext = C::kBytes >> 4;
     const int tiles = uniform(n);
-    bool any = false;
-    auto products = [&](int j) {
-      if (!warp_wait(&bk.k_full[j % kKStages], (j / kKStages) & 1, abort, lim) || (j > 0 && !warp_wait(&bk.s_empty, (j - 1) & 1, abort, lim)))
-        return false;
-      tc_fence_after_sync();
-      mma_scores<DP>(leader, tmem + 128, q_desc, k_desc + (j % kKStages) * kNext);
-      mma_commit_warp(leader, &bk.s_full);
-      any = true;
-      if (!warp_wait(&bk.v_full[j & 1], (j >> 1) & 1, abort, lim)) return false;
-      tc_fence_after_sync();
-      mma_scores<DP>(leader, tmem + 256 + 128 * (j & 1), do_desc, v_desc + (j & 1) * kNext);
-      mma_commit_warp(leader, &bk.dp_full[j & 1]);
-      if (j + 2 < tiles) mma_commit_warp(leader, &bk.v_empty[j & 1]);
-      return true;
-    };
-    bool ok = warp_wait(&bk.q_full, 0, abort, lim) && products(0);
-    for (int j = 0; ok && j < tiles; ++j) {
-      if (j + 1 < tiles && !products(j + 1)) { ok = false; break; }
-      if (!warp_wait(&bk.ds_full, j & 1, abort, lim)) { ok = false; break; }
-      tc_fence_after_sync();
-      mma_sums<DP, 2>(leader, tmem, tmem + 256 + 128 * (j & 1), kt_desc + (j % kKStages) * kNext, j > 0);
-      if (j + kKStages < tiles) mma_commit_warp(leader, &bk.k_empty[j % kKStages]);
+    if (warp == kBwdMmaWarp) {
+      const uint64_t q_desc = scores_desc(q_smem), do_desc = scores_desc(do_smem), k_desc = scores_desc(k_smem),
+                     v_desc = scores_desc(v_smem);
+      warp_wait(&bk.q_full, 0, abort, lim);
+      for (int j = 0; j < tiles; ++j) {
+        // (the scores once the last ones have been read; dp's buffer once the ds before the last is dq's)
+        warp_wait(&bk.k_full[j % kKStages], (j / kKStages) & 1, abort, lim);
+        if (j > 0) warp_wait(&bk.s_empty, (j - 1) & 1, abort, lim);
+        tc_fence_after_sync();
+        mma_scores<DP>(leader, tmem + 128, q_desc, k_desc + (j % kKStages) * kNext);
+        mma_commit_warp(leader, &bk.s_full);
+        warp_wait(&bk.v_full[j & 1], (j >> 1) & 1, abort, lim);
+        if (j >= 2) warp_wait(&bk.dp_empty[j & 1], ((j >> 1) & 1) ^ 1u, abort, lim);
+        tc_fence_after_sync();
+        mma_scores<DP>(leader, tmem + 256 + 128 * (j & 1), do_desc, v_desc + (j & 1) * kNext);
+        mma_commit_warp(leader, &bk.dp_full[j & 1]);
+        if (j + 2 < tiles) mma_commit_warp(leader, &bk.v_empty[j & 1]);
+      }
+    } else {
+      const uint64_t kt_desc = sums_desc(k_smem);
+      for (int j = 0; j < tiles; ++j) {
+        warp_wait(&bk.ds_full, j & 1, abort, lim);
+        tc_fence_after_sync();
+        mma_sums<DP, 2>(leader, tmem, tmem + 256 + 128 * (j & 1), kt_desc + (j % kKStages) * kNext, j > 0);
+        if (j + 2 < tiles) mma_commit_warp(leader, &bk.dp_empty[j & 1]);
+        if (j + kKStages < tiles) mma_commit_warp(leader, &bk.k_empty[j % kKStages]);
+      }
     }
-    if (any) {
-      mma_commit_warp(leader, &bk.done);
-      mbar_wait_drain(&bk.done, 0);
-    }
+    mma_commit_warp(leader, &bk.done);
+    mbar_wait_drain(&bk.done, 0);
    }
   } else {
    more_registers<kBwdRegs>();
@@ -749,14 +745,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     delta = -row_sum(delta);
     arith_sync();                                  // (read by all before the next sum)
     const F32x2 lse2 = make_f32x2(lse, lse), mul2_ = make_f32x2(p.scale2, p.scale2);
-    bool ok = true;
     auto step = [&](int j, auto masked_c) {
       constexpr bool masked = decltype(masked_c)::value;
-      auto give_up = [&] {
-        if (masked && j == 0) arith_sync();        // (the others come to theirs)
-        return false;
-      };
-      if (!warp_wait(&bk.s_full, j & 1, abort, lim)) return give_up();
+      warp_wait(&bk.s_full, j & 1, abort, lim);
       tc_fence_after_sync();
       const int k0 = top - kRows * (j + 1);
       const int lo = max(key_lo, k0) - k0 - 32 * part, hi = min(key_hi, k0 + kRows) - k0 - 32 * part;
@@ -777,10 +768,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         s[x + 1] = __float_as_uint(y.y);
       }
       if (masked) {
-        if (!warp_wait(&bk.k_full[j % kKStages], (j / kKStages) & 1, abort, lim)) return give_up();
-        clean_tile<DP>(k_smem + (j % kKStages) * C::kBytes, threadIdx.x, kBwdArith);
+        warp_wait(&bk.k_full[j % kKStages], (j / kKStages) & 1, abort, lim);
+        clean_tile<DP>(k_smem + (j % kKStages) * C::kBytes, threadIdx.x, kBwdArith, [] {});
       }
-      if (!warp_wait(&bk.dp_full[j & 1], (j >> 1) & 1, abort, lim)) return give_up();
+      warp_wait(&bk.dp_full[j & 1], (j >> 1) & 1, abort, lim);
       const uint32_t tdp = tmem + lanes + 256 + 128 * (j & 1) + 32 * part;
       tc_fence_after_sync();
       tmem_ld_x32(tdp, d);
@@ -815,12 +806,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       tmem_st_x16(tdp, w);
       tmem_st_wait();
       warp_arrive(&bk.ds_full, lane);
-      return true;
     };
-    for (int j = 0; ok && j < n; ++j)
-      ok = j == 0 || top - kRows * (j + 1) < all_from ? step(j, std::true_type{}) : step(j, std::false_type{});
-    if (ok && warp_wait(&bk.done, 0, abort, lim)) {
-      tc_fence_after_sync();
+    for (int j = 0; j < n; ++j) {
+      if (j == 0 || top - kRows * (j + 1) < all_from)
+        step(j, std::true_type{});
+      else
+        step(j, std::false_type{});
+    }
+    warp_wait(&bk.done, 0, abort, lim);
+    tc_fence_after_sync();
+    {
       const int col = 32 * part;
       if (col < DP) {
         uint32_t o[32];
@@ -969,47 +964,50 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       got.drain(&bk.kv_full);
     }
    } else if (n > 0 && warp == kBwdMmaWarp) {
+    // (One warp for all: one for the scores and dv and one for dp and dk took 0.82 ms where this takes 0.66.)
     const uint32_t leader = elect_one() ? 1u : 0u;
     const uint64_t k_desc = scores_desc(k_smem), v_desc = scores_desc(v_smem), q_desc = scores_desc(q_smem),
-                   do_desc = scores_desc(do_smem), qt_desc = sums_desc(q_smem), dot_desc = sums_desc(do_smem);
-    const uint64_t ones_desc = rows_desc(ones_smem, zero_smem);
+                   do_desc = scores_desc(do_smem), qt_desc = sums_desc(q_smem), dot_desc = sums_desc(do_smem),
+                   ones_desc = rows_desc(ones_smem, zero_smem);
     constexpr uint64_t kNext = C::kBytes >> 4;
     const int tiles = uniform(n);
-    bool any = false;
     auto scores = [&](int j) {
-      if (!warp_wait(&bk.q_full[j & 1], (j >> 1) & 1, abort, lim)) return false;
-      tc_fence_after_sync();
       mma_scores<DP>(leader, tmem + 256, k_desc, q_desc + (j & 1) * kNext);
       mma_bf16_ss_warp(leader, tmem + 256, ones_desc, rows_desc(lse_smem + (j & 1) * kRowBytes, zero_smem), C::kScores, 1u);
       mma_commit_warp(leader, &bk.s_full);
-      any = true;
-      return true;
     };
     auto dprob = [&](int j) {
-      if (!warp_wait(&bk.do_full[j & 1], (j >> 1) & 1, abort, lim)) return false;
-      tc_fence_after_sync();
       mma_scores<DP>(leader, tmem + 384, v_desc, do_desc + (j & 1) * kNext);
       mma_bf16_ss_warp(leader, tmem + 384, ones_desc, rows_desc(delta_smem + (j & 1) * kRowBytes, zero_smem), C::kScores, 1u);
       mma_commit_warp(leader, &bk.dp_full);
-      return true;
     };
-    bool ok = warp_wait(&bk.kv_full, 0, abort, lim) && scores(0) && dprob(0);
-    for (int j = 0; ok && j < tiles; ++j) {
-      if (!warp_wait(&bk.p_full, j & 1, abort, lim)) { ok = false; break; }
+    warp_wait(&bk.kv_full, 0, abort, lim);
+    warp_wait(&bk.q_full[0], 0, abort, lim);
+    tc_fence_after_sync();
+    scores(0);
+    warp_wait(&bk.do_full[0], 0, abort, lim);
+    tc_fence_after_sync();
+    dprob(0);
+    for (int j = 0; j < tiles; ++j) {
+      warp_wait(&bk.p_full, j & 1, abort, lim);
       tc_fence_after_sync();
       mma_sums<DP, 2>(leader, tmem + 128, tmem + 256, dot_desc + (j & 1) * kNext, j > 0);
       if (j + 2 < tiles) mma_commit_warp(leader, &bk.do_empty[j & 1]);
-      if (j + 1 < tiles && !scores(j + 1)) { ok = false; break; }
-      if (!warp_wait(&bk.ds_full, j & 1, abort, lim)) { ok = false; break; }
+      if (j + 1 < tiles) {
+        warp_wait(&bk.q_full[(j + 1) & 1], ((j + 1) >> 1) & 1, abort, lim);
+        scores(j + 1);
+      }
+      warp_wait(&bk.ds_full, j & 1, abort, lim);
       tc_fence_after_sync();
       mma_sums<DP, 2>(leader, tmem, tmem + 384, qt_desc + (j & 1) * kNext, j > 0);
       if (j + 2 < tiles) mma_commit_warp(leader, &bk.q_empty[j & 1]);
-      if (j + 1 < tiles && !dprob(j + 1)) { ok = false; break; }
+      if (j + 1 < tiles) {
+        warp_wait(&bk.do_full[(j + 1) & 1], ((j + 1) >> 1) & 1, abort, lim);
+        dprob(j + 1);
+      }
     }
-    if (any) {
-      mma_commit_warp(leader, &bk.done);
-      mbar_wait_drain(&bk.done, 0);
-    }
+    mma_commit_warp(leader, &bk.done);
+    mbar_wait_drain(&bk.done, 0);
    }
   } else {
    more_registers<kBwdRegs>();
@@ -1021,20 +1019,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int key_end = valid ? end_of(&bk.map, k0, key, kRows / 32) : INT_MAX;
     const int all_to = end_of(&bk.map, k0, a, kRows / 32);      // queries up to here see every key (from the diagonal)
     const F32x2 mul2_ = make_f32x2(p.scale2, p.scale2);
-    bool ok = true;
     auto step = [&](int j, int q0, auto masked_c) {
       constexpr bool masked = decltype(masked_c)::value;
-      if (!warp_wait(&bk.s_full, j & 1, abort, lim)) return false;
+      warp_wait(&bk.s_full, j & 1, abort, lim);
       tc_fence_after_sync();
       const int lo = max(key, q0) - q0 - 32 * part, hi = min(key_end, q0 + kRows) - q0 - 32 * part;   // queries [lo, hi)
       uint32_t s[32], d[32], w[16];
       tmem_ld_x32(tmem + lanes + 256 + 32 * part, s);
       tmem_ld_wait(s);
       if (masked) {
-        if (!warp_wait(&bk.q_full[j & 1], (j >> 1) & 1, abort, lim) || !warp_wait(&bk.do_full[j & 1], (j >> 1) & 1, abort, lim))
-          return false;
-        clean_tile<DP>(do_smem + (j & 1) * C::kBytes, threadIdx.x, kBwdArith);
-        clean_tile<DP>(q_smem + (j & 1) * C::kBytes, threadIdx.x, kBwdArith);
+        warp_wait(&bk.q_full[j & 1], (j >> 1) & 1, abort, lim);
+        warp_wait(&bk.do_full[j & 1], (j >> 1) & 1, abort, lim);
+        clean_tile<DP>(do_smem + (j & 1) * C::kBytes, threadIdx.x, kBwdArith, [] {});
+        clean_tile<DP>(q_smem + (j & 1) * C::kBytes, threadIdx.x, kBwdArith, [] {});
       }
       #pragma unroll
       for (int x = 0; x < 32; x += 2) {
@@ -1052,7 +1049,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       tmem_st_x16(tmem + lanes + 256 + 32 * part, w);
       tmem_st_wait();
       warp_arrive(&bk.p_full, lane);
-      if (!warp_wait(&bk.dp_full, j & 1, abort, lim)) return false;
+      warp_wait(&bk.dp_full, j & 1, abort, lim);
       tc_fence_after_sync();
       tmem_ld_x32(tmem + lanes + 384 + 32 * part, d);
       tmem_ld_wait(d);
@@ -1068,16 +1065,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       tmem_st_x16(tmem + lanes + 384 + 32 * part, w);
       tmem_st_wait();
       warp_arrive(&bk.ds_full, lane);
-      return true;
     };
     int q0 = k0;
-    for (int j = 0; ok && j < n; ++j) {
-      ok = q0 == k0 || q0 + kRows > all_to ? step(j, q0, std::true_type{}) : step(j, q0, std::false_type{});
+    for (int j = 0; j < n; ++j) {
+      if (q0 == k0 || q0 + kRows > all_to)
+        step(j, q0, std::true_type{});
+      else
+        step(j, q0, std::false_type{});
       q0 += kRows;
       if (q0 >= k0 + nq * kRows) q0 = k0;
     }
-    if (ok && warp_wait(&bk.done, 0, abort, lim)) {
-      tc_fence_after_sync();
+    warp_wait(&bk.done, 0, abort, lim);
+    tc_fence_after_sync();
+    {
       // eight warps store dk, the others dv
       const int half = part >> 1;
       const Heads& to = half == 0 ? p.d0 : p.d1;
