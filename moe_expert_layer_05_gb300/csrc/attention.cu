@@ -263,14 +263,25 @@ struct Issued {
   }
 };
 
-// 32 columns of this thread's row, rounded, the words below the head's width.
-__device__ __forceinline__ void store_cols(__nv_bfloat16* row, int col, int D, const float (&v)[32]) {
+// 32 columns of a warp's 32 rows, a row a thread, rounded: through 2 KB of shared memory, so that a row's 64 bytes
+// leave together.  `out`: the first row; rows: which of them are stored; columns from D on are not.
+__device__ __forceinline__ void store_cols(uint8_t* staging, __nv_bfloat16* out, long long stride, uint32_t rows, int col,
+                                           int D, const float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+  uint4* s = reinterpret_cast<uint4*>(staging);
   #pragma unroll
   for (int w = 0; w < 4; ++w)
-    if (col + 8 * w < D)
-      *reinterpret_cast<uint4*>(row + col + 8 * w) =
-          make_uint4(pack_bf16x2(v[8 * w], v[8 * w + 1]), pack_bf16x2(v[8 * w + 2], v[8 * w + 3]),
-                     pack_bf16x2(v[8 * w + 4], v[8 * w + 5]), pack_bf16x2(v[8 * w + 6], v[8 * w + 7]));
+    s[lane * 4 + (w ^ (lane >> 1 & 3))] =
+        make_uint4(pack_bf16x2(v[8 * w], v[8 * w + 1]), pack_bf16x2(v[8 * w + 2], v[8 * w + 3]),
+                   pack_bf16x2(v[8 * w + 4], v[8 * w + 5]), pack_bf16x2(v[8 * w + 6], v[8 * w + 7]));
+  __syncwarp();
+  #pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2), w = lane & 3;
+    if ((rows >> r & 1u) && col + 8 * w < D)
+      *reinterpret_cast<uint4*>(out + r * stride + col + 8 * w) = s[r * 4 + (w ^ (r >> 1 & 3))];
+  }
+  __syncwarp();
 }
 
 // ---------------------------------------------------------------- forward
@@ -306,7 +317,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     return;
   }
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
+  if (warp == kFwdLoadWarp && lane == 0) {          // (it uses them before the first barrier of all threads)
     for (int s = 0; s < 8; ++s) {
       mbar_init(&bk.full[s], 1);
       mbar_init(&bk.empty[s], 1);
@@ -339,6 +350,21 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const int item = static_cast<int>(blockIdx.x) % per;
   const int t = p.tiles - 1 - static_cast<int>(blockIdx.x) / per;
   const int q0 = t * (p.pair_rows ? 2 * kRows : kRows);
+  // The queries, and where both tiles have the same rows the first keys, do not wait for the sequences' boundaries.
+  const bool early = !p.pair_rows;
+  const int kv = (p.pair_rows ? item : 2 * item) / (p.Hq / p.Hkv);
+  if (warp == kFwdLoadWarp && lane == 0) {
+    mbar_arrive_expect_tx(&bk.q_full, 2 * C::kBytes);
+    for (int u = 0; u < 2; ++u)
+      load_tile<DP>(q_smem + u * C::kBytes, &tmQ, &bk.q_full, p.pair_rows ? item : 2 * item + u,
+                    q0 + (p.pair_rows ? kRows * u : 0));
+    if (early) {
+      for (int s = 0; s < 2; ++s) {
+        mbar_arrive_expect_tx(&bk.full[s], C::kBytes);
+        load_tile<DP>(ring + s * C::kBytes, s ? &tmV : &tmK, &bk.full[s], kv, q0);
+      }
+    }
+  }
   row_map<2 * kRows>(p, q0, &bk.map);
   tc_fence_after_sync();
   const uint32_t tmem = uniform(bk.tmem);
@@ -356,25 +382,24 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     from[u] = p.pair_rows ? 1 - u : 0;
     to[u] = a < b ? from[u] + (base[u] + kRows - start_of(&bk.map, q0, a) + kRows - 1) / kRows : from[u];
   }
-  const int kv = head[0] / (p.Hq / p.Hkv);
   const bool on0 = to[0] > from[0], on1 = to[1] > from[1];
   const int ib = on1 ? from[1] : from[0];
   const int n = (on0 || on1) ? max(to[0], to[1]) - ib : 0;      // key tiles of this CTA
 
   if (warp >= kFwdLoadWarp) {
    fewer_registers<kFwdOtherRegs>();
-   if (n > 0 && warp == kFwdLoadWarp) {
+   if (warp == kFwdLoadWarp) {
     if (lane == 0) {
       Issued got;
-      mbar_arrive_expect_tx(&bk.q_full, (on0 ? C::kBytes : 0) + (on1 ? C::kBytes : 0));
-      if (on0) load_tile<DP>(q_smem, &tmQ, &bk.q_full, head[0], base[0]);
-      if (on1) load_tile<DP>(q_smem + C::kBytes, &tmQ, &bk.q_full, head[1], base[1]);
       got.note(8, 0);
-      bool ok = true;
-      for (int s = 0; s < 2 * n && ok; ++s) {                   // key, value, key, ...
+      if (early) {
+        got.note(0, 0);
+        got.note(1, 0);
+      }
+      for (int s = early ? 2 : 0; s < 2 * n; ++s) {             // key, value, key, ...
         const int slot = s % ST;
         const uint32_t ph = (s / ST) & 1;
-        if (s >= ST && !mbar_wait(&bk.empty[slot], ph ^ 1u, abort, lim)) { ok = false; break; }
+        if (s >= ST && !mbar_wait(&bk.empty[slot], ph ^ 1u, abort, lim)) break;
         mbar_arrive_expect_tx(&bk.full[slot], C::kBytes);
         load_tile<DP>(ring + slot * C::kBytes, (s & 1) ? &tmV : &tmK, &bk.full[slot], kv,
                       top - kRows * (ib + (s >> 1) + 1));
@@ -526,7 +551,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       tc_fence_after_sync();
       const float inv = 1.f / sum;
       const int bad_lo = *const_cast<volatile int*>(&bk.bad_lo), bad_hi = *const_cast<volatile int*>(&bk.bad_hi);
-      __nv_bfloat16* out = p.o.p + row * p.o.token + h * p.o.head;
+      const uint32_t rows = __ballot_sync(kFull, valid);
+      __nv_bfloat16* out = p.o.p + (row - lane) * p.o.token + h * p.o.head;
+      uint8_t* staging = q_smem + u * C::kBytes + (warp & 3) * 2048;        // (this tile's queries have been read)
       #pragma unroll 1
       for (int c = 0; c < DP / 32; ++c) {
         uint32_t o[32];
@@ -545,8 +572,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
               if (!isfinite(y)) v[x] += y;
             }
           }
-          store_cols(out, 32 * c, p.D, v);
         }
+        store_cols(staging, out, p.o.token, rows, 32 * c, p.D, v);
       }
       if (valid) p.lse[static_cast<long long>(h) * p.T + row] = (ref == -INFINITY ? 0.f : ref * p.scale) + logf(sum);
     }
@@ -591,6 +618,7 @@ struct DqBook {
   uint32_t tmem;
   int abort_flag;
   RowMap map;
+  float delta[kRows];
   float sums[kParts][kRows];               // parts of rows' sums
 };
 
@@ -612,7 +640,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     return;
   }
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
+  if (warp == kBwdLoadWarp && lane == 0) {          // (it uses them before the first barrier of all threads)
     mbar_init(&bk.q_full, 1);
     for (int s = 0; s < kKStages; ++s) {
       mbar_init(&bk.k_full[s], 1);
@@ -643,33 +671,41 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   pdl_wait();
   const int h = static_cast<int>(blockIdx.x) % p.Hq;
   const int q0 = (p.tiles - 1 - static_cast<int>(blockIdx.x) / p.Hq) * kRows;
+  // The queries and the first keys do not wait for the sequences' boundaries.
+  const int kv = h / (p.Hq / p.Hkv), top = q0 + kRows;
+  if (warp == kBwdLoadWarp && lane == 0) {
+    mbar_arrive_expect_tx(&bk.q_full, 2 * C::kBytes);
+    load_tile<DP>(q_smem, &tmQ, &bk.q_full, h, q0);
+    load_tile<DP>(do_smem, &tmDo, &bk.q_full, h, q0);
+    mbar_arrive_expect_tx(&bk.k_full[0], C::kBytes);
+    load_tile<DP>(k_smem, &tmK, &bk.k_full[0], kv, q0);
+    mbar_arrive_expect_tx(&bk.v_full[0], C::kBytes);
+    load_tile<DP>(v_smem, &tmV, &bk.v_full[0], kv, q0);
+  }
   row_map<kRows>(p, q0, &bk.map);
   tc_fence_after_sync();
   const uint32_t tmem = uniform(bk.tmem);
   volatile int* abort = &bk.abort_flag;
   const unsigned long long lim = p.wait_ns;
-  const int kv = h / (p.Hq / p.Hkv), top = q0 + kRows;
   const int a = max(q0, bk.map.first), b = min(top, bk.map.last);
   const int n = a < b ? (top - start_of(&bk.map, q0, a) + kRows - 1) / kRows : 0;
 
   if (warp >= kBwdLoadWarp) {
    fewer_registers<kBwdOtherRegs>();
-   if (n > 0 && warp == kBwdLoadWarp) {
+   if (warp == kBwdLoadWarp) {
     if (lane == 0) {
       Issued got;
-      mbar_arrive_expect_tx(&bk.q_full, 2 * C::kBytes);
-      load_tile<DP>(q_smem, &tmQ, &bk.q_full, h, q0);
-      load_tile<DP>(do_smem, &tmDo, &bk.q_full, h, q0);
       got.note(0, 0);
-      bool ok = true;
-      for (int j = 0; j < n && ok; ++j) {
+      got.note(1, 0);
+      got.note(1 + kKStages, 0);
+      for (int j = 1; j < n; ++j) {
         const int s = j % kKStages, s2 = j & 1, row = top - kRows * (j + 1);
         const uint32_t ph = (j / kKStages) & 1, ph2 = (j >> 1) & 1;
-        if (j >= kKStages && !mbar_wait(&bk.k_empty[s], ph ^ 1u, abort, lim)) { ok = false; break; }
+        if (j >= kKStages && !mbar_wait(&bk.k_empty[s], ph ^ 1u, abort, lim)) break;
         mbar_arrive_expect_tx(&bk.k_full[s], C::kBytes);
         load_tile<DP>(k_smem + s * C::kBytes, &tmK, &bk.k_full[s], kv, row);
         got.note(1 + s, ph);
-        if (j >= 2 && !mbar_wait(&bk.v_empty[s2], ph2 ^ 1u, abort, lim)) { ok = false; break; }
+        if (j >= 2 && !mbar_wait(&bk.v_empty[s2], ph2 ^ 1u, abort, lim)) break;
         mbar_arrive_expect_tx(&bk.v_full[s2], C::kBytes);
         load_tile<DP>(v_smem + s2 * C::kBytes, &tmV, &bk.v_full[s2], kv, row);
         got.note(1 + kKStages + s2, ph2);
@@ -721,29 +757,34 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const bool valid = row >= bk.map.first && row < bk.map.last;
     const int key_lo = valid ? start_of(&bk.map, q0, row) : p.T, key_hi = valid ? row : -1;
     const int all_from = start_of(&bk.map, q0, b - 1);
-    float delta = 0.f, lse = 0.f, lse_raw = 0.f;
-    if (valid) {
-      const uint4* o = reinterpret_cast<const uint4*>(p.o.p + row * p.o.token + h * p.o.head);
-      const uint4* d = reinterpret_cast<const uint4*>(p.dout.p + row * p.dout.token + h * p.dout.head);
+    // <do, o> of eight rows a warp, 16 lanes a row
+    {
+      float d[4];
+      uint4 x[4], y[4];
       #pragma unroll
-      for (int w = part; w < DP / 8; w += kParts)
-        if (8 * w < p.D) {
-          const uint4 x = o[w], y = d[w];
-          delta += bf16_lo(x.x) * bf16_lo(y.x) + bf16_hi(x.x) * bf16_hi(y.x) + bf16_lo(x.y) * bf16_lo(y.y) +
-                   bf16_hi(x.y) * bf16_hi(y.y) + bf16_lo(x.z) * bf16_lo(y.z) + bf16_hi(x.z) * bf16_hi(y.z) +
-                   bf16_lo(x.w) * bf16_lo(y.w) + bf16_hi(x.w) * bf16_hi(y.w);
+      for (int i = 0; i < 4; ++i) {
+        const int r = q0 + 8 * warp + 2 * i + (lane >> 4), w = lane & 15;
+        const bool in = r >= bk.map.first && r < bk.map.last && 8 * w < p.D;
+        x[i] = y[i] = make_uint4(0, 0, 0, 0);
+        if (in) {
+          x[i] = *reinterpret_cast<const uint4*>(p.o.p + r * p.o.token + h * p.o.head + 8 * w);
+          y[i] = *reinterpret_cast<const uint4*>(p.dout.p + r * p.dout.token + h * p.dout.head + 8 * w);
         }
-      const float l = p.lse[static_cast<long long>(h) * p.T + row];
-      lse = -l * kLog2e;
-      lse_raw = -l / p.scale;
+      }
+      #pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        d[i] = bf16_lo(x[i].x) * bf16_lo(y[i].x) + bf16_hi(x[i].x) * bf16_hi(y[i].x) + bf16_lo(x[i].y) * bf16_lo(y[i].y) +
+               bf16_hi(x[i].y) * bf16_hi(y[i].y) + bf16_lo(x[i].z) * bf16_lo(y[i].z) + bf16_hi(x[i].z) * bf16_hi(y[i].z) +
+               bf16_lo(x[i].w) * bf16_lo(y[i].w) + bf16_hi(x[i].w) * bf16_hi(y[i].w);
+        #pragma unroll
+        for (int m = 8; m > 0; m >>= 1) d[i] += __shfl_xor_sync(kFull, d[i], m);
+        if ((lane & 15) == 0) bk.delta[8 * warp + 2 * i + (lane >> 4)] = -d[i];
+      }
     }
-    auto row_sum = [&](float v) {
-      bk.sums[part][lr] = v;
-      arith_sync();
-      return (bk.sums[0][lr] + bk.sums[1][lr]) + (bk.sums[2][lr] + bk.sums[3][lr]);
-    };
-    delta = -row_sum(delta);
-    arith_sync();                                  // (read by all before the next sum)
+    const float l = valid ? p.lse[static_cast<long long>(h) * p.T + row] : 0.f;
+    const float lse = -l * kLog2e;
+    arith_sync();
+    float delta = bk.delta[lr];
     const F32x2 lse2 = make_f32x2(lse, lse), mul2_ = make_f32x2(p.scale2, p.scale2);
     auto step = [&](int j, auto masked_c) {
       constexpr bool masked = decltype(masked_c)::value;
@@ -784,11 +825,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           sum = fma2(make_f32x2(as_f(s[x]), as_f(s[x + 1])), make_f32x2(a0, a1), sum);
         }
         const float2 t = split_f32x2(sum);
-        const float exact = row_sum(t.x + t.y);
-        if (key_lo >= k0) delta = -exact;
+        bk.sums[part][lr] = t.x + t.y;
+        arith_sync();
+        if (key_lo >= k0) delta = -((bk.sums[0][lr] + bk.sums[1][lr]) + (bk.sums[2][lr] + bk.sums[3][lr]));
         if (valid && part == 0) {
           // (where do is not finite, nor is delta: p of this row shall not be either)
-          p.stats[h * p.pitch + row] = split_row(isfinite(delta) ? lse_raw : delta - delta);
+          p.stats[h * p.pitch + row] = split_row(isfinite(delta) ? -l / p.scale : delta - delta);
           p.stats[(p.Hq + h) * p.pitch + row] = split_row(delta);
         }
       }
@@ -824,7 +866,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tmem_ld_wait(o);
         #pragma unroll
         for (int x = 0; x < 32; ++x) v[x] = as_f(o[x]) * p.scale;
-        if (valid) store_cols(p.d0.p + row * p.d0.token + h * p.d0.head, col, p.D, v);
+        // (the tiles have been read)
+        store_cols(q_smem + warp * 2048, p.d0.p + (row - lane) * p.d0.token + h * p.d0.head, p.d0.token,
+                   __ballot_sync(kFull, valid), col, p.D, v);
       }
     }
    }
@@ -887,7 +931,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     return;
   }
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
+  if (warp == kBwdLoadWarp && lane == 0) {          // (it uses them before the first barrier of all threads)
     mbar_init(&bk.kv_full, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bk.q_full[s], 1);
@@ -920,12 +964,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   pdl_wait();
   const int split = p.split, rank = static_cast<int>(blockIdx.x) % split, item = static_cast<int>(blockIdx.x) / split;
   const int kv = item % p.Hkv, k0 = item / p.Hkv * kRows;
+  // The keys and the first queries do not wait for the sequences' boundaries.
+  const int group = p.Hq / p.Hkv, h0 = kv * group + rank * (group / split);
+  if (warp == kBwdLoadWarp && lane == 0) {
+    mbar_arrive_expect_tx(&bk.kv_full, 2 * C::kBytes);
+    load_tile<DP>(k_smem, &tmK, &bk.kv_full, kv, k0);
+    load_tile<DP>(v_smem, &tmV, &bk.kv_full, kv, k0);
+    mbar_arrive_expect_tx(&bk.q_full[0], C::kBytes + kRowBytes);
+    load_tile<DP>(q_smem, &tmQ, &bk.q_full[0], h0, k0);
+    bulk_load(lse_smem, p.stats + h0 * p.pitch + k0, kRowBytes, &bk.q_full[0]);
+    mbar_arrive_expect_tx(&bk.do_full[0], C::kBytes + kRowBytes);
+    load_tile<DP>(do_smem, &tmDo, &bk.do_full[0], h0, k0);
+    bulk_load(delta_smem, p.stats + (p.Hq + h0) * p.pitch + k0, kRowBytes, &bk.do_full[0]);
+  }
   row_map<kRows>(p, k0, &bk.map);
   tc_fence_after_sync();
   const uint32_t tmem = uniform(bk.tmem);
   volatile int* abort = &bk.abort_flag;
   const unsigned long long lim = p.wait_ns;
-  const int group = p.Hq / p.Hkv;
   // query tiles k0, k0 + 128, ... up to the end of the last key's sequence, for each of this CTA's heads
   const int a = max(k0, bk.map.first), b = min(k0 + kRows, bk.map.last);
   const int end = a < b ? end_of(&bk.map, k0, b - 1, kRows / 32) : k0;
@@ -933,33 +989,31 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
   if (warp >= kBwdLoadWarp) {
    fewer_registers<kBwdOtherRegs>();
-   if (n > 0 && warp == kBwdLoadWarp) {
+   if (warp == kBwdLoadWarp) {
     if (lane == 0) {
       Issued got;
-      mbar_arrive_expect_tx(&bk.kv_full, 2 * C::kBytes);
-      load_tile<DP>(k_smem, &tmK, &bk.kv_full, kv, k0);
-      load_tile<DP>(v_smem, &tmV, &bk.kv_full, kv, k0);
       got.note(0, 0);
-      bool ok = true;
-      int h = kv * group + rank * (group / split), row = k0;
-      for (int j = 0; j < n && ok; ++j) {
-        const int s = j & 1;
-        const uint32_t ph = (j >> 1) & 1;
-        if (j >= 2 && !mbar_wait(&bk.q_empty[s], ph ^ 1u, abort, lim)) { ok = false; break; }
-        mbar_arrive_expect_tx(&bk.q_full[s], C::kBytes + kRowBytes);
-        load_tile<DP>(q_smem + s * C::kBytes, &tmQ, &bk.q_full[s], h, row);
-        bulk_load(lse_smem + s * kRowBytes, p.stats + h * p.pitch + row, kRowBytes, &bk.q_full[s]);
-        got.note(1 + s, ph);
-        if (j >= 2 && !mbar_wait(&bk.do_empty[s], ph ^ 1u, abort, lim)) { ok = false; break; }
-        mbar_arrive_expect_tx(&bk.do_full[s], C::kBytes + kRowBytes);
-        load_tile<DP>(do_smem + s * C::kBytes, &tmDo, &bk.do_full[s], h, row);
-        bulk_load(delta_smem + s * kRowBytes, p.stats + (p.Hq + h) * p.pitch + row, kRowBytes, &bk.do_full[s]);
-        got.note(3 + s, ph);
+      got.note(1, 0);
+      got.note(3, 0);
+      int h = h0, row = k0;
+      for (int j = 1; j < n; ++j) {
         row += kRows;
         if (row >= k0 + nq * kRows) {
           row = k0;
           ++h;
         }
+        const int s = j & 1;
+        const uint32_t ph = (j >> 1) & 1;
+        if (j >= 2 && !mbar_wait(&bk.q_empty[s], ph ^ 1u, abort, lim)) break;
+        mbar_arrive_expect_tx(&bk.q_full[s], C::kBytes + kRowBytes);
+        load_tile<DP>(q_smem + s * C::kBytes, &tmQ, &bk.q_full[s], h, row);
+        bulk_load(lse_smem + s * kRowBytes, p.stats + h * p.pitch + row, kRowBytes, &bk.q_full[s]);
+        got.note(1 + s, ph);
+        if (j >= 2 && !mbar_wait(&bk.do_empty[s], ph ^ 1u, abort, lim)) break;
+        mbar_arrive_expect_tx(&bk.do_full[s], C::kBytes + kRowBytes);
+        load_tile<DP>(do_smem + s * C::kBytes, &tmDo, &bk.do_full[s], h, row);
+        bulk_load(delta_smem + s * kRowBytes, p.stats + (p.Hq + h) * p.pitch + row, kRowBytes, &bk.do_full[s]);
+        got.note(3 + s, ph);
       }
       got.drain(&bk.kv_full);
     }
@@ -1082,7 +1136,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const int half = part >> 1;
       const Heads& to = half == 0 ? p.d0 : p.d1;
       const float mul = half == 0 ? p.scale : 1.f;
-      __nv_bfloat16* out = to.p + key * to.token + kv * to.head;
+      __nv_bfloat16* out = to.p + (key - lane) * to.token + kv * to.head;
+      const uint32_t keys = __ballot_sync(kFull, valid);
       float4* row = sums + (half * kRows + key - k0) * (DP / 4);
       #pragma unroll
       for (int c = part & 1; c < DP / 32; c += 2) {
@@ -1093,7 +1148,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         #pragma unroll
         for (int x = 0; x < 32; ++x) v[x] = as_f(o[x]) * mul;
         if (split == 1) {
-          if (valid) store_cols(out, 32 * c, p.D, v);
+          store_cols(q_smem + warp * 2048, out, to.token, keys, 32 * c, p.D, v);
         } else {
           #pragma unroll
           for (int x = 0; x < 8; ++x)
