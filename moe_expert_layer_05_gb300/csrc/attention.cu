@@ -234,6 +234,11 @@ __device__ __forceinline__ void clean_tile(uint8_t* tile, int t, int n, F found)
   fence_proxy_async_smem();
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
 __device__ __forceinline__ float as_f(uint32_t v) { return __uint_as_float(v); }
 
@@ -474,46 +479,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       uint32_t s[4][32];
       const int k0 = top - kRows * (i + 1);
       const bool masked = i == f || k0 < all_from;
-      float mx[4];
-      tmem_ld_x32(ts, s[0]);
       #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        tmem_ld_wait(s[c]);
-        if (c < 3) tmem_ld_x32(ts + 32 * (c + 1), s[c + 1 < 4 ? c + 1 : 3]);
-        if (masked) {
-          const int lo = key_lo - k0 - 32 * c, hi = key_hi - k0 - 32 * c;
-          #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (j < lo || j > hi) s[c][j] = 0xff800000u;
-        }
-        mx[c] = fmaxf(as_f(s[c][0]), as_f(s[c][1]));
-        #pragma unroll
-        for (int j = 2; j < 32; j += 2) mx[c] = fmaxf(fmaxf(mx[c], as_f(s[c][j])), as_f(s[c][j + 1]));
-      }
-      const float m = fmaxf(ref, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-      if (i == f) {
-        ref = m;
-      } else {
-        const bool grow = m > ref + slack;
-        if (__any_sync(kFull, grow)) {
-          // (this tile's s_full came after the sums so far)
-          const float a = grow ? ex2((ref - m) * p.scale2) : 1.f;
-          if (grow) ref = m;
-          sum *= a;
-          #pragma unroll
-          for (int c = 0; c < DP / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld_x32(to_ + 32 * c, o);
-            tmem_ld_wait(o);
-            #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(as_f(o[j]) * a);
-            tmem_st_x32(to_ + 32 * c, o);
-          }
-        }
-      }
-      const float off = ref == -INFINITY ? 0.f : -ref * p.scale2;
-      const F32x2 off2 = make_f32x2(off, off), mul2_ = make_f32x2(p.scale2, p.scale2);
+      for (int c = 0; c < 4; ++c) tmem_ld_x32(ts + 32 * c, s[c]);
+      #pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld_wait(s[c]);
       if (masked) {
+        const int lo = key_lo - k0, hi = key_hi - k0;
+        #pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c < lo || c > hi) s[c >> 5][c & 31] = 0xff800000u;
         const int turn = 2 * (i - ib) + 1;
         warp_wait(&bk.full[turn % ST], (turn / ST) & 1, abort, lim);
         clean_tile<DP>(ring + (turn % ST) * C::kBytes, threadIdx.x & 127, 128, [&] {
@@ -522,29 +496,72 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           __threadfence_block();                 // (the other tile of rows may find the zeros: it shall know)
         });
       }
-      F32x2 part[4];
-      #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t w[32];
+      uint32_t w[32];
+      // probabilities of half the keys, packed, and their sum
+      auto exps = [&](int half) {
+        const float off = ref == -INFINITY ? 0.f : -ref * p.scale2;
+        const F32x2 off2 = make_f32x2(off, off), mul2_ = make_f32x2(p.scale2, p.scale2);
+        F32x2 part[2];
         #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t(&x)[32] = s[2 * half + c];
-          F32x2& sum2 = part[2 * half + c];
-          sum2 = make_f32x2(0.f, 0.f);
+          const uint32_t(&x)[32] = s[2 * half + c];
+          part[c] = make_f32x2(0.f, 0.f);
           #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const float2 y = split_f32x2(fma2(make_f32x2(as_f(x[2 * j]), as_f(x[2 * j + 1])), mul2_, off2));
             const F32x2 q = make_f32x2(ex2(y.x), ex2(y.y));
-            sum2 = add2(sum2, q);
+            part[c] = add2(part[c], q);
             w[16 * c + j] = pack_bf16x2(q);
           }
         }
-        tmem_st_x32(ts + 32 * half, w);
-        tmem_st_wait();
-        warp_arrive(&bk.p_full[u][half], lane);
+        return add2(part[0], part[1]);
+      };
+      // Narrow heads, whose products leave the exponentials the longer part, work out the first half by the reference
+      // so far while the maximum is found (it seldom moves): 300 us against 319 at 8192 rows, 32 heads.  Wide ones,
+      // whose products are the longer part, do not: 383 us against 414.
+      constexpr bool kAhead = DP == 64;
+      F32x2 total;
+      if (kAhead) total = exps(0);
+      float mx[8];
+      #pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const uint32_t* x = s[c >> 1] + 16 * (c & 1);
+        mx[c] = max3(as_f(x[0]), as_f(x[1]), as_f(x[2]));
+        #pragma unroll
+        for (int j = 3; j < 15; j += 2) mx[c] = max3(mx[c], as_f(x[j]), as_f(x[j + 1]));
       }
-      const float2 total = split_f32x2(add2(add2(part[0], part[1]), add2(part[2], part[3])));
-      sum += total.x + total.y;
+      #pragma unroll
+      for (int c = 0; c < 8; c += 2) mx[c] = max3(mx[c], as_f(s[c >> 1][15]), as_f(s[c >> 1][31]));
+      const float m = max3(max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[4]), max3(mx[5], mx[6], mx[7]), ref);
+      const bool grow = m > ref + slack;
+      if (__any_sync(kFull, grow)) {
+        const float a = grow ? ex2((ref - m) * p.scale2) : 1.f;
+        if (grow) ref = m;
+        sum *= a;
+        if (i > f) {
+          // (this tile's s_full came after the sums so far)
+          #pragma unroll 1
+          for (int c = 0; c < DP / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld_x16(to_ + 16 * c, o);
+            tmem_ld_wait(o);
+            #pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(as_f(o[j]) * a);
+            tmem_st_x16(to_ + 16 * c, o);
+          }
+        }
+        if (kAhead) total = exps(0);
+      }
+      if (!kAhead) total = exps(0);
+      tmem_st_x32(ts, w);
+      tmem_st_wait();
+      warp_arrive(&bk.p_full[u][0], lane);
+      total = add2(total, exps(1));
+      tmem_st_x32(ts + 32, w);
+      tmem_st_wait();
+      warp_arrive(&bk.p_full[u][1], lane);
+      const float2 t = split_f32x2(total);
+      sum += t.x + t.y;
     }
     if (e > f) {
       warp_wait(&bk.o_full[u], 0, abort, lim);
