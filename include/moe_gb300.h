@@ -579,8 +579,8 @@ typedef struct {
   float scale;
 } moe_attention_config;
 
-/* Workspace bytes of the two calls (0 on a bad config): the status region and 8 bytes
- * per row and query head.  Host only. */
+/* Workspace bytes of the two calls (0 on a bad config): the status region and 32 bytes
+ * per row (rounded up to 128) and query head.  Host only. */
 size_t moe_attention_workspace_bytes(const moe_attention_config* cfg);
 
 /* out[i] = sum_j p[i,j] v[j],  p[i,j] = exp(scale <q[i], k[j]> - lse[i]), over the rows j <= i
@@ -659,7 +659,8 @@ size_t moe_balance_loss_workspace_bytes(int32_t T, int32_t E);
  * below 0 is padding and does not count, whatever its row of logits and choices holds.
  * Outputs: loss [1] fp32, counts [E] int32, slope [E] fp32 (for the backward pass).  A logit of
  * -infinity has probability 0 (a row of nothing else: all 0).  A choice outside [0,E) is
- * not counted and sets MOE_ERR_BAD_INDEX on the device.  1 <= k <= 32, k <= E.  Sums in a
+ * not counted and sets MOE_ERR_BAD_INDEX on the device.  1 <= k <= 32, k <= E.  loss, counts
+ * and slope need an alignment of 4 bytes only (rows of a table of layers).  Sums in a
  * fixed order. */
 moe_status moe_balance_loss_forward(const float* logits, const int32_t* topk_idx, const int32_t* tokens, int32_t T,
                                     int32_t E, int32_t k, int32_t score, float* loss, int32_t* counts, float* slope,
@@ -686,7 +687,7 @@ typedef struct {
 /* Workspace bytes of moe_grad_norm for n tensors (0 <= n <= 2^20; 0 on a bad n).  Host only. */
 size_t moe_grad_norm_workspace_bytes(int32_t n);
 
-/* norm [1] fp32, device = the square root of the sum of the squares of all values of all tensors,
+/* norm [1] fp32, device (4-byte aligned) = the square root of the sum of the squares of all values of all tensors,
  * fp32 squares joined in fp64 (in fp64 from the start where squares leave fp32's range), in a
  * fixed order.  grads: n descriptions in host memory, which may be reused when the call
  * returns; at most 2^40 values a tensor. */

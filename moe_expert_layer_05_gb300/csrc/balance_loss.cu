@@ -313,7 +313,7 @@ moe_status moe_balance_loss_forward(const float* logits, const int32_t* topk_idx
                                     int32_t E, int32_t k, int32_t score, float* loss, int32_t* counts, float* slope,
                                     void* ws, size_t ws_bytes, void* stream) {
   if (!sizes_ok(T, E) || k <= 0 || k > kMaxK || k > E || !score_ok(score)) return MOE_ERR_INVALID_ARG;
-  if (!ptr_ok(loss) || !ptr_ok(counts) || !ptr_ok(slope) || !ptr_ok(ws) || !opt_ok(tokens)) return MOE_ERR_INVALID_ARG;
+  if (!word_ok(loss) || !word_ok(counts) || !word_ok(slope) || !ptr_ok(ws) || !opt_ok(tokens)) return MOE_ERR_INVALID_ARG;
   if (T > 0 && (!ptr_ok(logits) || !ptr_ok(topk_idx))) return MOE_ERR_INVALID_ARG;
   if (ws_bytes < moe_balance_loss_workspace_bytes(T, E)) return MOE_ERR_WORKSPACE;
   if (!device_is_gb300()) return MOE_ERR_UNSUPPORTED;
@@ -339,7 +339,7 @@ moe_status moe_balance_loss_forward(const float* logits, const int32_t* topk_idx
 
 moe_status moe_balance_loss_backward(const float* logits, const float* slope, const int32_t* tokens, int32_t T,
                                      int32_t E, int32_t score, const float* dloss, float* dlogits, void* stream) {
-  if (!sizes_ok(T, E) || !score_ok(score) || !ptr_ok(slope) || !ptr_ok(dloss) || !opt_ok(tokens))
+  if (!sizes_ok(T, E) || !score_ok(score) || !word_ok(slope) || !word_ok(dloss) || !opt_ok(tokens))
     return MOE_ERR_INVALID_ARG;
   if (T > 0 && (!ptr_ok(logits) || !ptr_ok(dlogits))) return MOE_ERR_INVALID_ARG;
   if (!device_is_gb300()) return MOE_ERR_UNSUPPORTED;

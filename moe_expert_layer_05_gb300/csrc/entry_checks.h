@@ -19,6 +19,8 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 // A required device pointer, and one that may be left out.
 inline bool ptr_ok(const void* p) { return p != nullptr && aligned16(p); }
 inline bool opt_ok(const void* p) { return aligned16(p); }
+// One that is read and written value by value.
+inline bool word_ok(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Hidden sizes of these operators: rows of whole 16-byte words.
 constexpr int kMaxH = 16384;

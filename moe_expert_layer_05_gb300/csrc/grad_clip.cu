@@ -273,7 +273,7 @@ size_t moe_grad_norm_workspace_bytes(int32_t n) {
 }
 
 moe_status moe_grad_norm(const moe_tensor* grads, int32_t n, float* norm, void* ws, size_t ws_bytes, void* stream) {
-  if (!list_ok(grads, n) || !ptr_ok(norm) || !ptr_ok(ws)) return MOE_ERR_INVALID_ARG;
+  if (!list_ok(grads, n) || !word_ok(norm) || !ptr_ok(ws)) return MOE_ERR_INVALID_ARG;
   if (ws_bytes < moe_grad_norm_workspace_bytes(n)) return MOE_ERR_WORKSPACE;
   if (!device_is_gb300()) return MOE_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -295,7 +295,7 @@ moe_status moe_grad_norm(const moe_tensor* grads, int32_t n, float* norm, void* 
 
 moe_status moe_grad_clip(const moe_tensor* grads, const moe_tensor* outs, int32_t n, const float* norm, float limit,
                          void* stream) {
-  if (!list_ok(grads, n) || !ptr_ok(norm) || !(limit >= 0.f)) return MOE_ERR_INVALID_ARG;
+  if (!list_ok(grads, n) || !word_ok(norm) || !(limit >= 0.f)) return MOE_ERR_INVALID_ARG;
   if (outs != nullptr) {
     if (!list_ok(outs, n)) return MOE_ERR_INVALID_ARG;
     for (int32_t i = 0; i < n; ++i)
