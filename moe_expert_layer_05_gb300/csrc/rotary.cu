@@ -11,8 +11,10 @@
 // fraction of a turn, exactly: off by 2^-62 (for pairs of up to a radian a position) times the
 // position, 2^-31 turns at the last one.
 //
-// A block works out the sines of kTokens tokens once for all heads, while its first values
-// are on their way.  Bound by HBM: every value is read and written once.
+// A block works out the sines of its tokens once for all heads, while its first values
+// are on their way; then a thread loads one piece of 16 values while it turns the one before, five
+// blocks to an SM.  Bound by HBM: every value is read and written once.  16384 tokens of 40 heads of 128 beside
+// 8 heads of values, 58 us (5.7 TB/s; four pieces at a time 62, six blocks 62, eight 75); one token 2.7 us.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -25,7 +27,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTokens = 8;             // of one block, at most
-constexpr int kAhead = 4;              // pieces a thread has on their way
+constexpr int kAhead = 1;              // pieces a thread loads at a time, while it turns the ones before
 constexpr int kMaxHeads = 1024, kMaxWidth = 512;      // (kTokens of the widest: 16 KB of sines)
 
 struct RotaryParams {
@@ -74,7 +76,7 @@ __device__ __forceinline__ unsigned long long turn_fraction(double freq) {
   return bits >> 63 ? 0 - r : r;
 }
 
-__global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const RotaryParams p) {
+__global__ void __launch_bounds__(kThreads, 5) rotary_kernel(const RotaryParams p) {
   extern __shared__ __align__(16) float2 s_turn[];         // [token][pair]: cos, sin, times scale
   pdl_entry();
   const int t0 = static_cast<int>(blockIdx.x) * p.block_tokens;
@@ -87,20 +89,23 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const RotaryParams 
     const int t = row / p.heads;
     return reinterpret_cast<const uint4*>(p.x + (t0 + t) * p.x_token + (row - t * p.heads) * p.x_head);
   };
-  uint4 a[kAhead], b[kAhead];
-  auto load = [&](int i0) {
+  struct Piece {
+    uint4 v, w;
+  };
+  Piece cur[kAhead], next[kAhead];
+  auto load = [&](Piece (&q)[kAhead], int i0) {
     #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int i = i0 + u * kThreads;
       if (i < all) {
         const int row = i / p.tasks, j = i - row * p.tasks;
         const uint4* w = src(row);
-        a[u] = w[first_word(j)];
-        if (second_word(j) < p.words) b[u] = w[second_word(j)];
+        q[u].v = w[first_word(j)];
+        if (second_word(j) < p.words) q[u].w = w[second_word(j)];
       }
     }
   };
-  load(threadIdx.x);
+  load(cur, threadIdx.x);
   for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
     const int t = i / pairs;
     const unsigned long long frac = turn_fraction(p.freq[i - t * pairs]);
@@ -110,20 +115,19 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const RotaryParams 
     s_turn[i] = make_float2(c * p.scale, (p.inverse ? -s : s) * p.scale);
   }
   __syncthreads();
-  for (int i0 = threadIdx.x; i0 < all; i0 += kAhead * kThreads) {
-    if (i0 != static_cast<int>(threadIdx.x)) load(i0);
+  auto turn = [&](Piece (&q)[kAhead], int i0) {
     #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int i = i0 + u * kThreads;
       if (i >= all) break;
       const int row = i / p.tasks, j = i - row * p.tasks, t = row / p.heads;
-      uint4 v = a[u], w = b[u];
+      uint4 v = q[u].v, w = q[u].w;
       if (j < p.turned) {
         const float4* r = reinterpret_cast<const float4*>(s_turn + t * pairs + 8 * j);
         #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float4 q = r[e];
-          const float2 r0 = make_float2(q.x, q.y), r1 = make_float2(q.z, q.w);
+          const float4 z = r[e];
+          const float2 r0 = make_float2(z.x, z.y), r1 = make_float2(z.z, z.w);
           if (p.interleaved) {
             // pairs 8 j + 2 e, + 1: the piece's 32-bit words 2 e, 2 e + 1
             uint32_t& lo = e == 0 ? v.x : e == 1 ? v.z : e == 2 ? w.x : w.z;
@@ -141,11 +145,18 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const RotaryParams 
       dst[first_word(j)] = v;
       if (second_word(j) < p.words) dst[second_word(j)] = w;
     }
+  };
+  constexpr int kRound = kAhead * kThreads;
+  for (int i0 = threadIdx.x; i0 < all; i0 += 2 * kRound) {
+    load(next, i0 + kRound);
+    turn(cur, i0);
+    load(cur, i0 + 2 * kRound);
+    turn(next, i0 + kRound);
   }
 }
 
 // Tokens of a block: as many as fill whole rounds of kAhead pieces a thread best (40 heads of 128, 8 pieces each:
-// three tokens make 0.94 of a round; four 1.25, and took 68 us where three take 57 at 16384 tokens).
+// four tokens make five rounds).
 int tokens_of_block(int T, int heads, int tasks) {
   constexpr long long kRound = kThreads * kAhead;
   int best = 1;
