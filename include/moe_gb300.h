@@ -154,7 +154,8 @@ moe_status moe_activation_layout(const moe_config* cfg, int32_t with_backward, m
  * grouped GEMMs' tile counter (ints 32 and 33), which hands out output tiles
  * in order and is back at zero after every GEMM launch, and the permutation's
  * count of finished histogram blocks (int 40, back at zero after each
- * moe_permute / bf16 moe_layer_forward).  Initialise them
+ * moe_permute / bf16 moe_layer_forward), and those of the balance loss and the gradient norm
+ * (ints 42 and 43, back at zero after each call).  Initialise them
  * once with moe_workspace_init before first use.  Calls that share one
  * workspace must not overlap on the GPU (issue them on one stream). */
 size_t moe_workspace_bytes(const moe_config* cfg);
@@ -573,7 +574,8 @@ typedef struct {
 /* T rows that hold `sequences` sequences one after the other.  Query head h goes with
  * key-value head h / (q_heads / kv_heads).  Limits: 0 <= T <= 2^24; 0 <= sequences <=
  * 2^24; 1 <= kv_heads, q_heads <= 1024 and a multiple of kv_heads; head_dim a multiple of
- * 8, at most 128; scale (of the scores, 1/sqrt(head_dim) as a rule) finite, above 0. */
+ * 8, at most 128; scale (of the scores, 1/sqrt(head_dim) as a rule) from 2^-64
+ * to 2^64. */
 typedef struct {
   int32_t T, sequences, q_heads, kv_heads, head_dim;
   float scale;
@@ -593,8 +595,8 @@ size_t moe_attention_workspace_bytes(const moe_attention_config* cfg);
  * the results are then unspecified, and nothing outside the tensors is touched.
  * A value that is not finite reaches the rows that see it and no other.
  * The probabilities are rounded to bf16 for the product with v, relative to a
- * reference within 2^8 of their maximum.  The same bits on every run.  Uses only the
- * status region of ws. */
+ * reference within 2^8 of their maximum.  The same bits on every run.  Outputs do not
+ * overlap inputs.  Uses only the status region of ws. */
 moe_status moe_attention_forward(const moe_attention_config* cfg, const moe_heads* q, const moe_heads* k,
                                  const moe_heads* v, const int32_t* cu_seqlens, const moe_heads* out, float* lse,
                                  void* ws, size_t ws_bytes, void* stream);
@@ -604,7 +606,7 @@ moe_status moe_attention_forward(const moe_attention_config* cfg, const moe_head
  *   dq[i] = scale sum_j ds[i,j] k[j],  dk[j] = scale sum_i ds[i,j] q[i],  dv[j] = sum_i p[i,j] dout[i],
  * dk and dv summed over the query heads of the group.  Shapes as q, k, v; each
  * rounded once from fp32 sums in a fixed order; p and ds are rounded to bf16 between
- * the products.  Rows of no sequence are left as they were.  Where a row of dout is
+ * the products.  Outputs overlap neither inputs nor each other.  Rows of no sequence are left as they were.  Where a row of dout is
  * not finite, so are dv, dk (whole rows) of what it sees and its dq. */
 moe_status moe_attention_backward(const moe_attention_config* cfg, const moe_heads* q, const moe_heads* k,
                                   const moe_heads* v, const int32_t* cu_seqlens, const moe_heads* out, const float* lse,
@@ -636,7 +638,7 @@ moe_status moe_rotary_frequencies(int32_t R, double base, int32_t scaling, doubl
  * values 2i, 2i + 1 (interleaved = 1) or i, i + R/2 (0).  Values from R on are copied.
  * x, out [T,heads,width] bf16 in strides of their own (see moe_heads); out is x itself with
  * the same strides, or does not overlap it.  positions [T] int32, any value; freq [R/2]
- * fp64, finite (device: moe_rotary_frequencies' or any other).  Angles are exact to 2^-24 of
+ * fp64 (device: moe_rotary_frequencies' or any other, up to 64 in size).  Angles are exact to 2^-24 of
  * a turn at any position; each value is rounded once.  0 <= T <= 2^24, heads <= 1024, width a
  * multiple of 8, at most 512, R a multiple of 16, at most the width. */
 moe_status moe_rotary(const moe_heads* x, const int32_t* positions, const double* freq, int32_t T, int32_t heads,
@@ -694,8 +696,9 @@ size_t moe_grad_norm_workspace_bytes(int32_t n);
 moe_status moe_grad_norm(const moe_tensor* grads, int32_t n, float* norm, void* ws, size_t ws_bytes, void* stream);
 
 /* out = g * min(1, limit / (norm[0] + 1e-6)), each value rounded once.  outs: as many
- * tensors of the same sizes and types that do not overlap the gradients, or NULL: in place,
- * and nothing is written where the factor is 1.  limit >= 0.  With an infinite norm the factor is 0
+ * tensors of the same sizes and types, or NULL: in place, and nothing is written where the
+ * factor is 1.  What is written overlaps nothing else of the call: no gradient and no other output
+ * (MOE_ERR_INVALID_ARG); the same gradient twice in place would be scaled twice.  limit >= 0.  With an infinite norm the factor is 0
  * (infinite values become NaN), with a NaN norm everything becomes NaN. */
 moe_status moe_grad_clip(const moe_tensor* grads, const moe_tensor* outs, int32_t n, const float* norm, float limit,
                          void* stream);

@@ -41,6 +41,7 @@ constexpr int kBwdArith = 512, kBwdThreads = kBwdArith + 128;
 constexpr int kParts = kBwdArith / kRows;  // gradients: threads that share a row, 32 columns each
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kMaxTokens = 1 << 24, kMaxHeads = 1024, kMaxHeadDim = 128, kMaxSequences = 1 << 24;
+constexpr float kMinScale = 0x1p-64f;      // (lse / scale and score * scale stay in fp32's range)
 
 struct Heads {                             // [T, heads, D] bf16, strides in elements
   __nv_bfloat16* p;
@@ -1283,7 +1284,7 @@ bool config_ok(const moe_attention_config* c) {
   if (c == nullptr || c->T < 0 || c->T > kMaxTokens || c->sequences < 0 || c->sequences > kMaxSequences) return false;
   if (c->q_heads <= 0 || c->q_heads > kMaxHeads || c->kv_heads <= 0 || c->q_heads % c->kv_heads != 0) return false;
   if (c->head_dim <= 0 || c->head_dim > kMaxHeadDim || c->head_dim % 8 != 0) return false;
-  return c->scale > 0.f && c->scale < INFINITY;
+  return c->scale >= kMinScale && c->scale <= 1.f / kMinScale;
 }
 long long stats_pitch(int T) { return (static_cast<long long>(T) + kRows - 1) / kRows * kRows; }
 

@@ -18,7 +18,9 @@
 // 4.8 MB together: 5.6 and 4.2 us, the norm's mostly the join of its blocks.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
+#include <new>
 
 #include "entry_checks.h"
 #include "ptx.cuh"
@@ -223,6 +225,40 @@ long long chunks_of(const moe_tensor& t) {
   const long long per = t.type == MOE_TYPE_FP32 ? 4 : 8;
   return ((t.n + per - 1) / per + kChunkWords - 1) / kChunkWords;
 }
+
+// Whether what a scaling writes overlaps nothing else of it: two threads would scale the same value.
+struct Span {
+  uintptr_t begin, end;
+  bool written;
+};
+void add_spans(Span* s, size_t& count, const moe_tensor* t, int32_t n, bool written) {
+  for (int32_t i = 0; i < n; ++i) {
+    if (t[i].n == 0) continue;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(t[i].data);
+    s[count++] = {at, at + static_cast<uintptr_t>(t[i].n) * (t[i].type == MOE_TYPE_FP32 ? 4 : 2), written};
+  }
+}
+bool apart(Span* s, size_t count) {
+  std::sort(s, s + count, [](const Span& a, const Span& b) { return a.begin < b.begin; });
+  uintptr_t any = 0, written = 0;          // where what came before ends
+  for (size_t i = 0; i < count; ++i) {
+    if (s[i].begin < (s[i].written ? any : written)) return false;
+    any = std::max(any, s[i].end);
+    if (s[i].written) written = std::max(written, s[i].end);
+  }
+  return true;
+}
+moe_status writes_apart(const moe_tensor* t, const moe_tensor* outs, int32_t n) {
+  Span few[2 * kList], *s = few;
+  if (n > kList) s = new (std::nothrow) Span[2 * static_cast<size_t>(n)];
+  if (s == nullptr) return MOE_ERR_WORKSPACE;
+  size_t count = 0;
+  add_spans(s, count, t, n, outs == nullptr);
+  if (outs != nullptr) add_spans(s, count, outs, n, true);
+  const bool ok = apart(s, count);
+  if (s != few) delete[] s;
+  return ok ? MOE_OK : MOE_ERR_INVALID_ARG;
+}
 int launches_of(int32_t n) { return n <= kList ? 1 : (n + kLongList - 1) / kLongList; }
 
 template <int N>
@@ -310,6 +346,8 @@ moe_status moe_grad_clip(const moe_tensor* grads, const moe_tensor* outs, int32_
     for (int32_t i = 0; i < n; ++i)
       if (outs[i].n != grads[i].n || outs[i].type != grads[i].type) return MOE_ERR_INVALID_ARG;
   }
+  const moe_status apart = writes_apart(grads, outs, n);
+  if (apart != MOE_OK) return apart;
   if (!device_is_gb300()) return MOE_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int per = n <= kList ? kList : kLongList;

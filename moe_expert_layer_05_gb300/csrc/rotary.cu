@@ -8,8 +8,8 @@
 //
 // Angles of far positions have no digits left in fp32, so a pair's frequency is taken in
 // turns as a 64-bit binary fraction, and position * fraction modulo 2^64 is the angle's
-// fraction of a turn, exactly: off by 2^-62 (for pairs of up to a radian a position) times the
-// position, 2^-31 turns at the last one.
+// fraction of a turn: off by 2^-62 (for pairs of up to a radian a position) times the position,
+// 2^-31 turns at the last one.
 //
 // A block works out the sines of its tokens once for all heads, while its first values
 // are on their way; then a thread loads one piece of 16 values while it turns the one before, five

@@ -1,0 +1,55 @@
+"""Calls that the step operators refuse at the edges of their ranges: scales whose scores leave fp32's range,
+gradients that would be scaled twice.  No GPU needed."""
+import pytest
+import torch
+
+from moe_expert_layer_05_gb300 import api
+from test_step_ops_abi import bwd, config, fwd, tensors
+
+NO_GPU = not torch.cuda.is_available()
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -65, 1e-38, 1e-44, 2.0 ** 65, 3e38])
+def test_scales_out_of_range_are_refused(scale):
+    """The gradients' kernels form lse / scale, the forward scale * log2 e: both have to have fp32 values."""
+    lib = api.load()
+    c = config(scale=scale)
+    assert lib.moe_attention_workspace_bytes(c) == 0
+    assert fwd(lib, c) == -1 and bwd(lib, c) == -1
+
+
+@pytest.mark.skipif(not NO_GPU, reason="fake pointers")
+@pytest.mark.parametrize("scale", [2.0 ** -64, 2.0 ** 64])
+def test_scales_at_the_ends_of_the_range_are_taken(scale):
+    lib = api.load()
+    assert fwd(lib, config(scale=scale)) == -2 and bwd(lib, config(scale=scale)) == -2
+
+
+def _many(n, first=1 << 20, step=64):
+    return [(first + step * i, 16, 1) for i in range(n)]        # 16 fp32 values each, end to end
+
+
+@pytest.mark.parametrize("n", [2, 64, 65, 600])
+def test_what_is_scaled_twice_is_refused(n):
+    lib = api.load()
+    def clip(grads, outs=None):
+        return lib.moe_grad_clip(tensors(*grads), tensors(*outs) if outs else None, len(grads), 16, 1.0, None)
+    taken = -2 if NO_GPU else None
+    grads, outs = _many(n), _many(n, first=1 << 30)
+    again, into = list(grads), list(grads)
+    again[-1] = grads[0]                                        # the same gradient twice
+    into[-1] = (grads[0][0] + 48, 16, 1)                        # one that begins inside another
+    assert clip(again) == -1 and clip(into) == -1
+    twice = list(outs)
+    twice[0] = (outs[1][0] - 16, 16, 1)                         # outputs that overlap
+    assert clip(grads, twice) == -1
+    assert clip(grads, grads) == -1                             # an output that is a gradient
+    reaching = list(outs)
+    reaching[0] = (grads[-1][0] + 48, 16, 1)
+    assert clip(grads, reaching) == -1
+    if NO_GPU:                                                  # (the pointers are fakes)
+        assert clip(grads) == taken and clip(grads, outs) == taken
+        assert clip(again, outs) == taken                       # a gradient that is only read, twice
+        empty = list(grads)
+        empty[0] = (grads[1][0], 0, 1)                          # nothing of it
+        assert clip(empty) == taken
