@@ -155,6 +155,7 @@ struct Tile {
   static constexpr int kBytes = kRows * DP * 2;
   static constexpr int kChunk = kRows * 128;           // 64 columns of all rows, 128-byte swizzled
   static constexpr int kStages = DP == 128 ? 4 : 8;    // forward: key and value tiles in flight
+  static constexpr int kBuffers = DP == 128 ? 2 : 3;   // forward: of scores in TMEM
   static constexpr uint32_t kScores = idesc_bf16_f32(128, 128, false, false);
   static constexpr uint32_t kSums = idesc_bf16_f32(128, DP, false, true);
 };
@@ -294,11 +295,18 @@ __device__ __forceinline__ void store_cols(uint8_t* staging, __nv_bfloat16* out,
 // A CTA has two tiles of 128 query rows, each with four warps, and one stream of key
 // and value tiles for both: two heads of a group on the same rows, or (groups of an
 // odd size) 256 rows of one head.  The tensor cores alternate between them: while one
-// tile's scores are exponentiated, the other's products run.  TMEM: scores 128
-// columns each (their first 64 become the probabilities), sums DP columns each.
+// tile's scores are exponentiated, the other's products run.  TMEM: buffers of scores of
+// 128 columns (their first 64 become the probabilities), sums DP columns a tile.
+//
+// Heads of up to 64 leave room for three buffers, taken in turn by both tiles: a tile's next scores are
+// there when it has exponentiated the last ones.  Scores and sums are then issued by a warp
+// each (one for both waits for one while the other could go on: 322 us against 264 at 8192 rows,
+// 32 heads of 64; with a buffer a tile 300).  Wide heads have a buffer a tile and one issuing warp (two: 0.53 ms
+// against 0.41).
 struct FwdBook {
   uint64_t full[8], q_full;                // (one after the other: Issued counts on it)
-  uint64_t empty[8], s_full[2], p_full[2][2], o_full[2], drain;
+  uint64_t empty[8], s_full[2][2], p_full[2][2], o_full[2], drain;
+  uint64_t free[3];                        // three buffers: the sums that read this one are done
   uint32_t tmem;
   int abort_flag;
   int bad_lo, bad_hi;                      // key rows of tiles in which clean_tile found something
@@ -312,7 +320,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const AttnParams p) {
   using C = Tile<DP>;
-  constexpr int ST = C::kStages;
+  constexpr int ST = C::kStages, L = C::kBuffers;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* q_smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = q_smem + 2 * C::kBytes;
@@ -330,12 +338,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     }
     mbar_init(&bk.q_full, 1);
     for (int u = 0; u < 2; ++u) {
-      mbar_init(&bk.s_full[u], 1);
-      mbar_init(&bk.p_full[u][0], 4);
-      mbar_init(&bk.p_full[u][1], 4);
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(&bk.s_full[u][x], 1);
+        mbar_init(&bk.p_full[u][x], 4);
+      }
       mbar_init(&bk.o_full[u], 1);
     }
-    mbar_init(&bk.drain, 1);
+    for (int s = 0; s < 3; ++s) mbar_init(&bk.free[s], 1);
+    mbar_init(&bk.drain, L == 2 ? 1 : 2);
     bk.abort_flag = 0;
     bk.bad_lo = INT_MAX;
     bk.bad_hi = -1;
@@ -413,8 +423,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       }
       got.drain(bk.full);                    // (they have landed by the end, unless another warp gave up)
     }
-   } else if (n > 0 && warp == kFwdMmaWarp) {
-    // (One warp for both tiles of rows: two that issue in turn slow each other, 0.53 ms against 0.41.)
+   } else if (n > 0 && (warp == kFwdMmaWarp || (L > 2 && warp == kFwdMmaWarp + 1))) {
     const uint32_t leader = elect_one() ? 1u : 0u;
     const uint64_t q_desc = scores_desc(q_smem), k_desc = scores_desc(ring), v_desc = sums_desc(ring);
     const int f0 = uniform(from[0]), f1 = uniform(from[1]), e0 = uniform(to[0]), e1 = uniform(to[1]);
@@ -422,38 +431,72 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int turns = 2 * (last - first + 1);
     auto full = [&](int s) { warp_wait(&bk.full[s % ST], (s / ST) & 1, abort, lim); };
     auto release = [&](int s) { if (s + ST < turns) mma_commit_warp(leader, &bk.empty[s % ST]); };
-    auto scores = [&](int u, int s) {
-      mma_scores<DP>(leader, tmem + 128 * u, q_desc + u * (C::kBytes >> 4), k_desc + (s % ST) * (C::kBytes >> 4));
-      mma_commit_warp(leader, &bk.s_full[u]);
-    };
-    warp_wait(&bk.q_full, 0, abort, lim);
-    full(0);
-    tc_fence_after_sync();
-    if (first >= f0 && first < e0) scores(0, 0);
-    if (first >= f1 && first < e1) scores(1, 0);
-    release(0);
-    for (int i = first; i <= last; ++i) {
-      const int sk = 2 * (i - first), sv = sk + 1;              // this key tile's and value tile's turn
-      full(sv);
-      if (i < last) full(sk + 2);
-      #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int f = u ? f1 : f0, e = u ? e1 : e0;
-        if (i >= f && i < e) {
-          // (the first half of the keys while the second is still exponentiated)
-          #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            warp_wait(&bk.p_full[u][half], (i - f) & 1, abort, lim);
-            tc_fence_after_sync();
-            mma_sums<DP, 8>(leader, tmem + 256 + DP * u, tmem + 128 * u, v_desc + (sv % ST) * (C::kBytes >> 4),
-                            i > f || half, 4 * half, 4 * half + 4);
-          }
-          if (i + 1 == e) mma_commit_warp(leader, &bk.o_full[u]);
-        }
-        if (i + 1 >= f && i + 1 < e) scores(u, sk + 2);
+    // scores number k: of tile k % 2 with key tile k / 2, in buffer k % L
+    auto scores = [&](int u, int i, uint32_t buffer) {
+      if (i > last) return;
+      const int s = 2 * (i - first), f = u ? f1 : f0;
+      if (u == 0) {
+        full(s);
+        tc_fence_after_sync();
       }
-      release(sv);
-      if (i < last) release(sk + 2);
+      if (i >= f && i < (u ? e1 : e0)) {
+        mma_scores<DP>(leader, tmem + buffer, q_desc + u * (C::kBytes >> 4), k_desc + (s % ST) * (C::kBytes >> 4));
+        mma_commit_warp(leader, &bk.s_full[u][(i - f) & 1]);
+      }
+      if (u == 1) release(s);
+    };
+    // the sums of tile u over value tile i
+    auto sums = [&](int u, int i, uint32_t buffer) {
+      const int s = 2 * (i - first) + 1, f = u ? f1 : f0, e = u ? e1 : e0;
+      if (u == 0) full(s);
+      if (i >= f && i < e) {
+        // (the first half of the keys while the second is still exponentiated)
+        #pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          warp_wait(&bk.p_full[u][half], (i - f) & 1, abort, lim);
+          tc_fence_after_sync();
+          mma_sums<DP, 8>(leader, tmem + 128 * L + DP * u, tmem + buffer, v_desc + (s % ST) * (C::kBytes >> 4),
+                          i > f || half, 4 * half, 4 * half + 4);
+        }
+        if (i + 1 == e) mma_commit_warp(leader, &bk.o_full[u]);
+      }
+      if (u == 1) release(s);
+    };
+    if constexpr (L == 2) {
+      warp_wait(&bk.q_full, 0, abort, lim);
+      scores(0, first, 0);
+      scores(1, first, 128);
+      for (int i = first; i <= last; ++i) {
+        sums(0, i, 0);
+        scores(0, i + 1, 0);
+        sums(1, i, 128);
+        scores(1, i + 1, 128);
+      }
+    } else if (warp == kFwdMmaWarp) {
+      warp_wait(&bk.q_full, 0, abort, lim);
+      uint32_t b = 0, turn = 1;
+      for (int i = first; i <= last; ++i) {
+        #pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (2 * (i - first) + u >= L) warp_wait(&bk.free[b], turn & 1, abort, lim);
+          tc_fence_after_sync();
+          scores(u, i, 128 * b);
+          if (++b == L) {
+            b = 0;
+            ++turn;
+          }
+        }
+      }
+    } else {
+      uint32_t b = 0;
+      for (int i = first; i <= last; ++i) {
+        #pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          sums(u, i, 128 * b);
+          mma_commit_warp(leader, &bk.free[b]);
+          b = b + 1 == L ? 0 : b + 1;
+        }
+      }
     }
     mma_commit_warp(leader, &bk.drain);      // (TMEM is given back after them, whoever gave up)
     mbar_wait_drain(&bk.drain, 0);
@@ -465,7 +508,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int u = warp >> 2;
     const int f = u ? from[1] : from[0], e = u ? to[1] : to[0], r0 = u ? base[1] : base[0], h = u ? head[1] : head[0];
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + 128 * u + lanes, to_ = tmem + 256 + DP * u + lanes;
+    const uint32_t to_ = tmem + 128 * L + DP * u + lanes;
+    int buffer = (2 * (f - ib) + u) % L;
     const int row = r0 + (warp & 3) * 32 + lane;
     const bool valid = row >= bk.map.first && row < bk.map.last;
     const int key_lo = valid ? start_of(&bk.map, q0, row) : INT_MIN / 2, key_hi = valid ? row : INT_MAX / 2;
@@ -475,8 +519,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const float slack = 8.f / p.scale2;
     float ref = -INFINITY, sum = 0.f;
     for (int i = f; i < e; ++i) {
-      warp_wait(&bk.s_full[u], (i - f) & 1, abort, lim);
+      warp_wait(&bk.s_full[u][(i - f) & 1], ((i - f) >> 1) & 1, abort, lim);
       tc_fence_after_sync();
+      const uint32_t ts = tmem + 128 * buffer + lanes;
+      if (L > 2) buffer = buffer > 0 ? buffer - 1 : L - 1;      // (two on)
       uint32_t s[4][32];
       const int k0 = top - kRows * (i + 1);
       const bool masked = i == f || k0 < all_from;
@@ -517,12 +563,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         return add2(part[0], part[1]);
       };
-      // Narrow heads, whose products leave the exponentials the longer part, work out the first half by the reference
-      // so far while the maximum is found (it seldom moves): 300 us against 319 at 8192 rows, 32 heads.  Wide ones,
-      // whose products are the longer part, do not: 383 us against 414.
-      constexpr bool kAhead = DP == 64;
-      F32x2 total;
-      if (kAhead) total = exps(0);
       float mx[8];
       #pragma unroll
       for (int c = 0; c < 8; ++c) {
@@ -540,7 +580,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (grow) ref = m;
         sum *= a;
         if (i > f) {
-          // (this tile's s_full came after the sums so far)
+          // (with two buffers this tile's scores come after the sums so far)
+          if (L > 2) {
+            const int k = 2 * (i - ib) + u - 2;          // (its sums have to be done)
+            warp_wait(&bk.free[k % L], (k / L) & 1, abort, lim);
+            tc_fence_after_sync();
+          }
           #pragma unroll 1
           for (int c = 0; c < DP / 16; ++c) {
             uint32_t o[16];
@@ -551,9 +596,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             tmem_st_x16(to_ + 16 * c, o);
           }
         }
-        if (kAhead) total = exps(0);
       }
-      if (!kAhead) total = exps(0);
+      F32x2 total = exps(0);
       tmem_st_x32(ts, w);
       tmem_st_wait();
       warp_arrive(&bk.p_full[u][0], lane);
