@@ -103,17 +103,18 @@ struct RowMap {
 // ranges inside [0, T] all the same.
 template <int R>
 __device__ __forceinline__ void row_map(const AttnParams& p, int r0, RowMap* m) {
+  int c = static_cast<int>(threadIdx.x) <= p.B ? p.cu[threadIdx.x] : 0;     // (on its way across the barrier)
   if (threadIdx.x < 8) m->bits[threadIdx.x] = 0u;
   if (threadIdx.x == 0) {
     m->start = 0;
     m->end = p.T;
-    m->first = max(p.cu[0], 0);
-    m->last = min(p.cu[p.B], p.T);
+    m->first = max(c, 0);
   }
   __syncthreads();
   int lo = 0, hi = p.T;
   for (int i = threadIdx.x; i <= p.B; i += blockDim.x) {
-    const int c = p.cu[i];
+    if (i != static_cast<int>(threadIdx.x)) c = p.cu[i];
+    if (i == p.B) m->last = min(c, p.T);
     if (c <= r0)
       lo = max(lo, c);
     else if (c >= r0 + R)
@@ -147,6 +148,13 @@ __device__ __forceinline__ int end_of(const RowMap* m, int r0, int row, int word
     if (++w >= words) return m->end;
     b = m->bits[w];
   }
+}
+
+// Bits lo .. hi of 32: the columns that a row sees.  (As bits: a comparison with each end takes three
+// instructions a place, of a kind that the SM starts every other cycle.)
+__device__ __forceinline__ uint32_t seen(int lo, int hi) {
+  const uint32_t from = lo <= 0 ? ~0u : lo > 31 ? 0u : ~0u << lo, to = hi >= 31 ? ~0u : hi < 0 ? 0u : ~(~1u << hi);
+  return from & to;
 }
 
 // ---------------------------------------------------------------- tiles
@@ -289,6 +297,35 @@ __device__ __forceinline__ void store_cols(uint8_t* staging, __nv_bfloat16* out,
       *reinterpret_cast<uint4*>(out + r * stride + col + 8 * w) = s[r * 4 + (w ^ (r >> 1 & 3))];
   }
   __syncwarp();
+}
+
+// A warp's 32 rows of DP columns in shared memory, rounded, the 16-byte words of a row turned round by its number:
+// a row a thread going in, whole rows after one another coming out.
+template <int DP>
+__device__ __forceinline__ uint4* staged_word(uint8_t* staging, int r, int w) {
+  return reinterpret_cast<uint4*>(staging) + r * (DP / 8) + (w ^ (r & 7));
+}
+template <int DP>
+__device__ __forceinline__ __nv_bfloat16* staged(uint8_t* staging, int r, int col) {
+  return reinterpret_cast<__nv_bfloat16*>(staged_word<DP>(staging, r, col >> 3)) + (col & 7);
+}
+template <int DP>
+__device__ __forceinline__ void put_cols(uint8_t* staging, int r, int col, const float (&v)[32]) {
+  #pragma unroll
+  for (int w = 0; w < 4; ++w)
+    *staged_word<DP>(staging, r, col / 8 + w) =
+        make_uint4(pack_bf16x2(v[8 * w], v[8 * w + 1]), pack_bf16x2(v[8 * w + 2], v[8 * w + 3]),
+                   pack_bf16x2(v[8 * w + 4], v[8 * w + 5]), pack_bf16x2(v[8 * w + 6], v[8 * w + 7]));
+}
+template <int DP>
+__device__ __forceinline__ void store_rows(uint8_t* staging, __nv_bfloat16* out, long long stride, uint32_t rows, int D) {
+  constexpr int kWords = DP / 8, kRowsAtOnce = 32 / kWords;
+  const int lane = threadIdx.x & 31, w = lane % kWords;
+  #pragma unroll
+  for (int r0 = 0; r0 < 32; r0 += kRowsAtOnce) {
+    const int r = r0 + lane / kWords;
+    if ((rows >> r & 1u) && 8 * w < D) *reinterpret_cast<uint4*>(out + r * stride + 8 * w) = *staged_word<DP>(staging, r, w);
+  }
 }
 
 // ---------------------------------------------------------------- forward
@@ -518,12 +555,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     // probabilities are relative to a reference that follows the maximum once it is 2^8 above
     const float slack = 8.f / p.scale2;
     float ref = -INFINITY, sum = 0.f;
+    uint32_t s[4][32];
     for (int i = f; i < e; ++i) {
       warp_wait(&bk.s_full[u][(i - f) & 1], ((i - f) >> 1) & 1, abort, lim);
       tc_fence_after_sync();
       const uint32_t ts = tmem + 128 * buffer + lanes;
       if (L > 2) buffer = buffer > 0 ? buffer - 1 : L - 1;      // (two on)
-      uint32_t s[4][32];
       const int k0 = top - kRows * (i + 1);
       const bool masked = i == f || k0 < all_from;
       #pragma unroll
@@ -531,10 +568,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld_wait(s[c]);
       if (masked) {
-        const int lo = key_lo - k0, hi = key_hi - k0;
         #pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c < lo || c > hi) s[c >> 5][c & 31] = 0xff800000u;
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t on = seen(key_lo - k0 - 32 * c, key_hi - k0 - 32 * c);
+          if (__all_sync(kFull, on == kFull)) continue;
+          #pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (!(on >> j & 1u)) s[c][j] = 0xff800000u;
+        }
         const int turn = 2 * (i - ib) + 1;
         warp_wait(&bk.full[turn % ST], (turn / ST) & 1, abort, lim);
         clean_tile<DP>(ring + (turn % ST) * C::kBytes, threadIdx.x & 127, 128, [&] {
@@ -614,29 +655,30 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const float inv = 1.f / sum;
       const int bad_lo = *const_cast<volatile int*>(&bk.bad_lo), bad_hi = *const_cast<volatile int*>(&bk.bad_hi);
       const uint32_t rows = __ballot_sync(kFull, valid);
-      __nv_bfloat16* out = p.o.p + (row - lane) * p.o.token + h * p.o.head;
-      uint8_t* staging = q_smem + u * C::kBytes + (warp & 3) * 2048;        // (this tile's queries have been read)
-      #pragma unroll 1
+      uint8_t* staging = q_smem + u * C::kBytes + (warp & 3) * (32 * DP * 2);       // (this tile's queries have been read)
+      #pragma unroll
+      for (int c = 0; c < DP / 32; ++c) tmem_ld_x32(to_ + 32 * c, s[c]);
+      #pragma unroll
       for (int c = 0; c < DP / 32; ++c) {
-        uint32_t o[32];
+        tmem_ld_wait(s[c]);
         float v[32];
-        tmem_ld_x32(to_ + 32 * c, o);
-        tmem_ld_wait(o);
         #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = as_f(o[j]) * inv;
-        if (valid) {
-          // what clean_tile took out, for the rows that see it
-          for (int j = max(key_lo, bad_lo); j <= min(key_hi, bad_hi); ++j) {
-            const __nv_bfloat16* src = p.d0.p + j * p.d0.token + kv * p.d0.head + 32 * c;
-            #pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              const float y = 32 * c + x < p.D ? __bfloat162float(src[x]) : 0.f;
-              if (!isfinite(y)) v[x] += y;
-            }
+        for (int j = 0; j < 32; ++j) v[j] = as_f(s[c][j]) * inv;
+        put_cols<DP>(staging, lane, 32 * c, v);
+      }
+      if (valid) {
+        // what clean_tile took out, for the rows that see it
+        for (int j = max(key_lo, bad_lo); j <= min(key_hi, bad_hi); ++j) {
+          const __nv_bfloat16* src = p.d0.p + j * p.d0.token + kv * p.d0.head;
+          for (int x = 0; x < p.D; ++x) {
+            const float y = __bfloat162float(src[x]);
+            __nv_bfloat16* at = staged<DP>(staging, lane, x);
+            if (!isfinite(y)) *at = __float2bfloat16(__bfloat162float(*at) + y);
           }
         }
-        store_cols(staging, out, p.o.token, rows, 32 * c, p.D, v);
       }
+      __syncwarp();
+      store_rows<DP>(staging, p.o.p + (row - lane) * p.o.token + h * p.o.head, p.o.token, rows, p.D);
       if (valid) p.lse[static_cast<long long>(h) * p.T + row] = (ref == -INFINITY ? 0.f : ref * p.scale) + logf(sum);
     }
   }
@@ -853,7 +895,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       warp_wait(&bk.s_full, j & 1, abort, lim);
       tc_fence_after_sync();
       const int k0 = top - kRows * (j + 1);
-      const int lo = max(key_lo, k0) - k0 - 32 * part, hi = min(key_hi, k0 + kRows) - k0 - 32 * part;
+      const uint32_t on = masked ? seen(key_lo - k0 - 32 * part, key_hi - k0 - 32 * part) : kFull;
       uint32_t s[32], d[32], w[16];
       tmem_ld_x32(tmem + lanes + 128 + 32 * part, s);
       tmem_ld_wait(s);
@@ -864,8 +906,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         y.x = ex2(y.x);
         y.y = ex2(y.y);
         if (masked) {
-          if (x < lo || x > hi) y.x = 0.f;
-          if (x + 1 < lo || x + 1 > hi) y.y = 0.f;
+          if (!(on >> x & 1u)) y.x = 0.f;
+          if (!(on >> x & 2u)) y.y = 0.f;
         }
         s[x] = __float_as_uint(y.x);
         s[x + 1] = __float_as_uint(y.y);
@@ -883,7 +925,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         F32x2 sum = make_f32x2(0.f, 0.f);
         #pragma unroll
         for (int x = 0; x < 32; x += 2) {
-          const float a0 = (x < lo || x > hi) ? 0.f : as_f(d[x]), a1 = (x + 1 < lo || x + 1 > hi) ? 0.f : as_f(d[x + 1]);
+          const float a0 = on >> x & 1u ? as_f(d[x]) : 0.f, a1 = on >> x & 2u ? as_f(d[x + 1]) : 0.f;
           sum = fma2(make_f32x2(as_f(s[x]), as_f(s[x + 1])), make_f32x2(a0, a1), sum);
         }
         const float2 t = split_f32x2(sum);
@@ -902,8 +944,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         float2 y = split_f32x2(mul2(make_f32x2(as_f(s[x]), as_f(s[x + 1])),
                                     add2(make_f32x2(as_f(d[x]), as_f(d[x + 1])), delta2)));
         if (masked) {
-          if (x < lo || x > hi) y.x = 0.f;
-          if (x + 1 < lo || x + 1 > hi) y.y = 0.f;
+          if (!(on >> x & 1u)) y.x = 0.f;
+          if (!(on >> x & 2u)) y.y = 0.f;
         }
         w[x / 2] = pack_bf16x2(y.x, y.y);
       }
@@ -1139,7 +1181,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       constexpr bool masked = decltype(masked_c)::value;
       warp_wait(&bk.s_full, j & 1, abort, lim);
       tc_fence_after_sync();
-      const int lo = max(key, q0) - q0 - 32 * part, hi = min(key_end, q0 + kRows) - q0 - 32 * part;   // queries [lo, hi)
+      const uint32_t on = masked ? seen(key - q0 - 32 * part, key_end - 1 - q0 - 32 * part) : kFull;      // queries [key, key_end)
       uint32_t s[32], d[32], w[16];
       tmem_ld_x32(tmem + lanes + 256 + 32 * part, s);
       tmem_ld_wait(s);
@@ -1155,8 +1197,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         y.x = ex2(y.x);
         y.y = ex2(y.y);
         if (masked) {
-          if (x < lo || x >= hi) y.x = 0.f;
-          if (x + 1 < lo || x + 1 >= hi) y.y = 0.f;
+          if (!(on >> x & 1u)) y.x = 0.f;
+          if (!(on >> x & 2u)) y.y = 0.f;
         }
         s[x] = __float_as_uint(y.x);
         s[x + 1] = __float_as_uint(y.y);
@@ -1173,8 +1215,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       for (int x = 0; x < 32; x += 2) {
         float2 y = split_f32x2(mul2(make_f32x2(as_f(s[x]), as_f(s[x + 1])), make_f32x2(as_f(d[x]), as_f(d[x + 1]))));
         if (masked) {
-          if (x < lo || x >= hi) y.x = 0.f;
-          if (x + 1 < lo || x + 1 >= hi) y.y = 0.f;
+          if (!(on >> x & 1u)) y.x = 0.f;
+          if (!(on >> x & 2u)) y.y = 0.f;
         }
         w[x / 2] = pack_bf16x2(y.x, y.y);
       }
