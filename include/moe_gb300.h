@@ -154,8 +154,8 @@ moe_status moe_activation_layout(const moe_config* cfg, int32_t with_backward, m
  * grouped GEMMs' tile counter (ints 32 and 33), which hands out output tiles
  * in order and is back at zero after every GEMM launch, and the permutation's
  * count of finished histogram blocks (int 40, back at zero after each
- * moe_permute / bf16 moe_layer_forward), and those of the balance loss and the gradient norm
- * (ints 42 and 43, back at zero after each call).  Initialise them
+ * moe_permute / bf16 moe_layer_forward), those of the balance loss and the gradient norm
+ * and the attention's count of items handed out (ints 42, 43 and 44, back at zero after each call).  Initialise them
  * once with moe_workspace_init before first use.  Calls that share one
  * workspace must not overlap on the GPU (issue them on one stream). */
 size_t moe_workspace_bytes(const moe_config* cfg);

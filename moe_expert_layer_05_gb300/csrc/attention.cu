@@ -55,7 +55,7 @@ struct AttnParams {
   int pair_rows;           // forward: the two tiles of a CTA are rows of one head (else two heads of one group)
   int tiles;               // tiles along the rows
   int split;               // dk, dv: CTAs that share a group's heads
-  Heads o, d0, d1;         // forward: out; gradients: dq or dk, dv
+  Heads o, d0, d1;         // forward: out, v, q; gradients: out, dq or dk, dv
   Heads dout;
   float* lse;              // [Hq, T]
   uint4* stats;            // [2][Hq, pitch]: -lse / scale, -delta, each as eight bf16 (split_row)
@@ -148,6 +148,58 @@ __device__ __forceinline__ int end_of(const RowMap* m, int r0, int row, int word
     if (++w >= words) return m->end;
     b = m->bits[w];
   }
+}
+
+// The same by one warp, for kernels whose CTAs work through many tiles: the boundaries ascend, so a search by 32 at
+// a time finds the last one at or before r0.  mine: boundary number `lane`, or INT_MAX past the last.
+template <int R>
+__device__ __forceinline__ void find_map(const AttnParams& p, int r0, int mine, int first, int last, RowMap* m) {
+  const int lane = threadIdx.x & 31;
+  if (lane < 8) m->bits[lane] = 0u;
+  __syncwarp();
+  int at = 0, n = p.B + 1;                 // it is the first of these n, or further on among them (or there is none)
+  while (n > 32) {
+    const int step = (n + 31) / 32;
+    const int k = __popc(__ballot_sync(kFull, lane * step < n && p.cu[at + lane * step] <= r0));
+    if (k == 0) break;
+    at += (k - 1) * step;
+    n = min(step, n - (k - 1) * step);
+  }
+  int lo = 0, hi = p.T;
+  for (int i = at + lane;; i += 32) {
+    const bool in = i <= p.B;
+    const int c = i == lane ? mine : in ? p.cu[i] : INT_MAX;
+    if (c <= r0)
+      lo = max(lo, c);
+    else if (c >= r0 + R)
+      hi = min(hi, c);
+    else
+      atomicOr(&m->bits[(c - r0) >> 5], 1u << ((c - r0) & 31));
+    if (__any_sync(kFull, !in || c >= r0 + R)) break;
+  }
+  lo = __reduce_max_sync(kFull, lo);
+  hi = __reduce_min_sync(kFull, hi);
+  if (lane == 0) {
+    m->first = first;
+    m->last = last;
+    m->start = lo;
+    m->end = hi;
+  }
+  __syncwarp();
+}
+// Boundaries that do not ascend or lie outside [0, T] are reported; a warp of each CTA, its share.
+__device__ __forceinline__ void check_boundaries(const AttnParams& p) {
+  for (int i = static_cast<int>(blockIdx.x) * 32 + (threadIdx.x & 31); i <= p.B; i += static_cast<int>(gridDim.x) * 32) {
+    const int c = p.cu[i];
+    if (c < 0 || c > p.T || (i > 0 && p.cu[i - 1] > c)) set_status(p.status, kErrBadIndex);
+  }
+}
+// The next of `items` for one of `grid` CTAs, each of which began with the one of its own number and takes them until
+// there is none: of as many takes as items the last puts the counter back to zero.
+__device__ __forceinline__ int take_item(int* status, int items, int grid) {
+  const int before = atomicAdd(status + kAttentionItemWord, 1);
+  if (before == items - 1) atomicExch(status + kAttentionItemWord, 0);
+  return before + grid;
 }
 
 // Bits lo .. hi of 32: the columns that a row sees.  (As bits: a comparison with each end takes three
@@ -299,39 +351,37 @@ __device__ __forceinline__ void store_cols(uint8_t* staging, __nv_bfloat16* out,
   __syncwarp();
 }
 
-// A warp's 32 rows of DP columns in shared memory, rounded, the 16-byte words of a row turned round by its number:
+// A warp's 32 rows of 64 columns in shared memory, rounded, the 16-byte words of a row turned round by its number:
 // a row a thread going in, whole rows after one another coming out.
-template <int DP>
 __device__ __forceinline__ uint4* staged_word(uint8_t* staging, int r, int w) {
-  return reinterpret_cast<uint4*>(staging) + r * (DP / 8) + (w ^ (r & 7));
+  return reinterpret_cast<uint4*>(staging) + r * 8 + (w ^ (r & 7));
 }
-template <int DP>
 __device__ __forceinline__ __nv_bfloat16* staged(uint8_t* staging, int r, int col) {
-  return reinterpret_cast<__nv_bfloat16*>(staged_word<DP>(staging, r, col >> 3)) + (col & 7);
+  return reinterpret_cast<__nv_bfloat16*>(staged_word(staging, r, col >> 3)) + (col & 7);
 }
-template <int DP>
 __device__ __forceinline__ void put_cols(uint8_t* staging, int r, int col, const float (&v)[32]) {
   #pragma unroll
   for (int w = 0; w < 4; ++w)
-    *staged_word<DP>(staging, r, col / 8 + w) =
+    *staged_word(staging, r, col / 8 + w) =
         make_uint4(pack_bf16x2(v[8 * w], v[8 * w + 1]), pack_bf16x2(v[8 * w + 2], v[8 * w + 3]),
                    pack_bf16x2(v[8 * w + 4], v[8 * w + 5]), pack_bf16x2(v[8 * w + 6], v[8 * w + 7]));
 }
-template <int DP>
+// The first D columns of the rows that `rows` names.
 __device__ __forceinline__ void store_rows(uint8_t* staging, __nv_bfloat16* out, long long stride, uint32_t rows, int D) {
-  constexpr int kWords = DP / 8, kRowsAtOnce = 32 / kWords;
-  const int lane = threadIdx.x & 31, w = lane % kWords;
+  const int lane = threadIdx.x & 31, w = lane & 7;
   #pragma unroll
-  for (int r0 = 0; r0 < 32; r0 += kRowsAtOnce) {
-    const int r = r0 + lane / kWords;
-    if ((rows >> r & 1u) && 8 * w < D) *reinterpret_cast<uint4*>(out + r * stride + 8 * w) = *staged_word<DP>(staging, r, w);
+  for (int r0 = 0; r0 < 32; r0 += 4) {
+    const int r = r0 + (lane >> 3);
+    if ((rows >> r & 1u) && 8 * w < D) *reinterpret_cast<uint4*>(out + r * stride + 8 * w) = *staged_word(staging, r, w);
   }
 }
 
 // ---------------------------------------------------------------- forward
 // A CTA has two tiles of 128 query rows, each with four warps, and one stream of key
 // and value tiles for both: two heads of a group on the same rows, or (groups of an
-// odd size) 256 rows of one head.  The tensor cores alternate between them: while one
+// odd size) 256 rows of one head.  The CTAs stay and take such items one after the other: one's outputs are written
+// while the next one's first products run.  (A CTA for each lost 14 thousand cycles an item before its first key
+// tile and after its last, of 2800 a key tile; this one 9.)  The tensor cores alternate between them: while one
 // tile's scores are exponentiated, the other's products run.  TMEM: buffers of scores of
 // 128 columns (their first 64 become the probabilities), sums DP columns a tile.
 //
@@ -340,17 +390,36 @@ __device__ __forceinline__ void store_rows(uint8_t* staging, __nv_bfloat16* out,
 // each (one for both waits for one while the other could go on: 322 us against 264 at 8192 rows,
 // 32 heads of 64; with a buffer a tile 300).  Wide heads have a buffer a tile and one issuing warp (two: 0.53 ms
 // against 0.41).
+//
+// A barrier that is waited for by parity has to be seen before its next phase ends.  With three buffers a tile's next
+// probabilities can be there before the last ones' arrival has been looked at, so their barriers are two, in turns.
+struct FwdItem {                           // two tiles of query rows
+  RowMap map;
+  int item;                                // -1: no more
+  int q0, top, kv;
+  int from[2], to[2], base[2], head[2], ib, n;
+  int loaded;                              // key and value tiles in the ring: 2 n, or the first ones of an item without rows
+  int bad_lo, bad_hi;                      // key rows of tiles in which clean_tile found something
+};
 struct FwdBook {
   uint64_t full[8], q_full;                // (one after the other: Issued counts on it)
-  uint64_t empty[8], s_full[2][2], p_full[2][2], o_full[2], drain;
+  uint64_t empty[8], q_empty, s_full[2][2], p_full[2][2][2], o_full[2], o_empty[2], drain;
   uint64_t free[3];                        // three buffers: the sums that read this one are done
+  uint64_t item_full[2], item_empty[2], ending;
   uint32_t tmem;
   int abort_flag;
-  int bad_lo, bad_hi;                      // key rows of tiles in which clean_tile found something
-  RowMap map;
+  FwdItem item[2];
 };
 
-constexpr int kFwdLoadWarp = kFwdArith / 32, kFwdMmaWarp = kFwdLoadWarp + 1;
+constexpr int kFwdLoadWarp = kFwdArith / 32, kFwdMmaWarp = kFwdLoadWarp + 1, kFwdItemWarp = kFwdLoadWarp + 3;
+constexpr int kFwdStaging = kFwdArith / 32 * 4096;       // 32 rows of 64 columns a warp
+
+// Item i of the grid: the last tiles first, they have the longest rows of keys.
+__device__ __forceinline__ void fwd_place(const AttnParams& p, int i, int& q0, int& first_head) {
+  const int per = p.pair_rows ? p.Hq : p.Hq / 2;
+  q0 = (p.tiles - 1 - i / per) * (p.pair_rows ? 2 * kRows : kRows);
+  first_head = i % per * (p.pair_rows ? 1 : 2);
+}
 
 template <int DP>
 __global__ void __launch_bounds__(kFwdThreads, 1)
@@ -361,7 +430,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* q_smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = q_smem + 2 * C::kBytes;
-  FwdBook& bk = *reinterpret_cast<FwdBook*>(ring + ST * C::kBytes);
+  uint8_t* out_smem = ring + ST * C::kBytes;
+  FwdBook& bk = *reinterpret_cast<FwdBook*>(out_smem + kFwdStaging);
   if (!smem_fits(smem_raw, &bk + 1)) {
     pdl_wait();
     if (threadIdx.x == 0) set_status(p.status, kErrLaunch);
@@ -374,18 +444,22 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       mbar_init(&bk.empty[s], 1);
     }
     mbar_init(&bk.q_full, 1);
+    mbar_init(&bk.q_empty, 1);
     for (int u = 0; u < 2; ++u) {
       for (int x = 0; x < 2; ++x) {
         mbar_init(&bk.s_full[u][x], 1);
-        mbar_init(&bk.p_full[u][x], 4);
+        mbar_init(&bk.p_full[u][x][0], 4);
+        mbar_init(&bk.p_full[u][x][1], 4);
       }
       mbar_init(&bk.o_full[u], 1);
+      mbar_init(&bk.o_empty[u], 4);
+      mbar_init(&bk.item_full[u], 1);
+      mbar_init(&bk.item_empty[u], 1 + (L == 2 ? 1 : 2) + kFwdArith / 32);      // loads, products, arithmetic
     }
     for (int s = 0; s < 3; ++s) mbar_init(&bk.free[s], 1);
+    mbar_init(&bk.ending, 1);
     mbar_init(&bk.drain, L == 2 ? 1 : 2);
     bk.abort_flag = 0;
-    bk.bad_lo = INT_MAX;
-    bk.bad_hi = -1;
     fence_mbarrier_init();
     prefetch_tensormap(&tmQ);
     prefetch_tensormap(&tmK);
@@ -398,166 +472,268 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   tc_fence_before_sync();
   pdl_wait();
 
-  // the last tiles first: they have the longest rows of keys
-  const int per = p.pair_rows ? p.Hq : p.Hq / 2;
-  const int item = static_cast<int>(blockIdx.x) % per;
-  const int t = p.tiles - 1 - static_cast<int>(blockIdx.x) / per;
-  const int q0 = t * (p.pair_rows ? 2 * kRows : kRows);
-  // The queries, and where both tiles have the same rows the first keys, do not wait for the sequences' boundaries.
+  // The first queries, and where both tiles have the same rows the first keys, do not wait for the sequences' boundaries.
   const bool early = !p.pair_rows;
-  const int kv = (p.pair_rows ? item : 2 * item) / (p.Hq / p.Hkv);
-  if (warp == kFwdLoadWarp && lane == 0) {
+  if (warp == kFwdLoadWarp && lane == 0 && early) {
+    int q0, h;
+    fwd_place(p, blockIdx.x, q0, h);
     mbar_arrive_expect_tx(&bk.q_full, 2 * C::kBytes);
-    for (int u = 0; u < 2; ++u)
-      load_tile<DP>(q_smem + u * C::kBytes, &tmQ, &bk.q_full, p.pair_rows ? item : 2 * item + u,
-                    q0 + (p.pair_rows ? kRows * u : 0));
-    if (early) {
-      for (int s = 0; s < 2; ++s) {
-        mbar_arrive_expect_tx(&bk.full[s], C::kBytes);
-        load_tile<DP>(ring + s * C::kBytes, s ? &tmV : &tmK, &bk.full[s], kv, q0);
-      }
+    for (int u = 0; u < 2; ++u) load_tile<DP>(q_smem + u * C::kBytes, &tmQ, &bk.q_full, h + u, q0);
+    for (int s = 0; s < 2; ++s) {
+      mbar_arrive_expect_tx(&bk.full[s], C::kBytes);
+      load_tile<DP>(ring + s * C::kBytes, s ? &tmV : &tmK, &bk.full[s], h / (p.Hq / p.Hkv), q0);
     }
   }
-  row_map<2 * kRows>(p, q0, &bk.map);
+  // Item `item` as number `it` of this CTA, by the item warp; its queries are sent for to the L2.
+  int mine = INT_MAX, first_row = 0, last_row = 0;
+  auto place = [&](int item, int it) {
+    FwdItem& m = bk.item[it & 1];
+    int q0, h;
+    fwd_place(p, item, q0, h);
+    for (int r = it > 0 ? lane : 2 * kRows; r < 2 * kRows; r += 32) {
+      const int row = q0 + (p.pair_rows ? r : r & (kRows - 1)), head = h + (p.pair_rows ? 0 : r / kRows);
+      if (row < p.T) {
+        const __nv_bfloat16* q = p.d1.p + row * p.d1.token + head * p.d1.head;
+        prefetch_l2(q);
+        prefetch_l2(q + p.D - 1);
+      }
+    }
+    find_map<2 * kRows>(p, q0, mine, first_row, last_row, &m.map);
+    if (lane == 0) {
+      // key tile i: rows [top - 128 (i + 1), top - 128 i); query tile u meets tiles [from[u], to[u])
+      const int top = q0 + (p.pair_rows ? 2 * kRows : kRows);
+      for (int u = 0; u < 2; ++u) {
+        const int base = q0 + (p.pair_rows ? kRows * u : 0), a = max(base, first_row), b = min(base + kRows, last_row);
+        m.base[u] = base;
+        m.head[u] = h + (p.pair_rows ? 0 : u);
+        m.from[u] = p.pair_rows ? 1 - u : 0;
+        m.to[u] = m.from[u] + (a < b ? (base + kRows - start_of(&m.map, q0, a) + kRows - 1) / kRows : 0);
+      }
+      const bool on0 = m.to[0] > m.from[0], on1 = m.to[1] > m.from[1];
+      m.ib = on1 ? m.from[1] : m.from[0];
+      m.n = (on0 || on1) ? max(m.to[0], m.to[1]) - m.ib : 0;
+      m.loaded = m.n > 0 ? 2 * m.n : (early && it == 0 ? 2 : 0);
+      m.q0 = q0;
+      m.top = top;
+      m.kv = h / (p.Hq / p.Hkv);
+      m.bad_lo = INT_MAX;
+      m.bad_hi = -1;
+      m.item = item;
+    }
+    __syncwarp();
+  };
+  if (warp == kFwdItemWarp) {
+    if (lane <= p.B) mine = p.cu[lane];     // (the first boundaries stay with it)
+    const int begin = p.B < 32 ? __shfl_sync(kFull, mine, 0) : p.cu[0], end = p.B < 32 ? __shfl_sync(kFull, mine, p.B) : p.cu[p.B];
+    first_row = max(begin, 0);
+    last_row = min(end, p.T);
+    place(blockIdx.x, 0);
+  }
+  __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = uniform(bk.tmem);
   volatile int* abort = &bk.abort_flag;
   const unsigned long long lim = p.wait_ns;
-
-  // key tile i: rows [top - 128 (i + 1), top - 128 i); query tile u meets tiles [from[u], to[u])
-  const int top = q0 + (p.pair_rows ? 2 * kRows : kRows);
-  int from[2], to[2], base[2], head[2];
-  #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    base[u] = q0 + (p.pair_rows ? kRows * u : 0);
-    head[u] = p.pair_rows ? item : 2 * item + u;
-    const int a = max(base[u], bk.map.first), b = min(base[u] + kRows, bk.map.last);
-    from[u] = p.pair_rows ? 1 - u : 0;
-    to[u] = a < b ? from[u] + (base[u] + kRows - start_of(&bk.map, q0, a) + kRows - 1) / kRows : from[u];
-  }
-  const bool on0 = to[0] > from[0], on1 = to[1] > from[1];
-  const int ib = on1 ? from[1] : from[0];
-  const int n = (on0 || on1) ? max(to[0], to[1]) - ib : 0;      // key tiles of this CTA
+  // The next item for a role; false: no more (or a wait has given up).
+  auto next_item = [&](int it) {
+    mbar_wait(&bk.item_full[it & 1], (it >> 1) & 1, abort, lim);
+    return *const_cast<volatile int*>(&bk.item[it & 1].item) >= 0 && *abort == 0;
+  };
 
   if (warp >= kFwdLoadWarp) {
    fewer_registers<kFwdOtherRegs>();
-   if (warp == kFwdLoadWarp) {
+   if (warp == kFwdItemWarp) {
+    // ------------------------------------------------ the items
+    const int items = p.tiles * (p.pair_rows ? p.Hq : p.Hq / 2), grid = gridDim.x;
+    int next = blockIdx.x;
+    for (int it = 0;; ++it) {
+      if (it >= 2) warp_wait(&bk.item_empty[it & 1], ((it >> 1) & 1) ^ 1u, abort, lim);
+      if (next >= items || uniform(*abort) != 0) {
+        if (lane == 0) {
+          bk.item[it & 1].item = -1;
+          mbar_arrive(&bk.item_full[it & 1]);
+        }
+        break;
+      }
+      if (it > 0) place(next, it);          // (the first one has been placed)
+      if (lane == 0) mbar_arrive(&bk.item_full[it & 1]);
+      // The next one when this one's last loads have been issued.  (No earlier: a CTA that holds its next item from the
+      // start of a long one keeps it from those that end before; 186 us against 156 at sequences of 1 to 3907 rows.)
+      warp_wait(&bk.ending, it & 1, abort, lim);
+      next = uniform(lane == 0 ? take_item(p.status, items, grid) : 0);
+    }
+    while (next < items) next = uniform(lane == 0 ? take_item(p.status, items, grid) : 0);      // (given up)
+    check_boundaries(p);
+   } else if (warp == kFwdLoadWarp) {
     if (lane == 0) {
       Issued got;
-      got.note(8, 0);
+      int turn = 0, filled = 0;
+      bool go = true;
       if (early) {
+        got.note(8, 0);
         got.note(0, 0);
         got.note(1, 0);
       }
-      for (int s = early ? 2 : 0; s < 2 * n; ++s) {             // key, value, key, ...
-        const int slot = s % ST;
-        const uint32_t ph = (s / ST) & 1;
-        if (s >= ST && !mbar_wait(&bk.empty[slot], ph ^ 1u, abort, lim)) break;
-        mbar_arrive_expect_tx(&bk.full[slot], C::kBytes);
-        load_tile<DP>(ring + slot * C::kBytes, (s & 1) ? &tmV : &tmK, &bk.full[slot], kv,
-                      top - kRows * (ib + (s >> 1) + 1));
-        got.note(slot, ph);
+      for (int it = 0; go && next_item(it); ++it) {
+        const FwdItem& m = bk.item[it & 1];
+        const int loaded = m.loaded, ib = m.ib, top = m.top, kv = m.kv;
+        if (loaded > 0) {
+          const bool here = early && it == 0;
+          if (!here) {
+            if (filled > 0 && !mbar_wait(&bk.q_empty, (filled - 1) & 1, abort, lim)) break;
+            mbar_arrive_expect_tx(&bk.q_full, 2 * C::kBytes);
+            for (int u = 0; u < 2; ++u)
+              load_tile<DP>(q_smem + u * C::kBytes, &tmQ, &bk.q_full, m.head[u], m.base[u]);
+            got.note(8, filled & 1);
+          }
+          ++filled;
+          for (int s = here ? 2 : 0; s < loaded; ++s) {           // key, value, key, ...
+            const int slot = (turn + s) % ST;
+            const uint32_t ph = ((turn + s) / ST) & 1;
+            if (turn + s >= ST && !mbar_wait(&bk.empty[slot], ph ^ 1u, abort, lim)) {
+              go = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&bk.full[slot], C::kBytes);
+            load_tile<DP>(ring + slot * C::kBytes, (s & 1) ? &tmV : &tmK, &bk.full[slot], kv,
+                          top - kRows * (ib + (s >> 1) + 1));
+            got.note(slot, ph);
+          }
+          turn += loaded;
+        }
+        mbar_arrive(&bk.item_empty[it & 1]);
+        mbar_arrive(&bk.ending);
       }
       got.drain(bk.full);                    // (they have landed by the end, unless another warp gave up)
     }
-   } else if (n > 0 && (warp == kFwdMmaWarp || (L > 2 && warp == kFwdMmaWarp + 1))) {
+   } else if (warp == kFwdMmaWarp || (L > 2 && warp == kFwdMmaWarp + 1)) {
     const uint32_t leader = elect_one() ? 1u : 0u;
     const uint64_t q_desc = scores_desc(q_smem), k_desc = scores_desc(ring), v_desc = sums_desc(ring);
-    const int f0 = uniform(from[0]), f1 = uniform(from[1]), e0 = uniform(to[0]), e1 = uniform(to[1]);
-    const int first = uniform(ib), last = uniform(ib + n) - 1;
-    const int turns = 2 * (last - first + 1);
-    auto full = [&](int s) { warp_wait(&bk.full[s % ST], (s / ST) & 1, abort, lim); };
-    auto release = [&](int s) { if (s + ST < turns) mma_commit_warp(leader, &bk.empty[s % ST]); };
-    // scores number k: of tile k % 2 with key tile k / 2, in buffer k % L
-    auto scores = [&](int u, int i, uint32_t buffer) {
-      if (i > last) return;
-      const int s = 2 * (i - first), f = u ? f1 : f0;
-      if (u == 0) {
-        full(s);
-        tc_fence_after_sync();
-      }
-      if (i >= f && i < (u ? e1 : e0)) {
-        mma_scores<DP>(leader, tmem + buffer, q_desc + u * (C::kBytes >> 4), k_desc + (s % ST) * (C::kBytes >> 4));
-        mma_commit_warp(leader, &bk.s_full[u][(i - f) & 1]);
-      }
-      if (u == 1) release(s);
-    };
-    // the sums of tile u over value tile i
-    auto sums = [&](int u, int i, uint32_t buffer) {
-      const int s = 2 * (i - first) + 1, f = u ? f1 : f0, e = u ? e1 : e0;
-      if (u == 0) full(s);
-      if (i >= f && i < e) {
-        // (the first half of the keys while the second is still exponentiated)
-        #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          warp_wait(&bk.p_full[u][half], (i - f) & 1, abort, lim);
+    // this warp's counts over all items: tiles in the ring, fillings of the queries, key tiles met by each tile of
+    // rows, items with rows of each, and the buffer of scores and its round
+    int turn = 0, filled = 0, met0 = 0, met1 = 0, outs0 = 0, outs1 = 0;
+    uint32_t b = 0, round = 0;
+    for (int it = 0; uniform(next_item(it) ? 1 : 0) != 0; ++it) {
+      const FwdItem& m = bk.item[it & 1];
+      const int f0 = uniform(m.from[0]), f1 = uniform(m.from[1]), e0 = uniform(m.to[0]), e1 = uniform(m.to[1]);
+      const int first = uniform(m.ib), n = uniform(m.n), loaded = uniform(m.loaded), last = first + n - 1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bk.item_empty[it & 1]);
+      auto full = [&](int s) { warp_wait(&bk.full[s % ST], (s / ST) & 1, abort, lim); };
+      auto release = [&](int s) { mma_commit_warp(leader, &bk.empty[s % ST]); };
+      auto scores = [&](int u, int i, uint32_t buffer) {
+        if (i > last) return;
+        const int s = turn + 2 * (i - first), f = u ? f1 : f0, x = (u ? met1 : met0) + i - f;
+        if (u == 0) {
+          full(s);
           tc_fence_after_sync();
-          mma_sums<DP, 8>(leader, tmem + 128 * L + DP * u, tmem + buffer, v_desc + (s % ST) * (C::kBytes >> 4),
-                          i > f || half, 4 * half, 4 * half + 4);
         }
-        if (i + 1 == e) mma_commit_warp(leader, &bk.o_full[u]);
-      }
-      if (u == 1) release(s);
-    };
-    if constexpr (L == 2) {
-      warp_wait(&bk.q_full, 0, abort, lim);
-      scores(0, first, 0);
-      scores(1, first, 128);
-      for (int i = first; i <= last; ++i) {
-        sums(0, i, 0);
-        scores(0, i + 1, 0);
-        sums(1, i, 128);
-        scores(1, i + 1, 128);
-      }
-    } else if (warp == kFwdMmaWarp) {
-      warp_wait(&bk.q_full, 0, abort, lim);
-      uint32_t b = 0, turn = 1;
-      for (int i = first; i <= last; ++i) {
-        #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (2 * (i - first) + u >= L) warp_wait(&bk.free[b], turn & 1, abort, lim);
-          tc_fence_after_sync();
-          scores(u, i, 128 * b);
-          if (++b == L) {
-            b = 0;
-            ++turn;
+        if (i >= f && i < (u ? e1 : e0)) {
+          mma_scores<DP>(leader, tmem + buffer, q_desc + u * (C::kBytes >> 4), k_desc + (s % ST) * (C::kBytes >> 4));
+          mma_commit_warp(leader, &bk.s_full[u][x & 1]);
+        }
+        if (u == 1) {
+          release(s);
+          if (i == last) mma_commit_warp(leader, &bk.q_empty);
+        }
+      };
+      // the sums of tile u over value tile i
+      auto sums = [&](int u, int i, uint32_t buffer) {
+        const int s = turn + 2 * (i - first) + 1, f = u ? f1 : f0, e = u ? e1 : e0, x = (u ? met1 : met0) + i - f;
+        if (u == 0) full(s);
+        if (i >= f && i < e) {
+          const int outs = u ? outs1 : outs0;
+          if (i == f && outs > 0) warp_wait(&bk.o_empty[u], (outs - 1) & 1, abort, lim);
+          // (the first half of the keys while the second is still exponentiated)
+          #pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            warp_wait(&bk.p_full[u][x & 1][half], (x >> 1) & 1, abort, lim);
+            tc_fence_after_sync();
+            mma_sums<DP, 8>(leader, tmem + 128 * L + DP * u, tmem + buffer, v_desc + (s % ST) * (C::kBytes >> 4),
+                            i > f || half, 4 * half, 4 * half + 4);
+          }
+          if (i + 1 == e) mma_commit_warp(leader, &bk.o_full[u]);
+        }
+        if (u == 1) release(s);
+      };
+      if (n == 0) {
+        if (loaded > 0 && warp == kFwdMmaWarp) {                  // (loaded before it was known that nothing asks for it)
+          warp_wait(&bk.q_full, filled & 1, abort, lim);
+          mma_commit_warp(leader, &bk.q_empty);
+          for (int s = turn; s < turn + loaded; ++s) {
+            full(s);
+            release(s);
+          }
+        }
+      } else if (L == 2) {
+        warp_wait(&bk.q_full, filled & 1, abort, lim);
+        scores(0, first, 0);
+        scores(1, first, 128);
+        for (int i = first; i <= last; ++i) {
+          sums(0, i, 0);
+          scores(0, i + 1, 0);
+          sums(1, i, 128);
+          scores(1, i + 1, 128);
+        }
+      } else if (warp == kFwdMmaWarp) {
+        warp_wait(&bk.q_full, filled & 1, abort, lim);
+        for (int i = first; i <= last; ++i) {
+          #pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if (round > 0) warp_wait(&bk.free[b], (round - 1) & 1, abort, lim);
+            tc_fence_after_sync();
+            scores(u, i, 128 * b);
+            if (++b == L) {
+              b = 0;
+              ++round;
+            }
+          }
+        }
+      } else {
+        for (int i = first; i <= last; ++i) {
+          #pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            sums(u, i, 128 * b);
+            mma_commit_warp(leader, &bk.free[b]);
+            b = b + 1 == L ? 0 : b + 1;
           }
         }
       }
-    } else {
-      uint32_t b = 0;
-      for (int i = first; i <= last; ++i) {
-        #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          sums(u, i, 128 * b);
-          mma_commit_warp(leader, &bk.free[b]);
-          b = b + 1 == L ? 0 : b + 1;
-        }
-      }
+      turn += loaded;
+      filled += loaded > 0;
+      met0 += e0 - f0;
+      met1 += e1 - f1;
+      outs0 += e0 > f0;
+      outs1 += e1 > f1;
     }
     mma_commit_warp(leader, &bk.drain);      // (TMEM is given back after them, whoever gave up)
     mbar_wait_drain(&bk.drain, 0);
    }
   } else {
    more_registers<kFwdRegs>();
-   if (n > 0) {
-    // ------------------------------------------------ a thread a row
-    const int u = warp >> 2;
-    const int f = u ? from[1] : from[0], e = u ? to[1] : to[0], r0 = u ? base[1] : base[0], h = u ? head[1] : head[0];
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t to_ = tmem + 128 * L + DP * u + lanes;
-    int buffer = (2 * (f - ib) + u) % L;
-    const int row = r0 + (warp & 3) * 32 + lane;
-    const bool valid = row >= bk.map.first && row < bk.map.last;
-    const int key_lo = valid ? start_of(&bk.map, q0, row) : INT_MIN / 2, key_hi = valid ? row : INT_MAX / 2;
-    // keys from here on are seen by every row of the tile (up to the diagonal)
-    const int all_from = e > f ? start_of(&bk.map, q0, min(r0 + kRows, bk.map.last) - 1) : 0;
-    // probabilities are relative to a reference that follows the maximum once it is 2^8 above
-    const float slack = 8.f / p.scale2;
-    float ref = -INFINITY, sum = 0.f;
-    uint32_t s[4][32];
-    for (int i = f; i < e; ++i) {
-      warp_wait(&bk.s_full[u][(i - f) & 1], ((i - f) >> 1) & 1, abort, lim);
+   // ------------------------------------------------ a thread a row
+   const int u = warp >> 2;
+   const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+   const uint32_t to_ = tmem + 128 * L + DP * u + lanes;
+   int turn = 0, met = 0, outs = 0, scored = 0;         // as in the warp that issues; outs: items with rows of this tile
+   for (int it = 0; uniform(next_item(it) ? 1 : 0) != 0; ++it) {
+    FwdItem& m = bk.item[it & 1];
+    const int f = m.from[u], e = m.to[u], ib = m.ib, n = m.n, q0 = m.q0, top = m.top;
+    if (e > f) {
+     const int r0 = m.base[u], h = m.head[u], kv = m.kv;
+     const int row = r0 + (warp & 3) * 32 + lane;
+     const bool valid = row >= m.map.first && row < m.map.last;
+     const int key_lo = valid ? start_of(&m.map, q0, row) : INT_MIN / 2, key_hi = valid ? row : INT_MAX / 2;
+     // keys from here on are seen by every row of the tile (up to the diagonal)
+     const int all_from = start_of(&m.map, q0, min(r0 + kRows, m.map.last) - 1);
+     // probabilities are relative to a reference that follows the maximum once it is 2^8 above
+     const float slack = 8.f / p.scale2;
+     float ref = -INFINITY, sum = 0.f;
+     uint32_t s[4][32];
+     int buffer = (scored + 2 * (f - ib) + u) % L;
+     for (int i = f; i < e; ++i) {
+      const int x = met + i - f;
+      warp_wait(&bk.s_full[u][x & 1], (x >> 1) & 1, abort, lim);
       tc_fence_after_sync();
       const uint32_t ts = tmem + 128 * buffer + lanes;
       if (L > 2) buffer = buffer > 0 ? buffer - 1 : L - 1;      // (two on)
@@ -576,11 +752,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           for (int j = 0; j < 32; ++j)
             if (!(on >> j & 1u)) s[c][j] = 0xff800000u;
         }
-        const int turn = 2 * (i - ib) + 1;
-        warp_wait(&bk.full[turn % ST], (turn / ST) & 1, abort, lim);
-        clean_tile<DP>(ring + (turn % ST) * C::kBytes, threadIdx.x & 127, 128, [&] {
-          atomicMin(&bk.bad_lo, k0);
-          atomicMax(&bk.bad_hi, k0 + kRows - 1);
+        const int at = turn + 2 * (i - ib) + 1;
+        warp_wait(&bk.full[at % ST], (at / ST) & 1, abort, lim);
+        clean_tile<DP>(ring + (at % ST) * C::kBytes, threadIdx.x & 127, 128, [&] {
+          atomicMin(&m.bad_lo, k0);
+          atomicMax(&m.bad_hi, k0 + kRows - 1);
           __threadfence_block();                 // (the other tile of rows may find the zeros: it shall know)
         });
       }
@@ -607,23 +783,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       float mx[8];
       #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const uint32_t* x = s[c >> 1] + 16 * (c & 1);
-        mx[c] = max3(as_f(x[0]), as_f(x[1]), as_f(x[2]));
+        const uint32_t* y = s[c >> 1] + 16 * (c & 1);
+        mx[c] = max3(as_f(y[0]), as_f(y[1]), as_f(y[2]));
         #pragma unroll
-        for (int j = 3; j < 15; j += 2) mx[c] = max3(mx[c], as_f(x[j]), as_f(x[j + 1]));
+        for (int j = 3; j < 15; j += 2) mx[c] = max3(mx[c], as_f(y[j]), as_f(y[j + 1]));
       }
       #pragma unroll
       for (int c = 0; c < 8; c += 2) mx[c] = max3(mx[c], as_f(s[c >> 1][15]), as_f(s[c >> 1][31]));
-      const float m = max3(max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[4]), max3(mx[5], mx[6], mx[7]), ref);
-      const bool grow = m > ref + slack;
+      const float top_ = max3(max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[4]), max3(mx[5], mx[6], mx[7]), ref);
+      const bool grow = top_ > ref + slack;
       if (__any_sync(kFull, grow)) {
-        const float a = grow ? ex2((ref - m) * p.scale2) : 1.f;
-        if (grow) ref = m;
+        const float a = grow ? ex2((ref - top_) * p.scale2) : 1.f;
+        if (grow) ref = top_;
         sum *= a;
         if (i > f) {
           // (with two buffers this tile's scores come after the sums so far)
           if (L > 2) {
-            const int k = 2 * (i - ib) + u - 2;          // (its sums have to be done)
+            const int k = scored + 2 * (i - ib) + u - 2;          // (its sums have to be done)
             warp_wait(&bk.free[k % L], (k / L) & 1, abort, lim);
             tc_fence_after_sync();
           }
@@ -641,47 +817,58 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       F32x2 total = exps(0);
       tmem_st_x32(ts, w);
       tmem_st_wait();
-      warp_arrive(&bk.p_full[u][0], lane);
+      warp_arrive(&bk.p_full[u][x & 1][0], lane);
       total = add2(total, exps(1));
       tmem_st_x32(ts + 32, w);
       tmem_st_wait();
-      warp_arrive(&bk.p_full[u][1], lane);
+      warp_arrive(&bk.p_full[u][x & 1][1], lane);
       const float2 t = split_f32x2(total);
       sum += t.x + t.y;
-    }
-    if (e > f) {
-      warp_wait(&bk.o_full[u], 0, abort, lim);
-      tc_fence_after_sync();
-      const float inv = 1.f / sum;
-      const int bad_lo = *const_cast<volatile int*>(&bk.bad_lo), bad_hi = *const_cast<volatile int*>(&bk.bad_hi);
-      const uint32_t rows = __ballot_sync(kFull, valid);
-      uint8_t* staging = q_smem + u * C::kBytes + (warp & 3) * (32 * DP * 2);       // (this tile's queries have been read)
+     }
+     warp_wait(&bk.o_full[u], outs & 1, abort, lim);
+     tc_fence_after_sync();
+     #pragma unroll
+     for (int c = 0; c < DP / 32; ++c) tmem_ld_x32(to_ + 32 * c, s[c]);
+     #pragma unroll
+     for (int c = 0; c < DP / 32; ++c) tmem_ld_wait(s[c]);
+     warp_arrive(&bk.o_empty[u], lane);
+     const float inv = 1.f / sum;
+     if (valid) p.lse[static_cast<long long>(h) * p.T + row] = (ref == -INFINITY ? 0.f : ref * p.scale) + logf(sum);
+     const int bad_lo = *const_cast<volatile int*>(&m.bad_lo), bad_hi = *const_cast<volatile int*>(&m.bad_hi);
+     const uint32_t rows = __ballot_sync(kFull, valid);
+     uint8_t* staging = out_smem + warp * 4096;
+     #pragma unroll
+     for (int col = 0; col < DP; col += 64) {
       #pragma unroll
-      for (int c = 0; c < DP / 32; ++c) tmem_ld_x32(to_ + 32 * c, s[c]);
-      #pragma unroll
-      for (int c = 0; c < DP / 32; ++c) {
-        tmem_ld_wait(s[c]);
+      for (int c = 0; c < 2; ++c) {
         float v[32];
         #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = as_f(s[c][j]) * inv;
-        put_cols<DP>(staging, lane, 32 * c, v);
+        for (int j = 0; j < 32; ++j) v[j] = as_f(s[col / 32 + c][j]) * inv;
+        put_cols(staging, lane, 32 * c, v);
       }
       if (valid) {
         // what clean_tile took out, for the rows that see it
         for (int j = max(key_lo, bad_lo); j <= min(key_hi, bad_hi); ++j) {
-          const __nv_bfloat16* src = p.d0.p + j * p.d0.token + kv * p.d0.head;
-          for (int x = 0; x < p.D; ++x) {
-            const float y = __bfloat162float(src[x]);
-            __nv_bfloat16* at = staged<DP>(staging, lane, x);
-            if (!isfinite(y)) *at = __float2bfloat16(__bfloat162float(*at) + y);
+          const __nv_bfloat16* src = p.d0.p + j * p.d0.token + kv * p.d0.head + col;
+          for (int c = 0; c < 64 && col + c < p.D; ++c) {
+            const float y = __bfloat162float(src[c]);
+            __nv_bfloat16* to = staged(staging, lane, c);
+            if (!isfinite(y)) *to = __float2bfloat16(__bfloat162float(*to) + y);
           }
         }
       }
       __syncwarp();
-      store_rows<DP>(staging, p.o.p + (row - lane) * p.o.token + h * p.o.head, p.o.token, rows, p.D);
-      if (valid) p.lse[static_cast<long long>(h) * p.T + row] = (ref == -INFINITY ? 0.f : ref * p.scale) + logf(sum);
+      store_rows(staging, p.o.p + (row - lane) * p.o.token + h * p.o.head + col, p.o.token, rows, p.D - col);
+      __syncwarp();
+     }
+     ++outs;
     }
-  }
+    turn += m.loaded;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bk.item_empty[it & 1]);
+    met += e - f;
+    scored += 2 * n;
+   }
   }
   __syncwarp();
   tc_fence_before_sync();
@@ -718,7 +905,7 @@ __device__ __forceinline__ uint4 split_row(float v) {
 constexpr int kKStages = 3;                // key tiles in flight: one is held from its scores to its dq
 struct DqBook {
   uint64_t q_full, k_full[kKStages], v_full[2];
-  uint64_t k_empty[kKStages], v_empty[2], s_full, s_empty, dp_full[2], dp_empty[2], ds_full, done;
+  uint64_t k_empty[kKStages], v_empty[2], s_full, s_empty, dp_full[2], dp_empty[2], ds_full[2], done;
   uint32_t tmem;
   int abort_flag;
   RowMap map;
@@ -755,10 +942,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       mbar_init(&bk.v_empty[s], 1);
       mbar_init(&bk.dp_full[s], 1);
       mbar_init(&bk.dp_empty[s], 1);
+      mbar_init(&bk.ds_full[s], kBwdArith / 32);
     }
     mbar_init(&bk.s_full, 1);
     mbar_init(&bk.s_empty, kBwdArith / 32);
-    mbar_init(&bk.ds_full, kBwdArith / 32);
     mbar_init(&bk.done, 2);
     bk.abort_flag = 0;
     fence_mbarrier_init();
@@ -842,7 +1029,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     } else {
       const uint64_t kt_desc = sums_desc(k_smem);
       for (int j = 0; j < tiles; ++j) {
-        warp_wait(&bk.ds_full, j & 1, abort, lim);
+        warp_wait(&bk.ds_full[j & 1], (j >> 1) & 1, abort, lim);
         tc_fence_after_sync();
         mma_sums<DP, 2>(leader, tmem, tmem + 256 + 128 * (j & 1), kt_desc + (j % kKStages) * kNext, j > 0);
         if (j + 2 < tiles) mma_commit_warp(leader, &bk.dp_empty[j & 1]);
@@ -951,7 +1138,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
       tmem_st_x16(tdp, w);
       tmem_st_wait();
-      warp_arrive(&bk.ds_full, lane);
+      warp_arrive(&bk.ds_full[j & 1], lane);
     };
     for (int j = 0; j < n; ++j) {
       if (j == 0 || top - kRows * (j + 1) < all_from)
@@ -1298,7 +1485,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // may be less: each kernel looks).
 constexpr int smem_of(int used) { return used + 1024 < kMaxSmem ? used + 1024 : kMaxSmem; }
 template <int DP>
-constexpr int fwd_smem() { return (2 + Tile<DP>::kStages) * Tile<DP>::kBytes + static_cast<int>(sizeof(FwdBook)); }
+constexpr int fwd_smem() {
+  return (2 + Tile<DP>::kStages) * Tile<DP>::kBytes + kFwdStaging + static_cast<int>(sizeof(FwdBook));
+}
 template <int DP>
 constexpr int dq_smem() { return (4 + kKStages) * Tile<DP>::kBytes + static_cast<int>(sizeof(DqBook)); }
 template <int DP>
@@ -1402,8 +1591,8 @@ template <int DP>
 cudaError_t forward(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const AttnParams& p,
                     cudaStream_t st) {
   static std::atomic<bool> attr_set[kMaxDevices];
-  const int grid = p.tiles * (p.pair_rows ? p.Hq : p.Hq / 2);
-  return launch_big(attention_fwd_kernel<DP>, attr_set, grid, kFwdThreads, smem_of(fwd_smem<DP>()), st, 1, tq, tk, tv, p);
+  const int items = p.tiles * (p.pair_rows ? p.Hq : p.Hq / 2), sms = num_sms();
+  return launch_big(attention_fwd_kernel<DP>, attr_set, items < sms ? items : sms, kFwdThreads, smem_of(fwd_smem<DP>()), st, 1, tq, tk, tv, p);
 }
 template <int DP>
 cudaError_t backward(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& td,
@@ -1450,6 +1639,7 @@ moe_status moe_attention_forward(const moe_attention_config* cfg, const moe_head
   if (p.pair_rows) p.tiles = (T + 2 * kRows - 1) / (2 * kRows);
   p.o = heads_of(out, T, Hq, D);
   p.d0 = heads_of(v, T, Hkv, D);
+  p.d1 = heads_of(q, T, Hq, D);
   p.lse = lse;
   CUtensorMap tq, tk, tv;
   if (!make_map(&tq, q, T, Hq, D) || !make_map(&tk, k, T, Hkv, D) || !make_map(&tv, v, T, Hkv, D))

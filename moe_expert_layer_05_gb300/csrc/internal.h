@@ -19,6 +19,8 @@ constexpr int kFewDoneWord = 41;
 // The same for the balance loss and for the gradient norm.
 constexpr int kBalanceDoneWord = 42;
 constexpr int kNormDoneWord = 43;
+// Count of the items of attention handed out (zero between launches).
+constexpr int kAttentionItemWord = 44;
 
 int num_sms();
 bool device_is_gb300();

@@ -1,0 +1,42 @@
+"""Attention of more tiles than SMs: CTAs that work through several of them, some without rows."""
+import pytest
+import torch
+
+from moe_expert_layer_05_gb300 import api
+from test_gpu_attention import DEV, _case, _check, _run, _ws
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(400, 400), (480, 160)])
+def test_many_heads_of_few_rows(lib, Hq, Hkv, D):
+    """Groups of odd sizes take 256 rows at a time: the second 128 have none, in every item of every CTA."""
+    c = _case([60, 1, 39], Hq, Hkv, D, seed=Hq + D)
+    _check(_run(*c), *c)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(96, 96), (128, 64)])
+def test_sequences_between_rows_of_none(lib, Hq, Hkv):
+    """Tiles without a row before the first sequence and behind the last one, between those with rows."""
+    c = _case([200, 1, 0, 70], Hq, Hkv, 64, seed=Hq, first=300, tail=400)
+    _check(_run(*c), *c)
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D", [(16384, 8, 1, 64), (8192, 6, 2, 64), (8192, 8, 2, 128), (4100, 15, 5, 128)])
+def test_many_launches_end_and_agree(lib, T, Hq, Hkv, D):
+    """Launch after launch on one workspace: every wait ends, the bits are the same."""
+    cu, T, q, k, v, do = _case([T - 3000, 1, 2500, 499], Hq, Hkv, D, seed=T)
+    qd, kd, vd, dod = (t.to(DEV) for t in (q, k, v, do))
+    cud, ws = torch.from_numpy(cu).to(DEV), _ws(T, Hq, Hkv, D)
+    outs = [torch.zeros_like(qd) for _ in range(2)]
+    lse = torch.zeros(Hq, T, device=DEV)
+    grads = [[torch.zeros_like(t) for t in (qd, kd, vd)] for _ in range(2)]
+    for i in range(60):
+        api.moe_attention_forward(qd, kd, vd, cud, outs[i > 0], lse, ws)
+        if i % 10 == 0:
+            api.moe_attention_backward(qd, kd, vd, cud, outs[i > 0], lse, dod, *grads[i > 0], ws)
+    assert api.moe_read_device_status(ws) == 0
+    assert torch.equal(outs[0], outs[1])
+    for a, b in zip(*grads):
+        assert torch.equal(a, b)
