@@ -55,8 +55,7 @@ struct AttnParams {
   int pair_rows;           // forward: the two tiles of a CTA are rows of one head (else two heads of one group)
   int tiles;               // tiles along the rows
   int split;               // dk, dv: CTAs that share a group's heads
-  Heads o, d0, d1;         // forward: out, v, q; gradients: out, dq or dk, dv
-  Heads dout;
+  Heads q, o, d0, d1;      // forward: q, out, v; gradients: dq or dk, dv
   float* lse;              // [Hq, T]
   uint4* stats;            // [2][Hq, pitch]: -lse / scale, -delta, each as eight bf16 (split_row)
   long long pitch;
@@ -207,6 +206,13 @@ __device__ __forceinline__ int take_item(int* status, int items, int grid) {
 __device__ __forceinline__ uint32_t seen(int lo, int hi) {
   const uint32_t from = lo <= 0 ? ~0u : lo > 31 ? 0u : ~0u << lo, to = hi >= 31 ? ~0u : hi < 0 ? 0u : ~(~1u << hi);
   return from & to;
+}
+
+// 32 values of a row: zero where it does not see.
+__device__ __forceinline__ void blank(uint32_t (&v)[32], uint32_t on) {
+  #pragma unroll
+  for (int x = 0; x < 32; ++x)
+    if (!(on >> x & 1u)) v[x] = 0u;
 }
 
 // ---------------------------------------------------------------- tiles
@@ -493,7 +499,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     for (int r = it > 0 ? lane : 2 * kRows; r < 2 * kRows; r += 32) {
       const int row = q0 + (p.pair_rows ? r : r & (kRows - 1)), head = h + (p.pair_rows ? 0 : r / kRows);
       if (row < p.T) {
-        const __nv_bfloat16* q = p.d1.p + row * p.d1.token + head * p.d1.head;
+        const __nv_bfloat16* q = p.q.p + row * p.q.token + head * p.q.head;
         prefetch_l2(q);
         prefetch_l2(q + p.D - 1);
       }
@@ -904,12 +910,12 @@ __device__ __forceinline__ uint4 split_row(float v) {
 // take delta = sum_j p dp there instead.  Either goes to stats, for dk.
 constexpr int kKStages = 3;                // key tiles in flight: one is held from its scores to its dq
 struct DqBook {
-  uint64_t q_full, k_full[kKStages], v_full[2];
+  uint64_t q_full, k_full[kKStages], v_full[2], o_full;      // (one after the other: Issued counts on it)
+  uint64_t o_read;
   uint64_t k_empty[kKStages], v_empty[2], s_full, s_empty, dp_full[2], dp_empty[2], ds_full[2], done;
   uint32_t tmem;
   int abort_flag;
   RowMap map;
-  float delta[kRows];
   float sums[kParts][kRows];               // parts of rows' sums
 };
 
@@ -917,7 +923,7 @@ template <int DP>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     attention_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDo,
-                        const AttnParams p) {
+                        const __grid_constant__ CUtensorMap tmO, const AttnParams p) {
   using C = Tile<DP>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* q_smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -933,6 +939,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (warp == kBwdLoadWarp && lane == 0) {          // (it uses them before the first barrier of all threads)
     mbar_init(&bk.q_full, 1);
+    mbar_init(&bk.o_full, 1);
+    mbar_init(&bk.o_read, kBwdArith / 32);
     for (int s = 0; s < kKStages; ++s) {
       mbar_init(&bk.k_full[s], 1);
       mbar_init(&bk.k_empty[s], 1);
@@ -953,6 +961,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     prefetch_tensormap(&tmK);
     prefetch_tensormap(&tmV);
     prefetch_tensormap(&tmDo);
+    prefetch_tensormap(&tmO);
   }
   if (warp == kBwdMmaWarp) {
     tmem_alloc(&bk.tmem, 512);
@@ -962,7 +971,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   pdl_wait();
   const int h = static_cast<int>(blockIdx.x) % p.Hq;
   const int q0 = (p.tiles - 1 - static_cast<int>(blockIdx.x) / p.Hq) * kRows;
-  // The queries and the first keys do not wait for the sequences' boundaries.
+  // The queries and the first keys do not wait for the sequences' boundaries.  out takes the place of the third keys
+  // until delta has been worked out.
+  uint8_t* o_smem = k_smem + 2 * C::kBytes;
   const int kv = h / (p.Hq / p.Hkv), top = q0 + kRows;
   if (warp == kBwdLoadWarp && lane == 0) {
     mbar_arrive_expect_tx(&bk.q_full, 2 * C::kBytes);
@@ -972,6 +983,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     load_tile<DP>(k_smem, &tmK, &bk.k_full[0], kv, q0);
     mbar_arrive_expect_tx(&bk.v_full[0], C::kBytes);
     load_tile<DP>(v_smem, &tmV, &bk.v_full[0], kv, q0);
+    mbar_arrive_expect_tx(&bk.o_full, C::kBytes);
+    load_tile<DP>(o_smem, &tmO, &bk.o_full, h, q0);
   }
   row_map<kRows>(p, q0, &bk.map);
   tc_fence_after_sync();
@@ -989,9 +1002,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       got.note(0, 0);
       got.note(1, 0);
       got.note(1 + kKStages, 0);
+      got.note(3 + kKStages, 0);
       for (int j = 1; j < n; ++j) {
         const int s = j % kKStages, s2 = j & 1, row = top - kRows * (j + 1);
         const uint32_t ph = (j / kKStages) & 1, ph2 = (j >> 1) & 1;
+        if (j == 2 && !mbar_wait(&bk.o_read, 0, abort, lim)) break;
         if (j >= kKStages && !mbar_wait(&bk.k_empty[s], ph ^ 1u, abort, lim)) break;
         mbar_arrive_expect_tx(&bk.k_full[s], C::kBytes);
         load_tile<DP>(k_smem + s * C::kBytes, &tmK, &bk.k_full[s], kv, row);
@@ -1048,34 +1063,27 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const bool valid = row >= bk.map.first && row < bk.map.last;
     const int key_lo = valid ? start_of(&bk.map, q0, row) : p.T, key_hi = valid ? row : -1;
     const int all_from = start_of(&bk.map, q0, b - 1);
-    // <do, o> of eight rows a warp, 16 lanes a row
+    // <do, o>: a quarter of the columns a thread
+    warp_wait(&bk.q_full, 0, abort, lim);
+    warp_wait(&bk.o_full, 0, abort, lim);
     {
-      float d[4];
-      uint4 x[4], y[4];
+      float d = 0.f;
       #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = q0 + 8 * warp + 2 * i + (lane >> 4), w = lane & 15;
-        const bool in = r >= bk.map.first && r < bk.map.last && 8 * w < p.D;
-        x[i] = y[i] = make_uint4(0, 0, 0, 0);
-        if (in) {
-          x[i] = *reinterpret_cast<const uint4*>(p.o.p + r * p.o.token + h * p.o.head + 8 * w);
-          y[i] = *reinterpret_cast<const uint4*>(p.dout.p + r * p.dout.token + h * p.dout.head + 8 * w);
-        }
+      for (int i = 0; i < DP / 32; ++i) {
+        const int w = DP / 32 * part + i, at = w / 8 * C::kChunk + lr * 128 + ((w ^ lr) & 7) * 16;
+        const uint4 x = *reinterpret_cast<const uint4*>(o_smem + at), y = *reinterpret_cast<const uint4*>(do_smem + at);
+        d += bf16_lo(x.x) * bf16_lo(y.x) + bf16_hi(x.x) * bf16_hi(y.x) + bf16_lo(x.y) * bf16_lo(y.y) +
+             bf16_hi(x.y) * bf16_hi(y.y) + bf16_lo(x.z) * bf16_lo(y.z) + bf16_hi(x.z) * bf16_hi(y.z) +
+             bf16_lo(x.w) * bf16_lo(y.w) + bf16_hi(x.w) * bf16_hi(y.w);
       }
-      #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        d[i] = bf16_lo(x[i].x) * bf16_lo(y[i].x) + bf16_hi(x[i].x) * bf16_hi(y[i].x) + bf16_lo(x[i].y) * bf16_lo(y[i].y) +
-               bf16_hi(x[i].y) * bf16_hi(y[i].y) + bf16_lo(x[i].z) * bf16_lo(y[i].z) + bf16_hi(x[i].z) * bf16_hi(y[i].z) +
-               bf16_lo(x[i].w) * bf16_lo(y[i].w) + bf16_hi(x[i].w) * bf16_hi(y[i].w);
-        #pragma unroll
-        for (int m = 8; m > 0; m >>= 1) d[i] += __shfl_xor_sync(kFull, d[i], m);
-        if ((lane & 15) == 0) bk.delta[8 * warp + 2 * i + (lane >> 4)] = -d[i];
-      }
+      bk.sums[part][lr] = d;
     }
+    warp_arrive(&bk.o_read, lane);
+    arith_sync();
+    float delta = -((bk.sums[0][lr] + bk.sums[1][lr]) + (bk.sums[2][lr] + bk.sums[3][lr]));
+    arith_sync();
     const float l = valid ? p.lse[static_cast<long long>(h) * p.T + row] : 0.f;
     const float lse = -l * kLog2e;
-    arith_sync();
-    float delta = bk.delta[lr];
     const F32x2 lse2 = make_f32x2(lse, lse), mul2_ = make_f32x2(p.scale2, p.scale2);
     auto step = [&](int j, auto masked_c) {
       constexpr bool masked = decltype(masked_c)::value;
@@ -1083,23 +1091,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       tc_fence_after_sync();
       const int k0 = top - kRows * (j + 1);
       const uint32_t on = masked ? seen(key_lo - k0 - 32 * part, key_hi - k0 - 32 * part) : kFull;
+      const bool whole = !masked || __all_sync(kFull, on == kFull);           // (of the warp's places)
       uint32_t s[32], d[32], w[16];
       tmem_ld_x32(tmem + lanes + 128 + 32 * part, s);
       tmem_ld_wait(s);
       warp_arrive(&bk.s_empty, lane);
       #pragma unroll
       for (int x = 0; x < 32; x += 2) {
-        float2 y = split_f32x2(fma2(make_f32x2(as_f(s[x]), as_f(s[x + 1])), mul2_, lse2));
-        y.x = ex2(y.x);
-        y.y = ex2(y.y);
-        if (masked) {
-          if (!(on >> x & 1u)) y.x = 0.f;
-          if (!(on >> x & 2u)) y.y = 0.f;
-        }
-        s[x] = __float_as_uint(y.x);
-        s[x + 1] = __float_as_uint(y.y);
+        const float2 y = split_f32x2(fma2(make_f32x2(as_f(s[x]), as_f(s[x + 1])), mul2_, lse2));
+        s[x] = __float_as_uint(ex2(y.x));
+        s[x + 1] = __float_as_uint(ex2(y.y));
       }
       if (masked) {
+        if (!whole) blank(s, on);
         warp_wait(&bk.k_full[j % kKStages], (j / kKStages) & 1, abort, lim);
         clean_tile<DP>(k_smem + (j % kKStages) * C::kBytes, threadIdx.x, kBwdArith, [] {});
       }
@@ -1108,37 +1112,33 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       tc_fence_after_sync();
       tmem_ld_x32(tdp, d);
       tmem_ld_wait(d);
-      if (masked && j == 0) {
+      if (!whole) blank(d, on);               // (so that ds is zero there whatever the tensors hold)
+      if (masked && j == 0 && all_from >= q0) {
+        // (some rows begin within this key tile)
         F32x2 sum = make_f32x2(0.f, 0.f);
         #pragma unroll
-        for (int x = 0; x < 32; x += 2) {
-          const float a0 = on >> x & 1u ? as_f(d[x]) : 0.f, a1 = on >> x & 2u ? as_f(d[x + 1]) : 0.f;
-          sum = fma2(make_f32x2(as_f(s[x]), as_f(s[x + 1])), make_f32x2(a0, a1), sum);
-        }
+        for (int x = 0; x < 32; x += 2)
+          sum = fma2(make_f32x2(as_f(s[x]), as_f(s[x + 1])), make_f32x2(as_f(d[x]), as_f(d[x + 1])), sum);
         const float2 t = split_f32x2(sum);
         bk.sums[part][lr] = t.x + t.y;
         arith_sync();
         if (key_lo >= k0) delta = -((bk.sums[0][lr] + bk.sums[1][lr]) + (bk.sums[2][lr] + bk.sums[3][lr]));
-        if (valid && part == 0) {
-          // (where do is not finite, nor is delta: p of this row shall not be either)
-          p.stats[h * p.pitch + row] = split_row(isfinite(delta) ? -l / p.scale : delta - delta);
-          p.stats[(p.Hq + h) * p.pitch + row] = split_row(delta);
-        }
       }
       const F32x2 delta2 = make_f32x2(delta, delta);
       #pragma unroll
       for (int x = 0; x < 32; x += 2) {
-        float2 y = split_f32x2(mul2(make_f32x2(as_f(s[x]), as_f(s[x + 1])),
+        const float2 y = split_f32x2(mul2(make_f32x2(as_f(s[x]), as_f(s[x + 1])),
                                     add2(make_f32x2(as_f(d[x]), as_f(d[x + 1])), delta2)));
-        if (masked) {
-          if (!(on >> x & 1u)) y.x = 0.f;
-          if (!(on >> x & 2u)) y.y = 0.f;
-        }
         w[x / 2] = pack_bf16x2(y.x, y.y);
       }
       tmem_st_x16(tdp, w);
       tmem_st_wait();
       warp_arrive(&bk.ds_full[j & 1], lane);
+      if (masked && j == 0 && valid && part == 0) {
+        // (where do is not finite, nor is delta: p of this row shall not be either)
+        p.stats[h * p.pitch + row] = split_row(isfinite(delta) ? -l / p.scale : delta - delta);
+        p.stats[(p.Hq + h) * p.pitch + row] = split_row(delta);
+      }
     };
     for (int j = 0; j < n; ++j) {
       if (j == 0 || top - kRows * (j + 1) < all_from)
@@ -1372,39 +1372,40 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       uint32_t s[32], d[32], w[16];
       tmem_ld_x32(tmem + lanes + 256 + 32 * part, s);
       tmem_ld_wait(s);
+      const bool whole = !masked || __all_sync(kFull, on == kFull);           // (of the warp's places)
       if (masked) {
-        warp_wait(&bk.q_full[j & 1], (j >> 1) & 1, abort, lim);
         warp_wait(&bk.do_full[j & 1], (j >> 1) & 1, abort, lim);
         clean_tile<DP>(do_smem + (j & 1) * C::kBytes, threadIdx.x, kBwdArith, [] {});
-        clean_tile<DP>(q_smem + (j & 1) * C::kBytes, threadIdx.x, kBwdArith, [] {});
       }
       #pragma unroll
       for (int x = 0; x < 32; x += 2) {
         float2 y = split_f32x2(mul2(make_f32x2(as_f(s[x]), as_f(s[x + 1])), mul2_));
         y.x = ex2(y.x);
         y.y = ex2(y.y);
-        if (masked) {
-          if (!(on >> x & 1u)) y.x = 0.f;
-          if (!(on >> x & 2u)) y.y = 0.f;
-        }
         s[x] = __float_as_uint(y.x);
         s[x + 1] = __float_as_uint(y.y);
-        w[x / 2] = pack_bf16x2(y.x, y.y);
+        if (!masked) w[x / 2] = pack_bf16x2(y.x, y.y);
+      }
+      if (masked) {
+        if (!whole) blank(s, on);
+        #pragma unroll
+        for (int x = 0; x < 32; x += 2) w[x / 2] = pack_bf16x2(as_f(s[x]), as_f(s[x + 1]));
       }
       tmem_st_x16(tmem + lanes + 256 + 32 * part, w);
       tmem_st_wait();
       warp_arrive(&bk.p_full, lane);
+      if (masked) {
+        warp_wait(&bk.q_full[j & 1], (j >> 1) & 1, abort, lim);
+        clean_tile<DP>(q_smem + (j & 1) * C::kBytes, threadIdx.x, kBwdArith, [] {});
+      }
       warp_wait(&bk.dp_full, j & 1, abort, lim);
       tc_fence_after_sync();
       tmem_ld_x32(tmem + lanes + 384 + 32 * part, d);
       tmem_ld_wait(d);
+      if (!whole) blank(d, on);               // (so that ds is zero there whatever the tensors hold)
       #pragma unroll
       for (int x = 0; x < 32; x += 2) {
-        float2 y = split_f32x2(mul2(make_f32x2(as_f(s[x]), as_f(s[x + 1])), make_f32x2(as_f(d[x]), as_f(d[x + 1]))));
-        if (masked) {
-          if (!(on >> x & 1u)) y.x = 0.f;
-          if (!(on >> x & 2u)) y.y = 0.f;
-        }
+        const float2 y = split_f32x2(mul2(make_f32x2(as_f(s[x]), as_f(s[x + 1])), make_f32x2(as_f(d[x]), as_f(d[x + 1]))));
         w[x / 2] = pack_bf16x2(y.x, y.y);
       }
       tmem_st_x16(tmem + lanes + 384 + 32 * part, w);
@@ -1596,11 +1597,11 @@ cudaError_t forward(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensor
 }
 template <int DP>
 cudaError_t backward(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& td,
-                     AttnParams p, const Heads& dq, const Heads& dk, const Heads& dv, cudaStream_t st) {
+                     const CUtensorMap& to, AttnParams p, const Heads& dq, const Heads& dk, const Heads& dv, cudaStream_t st) {
   static std::atomic<bool> dq_set[kMaxDevices], dkv_set[kMaxDevices];
   p.d0 = dq;
   const cudaError_t e =
-      launch_big(attention_dq_kernel<DP>, dq_set, p.tiles * p.Hq, kBwdThreads, smem_of(dq_smem<DP>()), st, 1, tq, tk, tv, td, p);
+      launch_big(attention_dq_kernel<DP>, dq_set, p.tiles * p.Hq, kBwdThreads, smem_of(dq_smem<DP>()), st, 1, tq, tk, tv, td, to, p);
   if (e != cudaSuccess) return e;
   p.d0 = dk;
   p.d1 = dv;
@@ -1639,7 +1640,7 @@ moe_status moe_attention_forward(const moe_attention_config* cfg, const moe_head
   if (p.pair_rows) p.tiles = (T + 2 * kRows - 1) / (2 * kRows);
   p.o = heads_of(out, T, Hq, D);
   p.d0 = heads_of(v, T, Hkv, D);
-  p.d1 = heads_of(q, T, Hq, D);
+  p.q = heads_of(q, T, Hq, D);
   p.lse = lse;
   CUtensorMap tq, tk, tv;
   if (!make_map(&tq, q, T, Hq, D) || !make_map(&tk, k, T, Hkv, D) || !make_map(&tv, v, T, Hkv, D))
@@ -1663,17 +1664,15 @@ moe_status moe_attention_backward(const moe_attention_config* cfg, const moe_hea
   if (!device_is_gb300()) return MOE_ERR_UNSUPPORTED;
   if (none) return MOE_OK;
   AttnParams p = params_of(cfg, cu_seqlens, ws);
-  p.o = heads_of(out, T, Hq, D);
-  p.dout = heads_of(dout, T, Hq, D);
   p.lse = const_cast<float*>(lse);
-  CUtensorMap tq, tk, tv, td;
+  CUtensorMap tq, tk, tv, td, to;
   if (!make_map(&tq, q, T, Hq, D) || !make_map(&tk, k, T, Hkv, D) || !make_map(&tv, v, T, Hkv, D) ||
-      !make_map(&td, dout, T, Hq, D))
+      !make_map(&td, dout, T, Hq, D) || !make_map(&to, out, T, Hq, D))
     return MOE_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const Heads hq = heads_of(dq, T, Hq, D), hk = heads_of(dk, T, Hkv, D), hv = heads_of(dv, T, Hkv, D);
-  return status_of(D <= 64 ? backward<64>(tq, tk, tv, td, p, hq, hk, hv, st)
-                           : backward<128>(tq, tk, tv, td, p, hq, hk, hv, st));
+  return status_of(D <= 64 ? backward<64>(tq, tk, tv, td, to, p, hq, hk, hv, st)
+                           : backward<128>(tq, tk, tv, td, to, p, hq, hk, hv, st));
 }
 
 }  // extern "C"
