@@ -9,13 +9,18 @@
 // whatever the sequences: a tile's keys are the rows from its first row's start to its
 // own last one, and what a row does not see is masked.  So the tile list needs the
 // number of rows alone, which the host knows, and each CTA reads from cu_seqlens where
-// its own rows' sequences begin and end (row_map).  A key tile ends where the row
+// its own rows' sequences begin and end (row_map, find_map).  A key tile ends where the row
 // tile does, so each row finds its own key in the first tile it meets and its
 // maximum is finite from then on.
 //
 // Every product is a tcgen05.mma on 128-row tiles that TMA brings (zeros outside
-// the tensor and past the head's width); one thread issues them, and eight warps
-// work on the scores in TMEM, a thread a row.
+// the tensor and past the head's width); a warp or two issue them, and eight (forward) or
+// sixteen warps work on the scores in TMEM.
+//
+// Measured at 8192 rows of one sequence, 32/8 heads of 128 (a library's bf16 product of 8192 x 8192 x 8192: 1927
+// TFLOP/s): forward 354 us (1552), gradients 1150 (1195, of five products; the two kernels compute seven, of which
+// the scores and dp twice).  Eight packed sequences of 1 to 3907 rows: 154 and 484 us.  Heads of 64, 32768 rows, 8/1
+// heads: forward 926 us (1187).  One row: 7.4 us.
 //
 // Values that are not finite: a product with a probability of zero is still a NaN
 // on the tensor cores.  Where a tile has masked places the operand along the
@@ -382,6 +387,19 @@ __device__ __forceinline__ void store_rows(uint8_t* staging, __nv_bfloat16* out,
   }
 }
 
+// Lanes a and a ^ M (a without the bit): a's second word against the other's first.
+template <int M>
+__device__ __forceinline__ void exchange(uint4& first, uint4& second) {
+  const bool high = (threadIdx.x & M) != 0;
+  const uint4 give = high ? first : second;
+  const uint4 got = make_uint4(__shfl_xor_sync(kFull, give.x, M), __shfl_xor_sync(kFull, give.y, M),
+                               __shfl_xor_sync(kFull, give.z, M), __shfl_xor_sync(kFull, give.w, M));
+  if (high)
+    first = got;
+  else
+    second = got;
+}
+
 // ---------------------------------------------------------------- forward
 // A CTA has two tiles of 128 query rows, each with four warps, and one stream of key
 // and value tiles for both: two heads of a group on the same rows, or (groups of an
@@ -396,6 +414,10 @@ __device__ __forceinline__ void store_rows(uint8_t* staging, __nv_bfloat16* out,
 // each (one for both waits for one while the other could go on: 322 us against 264 at 8192 rows,
 // 32 heads of 64; with a buffer a tile 300).  Wide heads have a buffer a tile and one issuing warp (two: 0.53 ms
 // against 0.41).
+//
+// What bounds it: a step, one key tile against both tiles of rows, is 2770 cycles at heads of 128, of which the
+// tensor cores work 2048.  The rest is the chain of one tile (scores, maximum, exponentials, sums,
+// next scores), of which TMEM has room for two.
 //
 // A barrier that is waited for by parity has to be seen before its next phase ends.  With three buffers a tile's next
 // probabilities can be there before the last ones' arrival has been looked at, so their barriers are two, in turns.
@@ -901,23 +923,33 @@ __device__ __forceinline__ uint4 split_row(float v) {
                     __bfloat16_as_ushort(c), 0u, 0u);
 }
 
-// dq: 128 query rows of one head against their key tiles.  TMEM: dq DP columns from 0,
-// scores at 128, two buffers of dp at 256 and 384 (each becomes ds).  Both products of the
-// next key tile run while this one's ds is worked out, the scores once they have been read.
+// dq: 128 query rows of one head against their key tiles, CTAs that stay as in the forward.  TMEM: dq DP columns
+// from 0, scores at 128, two buffers of dp at 256 and 384 (each becomes ds).  Both products of the next key
+// tile run while this one's ds is worked out, the scores once they have been read.  A step is 2000
+// cycles at heads of 128, of which the tensor cores work 1536; an item takes 12 thousand besides (a CTA for each: 15).
+//
+// out, for delta, comes through a place of the keys (TMA; read from memory by the threads it
+// kept the first step waiting as long).
 //
 // delta comes from the rounded out, an error of out's rounding in each of its products.  Where a
 // row sees few keys that is of the size of ds; rows that begin within their first key tile
 // take delta = sum_j p dp there instead.  Either goes to stats, for dk.
 constexpr int kKStages = 3;                // key tiles in flight: one is held from its scores to its dq
+struct DqItem {
+  RowMap map;
+  int item, n;                             // item -1: no more; n: key tiles
+  int q0, head, kv;
+};
 struct DqBook {
-  uint64_t q_full, k_full[kKStages], v_full[2], o_full;      // (one after the other: Issued counts on it)
-  uint64_t o_read;
-  uint64_t k_empty[kKStages], v_empty[2], s_full, s_empty, dp_full[2], dp_empty[2], ds_full[2], done;
+  uint64_t q_full, k_full[kKStages], v_full[2];              // (one after the other: Issued counts on it)
+  uint64_t q_empty, o_read, k_empty[kKStages], v_empty[2], s_full, s_empty, dp_full[2], dp_empty[2], ds_full[2];
+  uint64_t out_full, out_empty, drain, item_full[2], item_empty[2], ending;
   uint32_t tmem;
   int abort_flag;
-  RowMap map;
+  DqItem item[2];
   float sums[kParts][kRows];               // parts of rows' sums
 };
+constexpr int kBwdItemWarp = kBwdLoadWarp + 3;
 
 template <int DP>
 __global__ void __launch_bounds__(kBwdThreads, 1)
@@ -937,9 +969,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     return;
   }
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (warp == kBwdLoadWarp && lane == 0) {          // (it uses them before the first barrier of all threads)
+  if (warp == kBwdLoadWarp && lane == 0) {
     mbar_init(&bk.q_full, 1);
-    mbar_init(&bk.o_full, 1);
+    mbar_init(&bk.q_empty, 1 + kBwdArith / 32);              // dp's products, and delta's reads
     mbar_init(&bk.o_read, kBwdArith / 32);
     for (int s = 0; s < kKStages; ++s) {
       mbar_init(&bk.k_full[s], 1);
@@ -951,10 +983,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       mbar_init(&bk.dp_full[s], 1);
       mbar_init(&bk.dp_empty[s], 1);
       mbar_init(&bk.ds_full[s], kBwdArith / 32);
+      mbar_init(&bk.item_full[s], 1);
+      mbar_init(&bk.item_empty[s], 3 + kBwdArith / 32);      // loads, the two that issue, arithmetic
     }
     mbar_init(&bk.s_full, 1);
     mbar_init(&bk.s_empty, kBwdArith / 32);
-    mbar_init(&bk.done, 2);
+    mbar_init(&bk.out_full, 1);
+    mbar_init(&bk.out_empty, kBwdArith / 32);
+    mbar_init(&bk.ending, 1);
+    mbar_init(&bk.drain, 2);
     bk.abort_flag = 0;
     fence_mbarrier_init();
     prefetch_tensormap(&tmQ);
@@ -969,104 +1006,190 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   }
   tc_fence_before_sync();
   pdl_wait();
-  const int h = static_cast<int>(blockIdx.x) % p.Hq;
-  const int q0 = (p.tiles - 1 - static_cast<int>(blockIdx.x) / p.Hq) * kRows;
-  // The queries and the first keys do not wait for the sequences' boundaries.  out takes the place of the third keys
-  // until delta has been worked out.
-  uint8_t* o_smem = k_smem + 2 * C::kBytes;
-  const int kv = h / (p.Hq / p.Hkv), top = q0 + kRows;
-  if (warp == kBwdLoadWarp && lane == 0) {
-    mbar_arrive_expect_tx(&bk.q_full, 2 * C::kBytes);
-    load_tile<DP>(q_smem, &tmQ, &bk.q_full, h, q0);
-    load_tile<DP>(do_smem, &tmDo, &bk.q_full, h, q0);
-    mbar_arrive_expect_tx(&bk.k_full[0], C::kBytes);
-    load_tile<DP>(k_smem, &tmK, &bk.k_full[0], kv, q0);
-    mbar_arrive_expect_tx(&bk.v_full[0], C::kBytes);
-    load_tile<DP>(v_smem, &tmV, &bk.v_full[0], kv, q0);
-    mbar_arrive_expect_tx(&bk.o_full, C::kBytes);
-    load_tile<DP>(o_smem, &tmO, &bk.o_full, h, q0);
+  // Item `item` as number `it` of this CTA, by the item warp: the last tiles first, they have the longest rows of keys.
+  int mine = INT_MAX, first_row = 0, last_row = 0;
+  auto place = [&](int item, int it) {
+    DqItem& m = bk.item[it & 1];
+    const int q0 = (p.tiles - 1 - item / p.Hq) * kRows, h = item % p.Hq;
+    find_map<kRows>(p, q0, mine, first_row, last_row, &m.map);
+    if (lane == 0) {
+      const int a = max(q0, first_row), b = min(q0 + kRows, last_row);
+      m.n = a < b ? (q0 + kRows - start_of(&m.map, q0, a) + kRows - 1) / kRows : 0;
+      m.q0 = q0;
+      m.head = h;
+      m.kv = h / (p.Hq / p.Hkv);
+      m.item = item;
+    }
+    __syncwarp();
+  };
+  if (warp == kBwdItemWarp) {
+    if (lane <= p.B) mine = p.cu[lane];     // (the first boundaries stay with it)
+    const int begin = p.B < 32 ? __shfl_sync(kFull, mine, 0) : p.cu[0], end = p.B < 32 ? __shfl_sync(kFull, mine, p.B) : p.cu[p.B];
+    first_row = max(begin, 0);
+    last_row = min(end, p.T);
+    place(blockIdx.x, 0);
   }
-  row_map<kRows>(p, q0, &bk.map);
+  __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = uniform(bk.tmem);
   volatile int* abort = &bk.abort_flag;
   const unsigned long long lim = p.wait_ns;
-  const int a = max(q0, bk.map.first), b = min(top, bk.map.last);
-  const int n = a < b ? (top - start_of(&bk.map, q0, a) + kRows - 1) / kRows : 0;
+  // The next item for a role; false: no more (or a wait has given up).
+  auto next_item = [&](int it) {
+    mbar_wait(&bk.item_full[it & 1], (it >> 1) & 1, abort, lim);
+    return *const_cast<volatile int*>(&bk.item[it & 1].item) >= 0 && *abort == 0;
+  };
 
   if (warp >= kBwdLoadWarp) {
    fewer_registers<kBwdOtherRegs>();
-   if (warp == kBwdLoadWarp) {
+   if (warp == kBwdItemWarp) {
+    // ------------------------------------------------ the items (as in the forward)
+    const int items = p.tiles * p.Hq, grid = gridDim.x;
+    int next = blockIdx.x;
+    for (int it = 0;; ++it) {
+      if (it >= 2) warp_wait(&bk.item_empty[it & 1], ((it >> 1) & 1) ^ 1u, abort, lim);
+      if (next >= items || uniform(*abort) != 0) {
+        if (lane == 0) {
+          bk.item[it & 1].item = -1;
+          mbar_arrive(&bk.item_full[it & 1]);
+        }
+        break;
+      }
+      if (it > 0) place(next, it);          // (the first one has been placed)
+      if (lane == 0) mbar_arrive(&bk.item_full[it & 1]);
+      warp_wait(&bk.ending, it & 1, abort, lim);
+      next = uniform(lane == 0 ? take_item(p.status, items, grid) : 0);
+    }
+    while (next < items) next = uniform(lane == 0 ? take_item(p.status, items, grid) : 0);      // (given up)
+    check_boundaries(p);
+   } else if (warp == kBwdLoadWarp) {
     if (lane == 0) {
       Issued got;
-      got.note(0, 0);
-      got.note(1, 0);
-      got.note(1 + kKStages, 0);
-      got.note(3 + kKStages, 0);
-      for (int j = 1; j < n; ++j) {
-        const int s = j % kKStages, s2 = j & 1, row = top - kRows * (j + 1);
-        const uint32_t ph = (j / kKStages) & 1, ph2 = (j >> 1) & 1;
-        if (j == 2 && !mbar_wait(&bk.o_read, 0, abort, lim)) break;
-        if (j >= kKStages && !mbar_wait(&bk.k_empty[s], ph ^ 1u, abort, lim)) break;
-        mbar_arrive_expect_tx(&bk.k_full[s], C::kBytes);
-        load_tile<DP>(k_smem + s * C::kBytes, &tmK, &bk.k_full[s], kv, row);
-        got.note(1 + s, ph);
-        if (j >= 2 && !mbar_wait(&bk.v_empty[s2], ph2 ^ 1u, abort, lim)) break;
-        mbar_arrive_expect_tx(&bk.v_full[s2], C::kBytes);
-        load_tile<DP>(v_smem + s2 * C::kBytes, &tmV, &bk.v_full[s2], kv, row);
-        got.note(1 + kKStages + s2, ph2);
+      int turn = 0, vturn = 0, live = 0;     // tiles through the stages of k and v, items with rows
+      bool go = true;
+      for (int it = 0; go && next_item(it); ++it) {
+        const DqItem& m = bk.item[it & 1];
+        const int n = m.n, q0 = m.q0, h = m.head, kv = m.kv;
+        // a place among the keys: for out first, then for them
+        auto place_k = [&](const CUtensorMap* map, int head, int row) {
+          const int s = turn % kKStages;
+          const uint32_t ph = (turn / kKStages) & 1;
+          if (turn >= kKStages && !mbar_wait(&bk.k_empty[s], ph ^ 1u, abort, lim)) return false;
+          mbar_arrive_expect_tx(&bk.k_full[s], C::kBytes);
+          load_tile<DP>(k_smem + s * C::kBytes, map, &bk.k_full[s], head, row);
+          got.note(1 + s, ph);
+          ++turn;
+          return true;
+        };
+        if (n > 0) {
+          if (live > 0 && !mbar_wait(&bk.q_empty, (live - 1) & 1, abort, lim)) break;
+          mbar_arrive_expect_tx(&bk.q_full, 2 * C::kBytes);
+          load_tile<DP>(q_smem, &tmQ, &bk.q_full, h, q0);
+          load_tile<DP>(do_smem, &tmDo, &bk.q_full, h, q0);
+          got.note(0, live & 1);
+          ++live;
+          if (!place_k(&tmO, h, q0)) break;
+          for (int j = 0; j < n && go; ++j) {
+            const int row = q0 - kRows * j, s = vturn & 1;
+            const uint32_t ph = (vturn >> 1) & 1;
+            if (!place_k(&tmK, kv, row) || (vturn >= 2 && !mbar_wait(&bk.v_empty[s], ph ^ 1u, abort, lim))) {
+              go = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&bk.v_full[s], C::kBytes);
+            load_tile<DP>(v_smem + s * C::kBytes, &tmV, &bk.v_full[s], kv, row);
+            got.note(1 + kKStages + s, ph);
+            ++vturn;
+          }
+        }
+        mbar_arrive(&bk.item_empty[it & 1]);
+        mbar_arrive(&bk.ending);
       }
       got.drain(&bk.q_full);
     }
-   } else if (n > 0 && (warp == kBwdMmaWarp || warp == kBwdMmaWarp + 1)) {
+   } else {
     // One warp issues the scores and dp, the other dq: what one waits for costs the other nothing.
     const uint32_t leader = elect_one() ? 1u : 0u;
     constexpr uint64_t kNext = C::kBytes >> 4;
-    const int tiles = uniform(n);
-    if (warp == kBwdMmaWarp) {
-      const uint64_t q_desc = scores_desc(q_smem), do_desc = scores_desc(do_smem), k_desc = scores_desc(k_smem),
-                     v_desc = scores_desc(v_smem);
-      warp_wait(&bk.q_full, 0, abort, lim);
-      for (int j = 0; j < tiles; ++j) {
-        // (the scores once the last ones have been read; dp's buffer once the ds before the last is dq's)
-        warp_wait(&bk.k_full[j % kKStages], (j / kKStages) & 1, abort, lim);
-        if (j > 0) warp_wait(&bk.s_empty, (j - 1) & 1, abort, lim);
-        tc_fence_after_sync();
-        mma_scores<DP>(leader, tmem + 128, q_desc, k_desc + (j % kKStages) * kNext);
-        mma_commit_warp(leader, &bk.s_full);
-        warp_wait(&bk.v_full[j & 1], (j >> 1) & 1, abort, lim);
-        if (j >= 2) warp_wait(&bk.dp_empty[j & 1], ((j >> 1) & 1) ^ 1u, abort, lim);
-        tc_fence_after_sync();
-        mma_scores<DP>(leader, tmem + 256 + 128 * (j & 1), do_desc, v_desc + (j & 1) * kNext);
-        mma_commit_warp(leader, &bk.dp_full[j & 1]);
-        if (j + 2 < tiles) mma_commit_warp(leader, &bk.v_empty[j & 1]);
+    const uint64_t q_desc = scores_desc(q_smem), do_desc = scores_desc(do_smem), k_desc = scores_desc(k_smem),
+                   v_desc = scores_desc(v_smem), kt_desc = sums_desc(k_smem);
+    // the place among the keys (of kKStages) and its round, key tiles met, items with rows
+    uint32_t ks = 0, kr = 0, at = 0;
+    int live = 0;
+    auto next_place = [&] {
+      if (++ks == kKStages) {
+        ks = 0;
+        kr ^= 1;
       }
-    } else {
-      const uint64_t kt_desc = sums_desc(k_smem);
-      for (int j = 0; j < tiles; ++j) {
-        warp_wait(&bk.ds_full[j & 1], (j >> 1) & 1, abort, lim);
-        tc_fence_after_sync();
-        mma_sums<DP, 2>(leader, tmem, tmem + 256 + 128 * (j & 1), kt_desc + (j % kKStages) * kNext, j > 0);
-        if (j + 2 < tiles) mma_commit_warp(leader, &bk.dp_empty[j & 1]);
-        if (j + kKStages < tiles) mma_commit_warp(leader, &bk.k_empty[j % kKStages]);
+    };
+    for (int it = 0; uniform(next_item(it) ? 1 : 0) != 0; ++it) {
+      const int n = uniform(bk.item[it & 1].n);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bk.item_empty[it & 1]);
+      if (n == 0) continue;
+      if (warp == kBwdMmaWarp) {
+        warp_wait(&bk.q_full, live & 1, abort, lim);
+        next_place();                        // (out's)
+        for (int j = 0; j < n; ++j) {
+          // (the scores once the last ones have been read; dp's buffer once the ds before the last is dq's)
+          const uint32_t b = at & 1;
+          warp_wait(&bk.k_full[ks], kr, abort, lim);
+          if (at > 0) warp_wait(&bk.s_empty, (at - 1) & 1, abort, lim);
+          tc_fence_after_sync();
+          mma_scores<DP>(leader, tmem + 128, q_desc, k_desc + ks * kNext);
+          mma_commit_warp(leader, &bk.s_full);
+          warp_wait(&bk.v_full[b], (at >> 1) & 1, abort, lim);
+          if (at >= 2) warp_wait(&bk.dp_empty[b], ((at >> 1) & 1) ^ 1u, abort, lim);
+          tc_fence_after_sync();
+          mma_scores<DP>(leader, tmem + 256 + 128 * b, do_desc, v_desc + b * kNext);
+          mma_commit_warp(leader, &bk.dp_full[b]);
+          mma_commit_warp(leader, &bk.v_empty[b]);
+          next_place();
+          ++at;
+        }
+        mma_commit_warp(leader, &bk.q_empty);
+      } else {
+        warp_wait(&bk.o_read, live & 1, abort, lim);
+        if (lane == 0) mbar_arrive(&bk.k_empty[ks]);
+        next_place();
+        if (live > 0) warp_wait(&bk.out_empty, (live - 1) & 1, abort, lim);
+        for (int j = 0; j < n; ++j) {
+          const uint32_t b = at & 1;
+          warp_wait(&bk.ds_full[b], (at >> 1) & 1, abort, lim);
+          tc_fence_after_sync();
+          mma_sums<DP, 2>(leader, tmem, tmem + 256 + 128 * b, kt_desc + ks * kNext, j > 0);
+          mma_commit_warp(leader, &bk.dp_empty[b]);
+          mma_commit_warp(leader, &bk.k_empty[ks]);
+          next_place();
+          ++at;
+        }
+        mma_commit_warp(leader, &bk.out_full);
       }
+      ++live;
     }
-    mma_commit_warp(leader, &bk.done);
-    mbar_wait_drain(&bk.done, 0);
+    mma_commit_warp(leader, &bk.drain);
+    mbar_wait_drain(&bk.drain, 0);
    }
   } else {
    more_registers<kBwdRegs>();
-   if (n > 0) {
-    const int part = warp >> 2;
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const int lr = (warp & 3) * 32 + lane, row = q0 + lr;
-    const bool valid = row >= bk.map.first && row < bk.map.last;
-    const int key_lo = valid ? start_of(&bk.map, q0, row) : p.T, key_hi = valid ? row : -1;
-    const int all_from = start_of(&bk.map, q0, b - 1);
+   const int part = warp >> 2;
+   const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+   const int lr = (warp & 3) * 32 + lane;
+   const F32x2 mul2_ = make_f32x2(p.scale2, p.scale2);
+   int turn = 0, steps = 0, live = 0;        // as in the warps that issue
+   for (int it = 0; uniform(next_item(it) ? 1 : 0) != 0; ++it) {
+    const DqItem& m = bk.item[it & 1];
+    const int n = m.n, q0 = m.q0, row = q0 + lr;
+    if (n > 0) {
+    const bool valid = row >= m.map.first && row < m.map.last;
+    const int key_lo = valid ? start_of(&m.map, q0, row) : p.T, key_hi = valid ? row : -1;
+    const int all_from = start_of(&m.map, q0, min(q0 + kRows, m.map.last) - 1);
+    const float lse = valid ? -p.lse[static_cast<long long>(m.head) * p.T + row] * kLog2e : 0.f;
     // <do, o>: a quarter of the columns a thread
-    warp_wait(&bk.q_full, 0, abort, lim);
-    warp_wait(&bk.o_full, 0, abort, lim);
+    warp_wait(&bk.q_full, live & 1, abort, lim);
+    warp_wait(&bk.k_full[turn % kKStages], (turn / kKStages) & 1, abort, lim);
     {
+      const uint8_t* o_smem = k_smem + turn % kKStages * C::kBytes;
       float d = 0.f;
       #pragma unroll
       for (int i = 0; i < DP / 32; ++i) {
@@ -1079,17 +1202,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       bk.sums[part][lr] = d;
     }
     warp_arrive(&bk.o_read, lane);
+    if (lane == 0) mbar_arrive(&bk.q_empty);
     arith_sync();
     float delta = -((bk.sums[0][lr] + bk.sums[1][lr]) + (bk.sums[2][lr] + bk.sums[3][lr]));
     arith_sync();
-    const float l = valid ? p.lse[static_cast<long long>(h) * p.T + row] : 0.f;
-    const float lse = -l * kLog2e;
-    const F32x2 lse2 = make_f32x2(lse, lse), mul2_ = make_f32x2(p.scale2, p.scale2);
+    const F32x2 lse2 = make_f32x2(lse, lse);
     auto step = [&](int j, auto masked_c) {
       constexpr bool masked = decltype(masked_c)::value;
-      warp_wait(&bk.s_full, j & 1, abort, lim);
+      const int at = steps + j, b = at & 1;
+      warp_wait(&bk.s_full, at & 1, abort, lim);
       tc_fence_after_sync();
-      const int k0 = top - kRows * (j + 1);
+      const int k0 = q0 - kRows * j;
       const uint32_t on = masked ? seen(key_lo - k0 - 32 * part, key_hi - k0 - 32 * part) : kFull;
       const bool whole = !masked || __all_sync(kFull, on == kFull);           // (of the warp's places)
       uint32_t s[32], d[32], w[16];
@@ -1104,11 +1227,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
       if (masked) {
         if (!whole) blank(s, on);
-        warp_wait(&bk.k_full[j % kKStages], (j / kKStages) & 1, abort, lim);
-        clean_tile<DP>(k_smem + (j % kKStages) * C::kBytes, threadIdx.x, kBwdArith, [] {});
+        const int k = turn + 1 + j;
+        warp_wait(&bk.k_full[k % kKStages], (k / kKStages) & 1, abort, lim);
+        clean_tile<DP>(k_smem + (k % kKStages) * C::kBytes, threadIdx.x, kBwdArith, [] {});
       }
-      warp_wait(&bk.dp_full[j & 1], (j >> 1) & 1, abort, lim);
-      const uint32_t tdp = tmem + lanes + 256 + 128 * (j & 1) + 32 * part;
+      warp_wait(&bk.dp_full[b], (at >> 1) & 1, abort, lim);
+      const uint32_t tdp = tmem + lanes + 256 + 128 * b + 32 * part;
       tc_fence_after_sync();
       tmem_ld_x32(tdp, d);
       tmem_ld_wait(d);
@@ -1133,35 +1257,54 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
       tmem_st_x16(tdp, w);
       tmem_st_wait();
-      warp_arrive(&bk.ds_full[j & 1], lane);
+      warp_arrive(&bk.ds_full[b], lane);
       if (masked && j == 0 && valid && part == 0) {
         // (where do is not finite, nor is delta: p of this row shall not be either)
-        p.stats[h * p.pitch + row] = split_row(isfinite(delta) ? -l / p.scale : delta - delta);
-        p.stats[(p.Hq + h) * p.pitch + row] = split_row(delta);
+        uint4* stats = p.stats + m.head * p.pitch + row;
+        stats[0] = split_row(isfinite(delta) ? lse / p.scale2 : delta - delta);
+        stats[p.Hq * p.pitch] = split_row(delta);
       }
     };
     for (int j = 0; j < n; ++j) {
-      if (j == 0 || top - kRows * (j + 1) < all_from)
+      if (j == 0 || q0 - kRows * j < all_from)
         step(j, std::true_type{});
       else
         step(j, std::false_type{});
     }
-    warp_wait(&bk.done, 0, abort, lim);
+    warp_wait(&bk.out_full, live & 1, abort, lim);
     tc_fence_after_sync();
-    {
-      const int col = 32 * part;
-      if (col < DP) {
-        uint32_t o[32];
-        float v[32];
-        tmem_ld_x32(tmem + lanes + col, o);
-        tmem_ld_wait(o);
-        #pragma unroll
-        for (int x = 0; x < 32; ++x) v[x] = as_f(o[x]) * p.scale;
-        // (the tiles have been read)
-        store_cols(q_smem + warp * 2048, p.d0.p + (row - lane) * p.d0.token + h * p.d0.head, p.d0.token,
-                   __ballot_sync(kFull, valid), col, p.D, v);
-      }
+    const int col = 32 * part;
+    uint32_t o[32];
+    tmem_ld_x32(tmem + lanes + col, o);
+    tmem_ld_wait(o);
+    warp_arrive(&bk.out_empty, lane);
+    // A row's 64 bytes by four lanes, which turn their words round among themselves: shared memory has the next
+    // item's tiles on their way to it.
+    uint4 w[4];
+    #pragma unroll
+    for (int x = 0; x < 4; ++x)
+      w[x] = make_uint4(pack_bf16x2(as_f(o[8 * x]) * p.scale, as_f(o[8 * x + 1]) * p.scale),
+                        pack_bf16x2(as_f(o[8 * x + 2]) * p.scale, as_f(o[8 * x + 3]) * p.scale),
+                        pack_bf16x2(as_f(o[8 * x + 4]) * p.scale, as_f(o[8 * x + 5]) * p.scale),
+                        pack_bf16x2(as_f(o[8 * x + 6]) * p.scale, as_f(o[8 * x + 7]) * p.scale));
+    exchange<1>(w[0], w[1]);
+    exchange<1>(w[2], w[3]);
+    exchange<2>(w[0], w[2]);
+    exchange<2>(w[1], w[3]);
+    const uint32_t rows = __ballot_sync(kFull, valid);
+    const int at_col = col + 8 * (lane & 3);
+    __nv_bfloat16* out = p.d0.p + (row - lane) * p.d0.token + m.head * p.d0.head + at_col;
+    #pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int r = (lane & ~3) + x;         // word lane % 4 of this row
+      if ((rows >> r & 1u) && at_col < p.D) *reinterpret_cast<uint4*>(out + r * p.d0.token) = w[x];
     }
+    turn += 1 + n;
+    steps += n;
+    ++live;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bk.item_empty[it & 1]);
    }
   }
   __syncwarp();
@@ -1180,7 +1323,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // key), so that the probabilities lie in TMEM as the A operand of the sums.  TMEM: dk, dv
 // DP columns from 0 and 128, scores at 256 (which become p), dp at 384 (ds).  In the
 // order dv(j), scores(j + 1), dk(j), dp(j + 1) each buffer is free again when its turn
-// comes.
+// comes.  A step is 2600 cycles at heads of 128, of which the tensor cores work 2176.
 //
 // A thread's columns are queries, each with an lse and a delta of its own.  Read from shared memory
 // they cost it 128 KB a step, as much as the tiles (a step 2900 cycles, whatever the width); so
@@ -1497,7 +1640,8 @@ constexpr int dkv_smem() {
 }
 static_assert(fwd_smem<128>() <= kMaxSmem && dq_smem<128>() <= kMaxSmem && dkv_smem<128>() <= kMaxSmem, "shared memory");
 
-// Launch of blocks with much shared memory, in clusters of `cluster`.
+// Launch of blocks with much shared memory, in clusters of `cluster`.  (Each takes an SM's registers for itself, so no
+// two blocks of an SM wait for each other's TMEM, which the blocks of two clusters might do in a ring.)
 template <class... KArgs, class... Args>
 cudaError_t launch_big(void (*kern)(KArgs...), std::atomic<bool>* attr_set, int grid, int threads, int smem, cudaStream_t st, int cluster,
                        Args&&... args) {
@@ -1600,8 +1744,9 @@ cudaError_t backward(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
                      const CUtensorMap& to, AttnParams p, const Heads& dq, const Heads& dk, const Heads& dv, cudaStream_t st) {
   static std::atomic<bool> dq_set[kMaxDevices], dkv_set[kMaxDevices];
   p.d0 = dq;
+  const int items = p.tiles * p.Hq, sms = num_sms();
   const cudaError_t e =
-      launch_big(attention_dq_kernel<DP>, dq_set, p.tiles * p.Hq, kBwdThreads, smem_of(dq_smem<DP>()), st, 1, tq, tk, tv, td, to, p);
+      launch_big(attention_dq_kernel<DP>, dq_set, items < sms ? items : sms, kBwdThreads, smem_of(dq_smem<DP>()), st, 1, tq, tk, tv, td, to, p);
   if (e != cudaSuccess) return e;
   p.d0 = dk;
   p.d1 = dv;
