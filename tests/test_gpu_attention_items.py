@@ -40,3 +40,35 @@ def test_many_launches_end_and_agree(lib, T, Hq, Hkv, D):
     assert torch.equal(outs[0], outs[1])
     for a, b in zip(*grads):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(32, 8, 64), (32, 8, 128), (15, 5, 80)])
+def test_a_limit_that_no_wait_can_meet_ends_the_launch(lib, Hq, Hkv, D):
+    """CTAs with items left return all the same, and the next call on the workspace has them all again."""
+    c = _case([3000, 1, 1100], Hq, Hkv, D, seed=3)
+    cu, T, q, k, v, do = c
+    want = _run(*c)
+    qd, kd, vd, dod = (t.to(DEV) for t in (q, k, v, do))
+    cud, ws = torch.from_numpy(cu).to(DEV), _ws(T, Hq, Hkv, D)
+    got = {n: torch.zeros(t.shape, dtype=t.dtype, device=DEV) for n, t in want.items()}
+
+    def forward():
+        api.moe_attention_forward(qd, kd, vd, cud, got["out"], got["lse"], ws)
+
+    def backward():
+        api.moe_attention_backward(qd, kd, vd, cud, got["out"], got["lse"], dod, got["dq"], got["dk"], got["dv"], ws)
+
+    for call in (forward, backward):
+        api.moe_debug_set_wait_limit_ns(1)
+        try:
+            call()
+            torch.cuda.synchronize()
+        finally:
+            api.moe_debug_set_wait_limit_ns(0)
+        assert api.moe_read_device_status(ws) == -6
+        ws[:4].zero_()               # (the status word alone: the counters have to be back at zero)
+    forward()
+    backward()
+    assert api.moe_read_device_status(ws) == 0
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
