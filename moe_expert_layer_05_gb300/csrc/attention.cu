@@ -281,17 +281,18 @@ template <int DP, class F>
 __device__ __forceinline__ void clean_tile(uint8_t* tile, int t, int n, F found) {
   uint4* w = reinterpret_cast<uint4*>(tile);
   const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
-  __nv_bfloat162 acc = zero;
-  auto add = [&](uint32_t v) { acc = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&v), zero, acc); };
-  #pragma unroll 4
+  __nv_bfloat162 acc[2] = {zero, zero};
+  auto add = [&](int k, uint32_t v) { acc[k] = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&v), zero, acc[k]); };
+  #pragma unroll 8
   for (int i = t; i < Tile<DP>::kBytes / 16; i += n) {
     const uint4 v = w[i];
-    add(v.x);
-    add(v.y);
-    add(v.z);
-    add(v.w);
+    add(0, v.x);
+    add(1, v.y);
+    add(0, v.z);
+    add(1, v.w);
   }
-  if ((*reinterpret_cast<uint32_t*>(&acc) & 0x7fff7fffu) == 0) return;      // (a sum of zeros)
+  const __nv_bfloat162 all = __hadd2(acc[0], acc[1]);
+  if ((*reinterpret_cast<const uint32_t*>(&all) & 0x7fff7fffu) == 0) return;      // (a sum of zeros)
   found();
   auto part = [](uint32_t v) {
     if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
