@@ -18,9 +18,9 @@
 // sixteen warps work on the scores in TMEM.
 //
 // Measured at 8192 rows of one sequence, 32/8 heads of 128 (a library's bf16 product of 8192 x 8192 x 8192: 1927
-// TFLOP/s): forward 354 us (1552), gradients 1150 (1195, of five products; the two kernels compute seven, of which
-// the scores and dp twice).  Eight packed sequences of 1 to 3907 rows: 154 and 484 us.  Heads of 64, 32768 rows, 8/1
-// heads: forward 926 us (1187).  One row: 7.4 us.
+// TFLOP/s): forward 353 us (1557), gradients 1140 (1206, of five products; the two kernels compute seven, of which
+// the scores and dp twice).  Eight packed sequences of 1 to 3907 rows: 153 and 487 us.  Heads of 64, 32768 rows, 8/1
+// heads: forward 928 us (1185).  One row: 7.4 us.
 //
 // Values that are not finite: a product with a probability of zero is still a NaN
 // on the tensor cores.  Where a tile has masked places the operand along the
@@ -1226,12 +1226,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       warp_arrive(&bk.s_empty, lane);
       #pragma unroll
       for (int x = 0; x < 32; x += 2) {
-        const float2 y = split_f32x2(fma2(make_f32x2(as_f(s[x]), as_f(s[x + 1])), mul2_, lse2));
-        s[x] = __float_as_uint(ex2(y.x));
-        s[x + 1] = __float_as_uint(ex2(y.y));
+        float2 y = split_f32x2(fma2(make_f32x2(as_f(s[x]), as_f(s[x + 1])), mul2_, lse2));
+        y.x = ex2(y.x);
+        y.y = ex2(y.y);
+        if (masked) {
+          if (!(on >> x & 1u)) y.x = 0.f;
+          if (!(on >> x & 2u)) y.y = 0.f;
+        }
+        s[x] = __float_as_uint(y.x);
+        s[x + 1] = __float_as_uint(y.y);
       }
       if (masked) {
-        if (!whole) blank(s, on);
         const int k = steps + live + 1 + j;
         warp_wait(&bk.k_full[k % kKStages], (k / kKStages) & 1, abort, lim);
         clean_tile<DP>(k_smem + (k % kKStages) * C::kBytes, threadIdx.x, kBwdArith, [] {});
@@ -1512,14 +1517,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int key = k0 + (warp & 3) * 32 + lane;
     const bool valid = key >= bk.map.first && key < bk.map.last;
-    const int key_end = valid ? end_of(&bk.map, k0, key, kRows / 32) : INT_MAX;
     const int all_to = end_of(&bk.map, k0, a, kRows / 32);      // queries up to here see every key (from the diagonal)
     const F32x2 mul2_ = make_f32x2(p.scale2, p.scale2);
     auto step = [&](int j, int q0, auto masked_c) {
       constexpr bool masked = decltype(masked_c)::value;
       warp_wait(&bk.s_full, j & 1, abort, lim);
       tc_fence_after_sync();
-      const uint32_t on = masked ? seen(key - q0 - 32 * part, key_end - 1 - q0 - 32 * part) : kFull;      // queries [key, key_end)
+      uint32_t on = kFull;                    // queries of the key's sequence, from its own on
+      if (masked) on = seen(key - q0 - 32 * part, (valid ? end_of(&bk.map, k0, key, kRows / 32) : INT_MAX) - 1 - q0 - 32 * part);
       uint32_t s[32], d[32], w[16];
       tmem_ld_x32(tmem + lanes + 256 + 32 * part, s);
       tmem_ld_wait(s);
@@ -1533,14 +1538,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         float2 y = split_f32x2(mul2(make_f32x2(as_f(s[x]), as_f(s[x + 1])), mul2_));
         y.x = ex2(y.x);
         y.y = ex2(y.y);
+        if (masked) {
+          if (!(on >> x & 1u)) y.x = 0.f;
+          if (!(on >> x & 2u)) y.y = 0.f;
+        }
         s[x] = __float_as_uint(y.x);
         s[x + 1] = __float_as_uint(y.y);
-        if (!masked) w[x / 2] = pack_bf16x2(y.x, y.y);
-      }
-      if (masked) {
-        if (!whole) blank(s, on);
-        #pragma unroll
-        for (int x = 0; x < 32; x += 2) w[x / 2] = pack_bf16x2(as_f(s[x]), as_f(s[x + 1]));
+        w[x / 2] = pack_bf16x2(y.x, y.y);
       }
       tmem_st_x16(tmem + lanes + 256 + 32 * part, w);
       tmem_st_wait();
