@@ -204,6 +204,10 @@ __device__ __forceinline__ int take_item(int* status, int items, int grid) {
   return before + grid;
 }
 
+// A count over all of a CTA's items, of which only places and phases are asked for: stages and barriers come round after 16,
+// 6, 4 or 2, so 48 may be taken off (kept above the first round, and from overflowing in very long calls).
+__device__ __forceinline__ int wrapped(int count) { return count < 96 ? count : 48 + count % 48; }
+
 // Bits lo .. hi of 32: the columns that a row sees.  (As bits: a comparison with each end takes three
 // instructions a place, of a kind that the SM starts every other cycle.)
 __device__ __forceinline__ uint32_t seen(int lo, int hi) {
@@ -626,7 +630,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                           top - kRows * (ib + (s >> 1) + 1));
             got.note(slot, ph);
           }
-          turn += loaded;
+          turn = wrapped(turn + loaded);
+          filled = wrapped(filled);
         }
         mbar_arrive(&bk.item_empty[it & 1]);
         mbar_arrive(&bk.ending);
@@ -639,7 +644,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     // this warp's counts over all items: tiles in the ring, fillings of the queries, key tiles met by each tile of
     // rows, items with rows of each, and the buffer of scores and its round
     int turn = 0, filled = 0, met0 = 0, met1 = 0, outs0 = 0, outs1 = 0;
-    uint32_t b = 0, round = 0;
+    uint32_t b = 0;
+    int round = 0;
     for (int it = 0; uniform(next_item(it) ? 1 : 0) != 0; ++it) {
       const FwdItem& m = bk.item[it & 1];
       const int f0 = uniform(m.from[0]), f1 = uniform(m.from[1]), e0 = uniform(m.to[0]), e1 = uniform(m.to[1]);
@@ -726,12 +732,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           }
         }
       }
-      turn += loaded;
-      filled += loaded > 0;
-      met0 += e0 - f0;
-      met1 += e1 - f1;
-      outs0 += e0 > f0;
-      outs1 += e1 > f1;
+      turn = wrapped(turn + loaded);
+      filled = wrapped(filled + (loaded > 0));
+      met0 = wrapped(met0 + e0 - f0);
+      met1 = wrapped(met1 + e1 - f1);
+      outs0 = wrapped(outs0 + (e0 > f0));
+      outs1 = wrapped(outs1 + (e1 > f1));
+      round = wrapped(round);
     }
     mma_commit_warp(leader, &bk.drain);      // (TMEM is given back after them, whoever gave up)
     mbar_wait_drain(&bk.drain, 0);
@@ -888,13 +895,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       store_rows(staging, p.o.p + (row - lane) * p.o.token + h * p.o.head + col, p.o.token, rows, p.D - col);
       __syncwarp();
      }
-     ++outs;
+     outs = wrapped(outs + 1);
     }
-    turn += m.loaded;
+    turn = wrapped(turn + m.loaded);
     __syncwarp();
     if (lane == 0) mbar_arrive(&bk.item_empty[it & 1]);
-    met += e - f;
-    scored += 2 * n;
+    met = wrapped(met + e - f);
+    scored = wrapped(scored + 2 * n);
    }
   }
   __syncwarp();
@@ -1104,6 +1111,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             got.note(1 + kKStages + s, ph);
             ++vturn;
           }
+          turn = wrapped(turn);
+          vturn = wrapped(vturn);
+          live = wrapped(live);
         }
         mbar_arrive(&bk.item_empty[it & 1]);
         mbar_arrive(&bk.ending);
@@ -1117,8 +1127,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const uint64_t q_desc = scores_desc(q_smem), do_desc = scores_desc(do_smem), k_desc = scores_desc(k_smem),
                    v_desc = scores_desc(v_smem), kt_desc = sums_desc(k_smem);
     // the place among the keys (of kKStages) and its round, key tiles met, items with rows
-    uint32_t ks = 0, kr = 0, at = 0;
-    int live = 0;
+    uint32_t ks = 0, kr = 0;
+    int at = 0, live = 0;
     auto next_place = [&] {
       if (++ks == kKStages) {
         ks = 0;
@@ -1168,7 +1178,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         mma_commit_warp(leader, &bk.out_full);
       }
-      ++live;
+      at = wrapped(at);
+      live = wrapped(live + 1);
     }
     mma_commit_warp(leader, &bk.drain);
     mbar_wait_drain(&bk.drain, 0);
@@ -1313,8 +1324,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const int r = (lane & ~3) + x;         // word lane % 4 of this row
       if ((rows >> r & 1u) && at_col < p.D) *reinterpret_cast<uint4*>(out + r * p.d0.token) = w[x];
     }
-    steps += n;
-    ++live;
+    steps = wrapped(steps + n);
+    live = wrapped(live + 1);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&bk.item_empty[it & 1]);

@@ -1,4 +1,5 @@
 """Attention of more tiles than SMs: CTAs that work through several of them, some without rows."""
+import numpy as np
 import pytest
 import torch
 
@@ -72,3 +73,41 @@ def test_a_limit_that_no_wait_can_meet_ends_the_launch(lib, Hq, Hkv, D):
     assert api.moe_read_device_status(ws) == 0
     for n in want:
         assert torch.equal(got[n], want[n]), n
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(4, 2), (3, 1)])
+@pytest.mark.parametrize("lengths", [[0] * 100 + [5] + [0] * 1500 + [130] + [0] * 70 + [1] * 90 + [0] * 33 + [300, 0, 0],
+                                     [3] * 200 + [0] * 31 + [150], [1] * 32, [2] * 31 + [200], [0] * 5000 + [140]])
+def test_many_sequences_most_of_them_empty(lib, lengths, Hq, Hkv):
+    c = _case(lengths, Hq, Hkv, 64, seed=len(lengths), first=3, tail=2)
+    _check(_run(*c), *c)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_many_bad_boundaries_are_reported(lib, seed):
+    """Boundaries in any order, below 0 and far past the rows: reported, nothing outside the tensors touched."""
+    rng = np.random.default_rng(seed)
+    cu, T, q, k, v, do = _case([700], 3 + seed % 2, 1, 64, seed=seed)
+    bad = rng.integers(-300, 1000, 200 + 500 * (seed % 3)).astype(np.int32)
+    bad[rng.integers(0, len(bad), 9)] = [-2 ** 31, 2 ** 31 - 1, 700, 0, 701, -1, 128, 127, 2 ** 30]
+    Hq = q.shape[1]
+    guard = 64
+    def placed(t):
+        whole = torch.full((T + 2 * guard, *t.shape[1:]), 5.0, dtype=torch.bfloat16, device=DEV)
+        whole[guard:guard + T] = t.to(DEV)
+        return whole, whole[guard:guard + T]
+    whole, out = placed(torch.zeros_like(q))
+    grads = [placed(torch.zeros_like(t)) for t in (q, k, v)]
+    lse = torch.full((Hq + 2, T), 5.0, device=DEV)
+    qd, kd, vd, dod = (t.to(DEV) for t in (q, k, v, do))
+    cud = torch.from_numpy(bad).to(DEV)
+    for call in range(2):
+        ws = _ws(T, Hq, 1, 64)
+        if call == 0:
+            api.moe_attention_forward(qd, kd, vd, cud, out, lse[1:-1], ws)
+        else:
+            api.moe_attention_backward(qd, kd, vd, cud, out, lse[1:-1], dod, *(g for _, g in grads), ws)
+        assert api.moe_read_device_status(ws) == -5
+    for w in [whole] + [w for w, _ in grads]:
+        assert (w[:guard] == 5).all() and (w[-guard:] == 5).all()
+    assert (lse[0] == 5).all() and (lse[-1] == 5).all()
