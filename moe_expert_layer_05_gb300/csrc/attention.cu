@@ -1696,8 +1696,8 @@ cudaError_t launch_big(void (*kern)(KArgs...), std::atomic<bool>* attr_set, int 
 // CTAs that share the heads of a group in dk and dv's kernel.  As few as leave no CTA more than 5/4 of an SM's share of
 // one long sequence's tiles: a CTA of the first keys has tiles * group / split of them, an SM (tiles + 1) tiles
 // q_heads / 2 / 152.  Large batches take one: clusters of four leave SMs of a GPC idle (8192 rows, 32/8 heads of
-// 128, backward: 1.38 ms alone, 1.41 in pairs, 1.56 by four); small ones gain (2048 rows, 32/4 heads: 0.28, 0.19, 0.16 and,
-// by eight, 0.23 ms; 1000 rows, 6/2 heads of 80: 69 us, 47 by three).
+// 128, backward: 1.15 ms alone, 1.20 in pairs, 1.35 by four); small ones gain (2048 rows, 32/4 heads: 0.22, 0.14, 0.12 and,
+// by eight, 0.19 ms; 1000 rows, 6/2 heads of 80: 53 us, 38 by three).
 int group_split(const AttnParams& p) {
   const int group = p.Hq / p.Hkv;
   int best = 1;
