@@ -20,7 +20,7 @@
 // Measured at 8192 rows of one sequence, 32/8 heads of 128 (a library's bf16 product of 8192 x 8192 x 8192: 1927
 // TFLOP/s): forward 353 us (1557), gradients 1140 (1206, of five products; the two kernels compute seven, of which
 // the scores and dp twice).  Eight packed sequences of 1 to 3907 rows: 153 and 487 us.  Heads of 64, 32768 rows, 8/1
-// heads: forward 928 us (1185).  One row: 7.4 us.
+// heads: forward 920 us (1195).  One row: 7.1 us.
 //
 // Values that are not finite: a product with a probability of zero is still a NaN
 // on the tensor cores.  Where a tile has masked places the operand along the
@@ -57,7 +57,7 @@ struct AttnParams {
   const int32_t* cu;       // [B + 1]
   int B, T, Hq, Hkv, D;
   float scale, scale2;     // scale, scale * log2 e
-  int pair_rows;           // forward: the two tiles of a CTA are rows of one head (else two heads of one group)
+  int mode;                // forward: what an item's tiles of 128 rows are (kTwoHeads, kTwoTiles, kOneTile)
   int tiles;               // tiles along the rows
   int split;               // dk, dv: CTAs that share a group's heads
   Heads q, o, d0, d1;      // forward: q, out, v; gradients: dq or dk, dv
@@ -406,7 +406,7 @@ __device__ __forceinline__ void exchange(uint4& first, uint4& second) {
 // ---------------------------------------------------------------- forward
 // A CTA has two tiles of 128 query rows, each with four warps, and one stream of key
 // and value tiles for both: two heads of a group on the same rows, or (groups of an
-// odd size) 256 rows of one head.  The CTAs stay and take such items one after the other: one's outputs are written
+// odd size) 256 rows of one head (or one tile, where there are few).  The CTAs stay and take such items one after the other: one's outputs are written
 // while the next one's first products run.  (A CTA for each lost 14 thousand cycles an item before its first key
 // tile and after its last, of 2800 a key tile; this one 9.)  The tensor cores alternate between them: while one
 // tile's scores are exponentiated, the other's products run.  TMEM: buffers of scores of
@@ -424,7 +424,9 @@ __device__ __forceinline__ void exchange(uint4& first, uint4& second) {
 //
 // A barrier that is waited for by parity has to be seen before its next phase ends.  With three buffers a tile's next
 // probabilities can be there before the last ones' arrival has been looked at, so their barriers are two, in turns.
-struct FwdItem {                           // two tiles of query rows
+// The tiles of an item: two heads of a group on the same rows, 256 rows of one head, or 128 of one.
+constexpr int kTwoHeads = 0, kTwoTiles = 1, kOneTile = 2;
+struct FwdItem {
   RowMap map;
   int item;                                // -1: no more
   int q0, top, kv;
@@ -447,9 +449,9 @@ constexpr int kFwdStaging = kFwdArith / 32 * 4096;       // 32 rows of 64 column
 
 // Item i of the grid: the last tiles first, they have the longest rows of keys.
 __device__ __forceinline__ void fwd_place(const AttnParams& p, int i, int& q0, int& first_head) {
-  const int per = p.pair_rows ? p.Hq : p.Hq / 2;
-  q0 = (p.tiles - 1 - i / per) * (p.pair_rows ? 2 * kRows : kRows);
-  first_head = i % per * (p.pair_rows ? 1 : 2);
+  const int per = p.mode == kTwoHeads ? p.Hq / 2 : p.Hq;
+  q0 = (p.tiles - 1 - i / per) * (p.mode == kTwoTiles ? 2 * kRows : kRows);
+  first_head = i % per * (p.mode == kTwoHeads ? 2 : 1);
 }
 
 template <int DP>
@@ -504,12 +506,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   pdl_wait();
 
   // The first queries, and where both tiles have the same rows the first keys, do not wait for the sequences' boundaries.
-  const bool early = !p.pair_rows;
+  const bool early = p.mode != kTwoTiles;
+  const int filled_by = p.mode == kOneTile ? 1 : 2;           // tiles of queries
   if (warp == kFwdLoadWarp && lane == 0 && early) {
     int q0, h;
     fwd_place(p, blockIdx.x, q0, h);
-    mbar_arrive_expect_tx(&bk.q_full, 2 * C::kBytes);
-    for (int u = 0; u < 2; ++u) load_tile<DP>(q_smem + u * C::kBytes, &tmQ, &bk.q_full, h + u, q0);
+    mbar_arrive_expect_tx(&bk.q_full, filled_by * C::kBytes);
+    for (int u = 0; u < filled_by; ++u) load_tile<DP>(q_smem + u * C::kBytes, &tmQ, &bk.q_full, h + u, q0);
     for (int s = 0; s < 2; ++s) {
       mbar_arrive_expect_tx(&bk.full[s], C::kBytes);
       load_tile<DP>(ring + s * C::kBytes, s ? &tmV : &tmK, &bk.full[s], h / (p.Hq / p.Hkv), q0);
@@ -521,8 +524,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     FwdItem& m = bk.item[it & 1];
     int q0, h;
     fwd_place(p, item, q0, h);
-    for (int r = it > 0 ? lane : 2 * kRows; r < 2 * kRows; r += 32) {
-      const int row = q0 + (p.pair_rows ? r : r & (kRows - 1)), head = h + (p.pair_rows ? 0 : r / kRows);
+    for (int r = it > 0 ? lane : 2 * kRows; r < filled_by * kRows; r += 32) {
+      const int row = q0 + (p.mode == kTwoTiles ? r : r & (kRows - 1)), head = h + (p.mode == kTwoTiles ? 0 : r / kRows);
       if (row < p.T) {
         const __nv_bfloat16* q = p.q.p + row * p.q.token + head * p.q.head;
         prefetch_l2(q);
@@ -532,13 +535,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     find_map<2 * kRows>(p, q0, mine, first_row, last_row, &m.map);
     if (lane == 0) {
       // key tile i: rows [top - 128 (i + 1), top - 128 i); query tile u meets tiles [from[u], to[u])
-      const int top = q0 + (p.pair_rows ? 2 * kRows : kRows);
+      const int top = q0 + (p.mode == kTwoTiles ? 2 * kRows : kRows);
       for (int u = 0; u < 2; ++u) {
-        const int base = q0 + (p.pair_rows ? kRows * u : 0), a = max(base, first_row), b = min(base + kRows, last_row);
+        const int base = q0 + (p.mode == kTwoTiles ? kRows * u : 0), a = max(base, first_row), b = min(base + kRows, last_row);
         m.base[u] = base;
-        m.head[u] = h + (p.pair_rows ? 0 : u);
-        m.from[u] = p.pair_rows ? 1 - u : 0;
-        m.to[u] = m.from[u] + (a < b ? (base + kRows - start_of(&m.map, q0, a) + kRows - 1) / kRows : 0);
+        m.head[u] = h + (p.mode == kTwoHeads ? u : 0);
+        m.from[u] = p.mode == kTwoTiles ? 1 - u : 0;
+        m.to[u] = m.from[u] + (a < b && u < filled_by ? (base + kRows - start_of(&m.map, q0, a) + kRows - 1) / kRows : 0);
       }
       const bool on0 = m.to[0] > m.from[0], on1 = m.to[1] > m.from[1];
       m.ib = on1 ? m.from[1] : m.from[0];
@@ -575,7 +578,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
    fewer_registers<kFwdOtherRegs>();
    if (warp == kFwdItemWarp) {
     // ------------------------------------------------ the items
-    const int items = p.tiles * (p.pair_rows ? p.Hq : p.Hq / 2), grid = gridDim.x;
+    const int items = p.tiles * (p.mode == kTwoHeads ? p.Hq / 2 : p.Hq), grid = gridDim.x;
     int next = blockIdx.x;
     for (int it = 0;; ++it) {
       if (it >= 2) warp_wait(&bk.item_empty[it & 1], ((it >> 1) & 1) ^ 1u, abort, lim);
@@ -612,8 +615,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           const bool here = early && it == 0;
           if (!here) {
             if (filled > 0 && !mbar_wait(&bk.q_empty, (filled - 1) & 1, abort, lim)) break;
-            mbar_arrive_expect_tx(&bk.q_full, 2 * C::kBytes);
-            for (int u = 0; u < 2; ++u)
+            mbar_arrive_expect_tx(&bk.q_full, filled_by * C::kBytes);
+            for (int u = 0; u < filled_by; ++u)
               load_tile<DP>(q_smem + u * C::kBytes, &tmQ, &bk.q_full, m.head[u], m.base[u]);
             got.note(8, filled & 1);
           }
@@ -1706,6 +1709,14 @@ int group_split(const AttnParams& p) {
   return best;
 }
 
+// The tiles of an item of the forward: two, which share the keys' loads and keep the tensor cores busy in turn; but one
+// where an SM would have none otherwise.  (Two, one: 1003 rows, 6/2 heads of 80: 17.5, 14.7 us; 2400 rows, 8/1 of 64: 25.0,
+// 20.6; 4000 rows, 4 of 128: 52, 43; one row, 32/8 of 128: 6.9, 6.3.)
+int forward_mode(const AttnParams& p) {
+  if (static_cast<long long>(p.tiles) * p.Hq <= num_sms()) return kOneTile;
+  return p.Hq / p.Hkv % 2 == 0 ? kTwoHeads : kTwoTiles;
+}
+
 // How a tensor's strides count where a dimension has one element: as if it were dense.
 Heads heads_of(const moe_heads* t, int T, int heads, int D) {
   Heads h;
@@ -1759,7 +1770,7 @@ template <int DP>
 cudaError_t forward(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const AttnParams& p,
                     cudaStream_t st) {
   static std::atomic<bool> attr_set[kMaxDevices];
-  const int items = p.tiles * (p.pair_rows ? p.Hq : p.Hq / 2), sms = num_sms();
+  const int items = p.tiles * (p.mode == kTwoHeads ? p.Hq / 2 : p.Hq), sms = num_sms();
   return launch_big(attention_fwd_kernel<DP>, attr_set, items < sms ? items : sms, kFwdThreads, smem_of(fwd_smem<DP>()), st, 1, tq, tk, tv, p);
 }
 template <int DP>
@@ -1804,8 +1815,8 @@ moe_status moe_attention_forward(const moe_attention_config* cfg, const moe_head
   if (!device_is_gb300()) return MOE_ERR_UNSUPPORTED;
   if (none) return MOE_OK;
   AttnParams p = params_of(cfg, cu_seqlens, ws);
-  p.pair_rows = Hq / Hkv % 2;
-  if (p.pair_rows) p.tiles = (T + 2 * kRows - 1) / (2 * kRows);
+  p.mode = forward_mode(p);
+  if (p.mode == kTwoTiles) p.tiles = (p.tiles + 1) / 2;
   p.o = heads_of(out, T, Hq, D);
   p.d0 = heads_of(v, T, Hkv, D);
   p.q = heads_of(q, T, Hq, D);

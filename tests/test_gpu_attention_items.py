@@ -111,3 +111,28 @@ def test_many_bad_boundaries_are_reported(lib, seed):
     for w in [whole] + [w for w, _ in grads]:
         assert (w[:guard] == 5).all() and (w[-guard:] == 5).all()
     assert (lse[0] == 5).all() and (lse[-1] == 5).all()
+
+
+@pytest.mark.parametrize("D", [8, 64, 80, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(200, 100), (160, 20), (180, 60), (170, 34)])
+@pytest.mark.parametrize("lengths,first,tail", [([1], 0, 0), ([129, 0, 130, 1], 2, 5), ([5, 120, 3, 128], 0, 40)])
+def test_two_tiles_an_item(lib, lengths, first, tail, Hq, Hkv, D):
+    """Heads enough that items have two tiles of rows: of two heads, or (groups of odd sizes) of 256 rows."""
+    c = _case(lengths, Hq, Hkv, D, seed=Hq + D, first=first, tail=tail)
+    _check(_run(*c), *c)
+
+
+def test_values_that_are_not_finite_with_two_tiles_an_item(lib):
+    """Row 200 of [150, 290) and 301 of [290, 400): only what sees them may differ from the call without them."""
+    for Hq, Hkv in ((200, 100), (180, 60)):
+        cu, T, q, k, v, do = c = _case([150, 140, 110], Hq, Hkv, 64, seed=Hq)
+        clean = _run(*c)
+        for t in (k, v):
+            dirty = {"k": k.clone(), "v": v.clone()}
+            name = "k" if t is k else "v"
+            dirty[name][200, :, ::3], dirty[name][301, :, 1::3] = float("nan"), float("inf")
+            got = _run(cu, T, q, dirty["k"], dirty["v"], do)
+            keep = torch.ones(T, dtype=torch.bool)
+            keep[200:290] = keep[301:400] = False
+            assert torch.equal(got["out"][keep], clean["out"][keep]) and torch.isfinite(got["out"][keep]).all()
+            assert not torch.isfinite(got["out"][250].float()).all() and not torch.isfinite(got["out"][350].float()).all()
