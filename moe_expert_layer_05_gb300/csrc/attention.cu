@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       mbar_init(&bk.item_full[u], 1);
       mbar_init(&bk.item_empty[u], 1 + (L == 2 ? 1 : 2) + kFwdArith / 32);      // loads, products, arithmetic
     }
-    for (int s = 0; s < 3; ++s) mbar_init(&bk.free[s], 1);
+    for (int s = 0; s < 3; ++s) mbar_init(&bk.free[s], 2);      // the scores have been issued, the sums are done
     mbar_init(&bk.ending, 1);
     mbar_init(&bk.drain, L == 2 ? 1 : 2);
     bk.abort_flag = 0;
@@ -719,6 +719,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (round > 0) warp_wait(&bk.free[b], (round - 1) & 1, abort, lim);
             tc_fence_after_sync();
             scores(u, i, 128 * b);
+            // (Without it the warp of the sums, which has nothing to wait for where a tile does not meet the keys, could end
+            // a second phase before this one has looked at the first.)
+            if (lane == 0) mbar_arrive(&bk.free[b]);
+            __syncwarp();
             if (++b == L) {
               b = 0;
               ++round;
