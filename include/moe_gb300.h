@@ -660,7 +660,8 @@ size_t moe_balance_loss_workspace_bytes(int32_t T, int32_t E);
  * logits [T,E] fp32 and topk_idx [T,k] int32 as moe_router_topk writes them; tokens [T] int32 or NULL: a token
  * below 0 is padding and does not count, whatever its row of logits and choices holds.
  * Outputs: loss [1] fp32, counts [E] int32, slope [E] fp32 (for the backward pass).  A logit of
- * -infinity has probability 0 (a row of nothing else: all 0).  A choice outside [0,E) is
+ * -infinity has probability 0 (a row of nothing else: all 0); a NaN makes the loss and its own row's gradient
+ * NaN.  A choice outside [0,E) is
  * not counted and sets MOE_ERR_BAD_INDEX on the device.  1 <= k <= 32, k <= E.  loss, counts
  * and slope need an alignment of 4 bytes only (rows of a table of layers).  Sums in a
  * fixed order. */

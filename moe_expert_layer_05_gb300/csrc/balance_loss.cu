@@ -64,13 +64,15 @@ __device__ __forceinline__ float exp_of(float x) { return ex2(x * 1.442695040888
 __device__ __forceinline__ float inverse(float x) { return __fdividef(1.f, x); }
 
 // x[i]: this lane's logits in, probabilities out (experts past E: -infinity in).
-// rest[i] (sigmoid): 1 - sigmoid.  A row of -infinity alone has no probabilities: zeros.
+// rest[i] (sigmoid): 1 - sigmoid.  A row of -infinity alone has no probabilities: zeros.  The maximum knows nothing of
+// NaN, so it is the sum that tells such a row (0) from one with a NaN (NaN throughout).
 template <int G, int NV>
 __device__ __forceinline__ void probabilities(float (&x)[NV], float (&rest)[NV], bool sigmoid) {
   float m = x[0];
   #pragma unroll
   for (int i = 1; i < NV; ++i) m = fmaxf(m, x[i]);
   m = row_max<G>(m);
+  if (m == -INFINITY) m = 0.f;
   float sum = 0.f;
   if (!sigmoid) {
     #pragma unroll
@@ -101,9 +103,9 @@ __device__ __forceinline__ void probabilities(float (&x)[NV], float (&rest)[NV],
     }
   }
   sum = row_sum<G>(sum);
-  const float inv = 1.f / sum;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   #pragma unroll
-  for (int i = 0; i < NV; ++i) x[i] = m == -INFINITY ? 0.f : x[i] * inv;
+  for (int i = 0; i < NV; ++i) x[i] *= inv;
 }
 
 // Expert of a lane's value i.

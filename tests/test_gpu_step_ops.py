@@ -204,6 +204,28 @@ def test_balance_masked_experts_and_extreme_logits(lib, sigmoid):
     _balance_check(logits, topk, None, sigmoid)
 
 
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("E", [5, 8, 24, 64, 100, 129, 160, 256])
+def test_balance_rows_of_nan_are_seen_in_the_loss(lib, E, sigmoid):
+    """A token whose activations are NaN has a row of nothing else, or of NaN beside experts that are out of use."""
+    rng = np.random.default_rng(E)
+    logits = rng.standard_normal((70, E)).astype(np.float32)
+    topk = np.argsort(-logits, 1)[:, :2].astype(np.int32).copy()
+    for row, lost in ((3, slice(None)), (40, slice(0, E // 2)), (69, slice(E - 1, E))):
+        x = logits.copy()
+        x[row] = -np.inf
+        x[row, lost] = np.nan
+        loss, counts, slope, d, ws = _balance_run(x, topk, None, sigmoid, dloss=1.0)
+        with np.errstate(invalid="ignore"):
+            ref = M.balance_loss(x.astype(np.float64), topk, 2, None, sigmoid)
+        assert math.isnan(ref["loss"]) and math.isnan(float(loss)) and api.moe_read_device_status(ws) == 0
+        np.testing.assert_array_equal(counts.cpu().numpy(), ref["counts"])
+        d, others = f64(d), np.arange(70) != row
+        assert np.isnan(d[row]).all()
+        rel = (2 * np.abs(logits).max() + E / 8 + 24) * U
+        _within(d[others], ref["grad"][others], ((3 * rel + 8 * U) * ref["grad_mag"] + 1e-37)[others], "dlogits")
+
+
 def test_balance_of_an_even_router_is_one(lib):
     E, k = 16, 4
     logits = np.zeros((32, E), np.float32)
