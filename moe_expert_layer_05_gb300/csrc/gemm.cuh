@@ -509,12 +509,13 @@ __device__ __forceinline__ void issue_loads(const CUtensorMap* tmA, const CUtens
   }
 }
 
+__device__ __forceinline__ void wait_ns(unsigned long long ns) {
+  bounded_wait<1>([] { return false; }, [] { return false; }, [] { return global_timer_ns(); }, ns);
+}
+
 __device__ __forceinline__ bool mbar_wait_drain(uint64_t* bar, uint32_t parity) {
-  const unsigned long long t0 = global_timer_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if (global_timer_ns() - t0 > kWaitLimitNs / 4) return false;
-  }
-  return true;
+  return bounded_wait<1>([&] { return mbar_try_wait(bar, parity); }, [] { return false; },
+                         [] { return global_timer_ns(); }, kWaitLimitNs / 4) == Waited::kDone;
 }
 
 template <class C>
@@ -2316,9 +2317,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (issued_mask & (1u << s)) mbar_wait_drain(&full_bar[s], (issued_parity >> s) & 1u);
         } else {
           // this CTA's loads complete on the peer's barriers: give them time to land
-          const unsigned long long t0 = global_timer_ns();
-          while (global_timer_ns() - t0 < 200000ull) {
-          }
+          wait_ns(200000ull);
         }
       }
     }
@@ -2453,9 +2452,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // loads that the odd CTA's producer had issued when another warp gave up: the
     // same time to land
     if (!leader && bk.abort_flag && threadIdx.x == 0) {
-      const unsigned long long t0 = global_timer_ns();
-      while (global_timer_ns() - t0 < 200000ull) {
-      }
+      wait_ns(200000ull);
     }
     __syncwarp();
   }

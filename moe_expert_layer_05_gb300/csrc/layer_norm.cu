@@ -364,10 +364,8 @@ __global__ void __launch_bounds__(512, 1) layer_norm_bwd_kernel(const uint4* __r
       const int rows = (T - t0 + step - 1) / step, stop = (s_stop[group] - t0 + step - 1) / step;
       const int started = min(rows, stop + stages);
       for (int k = max(started - stages, 0); k < started; ++k) {
-        const unsigned long long since = global_timer_ns();
-        while (!mbar_try_wait(&s_full[group][k % stages], k / stages & 1) &&
-               global_timer_ns() - since < kWaitLimitNs / 4) {
-        }
+        bounded_wait<1>([&] { return mbar_try_wait(&s_full[group][k % stages], k / stages & 1); }, [] { return false; },
+                        [] { return global_timer_ns(); }, kWaitLimitNs / 4);
       }
     }
     __syncthreads();

@@ -7,6 +7,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include "wait_clock.h"
+
 namespace moe {
 
 // Device status codes (same values as moe_status in the public header).
@@ -103,39 +105,50 @@ __device__ __forceinline__ bool mbar_try_wait_hint(uint64_t* bar, uint32_t parit
   return ok != 0;
 }
 
+// The same without suspending the thread.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred P;\n mbarrier.test_wait.parity.shared::cta.b64 P, [%1], %2;\n selp.b32 %0, 1, 0, P;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// A flag in shared memory, by its 32-bit address.
+__device__ __forceinline__ bool raised(const volatile int* flag) {
+  int v;
+  asm volatile("ld.volatile.shared.s32 %0, [%1];" : "=r"(v) : "r"(smem_u32(const_cast<const int*>(flag))) : "memory");
+  return v != 0;
+}
+
 // Limits below this (set for tests of the failure path) use the hinted test.
 constexpr unsigned long long kShortWaitNs = 1000000ull;
 
 // Wait until the phase with the given parity has completed.  Gives up when
-// *abort is raised by another warp or after limit_ns; then raises *abort
-// itself and returns false.
+// *abort (in shared memory) is raised by another warp or after limit_ns; then
+// raises *abort itself and returns false.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
                                           unsigned long long limit_ns = kWaitLimitNs) {
+  if (mbar_test_wait(bar, parity)) return true;
   if (limit_ns < kShortWaitNs) {
     // short limits (tests of the failure path): short suspensions, the clock
-    // read after every unsuccessful test
+    // read after every unsuccessful test, and believed
     const unsigned long long ts = global_timer_ns();
     for (;;) {
       if (mbar_try_wait_hint(bar, parity, 100u)) return true;
-      if (*abort) return false;
+      if (raised(abort)) return false;
       if (global_timer_ns() - ts > limit_ns) {
         *abort = 1;
         return false;
       }
     }
   }
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = global_timer_ns();
-  for (uint32_t n = 1;; ++n) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((n & 63u) == 0) {
-      if (*abort) return false;
-      if (global_timer_ns() - t0 > limit_ns) {
-        *abort = 1;
-        return false;
-      }
-    }
-  }
+  const Waited w = bounded_wait<64>([&] { return mbar_try_wait(bar, parity); }, [&] { return raised(abort); },
+                                    [] { return global_timer_ns(); }, limit_ns);
+  if (w == Waited::kOver) *abort = 1;
+  return w == Waited::kDone;
 }
 
 // ---------------------------------------------------------------- TMA
@@ -565,17 +578,10 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort,
                                                   unsigned long long limit_ns = kWaitLimitNs) {
   if (mbar_try_wait_cluster(bar, parity)) return true;
-  const unsigned long long t0 = global_timer_ns();
-  for (uint32_t n = 1;; ++n) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if ((n & 63u) == 0) {
-      if (*abort) return false;
-      if (global_timer_ns() - t0 > limit_ns) {
-        *abort = 1;
-        return false;
-      }
-    }
-  }
+  const Waited w = bounded_wait<64>([&] { return mbar_try_wait_cluster(bar, parity); }, [&] { return raised(abort); },
+                                    [] { return global_timer_ns(); }, limit_ns);
+  if (w == Waited::kOver) *abort = 1;
+  return w == Waited::kDone;
 }
 // Tiled load into this CTA's shared memory whose completion is counted on a
 // barrier that may sit in the peer CTA (bar_cluster_addr from mapa_shared).
