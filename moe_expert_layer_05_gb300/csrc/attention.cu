@@ -432,6 +432,7 @@ struct FwdItem {
   int q0, top, kv;
   int from[2], to[2], base[2], head[2], ib, n;
   int loaded;                              // key and value tiles in the ring: 2 n, or the first ones of an item without rows
+  int mixed;                               // 256 rows of one head: key tiles from here on are masked for one of its tiles
   int bad_lo, bad_hi;                      // key rows of tiles in which clean_tile found something
 };
 struct FwdBook {
@@ -547,6 +548,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       m.ib = on1 ? m.from[1] : m.from[0];
       m.n = (on0 || on1) ? max(m.to[0], m.to[1]) - m.ib : 0;
       m.loaded = m.n > 0 ? 2 * m.n : (early && it == 0 ? 2 : 0);
+      // (a boundary between a tile's rows masks their keys in front of it; the second tile's last one is the furthest)
+      m.mixed = p.mode == kTwoTiles && on1 ? (top - start_of(&m.map, q0, min(m.base[1] + kRows, last_row) - 1)) / kRows : INT_MAX;
       m.q0 = q0;
       m.top = top;
       m.kv = h / (p.Hq / p.Hkv);
@@ -653,6 +656,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const FwdItem& m = bk.item[it & 1];
       const int f0 = uniform(m.from[0]), f1 = uniform(m.from[1]), e0 = uniform(m.to[0]), e1 = uniform(m.to[1]);
       const int first = uniform(m.ib), n = uniform(m.n), loaded = uniform(m.loaded), last = first + n - 1;
+      const int mixed = uniform(m.mixed);
       __syncwarp();
       if (lane == 0) mbar_arrive(&bk.item_empty[it & 1]);
       auto full = [&](int s) { warp_wait(&bk.full[s % ST], (s / ST) & 1, abort, lim); };
@@ -680,10 +684,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (i >= f && i < e) {
           const int outs = u ? outs1 : outs0;
           if (i == f && outs > 0) warp_wait(&bk.o_empty[u], (outs - 1) & 1, abort, lim);
+          // Where the second tile of rows looks through the value tile (masked there, perhaps not here) the first one's product
+          // waits for it: what is not finite shall be there for both or for neither.  (The other way round the first tile's
+          // probabilities, which come after its own look, have been waited for.)
+          const int x1 = met1 + i - f1;
+          const bool both = p.mode == kTwoTiles && u == 0 && i >= f1 && i < e1 && (i == f0 || i >= mixed);
+          #pragma unroll 1
+          for (int w = both ? 1 : 0; w >= 0; --w) {
+            const int y = w ? x1 : x;
+            warp_wait(&bk.p_full[w ? 1 : u][y & 1][0], (y >> 1) & 1, abort, lim);
+          }
           // (the first half of the keys while the second is still exponentiated)
           #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            warp_wait(&bk.p_full[u][x & 1][half], (x >> 1) & 1, abort, lim);
+            if (half) warp_wait(&bk.p_full[u][x & 1][half], (x >> 1) & 1, abort, lim);
             tc_fence_after_sync();
             mma_sums<DP, 8>(leader, tmem + 128 * L + DP * u, tmem + buffer, v_desc + (s % ST) * (C::kBytes >> 4),
                             i > f || half, 4 * half, 4 * half + 4);
@@ -798,7 +812,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         clean_tile<DP>(ring + (at % ST) * C::kBytes, threadIdx.x & 127, 128, [&] {
           atomicMin(&m.bad_lo, k0);
           atomicMax(&m.bad_hi, k0 + kRows - 1);
-          __threadfence_block();                 // (the other tile of rows may find the zeros: it shall know)
+          __threadfence_block();                 // (the other tile of rows finds the zeros: it shall know)
         });
       }
       uint32_t w[32];
