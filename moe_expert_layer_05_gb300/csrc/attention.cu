@@ -370,15 +370,30 @@ __device__ __forceinline__ void store_cols(uint8_t* staging, __nv_bfloat16* out,
 __device__ __forceinline__ uint4* staged_word(uint8_t* staging, int r, int w) {
   return reinterpret_cast<uint4*>(staging) + r * 8 + (w ^ (r & 7));
 }
-__device__ __forceinline__ __nv_bfloat16* staged(uint8_t* staging, int r, int col) {
-  return reinterpret_cast<__nv_bfloat16*>(staged_word(staging, r, col >> 3)) + (col & 7);
-}
 __device__ __forceinline__ void put_cols(uint8_t* staging, int r, int col, const float (&v)[32]) {
   #pragma unroll
   for (int w = 0; w < 4; ++w)
     *staged_word(staging, r, col / 8 + w) =
         make_uint4(pack_bf16x2(v[8 * w], v[8 * w + 1]), pack_bf16x2(v[8 * w + 2], v[8 * w + 3]),
                    pack_bf16x2(v[8 * w + 4], v[8 * w + 5]), pack_bf16x2(v[8 * w + 6], v[8 * w + 7]));
+}
+// Eight columns of a row of values: what is not finite among them is added to the row's sums; true: these are all NaN.
+__device__ __forceinline__ bool give_back(uint4* sums, const uint4& v) {
+  const uint32_t y[4] = {v.x, v.y, v.z, v.w};
+  uint32_t* to = reinterpret_cast<uint32_t*>(sums);
+  uint32_t found = 0u, nan = ~0u;
+  #pragma unroll
+  for (int i = 0; i < 4; ++i) found |= __vcmpeq2(y[i] & 0x7f807f80u, 0x7f807f80u);
+  if (found == 0u) return false;
+  #pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t on = __vcmpeq2(y[i] & 0x7f807f80u, 0x7f807f80u);
+    const uint32_t add = (y[i] & on) | (0x80008000u & ~on);                 // (-0 changes nothing)
+    const __nv_bfloat162 r = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(to + i), *reinterpret_cast<const __nv_bfloat162*>(&add));
+    to[i] = *reinterpret_cast<const uint32_t*>(&r);
+    nan &= __vcmpgtu2(to[i] & 0x7fff7fffu, 0x7f807f80u);
+  }
+  return nan == ~0u;
 }
 // The first D columns of the rows that `rows` names.
 __device__ __forceinline__ void store_rows(uint8_t* staging, __nv_bfloat16* out, long long stride, uint32_t rows, int D) {
@@ -902,14 +917,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         put_cols(staging, lane, 32 * c, v);
       }
       if (valid) {
-        // what clean_tile took out, for the rows that see it
-        for (int j = max(key_lo, bad_lo); j <= min(key_hi, bad_hi); ++j) {
-          const __nv_bfloat16* src = p.d0.p + j * p.d0.token + kv * p.d0.head + col;
-          for (int c = 0; c < 64 && col + c < p.D; ++c) {
-            const float y = __bfloat162float(src[c]);
-            __nv_bfloat16* to = staged(staging, lane, c);
-            if (!isfinite(y)) *to = __float2bfloat16(__bfloat162float(*to) + y);
-          }
+        // what clean_tile took out, for the rows that see it; eight columns that are all NaN have seen enough
+        uint32_t words = (1u << min((p.D - col) / 8, 8)) - 1u;
+        for (int j = max(key_lo, bad_lo); words != 0 && j <= min(key_hi, bad_hi); ++j) {
+          const uint4* src = reinterpret_cast<const uint4*>(p.d0.p + j * p.d0.token + kv * p.d0.head + col);
+          for (int w = 0; w < 8; ++w)
+            if ((words >> w & 1u) && give_back(staged_word(staging, lane, w), src[w])) words &= ~(1u << w);
         }
       }
       __syncwarp();

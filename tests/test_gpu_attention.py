@@ -211,6 +211,37 @@ def test_out_has_the_column_that_is_not_finite(lib):
     assert (x[170:200, :, 5] == np.inf).all()
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(2, 1, 64), (2, 2, 80), (300, 100, 64)])
+def test_every_column_that_is_not_finite_is_given_back(lib, Hq, Hkv, D):
+    """Infinities of both signs and NaN in the values, each in columns of its own, in masked tiles and others."""
+    cu, T, q, k, v, do = _case([3, 497], Hq, Hkv, D, seed=27, std=0.5)
+    want = np.zeros((T, D), np.float32)
+    for row, col, y in ((0, 1, np.inf), (2, 2, -np.inf), (5, 3, np.inf), (5, 63, np.nan), (130, 9, -np.inf), (300, 9, np.inf),
+                        (300, 8, -np.inf), (301, 10, np.nan), (400, 10, np.inf), (450, 16, np.nan), (499, D - 1, np.inf)):
+        v[row, :, col] = y
+        with np.errstate(invalid="ignore"):
+            want[row:3 if row < 3 else T, col] += y
+    x = _run(cu, T, q, k, v, do)["out"].float().cpu().numpy()
+    for h in range(Hq):
+        y = np.where(np.isfinite(x[:, h]), 0.0, x[:, h])
+        assert np.array_equal(y, want, equal_nan=True), h
+
+
+def test_values_of_nan_through_a_long_sequence(lib):
+    """Every value NaN, in a sequence of 2^19 rows that begins inside a tile: each row gives up looking at the first key
+    that it sees, and no wait of the launch runs into its limit."""
+    T = 2 ** 19
+    gen = torch.Generator(DEV).manual_seed(2)
+    q, k = (torch.randn(T, 1, 64, device=DEV, generator=gen).to(torch.bfloat16) for _ in range(2))
+    v = torch.full_like(k, float("nan"))
+    out, lse, ws = torch.zeros_like(q), torch.zeros(1, T, device=DEV), _ws(T, 1, 1, 64)
+    cu = torch.tensor([5, T - 100], dtype=torch.int32, device=DEV)
+    api.moe_attention_forward(q, k, v, cu, out, lse, ws)
+    assert api.moe_read_device_status(ws) == 0
+    assert torch.isnan(out[5:-100]).all() and not out[:5].any() and not out[-100:].any()
+    assert torch.isfinite(lse[:, 5:-100]).all()
+
+
 # ---------------------------------------------------------------- boundaries
 @pytest.mark.parametrize("cu", [[0, 90, 60, 200], [-5, 100, 200], [0, 100, 900], [0, 2 ** 31 - 1, 200]])
 def test_bad_boundaries_are_reported(lib, cu):
