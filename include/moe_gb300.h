@@ -699,8 +699,9 @@ moe_status moe_grad_norm(const moe_tensor* grads, int32_t n, float* norm, void* 
 /* out = g * min(1, limit / (norm[0] + 1e-6)), each value rounded once.  outs: as many
  * tensors of the same sizes and types, or NULL: in place, and nothing is written where the
  * factor is 1.  What is written overlaps nothing else of the call: no gradient and no other output
- * (MOE_ERR_INVALID_ARG); the same gradient twice in place would be scaled twice.  limit >= 0.  With an infinite norm the factor is 0
- * (infinite values become NaN), with a NaN norm everything becomes NaN. */
+ * (MOE_ERR_INVALID_ARG); the same gradient twice in place would be scaled twice.  limit >= 0; infinity: the factor is 1,
+ * with an infinite norm, too.  With an infinite norm and a finite limit the factor is 0 (infinite values become NaN),
+ * with a NaN norm everything becomes NaN. */
 moe_status moe_grad_clip(const moe_tensor* grads, const moe_tensor* outs, int32_t n, const float* norm, float limit,
                          void* stream);
 

@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kThreads) grad_clip_kernel(const __grid_consta
                                                              const float* __restrict__ norm, float limit, int in_place) {
   pdl_entry();
   float c = limit / (norm[0] + 1e-6f);
-  if (c >= 1.f) {
+  if (c >= 1.f || (limit == INFINITY && norm[0] == INFINITY)) {      // (infinity / infinity: no limit is none)
     if (in_place) return;
     c = 1.f;
   }

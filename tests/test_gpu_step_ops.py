@@ -344,6 +344,24 @@ def test_no_gradients_zeros_and_not_finite(lib):
         assert torch.isnan(g[1][7]) and bool(((g[0] == 0) if math.isinf(bad) else torch.isnan(g[0])).all())
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_no_limit_leaves_every_gradient(lib, in_place):
+    """An infinite limit: the factor is 1 with a finite norm, with one past fp32's range and with an infinite value."""
+    rng = np.random.default_rng(14)
+    norm = torch.zeros(1, device=DEV)
+    for scale, bad in ((1.0, None), (3e37, None), (1.0, math.inf), (1.0, math.nan)):
+        grads = _grads(rng, [5001, 64, 9], scale)
+        if bad is not None:
+            grads[1][5] = bad
+        d = [g.to(DEV) for g in grads]
+        api.moe_grad_norm(d, norm, _ws(api.moe_grad_norm_workspace_bytes(3)))
+        assert math.isfinite(float(norm)) == (scale == 1.0 and bad is None)
+        outs = d if in_place else [torch.full_like(g, 9.0) for g in d]
+        api.moe_grad_clip(d, norm, math.inf, outs=None if in_place else outs)
+        for got, g in zip(outs, grads):
+            assert torch.isnan(got).all() if bad is math.nan else torch.equal(got.cpu(), g)
+
+
 def test_clip_in_a_graph_that_is_replayed(lib):
     rng = np.random.default_rng(4)
     g = [t.to(DEV) for t in _grads(rng, [5000, 333, 70000])]
