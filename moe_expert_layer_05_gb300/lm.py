@@ -125,7 +125,9 @@ class MoEModel:
         self.dgate = torch.empty(T, k, dtype=torch.float32, device=device)
         if heads:
             self.d_out, self.dqkv = torch.zeros_like(self.attentions[0].out), torch.zeros_like(self.attentions[0].qkv)
-            self.cu_seqlens, self.positions = self._one_sequence(device)
+            self.one_sequence = (torch.tensor([0, T], dtype=torch.int32, device=device),
+                                 torch.arange(T, dtype=torch.int32, device=device))
+            self.cu_seqlens, self.positions = self.one_sequence
         if balance:
             self.balance_loss, self.slope = torch.zeros(layers, 1, device=device), torch.zeros(layers, E, device=device)
             self.counts = torch.zeros(layers, E, dtype=torch.int32, device=device)      # choices of each expert
@@ -141,10 +143,6 @@ class MoEModel:
     @property
     def head(self) -> torch.Tensor:
         return self.params["table" if self.tied else "head"]
-
-    def _one_sequence(self, device):
-        return (torch.tensor([0, self.T], dtype=torch.int32, device=device),
-                torch.arange(self.T, dtype=torch.int32, device=device))
 
     def _norm(self, i: int, x, residual=None) -> None:
         p = self.params
@@ -164,7 +162,7 @@ class MoEModel:
         """
         if self.heads:
             if cu_seqlens is None:
-                self.cu_seqlens, self.positions = self._one_sequence(tokens.device)
+                self.cu_seqlens, self.positions = self.one_sequence
             else:
                 at = torch.arange(self.T, dtype=torch.int32, device=tokens.device)
                 first = cu_seqlens[torch.searchsorted(cu_seqlens, at, right=True).sub_(1).clamp_(min=0)]

@@ -108,6 +108,28 @@ def test_step_twice_gives_the_same_bits(lib):
     assert all(torch.equal(first[n], g) for n, g in m.grads.items())
 
 
+def test_a_step_of_one_sequence_is_captured(lib):
+    """Without boundaries (one sequence of all tokens) a step copies nothing from the host: it can be captured, and the
+    graph replayed on other tokens."""
+    m = lm.MoEModel(300, 128, 8, 2, 128, 777, layers=1, heads=4, kv_heads=2, balance=0.01)
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    tokens, labels = (torch.randint(0, 777, (300,), generator=gen, device="cuda", dtype=torch.int32) for _ in range(2))
+    others = [torch.randint(0, 777, (300,), generator=gen, device="cuda", dtype=torch.int32) for _ in range(2)]
+    m.step(tokens, labels, torch.tensor([0, 50, 300], dtype=torch.int32, device="cuda"))
+    want = float(m.step(*others))
+    grads = {n: g.clone() for n, g in m.grads.items()}
+    m.step(tokens, labels)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loss = m.step(tokens, labels)
+    tokens.copy_(others[0])
+    labels.copy_(others[1])
+    graph.replay()
+    assert float(loss) == want and m.status() == 0
+    assert all(torch.equal(grads[n], g) for n, g in m.grads.items())
+
+
 def test_clip_scales_every_gradient(lib):
     m = lm.MoEModel(130, 128, 4, 2, 128, 301, layers=1, heads=2, balance=0.01)
     gen = torch.Generator(device="cuda").manual_seed(6)
