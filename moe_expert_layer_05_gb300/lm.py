@@ -160,6 +160,12 @@ class MoEModel:
         cu_seqlens (models with heads): the packed sequences' first rows and the last one's end, int32; one
         sequence of all tokens where it is not given.
         """
+        if cu_seqlens is not None:
+            if not self.heads:
+                raise ValueError("cu_seqlens: this model has no attention, its tokens do not know of sequences")
+            if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or len(cu_seqlens) == 0:
+                raise ValueError(f"cu_seqlens: expected the sequences' first rows and the last one's end, int32, got "
+                                 f"{tuple(cu_seqlens.shape)} of {cu_seqlens.dtype}")
         if self.heads:
             if cu_seqlens is None:
                 self.cu_seqlens, self.positions = self.one_sequence

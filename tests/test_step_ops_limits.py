@@ -3,7 +3,7 @@ gradients that would be scaled twice.  No GPU needed."""
 import pytest
 import torch
 
-from moe_expert_layer_05_gb300 import api
+from moe_expert_layer_05_gb300 import api, lm
 from test_step_ops_abi import bwd, config, fwd, tensors
 
 NO_GPU = not torch.cuda.is_available()
@@ -53,3 +53,15 @@ def test_what_is_scaled_twice_is_refused(n):
         empty = list(grads)
         empty[0] = (grads[1][0], 0, 1)                          # nothing of it
         assert clip(empty) == taken
+
+
+@pytest.mark.parametrize("heads,cu", [(0, torch.tensor([0, 9], dtype=torch.int32)), (2, torch.zeros(0, dtype=torch.int32)),
+                                      (2, torch.tensor([0, 9])), (2, torch.tensor([[0, 9]], dtype=torch.int32))])
+def test_a_model_refuses_boundaries_that_it_cannot_use(heads, cu):
+    """Before anything is launched: none at all (an index into an empty tensor fails on the device), another type, or a
+    model without attention, which would have left them unread."""
+    m = lm.MoEModel.__new__(lm.MoEModel)
+    m.T, m.heads = 9, heads
+    tokens = torch.zeros(9, dtype=torch.int32)
+    with pytest.raises(ValueError, match="cu_seqlens"):
+        m.forward(tokens, tokens, cu)
