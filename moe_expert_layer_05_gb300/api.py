@@ -489,6 +489,8 @@ def _attention(q, k, cu_seqlens, scale):
         raise MoeError(-1, "q, k, cu_seqlens")
     if scale is None:
         scale = D ** -0.5 if D > 0 else 1.0
+    elif not abs(scale) < 2.0 ** 127:         # (struct has no fp32 form of more, the call none of 2^65)
+        raise MoeError(-1, "scale")
     return struct.pack("5if", T, n, Hq, Hkv, D, scale), n, (T, Hq, D), (T, Hkv, D)
 
 

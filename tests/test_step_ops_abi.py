@@ -332,3 +332,13 @@ def test_gradient_lists_are_checked(calls):
     with pytest.raises(ValueError):
         api.moe_grad_norm([FakeTensor(3, dtype=torch.float16)], norm, ws)
     assert len(calls) == 3
+
+
+@pytest.mark.parametrize("scale", [1e39, -1e300, math.inf, math.nan, 10 ** 40])
+def test_scales_without_an_fp32_form_are_refused_as_others_are(calls, scale):
+    made = _calls()
+    for call in (api.moe_attention_forward, api.moe_attention_backward):
+        with pytest.raises(api.MoeError) as e:
+            call(*made[call], scale=scale)
+        assert e.value.code == -1
+    assert calls == []
