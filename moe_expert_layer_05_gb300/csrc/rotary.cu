@@ -204,7 +204,8 @@ moe_status moe_rotary_frequencies(int32_t R, double base, int32_t scaling, doubl
     const double f = pow(base, -2.0 * i / R);
     double slowed = scaling == MOE_ROTARY_LINEAR ? 1.0 : 0.0;       // the part of it divided by the factor
     if (scaling == MOE_ROTARY_BY_PARTS) {
-      slowed = (i - lo) / (hi - lo > 0.001 ? hi - lo : 0.001);
+      // (hi <= 0: the first pair, the fastest, turns no more than `slow` times)
+      slowed = hi <= 0.0 ? 1.0 : (i - lo) / (hi - lo > 0.001 ? hi - lo : 0.001);
       slowed = slowed < 0.0 ? 0.0 : slowed > 1.0 ? 1.0 : slowed;
     }
     freq[i] = scaling == MOE_ROTARY_PLAIN ? f : f * (1.0 - slowed) + f / factor * slowed;

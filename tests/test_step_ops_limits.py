@@ -1,5 +1,8 @@
 """Calls that the step operators refuse at the edges of their ranges: scales whose scores leave fp32's range,
 gradients that would be scaled twice.  No GPU needed."""
+import math
+
+import numpy as np
 import pytest
 import torch
 
@@ -65,3 +68,37 @@ def test_a_model_refuses_boundaries_that_it_cannot_use(heads, cu):
     tokens = torch.zeros(9, dtype=torch.int32)
     with pytest.raises(ValueError, match="cu_seqlens"):
         m.forward(tokens, tokens, cu)
+
+
+# ---------------------------------------------------------------- rotary frequencies by parts
+def _by_parts(R, base, factor, length, fast=32.0, slow=1.0):
+    """The ramp over the pairs' indices, from the last whole pair that turns `fast` times to the first that turns `slow` times."""
+    freq = base ** (-np.arange(0, R, 2) / R)
+
+    def pair(turns):                                   # length base^(-2 i / R) = 2 pi turns
+        return R / 2 * math.log(length / (2 * math.pi * turns)) / math.log(base)
+
+    lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), R - 1)
+    slowed = np.clip((np.arange(R // 2) - lo) / max(hi - lo, 1e-3), 0.0, 1.0)
+    return freq * (1 - slowed) + freq / factor * slowed, slowed
+
+
+@pytest.mark.parametrize("R,base,factor,length,fast,slow", [
+    (64, 10000.0, 8.0, 4096, 32.0, 1.0), (128, 500000.0, 32.0, 8192, 32.0, 1.0), (16, 10000.0, 4.0, 512, 16.0, 2.0),
+    (512, 1e6, 1.0, 32768, 32.0, 1.0), (48, 10000.0, 40.0, 100, 32.0, 1.0), (64, 10.0, 2.0, 4096, 32.0, 1.0),
+    (64, 10000.0, 8.0, 4096, 7.3, 7.3)])
+def test_the_ramp_between_the_parts(R, base, factor, length, fast, slow):
+    freq, scale = api.moe_rotary_frequencies(R, base, "by_parts", factor, length, fast, slow, device="cpu")
+    want, slowed = _by_parts(R, base, factor, length, fast, slow)
+    assert ((slowed > 0) & (slowed < 1)).any() or R == 64 and (base == 10.0 or fast == slow)
+    # pow and log to a few units of fp64 each, the ramp's ends whole numbers
+    np.testing.assert_allclose(freq.numpy(), want, rtol=1e-13)
+    assert abs(scale - (0.1 * math.log(factor) + 1)) <= 2.0 ** -23
+
+
+@pytest.mark.parametrize("length,slow", [(1, 1.0), (4, 1.0), (6, 1.0), (100, 16.0), (4096, 1e6)])
+def test_pairs_that_all_turn_less_than_the_slow_ones_are_all_slowed(length, slow):
+    """The first pair turns length / (2 pi) times, fewer than `slow`: it is divided by the factor as the others are."""
+    assert length / (2 * math.pi) < slow
+    freq, _ = api.moe_rotary_frequencies(64, 10000.0, "by_parts", 8.0, length, max(slow, 32.0), slow, device="cpu")
+    np.testing.assert_allclose(freq.numpy(), 10000.0 ** (-np.arange(0, 64, 2) / 64) / 8, rtol=1e-13)
