@@ -37,7 +37,7 @@ struct BalanceParams {
   const int32_t* topk;       // [T, k]
   const int32_t* tokens;     // [T] or nullptr
   int T, E, k, score;
-  uint4* part;               // [clusters][part_words(E)]
+  uint4* part;               // [blocks][part_words(E)]
   float* loss;
   int32_t* counts;
   float* slope;              // [E]

@@ -286,16 +286,6 @@ __device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
-// The same with A in TMEM: lane = row, each 32-bit column two consecutive values along K.
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred P;\n setp.ne.b32 P, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, P;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // D[tmem] (+)= (A * 2^sfa) * (B * 2^sfb)^T with E4M3 A and B and one E8M0
 // scale per 32 elements along K (MXFP8); K = 32 per instruction.  The scale
 // bytes come from TMEM; which byte of each 32-bit cell is used is part of idesc.
@@ -321,10 +311,11 @@ __device__ __forceinline__ void mma_nvf4_ss(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
-// The same two, and the commit, for a warp that runs converged: every lane calls with the same
-// operands and the lane whose `leader` is set issues.  Without a branch around them the operands stay
-// in uniform registers, which is where these instructions take them from; behind `if (lane == 0)` each
-// one is moved there first, some 100 cycles an MMA against the 64 that a 128 x 128 x 16 product runs.
+// The bf16 product, the same with A in TMEM (lane = row, each 32-bit column two consecutive values along
+// K), and the commit, for a warp that runs converged: every lane calls with the same operands and the
+// lane whose `leader` is set issues.  Without a branch around them the operands stay in uniform
+// registers, which is where these instructions take them from; behind `if (lane == 0)` each one is
+// moved there first, some 100 cycles an MMA against the 64 that a 128 x 128 x 16 product runs.
 __device__ __forceinline__ void mma_bf16_ss_warp(uint32_t leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                                  uint32_t idesc, uint32_t accumulate) {
   asm volatile(
