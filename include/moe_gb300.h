@@ -607,7 +607,8 @@ moe_status moe_attention_forward(const moe_attention_config* cfg, const moe_head
  * dk and dv summed over the query heads of the group.  Shapes as q, k, v; each
  * rounded once from fp32 sums in a fixed order; p and ds are rounded to bf16 between
  * the products.  Outputs overlap neither inputs nor each other.  Rows of no sequence are left as they were.  Where a row of dout is
- * not finite, so are dv, dk (whole rows) of what it sees and its dq. */
+ * not finite, so are dv, dk (whole rows) of what it sees and its dq.  An infinite key that a row gives a probability
+ * of 0 may leave the row's dq finite, where 0 * infinity is NaN. */
 moe_status moe_attention_backward(const moe_attention_config* cfg, const moe_heads* q, const moe_heads* k,
                                   const moe_heads* v, const int32_t* cu_seqlens, const moe_heads* out, const float* lse,
                                   const moe_heads* dout, const moe_heads* dq, const moe_heads* dk, const moe_heads* dv,

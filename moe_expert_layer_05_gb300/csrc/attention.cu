@@ -18,14 +18,20 @@
 // sixteen warps work on the scores in TMEM.
 //
 // Measured at 8192 rows of one sequence, 32/8 heads of 128 (a library's bf16 product of 8192 x 8192 x 8192: 1927
-// TFLOP/s): forward 353 us (1557), gradients 1140 (1206, of five products; the two kernels compute seven, of which
-// the scores and dp twice).  Eight packed sequences of 1 to 3907 rows: 153 and 487 us.  Heads of 64, 32768 rows, 8/1
-// heads: forward 920 us (1195).  One row: 7.1 us.
+// TFLOP/s): forward 326 us (1687), gradients 1080 (1273, of five products; the two kernels compute seven, of which
+// the scores and dp twice).  Eight packed sequences of 1 to 3907 rows: 144 and 458 us.  Heads of 64, 32768 rows, 8/1
+// heads: forward 890 us (1235).  One row: 6.6 us.
+//
+// Rounded between the products, as operands of the tensor cores have to be: the probabilities (relative to a
+// reference within 2^8 of their maximum; the sum that divides them is of the fp32 values), p for dv, ds for dq and
+// dk.  Each is off by 2^-8 of itself at most, independently, which leaves out 2.0e-3 and the gradients 2.4e-3
+// off as a whole, of which the results' own rounding is 1.5e-3 and 1.7e-3.  In two parts, as the statistics below,
+// they would double the products.
 //
 // Values that are not finite: a product with a probability of zero is still a NaN
 // on the tensor cores.  Where a tile has masked places the operand along the
 // contraction is therefore looked through first, and what is not finite there is
-// put to zero (clean_tile); rows that do see it are given it back at the end.
+// put to zero (clean_tile); the forward gives it back at the end to the rows that do see it.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -191,7 +197,8 @@ __device__ __forceinline__ void find_map(const AttnParams& p, int r0, int mine, 
 }
 // Boundaries that do not ascend or lie outside [0, T] are reported; a warp of each CTA, its share.
 __device__ __forceinline__ void check_boundaries(const AttnParams& p) {
-  for (int i = static_cast<int>(blockIdx.x) * 32 + (threadIdx.x & 31); i <= p.B; i += static_cast<int>(gridDim.x) * 32) {
+  const int lane = threadIdx.x & 31, step = static_cast<int>(gridDim.x) * 32;
+  for (int i = static_cast<int>(blockIdx.x) * 32 + lane; i <= p.B; i += step) {
     const int c = p.cu[i];
     if (c < 0 || c > p.T || (i > 0 && p.cu[i - 1] > c)) set_status(p.status, kErrBadIndex);
   }
@@ -204,8 +211,8 @@ __device__ __forceinline__ int take_item(int* status, int items, int grid) {
   return before + grid;
 }
 
-// A count over all of a CTA's items, of which only places and phases are asked for: stages and barriers come round after 16,
-// 6, 4 or 2, so 48 may be taken off (kept above the first round, and from overflowing in very long calls).
+// A count over all of a CTA's items, of which only places and phases are asked for: stages and barriers come round
+// after 16, 6, 4 or 2, so 48 may be taken off (kept above the first round, and from overflowing in very long calls).
 __device__ __forceinline__ int wrapped(int count) { return count < 96 ? count : 48 + count % 48; }
 
 // Bits lo .. hi of 32: the columns that a row sees.  (As bits: a comparison with each end takes three
@@ -242,7 +249,9 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, 
 // The warp that issues the products runs converged, one lane issuing (mma_bf16_ss_warp).
 // Descriptors of a tile's first rows and columns: as the operand of the scores (columns along the
 // contraction) and of the sums (rows along it).
-__device__ __forceinline__ uint64_t scores_desc(const uint8_t* tile) { return smem_desc_sw128(smem_u32(tile), 16, 1024); }
+__device__ __forceinline__ uint64_t scores_desc(const uint8_t* tile) {
+  return smem_desc_sw128(smem_u32(tile), 16, 1024);
+}
 __device__ __forceinline__ uint64_t sums_desc(const uint8_t* tile) {
   return smem_desc_sw128(smem_u32(tile), kRows * 128, 1024);
 }
@@ -315,7 +324,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
 __device__ __forceinline__ float as_f(uint32_t v) { return __uint_as_float(v); }
 
 // A converged warp's wait.  It returns when the phase is complete, or when a wait of the block has given up: the
@@ -346,8 +357,8 @@ struct Issued {
 
 // 32 columns of a warp's 32 rows, a row a thread, rounded: through 2 KB of shared memory, so that a row's 64 bytes
 // leave together.  `out`: the first row; rows: which of them are stored; columns from D on are not.
-__device__ __forceinline__ void store_cols(uint8_t* staging, __nv_bfloat16* out, long long stride, uint32_t rows, int col,
-                                           int D, const float (&v)[32]) {
+__device__ __forceinline__ void store_cols(uint8_t* staging, __nv_bfloat16* out, long long stride, uint32_t rows,
+                                           int col, int D, const float (&v)[32]) {
   const int lane = threadIdx.x & 31;
   uint4* s = reinterpret_cast<uint4*>(staging);
   #pragma unroll
@@ -389,19 +400,22 @@ __device__ __forceinline__ bool give_back(uint4* sums, const uint4& v) {
   for (int i = 0; i < 4; ++i) {
     const uint32_t on = __vcmpeq2(y[i] & 0x7f807f80u, 0x7f807f80u);
     const uint32_t add = (y[i] & on) | (0x80008000u & ~on);                 // (-0 changes nothing)
-    const __nv_bfloat162 r = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(to + i), *reinterpret_cast<const __nv_bfloat162*>(&add));
+    const __nv_bfloat162 r =
+        __hadd2(*reinterpret_cast<const __nv_bfloat162*>(to + i), *reinterpret_cast<const __nv_bfloat162*>(&add));
     to[i] = *reinterpret_cast<const uint32_t*>(&r);
     nan &= __vcmpgtu2(to[i] & 0x7fff7fffu, 0x7f807f80u);
   }
   return nan == ~0u;
 }
 // The first D columns of the rows that `rows` names.
-__device__ __forceinline__ void store_rows(uint8_t* staging, __nv_bfloat16* out, long long stride, uint32_t rows, int D) {
+__device__ __forceinline__ void store_rows(uint8_t* staging, __nv_bfloat16* out, long long stride, uint32_t rows,
+                                           int D) {
   const int lane = threadIdx.x & 31, w = lane & 7;
   #pragma unroll
   for (int r0 = 0; r0 < 32; r0 += 4) {
     const int r = r0 + (lane >> 3);
-    if ((rows >> r & 1u) && 8 * w < D) *reinterpret_cast<uint4*>(out + r * stride + 8 * w) = *staged_word(staging, r, w);
+    if ((rows >> r & 1u) && 8 * w < D)
+      *reinterpret_cast<uint4*>(out + r * stride + 8 * w) = *staged_word(staging, r, w);
   }
 }
 
@@ -421,8 +435,9 @@ __device__ __forceinline__ void exchange(uint4& first, uint4& second) {
 // ---------------------------------------------------------------- forward
 // A CTA has two tiles of 128 query rows, each with four warps, and one stream of key
 // and value tiles for both: two heads of a group on the same rows, or (groups of an
-// odd size) 256 rows of one head (or one tile, where there are few).  The CTAs stay and take such items one after the other: one's outputs are written
-// while the next one's first products run.  (A CTA for each lost 14 thousand cycles an item before its first key
+// odd size) 256 rows of one head (or one tile, where there are few).  The CTAs stay and take such
+// items one after the other: one's outputs are written while the next one's first
+// products run.  (A CTA for each lost 14 thousand cycles an item before its first key
 // tile and after its last, of 2800 a key tile; this one 9.)  The tensor cores alternate between them: while one
 // tile's scores are exponentiated, the other's products run.  TMEM: buffers of scores of
 // 128 columns (their first 64 become the probabilities), sums DP columns a tile.
@@ -433,7 +448,7 @@ __device__ __forceinline__ void exchange(uint4& first, uint4& second) {
 // 32 heads of 64; with a buffer a tile 300).  Wide heads have a buffer a tile and one issuing warp (two: 0.53 ms
 // against 0.41).
 //
-// What bounds it: a step, one key tile against both tiles of rows, is 2770 cycles at heads of 128, of which the
+// What bounds it: a step, one key tile against both tiles of rows, is 2540 cycles at heads of 128, of which the
 // tensor cores work 2048.  The rest is the chain of one tile (scores, maximum, exponentials, sums,
 // next scores), of which TMEM has room for two.
 //
@@ -446,8 +461,8 @@ struct FwdItem {
   int item;                                // -1: no more
   int q0, top, kv;
   int from[2], to[2], base[2], head[2], ib, n;
-  int loaded;                              // key and value tiles in the ring: 2 n, or the first ones of an item without rows
-  int mixed;                               // 256 rows of one head: key tiles from here on are masked for one of its tiles
+  int loaded;                              // tiles in the ring: 2 n, or the first ones of an item without rows
+  int mixed;                               // 256 rows of one head: key tiles from here on are masked for one half
   int bad_lo, bad_hi;                      // key rows of tiles in which clean_tile found something
 };
 struct FwdBook {
@@ -521,7 +536,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   tc_fence_before_sync();
   pdl_wait();
 
-  // The first queries, and where both tiles have the same rows the first keys, do not wait for the sequences' boundaries.
+  // The first queries, and where both tiles have the same rows the first keys, do not wait for the sequences'
+  // boundaries.
   const bool early = p.mode != kTwoTiles;
   const int filled_by = p.mode == kOneTile ? 1 : 2;           // tiles of queries
   if (warp == kFwdLoadWarp && lane == 0 && early) {
@@ -541,7 +557,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     int q0, h;
     fwd_place(p, item, q0, h);
     for (int r = it > 0 ? lane : 2 * kRows; r < filled_by * kRows; r += 32) {
-      const int row = q0 + (p.mode == kTwoTiles ? r : r & (kRows - 1)), head = h + (p.mode == kTwoTiles ? 0 : r / kRows);
+      const int row = q0 + (p.mode == kTwoTiles ? r : r & (kRows - 1));
+      const int head = h + (p.mode == kTwoTiles ? 0 : r / kRows);
       if (row < p.T) {
         const __nv_bfloat16* q = p.q.p + row * p.q.token + head * p.q.head;
         prefetch_l2(q);
@@ -553,18 +570,22 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       // key tile i: rows [top - 128 (i + 1), top - 128 i); query tile u meets tiles [from[u], to[u])
       const int top = q0 + (p.mode == kTwoTiles ? 2 * kRows : kRows);
       for (int u = 0; u < 2; ++u) {
-        const int base = q0 + (p.mode == kTwoTiles ? kRows * u : 0), a = max(base, first_row), b = min(base + kRows, last_row);
+        const int base = q0 + (p.mode == kTwoTiles ? kRows * u : 0);
+        const int a = max(base, first_row), b = min(base + kRows, last_row);
         m.base[u] = base;
         m.head[u] = h + (p.mode == kTwoHeads ? u : 0);
         m.from[u] = p.mode == kTwoTiles ? 1 - u : 0;
-        m.to[u] = m.from[u] + (a < b && u < filled_by ? (base + kRows - start_of(&m.map, q0, a) + kRows - 1) / kRows : 0);
+        const bool on = a < b && u < filled_by;
+        m.to[u] = m.from[u] + (on ? (base + kRows - start_of(&m.map, q0, a) + kRows - 1) / kRows : 0);
       }
       const bool on0 = m.to[0] > m.from[0], on1 = m.to[1] > m.from[1];
       m.ib = on1 ? m.from[1] : m.from[0];
       m.n = (on0 || on1) ? max(m.to[0], m.to[1]) - m.ib : 0;
       m.loaded = m.n > 0 ? 2 * m.n : (early && it == 0 ? 2 : 0);
       // (a boundary between a tile's rows masks their keys in front of it; the second tile's last one is the furthest)
-      m.mixed = p.mode == kTwoTiles && on1 ? (top - start_of(&m.map, q0, min(m.base[1] + kRows, last_row) - 1)) / kRows : INT_MAX;
+      m.mixed = INT_MAX;
+      if (p.mode == kTwoTiles && on1)
+        m.mixed = (top - start_of(&m.map, q0, min(m.base[1] + kRows, last_row) - 1)) / kRows;
       m.q0 = q0;
       m.top = top;
       m.kv = h / (p.Hq / p.Hkv);
@@ -576,7 +597,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   };
   if (warp == kFwdItemWarp) {
     if (lane <= p.B) mine = p.cu[lane];     // (the first boundaries stay with it)
-    const int begin = p.B < 32 ? __shfl_sync(kFull, mine, 0) : p.cu[0], end = p.B < 32 ? __shfl_sync(kFull, mine, p.B) : p.cu[p.B];
+    const int begin = p.B < 32 ? __shfl_sync(kFull, mine, 0) : p.cu[0];
+    const int end = p.B < 32 ? __shfl_sync(kFull, mine, p.B) : p.cu[p.B];
     first_row = max(begin, 0);
     last_row = min(end, p.T);
     place(blockIdx.x, 0);
@@ -699,9 +721,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (i >= f && i < e) {
           const int outs = u ? outs1 : outs0;
           if (i == f && outs > 0) warp_wait(&bk.o_empty[u], (outs - 1) & 1, abort, lim);
-          // Where the second tile of rows looks through the value tile (masked there, perhaps not here) the first one's product
-          // waits for it: what is not finite shall be there for both or for neither.  (The other way round the first tile's
-          // probabilities, which come after its own look, have been waited for.)
+          // Where the second tile of rows looks through the value tile (masked there, perhaps not here) the first
+          // one's product waits for it: what is not finite shall be there for both or for neither.  (The other way
+          // round the first tile's probabilities, which come after its own look, have been waited for.)
           const int x1 = met1 + i - f1;
           const bool both = p.mode == kTwoTiles && u == 0 && i >= f1 && i < e1 && (i == f0 || i >= mixed);
           #pragma unroll 1
@@ -722,7 +744,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (u == 1) release(s);
       };
       if (n == 0) {
-        if (loaded > 0 && warp == kFwdMmaWarp) {                  // (loaded before it was known that nothing asks for it)
+        if (loaded > 0 && warp == kFwdMmaWarp) {         // (loaded before it was known that nothing asks for it)
           warp_wait(&bk.q_full, filled & 1, abort, lim);
           mma_commit_warp(leader, &bk.q_empty);
           for (int s = turn; s < turn + loaded; ++s) {
@@ -748,8 +770,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (round > 0) warp_wait(&bk.free[b], (round - 1) & 1, abort, lim);
             tc_fence_after_sync();
             scores(u, i, 128 * b);
-            // (Without it the warp of the sums, which has nothing to wait for where a tile does not meet the keys, could end
-            // a second phase before this one has looked at the first.)
+            // (Without it the warp of the sums, which has nothing to wait for where a tile does not meet the keys,
+            // could end a second phase before this one has looked at the first.)
             if (lane == 0) mbar_arrive(&bk.free[b]);
             __syncwarp();
             if (++b == L) {
@@ -785,7 +807,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
    const int u = warp >> 2;
    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
    const uint32_t to_ = tmem + 128 * L + DP * u + lanes;
-   int turn = 0, met = 0, outs = 0, scored = 0;         // as in the warp that issues; outs: items with rows of this tile
+   int turn = 0, met = 0, outs = 0, scored = 0;   // as in the warp that issues; outs: items with rows of this tile
    for (int it = 0; uniform(next_item(it) ? 1 : 0) != 0; ++it) {
     FwdItem& m = bk.item[it & 1];
     const int f = m.from[u], e = m.to[u], ib = m.ib, n = m.n, q0 = m.q0, top = m.top;
@@ -959,14 +981,15 @@ __device__ __forceinline__ uint4 split_row(float v) {
   const __nv_bfloat16 a = __float2bfloat16(v);
   const float r = v - __bfloat162float(a);
   const __nv_bfloat16 b = __float2bfloat16(r), c = __float2bfloat16(r - __bfloat162float(b));
-  return make_uint4(static_cast<uint32_t>(__bfloat16_as_ushort(a)) | static_cast<uint32_t>(__bfloat16_as_ushort(b)) << 16,
-                    __bfloat16_as_ushort(c), 0u, 0u);
+  const uint32_t lo = __bfloat16_as_ushort(a), hi = __bfloat16_as_ushort(b);
+  return make_uint4(lo | hi << 16, __bfloat16_as_ushort(c), 0u, 0u);
 }
 
 // dq: 128 query rows of one head against their key tiles, CTAs that stay as in the forward.  TMEM: dq DP columns
 // from 0, scores at 128, two buffers of dp at 256 and 384 (each becomes ds).  Both products of the next key
-// tile run while this one's ds is worked out, the scores once they have been read.  A step is 2000
-// cycles at heads of 128, of which the tensor cores work 1536; an item takes 12 thousand besides (a CTA for each: 15).
+// tile run while this one's ds is worked out, the scores once they have been read.  A step is 1630
+// cycles at heads of 128, of which the tensor cores work 1536; an item takes 10 thousand besides (a CTA for each
+// took 3 thousand more).
 //
 // out, for delta, comes through a place of the keys (TMA; read from memory by the threads it
 // kept the first step waiting as long).  Sixteen warps work on one step, 32 columns a thread (two
@@ -1068,7 +1091,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   };
   if (warp == kBwdItemWarp) {
     if (lane <= p.B) mine = p.cu[lane];     // (the first boundaries stay with it)
-    const int begin = p.B < 32 ? __shfl_sync(kFull, mine, 0) : p.cu[0], end = p.B < 32 ? __shfl_sync(kFull, mine, p.B) : p.cu[p.B];
+    const int begin = p.B < 32 ? __shfl_sync(kFull, mine, 0) : p.cu[0];
+    const int end = p.B < 32 ? __shfl_sync(kFull, mine, p.B) : p.cu[p.B];
     first_row = max(begin, 0);
     last_row = min(end, p.T);
     place(blockIdx.x, 0);
@@ -1381,7 +1405,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // key), so that the probabilities lie in TMEM as the A operand of the sums.  TMEM: dk, dv
 // DP columns from 0 and 128, scores at 256 (which become p), dp at 384 (ds).  In the
 // order dv(j), scores(j + 1), dk(j), dp(j + 1) each buffer is free again when its turn
-// comes.  A step is 2600 cycles at heads of 128, of which the tensor cores work 2176.
+// comes.  A step is 2440 cycles at heads of 128, of which the tensor cores work 2176.
 //
 // A thread's columns are queries, each with an lse and a delta of its own.  Read from shared memory
 // they cost it 128 KB a step, as much as the tiles (a step 2900 cycles, whatever the width); so
@@ -1415,7 +1439,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   uint8_t* delta_smem = lse_smem + 2 * kRowBytes;        // the same, with do
   uint8_t* ones_smem = delta_smem + 2 * kRowBytes;       // 128 rows of three ones and five zeros
   uint8_t* zero_smem = ones_smem + kRowBytes;            // the other half of each operand's 16 columns
-  float4* sums = reinterpret_cast<float4*>(q_smem);                            // [dk, dv][128][DP], in place of q and do
+  float4* sums = reinterpret_cast<float4*>(q_smem);      // [dk, dv][128][DP], in place of q and do
   DkvBook& bk = *reinterpret_cast<DkvBook*>(zero_smem + kRowBytes);
   if (!smem_fits(smem_raw, &bk + 1)) {
     pdl_wait();
@@ -1519,12 +1543,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int tiles = uniform(n);
     auto scores = [&](int j) {
       mma_scores<DP>(leader, tmem + 256, k_desc, q_desc + (j & 1) * kNext);
-      mma_bf16_ss_warp(leader, tmem + 256, ones_desc, rows_desc(lse_smem + (j & 1) * kRowBytes, zero_smem), C::kScores, 1u);
+      mma_bf16_ss_warp(leader, tmem + 256, ones_desc, rows_desc(lse_smem + (j & 1) * kRowBytes, zero_smem), C::kScores,
+                       1u);
       mma_commit_warp(leader, &bk.s_full);
     };
     auto dprob = [&](int j) {
       mma_scores<DP>(leader, tmem + 384, v_desc, do_desc + (j & 1) * kNext);
-      mma_bf16_ss_warp(leader, tmem + 384, ones_desc, rows_desc(delta_smem + (j & 1) * kRowBytes, zero_smem), C::kScores, 1u);
+      mma_bf16_ss_warp(leader, tmem + 384, ones_desc, rows_desc(delta_smem + (j & 1) * kRowBytes, zero_smem),
+                       C::kScores, 1u);
       mma_commit_warp(leader, &bk.dp_full);
     };
     warp_wait(&bk.kv_full, 0, abort, lim);
@@ -1569,7 +1595,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       warp_wait(&bk.s_full, j & 1, abort, lim);
       tc_fence_after_sync();
       uint32_t on = kFull;                    // queries of the key's sequence, from its own on
-      if (masked) on = seen(key - q0 - 32 * part, (valid ? end_of(&bk.map, k0, key, kRows / 32) : INT_MAX) - 1 - q0 - 32 * part);
+      if (masked) {
+        const int to = valid ? end_of(&bk.map, k0, key, kRows / 32) : INT_MAX;
+        on = seen(key - q0 - 32 * part, to - 1 - q0 - 32 * part);
+      }
       uint32_t s[32], d[32], w[16];
       tmem_ld_x32(tmem + lanes + 256 + 32 * part, s);
       tmem_ld_wait(s);
@@ -1605,7 +1634,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (!whole) blank(d, on);               // (so that ds is zero there whatever the tensors hold)
       #pragma unroll
       for (int x = 0; x < 32; x += 2) {
-        const float2 y = split_f32x2(mul2(make_f32x2(as_f(s[x]), as_f(s[x + 1])), make_f32x2(as_f(d[x]), as_f(d[x + 1]))));
+        const F32x2 prob = make_f32x2(as_f(s[x]), as_f(s[x + 1]));
+        const float2 y = split_f32x2(mul2(prob, make_f32x2(as_f(d[x]), as_f(d[x + 1]))));
         w[x / 2] = pack_bf16x2(y.x, y.y);
       }
       tmem_st_x16(tmem + lanes + 384 + 32 * part, w);
@@ -1657,7 +1687,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     for (int i = threadIdx.x; i < 2 * rows * (DP / 8); i += kBwdThreads) {
       const int w = i % (DP / 8), r = r0 + i / (DP / 8) % rows, half = i / (DP / 8) / rows, key = k0 + r;
       const float4* mine = sums + (half * kRows + r) * (DP / 4);
-      const uint32_t lo = smem_u32(mine + ((2 * w) ^ (key & (DP / 4 - 1)))), hi = smem_u32(mine + ((2 * w + 1) ^ (key & (DP / 4 - 1))));
+      const int turned = key & (DP / 4 - 1);
+      const uint32_t lo = smem_u32(mine + ((2 * w) ^ turned)), hi = smem_u32(mine + ((2 * w + 1) ^ turned));
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
       for (int c = 0; c < split; ++c) {
         x = add4(x, ld_cluster_v4(mapa_shared(lo, c)));
@@ -1695,13 +1726,14 @@ template <int DP>
 constexpr int dkv_smem() {
   return 6 * Tile<DP>::kBytes + 6 * kRowBytes + static_cast<int>(sizeof(DkvBook));
 }
-static_assert(fwd_smem<128>() <= kMaxSmem && dq_smem<128>() <= kMaxSmem && dkv_smem<128>() <= kMaxSmem, "shared memory");
+static_assert(fwd_smem<128>() <= kMaxSmem && dq_smem<128>() <= kMaxSmem && dkv_smem<128>() <= kMaxSmem,
+              "shared memory");
 
 // Launch of blocks with much shared memory, in clusters of `cluster`.  (Each takes an SM's registers for itself, so no
 // two blocks of an SM wait for each other's TMEM, which the blocks of two clusters might do in a ring.)
 template <class... KArgs, class... Args>
-cudaError_t launch_big(void (*kern)(KArgs...), std::atomic<bool>* attr_set, int grid, int threads, int smem, cudaStream_t st, int cluster,
-                       Args&&... args) {
+cudaError_t launch_big(void (*kern)(KArgs...), std::atomic<bool>* attr_set, int grid, int threads, int smem,
+                       cudaStream_t st, int cluster, Args&&... args) {
   const int dev = current_device();
   if (dev < 0) return cudaErrorInvalidDevice;
   if (!attr_set[dev].load(std::memory_order_acquire)) {
@@ -1730,8 +1762,8 @@ cudaError_t launch_big(void (*kern)(KArgs...), std::atomic<bool>* attr_set, int 
 // CTAs that share the heads of a group in dk and dv's kernel.  As few as leave no CTA more than 5/4 of an SM's share of
 // one long sequence's tiles: a CTA of the first keys has tiles * group / split of them, an SM (tiles + 1) tiles
 // q_heads / 2 / 152.  Large batches take one: clusters of four leave SMs of a GPC idle (8192 rows, 32/8 heads of
-// 128, backward: 1.15 ms alone, 1.20 in pairs, 1.35 by four); small ones gain (2048 rows, 32/4 heads: 0.22, 0.14, 0.12 and,
-// by eight, 0.19 ms; 1000 rows, 6/2 heads of 80: 53 us, 38 by three).
+// 128, both kernels: 1.08 ms alone, 1.20 in pairs, 1.36 by four); small ones gain (2048 rows, 32/4 heads: 0.23, 0.14,
+// 0.11 and, by eight, 0.18 ms; 1000 rows, 6/2 heads of 80: 51 us, 36 by three).
 int group_split(const AttnParams& p) {
   const int group = p.Hq / p.Hkv;
   int best = 1;
@@ -1741,8 +1773,10 @@ int group_split(const AttnParams& p) {
 }
 
 // The tiles of an item of the forward: two, which share the keys' loads and keep the tensor cores busy in turn; but one
-// where an SM would have none otherwise.  (Two, one: 1003 rows, 6/2 heads of 80: 17.5, 14.7 us; 2400 rows, 8/1 of 64: 25.0,
-// 20.6; 4000 rows, 4 of 128: 52, 43; one row, 32/8 of 128: 6.9, 6.3.)
+// where an SM would have none otherwise.  (One, two, by tiles * heads: 32, a row of 32/8 heads of 128: 6.6, 7.0 us;
+// 48, 1003 rows, 6/2 of 80: 15.1, 18.0; 128, 4000 rows, 4 of 128: 43, 49; 152, 2400 rows, 8/1 of 64: 19.7, 24.2; 512,
+// 2048 rows, 32/8 of 128: 50, 31; 2048, 8192 rows: 557, 326.  Past the limit one stays ahead for a while, as most of
+// its SMs still have one tile: 208: 67, 76; 304: 101, 108 and 67, 80 (heads of 64); 312: 42, 44; 384: 92, 71.)
 int forward_mode(const AttnParams& p) {
   if (static_cast<long long>(p.tiles) * p.Hq <= num_sms()) return kOneTile;
   return p.Hq / p.Hkv % 2 == 0 ? kTwoHeads : kTwoTiles;
@@ -1802,22 +1836,25 @@ cudaError_t forward(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensor
                     cudaStream_t st) {
   static std::atomic<bool> attr_set[kMaxDevices];
   const int items = p.tiles * (p.mode == kTwoHeads ? p.Hq / 2 : p.Hq), sms = num_sms();
-  return launch_big(attention_fwd_kernel<DP>, attr_set, items < sms ? items : sms, kFwdThreads, smem_of(fwd_smem<DP>()), st, 1, tq, tk, tv, p);
+  return launch_big(attention_fwd_kernel<DP>, attr_set, items < sms ? items : sms, kFwdThreads, smem_of(fwd_smem<DP>()),
+                    st, 1, tq, tk, tv, p);
 }
 template <int DP>
 cudaError_t backward(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& td,
-                     const CUtensorMap& to, AttnParams p, const Heads& dq, const Heads& dk, const Heads& dv, cudaStream_t st) {
+                     const CUtensorMap& to, AttnParams p, const Heads& dq, const Heads& dk, const Heads& dv,
+                     cudaStream_t st) {
   static std::atomic<bool> dq_set[kMaxDevices], dkv_set[kMaxDevices];
   p.d0 = dq;
   const int items = p.tiles * p.Hq, sms = num_sms();
   const cudaError_t e =
-      launch_big(attention_dq_kernel<DP>, dq_set, items < sms ? items : sms, kBwdThreads, smem_of(dq_smem<DP>()), st, 1, tq, tk, tv, td, to, p);
+      launch_big(attention_dq_kernel<DP>, dq_set, items < sms ? items : sms, kBwdThreads, smem_of(dq_smem<DP>()), st, 1,
+                 tq, tk, tv, td, to, p);
   if (e != cudaSuccess) return e;
   p.d0 = dk;
   p.d1 = dv;
   p.split = group_split(p);
-  return launch_big(attention_dkv_kernel<DP>, dkv_set, p.tiles * p.Hkv * p.split, kBwdThreads, smem_of(dkv_smem<DP>()), st, p.split,
-                    tq, tk, tv, td, p);
+  return launch_big(attention_dkv_kernel<DP>, dkv_set, p.tiles * p.Hkv * p.split, kBwdThreads,
+                    smem_of(dkv_smem<DP>()), st, p.split, tq, tk, tv, td, p);
 }
 
 }  // namespace
@@ -1839,7 +1876,8 @@ moe_status moe_attention_forward(const moe_attention_config* cfg, const moe_head
   if (!config_ok(cfg) || !ptr_ok(ws)) return MOE_ERR_INVALID_ARG;
   const int T = cfg->T, Hq = cfg->q_heads, Hkv = cfg->kv_heads, D = cfg->head_dim;
   const bool none = T == 0 || cfg->sequences == 0;
-  if (!none && (!ptr_ok(cu_seqlens) || !ptr_ok(lse) || !heads_ok(q, T, Hq, D, false) || !heads_ok(k, T, Hkv, D, false) ||
+  if (!none && (!ptr_ok(cu_seqlens) || !ptr_ok(lse) || !heads_ok(q, T, Hq, D, false) ||
+                !heads_ok(k, T, Hkv, D, false) ||
                 !heads_ok(v, T, Hkv, D, false) || !heads_ok(out, T, Hq, D, true)))
     return MOE_ERR_INVALID_ARG;
   if (ws_bytes < kStatusBytes) return MOE_ERR_WORKSPACE;
@@ -1866,7 +1904,8 @@ moe_status moe_attention_backward(const moe_attention_config* cfg, const moe_hea
   if (!config_ok(cfg) || !ptr_ok(ws)) return MOE_ERR_INVALID_ARG;
   const int T = cfg->T, Hq = cfg->q_heads, Hkv = cfg->kv_heads, D = cfg->head_dim;
   const bool none = T == 0 || cfg->sequences == 0;
-  if (!none && (!ptr_ok(cu_seqlens) || !ptr_ok(lse) || !heads_ok(q, T, Hq, D, false) || !heads_ok(k, T, Hkv, D, false) ||
+  if (!none && (!ptr_ok(cu_seqlens) || !ptr_ok(lse) || !heads_ok(q, T, Hq, D, false) ||
+                !heads_ok(k, T, Hkv, D, false) ||
                 !heads_ok(v, T, Hkv, D, false) || !heads_ok(out, T, Hq, D, false) || !heads_ok(dout, T, Hq, D, false) ||
                 !heads_ok(dq, T, Hq, D, true) || !heads_ok(dk, T, Hkv, D, true) || !heads_ok(dv, T, Hkv, D, true)))
     return MOE_ERR_INVALID_ARG;

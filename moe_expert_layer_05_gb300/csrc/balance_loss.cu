@@ -385,7 +385,8 @@ moe_status moe_balance_loss_forward(const float* logits, const int32_t* topk_idx
                                     int32_t E, int32_t k, int32_t score, float* loss, int32_t* counts, float* slope,
                                     void* ws, size_t ws_bytes, void* stream) {
   if (!sizes_ok(T, E) || k <= 0 || k > kMaxK || k > E || !score_ok(score)) return MOE_ERR_INVALID_ARG;
-  if (!word_ok(loss) || !word_ok(counts) || !word_ok(slope) || !ptr_ok(ws) || !opt_ok(tokens)) return MOE_ERR_INVALID_ARG;
+  if (!word_ok(loss) || !word_ok(counts) || !word_ok(slope) || !ptr_ok(ws) || !opt_ok(tokens))
+    return MOE_ERR_INVALID_ARG;
   if (T > 0 && (!ptr_ok(logits) || !ptr_ok(topk_idx))) return MOE_ERR_INVALID_ARG;
   if (ws_bytes < moe_balance_loss_workspace_bytes(T, E)) return MOE_ERR_WORKSPACE;
   if (!device_is_gb300()) return MOE_ERR_UNSUPPORTED;
@@ -429,7 +430,8 @@ moe_status moe_balance_loss_backward(const float* logits, const float* slope, co
   static void (*const kern[6])(BalanceParams) = {balance_bwd_kernel<2, 4>,  balance_bwd_kernel<4, 4>,
                                                  balance_bwd_kernel<8, 4>,  balance_bwd_kernel<16, 4>,
                                                  balance_bwd_kernel<32, 4>, balance_bwd_kernel<32, 8>};
-  return status_of(run(kern, p, need < 4 * kMaxBlocks ? need : 4 * kMaxBlocks, kThreads, static_cast<cudaStream_t>(stream)));
+  const int blocks = need < 4 * kMaxBlocks ? need : 4 * kMaxBlocks;
+  return status_of(run(kern, p, blocks, kThreads, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -174,8 +174,9 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads) grad_clip_kernel(const __grid_constant__ TensorList<N> list,
-                                                             const float* __restrict__ norm, float limit, int in_place) {
+__global__ void __launch_bounds__(kThreads)
+    grad_clip_kernel(const __grid_constant__ TensorList<N> list, const float* __restrict__ norm, float limit,
+                     int in_place) {
   pdl_entry();
   float c = limit / (norm[0] + 1e-6f);
   if (c >= 1.f || (limit == INFINITY && norm[0] == INFINITY)) {      // (infinity / infinity: no limit is none)
@@ -300,8 +301,8 @@ cudaError_t clip_launch(const moe_tensor* t, const moe_tensor* out, int count, c
   count_launches(1);
   // a block a chunk: 2.3 GB scaled in 700 us; 805 where 912 blocks take 80 each in turn
   const long long chunks = all_chunks(t, count);
-  return launch_k(grad_clip_kernel<N>, static_cast<int>(chunks < kMaxClipBlocks ? chunks : kMaxClipBlocks), kThreads, 0, st,
-                  list, norm, limit, out == nullptr ? 1 : 0);
+  const int blocks = static_cast<int>(chunks < kMaxClipBlocks ? chunks : kMaxClipBlocks);
+  return launch_k(grad_clip_kernel<N>, blocks, kThreads, 0, st, list, norm, limit, out == nullptr ? 1 : 0);
 }
 
 }  // namespace
@@ -330,8 +331,9 @@ moe_status moe_grad_norm(const moe_tensor* grads, int32_t n, float* norm, void* 
   for (int32_t i = 0; i == 0 || i < n; i += per) {
     const int count = n - i < per ? n - i : per, blocks = blocks_of(grads + i, count);
     const cudaError_t e =
-        per == kList ? norm_launch<kList>(grads + i, count, blocks, part, part0, total, norm, static_cast<int*>(ws), st)
-                     : norm_launch<kLongList>(grads + i, count, blocks, part, part0, total, norm, static_cast<int*>(ws), st);
+        per == kList
+            ? norm_launch<kList>(grads + i, count, blocks, part, part0, total, norm, static_cast<int*>(ws), st)
+            : norm_launch<kLongList>(grads + i, count, blocks, part, part0, total, norm, static_cast<int*>(ws), st);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
     part0 += blocks;
   }

@@ -109,7 +109,8 @@ __global__ void __launch_bounds__(kThreads, 5) rotary_kernel(const RotaryParams 
   for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
     const int t = i / pairs;
     const unsigned long long frac = turn_fraction(p.freq[i - t * pairs]);
-    const unsigned long long angle = static_cast<unsigned long long>(static_cast<long long>(p.positions[t0 + t])) * frac;
+    const long long position = p.positions[t0 + t];
+    const unsigned long long angle = static_cast<unsigned long long>(position) * frac;
     float s, c;
     sincospif(static_cast<float>(static_cast<int>(angle >> 32)) * (1.f / 2147483648.f), &s, &c);   // (half turns)
     s_turn[i] = make_float2(c * p.scale, (p.inverse ? -s : s) * p.scale);
