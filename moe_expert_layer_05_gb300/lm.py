@@ -189,7 +189,8 @@ class MoEModel:
         return self.loss
 
     def _balance_backward(self, i: int, x, tokens) -> None:
-        """The balance loss's gradients through the router, added to those of the expert layer."""
+        """The balance loss's gradients through the router, added to those of the expert layer (whose dx, bf16, is rounded a
+        second time here)."""
         logits, _ = self._routing(i)
         api.moe_balance_loss_backward(logits, self.slope[i], self.factor, self.dlogits, tokens=tokens, score=self.score)
         self.d_normed.copy_(torch.addmm(self.d_normed.float(), self.dlogits, self.params[f"layer{i}.w_router"].float()))
